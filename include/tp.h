@@ -406,9 +406,197 @@ tp_status tp_shard_gather(int t, int64_t rows, const int64_t* cols, tp_dtype dty
                           const void* const* shards, void* out, tp_stream stream);
 
 /*
+ * ---------------------------------------------------------------------
+ * Decode-loop operators: a paged KV cache held in 4 bits, attention over
+ * it, its pages, and beam selection.  The pages this library follows name
+ * the KV cache and split it by heads over the ranks ("Tensor parallelism
+ * from scratch", TPAttention) without giving a paged or quantised form;
+ * the definitions below are this library's own.
+ *
+ * Cache.  Rank r owns the kv heads of its QKV shard and holds them in one
+ * pool per layer: [pages, kv_heads, page_size/16] blocks of 16 tokens,
+ * page_size 16, 32, 64 or 128, head_dim 64 or 128.  One block is
+ * 16 (head_dim + 8) bytes: the codes of 16 keys (head_dim/2 bytes each,
+ * element 2i in the low and 2i+1 in the high half of byte i), the codes of
+ * 16 values, 16 pairs (step, base) of bf16 for the keys, 16 for the values.
+ * A row x of head_dim bf16 elements is held as
+ *     base = min(x),  step = bf16((max(x) - min(x)) * fp32(1/15)),
+ *     u_d = clamp(rint((x_d - base) / step), 0, 15)   (0 when step is 0)
+ * with each operation rounded to fp32, and stands for step * u_d + base.
+ * A row with a NaN or an infinity, or whose range passes fp32, stands for
+ * NaN in every element (step 0, base NaN).
+ *
+ * Sequences.  table [nseq, max_blocks] int32 (contiguous) lists each
+ * sequence's pages in order, lens [nseq] int32 its length in tokens.  The n
+ * rows of a call are the LAST rows of their sequences: with cu_rows NULL,
+ * n == nseq and row i is token lens[i] - 1 of sequence i; else cu_rows
+ * [nseq + 1] int32 is non-decreasing from 0 to n, rows [cu_rows[i],
+ * cu_rows[i+1]) belong to sequence i and the last of them is token
+ * lens[i] - 1.  lens counts the rows of the call.  All ranks share the
+ * table.  A page number outside [0, pages), or a position outside the
+ * table, met while a call runs is never read or written: its tokens count
+ * as not there, and tp_device_status() then returns TP_ERR_INVALID_ARG.
+ * ---------------------------------------------------------------------
+ */
+
+/* Bytes of one page of one rank and layer, kv_heads * page_size *
+ * (head_dim + 8); 0 for sizes that are not provided. */
+size_t tp_kv4_page_bytes(int page_size, int kv_heads, int head_dim);
+
+/*
+ * Quantise the n rows' keys and values and store them at their sequences'
+ * positions.  k[r], v[r] are [n, kv_heads * head_dim] bf16 (views of the
+ * merged QKV output will do), row strides ldk and ldv; pool[r] is rank r's
+ * pool of `pages` pages.  Rows at negative positions (lens shorter than the
+ * rows) are not stored.  Rows must have distinct positions in distinct
+ * pages' slots; nothing else of the pool changes.
+ */
+tp_status tp_kv4_append(int t, int64_t n, int64_t nseq, int kv_heads, int head_dim,
+                        const void* const* k, int64_t ldk, const void* const* v, int64_t ldv,
+                        void* const* pool, int64_t pages, int page_size,
+                        const int32_t* table, int64_t max_blocks, const int32_t* lens,
+                        const int32_t* cu_rows, tp_stream stream);
+
+/*
+ * The values that the n rows' cached keys and values stand for, as bf16
+ * (rounded once) or fp32 (fp32 step * u + base): the inverse of
+ * tp_kv4_append.  k[r], v[r] are [n, kv_heads * head_dim] of dtype with row
+ * strides ldk, ldv; either list may be NULL.  Rows that are not in the
+ * cache read as 0.
+ */
+tp_status tp_kv4_load(int t, int64_t n, int64_t nseq, int kv_heads, int head_dim,
+                      const void* const* pool, int64_t pages, int page_size,
+                      const int32_t* table, int64_t max_blocks, const int32_t* lens,
+                      const int32_t* cu_rows, void* const* k, int64_t ldk, void* const* v, int64_t ldv,
+                      tp_dtype dtype, tp_stream stream);
+
+/*
+ * Workspace bytes of tp_kv4_attention (0 for invalid arguments): partial
+ * results of rows whose context is split over several thread blocks.
+ */
+size_t tp_kv4_attention_workspace_size(int t, int64_t n, int64_t nseq, int heads, int kv_heads, int head_dim);
+
+/*
+ * Attention of the n rows over the cached tokens of their sequences,
+ *     out = softmax_j(scale * q . k_j) v_j
+ * for every rank and head, the keys and values being what the cache stands
+ * for.  The row at position i sees the tokens j <= i with window == 0, or
+ * j > i - window, or j < sinks (the first tokens, which stay visible when
+ * the window has left them).  A row that sees nothing (an empty sequence)
+ * gives 0.
+ *
+ *   q[r]    [n, heads * head_dim] bf16, row stride ldq: rank r's query
+ *           heads; query head i reads kv head i / (heads / kv_heads).
+ *   out[r]  [n, heads * head_dim] bf16, row stride ldo: what tp_linear_row
+ *           (o_proj) reads.
+ *   scale   finite; window, sinks >= 0.
+ *   workspace  tp_kv4_attention_workspace_size() bytes, 256-byte aligned;
+ *           overwritten.
+ * heads must be a multiple of kv_heads with at most 128 query heads per kv
+ * head (TP_ERR_NOT_DIVISIBLE, TP_ERR_UNSUPPORTED).  Statistics and sums are
+ * fp32; q enters the products exactly (as fp16 after a power-of-two
+ * scaling), the probabilities rounded to fp16.  The order of the sums is
+ * fixed by the sizes and lengths.
+ */
+tp_status tp_kv4_attention(int t, int64_t n, int64_t nseq, int heads, int kv_heads, int head_dim,
+                           const void* const* q, int64_t ldq, const void* const* pool, int64_t pages, int page_size,
+                           const int32_t* table, int64_t max_blocks, const int32_t* lens, const int32_t* cu_rows,
+                           float scale, int64_t window, int64_t sinks, void* workspace, size_t workspace_bytes,
+                           void* const* out, int64_t ldo, tp_stream stream);
+
+/* Workspace bytes of tp_kv_fork and tp_kv_compact for that many output rows
+ * and pages (0 for invalid arguments). */
+size_t tp_kv_pages_workspace_size(int64_t rows, int64_t pages);
+
+/*
+ * Fork, reorder, grow, shorten and free sequences: the page bookkeeping of
+ * one decode step, and the page copies it needs, without a host round trip.
+ * Output row i continues sequence parents[i] of the input table:
+ *   - parents[i] outside [0, rows_in) gives an empty row (a freed sequence);
+ *   - its length is lens[parent] + g, at least 0, g = grow[i] (or grow_all
+ *     when grow is NULL; negative to drop tokens), at most max_blocks *
+ *     page_size;
+ *   - it keeps its parent's pages up to min(old length, new length).  Pages
+ *     that several rows keep are shared.  A row that will write inside its
+ *     last kept page (the kept length is not a multiple of page_size and the
+ *     row grows) needs that page for itself: it gets a copy, unless every row
+ *     that keeps the page is such a writer, it is the first of them, and the
+ *     page is not held;
+ *   - pages for the new tokens come from the free pages, those that no
+ *     output row keeps and held does not name, lowest number first, dealt
+ *     out by row: the copy first, then the new pages in order.
+ * A page that no output row keeps is thereby free.  When pages run out the
+ * entries that could not be had are -1 and info[1] counts them; an input
+ * entry outside [0, pages) is kept as -1 and counted too.
+ *
+ *   pool[r]   NULL list, or rank r's pools of all layers,
+ *             [layers, pages, page_bytes], page_bytes a multiple of 16.
+ *   held      NULL, or [pages] uint8: non-zero for pages that someone else
+ *             holds (a prefix cache); they are neither dealt out nor
+ *             written.
+ *   table_out [rows_out, max_blocks] (unused entries -1), lens_out
+ *             [rows_out]; they must not overlap table and lens.
+ *   refs      [pages] int32: how many entries of table_out name each page.
+ *   info      [4] int32: pages in use (named or held), entries missing,
+ *             pages copied, input entries out of range.
+ */
+tp_status tp_kv_fork(int t, int64_t rows_in, int64_t rows_out, int64_t max_blocks, int page_size, int64_t pages,
+                     const int32_t* table, const int32_t* lens, const int32_t* parents, const int32_t* grow,
+                     int32_t grow_all, const uint8_t* held, void* const* pool, int64_t layers, int64_t page_bytes,
+                     int32_t* table_out, int32_t* lens_out, int32_t* refs, int32_t* info,
+                     void* workspace, size_t workspace_bytes, tp_stream stream);
+
+/*
+ * Move the pages in use to the front of the pool.  With L pages in use
+ * (named by the first ceil(lens[i] / page_size) entries of a row, or held),
+ * the pages in use at or above L that are not held move, in ascending
+ * order, to the free pages below L in ascending order; every table entry
+ * follows.  Without held pages the pages [L, pages) are free afterwards.
+ * Arguments as tp_kv_fork; info[2] counts the pages moved.
+ */
+tp_status tp_kv_compact(int t, int64_t rows, int64_t max_blocks, int page_size, int64_t pages,
+                        const int32_t* table, const int32_t* lens, const uint8_t* held,
+                        void* const* pool, int64_t layers, int64_t page_bytes,
+                        int32_t* table_out, int32_t* refs, int32_t* info,
+                        void* workspace, size_t workspace_bytes, tp_stream stream);
+
+#define TP_MAX_BEAMS 64
+/* Workspace bytes of tp_beam_select (0 for invalid arguments). */
+size_t tp_beam_workspace_size(int64_t items, int beams, int k, int64_t vocab);
+
+/*
+ * One step of beam search over vocab-sharded logits (lm_head_sharded's
+ * shards as they are; no gather): for every item the k best of its
+ * beams x vocab continuations by scores[item, beam] + log_softmax(logits)
+ * [token], best first, ties to the lowest (beam, token).
+ *
+ *   logits[r]  [items * beams, cols[r]] of dtype, row stride ldl[r] elements:
+ *              tokens [sum(cols[:r]), sum(cols[:r+1])); cols and ldl are host
+ *              arrays.  A shard of width 0 may be NULL.
+ *   scores     [items, beams] fp32: log-probabilities so far.
+ *   finished   NULL, or [items, beams] bytes: a non-zero beam is complete; its
+ *              only continuation is token `eos` with its score unchanged.
+ *   scores_out, rows_out, tokens_out  [items, k]: the new score, the row
+ *              item * beams + beam it continues (what tp_kv_fork takes as
+ *              parents), and the token.
+ * Logits of -inf are no continuations, nor are those of a row whose
+ * log-sum-exp is not finite or whose score is -inf or NaN.  Where fewer than
+ * k remain the rest are score -inf, row -1, token -1.  k <= TP_MAX_BEAMS,
+ * beams <= TP_MAX_BEAMS; vocab = sum(cols) < 2^31.  Scores are ordered as
+ * fp64 sums (the log-sum-exp is accumulated in fp64 across threads), so that
+ * rounding does not reorder neighbours, and stored as fp32.
+ */
+tp_status tp_beam_select(int t, int64_t items, int beams, int k, const int64_t* cols, const void* const* logits,
+                         const int64_t* ldl, tp_dtype dtype, const float* scores, const uint8_t* finished, int32_t eos,
+                         float* scores_out, int32_t* rows_out, int32_t* tokens_out,
+                         void* workspace, size_t workspace_bytes, tp_stream stream);
+
+/*
  * Synchronises `stream`, then returns and clears the library's device
  * status word: TP_ERR_TIMEOUT if a bounded device-side wait of an earlier
- * kernel expired, TP_ERR_CUDA if the stream reported an error, else TP_OK.
+ * kernel expired, TP_ERR_INVALID_ARG if one met a page table or row offset
+ * outside its range, TP_ERR_CUDA if the stream reported an error, else
+ * TP_OK.
  */
 tp_status tp_device_status(tp_stream stream);
 
@@ -460,6 +648,16 @@ tp_status tp_set_gemm_split(int mode, int max_clusters);
  * then returns.  The kernel always exits normally.
  */
 tp_status tp_debug_expire_wait(uint64_t limit_ns, tp_stream stream);
+
+/*
+ * Test hook for the cache's addressing (host logic only, the code the kernels
+ * run): the byte offset, in one rank's pool, of the 16-token block that holds
+ * token `position` of the sequence whose page table row is the HOST array
+ * row[max_blocks], for kv head `head`; -1 when the row does not reach that far
+ * or names a page outside [0, pages), and for sizes that are not provided.
+ */
+int64_t tp_debug_kv4_block(const int32_t* row, int64_t max_blocks, int64_t pages, int page_size, int kv_heads,
+                           int head_dim, int head, int64_t position);
 
 /*
  * Test hook for the host-side kernel choice (no CUDA call): the GEMM kernel

@@ -14,9 +14,19 @@ from ._lib import (  # noqa: F401
     load,
     prepare,
     tp_abi_version,
+    tp_beam_select,
+    tp_beam_workspace_size,
     tp_collective_count,
     tp_debug_expire_wait,
     tp_device_status,
+    tp_kv4_append,
+    tp_kv4_attention,
+    tp_kv4_attention_workspace_size,
+    tp_kv4_load,
+    tp_kv4_pool,
+    tp_kv_compact,
+    tp_kv_fork,
+    tp_kv_pages_workspace_size,
     tp_linear_col,
     tp_linear_row,
     tp_mlp_forward,

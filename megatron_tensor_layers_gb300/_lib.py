@@ -35,6 +35,9 @@ EXPORTED = [
     "tp_shard_gather", "tp_device_status", "tp_collective_count", "tp_reset_collective_count",
     "tp_debug_expire_wait", "tp_set_gemm_tile_n", "tp_mlp_forward_static", "tp_set_gemm_cta_pair", "tp_mlp_forward_host",
     "tp_reduce_scatter_rmsnorm", "tp_set_gemm_split", "tp_debug_gemm_plan", "tp_mlp_host_blocks",
+    "tp_kv4_page_bytes", "tp_kv4_append", "tp_kv4_load", "tp_kv4_attention_workspace_size", "tp_kv4_attention",
+    "tp_kv_pages_workspace_size", "tp_kv_fork", "tp_kv_compact", "tp_beam_workspace_size", "tp_beam_select",
+    "tp_debug_kv4_block",
 ]
 STATIC_SCRATCH_BYTES = 16 * 1024 * 1024
 
@@ -83,6 +86,19 @@ def load() -> ctypes.CDLL:
                                       I32, I32, P, P]),
         "tp_mlp_forward_static": (I32, [I32, I64, I64, I64, P, I64, P, P, I64, P, I32, I32, I32, P, I32, P]),
         "tp_mlp_host_blocks": (I32, [I64, I32, P, I32]),
+        "tp_debug_kv4_block": (I64, [P, I64, I64, I32, I32, I32, I32, I64]),
+        "tp_kv4_page_bytes": (ctypes.c_size_t, [I32, I32, I32]),
+        "tp_kv4_append": (I32, [I32, I64, I64, I32, I32, P, I64, P, I64, P, I64, I32, P, I64, P, P, P]),
+        "tp_kv4_load": (I32, [I32, I64, I64, I32, I32, P, I64, I32, P, I64, P, P, P, I64, P, I64, I32, P]),
+        "tp_kv4_attention_workspace_size": (ctypes.c_size_t, [I32, I64, I64, I32, I32, I32]),
+        "tp_kv4_attention": (I32, [I32, I64, I64, I32, I32, I32, P, I64, P, I64, I32, P, I64, P, P, ctypes.c_float, I64,
+                                   I64, P, ctypes.c_size_t, P, I64, P]),
+        "tp_kv_pages_workspace_size": (ctypes.c_size_t, [I64, I64]),
+        "tp_kv_fork": (I32, [I32, I64, I64, I64, I32, I64, P, P, P, P, ctypes.c_int32, P, P, I64, I64, P, P, P, P, P,
+                             ctypes.c_size_t, P]),
+        "tp_kv_compact": (I32, [I32, I64, I64, I32, I64, P, P, P, P, I64, I64, P, P, P, P, ctypes.c_size_t, P]),
+        "tp_beam_workspace_size": (ctypes.c_size_t, [I64, I32, I32, I64]),
+        "tp_beam_select": (I32, [I32, I64, I32, I32, P, P, P, I32, P, P, ctypes.c_int32, P, P, P, P, ctypes.c_size_t, P]),
     }
     for name, (res, args) in sig.items():
         f = getattr(lib, name)
@@ -720,3 +736,289 @@ def tp_reduce_scatter_rmsnorm(partials: Sequence[torch.Tensor], weight: torch.Te
             _ptr(weight), eps, MODES[mode], _ptr(residual_out), _ptr(out),
             _stream(stream))
     return residual_out, out
+
+
+# ----------------------------------------------------------------- decode loop: paged 4-bit cache, pages, beams
+
+I32S = (torch.int32,)
+KV_BLOCK = 16
+
+
+def tp_kv4_pool(pages: int, page_size: int, kv_heads: int, head_dim: int, *, layers: Optional[int] = None,
+                device="cuda") -> torch.Tensor:
+    """One rank's zeroed pool of the 4-bit cache, uint8 [pages, kv_heads,
+    page_size/16, 16 (head_dim + 8)], or [layers, ...] with `layers` (pool[l]
+    is then layer l's pool, and the whole is what tp_kv_fork and
+    tp_kv_compact take)."""
+    if not load().tp_kv4_page_bytes(page_size, kv_heads, head_dim):
+        raise ValueError("page_size must be 16, 32, 64 or 128, head_dim 64 or 128, kv_heads 1..1024")
+    shape = (pages, kv_heads, page_size // KV_BLOCK, KV_BLOCK * (head_dim + 8))
+    return torch.zeros(shape if layers is None else (layers, *shape), dtype=torch.uint8, device=device)
+
+
+def _pools(pools, dims: int):
+    """Checks every rank's pool and returns (t, pages, kv_heads, page_size, head_dim)."""
+    t = _shard_count("pools", pools)
+    p0 = _dense(("pools", 0), pools[0], dtypes=(torch.uint8,))
+    if p0.dim() != dims:
+        raise ValueError(f"pools[0] must have {dims} dimensions: a pool is [pages, kv_heads, page_size/16, "
+                         "16 (head_dim + 8)], with the layers in front where all are meant")
+    _denses("pools", pools, p0.shape, (torch.uint8,))
+    pages, kv, blocks, rec = p0.shape[-4:]
+    if rec % KV_BLOCK or rec // KV_BLOCK - 8 not in (64, 128) or blocks not in (1, 2, 4, 8):
+        raise ValueError(f"pools[0] has shape {tuple(p0.shape)}, which no page_size (16, 32, 64, 128) and head_dim "
+                         "(64, 128) gives")
+    return t, pages, kv, blocks * KV_BLOCK, rec // KV_BLOCK - 8
+
+
+def _seqs(table, lens, cu_rows, n: int) -> int:
+    """Checks the sequences of a call with n rows and returns how many there are."""
+    _dense("table", table, dtypes=I32S)
+    if table.dim() != 2 or table.shape[1] < 1:
+        raise ValueError("table must be [sequences, max_blocks]")
+    nseq = table.shape[0]
+    _dense("lens", lens, (nseq,), I32S)
+    if cu_rows is None:
+        if n != nseq:
+            raise ValueError(f"without cu_rows every sequence has one row: {n} rows, {nseq} sequences")
+    else:
+        _dense("cu_rows", cu_rows, (nseq + 1,), I32S)
+    return nseq
+
+
+def tp_kv4_append(k: Sequence[torch.Tensor], v: Sequence[torch.Tensor], pools: Sequence[torch.Tensor],
+                  table: torch.Tensor, lens: torch.Tensor, *, cu_rows: Optional[torch.Tensor] = None, stream=None):
+    """Quantise the rows k[r], v[r] [n, kv_heads * head_dim] (views of the
+    merged QKV output will do) to 4 bits and store them in rank r's pool as
+    the last tokens of their sequences (lens counts them).  cu_rows
+    [sequences + 1] cuts the rows into sequences; without it every sequence
+    has one row.  Returns pools."""
+    t, pages, kv, ps, hd = _pools(pools, 4)
+    if len(k) != t or len(v) != t:
+        raise ValueError("k, v and pools must hold the same number of shards")
+    n = _matrix(("k", 0), k[0], dtypes=BF16).shape[0]
+    ldk = _matrices("k", k, (n, kv * hd), BF16)
+    ldv = _matrices("v", v, (n, kv * hd), BF16)
+    nseq = _seqs(table, lens, cu_rows, n)
+    _on_gpu(k, v, pools, table, lens, cu_rows)
+    _launch("tp_kv4_append", t, n, nseq, kv, hd, _ptrs(k), ldk, _ptrs(v), ldv, _ptrs(pools), pages, ps, _ptr(table),
+            table.shape[1], _ptr(lens), _ptr(cu_rows), _stream(stream))
+    return pools
+
+
+def tp_kv4_load(pools: Sequence[torch.Tensor], table: torch.Tensor, lens: torch.Tensor, n: int, *,
+                cu_rows: Optional[torch.Tensor] = None, k: Optional[List[torch.Tensor]] = None,
+                v: Optional[List[torch.Tensor]] = None, dtype=torch.bfloat16, stream=None):
+    """What the cache holds for the last rows of the sequences (n in all, cut
+    by cu_rows as in tp_kv4_append): (k, v), lists of t [n, kv_heads *
+    head_dim] of dtype."""
+    t, pages, kv, ps, hd = _pools(pools, 4)
+    nseq = _seqs(table, lens, cu_rows, n)
+    dev = pools[0].device
+    if k is None:
+        k = [torch.empty((n, kv * hd), dtype=dtype, device=dev) for _ in range(t)]
+    if v is None:
+        v = [torch.empty((n, kv * hd), dtype=dtype, device=dev) for _ in range(t)]
+    if len(k) != t or len(v) != t:
+        raise ValueError("k, v and pools must hold the same number of shards")
+    _matrix(("k", 0), k[0], (n, kv * hd), BF16_F32)
+    ldk = _matrices("k", k, (n, kv * hd), (k[0].dtype,))
+    ldv = _matrices("v", v, (n, kv * hd), (k[0].dtype,))
+    _on_gpu(k, v, pools, table, lens, cu_rows)
+    _launch("tp_kv4_load", t, n, nseq, kv, hd, _ptrs(pools), pages, ps, _ptr(table), table.shape[1], _ptr(lens),
+            _ptr(cu_rows), _ptrs(k), ldk, _ptrs(v), ldv, _dt(k[0].dtype), _stream(stream))
+    return k, v
+
+
+def tp_kv4_attention_workspace_size(t: int, n: int, nseq: int, heads: int, kv_heads: int, head_dim: int) -> int:
+    return load().tp_kv4_attention_workspace_size(t, n, nseq, heads, kv_heads, head_dim)
+
+
+def tp_kv4_attention(q: Sequence[torch.Tensor], pools: Sequence[torch.Tensor], table: torch.Tensor, lens: torch.Tensor, *,
+                     cu_rows: Optional[torch.Tensor] = None, scale: Optional[float] = None, window: int = 0,
+                     sinks: int = 0, workspace: Optional[torch.Tensor] = None, out: Optional[List[torch.Tensor]] = None,
+                     stream=None):
+    """Attention of the rows q[r] [n, heads * head_dim] (the last tokens of
+    their sequences, cut by cu_rows; already appended) over the 4-bit cache.
+    A row at position i sees tokens j <= i; with window > 0 only j > i -
+    window and the first `sinks`.  scale defaults to head_dim ** -0.5.
+    Returns the list of [n, heads * head_dim] bf16 outputs, which
+    tp_linear_row (o_proj) takes as x."""
+    t, pages, kv, ps, hd = _pools(pools, 4)
+    if len(q) != t:
+        raise ValueError("q and pools must hold the same number of shards")
+    n, width = _matrix(("q", 0), q[0], dtypes=BF16).shape
+    ldq = _matrices("q", q, (n, width), BF16)
+    if width % hd or (width // hd) % kv:
+        raise ValueError(f"q[0] has {width} columns, expected a multiple of kv_heads * head_dim = {kv * hd}")
+    heads = width // hd
+    nseq = _seqs(table, lens, cu_rows, n)
+    if window < 0 or sinks < 0:
+        raise ValueError("window and sinks must not be negative")
+    if out is None:
+        out = [torch.empty((n, width), dtype=torch.bfloat16, device=q[0].device) for _ in range(t)]
+    if len(out) != t:
+        raise ValueError("out must hold one tensor per shard")
+    ldo = _matrices("out", out, (n, width), BF16)
+    if workspace is None:
+        need = tp_kv4_attention_workspace_size(t, n, nseq, heads, kv, hd)
+        workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=q[0].device)
+    _dense("workspace", workspace)
+    _on_gpu(q, pools, table, lens, cu_rows, workspace, out)
+    _launch("tp_kv4_attention", t, n, nseq, heads, kv, hd, _ptrs(q), ldq, _ptrs(pools), pages, ps, _ptr(table),
+            table.shape[1], _ptr(lens), _ptr(cu_rows), hd ** -0.5 if scale is None else scale, window, sinks,
+            _ptr(workspace), workspace.numel() * workspace.element_size(), _ptrs(out), ldo, _stream(stream))
+    return out
+
+
+def _page_args(table, lens, pools, page_size, pages, held, rows_out, table_out, refs, info, workspace):
+    """What tp_kv_fork and tp_kv_compact share: checks, defaults, and (t, layers, page_bytes, page_size, pages)."""
+    t, layers, page_bytes = 1, 1, 16
+    if pools is not None:
+        t, pages, kv, page_size, hd = _pools(pools, 5)
+        layers, page_bytes = pools[0].shape[0], kv * page_size * (hd + 8)
+    elif page_size is None or pages is None:
+        raise ValueError("page_size and pages are needed without pools")
+    _dense("table", table, dtypes=I32S)
+    if table.dim() != 2 or table.shape[1] < 1:
+        raise ValueError("table must be [rows, max_blocks]")
+    rows, mb = table.shape
+    _dense("lens", lens, (rows,), I32S)
+    if held is not None:
+        _dense("held", held, (pages,), (torch.uint8, torch.bool))
+    dev = table.device
+    if table_out is None:
+        table_out = torch.empty((rows_out, mb), dtype=torch.int32, device=dev)
+    if refs is None:
+        refs = torch.empty(pages, dtype=torch.int32, device=dev)
+    if info is None:
+        info = torch.empty(4, dtype=torch.int32, device=dev)
+    if workspace is None:
+        workspace = torch.empty(max(load().tp_kv_pages_workspace_size(rows_out, pages), 256), dtype=torch.uint8, device=dev)
+    _dense("table_out", table_out, (rows_out, mb), I32S)
+    _dense("refs", refs, (pages,), I32S)
+    _dense("info", info, (4,), I32S)
+    _dense("workspace", workspace)
+    return t, layers, page_bytes, page_size, pages, table_out, refs, info, workspace
+
+
+def tp_kv_pages_workspace_size(rows: int, pages: int) -> int:
+    return load().tp_kv_pages_workspace_size(rows, pages)
+
+
+def tp_kv_fork(table: torch.Tensor, lens: torch.Tensor, parents: torch.Tensor, pools: Optional[Sequence[torch.Tensor]], *,
+               grow=1, held: Optional[torch.Tensor] = None, page_size: Optional[int] = None, pages: Optional[int] = None,
+               table_out: Optional[torch.Tensor] = None, lens_out: Optional[torch.Tensor] = None,
+               refs: Optional[torch.Tensor] = None, info: Optional[torch.Tensor] = None,
+               workspace: Optional[torch.Tensor] = None, stream=None):
+    """New sequences from old ones: row i continues sequence parents[i] (any
+    other number: an empty row), grown by `grow` tokens (an int, or an int32
+    tensor [rows_out]; negative drops tokens).  Pages are shared; a partly
+    filled last page that several rows would write is copied; pages that
+    nobody keeps are free and dealt out again, lowest first.  pools[r] is
+    rank r's [layers, pages, kv_heads, page_size/16, bytes], or None for the
+    bookkeeping alone (page_size and pages are then given).  Returns
+    (table_out, lens_out, refs, info), info = pages in use, entries missing,
+    pages copied, input entries out of range."""
+    _dense("parents", parents, dtypes=I32S)
+    if parents.dim() != 1:
+        raise ValueError("parents must be a 1-D int32 tensor")
+    m = parents.shape[0]
+    t, layers, page_bytes, page_size, pages, table_out, refs, info, workspace = _page_args(
+        table, lens, pools, page_size, pages, held, m, table_out, refs, info, workspace)
+    if lens_out is None:
+        lens_out = torch.empty(m, dtype=torch.int32, device=table.device)
+    _dense("lens_out", lens_out, (m,), I32S)
+    grow_t = grow if isinstance(grow, torch.Tensor) else None
+    if grow_t is not None:
+        _dense("grow", grow_t, (m,), I32S)
+    elif not -2 ** 31 <= grow < 2 ** 31:
+        raise ValueError("grow must fit 32 bits")
+    _on_gpu(table, lens, parents, grow_t, held, pools, table_out, lens_out, refs, info, workspace)
+    _launch("tp_kv_fork", t, table.shape[0], m, table.shape[1], page_size, pages, _ptr(table), _ptr(lens), _ptr(parents),
+            _ptr(grow_t), 0 if grow_t is not None else grow, _ptr(held), _ptrs(pools), layers, page_bytes,
+            _ptr(table_out), _ptr(lens_out), _ptr(refs), _ptr(info), _ptr(workspace),
+            workspace.numel() * workspace.element_size(), _stream(stream))
+    return table_out, lens_out, refs, info
+
+
+def tp_kv_compact(table: torch.Tensor, lens: torch.Tensor, pools: Optional[Sequence[torch.Tensor]], *,
+                  held: Optional[torch.Tensor] = None, page_size: Optional[int] = None, pages: Optional[int] = None,
+                  table_out: Optional[torch.Tensor] = None, refs: Optional[torch.Tensor] = None,
+                  info: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None, stream=None):
+    """Move the pages in use to the front of the pool.  Returns (table_out,
+    refs, info); arguments and results as in tp_kv_fork, info[2] counting the
+    pages moved."""
+    rows = table.shape[0] if isinstance(table, torch.Tensor) and table.dim() == 2 else 0
+    t, layers, page_bytes, page_size, pages, table_out, refs, info, workspace = _page_args(
+        table, lens, pools, page_size, pages, held, rows, table_out, refs, info, workspace)
+    _on_gpu(table, lens, held, pools, table_out, refs, info, workspace)
+    _launch("tp_kv_compact", t, rows, table.shape[1], page_size, pages, _ptr(table), _ptr(lens), _ptr(held), _ptrs(pools),
+            layers, page_bytes, _ptr(table_out), _ptr(refs), _ptr(info), _ptr(workspace),
+            workspace.numel() * workspace.element_size(), _stream(stream))
+    return table_out, refs, info
+
+
+MAX_BEAMS = 64
+
+
+def tp_beam_workspace_size(items: int, beams: int, k: int, vocab: int) -> int:
+    return load().tp_beam_workspace_size(items, beams, k, vocab)
+
+
+def tp_beam_select(logits: Sequence[Optional[torch.Tensor]], scores: torch.Tensor, k: int, *,
+                   finished: Optional[torch.Tensor] = None, eos: int = -1, scores_out: Optional[torch.Tensor] = None,
+                   rows_out: Optional[torch.Tensor] = None, tokens_out: Optional[torch.Tensor] = None,
+                   workspace: Optional[torch.Tensor] = None, stream=None):
+    """The k best continuations of every item's beams by scores[item, beam] +
+    log_softmax(logits)[token], best first.  logits: the vocab shards
+    [items * beams, width_r] of lm_head_sharded (per_shard=True), or one
+    gathered matrix in a list.  A finished beam continues with `eos` alone,
+    its score unchanged.  Returns (scores, rows, tokens) [items, k]; rows
+    (item * beams + beam) are tp_kv_fork's parents.  Missing continuations are
+    score -inf, row -1, token -1."""
+    t = _shard_count("logits", logits)
+    _dense("scores", scores, dtypes=(torch.float32,))
+    if scores.dim() != 2:
+        raise ValueError("scores must be [items, beams]")
+    items, beams = scores.shape
+    if not 1 <= beams <= MAX_BEAMS or not 1 <= k <= MAX_BEAMS:
+        raise ValueError(f"beams and k must be in 1..{MAX_BEAMS}")
+    ref = next((x for x in logits if x is not None), None)
+    if ref is None:
+        raise ValueError("logits holds no shard")
+    _tensor("logits shard", ref, dtypes=BF16_F32)
+    cols, ldl, vocab = (ctypes.c_int64 * t)(), (ctypes.c_int64 * t)(), 0
+    for r in range(t):
+        if logits[r] is None:
+            continue
+        x = _tensor(("logits", r), logits[r], dtypes=(ref.dtype,))
+        if x.dim() != 2 or x.shape[0] != items * beams:
+            raise ValueError(f"logits[{r}] must be [{items * beams}, width]")
+        if x.shape[1] and items:
+            _matrix(("logits", r), x)
+        cols[r], ldl[r] = x.shape[1], max(x.stride(0), x.shape[1])
+        vocab += x.shape[1]
+    if finished is not None:
+        _dense("finished", finished, (items, beams), (torch.uint8, torch.bool))
+        if not 0 <= eos < vocab:
+            raise ValueError("eos must be a token of the vocabulary when finished is given")
+    dev = scores.device
+    if scores_out is None:
+        scores_out = torch.empty((items, k), dtype=torch.float32, device=dev)
+    if rows_out is None:
+        rows_out = torch.empty((items, k), dtype=torch.int32, device=dev)
+    if tokens_out is None:
+        tokens_out = torch.empty((items, k), dtype=torch.int32, device=dev)
+    _dense("scores_out", scores_out, (items, k), (torch.float32,))
+    _dense("rows_out", rows_out, (items, k), I32S)
+    _dense("tokens_out", tokens_out, (items, k), I32S)
+    if workspace is None:
+        need = tp_beam_workspace_size(items, beams, k, max(vocab, 1))
+        workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=dev)
+    _dense("workspace", workspace)
+    _on_gpu(logits, scores, finished, scores_out, rows_out, tokens_out, workspace)
+    _launch("tp_beam_select", t, items, beams, k, cols, _ptrs(logits), ldl, _dt(ref.dtype), _ptr(scores), _ptr(finished),
+            eos, _ptr(scores_out), _ptr(rows_out), _ptr(tokens_out), _ptr(workspace),
+            workspace.numel() * workspace.element_size(), _stream(stream))
+    return scores_out, rows_out, tokens_out

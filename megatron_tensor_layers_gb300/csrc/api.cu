@@ -62,6 +62,8 @@ inline cudaStream_t cs(tp_stream s) { return reinterpret_cast<cudaStream_t>(s); 
 
 }  // namespace
 
+int* tpk::device_status_word() { return status_ptr(); }
+
 // tp_mlp_forward's workspace: H [n, f] bf16, then (unless the reduce is
 // fused) t partials [n, h]; that much is required.  A fused reduce of more
 // than 128 rows (CTA-pair tiles) may also use the stream-K tail area of its

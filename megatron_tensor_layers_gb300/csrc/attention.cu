@@ -1,0 +1,839 @@
+// Attention over the paged 4-bit cache for few rows per sequence (decode,
+// speculation): one pass over the cached codes, bound by their bytes.
+//
+// Mathematics.  With key j = s_j u_j + b_j (u_j the codes),
+//     x_j = c (s_j (q . u_j) + b_j sum(q)),      c = scale log2(e),
+// so the matrix product runs on the bare codes and step and base enter per
+// (token, column) afterwards.  With value j = s'_j u'_j + b'_j,
+//     out = (sum_j (p_j s'_j) u'_j + sum_j p_j b'_j) / sum_j p_j,  p_j = 2^(x_j - m).
+//
+// Codes to operands.  A code is four bits of an fp16 whose other bits are zero:
+// the subnormal u 2^-24, exact, with no bias to subtract.  Of a 32-bit word of
+// eight codes, `w & 0x000f000f` is a pair of such numbers, `w & 0x00f000f0` a
+// pair scaled by 16, and w >> 8 gives the other two: five instructions for
+// eight codes.  The 16 is taken back in q (keys) and in the output's scale
+// (values), both exact.  q is scaled by a power of two per row so that its
+// largest element is in [2^10, 2^11): a bf16 q is exact in fp16 down to 2^-24 of
+// that.  p s' is scaled by 2^(13 - E), E the exponent of the largest step seen,
+// and rounded to fp16 (2^-11 relative): the one rounding of the products.
+//
+// Split.  The unit of work is a cache block (16 tokens).  All blocks of all
+// (sequence, row tile, head) items form one line, cut into equal parts, one for
+// each worker of WS warps (8, or fewer when items are short, so that a worker
+// then takes whole items); the warps of a worker share each item's part of its
+// range and merge through shared memory.  A worker's part of an item that it
+// does not hold whole goes to the workspace, and a second kernel adds the parts
+// in order.  The cut depends on lengths the host does not know, so every thread
+// block finds its own.
+//
+// Each warp feeds itself: a ring of 2 stages of 4 blocks, filled by bulk copies
+// (a block is one contiguous record) and read as mma.sync fragments without
+// conflicts: the transposed products K q^T and V^T p^T have the tokens and the
+// head dimension as their 16 rows and only 8 columns, so 8 query heads of a
+// group fill them.  tcgen05 would want 128 rows of them.
+#include <algorithm>
+
+#include "kv4.cuh"
+
+namespace tpk {
+namespace {
+
+constexpr int kWarps = 8;
+constexpr int kStageBlocks = 4;
+constexpr int kStages = 2;
+constexpr int kPShift = 13;          // p s' is held times 2^(kPShift - E)
+constexpr float kNegInf = -INFINITY;
+
+struct AttnArgs {
+    KvSeqs seqs;
+    KvPools pools;
+    const uint16_t* q[TP_MAX_SHARDS];
+    uint16_t* out[TP_MAX_SHARDS];
+    int64_t ldq, ldo;
+    int group;
+    float scale_log2;                // scale * log2(e)
+    int window, sinks;
+    uint8_t* ws;
+};
+
+// Head of the workspace: what the second kernel needs to know of the cut.
+struct Cut {
+    int64_t total;                   // units of all items
+    int workers, ws;                 // parts, warps of a worker
+};
+// A worker whose range begins inside an item describes it.
+struct Split {
+    int64_t begin;                   // first unit of the item on the line
+    int units;                       // of the item; 0: the worker begins with an item's first unit
+    int first_row, rows, tile, head;
+    int pad;
+};
+
+constexpr size_t kSplitAt = 256;
+
+__host__ __device__ constexpr size_t slot_floats(int cols, int hd) { return static_cast<size_t>(cols) * (hd + 2); }
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                        uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+    uint32_t r;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+    return r;
+}
+
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+                 "l"(src), "r"(bytes), "r"(bar)
+                 : "memory");
+}
+
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
+    return v;
+}
+__device__ __forceinline__ uint2 lds64(uint32_t a) {
+    uint2 v;
+    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
+    return v;
+}
+__device__ __forceinline__ uint32_t lds32(uint32_t a) {
+    uint32_t v;
+    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a));
+    return v;
+}
+
+// What one sequence asks for: its rows, and the blocks that any of them sees:
+// [0, front) for the sinks, then [start, start + units - front).
+struct Need {
+    int first_row, rows, len;
+    int front, start, blocks;        // blocks: how many of the units are cache blocks
+    int units, tiles;                // units >= 1 per item (an item that sees nothing writes zeros)
+};
+
+__device__ __forceinline__ Need seq_need(const AttnArgs& a, int s, int cols_per_tile) {
+    Need n;
+    const SeqRows r = seq_rows(a.seqs, s);
+    n.first_row = r.first;
+    n.rows = r.count;
+    n.len = max(a.seqs.lens[s], 0);
+    const int64_t cols = static_cast<int64_t>(r.count) * a.group;
+    n.tiles = static_cast<int>((cols + cols_per_tile - 1) / cols_per_tile);
+    const int64_t low = a.window > 0 ? static_cast<int64_t>(n.len) - r.count - a.window + 1 : 0;
+    const int lo = low > 0 ? static_cast<int>(low) : 0;
+    n.front = lo > 0 ? (min(a.sinks, lo) + kKvBlock - 1) / kKvBlock : 0;
+    n.start = max(lo / kKvBlock, n.front);
+    int64_t end = (static_cast<int64_t>(n.len) + kKvBlock - 1) / kKvBlock;
+    const int64_t most = a.seqs.max_blocks << a.pools.page_shift;
+    if (end > most) {                // tokens past the table are not there
+        if (r.count > 0) raise_status(a.seqs.status, TP_ERR_INVALID_ARG);
+        end = most;
+    }
+    n.front = min(n.front, static_cast<int>(end));
+    n.blocks = n.front + max(0, static_cast<int>(end) - n.start);
+    n.units = max(n.blocks, 1);
+    return n;
+}
+
+__device__ __forceinline__ int64_t seq_weight(const AttnArgs& a, int s, int cols_per_tile, int heads) {
+    const Need n = seq_need(a, s, cols_per_tile);
+    return static_cast<int64_t>(n.units) * n.tiles * heads;
+}
+
+// First unit of part b of `workers` equal parts (the first total % workers parts hold one more);
+// workers <= total.
+__device__ __forceinline__ int64_t part_begin(int64_t total, int workers, int b) {
+    const int64_t q = total / workers, r = total - q * workers;
+    return q * b + min(static_cast<int64_t>(b), r);
+}
+
+// The part that holds unit u.
+__device__ __forceinline__ int worker_of(int64_t total, int workers, int64_t u) {
+    const int64_t q = total / workers, r = total - q * workers;
+    return static_cast<int>(u < r * (q + 1) ? u / (q + 1) : r + (u - r * (q + 1)) / q);
+}
+
+// A position on the line of units, walked item by item.
+struct Cursor {
+    int64_t left;                    // units of the worker's range from here on
+    int s, tile, head, off;          // current item and the unit in it
+    Need n;
+    __device__ __forceinline__ int count() const { return static_cast<int>(min(static_cast<int64_t>(n.units - off), left)); }
+    __device__ __forceinline__ void next(const AttnArgs& a, int cols_per_tile, int heads) {
+        const int c = count();
+        left -= c;
+        off += c;
+        if (left <= 0) return;
+        off = 0;                     // more of the range left: the item is done
+        if (++head < heads) return;
+        head = 0;
+        if (++tile < n.tiles) return;
+        tile = 0;
+        do {
+            ++s;
+            if (s >= a.seqs.nseq) {
+                left = 0;
+                return;
+            }
+            n = seq_need(a, s, cols_per_tile);
+        } while (n.tiles == 0);
+    }
+};
+
+template <int HD, int NT>
+struct Cfg {
+    static constexpr int COLS = 8 * NT;
+    static constexpr int MT = HD / 16;                       // 16-row tiles of the output's dimensions
+    static constexpr int STAGE = kStageBlocks * KvBlock<HD>::BYTES;
+    static constexpr int RING = kWarps * kStages * STAGE;
+    static constexpr int MERGE = (MT * 4 + 4) * NT * 32 * 4;  // accumulators, maxima and sums of one warp
+    static constexpr int SMEM = RING + kWarps / 2 * MERGE;
+};
+
+template <int HD, int NT>
+__global__ void __launch_bounds__(kWarps * 32, 1) kv4_attention_kernel(const __grid_constant__ AttnArgs a) {
+    using B = KvBlock<HD>;
+    using C = Cfg<HD, NT>;
+    constexpr int MT = C::MT, COLS = C::COLS;
+    extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ __align__(8) uint64_t bars[kWarps * kStages];
+    __shared__ int stage_mask[kWarps * kStages];
+    __shared__ int64_t scan[kWarps];
+    __shared__ int64_t s_items;
+    __shared__ Cursor s_cursor[kWarps];
+    __shared__ int s_abort;
+
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int g = lane >> 2, t4 = lane & 3;
+    const int heads = a.pools.t * a.pools.kv_heads;
+
+    if (tid == 0) s_abort = 0;
+    if (lane == 0)
+        for (int i = 0; i < kStages; ++i) mbar_init(smem_u32(&bars[warp * kStages + i]), 1);
+    fence_barrier_init();
+    pdl_wait();
+    pdl_trigger();
+
+    // ---- the cut: total units, items, then where each of this block's workers begins
+    int64_t mine = 0, items = 0;
+    const int per = (a.seqs.nseq + kWarps * 32 - 1) / (kWarps * 32);
+    for (int s = tid * per; s < min(a.seqs.nseq, (tid + 1) * per); ++s) {
+        const Need n = seq_need(a, s, COLS);
+        mine += static_cast<int64_t>(n.units) * n.tiles * heads;
+        items += static_cast<int64_t>(n.tiles) * heads;
+    }
+    int64_t before = mine;
+#pragma unroll
+    for (int m = 1; m < 32; m <<= 1) {
+        const int64_t v = __shfl_up_sync(0xffffffffu, before, m);
+        if (lane >= m) before += v;
+        items += __shfl_xor_sync(0xffffffffu, items, m);
+    }
+    if (tid == 0) s_items = 0;
+    if (lane == 31) scan[warp] = before;
+    __syncthreads();
+    if (lane == 0 && items != 0) atomicAdd(reinterpret_cast<unsigned long long*>(&s_items), static_cast<unsigned long long>(items));
+    int64_t total = 0, base = 0;
+    for (int i = 0; i < kWarps; ++i) {
+        if (i < warp) base += scan[i];
+        total += scan[i];
+    }
+    before += base - mine;           // units before this thread's sequences
+    __syncthreads();
+    if (total == 0) {
+        if (blockIdx.x == 0 && tid == 0) *reinterpret_cast<Cut*>(a.ws) = Cut{0, 0, 0};
+        return;
+    }
+    // Warps of a worker: 8 while the average item has at least 32 blocks (4 for each warp, one
+    // stage), fewer below.  At least 4 blocks for each warp where there are few units in all.
+    int ws = kWarps;
+    while (ws > 1 && total < static_cast<int64_t>(4 * ws) * s_items) ws >>= 1;
+    const int groups = kWarps / ws;
+    const int workers = static_cast<int>(
+        max(static_cast<int64_t>(1), min(static_cast<int64_t>(gridDim.x) * groups, (total + 4 * ws - 1) / (4 * ws))));
+    for (int i = 0; i < groups; ++i) {
+        const int w = i * gridDim.x + blockIdx.x;
+        const int64_t begin = w < workers ? part_begin(total, workers, w) : total;
+        const int64_t end = w < workers ? part_begin(total, workers, w + 1) : total;
+        if (begin >= end) {
+            if (tid == 0) s_cursor[i].left = 0;
+            continue;
+        }
+        if (begin >= before && begin < before + mine) {      // one thread's sequences hold the beginning
+            int64_t u = begin - before;
+            int s = tid * per;
+            while (true) {
+                const int64_t w_s = seq_weight(a, s, COLS, heads);
+                if (u < w_s) break;
+                u -= w_s;
+                ++s;
+            }
+            Cursor c;
+            c.left = end - begin;
+            c.s = s;
+            c.n = seq_need(a, s, COLS);
+            const int item = static_cast<int>(u / c.n.units);
+            c.off = static_cast<int>(u - static_cast<int64_t>(item) * c.n.units);
+            c.tile = item / heads;
+            c.head = item - c.tile * heads;
+            s_cursor[i] = c;
+            Split sp;
+            sp.begin = begin - c.off;
+            sp.units = c.off > 0 ? c.n.units : 0;
+            sp.first_row = c.n.first_row;
+            sp.rows = c.n.rows;
+            sp.tile = c.tile;
+            sp.head = c.head;
+            sp.pad = 0;
+            reinterpret_cast<Split*>(a.ws + kSplitAt)[w] = sp;
+        }
+    }
+    if (blockIdx.x == 0 && tid == 0) {
+        Cut cut;
+        cut.total = total;
+        cut.workers = workers;
+        cut.ws = ws;
+        *reinterpret_cast<Cut*>(a.ws) = cut;
+    }
+    __syncthreads();
+
+    const int grp = warp / ws, wi = warp % ws;
+    const int worker = grp * gridDim.x + blockIdx.x;
+    float* slots = reinterpret_cast<float*>(a.ws + kSplitAt + static_cast<size_t>(gridDim.x) * kWarps * sizeof(Split));
+
+    Cursor cur = s_cursor[grp];      // the item being computed
+    if (cur.left <= 0) return;       // the whole worker
+    Cursor ahead = cur;              // the item being loaded
+    bool first_segment = true;
+
+    // ---- loading
+    const uint32_t ring = smem_u32(smem) + warp * kStages * C::STAGE;
+    const uint32_t my_bars = smem_u32(&bars[warp * kStages]);
+    int load_u = ahead.off + static_cast<int>(static_cast<int64_t>(ahead.count()) * wi / ws);
+    int load_end = ahead.off + static_cast<int>(static_cast<int64_t>(ahead.count()) * (wi + 1) / ws);
+    int batch_u = -(1 << 30);        // lane l holds the offset of unit batch_u + l
+    int64_t batch_off = -1;
+    int issued = 0;
+    auto load_stage = [&]() {
+        while (load_u >= load_end) {
+            ahead.next(a, COLS, heads);
+            if (ahead.left <= 0) return;
+            load_u = ahead.off + static_cast<int>(static_cast<int64_t>(ahead.count()) * wi / ws);
+            load_end = ahead.off + static_cast<int>(static_cast<int64_t>(ahead.count()) * (wi + 1) / ws);
+            batch_u = -(1 << 30);
+        }
+        const int cnt = min(kStageBlocks, load_end - load_u);
+        const int rank = ahead.head / a.pools.kv_heads;
+        if (load_u + cnt > batch_u + 32) {
+            batch_u = load_u;
+            const int u = load_u + lane;
+            batch_off = -1;
+            if (u < load_end && u < ahead.n.blocks) {
+                const int block = u < ahead.n.front ? u : ahead.n.start + u - ahead.n.front;
+                batch_off = kv_block_offset(a.seqs.table + ahead.s * a.seqs.max_blocks, a.seqs.max_blocks,
+                                            a.pools.pages, a.pools.page_shift, a.pools.kv_heads,
+                                            ahead.head - rank * a.pools.kv_heads, block, B::BYTES);
+                if (batch_off < 0) raise_status(a.seqs.status, TP_ERR_INVALID_ARG);
+            }
+        }
+        const int64_t off = __shfl_sync(0xffffffffu, batch_off, (load_u - batch_u + lane) & 31);
+        const bool go = lane < cnt && off >= 0;
+        const uint32_t mask = __ballot_sync(0xffffffffu, go);
+        const int st = issued % kStages;
+        const uint32_t bar = my_bars + st * 8;
+        if (lane == 0) {
+            stage_mask[warp * kStages + st] = static_cast<int>(mask);
+            mbar_arrive_expect_tx(bar, __popc(mask) * B::BYTES);
+        }
+        __syncwarp();
+        if (go) bulk_load(ring + st * C::STAGE + lane * B::BYTES, a.pools.pool[rank] + off, B::BYTES, bar);
+        ++issued;
+        load_u += cnt;
+    };
+    for (int i = 0; i < kStages; ++i) load_stage();
+
+    // ---- computing
+    const int tok = (g & 1) ? 4 + ((g >> 1) ^ 1) : g >> 1;   // token of row g of a key tile; row g + 8: tok + 8
+    bool dead = false;
+    int used = 0;
+    while (true) {
+        const int seg_off = cur.off, seg_n = cur.count();
+        const int u0 = seg_off + static_cast<int>(static_cast<int64_t>(seg_n) * wi / ws);
+        const int u1 = seg_off + static_cast<int>(static_cast<int64_t>(seg_n) * (wi + 1) / ws);
+        const int rank = cur.head / a.pools.kv_heads, kvh = cur.head - rank * a.pools.kv_heads;
+        const int cols = cur.n.rows * a.group - cur.tile * COLS;         // columns left from this tile on
+        const int pos0 = cur.n.len - cur.n.rows;                        // position of the sequence's first row
+
+        // q as B fragments; per-column scale of the products, and sum(q), both times scale log2(e)
+        uint32_t qf[NT][HD / 16][2];
+        float cmul[NT][2], cadd[NT][2];
+        int cpos[NT][2];
+        int row_lo = 0x7fffffff, row_hi = -1;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            const int ci = nt * 8 + g;
+            const bool have = ci < cols;
+            const int cc = cur.tile * COLS + ci;
+            const int r = have ? cc / a.group : 0;
+            const int h = cc - r * a.group;
+            constexpr int D = HD / 4;                                    // elements of this lane
+            uint32_t raw[D / 2];
+            const uint4* src = reinterpret_cast<const uint4*>(a.q[rank] + (cur.n.first_row + r) * a.ldq +
+                                                              (kvh * a.group + h) * HD + t4 * D);
+#pragma unroll
+            for (int i = 0; i < D / 8; ++i) {
+                const uint4 v = have ? __ldg(src + i) : make_uint4(0, 0, 0, 0);
+                raw[4 * i] = v.x, raw[4 * i + 1] = v.y, raw[4 * i + 2] = v.z, raw[4 * i + 3] = v.w;
+            }
+            uint32_t top = 0;
+            float sum = 0.0f;
+#pragma unroll
+            for (int i = 0; i < D / 2; ++i) {
+                top = max(top, max(raw[i] & 0x7fffu, (raw[i] >> 16) & 0x7fffu));
+                sum += __uint_as_float(raw[i] << 16) + __uint_as_float(raw[i] & 0xffff0000u);
+            }
+#pragma unroll
+            for (int m = 1; m < 4; m <<= 1) {
+                top = max(top, __shfl_xor_sync(0xffffffffu, top, m));
+                sum += __shfl_xor_sync(0xffffffffu, sum, m);
+            }
+            // 2^k with the row's largest element in [2^10, 2^11); k within the fp32 exponents
+            const int k = min(10 - (static_cast<int>(top >> 7) - 127), 126);
+            const float up = __uint_as_float(static_cast<uint32_t>(k + 127) << 23);
+            const float up16 = up * 0.0625f;
+#pragma unroll
+            for (int j = 0; j < D / 8; ++j) {                            // a word of eight codes
+                float x[8];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    x[2 * i] = __uint_as_float(raw[4 * j + i] << 16);
+                    x[2 * i + 1] = __uint_as_float(raw[4 * j + i] & 0xffff0000u);
+                }
+                qf[nt][2 * j][0] = pack_f16x2(x[0] * up, x[4] * up);
+                qf[nt][2 * j][1] = pack_f16x2(x[1] * up16, x[5] * up16);
+                qf[nt][2 * j + 1][0] = pack_f16x2(x[2] * up, x[6] * up);
+                qf[nt][2 * j + 1][1] = pack_f16x2(x[3] * up16, x[7] * up16);
+            }
+            const float mul = a.scale_log2 * __uint_as_float(static_cast<uint32_t>(min(24 - k, 127) + 127) << 23);
+            const float add = a.scale_log2 * sum;
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int from = (2 * t4 + e) * 4;
+                cmul[nt][e] = __shfl_sync(0xffffffffu, mul, from);
+                cadd[nt][e] = __shfl_sync(0xffffffffu, add, from);
+                const int ce = nt * 8 + 2 * t4 + e;
+                cpos[nt][e] = ce < cols ? pos0 + (cur.tile * COLS + ce) / a.group : -1;
+            }
+        }
+        row_lo = pos0 + (cur.tile * COLS) / a.group;
+        row_hi = pos0 + (cur.tile * COLS + min(cols, COLS) - 1) / a.group;
+
+        float acc[NT][MT][4];
+        float mx[NT][2], sum[NT][2], corr[NT][2];
+        // exponent field of the largest value step, at least 16 so that 2^(kPShift - E) stays finite
+        int vexp = 16;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+            for (int i = 0; i < MT; ++i)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) acc[nt][i][e] = 0.0f;
+#pragma unroll
+            for (int e = 0; e < 2; ++e) mx[nt][e] = kNegInf, sum[nt][e] = 0.0f, corr[nt][e] = 0.0f;
+        }
+
+        for (int u = u0; u < u1; u += kStageBlocks) {
+            const int cnt = min(kStageBlocks, u1 - u);
+            const int st = used % kStages;
+            if (!dead) dead = !mbar_wait_warp(my_bars + st * 8, (used / kStages) & 1, &s_abort, a.seqs.status);
+            const uint32_t mask = dead ? 0u : static_cast<uint32_t>(stage_mask[warp * kStages + st]);
+            const uint32_t buf = ring + st * C::STAGE;
+
+            // scores of up to 64 tokens
+            float x[kStageBlocks][NT][4];
+            uint32_t vp[kStageBlocks][2];
+            float cmax[NT][2];
+            uint32_t vtop = 0;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) cmax[nt][0] = cmax[nt][1] = kNegInf;
+#pragma unroll
+            for (int i = 0; i < kStageBlocks; ++i) {
+                vp[i][0] = vp[i][1] = 0;
+                if (!((mask >> i) & 1)) {
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) x[i][nt][e] = kNegInf;
+                    continue;
+                }
+                const uint32_t rec = buf + i * B::BYTES;
+                uint32_t wa[HD / 32], wb[HD / 32];
+                const uint32_t ka = rec + B::KEYS + tok * B::ROW + t4 * (B::ROW / 4);
+                if constexpr (HD == 128) {
+                    const uint4 p = lds128(ka), q = lds128(ka + 8 * B::ROW);
+                    wa[0] = p.x, wa[1] = p.y, wa[2] = p.z, wa[3] = p.w;
+                    wb[0] = q.x, wb[1] = q.y, wb[2] = q.z, wb[3] = q.w;
+                } else {
+                    const uint2 p = lds64(ka), q = lds64(ka + 8 * B::ROW);
+                    wa[0] = p.x, wa[1] = p.y;
+                    wb[0] = q.x, wb[1] = q.y;
+                }
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) x[i][nt][e] = 0.0f;
+#pragma unroll
+                for (int j = 0; j < HD / 32; ++j) {
+                    const uint32_t ha = wa[j] >> 8, hb = wb[j] >> 8;
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) {
+                        mma_f16(x[i][nt], wa[j] & 0x000f000fu, wb[j] & 0x000f000fu, wa[j] & 0x00f000f0u,
+                                wb[j] & 0x00f000f0u, qf[nt][2 * j][0], qf[nt][2 * j][1]);
+                        mma_f16(x[i][nt], ha & 0x000f000fu, hb & 0x000f000fu, ha & 0x00f000f0u, hb & 0x00f000f0u,
+                                qf[nt][2 * j + 1][0], qf[nt][2 * j + 1][1]);
+                    }
+                }
+                const uint32_t kp0 = lds32(rec + B::KPAIR + tok * 4), kp1 = lds32(rec + B::KPAIR + (tok + 8) * 4);
+                vp[i][0] = lds32(rec + B::VPAIR + tok * 4);
+                vp[i][1] = lds32(rec + B::VPAIR + (tok + 8) * 4);
+                const int uu = u + i;
+                const int j0 = (uu < cur.n.front ? uu : cur.n.start + uu - cur.n.front) * kKvBlock;
+                const float s0 = __uint_as_float(kp0 << 16), b0 = __uint_as_float(kp0 & 0xffff0000u);
+                const float s1 = __uint_as_float(kp1 << 16), b1 = __uint_as_float(kp1 & 0xffff0000u);
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        x[i][nt][e] = fmaf(x[i][nt][e], cmul[nt][e] * s0, cadd[nt][e] * b0);
+                        x[i][nt][2 + e] = fmaf(x[i][nt][2 + e], cmul[nt][e] * s1, cadd[nt][e] * b1);
+                    }
+                // every column sees the whole block, except at the edges of what is visible
+                const bool whole = j0 + kKvBlock - 1 <= row_lo &&
+                                   (a.window == 0 || j0 > row_hi - a.window || j0 + kKvBlock <= a.sinks);
+                if (!whole) {
+                    const int ja = j0 + tok, jb = ja + 8;
+                    // a pair that no column sees may hold anything
+                    if (ja > row_hi || !(a.window == 0 || ja > row_lo - a.window || ja < a.sinks)) vp[i][0] = 0;
+                    if (jb > row_hi || !(a.window == 0 || jb > row_lo - a.window || jb < a.sinks)) vp[i][1] = 0;
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const int p = cpos[nt][e];
+                            if (!(ja <= p && (a.window == 0 || ja > p - a.window || ja < a.sinks))) x[i][nt][e] = kNegInf;
+                            if (!(jb <= p && (a.window == 0 || jb > p - a.window || jb < a.sinks)))
+                                x[i][nt][2 + e] = kNegInf;
+                        }
+                }
+                vtop = max(vtop, max(vp[i][0] & 0xffffu, vp[i][1] & 0xffffu));   // steps are not negative
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) cmax[nt][e] = fmaxf(cmax[nt][e], fmaxf(x[i][nt][e], x[i][nt][2 + e]));
+            }
+#pragma unroll
+            for (int m = 4; m < 32; m <<= 1) {
+                vtop = max(vtop, __shfl_xor_sync(0xffffffffu, vtop, m));
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e)
+                        cmax[nt][e] = fmaxf(cmax[nt][e], __shfl_xor_sync(0xffffffffu, cmax[nt][e], m));
+            }
+            // new maxima; sums and accumulators follow when any changed
+            const int e_new = max(vexp, min(static_cast<int>(vtop >> 7), 250));
+            const float vdown = __uint_as_float(static_cast<uint32_t>(max(127 - (e_new - vexp), 0)) << 23);
+            vexp = e_new;
+            float alpha[NT][2];
+            bool moved = vdown != 1.0f;
+            float base[NT][2];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const float m = fmaxf(mx[nt][e], cmax[nt][e]);
+                    base[nt][e] = m == kNegInf ? 0.0f : m;
+                    alpha[nt][e] = ex2(mx[nt][e] - base[nt][e]);
+                    moved |= m != mx[nt][e];
+                    mx[nt][e] = m;
+                }
+            if (__any_sync(0xffffffffu, moved)) {
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        sum[nt][e] *= alpha[nt][e];
+                        corr[nt][e] *= alpha[nt][e];
+                        const float f = alpha[nt][e] * vdown;
+#pragma unroll
+                        for (int i = 0; i < MT; ++i) acc[nt][i][e] *= f, acc[nt][i][2 + e] *= f;
+                    }
+            }
+            const float vscale = __uint_as_float(static_cast<uint32_t>(253 - vexp) << 23) * (1 << kPShift);
+#pragma unroll
+            for (int i = 0; i < kStageBlocks; ++i) {
+                if (!((mask >> i) & 1)) continue;
+                const float s0 = __uint_as_float(vp[i][0] << 16) * vscale, b0 = __uint_as_float(vp[i][0] & 0xffff0000u);
+                const float s1 = __uint_as_float(vp[i][1] << 16) * vscale, b1 = __uint_as_float(vp[i][1] & 0xffff0000u);
+                uint32_t pf[NT][2];
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    float ps[4];
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const float xa = x[i][nt][e], xb = x[i][nt][2 + e];
+                        const float pa = ex2(xa - base[nt][e]), pb = ex2(xb - base[nt][e]);
+                        sum[nt][e] += pa + pb;
+                        // a token that this column does not see may stand for NaN or infinities
+                        ps[e] = xa == kNegInf ? 0.0f : pa * s0;
+                        ps[2 + e] = xb == kNegInf ? 0.0f : pb * s1;
+                        corr[nt][e] += (xa == kNegInf ? 0.0f : pa * b0) + (xb == kNegInf ? 0.0f : pb * b1);
+                    }
+                    pf[nt][0] = transpose8x8(pack_f16x2(ps[0], ps[1]));
+                    pf[nt][1] = transpose8x8(pack_f16x2(ps[2], ps[3]));
+                }
+                // values: tokens t4, 4 + (t4 ^ 1) and the same + 8 are this lane's columns of k
+                const uint32_t va = buf + i * B::BYTES + B::VALS + g * (B::ROW / 8);
+                constexpr int W = HD / 64;
+                uint32_t y[4][W];
+#pragma unroll
+                for (int p = 0; p < 4; ++p) {
+                    const int tk = ((p & 1) ? 4 + (t4 ^ 1) : t4) + (p >> 1) * 8;
+                    if constexpr (W == 2) {
+                        const uint2 v = lds64(va + tk * B::ROW);
+                        y[p][0] = v.x, y[p][1] = v.y;
+                    } else {
+                        y[p][0] = lds32(va + tk * B::ROW);
+                    }
+                }
+#pragma unroll
+                for (int j = 0; j < W; ++j)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        uint32_t p01 = __byte_perm(y[0][j], y[1][j], h ? 0x7632 : 0x5410);
+                        uint32_t p23 = __byte_perm(y[2][j], y[3][j], h ? 0x7632 : 0x5410);
+#pragma unroll
+                        for (int b = 0; b < 2; ++b) {
+#pragma unroll
+                            for (int nt = 0; nt < NT; ++nt)
+                                mma_f16(acc[nt][j * 4 + h * 2 + b], p01 & 0x000f000fu, p01 & 0x00f000f0u,
+                                        p23 & 0x000f000fu, p23 & 0x00f000f0u, pf[nt][0], pf[nt][1]);
+                            p01 >>= 8, p23 >>= 8;
+                        }
+                    }
+            }
+            __syncwarp();                                                // every lane is done with the stage
+            ++used;
+            if (!dead) load_stage();
+        }
+
+        // ---- the warp's result: O, maximum and sum of each column, every lane with its own dimensions
+        const float down = __uint_as_float(static_cast<uint32_t>(min(24 - kPShift + vexp + 1, 254)) << 23);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+#pragma unroll
+                for (int m = 4; m < 32; m <<= 1) {
+                    sum[nt][e] += __shfl_xor_sync(0xffffffffu, sum[nt][e], m);
+                    corr[nt][e] += __shfl_xor_sync(0xffffffffu, corr[nt][e], m);
+                }
+#pragma unroll
+                for (int i = 0; i < MT; ++i) {
+                    acc[nt][i][e] = fmaf(acc[nt][i][e], down, corr[nt][e]);
+                    acc[nt][i][2 + e] = fmaf(acc[nt][i][2 + e], down * 0.0625f, corr[nt][e]);
+                }
+            }
+        // merge the worker's warps, halves at a time
+        for (int half = ws / 2; half >= 1; half >>= 1) {
+            float4* area = reinterpret_cast<float4*>(smem + C::RING) + (grp * (ws / 2) + (wi % half)) * (C::MERGE / 16);
+            if (wi >= half && wi < 2 * half) {
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+                    for (int i = 0; i < MT; ++i)
+                        area[(nt * (MT + 1) + i) * 32 + lane] =
+                            make_float4(acc[nt][i][0], acc[nt][i][1], acc[nt][i][2], acc[nt][i][3]);
+                    area[(nt * (MT + 1) + MT) * 32 + lane] = make_float4(mx[nt][0], mx[nt][1], sum[nt][0], sum[nt][1]);
+                }
+            }
+            asm volatile("bar.sync %0, %1;" ::"r"(1 + grp), "r"(ws * 32) : "memory");
+            if (wi < half) {
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    const float4 o = area[(nt * (MT + 1) + MT) * 32 + lane];
+                    const float om[2] = {o.x, o.y}, os[2] = {o.z, o.w};
+                    float fa[2], fb[2];
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const float m = fmaxf(mx[nt][e], om[e]), b = m == kNegInf ? 0.0f : m;
+                        fa[e] = ex2(mx[nt][e] - b);
+                        fb[e] = ex2(om[e] - b);
+                        mx[nt][e] = m;
+                        sum[nt][e] = sum[nt][e] * fa[e] + os[e] * fb[e];
+                    }
+#pragma unroll
+                    for (int i = 0; i < MT; ++i) {
+                        const float4 v = area[(nt * (MT + 1) + i) * 32 + lane];
+                        acc[nt][i][0] = acc[nt][i][0] * fa[0] + v.x * fb[0];
+                        acc[nt][i][1] = acc[nt][i][1] * fa[1] + v.y * fb[1];
+                        acc[nt][i][2] = acc[nt][i][2] * fa[0] + v.z * fb[0];
+                        acc[nt][i][3] = acc[nt][i][3] * fa[1] + v.w * fb[1];
+                    }
+                }
+            }
+            asm volatile("bar.sync %0, %1;" ::"r"(1 + grp), "r"(ws * 32) : "memory");
+        }
+        if (wi == 0) {
+            const bool complete = seg_off == 0 && seg_n == cur.n.units;
+            constexpr int DL = HD / 8;                                   // dimensions of this lane
+            float* slot = slots + (static_cast<size_t>(worker) * 2 + (first_segment ? 0 : 1)) * slot_floats(COLS, HD);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int ci = nt * 8 + 2 * t4 + e;
+                    if (complete) {
+                        if (ci >= cols) continue;
+                        const float inv = sum[nt][e] == 0.0f ? 0.0f : 1.0f / sum[nt][e];
+                        const int cc = cur.tile * COLS + ci;
+                        const int r = cc / a.group, h = cc - r * a.group;
+                        uint16_t* dst = a.out[rank] + (cur.n.first_row + r) * a.ldo + (kvh * a.group + h) * HD + g * DL;
+#pragma unroll
+                        for (int i = 0; i < MT; i += 4)
+                            *reinterpret_cast<uint4*>(dst + 2 * i) =
+                                make_uint4(pack_bf16x2(acc[nt][i][e] * inv, acc[nt][i][2 + e] * inv),
+                                           pack_bf16x2(acc[nt][i + 1][e] * inv, acc[nt][i + 1][2 + e] * inv),
+                                           pack_bf16x2(acc[nt][i + 2][e] * inv, acc[nt][i + 2][2 + e] * inv),
+                                           pack_bf16x2(acc[nt][i + 3][e] * inv, acc[nt][i + 3][2 + e] * inv));
+                    } else {
+                        float4* dst = reinterpret_cast<float4*>(slot + ci * HD + g * DL);
+#pragma unroll
+                        for (int i = 0; i < MT; i += 2)
+                            dst[i / 2] = make_float4(acc[nt][i][e], acc[nt][i][2 + e], acc[nt][i + 1][e],
+                                                     acc[nt][i + 1][2 + e]);
+                        if (g == 0) {
+                            slot[COLS * HD + ci] = mx[nt][e];
+                            slot[COLS * (HD + 1) + ci] = sum[nt][e];
+                        }
+                    }
+                }
+        }
+        first_segment = false;
+        cur.next(a, COLS, heads);
+        if (cur.left <= 0) break;
+    }
+    if (dead) spin_ns(1000000);      // copies that were issued land before the block's memory is given back
+}
+
+// Adds, in order, the parts of an item that several workers hold.  One thread
+// block per worker; the block of the first worker that begins inside the item does it.
+template <int HD, int NT>
+__global__ void __launch_bounds__(256) kv4_attention_join_kernel(const __grid_constant__ AttnArgs a, int main_grid) {
+    constexpr int COLS = 8 * NT;
+    pdl_wait();
+    pdl_trigger();
+    const Cut cut = *reinterpret_cast<const Cut*>(a.ws);
+    const int b = blockIdx.x;
+    if (b >= cut.workers || b == 0) return;
+    const int64_t begin = part_begin(cut.total, cut.workers, b);
+    if (begin >= part_begin(cut.total, cut.workers, b + 1)) return;
+    const Split sp = reinterpret_cast<const Split*>(a.ws + kSplitAt)[b];
+    if (sp.units == 0) return;
+    const int b_lo = worker_of(cut.total, cut.workers, sp.begin);
+    if (worker_of(cut.total, cut.workers, begin - 1) != b_lo) return;
+    const int b_hi = worker_of(cut.total, cut.workers, sp.begin + sp.units - 1);
+    const bool lo_first = part_begin(cut.total, cut.workers, b_lo) == sp.begin;
+    const float* slots = reinterpret_cast<const float*>(a.ws + kSplitAt + static_cast<size_t>(main_grid) * kWarps * sizeof(Split));
+    const int rank = sp.head / a.pools.kv_heads, kvh = sp.head - rank * a.pools.kv_heads;
+    const int cols = min(COLS, sp.rows * a.group - sp.tile * COLS);
+    for (int i = threadIdx.x; i < cols * (HD / 4); i += 256) {
+        const int ci = i / (HD / 4), d = (i - ci * (HD / 4)) * 4;
+        float m = kNegInf, l = 0.0f;
+        float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 4
+        for (int w = b_lo; w <= b_hi; ++w) {
+            const float* slot = slots + (static_cast<size_t>(w) * 2 + (w == b_lo && !lo_first ? 1 : 0)) * slot_floats(COLS, HD);
+            const float wm = slot[COLS * HD + ci], wl = slot[COLS * (HD + 1) + ci];
+            const float4 v = *reinterpret_cast<const float4*>(slot + ci * HD + d);
+            const float nm = fmaxf(m, wm), nb = nm == kNegInf ? 0.0f : nm;
+            const float fa = ex2(m - nb), fb = ex2(wm - nb);
+            m = nm;
+            l = l * fa + wl * fb;
+            o.x = o.x * fa + v.x * fb;
+            o.y = o.y * fa + v.y * fb;
+            o.z = o.z * fa + v.z * fb;
+            o.w = o.w * fa + v.w * fb;
+        }
+        const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+        const int cc = sp.tile * COLS + ci;
+        const int r = cc / a.group, h = cc - r * a.group;
+        *reinterpret_cast<uint2*>(a.out[rank] + (sp.first_row + r) * a.ldo + (kvh * a.group + h) * HD + d) =
+            make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
+    }
+}
+
+template <int HD, int NT>
+tp_status launch_few(const AttnArgs& a, int sms, cudaStream_t stream) {
+    using C = Cfg<HD, NT>;
+    static std::atomic<uint64_t> smem_set{0};
+    auto* kern = kv4_attention_kernel<HD, NT>;
+    if (!smem_attribute_once(reinterpret_cast<const void*>(kern), C::SMEM, smem_set)) return TP_ERR_CUDA;
+    if (launch_pdl(kern, dim3(sms), dim3(kWarps * 32), C::SMEM, stream, a) != cudaSuccess) return TP_ERR_CUDA;
+    if (launch_pdl(kv4_attention_join_kernel<HD, NT>, dim3(sms * kWarps), dim3(256), 0, stream, a, sms) != cudaSuccess)
+        return TP_ERR_CUDA;
+    return TP_OK;
+}
+
+}  // namespace
+
+size_t kv4_attention_workspace(int t, int64_t n, int64_t nseq, int heads, int kv_heads, int head_dim) {
+    (void)t, (void)n, (void)nseq, (void)heads, (void)kv_heads;
+    // two slots of 16 columns for each of the 8 workers that an SM can have
+    const size_t workers = static_cast<size_t>(std::max(device_sms(), 160)) * kWarps;
+    return kSplitAt + workers * (sizeof(Split) + 2 * slot_floats(16, head_dim) * sizeof(float));
+}
+
+tp_status launch_kv4_attention(const KvAttentionDesc& d, cudaStream_t stream) {
+    AttnArgs a;
+    a.seqs = d.seqs;
+    a.pools = d.pools;
+    for (int r = 0; r < TP_MAX_SHARDS; ++r) {
+        a.q[r] = static_cast<const uint16_t*>(d.q[r]);
+        a.out[r] = static_cast<uint16_t*>(d.out[r]);
+    }
+    a.ldq = d.ldq;
+    a.ldo = d.ldo;
+    a.group = d.group;
+    a.scale_log2 = d.scale * 1.44269504088896f;
+    a.window = d.window;
+    a.sinks = d.sinks;
+    a.ws = static_cast<uint8_t*>(d.ws);
+    const int sms = device_sms();
+    if (sms <= 0 || sms > 160) return TP_ERR_CUDA;
+    // 16 columns per tile when a sequence's rows fill more than 8
+    const bool wide = d.group > 8 || (d.seqs.cu_rows != nullptr && d.group * (d.seqs.n / std::max(d.seqs.nseq, 1)) > 8);
+    if (d.head_dim == 128) return wide ? launch_few<128, 2>(a, sms, stream) : launch_few<128, 1>(a, sms, stream);
+    return wide ? launch_few<64, 2>(a, sms, stream) : launch_few<64, 1>(a, sms, stream);
+}
+
+}  // namespace tpk

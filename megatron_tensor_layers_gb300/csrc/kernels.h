@@ -188,6 +188,130 @@ struct SeqParDesc {
 };
 tp_status launch_seqpar_rmsnorm(const SeqParDesc& d, cudaStream_t stream);
 
+// ---------------------------------------------------------------- paged 4-bit KV cache
+constexpr int kKvBlock = 16;             // tokens of a cache block
+
+// The sequences of a call (see include/tp.h): n rows, page table, lengths.
+struct KvSeqs {
+    int n = 0, nseq = 0;
+    const int32_t* table = nullptr;      // [nseq, max_blocks]
+    int64_t max_blocks = 0;
+    const int32_t* lens = nullptr;
+    const int32_t* cu_rows = nullptr;    // [nseq + 1], or null: one row per sequence
+    int* status = nullptr;
+};
+
+// The pools of one layer.
+struct KvPools {
+    int t = 0;
+    uint8_t* pool[TP_MAX_SHARDS] = {};
+    int64_t pages = 0;
+    int page_shift = 0;                  // log2 of the blocks of a page
+    int kv_heads = 0;
+};
+
+// Byte offset in a pool of block `block` (16 tokens) of the sequence with page
+// table row `row`, for kv head `head`; -1 when the table does not reach that
+// far or names no page of the pool.  The only place where a page number
+// becomes an address.
+#ifdef __CUDACC__
+__host__ __device__
+#endif
+inline int64_t kv_block_offset(const int32_t* row, int64_t max_blocks, int64_t pages, int page_shift, int kv_heads,
+                               int head, int64_t block, int block_bytes) {
+    const int64_t at = block >> page_shift;
+    if (block < 0 || at >= max_blocks) return -1;
+    const int64_t page = row[at];
+    if (page < 0 || page >= pages) return -1;
+    return (((page * kv_heads + head) << page_shift) + (block & ((1 << page_shift) - 1))) * block_bytes;
+}
+
+struct KvAppendDesc {
+    KvSeqs seqs;
+    KvPools pools;
+    int head_dim = 0;
+    const void* k[TP_MAX_SHARDS] = {};
+    const void* v[TP_MAX_SHARDS] = {};
+    int64_t ldk = 0, ldv = 0;
+};
+tp_status launch_kv4_append(const KvAppendDesc& d, cudaStream_t stream);
+
+struct KvLoadDesc {
+    KvSeqs seqs;
+    KvPools pools;
+    int head_dim = 0;
+    void* k[TP_MAX_SHARDS] = {};
+    void* v[TP_MAX_SHARDS] = {};
+    int with_k = 0, with_v = 0;
+    int64_t ldk = 0, ldv = 0;
+    int out_f32 = 0;
+};
+tp_status launch_kv4_load(const KvLoadDesc& d, cudaStream_t stream);
+
+struct KvAttentionDesc {
+    KvSeqs seqs;
+    KvPools pools;
+    int head_dim = 0;
+    int group = 0;                       // query heads per kv head
+    const void* q[TP_MAX_SHARDS] = {};
+    void* out[TP_MAX_SHARDS] = {};
+    int64_t ldq = 0, ldo = 0;
+    float scale = 0.0f;
+    int window = 0, sinks = 0;           // window 0: none
+    void* ws = nullptr;
+};
+size_t kv4_attention_workspace(int t, int64_t n, int64_t nseq, int heads, int kv_heads, int head_dim);
+tp_status launch_kv4_attention(const KvAttentionDesc& d, cudaStream_t stream);
+
+// Page bookkeeping (fork and compact) and the page copies it asks for.
+struct KvPagesDesc {
+    int t = 0;
+    int rows_in = 0, rows_out = 0;
+    int64_t max_blocks = 0;
+    int page_size = 0;
+    int pages = 0;
+    const int32_t* table = nullptr;
+    const int32_t* lens = nullptr;
+    const int32_t* parents = nullptr;    // fork only
+    const int32_t* grow = nullptr;
+    int grow_all = 0;
+    const uint8_t* held = nullptr;
+    uint8_t* pool[TP_MAX_SHARDS] = {};
+    int with_pool = 0;
+    int64_t layers = 0, page_bytes = 0;
+    int32_t* table_out = nullptr;
+    int32_t* lens_out = nullptr;         // fork only
+    int32_t* refs = nullptr;
+    int32_t* info = nullptr;
+    void* ws = nullptr;
+};
+size_t kv_pages_workspace(int64_t rows, int64_t pages);
+tp_status launch_kv_fork(const KvPagesDesc& d, cudaStream_t stream);
+tp_status launch_kv_compact(const KvPagesDesc& d, cudaStream_t stream);
+
+struct BeamDesc {
+    int t = 0;
+    int items = 0, beams = 0, k = 0;
+    int64_t cols[TP_MAX_SHARDS] = {};
+    const void* logits[TP_MAX_SHARDS] = {};
+    int64_t ldl[TP_MAX_SHARDS] = {};
+    int f32 = 0;
+    const float* scores = nullptr;
+    const uint8_t* finished = nullptr;
+    int eos = 0;
+    float* scores_out = nullptr;
+    int32_t* rows_out = nullptr;
+    int32_t* tokens_out = nullptr;
+    void* ws = nullptr;
+};
+size_t beam_workspace(int64_t items, int beams, int k, int64_t vocab);
+tp_status launch_beam_select(const BeamDesc& d, cudaStream_t stream);
+
+// Device address of the library's status word on the current device (null on failure).
+int* device_status_word();
+// Streaming multiprocessors of the current device, looked up once per device (0 on failure).
+int device_sms();
+
 tp_status launch_expire_wait(uint64_t limit_ns, int* status, cudaStream_t stream);
 
 }  // namespace tpk

@@ -1,0 +1,71 @@
+// The paged 4-bit KV cache: the layout of a block, where a token's block is,
+// and which row belongs to which sequence.  See include/tp.h for the format.
+#pragma once
+
+#include <cstdint>
+
+#include "common.cuh"
+#include "kernels.h"
+
+namespace tpk {
+
+// A block of 16 tokens of one kv head: key codes, value codes, key pairs, value pairs.
+template <int HD>
+struct KvBlock {
+    static constexpr int ROW = HD / 2;                  // code bytes of one token
+    static constexpr int KEYS = 0;
+    static constexpr int VALS = kKvBlock * ROW;
+    static constexpr int KPAIR = 2 * kKvBlock * ROW;    // (step, base) bf16 of each key
+    static constexpr int VPAIR = KPAIR + 4 * kKvBlock;
+    static constexpr int BYTES = VPAIR + 4 * kKvBlock;
+    static_assert(BYTES == kKvBlock * (HD + 8), "block size of the format");
+};
+
+// A page table or row offset outside its range (or a lost wait) is recorded
+// once; an earlier error stays.
+__device__ __forceinline__ void raise_status(int* status, tp_status code) {
+    if (status != nullptr) atomicCAS(status, 0, static_cast<int>(code));
+}
+
+// Rows [first, first + count) of sequence s, count 0 when the offsets are out of order or range.
+struct SeqRows {
+    int first, count;
+};
+__device__ __forceinline__ SeqRows seq_rows(const KvSeqs& q, int s) {
+    if (q.cu_rows == nullptr) return {s, 1};
+    const int a = q.cu_rows[s], b = q.cu_rows[s + 1];
+    if (a < 0 || b < a || b > q.n) {
+        raise_status(q.status, TP_ERR_INVALID_ARG);
+        return {0, 0};
+    }
+    return {a, b - a};
+}
+
+// The sequence that row `row` belongs to, found by the whole warp (32-way
+// search over cu_rows), and the row's position in it; false when no sequence
+// holds the row.
+__device__ __forceinline__ bool row_place(const KvSeqs& q, int row, int lane, int& seq, int& pos) {
+    if (q.cu_rows == nullptr) {
+        seq = row;
+        pos = q.lens[row] - 1;
+        return true;
+    }
+    int lo = 0, len = q.nseq;
+    while (len > 1) {
+        const int step = (len + 31) >> 5;
+        const int at = lane * step;
+        const bool le = at < len && q.cu_rows[lo + at] <= row;
+        const int k = __popc(__ballot_sync(0xffffffffu, le)) - 1;
+        if (k < 0) break;
+        lo += k * step;
+        len = min(step, len - k * step);
+    }
+    const int a = q.cu_rows[lo], b = q.cu_rows[lo + 1];
+    seq = lo;
+    // 64 bits: a length of any value minus any row count stays in range
+    const int64_t p = static_cast<int64_t>(q.lens[lo]) - (static_cast<int64_t>(b) - row);
+    pos = p < 0 ? -1 : static_cast<int>(p);
+    return a >= 0 && a <= row && row < b && b <= q.n;
+}
+
+}  // namespace tpk
