@@ -33,7 +33,7 @@
 // group fill them.  tcgen05 would want 128 rows of them.
 #include <algorithm>
 
-#include "kv4.cuh"
+#include "attention_args.cuh"
 
 namespace tpk {
 namespace {
@@ -42,19 +42,8 @@ constexpr int kWarps = 8;
 constexpr int kStageBlocks = 4;
 constexpr int kStages = 2;
 constexpr int kPShift = 13;          // p s' is held times 2^(kPShift - E)
+constexpr int kMany = 64;            // columns from which a sequence's rows go to the many-rows kernel
 constexpr float kNegInf = -INFINITY;
-
-struct AttnArgs {
-    KvSeqs seqs;
-    KvPools pools;
-    const uint16_t* q[TP_MAX_SHARDS];
-    uint16_t* out[TP_MAX_SHARDS];
-    int64_t ldq, ldo;
-    int group;
-    float scale_log2;                // scale * log2(e)
-    int window, sinks;
-    uint8_t* ws;
-};
 
 // Head of the workspace: what the second kernel needs to know of the cut.
 struct Cut {
@@ -73,12 +62,6 @@ constexpr size_t kSplitAt = 256;
 
 __host__ __device__ constexpr size_t slot_floats(int cols, int hd) { return static_cast<size_t>(cols) * (hd + 2); }
 
-__device__ __forceinline__ float ex2(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-
 __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                         uint32_t b1) {
     asm volatile(
@@ -86,12 +69,6 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1,
         "{%0, %1, %2, %3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-
-__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
-    uint32_t r;
-    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-    return r;
 }
 
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
@@ -137,19 +114,12 @@ __device__ __forceinline__ Need seq_need(const AttnArgs& a, int s, int cols_per_
     n.rows = r.count;
     n.len = max(a.seqs.lens[s], 0);
     const int64_t cols = static_cast<int64_t>(r.count) * a.group;
-    n.tiles = static_cast<int>((cols + cols_per_tile - 1) / cols_per_tile);
-    const int64_t low = a.window > 0 ? static_cast<int64_t>(n.len) - r.count - a.window + 1 : 0;
-    const int lo = low > 0 ? static_cast<int>(low) : 0;
-    n.front = lo > 0 ? (min(a.sinks, lo) + kKvBlock - 1) / kKvBlock : 0;
-    n.start = max(lo / kKvBlock, n.front);
-    int64_t end = (static_cast<int64_t>(n.len) + kKvBlock - 1) / kKvBlock;
-    const int64_t most = a.seqs.max_blocks << a.pools.page_shift;
-    if (end > most) {                // tokens past the table are not there
-        if (r.count > 0) raise_status(a.seqs.status, TP_ERR_INVALID_ARG);
-        end = most;
-    }
-    n.front = min(n.front, static_cast<int>(end));
-    n.blocks = n.front + max(0, static_cast<int>(end) - n.start);
+    n.tiles = cols >= a.many ? 0 : static_cast<int>((cols + cols_per_tile - 1) / cols_per_tile);
+    Spans v{0, 0, 0};
+    if (n.tiles > 0) v = visible_spans(a, static_cast<int64_t>(n.len) - r.count, static_cast<int64_t>(n.len) - 1, kKvBlock);
+    n.front = v.front;
+    n.start = v.start;
+    n.blocks = v.count;
     n.units = max(n.blocks, 1);
     return n;
 }
@@ -828,6 +798,13 @@ tp_status launch_kv4_attention(const KvAttentionDesc& d, cudaStream_t stream) {
     a.window = d.window;
     a.sinks = d.sinks;
     a.ws = static_cast<uint8_t*>(d.ws);
+    // Sequences with at least kMany columns go to the many-rows kernel (none can without cu_rows).
+    a.many = kMany;
+    if (d.seqs.cu_rows != nullptr && static_cast<int64_t>(d.seqs.n) * d.group >= kMany) {
+        const tp_status s = launch_attention_many(a, d.head_dim, stream);
+        if (s != TP_OK) return s;
+    }
+    if (d.seqs.cu_rows == nullptr) a.many = INT32_MAX;
     const int sms = device_sms();
     if (sms <= 0 || sms > 160) return TP_ERR_CUDA;
     // 16 columns per tile when a sequence's rows fill more than 8

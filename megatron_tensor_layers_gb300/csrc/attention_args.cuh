@@ -1,0 +1,61 @@
+// What the two attention kernels share: arguments, which blocks of its cache a
+// run of rows sees, and which of the kernels takes a sequence.
+#pragma once
+
+#include "kv4.cuh"
+
+namespace tpk {
+
+struct AttnArgs {
+    KvSeqs seqs;
+    KvPools pools;
+    const uint16_t* q[TP_MAX_SHARDS];
+    uint16_t* out[TP_MAX_SHARDS];
+    int64_t ldq, ldo;
+    int group;                       // query heads per kv head
+    float scale_log2;                // scale * log2(e)
+    int window, sinks;
+    int many;                        // columns (rows * group) from which a sequence goes to the many-rows kernel
+    uint8_t* ws;
+};
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+// Spans of `span` tokens that rows at positions first .. last see: [0, front)
+// for the sinks, then [start, start + count - front).
+struct Spans {
+    int front, start, count;
+};
+__device__ __forceinline__ Spans visible_spans(const AttnArgs& a, int64_t first, int64_t last, int span) {
+    Spans v;
+    const int64_t low = a.window > 0 ? first - a.window + 1 : 0;
+    const int lo = low > 0 ? static_cast<int>(low) : 0;
+    // tokens past the table are not there
+    const int64_t most = a.seqs.max_blocks << a.pools.page_shift;
+    int64_t end = (last + 1 + kKvBlock - 1) / kKvBlock;
+    if (last < 0) end = 0;
+    if (end > most) {
+        raise_status(a.seqs.status, TP_ERR_INVALID_ARG);
+        end = most;
+    }
+    const int per = span / kKvBlock;
+    const int stop = static_cast<int>((end + per - 1) / per);
+    v.front = lo > 0 ? min((min(a.sinks, lo) + span - 1) / span, stop) : 0;
+    v.start = max(lo / span, v.front);
+    v.count = v.front + max(0, stop - v.start);
+    return v;
+}
+
+tp_status launch_attention_many(const AttnArgs& a, int head_dim, cudaStream_t stream);
+
+}  // namespace tpk

@@ -1,0 +1,644 @@
+// Attention over the paged 4-bit cache for many rows per sequence (chunks of
+// prompts): matrix products on the 5th-generation tensor cores, bound by them
+// and by the exponentials.
+//
+// A thread block takes 256 columns (a column is one row's query head) of one kv
+// head as two tiles of 128, and walks the cached tokens 128 at a time:
+//   S = Q K^T          tcgen05, Q and K from shared memory, S in TMEM;
+//   P = 2^(c S - m)    one thread per column, fp32, P as fp16 over S in TMEM;
+//   O += P V           tcgen05, P from TMEM, V^T from shared memory, O in TMEM.
+// Warps 0-3 and 4-7 are the softmax of one tile each and take turns with the
+// tensor core, warps 8-11 turn codes into operands, warp 12 issues the products.
+//
+// Codes to operands.  A code is an fp16 subnormal u 2^-24 (or 16 u 2^-24) after
+// one mask, and one HFMA2 makes the fp16 value (s u + b) 2^-F of two elements:
+// 9 instructions for 8 keys, shared by all 256 columns.  F is the exponent of
+// the largest step or base of the 128 tokens, so that nothing overflows; a value
+// is rounded once, by at most 2^-11 of itself or 2^-25 of the tile's scale
+// 2^F.  The scale of K enters the exponent's factor c, the scale of V the
+// exponent itself (P 2^(F - Fref)), both per tile.  Keys keep their packed order
+// (q is permuted to it), values are transposed while they are unpacked: eight
+// tokens' words give eight dimensions' 16-byte chunks of V^T.
+//
+// The maximum m that is subtracted follows the true one lazily: O and the sum
+// are rescaled only when a column's maximum has grown by more than 2^8, which
+// fp16 and fp32 have room for.
+//
+// A value row that stands for NaN is put in as 0 and its token noted; a column
+// that sees such a token gets a NaN sum, the others are not touched by it.
+#include <algorithm>
+
+#include <cuda_fp16.h>
+
+#include "attention_args.cuh"
+
+namespace tpk {
+namespace {
+
+constexpr int kThreads = 512;
+constexpr int kTile = 128;           // tokens of a step, columns of a tile
+constexpr int kCols = 2 * kTile;     // columns of a thread block
+constexpr int kInfo = 4;
+constexpr float kNegInf = -INFINITY;
+constexpr float kGrow = 8.0f;        // log2 by which a maximum may grow before O is rescaled
+
+template <int HD>
+struct Cfg {
+    static constexpr int QB = kTile * HD * 2;            // one tile of Q
+    static constexpr int KB = kTile * HD * 2;            // K, and V^T
+    static constexpr int ATOM = kTile * 128;             // 64 elements of 128 rows
+    static constexpr int VATOM = HD * 128;               // 64 tokens of HD rows
+    static constexpr int Q = 0, K = 2 * QB, V = K + 2 * KB, SMEM = V + 2 * KB + 1024;
+    static constexpr int S_COL = 0, O_COL = 256;         // TMEM columns: S of the tiles, then O of the tiles
+};
+
+// What the softmax has to know of a step.
+struct StepInfo {
+    float kmul;                      // 2^(F - 127) of the keys
+    int vexp;                        // F of the values
+    uint32_t bad;                    // blocks that are not there
+    uint32_t any_nan;
+    uint32_t nan[4];                 // tokens whose value row stands for NaN
+};
+
+__device__ __forceinline__ float pow2_field(int field) { return __uint_as_float(static_cast<uint32_t>(field) << 23); }
+
+// fp16 A and B, f32 accumulator, K-major.
+__host__ __device__ constexpr uint32_t idesc_f16(int m, int n) {
+    return (1u << 4) | (static_cast<uint32_t>(n >> 3) << 17) | (static_cast<uint32_t>(m >> 4) << 24);
+}
+
+// D[tmem] (+)= A[tmem] * B[smem]^T, issued by one thread.
+__device__ __forceinline__ void tc_mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
+                                          uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31};" ::"r"(r[0]),
+        "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
+        "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]),
+        "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]),
+        "r"(r[29]), "r"(r[30]), "r"(r[31]), "r"(taddr)
+        : "memory");
+}
+__device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+__device__ __forceinline__ uint32_t hfma2(uint32_t a, uint32_t b, uint32_t c) {
+    uint32_t d;
+    asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
+    return d;
+}
+
+template <int N>
+__device__ __forceinline__ void more_registers() {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void fewer_registers() {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+struct Bars {
+    uint64_t q_full, k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_full[2], o_full;
+};
+
+// What the thread block works on.
+struct Item {
+    int seq, first_row, rows, len, tile, head;
+};
+
+template <int HD>
+__global__ void __launch_bounds__(kThreads, 1) kv4_attention_many_kernel(const __grid_constant__ AttnArgs a) {
+    using B = KvBlock<HD>;
+    using C = Cfg<HD>;
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ __align__(8) Bars bars;
+    __shared__ uint32_t s_tmem;
+    __shared__ int s_abort;
+    __shared__ int s_found;
+    __shared__ Item s_item;
+    __shared__ int64_t s_scan[kThreads / 32];
+    __shared__ StepInfo s_info[kInfo];
+    __shared__ __align__(16) uint32_t s_key[kTile];      // fp16 pairs (step, base) of the step's keys
+    __shared__ __align__(16) uint16_t s_vstep[kTile], s_vbase[kTile];
+    __shared__ int s_exp[4][2];
+    __shared__ uint32_t s_nan[4];
+
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const uint32_t sm = (smem_u32(smem_raw) + 1023u) & ~1023u;
+    const int heads = a.pools.t * a.pools.kv_heads;
+    pdl_wait();
+    pdl_trigger();
+
+    // ---- which sequence and tile: block / heads counts tiles of 256 columns over the sequences
+    {
+        const int64_t want = blockIdx.x / heads;
+        const int per = (a.seqs.nseq + kThreads - 1) / kThreads;
+        auto tiles_of = [&](int s) -> int64_t {
+            const int64_t cols = static_cast<int64_t>(seq_rows(a.seqs, s).count) * a.group;
+            return cols < a.many ? 0 : (cols + kCols - 1) / kCols;
+        };
+        if (tid == 0) s_found = 0;
+        const int lo = min(a.seqs.nseq, tid * per), hi = min(a.seqs.nseq, (tid + 1) * per);
+        int64_t mine = 0;
+        for (int s = lo; s < hi; ++s) mine += tiles_of(s);
+        int64_t upto = mine;
+#pragma unroll
+        for (int m = 1; m < 32; m <<= 1) {
+            const int64_t v = __shfl_up_sync(0xffffffffu, upto, m);
+            if (lane >= m) upto += v;
+        }
+        if (lane == 31) s_scan[warp] = upto;
+        __syncthreads();
+        int64_t before = upto - mine;
+        for (int i = 0; i < warp; ++i) before += s_scan[i];
+        if (want >= before && want < before + mine) {
+            int64_t u = want - before;
+            int s = lo;
+            while (true) {
+                const int64_t n = tiles_of(s);
+                if (u < n) break;
+                u -= n;
+                ++s;
+            }
+            const SeqRows r = seq_rows(a.seqs, s);
+            Item it;
+            it.seq = s;
+            it.first_row = r.first;
+            it.rows = r.count;
+            it.len = max(a.seqs.lens[s], 0);
+            // the last tiles see the most tokens: they start first
+            it.tile = static_cast<int>(tiles_of(s) - 1 - u);
+            it.head = static_cast<int>(blockIdx.x % heads);
+            s_item = it;
+            s_found = 1;
+        }
+        __syncthreads();
+        if (!s_found) return;
+    }
+    const Item it = s_item;
+    const int rank = it.head / a.pools.kv_heads, kvh = it.head - rank * a.pools.kv_heads;
+    const int pos0 = it.len - it.rows;                   // position of the sequence's first row
+    const int col0 = it.tile * kCols;
+    const int cols = min(kCols, it.rows * a.group - col0);
+    const int64_t first_pos = pos0 + col0 / a.group, last_pos = pos0 + (col0 + cols - 1) / a.group;
+    const Spans span = visible_spans(a, first_pos, last_pos, kTile);
+    const int steps = span.count;
+
+    if (warp == 0) tmem_alloc<512>(smem_u32(&s_tmem));
+    if (tid == 0) {
+        s_abort = 0;
+        mbar_init(smem_u32(&bars.q_full), kCols);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(smem_u32(&bars.k_full[i]), kTile);
+            mbar_init(smem_u32(&bars.k_empty[i]), 1);
+            mbar_init(smem_u32(&bars.v_full[i]), kTile);
+            mbar_init(smem_u32(&bars.v_empty[i]), 1);
+            mbar_init(smem_u32(&bars.s_full[i]), 1);
+            mbar_init(smem_u32(&bars.p_full[i]), kTile);
+        }
+        mbar_init(smem_u32(&bars.o_full), 1);
+    }
+    fence_barrier_init();
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = s_tmem;
+    bool ok = true;
+
+    if (warp < 8) {
+        more_registers<192>();
+        // ------------------------------------------------ softmax: one thread per column
+        const int t = warp >> 2;                         // tile
+        const int ci = tid;                              // column of the block
+        const bool have = ci < cols;
+        const int cc = col0 + ci;
+        const int r = have ? cc / a.group : 0;
+        const int h = have ? cc - r * a.group : 0;
+        const int pos = have ? pos0 + r : -1;
+        float cmul;
+        {
+            const uint4* src = reinterpret_cast<const uint4*>(a.q[rank] + (it.first_row + r) * a.ldq + (kvh * a.group + h) * HD);
+            uint32_t raw[HD / 2];
+#pragma unroll
+            for (int i = 0; i < HD / 8; ++i) {
+                const uint4 v = have ? __ldg(src + i) : make_uint4(0, 0, 0, 0);
+                raw[4 * i] = v.x, raw[4 * i + 1] = v.y, raw[4 * i + 2] = v.z, raw[4 * i + 3] = v.w;
+            }
+            uint32_t top = 0;
+#pragma unroll
+            for (int i = 0; i < HD / 2; ++i) top = max(top, max(raw[i] & 0x7fffu, (raw[i] >> 16) & 0x7fffu));
+            // scaled by 2^k so that the largest element is in [2^10, 2^11): exact in fp16
+            const int k = top == 0 || a.scale_log2 == 0.0f ? 0 : min(137 - static_cast<int>(top >> 7), 126);
+            float up = pow2_field(k + 127);
+            if (a.scale_log2 < 0.0f) up = -up;
+            if (a.scale_log2 == 0.0f) up = 0.0f;
+            cmul = a.scale_log2 == 0.0f ? 1.0f : fabsf(a.scale_log2) * pow2_field(min(127 - k, 254));
+            const uint32_t row = sm + C::Q + t * C::QB + (ci & 127) * 128;
+#pragma unroll
+            for (int i = 0; i < HD / 8; ++i) {           // a word of eight codes: its order of elements
+                float x[8];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    x[2 * e] = __uint_as_float(raw[4 * i + e] << 16) * up;
+                    x[2 * e + 1] = __uint_as_float(raw[4 * i + e] & 0xffff0000u) * up;
+                }
+                st_shared_v4(row + (i >> 3) * C::ATOM + (((i & 7) ^ (ci & 7)) << 4), pack_f16x2(x[0], x[4]),
+                             pack_f16x2(x[1], x[5]), pack_f16x2(x[2], x[6]), pack_f16x2(x[3], x[7]));
+            }
+        }
+        fence_proxy_async_cta();
+        mbar_arrive(smem_u32(&bars.q_full));
+
+        const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
+        const uint32_t s_addr = tmem + lane_base + C::S_COL + t * kTile;
+        const uint32_t o_addr = tmem + lane_base + C::O_COL + t * HD;
+        // positions of the tile's columns, for whole-tile decisions
+        const int tile_lo = pos0 + (col0 + t * kTile) / a.group;
+        const int tile_hi = pos0 + (col0 + max(min(cols, (t + 1) * kTile), t * kTile + 1) - 1) / a.group;
+        float m = kNegInf, l = 0.0f;
+        int vref = 0;
+        for (int j = 0; j < steps && ok; ++j) {
+            const int tok0 = (j < span.front ? j : span.start + j - span.front) * kTile;
+            ok = mbar_wait_warp(smem_u32(&bars.k_full[j & 1]), (j >> 1) & 1, &s_abort, a.seqs.status) &&
+                 mbar_wait_warp(smem_u32(&bars.s_full[t]), j & 1, &s_abort, a.seqs.status);
+            if (!ok) break;
+            tc_fence_after();
+            const StepInfo& info = s_info[j % kInfo];
+            const float c = fmaxf(cmul * info.kmul, 1e-37f);
+            const int vexp = info.vexp;
+            const uint32_t bad = info.bad;
+            uint32_t s[4][32];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) tmem_ld32(s_addr + i * 32, s[i]);
+            tmem_ld_wait();
+            const bool whole = bad == 0 && tok0 + kTile - 1 <= tile_lo &&
+                               (a.window == 0 || tok0 > tile_hi - a.window || tok0 + kTile <= a.sinks);
+            if (!whole) {
+                const int lim = max(pos - tok0, -1), low = a.window == 0 ? -(1 << 30) : lim - a.window, sk = a.sinks - tok0;
+#pragma unroll
+                for (int i = 0; i < 128; ++i) {
+                    const bool see = i <= lim && (i > low || i < sk) && !((bad >> (i >> 4)) & 1u);
+                    if (!see) s[i >> 5][i & 31] = __float_as_uint(kNegInf);
+                }
+            }
+            if (info.any_nan) {
+                // a column that sees a NaN value row is NaN
+#pragma unroll 1
+                for (int w = 0; w < 4; ++w) {
+                    uint32_t set = info.nan[w];
+                    while (set) {
+                        const int i = w * 32 + __ffs(set) - 1;
+                        set &= set - 1;
+                        const int p = tok0 + i;
+                        if (p <= pos && (a.window == 0 || p > pos - a.window || p < a.sinks)) l = __uint_as_float(0x7fc00000u);
+                    }
+                }
+            }
+            float top[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) top[e] = __uint_as_float(s[e][0]);
+#pragma unroll
+            for (int i = 1; i < 32; ++i)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) top[e] = fmaxf(top[e], __uint_as_float(s[e][i]));
+            const float mt = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * c;
+            if (j == 0) vref = vexp;
+            bool grow = mt > m + kGrow || (m == kNegInf && mt > kNegInf);
+            const bool vgrow = vexp > vref + 3;
+            if (__any_sync(0xffffffffu, grow) || vgrow) {
+                const float m_new = fmaxf(m, mt);
+                float f = m == kNegInf ? 0.0f : ex2(m - m_new);
+                if (!(m_new > kNegInf)) f = 1.0f;
+                l *= f;
+                m = m_new;
+                if (vgrow) {
+                    f *= ex2(static_cast<float>(vref - vexp));
+                    vref = vexp;
+                }
+                if (j > 0) {                             // P V of the steps before is done: S came after it
+#pragma unroll 1
+                    for (int i = 0; i < HD; i += 32) {
+                        uint32_t o[32];
+                        tmem_ld32(o_addr + i, o);
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                        tmem_st32(o_addr + i, o);
+                    }
+                    tmem_st_wait();
+                }
+            }
+            const float dv = static_cast<float>(vexp - vref);
+            const float off = (m == kNegInf ? 0.0f : m) - dv;
+            float sum[2] = {0.0f, 0.0f};
+#pragma unroll
+            for (int g = 0; g < 2; ++g) {
+                uint32_t p[32];
+#pragma unroll
+                for (int i = 0; i < 32; ++i) {
+                    const int e = g * 64 + 2 * i;
+                    const float p0 = ex2(fmaf(__uint_as_float(s[e >> 5][e & 31]), c, -off));
+                    const float p1 = ex2(fmaf(__uint_as_float(s[e >> 5][(e & 31) + 1]), c, -off));
+                    sum[0] += p0;
+                    sum[1] += p1;
+                    p[i] = pack_f16x2(p0, p1);
+                }
+                tmem_st32(s_addr + g * 32, p);
+            }
+            l += (sum[0] + sum[1]) * ex2(-dv);
+            tmem_st_wait();
+            tc_fence_before();
+            mbar_arrive(smem_u32(&bars.p_full[t]));
+        }
+        // ---- the result
+        float scale = 0.0f;
+        if (ok && steps > 0) {
+            ok = mbar_wait_warp(smem_u32(&bars.o_full), 0, &s_abort, a.seqs.status);
+            tc_fence_after();
+            scale = l == 0.0f ? 0.0f : pow2_field(min(max(vref, 1), 254)) / l;
+        }
+        if (ok) {
+            uint16_t* dst = a.out[rank] + (it.first_row + r) * a.ldo + (kvh * a.group + h) * HD;
+#pragma unroll 1
+            for (int i = 0; i < HD; i += 32) {
+                uint32_t o[32];
+                if (steps > 0) {
+                    tmem_ld32(o_addr + i, o);
+                    tmem_ld_wait();
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) o[e] = 0;
+                }
+                if (have) {
+#pragma unroll
+                    for (int e = 0; e < 32; e += 8) {
+                        uint32_t w[4];
+#pragma unroll
+                        for (int x = 0; x < 4; ++x)
+                            w[x] = pack_bf16x2(__uint_as_float(o[e + 2 * x]) * scale, __uint_as_float(o[e + 2 * x + 1]) * scale);
+                        *reinterpret_cast<uint4*>(dst + i + e) = make_uint4(w[0], w[1], w[2], w[3]);
+                    }
+                }
+            }
+        }
+    } else if (warp < 12) {
+        fewer_registers<88>();
+        // ------------------------------------------------ codes to operands
+        const int id = tid - 256, w = warp - 8;
+        const int32_t* row = a.seqs.table + it.seq * a.seqs.max_blocks;
+        const uint8_t* pool = a.pools.pool[rank];
+        constexpr int PARTS = HD / 32, KU = PARTS;       // 16-byte parts (32 elements) of a key; units of a thread
+        constexpr int VW = HD / 64;                      // words of a value row that a thread takes of eight tokens
+        const int tg = (lane & 7) + 8 * (w & 1), dw = (lane >> 3) + 4 * (w >> 1);
+        auto first_block = [&](int j) { return (j < span.front ? j : span.start + j - span.front) * (kTile / kKvBlock); };
+        // lanes 0-7: where the eight blocks of step j are, -1 when not there; past the last visible token
+        // there is nothing to read
+        auto fetch_offsets = [&](int j) -> int64_t {
+            int64_t off = -1;
+            if (lane < 8 && j < steps) {
+                const int64_t b = first_block(j) + lane;
+                if (b * kKvBlock <= last_pos) {
+                    off = kv_block_offset(row, a.seqs.max_blocks, a.pools.pages, a.pools.page_shift, a.pools.kv_heads, kvh,
+                                          b, B::BYTES);
+                    if (off < 0) raise_status(a.seqs.status, TP_ERR_INVALID_ARG);
+                }
+            }
+            return off;
+        };
+        auto fetch_pairs = [&](int j, int64_t off, uint32_t& kp, uint32_t& vp) {
+            const int64_t b = __shfl_sync(0xffffffffu, off, id >> 4);
+            kp = vp = 0;
+            if (b >= 0 && static_cast<int64_t>(first_block(j)) * kKvBlock + id <= last_pos) {
+                kp = __ldg(reinterpret_cast<const uint32_t*>(pool + b + B::KPAIR) + (id & 15));
+                vp = __ldg(reinterpret_cast<const uint32_t*>(pool + b + B::VPAIR) + (id & 15));
+            }
+        };
+        uint4 kc[KU];
+        auto fetch_keys = [&](int64_t off) {
+#pragma unroll
+            for (int i = 0; i < KU; ++i) {
+                const int u = i * kTile + id, token = u / PARTS, part = u % PARTS;
+                const int64_t b = __shfl_sync(0xffffffffu, off, token >> 4);
+                kc[i] = b >= 0 ? __ldg(reinterpret_cast<const uint4*>(pool + b + B::KEYS + (token & 15) * B::ROW) + part)
+                               : make_uint4(0, 0, 0, 0);
+            }
+        };
+        uint32_t vc[8][VW];
+        auto fetch_values = [&](int64_t off) {
+            const int64_t b = __shfl_sync(0xffffffffu, off, tg >> 1);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const uint8_t* p = pool + b + B::VALS + ((tg & 1) * 8 + i) * B::ROW + dw * 4 * VW;
+                if constexpr (VW == 2) {
+                    const uint2 v = b >= 0 ? __ldg(reinterpret_cast<const uint2*>(p)) : make_uint2(0, 0);
+                    vc[i][0] = v.x, vc[i][1] = v.y;
+                } else {
+                    vc[i][0] = b >= 0 ? __ldg(reinterpret_cast<const uint32_t*>(p)) : 0u;
+                }
+            }
+        };
+        // Registers of a step are refilled as soon as they are used: the loads of step j + 1 run under the
+        // conversions of step j.
+        int64_t off_now = fetch_offsets(0), off_next = fetch_offsets(1);
+        uint32_t kp, vp;
+        fetch_pairs(0, off_now, kp, vp);
+        fetch_keys(off_now);
+        fetch_values(off_now);
+        for (int j = 0; j < steps; ++j) {                // after a lost wait: no stores, but every barrier
+            const int st = j & 1;
+            const uint32_t there = __ballot_sync(0xffffffffu, off_now >= 0) & 0xffu;
+            const bool vnan = ((vp >> 16) & 0x7f80u) == 0x7f80u || (vp & 0x7f80u) == 0x7f80u;
+            if (vnan) vp = 0;
+            // F of the step: s 2^(127 - F) below 2^-8, |b| 2^(127 - F) below 2^15
+            auto field = [](uint32_t p) {
+                const int es = static_cast<int>((p >> 7) & 0xffu), eb = static_cast<int>((p >> 23) & 0xffu);
+                return max(es + 9, (eb == 255 ? 0 : eb) - 14);
+            };
+            const int kf = __reduce_max_sync(0xffffffffu, field(kp)), vf = __reduce_max_sync(0xffffffffu, field(vp));
+            const uint32_t nan_set = __ballot_sync(0xffffffffu, vnan);
+            if (lane == 0) {
+                s_exp[w][0] = kf;
+                s_exp[w][1] = vf;
+                s_nan[w] = nan_set;
+            }
+            asm volatile("bar.sync 1, 128;" ::: "memory");
+            const int kF = min(max(max(max(s_exp[0][0], s_exp[1][0]), max(s_exp[2][0], s_exp[3][0])), 24), 253);
+            const int vF = min(max(max(max(s_exp[0][1], s_exp[1][1]), max(s_exp[2][1], s_exp[3][1])), 24), 253);
+            {
+                // the step times 2^24: codes are u 2^-24
+                const float ks = __uint_as_float(kp << 16) * pow2_field(278 - kF);
+                const float kb = __uint_as_float(kp & 0xffff0000u) * pow2_field(254 - kF);
+                const float vs = __uint_as_float(vp << 16) * pow2_field(278 - vF);
+                const float vb = __uint_as_float(vp & 0xffff0000u) * pow2_field(254 - vF);
+                s_key[id] = pack_f16x2(ks, kb);
+                s_vstep[id] = static_cast<uint16_t>(pack_f16x2(vs, 0.0f));
+                s_vbase[id] = static_cast<uint16_t>(pack_f16x2(vb, 0.0f));
+                if (id == 0) {
+                    StepInfo& info = s_info[j % kInfo];
+                    info.kmul = pow2_field(kF);
+                    info.vexp = vF;
+                    // blocks past the last visible token are hidden by position
+                    info.bad = ~there & 0xffu;
+                    uint32_t any = 0;
+                    for (int i = 0; i < 4; ++i) any |= info.nan[i] = s_nan[i];
+                    info.any_nan = any;
+                }
+            }
+            asm volatile("bar.sync 1, 128;" ::: "memory");
+            off_now = off_next;
+            fetch_pairs(j + 1, off_now, kp, vp);
+            off_next = fetch_offsets(j + 2);
+            if (ok && j >= 2)
+                ok = mbar_wait_warp(smem_u32(&bars.k_empty[st]), ((j >> 1) + 1) & 1, &s_abort, a.seqs.status);
+            constexpr uint32_t M0 = 0x000f000fu, M4 = 0x00f000f0u, SIXTEENTH = 0x2c002c00u;   // (1/16, 1/16)
+            if (ok) {
+#pragma unroll
+            for (int i = 0; i < KU; ++i) {
+                const int u = i * kTile + id, token = u / PARTS, part = u % PARTS;
+                const uint32_t sb = s_key[token];
+                const uint32_t s1 = __byte_perm(sb, sb, 0x1010), b1 = __byte_perm(sb, sb, 0x3232);
+                const uint32_t s16 = hfma2(s1, SIXTEENTH, 0u);
+                // the two halves of the lanes store in another order, so that eight lanes meet eight bank groups
+                const bool flip = part & 2;
+                const uint32_t wd[4] = {flip ? kc[i].z : kc[i].x, flip ? kc[i].w : kc[i].y, flip ? kc[i].x : kc[i].z,
+                                        flip ? kc[i].y : kc[i].w};
+                const uint32_t base = sm + C::K + st * C::KB + (part >> 1) * C::ATOM + token * 128;
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                    const int chunk = (part & 1) * 4 + (flip ? x ^ 2 : x);
+                    const uint32_t v = wd[x], hgh = v >> 8;
+                    st_shared_v4(base + ((chunk ^ (token & 7)) << 4), hfma2(v & M0, s1, b1), hfma2(v & M4, s16, b1),
+                                 hfma2(hgh & M0, s1, b1), hfma2(hgh & M4, s16, b1));
+                }
+            }
+            fence_proxy_async_cta();
+            mbar_arrive(smem_u32(&bars.k_full[st]));
+            }
+            fetch_keys(off_now);
+
+            if (ok && j >= 2)
+                ok = mbar_wait_warp(smem_u32(&bars.v_empty[st]), ((j >> 1) + 1) & 1, &s_abort, a.seqs.status);
+            if (ok) {
+                const uint4 vs = *reinterpret_cast<const uint4*>(&s_vstep[tg * 8]);
+                const uint4 vb = *reinterpret_cast<const uint4*>(&s_vbase[tg * 8]);
+                const uint32_t s1[4] = {vs.x, vs.y, vs.z, vs.w}, b1[4] = {vb.x, vb.y, vb.z, vb.w};
+                uint32_t s16[4];
+#pragma unroll
+                for (int p = 0; p < 4; ++p) s16[p] = hfma2(s1[p], SIXTEENTH, 0u);
+#pragma unroll
+                for (int x = 0; x < VW; ++x)
+#pragma unroll
+                    for (int hw = 0; hw < 2; ++hw) {
+                        uint32_t pr[4];
+#pragma unroll
+                        for (int p = 0; p < 4; ++p) pr[p] = __byte_perm(vc[2 * p][x], vc[2 * p + 1][x], hw ? 0x7632 : 0x5410);
+#pragma unroll
+                        for (int b = 0; b < 2; ++b) {
+                            const int d = dw * 8 * VW + x * 8 + hw * 4 + b * 2;     // and d + 1
+                            const uint32_t at = sm + C::V + st * C::KB + (tg >> 3) * C::VATOM;
+                            st_shared_v4(at + d * 128 + (((tg & 7) ^ (d & 7)) << 4), hfma2(pr[0] & M0, s1[0], b1[0]),
+                                         hfma2(pr[1] & M0, s1[1], b1[1]), hfma2(pr[2] & M0, s1[2], b1[2]),
+                                         hfma2(pr[3] & M0, s1[3], b1[3]));
+                            st_shared_v4(at + (d + 1) * 128 + (((tg & 7) ^ ((d + 1) & 7)) << 4),
+                                         hfma2(pr[0] & M4, s16[0], b1[0]), hfma2(pr[1] & M4, s16[1], b1[1]),
+                                         hfma2(pr[2] & M4, s16[2], b1[2]), hfma2(pr[3] & M4, s16[3], b1[3]));
+#pragma unroll
+                            for (int p = 0; p < 4; ++p) pr[p] >>= 8;
+                        }
+                    }
+                fence_proxy_async_cta();
+                mbar_arrive(smem_u32(&bars.v_full[st]));
+            }
+            fetch_values(off_now);
+        }
+    } else {
+        fewer_registers<40>();
+        if (warp == 12 && lane == 0 && steps > 0) {
+            // ------------------------------------------------ the products
+            constexpr uint32_t QK = idesc_f16(128, 128), PV = idesc_f16(128, HD);
+            auto wait = [&](uint64_t& b, int parity) {
+                ok = ok && mbar_wait(smem_u32(&b), parity, &s_abort, a.seqs.status);
+                tc_fence_after();
+                return ok;
+            };
+            auto scores = [&](int t, int j) {
+                const uint64_t qd = sw128_kmajor_desc(sm + C::Q + t * C::QB);
+                const uint64_t kd = sw128_kmajor_desc(sm + C::K + (j & 1) * C::KB);
+#pragma unroll
+                for (int k = 0; k < HD / 16; ++k) {
+                    const uint64_t o = static_cast<uint64_t>(((k >> 2) * C::ATOM + (k & 3) * 32) >> 4);
+                    tc_mma(tmem + C::S_COL + t * kTile, qd + o, kd + o, QK, k > 0);
+                }
+                tc_commit(smem_u32(&bars.s_full[t]));
+            };
+            auto values = [&](int t, int j) {
+                const uint64_t vd = sw128_kmajor_desc(sm + C::V + (j & 1) * C::KB);
+#pragma unroll
+                for (int k = 0; k < kTile / 16; ++k) {
+                    const uint64_t o = static_cast<uint64_t>(((k >> 2) * C::VATOM + (k & 3) * 32) >> 4);
+                    tc_mma_ts(tmem + C::O_COL + t * HD, tmem + C::S_COL + t * kTile + k * 8, vd + o, PV, j > 0 || k > 0);
+                }
+            };
+            if (wait(bars.q_full, 0) && wait(bars.k_full[0], 0)) {
+                scores(0, 0);
+                scores(1, 0);
+                tc_commit(smem_u32(&bars.k_empty[0]));
+            }
+            for (int j = 0; j < steps && ok; ++j) {
+                const bool more = j + 1 < steps;
+                if (!wait(bars.v_full[j & 1], (j >> 1) & 1) || !wait(bars.p_full[0], j & 1)) break;
+                values(0, j);
+                if (more) {
+                    if (!wait(bars.k_full[(j + 1) & 1], ((j + 1) >> 1) & 1)) break;
+                    scores(0, j + 1);
+                }
+                if (!wait(bars.p_full[1], j & 1)) break;
+                values(1, j);
+                tc_commit(smem_u32(&bars.v_empty[j & 1]));
+                if (more) {
+                    scores(1, j + 1);
+                    tc_commit(smem_u32(&bars.k_empty[(j + 1) & 1]));
+                }
+            }
+            if (ok) tc_commit(smem_u32(&bars.o_full));
+        }
+        __syncwarp();
+    }
+    if (s_abort) spin_ns(1000000);   // products that were issued end before their memory is given back
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 0) tmem_dealloc<512>(tmem);
+}
+
+template <int HD>
+tp_status launch(const AttnArgs& a, cudaStream_t stream) {
+    static std::atomic<uint64_t> smem_set{0};
+    auto* kern = kv4_attention_many_kernel<HD>;
+    if (!smem_attribute_once(reinterpret_cast<const void*>(kern), Cfg<HD>::SMEM, smem_set)) return TP_ERR_CUDA;
+    // as many tiles as n rows in at most nseq sequences can make
+    const int64_t cols = static_cast<int64_t>(a.seqs.n) * a.group;
+    const int64_t tiles = cols / kCols + std::min<int64_t>(a.seqs.nseq, cols / a.many);
+    const int64_t blocks = tiles * a.pools.t * a.pools.kv_heads;
+    if (blocks > INT32_MAX) return TP_ERR_UNSUPPORTED;
+    const cudaError_t e = launch_pdl(kern, dim3(static_cast<unsigned>(blocks)), dim3(kThreads), Cfg<HD>::SMEM, stream, a);
+    return e == cudaSuccess ? TP_OK : TP_ERR_CUDA;
+}
+
+}  // namespace
+
+tp_status launch_attention_many(const AttnArgs& a, int head_dim, cudaStream_t stream) {
+    return head_dim == 128 ? launch<128>(a, stream) : launch<64>(a, stream);
+}
+
+}  // namespace tpk
