@@ -52,13 +52,12 @@ struct Cfg {
     static constexpr int S_COL = 0, O_COL = 256;         // TMEM columns: S of the tiles, then O of the tiles
 };
 
-// What the softmax has to know of a step.
+// What the softmax has to know of a step, by quarters of 32 tokens.
 struct StepInfo {
-    float kmul;                      // 2^(F - 127) of the keys
-    int vexp;                        // F of the values
-    uint32_t bad;                    // blocks that are not there
-    uint32_t any_nan;
+    float kmul[4];                   // 2^(F - 127) of the keys
+    int vexp[4];                     // F of the values
     uint32_t nan[4];                 // tokens whose value row stands for NaN
+    uint32_t bad[4];                 // blocks that are not there, as bits of the step's eight
 };
 
 __device__ __forceinline__ float pow2_field(int field) { return __uint_as_float(static_cast<uint32_t>(field) << 23); }
@@ -98,6 +97,38 @@ __device__ __forceinline__ uint32_t hfma2(uint32_t a, uint32_t b, uint32_t c) {
     return d;
 }
 
+// One lane of the (converged) warp.  The compiler knows elect.sync's predicate for one lane's and keeps
+// descriptors in uniform registers under it.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t e;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xffffffff;\n\t"
+        "selp.b32 %0, 1, 0, p;\n\t}"
+        : "=r"(e));
+    return e != 0;
+}
+
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ uint64_t pack2(float lo, float hi) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ void unpack2(uint64_t v, float& lo, float& hi) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+
 template <int N>
 __device__ __forceinline__ void more_registers() {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
@@ -130,8 +161,6 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_many_kernel(const _
     __shared__ StepInfo s_info[kInfo];
     __shared__ __align__(16) uint32_t s_key[kTile];      // fp16 pairs (step, base) of the step's keys
     __shared__ __align__(16) uint16_t s_vstep[kTile], s_vbase[kTile];
-    __shared__ int s_exp[4][2];
-    __shared__ uint32_t s_nan[4];
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t sm = (smem_u32(smem_raw) + 1023u) & ~1023u;
@@ -274,9 +303,16 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_many_kernel(const _
             if (!ok) break;
             tc_fence_after();
             const StepInfo& info = s_info[j % kInfo];
-            const float c = fmaxf(cmul * info.kmul, 1e-37f);
-            const int vexp = info.vexp;
-            const uint32_t bad = info.bad;
+            float c[4];
+            int vexp[4];
+            uint32_t bad = 0, any_nan = 0;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                c[e] = fmaxf(cmul * info.kmul[e], 1e-37f);
+                vexp[e] = info.vexp[e];
+                bad |= info.bad[e];
+                any_nan |= info.nan[e];
+            }
             uint32_t s[4][32];
 #pragma unroll
             for (int i = 0; i < 4; ++i) tmem_ld32(s_addr + i * 32, s[i]);
@@ -291,7 +327,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_many_kernel(const _
                     if (!see) s[i >> 5][i & 31] = __float_as_uint(kNegInf);
                 }
             }
-            if (info.any_nan) {
+            if (any_nan) {
                 // a column that sees a NaN value row is NaN
 #pragma unroll 1
                 for (int w = 0; w < 4; ++w) {
@@ -304,17 +340,21 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_many_kernel(const _
                     }
                 }
             }
-            float top[4];
+            float mt = kNegInf;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) top[e] = __uint_as_float(s[e][0]);
+            for (int e = 0; e < 4; ++e) {
+                float u = __uint_as_float(s[e][0]), v = __uint_as_float(s[e][1]);
 #pragma unroll
-            for (int i = 1; i < 32; ++i)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) top[e] = fmaxf(top[e], __uint_as_float(s[e][i]));
-            const float mt = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * c;
-            if (j == 0) vref = vexp;
-            bool grow = mt > m + kGrow || (m == kNegInf && mt > kNegInf);
-            const bool vgrow = vexp > vref + 3;
+                for (int i = 2; i < 32; i += 4) {
+                    u = fmaxf(fmaxf(u, __uint_as_float(s[e][i])), __uint_as_float(s[e][i + 1]));
+                    if (i + 2 < 32) v = fmaxf(fmaxf(v, __uint_as_float(s[e][i + 2])), __uint_as_float(s[e][i + 3]));
+                }
+                mt = fmaxf(mt, fmaxf(u, v) * c[e]);
+            }
+            const int vtop = max(max(vexp[0], vexp[1]), max(vexp[2], vexp[3]));
+            if (j == 0) vref = vtop;
+            const bool grow = mt > m + kGrow || (m == kNegInf && mt > kNegInf);
+            const bool vgrow = vtop > vref + 3;
             if (__any_sync(0xffffffffu, grow) || vgrow) {
                 const float m_new = fmaxf(m, mt);
                 float f = m == kNegInf ? 0.0f : ex2(m - m_new);
@@ -322,8 +362,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_many_kernel(const _
                 l *= f;
                 m = m_new;
                 if (vgrow) {
-                    f *= ex2(static_cast<float>(vref - vexp));
-                    vref = vexp;
+                    f *= ex2(static_cast<float>(vref - vtop));
+                    vref = vtop;
                 }
                 if (j > 0) {                             // P V of the steps before is done: S came after it
 #pragma unroll 1
@@ -338,24 +378,30 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_many_kernel(const _
                     tmem_st_wait();
                 }
             }
-            const float dv = static_cast<float>(vexp - vref);
-            const float off = (m == kNegInf ? 0.0f : m) - dv;
-            float sum[2] = {0.0f, 0.0f};
+            const float base = m == kNegInf ? 0.0f : m;
 #pragma unroll
             for (int g = 0; g < 2; ++g) {
                 uint32_t p[32];
 #pragma unroll
-                for (int i = 0; i < 32; ++i) {
-                    const int e = g * 64 + 2 * i;
-                    const float p0 = ex2(fmaf(__uint_as_float(s[e >> 5][e & 31]), c, -off));
-                    const float p1 = ex2(fmaf(__uint_as_float(s[e >> 5][(e & 31) + 1]), c, -off));
-                    sum[0] += p0;
-                    sum[1] += p1;
-                    p[i] = pack_f16x2(p0, p1);
+                for (int h2 = 0; h2 < 2; ++h2) {
+                    const int e = 2 * g + h2;
+                    const float dv = static_cast<float>(vexp[e] - vref);
+                    const uint64_t cc2 = pack2(c[e], c[e]), off2 = pack2(dv - base, dv - base);
+                    uint64_t sum2 = 0;
+#pragma unroll
+                    for (int i = 0; i < 32; i += 2) {
+                        float x0, x1;
+                        unpack2(fma2(pack2(__uint_as_float(s[e][i]), __uint_as_float(s[e][i + 1])), cc2, off2), x0, x1);
+                        const float p0 = ex2(x0), p1 = ex2(x1);
+                        sum2 = add2(sum2, pack2(p0, p1));
+                        p[h2 * 16 + i / 2] = pack_f16x2(p0, p1);
+                    }
+                    float a0, a1;
+                    unpack2(sum2, a0, a1);
+                    l = fmaf(a0 + a1, ex2(-dv), l);
                 }
                 tmem_st32(s_addr + g * 32, p);
             }
-            l += (sum[0] + sum[1]) * ex2(-dv);
             tmem_st_wait();
             tc_fence_before();
             mbar_arrive(smem_u32(&bars.p_full[t]));
@@ -399,35 +445,34 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_many_kernel(const _
         const uint8_t* pool = a.pools.pool[rank];
         constexpr int PARTS = HD / 32, KU = PARTS;       // 16-byte parts (32 elements) of a key; units of a thread
         constexpr int VW = HD / 64;                      // words of a value row that a thread takes of eight tokens
-        const int tg = (lane & 7) + 8 * (w & 1), dw = (lane >> 3) + 4 * (w >> 1);
+        // A warp takes 32 tokens, so nothing but their shared-memory words passes between its lanes.
+        const int tg = 4 * w + (lane & 3), dw = lane >> 2;
         auto first_block = [&](int j) { return (j < span.front ? j : span.start + j - span.front) * (kTile / kKvBlock); };
-        // lanes 0-7: where the eight blocks of step j are, -1 when not there; past the last visible token
-        // there is nothing to read
-        auto fetch_offsets = [&](int j) -> int64_t {
-            int64_t off = -1;
-            if (lane < 8 && j < steps) {
-                const int64_t b = first_block(j) + lane;
-                if (b * kKvBlock <= last_pos) {
-                    off = kv_block_offset(row, a.seqs.max_blocks, a.pools.pages, a.pools.page_shift, a.pools.kv_heads, kvh,
-                                          b, B::BYTES);
-                    if (off < 0) raise_status(a.seqs.status, TP_ERR_INVALID_ARG);
-                }
-            }
+        // lanes 0 and 1: the page of the warp's two blocks of step j; -2 past the last visible token, where
+        // nothing is read
+        auto fetch_page = [&](int j) -> int {
+            const int64_t b = first_block(j) + 2 * w + (lane & 1);
+            return j < steps && b * kKvBlock <= last_pos ? kv_page_at(row, a.seqs.max_blocks, a.pools.page_shift, b) : -2;
+        };
+        auto offset_of = [&](int j, int page) -> int64_t {
+            const int64_t off = kv_page_offset(page, a.pools.pages, a.pools.page_shift, a.pools.kv_heads, kvh,
+                                               first_block(j) + 2 * w + (lane & 1), B::BYTES);
+            if (off < 0 && page != -2) raise_status(a.seqs.status, TP_ERR_INVALID_ARG);
             return off;
         };
         auto fetch_pairs = [&](int j, int64_t off, uint32_t& kp, uint32_t& vp) {
-            const int64_t b = __shfl_sync(0xffffffffu, off, id >> 4);
+            const int64_t b = __shfl_sync(0xffffffffu, off, lane >> 4);
             kp = vp = 0;
             if (b >= 0 && static_cast<int64_t>(first_block(j)) * kKvBlock + id <= last_pos) {
-                kp = __ldg(reinterpret_cast<const uint32_t*>(pool + b + B::KPAIR) + (id & 15));
-                vp = __ldg(reinterpret_cast<const uint32_t*>(pool + b + B::VPAIR) + (id & 15));
+                kp = __ldg(reinterpret_cast<const uint32_t*>(pool + b + B::KPAIR) + (lane & 15));
+                vp = __ldg(reinterpret_cast<const uint32_t*>(pool + b + B::VPAIR) + (lane & 15));
             }
         };
         uint4 kc[KU];
         auto fetch_keys = [&](int64_t off) {
 #pragma unroll
             for (int i = 0; i < KU; ++i) {
-                const int u = i * kTile + id, token = u / PARTS, part = u % PARTS;
+                const int u = i * 32 + lane, token = u / PARTS, part = u % PARTS;      // token of the warp's 32
                 const int64_t b = __shfl_sync(0xffffffffu, off, token >> 4);
                 kc[i] = b >= 0 ? __ldg(reinterpret_cast<const uint4*>(pool + b + B::KEYS + (token & 15) * B::ROW) + part)
                                : make_uint4(0, 0, 0, 0);
@@ -435,7 +480,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_many_kernel(const _
         };
         uint32_t vc[8][VW];
         auto fetch_values = [&](int64_t off) {
-            const int64_t b = __shfl_sync(0xffffffffu, off, tg >> 1);
+            const int64_t b = __shfl_sync(0xffffffffu, off, (lane >> 1) & 1);
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 const uint8_t* p = pool + b + B::VALS + ((tg & 1) * 8 + i) * B::ROW + dw * 4 * VW;
@@ -448,32 +493,27 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_many_kernel(const _
             }
         };
         // Registers of a step are refilled as soon as they are used: the loads of step j + 1 run under the
-        // conversions of step j.
-        int64_t off_now = fetch_offsets(0), off_next = fetch_offsets(1);
+        // conversions of step j, and the page numbers are one more step ahead.
+        int page_next = fetch_page(1);
+        int64_t off = offset_of(0, fetch_page(0));
         uint32_t kp, vp;
-        fetch_pairs(0, off_now, kp, vp);
-        fetch_keys(off_now);
-        fetch_values(off_now);
-        for (int j = 0; j < steps; ++j) {                // after a lost wait: no stores, but every barrier
+        fetch_pairs(0, off, kp, vp);
+        fetch_keys(off);
+        fetch_values(off);
+        for (int j = 0; j < steps; ++j) {
             const int st = j & 1;
-            const uint32_t there = __ballot_sync(0xffffffffu, off_now >= 0) & 0xffu;
+            const uint32_t there = __ballot_sync(0xffffffffu, off >= 0) & 3u;
             const bool vnan = ((vp >> 16) & 0x7f80u) == 0x7f80u || (vp & 0x7f80u) == 0x7f80u;
             if (vnan) vp = 0;
-            // F of the step: s 2^(127 - F) below 2^-8, |b| 2^(127 - F) below 2^15
+            // F of the quarter: s 2^(127 - F) below 2^-8, |b| 2^(127 - F) below 2^15
             auto field = [](uint32_t p) {
                 const int es = static_cast<int>((p >> 7) & 0xffu), eb = static_cast<int>((p >> 23) & 0xffu);
                 return max(es + 9, (eb == 255 ? 0 : eb) - 14);
             };
-            const int kf = __reduce_max_sync(0xffffffffu, field(kp)), vf = __reduce_max_sync(0xffffffffu, field(vp));
+            const int kF = min(max(__reduce_max_sync(0xffffffffu, field(kp)), 24), 253);
+            const int vF = min(max(__reduce_max_sync(0xffffffffu, field(vp)), 24), 253);
             const uint32_t nan_set = __ballot_sync(0xffffffffu, vnan);
-            if (lane == 0) {
-                s_exp[w][0] = kf;
-                s_exp[w][1] = vf;
-                s_nan[w] = nan_set;
-            }
-            asm volatile("bar.sync 1, 128;" ::: "memory");
-            const int kF = min(max(max(max(s_exp[0][0], s_exp[1][0]), max(s_exp[2][0], s_exp[3][0])), 24), 253);
-            const int vF = min(max(max(max(s_exp[0][1], s_exp[1][1]), max(s_exp[2][1], s_exp[3][1])), 24), 253);
+            __syncwarp();                                // the lanes are done with the words of step j - 1
             {
                 // the step times 2^24: codes are u 2^-24
                 const float ks = __uint_as_float(kp << 16) * pow2_field(278 - kF);
@@ -483,28 +523,24 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_many_kernel(const _
                 s_key[id] = pack_f16x2(ks, kb);
                 s_vstep[id] = static_cast<uint16_t>(pack_f16x2(vs, 0.0f));
                 s_vbase[id] = static_cast<uint16_t>(pack_f16x2(vb, 0.0f));
-                if (id == 0) {
+                if (lane == 0) {
                     StepInfo& info = s_info[j % kInfo];
-                    info.kmul = pow2_field(kF);
-                    info.vexp = vF;
-                    // blocks past the last visible token are hidden by position
-                    info.bad = ~there & 0xffu;
-                    uint32_t any = 0;
-                    for (int i = 0; i < 4; ++i) any |= info.nan[i] = s_nan[i];
-                    info.any_nan = any;
+                    info.kmul[w] = pow2_field(kF);
+                    info.vexp[w] = vF;
+                    info.nan[w] = nan_set;
+                    info.bad[w] = (~there & 3u) << (2 * w);      // past the last visible token too: no matter
                 }
             }
-            asm volatile("bar.sync 1, 128;" ::: "memory");
-            off_now = off_next;
-            fetch_pairs(j + 1, off_now, kp, vp);
-            off_next = fetch_offsets(j + 2);
-            if (ok && j >= 2)
-                ok = mbar_wait_warp(smem_u32(&bars.k_empty[st]), ((j >> 1) + 1) & 1, &s_abort, a.seqs.status);
+            __syncwarp();
+            off = offset_of(j + 1, page_next);
+            fetch_pairs(j + 1, off, kp, vp);
+            page_next = fetch_page(j + 2);
+            if (j >= 2) ok = mbar_wait_warp(smem_u32(&bars.k_empty[st]), ((j >> 1) + 1) & 1, &s_abort, a.seqs.status);
+            if (!ok) break;
             constexpr uint32_t M0 = 0x000f000fu, M4 = 0x00f000f0u, SIXTEENTH = 0x2c002c00u;   // (1/16, 1/16)
-            if (ok) {
 #pragma unroll
             for (int i = 0; i < KU; ++i) {
-                const int u = i * kTile + id, token = u / PARTS, part = u % PARTS;
+                const int u = i * 32 + lane, token = 32 * w + u / PARTS, part = u % PARTS;
                 const uint32_t sb = s_key[token];
                 const uint32_t s1 = __byte_perm(sb, sb, 0x1010), b1 = __byte_perm(sb, sb, 0x3232);
                 const uint32_t s16 = hfma2(s1, SIXTEENTH, 0u);
@@ -523,29 +559,31 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_many_kernel(const _
             }
             fence_proxy_async_cta();
             mbar_arrive(smem_u32(&bars.k_full[st]));
-            }
-            fetch_keys(off_now);
+            fetch_keys(off);
 
-            if (ok && j >= 2)
-                ok = mbar_wait_warp(smem_u32(&bars.v_empty[st]), ((j >> 1) + 1) & 1, &s_abort, a.seqs.status);
-            if (ok) {
+            if (j >= 2) ok = mbar_wait_warp(smem_u32(&bars.v_empty[st]), ((j >> 1) + 1) & 1, &s_abort, a.seqs.status);
+            if (!ok) break;
+            {
                 const uint4 vs = *reinterpret_cast<const uint4*>(&s_vstep[tg * 8]);
                 const uint4 vb = *reinterpret_cast<const uint4*>(&s_vbase[tg * 8]);
                 const uint32_t s1[4] = {vs.x, vs.y, vs.z, vs.w}, b1[4] = {vb.x, vb.y, vb.z, vb.w};
                 uint32_t s16[4];
 #pragma unroll
                 for (int p = 0; p < 4; ++p) s16[p] = hfma2(s1[p], SIXTEENTH, 0u);
+                const uint32_t at = sm + C::V + st * C::KB + (tg >> 3) * C::VATOM;
 #pragma unroll
                 for (int x = 0; x < VW; ++x)
 #pragma unroll
-                    for (int hw = 0; hw < 2; ++hw) {
+                    for (int i = 0; i < 2; ++i) {
+                        // dimensions 0-3 or 4-7 of the word; odd lanes of dw the other half first (bank groups)
+                        const int hw = i ^ (dw & 1);
+                        const uint32_t sel = hw ? 0x7632u : 0x5410u;
                         uint32_t pr[4];
 #pragma unroll
-                        for (int p = 0; p < 4; ++p) pr[p] = __byte_perm(vc[2 * p][x], vc[2 * p + 1][x], hw ? 0x7632 : 0x5410);
+                        for (int p = 0; p < 4; ++p) pr[p] = __byte_perm(vc[2 * p][x], vc[2 * p + 1][x], sel);
 #pragma unroll
                         for (int b = 0; b < 2; ++b) {
                             const int d = dw * 8 * VW + x * 8 + hw * 4 + b * 2;     // and d + 1
-                            const uint32_t at = sm + C::V + st * C::KB + (tg >> 3) * C::VATOM;
                             st_shared_v4(at + d * 128 + (((tg & 7) ^ (d & 7)) << 4), hfma2(pr[0] & M0, s1[0], b1[0]),
                                          hfma2(pr[1] & M0, s1[1], b1[1]), hfma2(pr[2] & M0, s1[2], b1[2]),
                                          hfma2(pr[3] & M0, s1[3], b1[3]));
@@ -556,43 +594,51 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_many_kernel(const _
                             for (int p = 0; p < 4; ++p) pr[p] >>= 8;
                         }
                     }
-                fence_proxy_async_cta();
-                mbar_arrive(smem_u32(&bars.v_full[st]));
             }
-            fetch_values(off_now);
+            fence_proxy_async_cta();
+            mbar_arrive(smem_u32(&bars.v_full[st]));
+            fetch_values(off);
         }
     } else {
         fewer_registers<40>();
-        if (warp == 12 && lane == 0 && steps > 0) {
+        if (warp == 12 && steps > 0) {
             // ------------------------------------------------ the products
             constexpr uint32_t QK = idesc_f16(128, 128), PV = idesc_f16(128, HD);
             auto wait = [&](uint64_t& b, int parity) {
-                ok = ok && mbar_wait(smem_u32(&b), parity, &s_abort, a.seqs.status);
+                ok = ok && mbar_wait_warp(smem_u32(&b), parity, &s_abort, a.seqs.status);
                 tc_fence_after();
                 return ok;
             };
-            auto scores = [&](int t, int j) {
+            auto scores = [&](int t, int j) {            // and what waits for them
                 const uint64_t qd = sw128_kmajor_desc(sm + C::Q + t * C::QB);
                 const uint64_t kd = sw128_kmajor_desc(sm + C::K + (j & 1) * C::KB);
+                if (elect_one()) {
 #pragma unroll
-                for (int k = 0; k < HD / 16; ++k) {
-                    const uint64_t o = static_cast<uint64_t>(((k >> 2) * C::ATOM + (k & 3) * 32) >> 4);
-                    tc_mma(tmem + C::S_COL + t * kTile, qd + o, kd + o, QK, k > 0);
+                    for (int k = 0; k < HD / 16; ++k) {
+                        const uint64_t o = static_cast<uint64_t>(((k >> 2) * C::ATOM + (k & 3) * 32) >> 4);
+                        tc_mma(tmem + C::S_COL + t * kTile, qd + o, kd + o, QK, k > 0);
+                    }
+                    tc_commit(smem_u32(&bars.s_full[t]));
+                    if (t == 1) tc_commit(smem_u32(&bars.k_empty[j & 1]));
                 }
-                tc_commit(smem_u32(&bars.s_full[t]));
+                __syncwarp();
             };
             auto values = [&](int t, int j) {
                 const uint64_t vd = sw128_kmajor_desc(sm + C::V + (j & 1) * C::KB);
+                if (elect_one()) {
 #pragma unroll
-                for (int k = 0; k < kTile / 16; ++k) {
-                    const uint64_t o = static_cast<uint64_t>(((k >> 2) * C::VATOM + (k & 3) * 32) >> 4);
-                    tc_mma_ts(tmem + C::O_COL + t * HD, tmem + C::S_COL + t * kTile + k * 8, vd + o, PV, j > 0 || k > 0);
+                    for (int k = 0; k < kTile / 16; ++k) {
+                        const uint64_t o = static_cast<uint64_t>(((k >> 2) * C::VATOM + (k & 3) * 32) >> 4);
+                        tc_mma_ts(tmem + C::O_COL + t * HD, tmem + C::S_COL + t * kTile + k * 8, vd + o, PV, j > 0 || k > 0);
+                    }
+                    if (t == 1) tc_commit(smem_u32(&bars.v_empty[j & 1]));
+                    if (t == 1 && j + 1 == steps) tc_commit(smem_u32(&bars.o_full));
                 }
+                __syncwarp();
             };
             if (wait(bars.q_full, 0) && wait(bars.k_full[0], 0)) {
                 scores(0, 0);
                 scores(1, 0);
-                tc_commit(smem_u32(&bars.k_empty[0]));
             }
             for (int j = 0; j < steps && ok; ++j) {
                 const bool more = j + 1 < steps;
@@ -604,13 +650,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_many_kernel(const _
                 }
                 if (!wait(bars.p_full[1], j & 1)) break;
                 values(1, j);
-                tc_commit(smem_u32(&bars.v_empty[j & 1]));
-                if (more) {
-                    scores(1, j + 1);
-                    tc_commit(smem_u32(&bars.k_empty[(j + 1) & 1]));
-                }
+                if (more) scores(1, j + 1);
             }
-            if (ok) tc_commit(smem_u32(&bars.o_full));
         }
         __syncwarp();
     }

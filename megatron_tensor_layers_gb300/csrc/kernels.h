@@ -210,20 +210,32 @@ struct KvPools {
     int kv_heads = 0;
 };
 
-// Byte offset in a pool of block `block` (16 tokens) of the sequence with page
-// table row `row`, for kv head `head`; -1 when the table does not reach that
-// far or names no page of the pool.  The only place where a page number
-// becomes an address.
 #ifdef __CUDACC__
-__host__ __device__
+#define TPK_BOTH __host__ __device__
+#else
+#define TPK_BOTH
 #endif
-inline int64_t kv_block_offset(const int32_t* row, int64_t max_blocks, int64_t pages, int page_shift, int kv_heads,
-                               int head, int64_t block, int block_bytes) {
+
+// The page number that page table row `row` names for block `block` (16
+// tokens); -1 past the row's end.  Not checked against the pool.
+TPK_BOTH inline int32_t kv_page_at(const int32_t* row, int64_t max_blocks, int page_shift, int64_t block) {
     const int64_t at = block >> page_shift;
-    if (block < 0 || at >= max_blocks) return -1;
-    const int64_t page = row[at];
+    return block < 0 || at >= max_blocks ? -1 : row[at];
+}
+
+// Byte offset in a pool of block `block` of a sequence whose page for it is
+// `page`, for kv head `head`; -1 when the pool has no such page.  The only
+// place where a page number becomes an address.
+TPK_BOTH inline int64_t kv_page_offset(int32_t page, int64_t pages, int page_shift, int kv_heads, int head, int64_t block,
+                                       int block_bytes) {
     if (page < 0 || page >= pages) return -1;
-    return (((page * kv_heads + head) << page_shift) + (block & ((1 << page_shift) - 1))) * block_bytes;
+    return (((static_cast<int64_t>(page) * kv_heads + head) << page_shift) + (block & ((1 << page_shift) - 1))) * block_bytes;
+}
+
+TPK_BOTH inline int64_t kv_block_offset(const int32_t* row, int64_t max_blocks, int64_t pages, int page_shift, int kv_heads,
+                                        int head, int64_t block, int block_bytes) {
+    return kv_page_offset(kv_page_at(row, max_blocks, page_shift, block), pages, page_shift, kv_heads, head, block,
+                          block_bytes);
 }
 
 struct KvAppendDesc {
