@@ -8,21 +8,31 @@
 //   P = 2^(c S - m)    one thread per column, fp32, P as fp16 over S in TMEM;
 //   O += P V           tcgen05, P from TMEM, V^T from shared memory, O in TMEM.
 // Warps 0-3 and 4-7 are the softmax of one tile each and take turns with the
-// tensor core, warps 8-11 turn codes into operands, warp 12 issues the products.
+// tensor core, warps 8-11 turn codes into operands (two cache blocks of 16
+// tokens each), warp 12 issues the products.
 //
 // Codes to operands.  A code is an fp16 subnormal u 2^-24 (or 16 u 2^-24) after
 // one mask, and one HFMA2 makes the fp16 value (s u + b) 2^-F of two elements:
 // 9 instructions for 8 keys, shared by all 256 columns.  F is the exponent of
-// the largest step or base of the 128 tokens, so that nothing overflows; a value
-// is rounded once, by at most 2^-11 of itself or 2^-25 of the tile's scale
-// 2^F.  The scale of K enters the exponent's factor c, the scale of V the
-// exponent itself (P 2^(F - Fref)), both per tile.  Keys keep their packed order
+// the largest step or base of 32 tokens, so that nothing overflows; a value is
+// rounded once, by at most 2^-11 of itself or 2^-25 of their scale 2^F.  The
+// scale of K enters the exponent's factor c, the scale of V the exponent itself
+// (P 2^(F - Fref)), both per 32 tokens.  Keys keep their packed order
 // (q is permuted to it), values are transposed while they are unpacked: eight
 // tokens' words give eight dimensions' 16-byte chunks of V^T.
 //
-// The maximum m that is subtracted follows the true one lazily: O and the sum
-// are rescaled only when a column's maximum has grown by more than 2^8, which
-// fp16 and fp32 have room for.
+// What is subtracted, m, is a column's maximum as of the last time it was
+// needed.  A step first takes P under the old m and adds it up; a sum of at most
+// 2^12 says that no P has left fp16, and m stays.  Only otherwise, or while the
+// column has seen nothing, the step's maximum is taken, O and the sum are
+// rescaled to it and P is taken again.  The usual step therefore reads S once
+// and has no maximum in it (128 fewer operations on the pipe that the unpacking
+// needs too).
+//
+// What bounds it now is shared memory: per step Q and K are read for both
+// tiles' S, V for both O, and the operands written, 256 KB at 128 bytes a cycle.
+// Codes therefore go from global memory to registers (a ring of records in
+// shared memory, filled by bulk copies, measured 5 % slower).
 //
 // A value row that stands for NaN is put in as 0 and its token noted; a column
 // that sees such a token gets a NaN sum, the others are not touched by it.
@@ -35,12 +45,18 @@
 namespace tpk {
 namespace {
 
-constexpr int kThreads = 512;
+constexpr int kUnpackWarps = 4;
+constexpr int kThreads = 256 + 32 * kUnpackWarps + 128;    // softmax, unpacking, one warp that issues (of a warpgroup)
+// Registers: 512 threads are launched with 128 each.  The softmax needs more (128 values of S, which become
+// P), the others give: 256 * 192 + 128 * 88 + 128 * 40 = 512 * 128.
+constexpr int kLaunchRegs = 128, kSoftmaxRegs = 192, kUnpackRegs = 88, kIssueRegs = 40;
+static_assert(256 * kSoftmaxRegs + 32 * kUnpackWarps * kUnpackRegs + 128 * kIssueRegs <= kThreads * kLaunchRegs,
+              "a warpgroup would wait for registers that never come");
 constexpr int kTile = 128;           // tokens of a step, columns of a tile
 constexpr int kCols = 2 * kTile;     // columns of a thread block
 constexpr int kInfo = 4;
 constexpr float kNegInf = -INFINITY;
-constexpr float kGrow = 8.0f;        // log2 by which a maximum may grow before O is rescaled
+constexpr float kMost = 4096.0f;     // sum of a step's 2^(x - m) up to which the old maximum will do (P is 8 times as much at most)
 
 template <int HD>
 struct Cfg {
@@ -52,13 +68,14 @@ struct Cfg {
     static constexpr int S_COL = 0, O_COL = 256;         // TMEM columns: S of the tiles, then O of the tiles
 };
 
-// What the softmax has to know of a step, by quarters of 32 tokens.
-struct StepInfo {
-    float kmul[4];                   // 2^(F - 127) of the keys
-    int vexp[4];                     // F of the values
-    uint32_t nan[4];                 // tokens whose value row stands for NaN
-    uint32_t bad[4];                 // blocks that are not there, as bits of the step's eight
+// What the softmax has to know of a step, by unpacking warp (32 tokens each).
+struct __align__(16) StepInfo {
+    float4 kmul;                     // 2^(F - 127) of the keys
+    int4 vexp;                       // F of the values
+    uint4 nan;                       // tokens whose value row stands for NaN
+    uint4 gone;                      // blocks that are not there, two bits each
 };
+static_assert(kUnpackWarps == 4, "StepInfo has a word for each");
 
 __device__ __forceinline__ float pow2_field(int field) { return __uint_as_float(static_cast<uint32_t>(field) << 23); }
 
@@ -159,7 +176,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_many_kernel(const _
     __shared__ Item s_item;
     __shared__ int64_t s_scan[kThreads / 32];
     __shared__ StepInfo s_info[kInfo];
-    __shared__ __align__(16) uint32_t s_key[kTile];      // fp16 pairs (step, base) of the step's keys
+    // each unpacking warp's own: fp16 pairs (step, base) of its keys, steps and bases of its values
+    __shared__ __align__(16) uint32_t s_key[kTile];
     __shared__ __align__(16) uint16_t s_vstep[kTile], s_vbase[kTile];
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -228,12 +246,12 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_many_kernel(const _
         s_abort = 0;
         mbar_init(smem_u32(&bars.q_full), kCols);
         for (int i = 0; i < 2; ++i) {
-            mbar_init(smem_u32(&bars.k_full[i]), kTile);
+            mbar_init(smem_u32(&bars.k_full[i]), kUnpackWarps);
             mbar_init(smem_u32(&bars.k_empty[i]), 1);
-            mbar_init(smem_u32(&bars.v_full[i]), kTile);
+            mbar_init(smem_u32(&bars.v_full[i]), kUnpackWarps);
             mbar_init(smem_u32(&bars.v_empty[i]), 1);
             mbar_init(smem_u32(&bars.s_full[i]), 1);
-            mbar_init(smem_u32(&bars.p_full[i]), kTile);
+            mbar_init(smem_u32(&bars.p_full[i]), 4);
         }
         mbar_init(smem_u32(&bars.o_full), 1);
     }
@@ -245,7 +263,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_many_kernel(const _
     bool ok = true;
 
     if (warp < 8) {
-        more_registers<192>();
+        more_registers<kSoftmaxRegs>();
         // ------------------------------------------------ softmax: one thread per column
         const int t = warp >> 2;                         // tile
         const int ci = tid;                              // column of the block
@@ -303,59 +321,75 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_many_kernel(const _
             if (!ok) break;
             tc_fence_after();
             const StepInfo& info = s_info[j % kInfo];
-            float c[4];
-            int vexp[4];
-            uint32_t bad = 0, any_nan = 0;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                c[e] = fmaxf(cmul * info.kmul[e], 1e-37f);
-                vexp[e] = info.vexp[e];
-                bad |= info.bad[e];
-                any_nan |= info.nan[e];
-            }
-            uint32_t s[4][32];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) tmem_ld32(s_addr + i * 32, s[i]);
-            tmem_ld_wait();
-            const bool whole = bad == 0 && tok0 + kTile - 1 <= tile_lo &&
+            // the quarters' constants: x = c S, P = 2^(x + d - m), d = F - Fref of the values
+            const float4 km = info.kmul;
+            const int4 ve = info.vexp;
+            const uint4 nn = info.nan, gg = info.gone;
+            const float c[4] = {fmaxf(cmul * km.x, 1e-37f), fmaxf(cmul * km.y, 1e-37f), fmaxf(cmul * km.z, 1e-37f),
+                                fmaxf(cmul * km.w, 1e-37f)};
+            const int vtop = max(max(ve.x, ve.y), max(ve.z, ve.w));
+            const uint32_t gone = gg.x | gg.y << 2 | gg.z << 4 | gg.w << 6;
+            const bool any_nan = (nn.x | nn.y | nn.z | nn.w) != 0;
+            const bool whole = gone == 0 && tok0 + kTile - 1 <= tile_lo &&
                                (a.window == 0 || tok0 > tile_hi - a.window || tok0 + kTile <= a.sinks);
-            if (!whole) {
-                const int lim = max(pos - tok0, -1), low = a.window == 0 ? -(1 << 30) : lim - a.window, sk = a.sinks - tok0;
+            const int lim = max(pos - tok0, -1), low = a.window == 0 ? -(1 << 30) : lim - a.window, sk = a.sinks - tok0;
+            uint32_t s[4][32];
+            auto load = [&]() {                          // S, hidden tokens -inf
 #pragma unroll
-                for (int i = 0; i < 128; ++i) {
-                    const bool see = i <= lim && (i > low || i < sk) && !((bad >> (i >> 4)) & 1u);
-                    if (!see) s[i >> 5][i & 31] = __float_as_uint(kNegInf);
-                }
-            }
-            if (any_nan) {
-                // a column that sees a NaN value row is NaN
-#pragma unroll 1
-                for (int w = 0; w < 4; ++w) {
-                    uint32_t set = info.nan[w];
-                    while (set) {
-                        const int i = w * 32 + __ffs(set) - 1;
-                        set &= set - 1;
-                        const int p = tok0 + i;
-                        if (p <= pos && (a.window == 0 || p > pos - a.window || p < a.sinks)) l = __uint_as_float(0x7fc00000u);
+                for (int i = 0; i < 4; ++i) tmem_ld32(s_addr + i * 32, s[i]);
+                tmem_ld_wait();
+                if (!whole) {
+#pragma unroll
+                    for (int k = 0; k < 128; ++k) {
+                        const bool see = k <= lim && (k > low || k < sk) && !((gone >> (k >> 4)) & 1u);
+                        if (!see) s[k >> 5][k & 31] = __float_as_uint(kNegInf);
                     }
                 }
-            }
-            float mt = kNegInf;
+            };
+            // P into the front of S's registers, and its sum
+            auto powers = [&](float base) {
+                float sum = 0.0f;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                float u = __uint_as_float(s[e][0]), v = __uint_as_float(s[e][1]);
+                for (int e = 0; e < 4; ++e) {
+                    const float dv = static_cast<float>((e == 0 ? ve.x : e == 1 ? ve.y : e == 2 ? ve.z : ve.w) - vref);
+                    const uint64_t cc2 = pack2(c[e], c[e]), off2 = pack2(dv - base, dv - base);
+                    uint64_t sum2 = 0;
 #pragma unroll
-                for (int i = 2; i < 32; i += 4) {
-                    u = fmaxf(fmaxf(u, __uint_as_float(s[e][i])), __uint_as_float(s[e][i + 1]));
-                    if (i + 2 < 32) v = fmaxf(fmaxf(v, __uint_as_float(s[e][i + 2])), __uint_as_float(s[e][i + 3]));
+                    for (int k = 0; k < 32; k += 2) {
+                        float x0, x1;
+                        unpack2(fma2(pack2(__uint_as_float(s[e][k]), __uint_as_float(s[e][k + 1])), cc2, off2), x0, x1);
+                        const float p0 = ex2(x0), p1 = ex2(x1);
+                        sum2 = add2(sum2, pack2(p0, p1));
+                        s[e >> 1][(e & 1) * 16 + k / 2] = pack_f16x2(p0, p1);
+                    }
+                    float a0, a1;
+                    unpack2(sum2, a0, a1);
+                    sum = fmaf(a0 + a1, ex2(-dv), sum);
                 }
-                mt = fmaxf(mt, fmaxf(u, v) * c[e]);
-            }
-            const int vtop = max(max(vexp[0], vexp[1]), max(vexp[2], vexp[3]));
+                return sum;
+            };
             if (j == 0) vref = vtop;
-            const bool grow = mt > m + kGrow || (m == kNegInf && mt > kNegInf);
             const bool vgrow = vtop > vref + 3;
-            if (__any_sync(0xffffffffu, grow) || vgrow) {
+            bool again = have && (vgrow || m == kNegInf);
+            float sum = 0.0f;
+            if (!__any_sync(0xffffffffu, again)) {       // the old maximum may do
+                load();
+                sum = powers(m == kNegInf ? 0.0f : m);
+                again = have && !(sum <= kMost);
+            }
+            if (__any_sync(0xffffffffu, again)) {
+                load();
+                float mt = kNegInf;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    float u = kNegInf, v = kNegInf;
+#pragma unroll
+                    for (int k = 0; k < 32; k += 2) {
+                        u = fmaxf(u, __uint_as_float(s[e][k]));
+                        v = fmaxf(v, __uint_as_float(s[e][k + 1]));
+                    }
+                    mt = fmaxf(mt, fmaxf(u, v) * c[e]);
+                }
                 const float m_new = fmaxf(m, mt);
                 float f = m == kNegInf ? 0.0f : ex2(m - m_new);
                 if (!(m_new > kNegInf)) f = 1.0f;
@@ -365,6 +399,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_many_kernel(const _
                     f *= ex2(static_cast<float>(vref - vtop));
                     vref = vtop;
                 }
+                sum = powers(m == kNegInf ? 0.0f : m);
                 if (j > 0) {                             // P V of the steps before is done: S came after it
 #pragma unroll 1
                     for (int i = 0; i < HD; i += 32) {
@@ -375,36 +410,27 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_many_kernel(const _
                         for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
                         tmem_st32(o_addr + i, o);
                     }
-                    tmem_st_wait();
                 }
             }
-            const float base = m == kNegInf ? 0.0f : m;
-#pragma unroll
-            for (int g = 0; g < 2; ++g) {
-                uint32_t p[32];
-#pragma unroll
-                for (int h2 = 0; h2 < 2; ++h2) {
-                    const int e = 2 * g + h2;
-                    const float dv = static_cast<float>(vexp[e] - vref);
-                    const uint64_t cc2 = pack2(c[e], c[e]), off2 = pack2(dv - base, dv - base);
-                    uint64_t sum2 = 0;
-#pragma unroll
-                    for (int i = 0; i < 32; i += 2) {
-                        float x0, x1;
-                        unpack2(fma2(pack2(__uint_as_float(s[e][i]), __uint_as_float(s[e][i + 1])), cc2, off2), x0, x1);
-                        const float p0 = ex2(x0), p1 = ex2(x1);
-                        sum2 = add2(sum2, pack2(p0, p1));
-                        p[h2 * 16 + i / 2] = pack_f16x2(p0, p1);
+            l += sum;
+            if (any_nan) {
+                // a column that sees a NaN value row is NaN
+#pragma unroll 1
+                for (int e = 0; e < 4; ++e) {
+                    uint32_t set = e == 0 ? nn.x : e == 1 ? nn.y : e == 2 ? nn.z : nn.w;
+                    while (set) {
+                        const int k = e * 32 + __ffs(set) - 1;
+                        set &= set - 1;
+                        if (k <= lim && (k > low || k < sk)) l = __uint_as_float(0x7fc00000u);
                     }
-                    float a0, a1;
-                    unpack2(sum2, a0, a1);
-                    l = fmaf(a0 + a1, ex2(-dv), l);
                 }
-                tmem_st32(s_addr + g * 32, p);
             }
+            tmem_st32(s_addr, s[0]);
+            tmem_st32(s_addr + 32, s[1]);
             tmem_st_wait();
             tc_fence_before();
-            mbar_arrive(smem_u32(&bars.p_full[t]));
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&bars.p_full[t]));
         }
         // ---- the result
         float scale = 0.0f;
@@ -437,8 +463,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_many_kernel(const _
                 }
             }
         }
-    } else if (warp < 12) {
-        fewer_registers<88>();
+    } else if (warp < 8 + kUnpackWarps) {
+        if constexpr (kUnpackRegs > kLaunchRegs) more_registers<kUnpackRegs>(); else fewer_registers<kUnpackRegs>();
         // ------------------------------------------------ codes to operands
         const int id = tid - 256, w = warp - 8;
         const int32_t* row = a.seqs.table + it.seq * a.seqs.max_blocks;
@@ -525,10 +551,11 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_many_kernel(const _
                 s_vbase[id] = static_cast<uint16_t>(pack_f16x2(vb, 0.0f));
                 if (lane == 0) {
                     StepInfo& info = s_info[j % kInfo];
-                    info.kmul[w] = pow2_field(kF);
-                    info.vexp[w] = vF;
-                    info.nan[w] = nan_set;
-                    info.bad[w] = (~there & 3u) << (2 * w);      // past the last visible token too: no matter
+                    reinterpret_cast<float*>(&info.kmul)[w] = pow2_field(kF);
+                    reinterpret_cast<int*>(&info.vexp)[w] = vF;
+                    reinterpret_cast<uint32_t*>(&info.nan)[w] = nan_set;
+                    // past the last visible token nothing is there: hidden by position, no matter
+                    reinterpret_cast<uint32_t*>(&info.gone)[w] = ~there & 3u;
                 }
             }
             __syncwarp();
@@ -558,7 +585,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_many_kernel(const _
                 }
             }
             fence_proxy_async_cta();
-            mbar_arrive(smem_u32(&bars.k_full[st]));
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&bars.k_full[st]));
             fetch_keys(off);
 
             if (j >= 2) ok = mbar_wait_warp(smem_u32(&bars.v_empty[st]), ((j >> 1) + 1) & 1, &s_abort, a.seqs.status);
@@ -596,12 +624,13 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_many_kernel(const _
                     }
             }
             fence_proxy_async_cta();
-            mbar_arrive(smem_u32(&bars.v_full[st]));
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&bars.v_full[st]));
             fetch_values(off);
         }
     } else {
-        fewer_registers<40>();
-        if (warp == 12 && steps > 0) {
+        fewer_registers<kIssueRegs>();
+        if (warp == 8 + kUnpackWarps && steps > 0) {
             // ------------------------------------------------ the products
             constexpr uint32_t QK = idesc_f16(128, 128), PV = idesc_f16(128, HD);
             auto wait = [&](uint64_t& b, int parity) {
