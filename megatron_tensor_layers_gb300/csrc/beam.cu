@@ -1,16 +1,18 @@
 // Beam selection over vocab-sharded logits: one pass over the logits, bound by
 // reading them.
 //
-// First kernel, one thread block per (row, slice of a shard): the slice stays in
-// registers; its maximum and the sum of exponentials under it (each term fp32,
-// the terms of a thread added in fp32, the threads in fp64), and its k best
-// logits.  A logit and its token make one 64-bit key, larger for a larger logit
-// and, among equals, for a lower token, so the k best are unique.  The k-th
-// largest of 64 group maxima (a group is 4 threads) is a lower bound of the k-th
-// largest of the slice; what is not below it, a few more than k elements, goes
-// to shared memory and is ranked by counting.  Where more than kRoom elements
-// are not below the bound (many equal logits), k rounds of a block-wide
-// maximum find them instead.
+// First kernel, one thread block per (row, slice of a shard), which walks its
+// slice 4096 logits at a time, the next ones already on their way.  Each thread
+// keeps a running maximum and the sum of exponentials under it (fp32; the
+// threads' sums are added in fp64).  A logit and its token make one 64-bit key,
+// larger for a larger logit and, among equals, for a lower token, so the k best
+// are unique.  The k-th largest of 64 group maxima (a group is 4 threads) of the
+// first 4096 is a lower bound of the k-th largest of the slice; what is not
+// below it goes to shared memory, a few logits in a hundred threads' worth, so
+// the pass costs one comparison per thread and 16 logits.  When the room fills
+// up, the k best are found by counting and the bound rises to the last of them.
+// Where more than kRoom at once are not below the bound (many equal logits), k
+// rounds of a block-wide maximum over the slice find them instead.
 //
 // Second kernel, one thread block per item: the log-sum-exp of each beam from
 // its slices, then the k best of all beams' candidates by the fp64 sum
@@ -38,7 +40,7 @@ struct BeamArgs {
     const void* logits[TP_MAX_SHARDS];
     int64_t cols[TP_MAX_SHARDS], ldl[TP_MAX_SHARDS], start[TP_MAX_SHARDS];
     int first_slice[TP_MAX_SHARDS + 1];  // slices of a row, by shard
-    int t, items, beams, k, slices;
+    int t, items, beams, k, slices, chunks;
     int64_t vocab;
     const float* scores;
     const uint8_t* finished;
@@ -105,14 +107,23 @@ __device__ __forceinline__ uint64_t block_max64(uint64_t v, uint64_t* tmp, int t
     return v;
 }
 
-// EPT elements per thread, VEC of them per 16-byte load.
-template <int EPT, bool F32>
+constexpr int kChunk = 16;           // logits of a thread in one go
+constexpr float kLog2e = 1.4426950408889634f;
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+template <bool F32>
 __global__ void __launch_bounds__(kThreads) beam_slice_kernel(const __grid_constant__ BeamArgs a) {
-    constexpr int VEC = F32 ? 4 : 8, NV = EPT / VEC;
+    constexpr int VEC = F32 ? 4 : 8, NV = kChunk / VEC, ES = F32 ? 4 : 2;
+    constexpr uint32_t NONE = F32 ? 0xff800000u : 0xff80ff80u;           // -inf
     __shared__ float s_top[kWarps];
     __shared__ double s_sum[kWarps];
     __shared__ uint32_t s_group[kGroups];
-    __shared__ uint64_t s_cand[kRoom];
+    __shared__ uint64_t s_cand[kRoom], s_best[TP_MAX_BEAMS];
     __shared__ uint64_t s_tmp[kWarps];
     __shared__ int s_count;
     pdl_wait();
@@ -123,113 +134,158 @@ __global__ void __launch_bounds__(kThreads) beam_slice_kernel(const __grid_const
     int r = 0;
     while (slice >= a.first_slice[r + 1]) ++r;
     const int64_t cols = a.cols[r];
-    constexpr int ES = F32 ? 4 : 2;
     const uint8_t* base = static_cast<const uint8_t*>(a.logits[r]) + row * a.ldl[r] * ES;
     // 16-byte words counted from the one that holds the row's first element
     const int off = static_cast<int>((reinterpret_cast<uintptr_t>(base) & 15u) / ES);
-    const int64_t word0 = static_cast<int64_t>(slice - a.first_slice[r]) * (kThreads * NV);
-    float x[EPT];
+    const int64_t word0 = static_cast<int64_t>(slice - a.first_slice[r]) * a.chunks * (kThreads * NV);
+    const int64_t words = (off + cols + VEC - 1) / VEC - word0;  // of the row from this slice on
+    const int chunks = static_cast<int>(min(static_cast<int64_t>(a.chunks), (words + kThreads * NV - 1) / (kThreads * NV)));
+    // column of the first element of this thread's word j of a chunk
+    auto column = [&](int chunk, int j) { return (word0 + static_cast<int64_t>(chunk * NV + j) * kThreads + tid) * VEC - off; };
+    auto load = [&](int chunk, uint4 (&w)[NV]) {
 #pragma unroll
-    for (int j = 0; j < NV; ++j) {
-        const int64_t c = (word0 + j * kThreads + tid) * VEC - off;      // column of the word's first element
-        if (c >= 0 && c + VEC <= cols) {
-            const uint4 v = __ldg(reinterpret_cast<const uint4*>(base + c * ES));
-            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+        for (int j = 0; j < NV; ++j) {
+            const int64_t c = column(chunk, j);
+            if (c >= 0 && c + VEC <= cols) {
+                w[j] = __ldg(reinterpret_cast<const uint4*>(base + c * ES));
+            } else {                             // a word that the row's edge cuts, or one outside
+                uint32_t v[4] = {NONE, NONE, NONE, NONE};
+#pragma unroll
+                for (int e = 0; e < VEC; ++e)
+                    if (c + e >= 0 && c + e < cols) {
+                        if constexpr (F32) {
+                            v[e] = reinterpret_cast<const uint32_t*>(base)[c + e];
+                        } else {
+                            const uint32_t h = reinterpret_cast<const uint16_t*>(base)[c + e];
+                            v[e / 2] = e & 1 ? (v[e / 2] & 0xffffu) | h << 16 : (v[e / 2] & 0xffff0000u) | h;
+                        }
+                    }
+                w[j] = make_uint4(v[0], v[1], v[2], v[3]);
+            }
+        }
+    };
+    auto values = [&](const uint4 (&w)[NV], float (&x)[kChunk]) {
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            const uint32_t v[4] = {w[j].x, w[j].y, w[j].z, w[j].w};
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 if constexpr (F32) {
-                    x[j * VEC + e] = __uint_as_float(w[e]);
+                    x[j * 4 + e] = __uint_as_float(v[e]);
                 } else {
-                    x[j * VEC + 2 * e] = __uint_as_float(w[e] << 16);
-                    x[j * VEC + 2 * e + 1] = __uint_as_float(w[e] & 0xffff0000u);
+                    x[j * 8 + 2 * e] = __uint_as_float(v[e] << 16);
+                    x[j * 8 + 2 * e + 1] = __uint_as_float(v[e] & 0xffff0000u);
                 }
-            }
-        } else {
-#pragma unroll
-            for (int e = 0; e < VEC; ++e) {
-                float v = -INFINITY;
-                if (c + e >= 0 && c + e < cols) {
-                    if constexpr (F32)
-                        v = reinterpret_cast<const float*>(base)[c + e];
-                    else
-                        v = bf16_to_f32(reinterpret_cast<const uint16_t*>(base)[c + e]);
-                }
-                x[j * VEC + e] = v;
             }
         }
-    }
-    float best = -INFINITY;
-#pragma unroll
-    for (int i = 0; i < EPT; ++i) best = fmaxf(best, x[i]);
-    float top = best;
-#pragma unroll
-    for (int m = 16; m >= 1; m >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, m));
-    if (lane == 0) s_top[warp] = top;
-    group_max(best == -INFINITY ? 0u : ordered(best), s_group, tid);
+    };
+    auto key = [&](int chunk, int i, float x) {
+        return (static_cast<uint64_t>(ordered(x)) << 32) |
+               (0xffffffffu - static_cast<uint32_t>(a.start[r] + column(chunk, i / VEC) + i % VEC));
+    };
+    // the k best of the candidates, in order, into s_best (0 where there are fewer)
+    auto rank = [&](int count) {
+        for (int i = tid; i < count; i += kThreads) {
+            const uint64_t mine = s_cand[i];
+            int before = 0;
+            for (int j = 0; j < count; ++j) before += s_cand[j] > mine;
+            if (before < a.k) s_best[before] = mine;
+        }
+        for (int i = count + tid; i < a.k; i += kThreads) s_best[i] = 0;
+        __syncthreads();
+    };
     if (tid == 0) s_count = 0;
+    uint4 next[NV];
+    load(0, next);
+    float m = -INFINITY, s = 0.0f;
+    float bound = -INFINITY;
+    bool over = false;
+    for (int c = 0; c < chunks; ++c) {
+        float x[kChunk];
+        values(next, x);
+        if (c + 1 < chunks) load(c + 1, next);
+        float best = x[0];
+#pragma unroll
+        for (int i = 1; i < kChunk; ++i) best = fmaxf(best, x[i]);
+        const float m_new = fmaxf(m, best), b = m_new == -INFINITY ? 0.0f : m_new;
+        s *= ex2((m - b) * kLog2e);
+        m = m_new;
+#pragma unroll
+        for (int i = 0; i < kChunk; ++i) s += ex2((x[i] - b) * kLog2e);  // NaN and +inf make it NaN
+        if (c == 0) {
+            group_max(best > -INFINITY ? ordered(best) : 0u, s_group, tid);
+            __syncthreads();
+            const uint32_t o = kth_of_groups(s_group, a.k, lane);
+            bound = o == 0 ? -INFINITY : unordered(o);
+        }
+        if (best >= bound) {
+#pragma unroll
+            for (int i = 0; i < kChunk; ++i)
+                if (x[i] >= bound && x[i] > -INFINITY) {
+                    const int at = atomicAdd(&s_count, 1);
+                    if (at < kRoom) s_cand[at] = key(c, i, x[i]);
+                }
+        }
+        __syncthreads();
+        const int count = s_count;
+        __syncthreads();                         // nobody adds before everybody has read
+        over = count > kRoom;
+        if (over) {                              // the sum goes on, the candidates are found below
+            bound = INFINITY;
+            if (tid == 0) s_count = kRoom + 1;
+        } else if (count > kRoom / 2 && c + 1 < chunks) {
+            rank(count);
+            if (tid < a.k) s_cand[tid] = s_best[tid];
+            bound = unordered(static_cast<uint32_t>(s_best[a.k - 1] >> 32));
+            if (tid == 0) s_count = a.k;
+            __syncthreads();
+        }
+    }
+    // the slice's maximum and sum
+    float top = m;
+#pragma unroll
+    for (int i = 16; i >= 1; i >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, i));
+    if (lane == 0) s_top[warp] = top;
     __syncthreads();
     top = s_top[0];
 #pragma unroll
     for (int i = 1; i < kWarps; ++i) top = fmaxf(top, s_top[i]);
-    float part = 0.0f;
-    if (top > -INFINITY) {
+    double sum = static_cast<double>(s * ex2((m - (top == -INFINITY ? 0.0f : top)) * kLog2e));
 #pragma unroll
-        for (int i = 0; i < EPT; ++i) part += expf(x[i] - top);          // NaN and +inf make it NaN
-    } else {
-#pragma unroll
-        for (int i = 0; i < EPT; ++i) part += x[i] == x[i] ? 0.0f : x[i];
-    }
-    double sum = part;
-#pragma unroll
-    for (int m = 16; m >= 1; m >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, m);
+    for (int i = 16; i >= 1; i >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, i);
     if (lane == 0) s_sum[warp] = sum;
-
-    const uint32_t bound = max(kth_of_groups(s_group, a.k, lane), 1u);
-    auto key = [&](int i) {
-        const int64_t c = (word0 + (i / VEC) * kThreads + tid) * VEC - off + i % VEC;
-        return (static_cast<uint64_t>(ordered(x[i])) << 32) | (0xffffffffu - static_cast<uint32_t>(a.start[r] + c));
-    };
-    if (best > -INFINITY && ordered(best) >= bound) {
-#pragma unroll
-        for (int i = 0; i < EPT; ++i)
-            if (x[i] > -INFINITY && ordered(x[i]) >= bound) {
-                const int at = atomicAdd(&s_count, 1);
-                if (at < kRoom) s_cand[at] = key(i);
-            }
-    }
-    __syncthreads();
     const int64_t out = static_cast<int64_t>(row) * a.slices + slice;
-    if (tid == 0) {
-        Slice s;
-        s.top = top;
-        s.pad = 0;
-        s.sum = 0.0;
-        for (int i = 0; i < kWarps; ++i) s.sum += s_sum[i];
-        a.stats[out] = s;
-    }
     uint64_t* keys = a.keys + out * a.k;
-    const int count = s_count;
-    if (count <= kRoom) {
-        for (int i = tid; i < count; i += kThreads) {
-            const uint64_t mine = s_cand[i];
-            int rank = 0;
-            for (int j = 0; j < count; ++j) rank += s_cand[j] > mine;
-            if (rank < a.k) keys[rank] = mine;
-        }
-        for (int i = count + tid; i < a.k; i += kThreads) keys[i] = 0;
+    if (!over) {
+        rank(s_count);
+        if (tid < a.k) keys[tid] = s_best[tid];
     } else {
         uint64_t last = ~0ull;
         for (int n = 0; n < a.k; ++n) {
             uint64_t mine = 0;
+            for (int c = 0; c < chunks; ++c) {
+                uint4 w[NV];
+                float x[kChunk];
+                load(c, w);
+                values(w, x);
 #pragma unroll
-            for (int i = 0; i < EPT; ++i)
-                if (x[i] > -INFINITY) {
-                    const uint64_t v = key(i);
-                    if (v < last && v > mine) mine = v;
-                }
+                for (int i = 0; i < kChunk; ++i)
+                    if (x[i] > -INFINITY) {
+                        const uint64_t v = key(c, i, x[i]);
+                        if (v < last && v > mine) mine = v;
+                    }
+            }
             last = block_max64(mine, s_tmp, tid);
             if (tid == 0) keys[n] = last;
         }
+    }
+    if (tid == 0) {
+        Slice st;
+        st.top = top;
+        st.pad = 0;
+        st.sum = 0.0;
+        for (int i = 0; i < kWarps; ++i) st.sum += s_sum[i];
+        a.stats[out] = st;
     }
 }
 
@@ -358,25 +414,27 @@ __global__ void __launch_bounds__(kThreads) beam_pick_kernel(const __grid_consta
     }
 }
 
-// Elements per thread of a slice: 32, or fewer while the slices would not fill the GPU twice.
-int pick_ept(int64_t rows, int64_t vocab, int sms) {
-    for (int e = 32; e > 8; e >>= 1)
-        if (rows * ((vocab + kThreads * e - 1) / (kThreads * e)) >= 2 * sms) return e;
-    return 8;
+constexpr int kChunkLogits = kThreads * kChunk;
+
+// Chunks of a slice: as many as leave six blocks for each SM (the registers allow five to run at once),
+// at most 16.
+int pick_chunks(int64_t rows, int64_t vocab, int sms) {
+    const int64_t all = rows * ((vocab + kChunkLogits - 1) / kChunkLogits);
+    return static_cast<int>(std::min<int64_t>(16, std::max<int64_t>(1, all / (6 * sms))));
 }
 
 // Slices of a shard: its 16-byte words, one more for a row that begins inside a word.
-int64_t slices_of(int64_t cols, int vec, int ept) {
+int64_t slices_of(int64_t cols, int vec, int chunks) {
     if (cols == 0) return 0;
-    const int64_t words = (cols + 2 * vec - 2) / vec, per = static_cast<int64_t>(kThreads) * (ept / vec);
+    const int64_t words = (cols + 2 * vec - 2) / vec, per = static_cast<int64_t>(kChunkLogits / vec) * chunks;
     return (words + per - 1) / per;
 }
 
 }  // namespace
 
 size_t beam_workspace(int64_t items, int beams, int k, int64_t vocab) {
-    // the most slices any cut of the vocabulary gives (8 elements per thread, 8 shards)
-    const int64_t slices = (vocab + kThreads * 8 - 1) / (kThreads * 8) + 2 * TP_MAX_SHARDS;
+    // the most slices any cut of the vocabulary gives
+    const int64_t slices = (vocab + kChunkLogits - 1) / kChunkLogits + 2 * TP_MAX_SHARDS;
     const int64_t rows = items * beams;
     return static_cast<size_t>(rows) * slices * (sizeof(Slice) + static_cast<size_t>(k) * 8);
 }
@@ -394,11 +452,11 @@ tp_status launch_beam_select(const BeamDesc& d, cudaStream_t stream) {
     }
     const int sms = device_sms();
     if (sms <= 0) return TP_ERR_CUDA;
-    const int ept = pick_ept(rows, vocab, sms);
+    a.chunks = pick_chunks(rows, vocab, sms);
     int64_t slices = 0;
     for (int r = 0; r < TP_MAX_SHARDS; ++r) {
         a.first_slice[r] = static_cast<int>(slices);
-        if (r < d.t) slices += slices_of(d.cols[r], d.f32 ? 4 : 8, ept);
+        if (r < d.t) slices += slices_of(d.cols[r], d.f32 ? 4 : 8, a.chunks);
     }
     a.first_slice[TP_MAX_SHARDS] = static_cast<int>(slices);
     a.t = d.t;
@@ -417,15 +475,8 @@ tp_status launch_beam_select(const BeamDesc& d, cudaStream_t stream) {
     a.keys = reinterpret_cast<uint64_t*>(a.stats + rows * slices);
     if (slices * rows > INT32_MAX) return TP_ERR_UNSUPPORTED;
     const dim3 grid(static_cast<unsigned>(slices * rows)), block(kThreads);
-    cudaError_t e;
-    if (d.f32)
-        e = ept == 32   ? launch_pdl(beam_slice_kernel<32, true>, grid, block, 0, stream, a)
-            : ept == 16 ? launch_pdl(beam_slice_kernel<16, true>, grid, block, 0, stream, a)
-                        : launch_pdl(beam_slice_kernel<8, true>, grid, block, 0, stream, a);
-    else
-        e = ept == 32   ? launch_pdl(beam_slice_kernel<32, false>, grid, block, 0, stream, a)
-            : ept == 16 ? launch_pdl(beam_slice_kernel<16, false>, grid, block, 0, stream, a)
-                        : launch_pdl(beam_slice_kernel<8, false>, grid, block, 0, stream, a);
+    const cudaError_t e = d.f32 ? launch_pdl(beam_slice_kernel<true>, grid, block, 0, stream, a)
+                                : launch_pdl(beam_slice_kernel<false>, grid, block, 0, stream, a);
     if (e != cudaSuccess) return TP_ERR_CUDA;
     return launch_pdl(beam_pick_kernel, dim3(d.items), block, 0, stream, a) == cudaSuccess ? TP_OK : TP_ERR_CUDA;
 }
