@@ -17,6 +17,11 @@
 // that.  p s' is scaled by 2^(13 - E), E the exponent of the largest step seen,
 // and rounded to fp16 (2^-11 relative): the one rounding of the products.
 //
+// What is subtracted, m, is a column's maximum as of the last time it was
+// needed: a stage first takes p under the old m, and only when a sum exceeds 2^7
+// (so that p s' could leave fp16), a larger step turns up, or a column has seen
+// nothing yet, are the maxima taken across the warp and everything rescaled.
+//
 // Split.  The unit of work is a cache block (16 tokens).  All blocks of all
 // (sequence, row tile, head) items form one line, cut into equal parts, one for
 // each worker of WS warps (8, or fewer when items are short, so that a worker
@@ -26,12 +31,15 @@
 // in order.  The cut depends on lengths the host does not know, so every thread
 // block finds its own.
 //
-// Each warp feeds itself: a ring of 2 stages of 4 blocks, filled by bulk copies
-// (a block is one contiguous record) and read as mma.sync fragments without
-// conflicts: the transposed products K q^T and V^T p^T have the tokens and the
-// head dimension as their 16 rows and only 8 columns, so 8 query heads of a
-// group fill them.  tcgen05 would want 128 rows of them.
+// Each warp feeds itself: a ring of 2 stages of 4 blocks (2 with 16 columns),
+// filled by bulk copies (a block is one contiguous record) and read as mma.sync
+// fragments without conflicts: the transposed products K q^T and V^T p^T have
+// the tokens and the head dimension as their 16 rows and only 8 columns, so 8
+// query heads of a group fill them.  tcgen05 would want 128 rows of them.  With
+// two warps on a scheduler it is the independent work within a warp that hides
+// latencies: the blocks of a full, fully visible stage run as one straight line.
 #include <algorithm>
+#include <type_traits>
 
 #include "attention_args.cuh"
 
@@ -39,28 +47,30 @@ namespace tpk {
 namespace {
 
 constexpr int kWarps = 8;
-constexpr int kStageBlocks = 4;
+constexpr int kBatch = 32;           // blocks whose addresses a warp holds, one in each lane
 constexpr int kStages = 2;
-constexpr int kPShift = 13;          // p s' is held times 2^(kPShift - E)
+constexpr int kPShift = 8;           // p s' is held times 2^(kPShift - E)
+constexpr float kMost = 128.0f;      // sum of a lane's 2^(x - m) up to which the old maximum will do
 constexpr int kMany = 64;            // columns from which a sequence's rows go to the many-rows kernel
 constexpr float kNegInf = -INFINITY;
 
 // Head of the workspace: what the second kernel needs to know of the cut.
 struct Cut {
-    int64_t total;                   // units of all items
-    int workers, ws;                 // parts, warps of a worker
+    int workers;                     // parts
 };
-// A worker whose range begins inside an item describes it.
+// A worker whose range begins inside an item describes it, and which workers hold the rest.
 struct Split {
-    int64_t begin;                   // first unit of the item on the line
     int units;                       // of the item; 0: the worker begins with an item's first unit
+    int from, to;                    // the workers that hold parts of it
+    int from_slot;                   // which of the first one's two parts is the item's
     int first_row, rows, tile, head;
-    int pad;
 };
 
 constexpr size_t kSplitAt = 256;
 
-__host__ __device__ constexpr size_t slot_floats(int cols, int hd) { return static_cast<size_t>(cols) * (hd + 2); }
+// A part of an item: for each (16-row tile of dimensions, column tile) 32 lanes' four accumulators, then
+// 32 lanes' maxima and sums of two columns.
+__host__ __device__ constexpr int slot_vectors(int nt, int hd) { return nt * (hd / 16 + 1) * 32; }
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                         uint32_t b1) {
@@ -144,10 +154,10 @@ __device__ __forceinline__ int worker_of(int64_t total, int workers, int64_t u) 
 
 // A position on the line of units, walked item by item.
 struct Cursor {
-    int64_t left;                    // units of the worker's range from here on
+    int left;                        // units of the worker's range from here on
     int s, tile, head, off;          // current item and the unit in it
     Need n;
-    __device__ __forceinline__ int count() const { return static_cast<int>(min(static_cast<int64_t>(n.units - off), left)); }
+    __device__ __forceinline__ int count() const { return min(n.units - off, left); }
     __device__ __forceinline__ void next(const AttnArgs& a, int cols_per_tile, int heads) {
         const int c = count();
         left -= c;
@@ -172,24 +182,66 @@ struct Cursor {
 template <int HD, int NT>
 struct Cfg {
     static constexpr int COLS = 8 * NT;
+    static constexpr int WARPS = kWarps;
     static constexpr int MT = HD / 16;                       // 16-row tiles of the output's dimensions
-    static constexpr int STAGE = kStageBlocks * KvBlock<HD>::BYTES;
-    static constexpr int RING = kWarps * kStages * STAGE;
-    static constexpr int MERGE = (MT * 4 + 4) * NT * 32 * 4;  // accumulators, maxima and sums of one warp
-    static constexpr int SMEM = RING + kWarps / 2 * MERGE;
+    static constexpr int BLOCKS = 4 / NT;                    // of a stage
+    static constexpr int STAGE = BLOCKS * KvBlock<HD>::BYTES;
+    static constexpr int RING = WARPS * kStages * STAGE;
+    static constexpr int PART = slot_vectors(NT, HD);        // of a warp, in float4
+    static constexpr int SMEM = RING + WARPS * PART * 16;
 };
 
+// The sum, in order, of `count` parts at part(i), for vector v of the result (see slot_vectors):
+// four accumulators already divided by the sum.
+template <int HD, int NT, typename Part>
+__device__ __forceinline__ float4 join_parts(int v, int count, Part part, float2& top, float2& total) {
+    constexpr int MT = HD / 16;
+    const int nt = v / (MT * 32), stats = nt * 32 + v % 32;
+    top = make_float2(kNegInf, kNegInf);
+    total = make_float2(0.0f, 0.0f);
+    float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 8
+    for (int i = 0; i < count; ++i) {
+        const float4 st = part(i)[NT * MT * 32 + stats], x = part(i)[v];
+        const float2 m = make_float2(fmaxf(top.x, st.x), fmaxf(top.y, st.y));
+        const float2 b = make_float2(m.x == kNegInf ? 0.0f : m.x, m.y == kNegInf ? 0.0f : m.y);
+        const float2 fa = make_float2(ex2(top.x - b.x), ex2(top.y - b.y)), fb = make_float2(ex2(st.x - b.x), ex2(st.y - b.y));
+        top = m;
+        total = make_float2(total.x * fa.x + st.z * fb.x, total.y * fa.y + st.w * fb.y);
+        o = make_float4(o.x * fa.x + x.x * fb.x, o.y * fa.y + x.y * fb.y, o.z * fa.x + x.z * fb.x, o.w * fa.y + x.w * fb.y);
+    }
+    return o;
+}
+
+// Vector v of an item's result to the output: two dimensions of two columns.
 template <int HD, int NT>
-__global__ void __launch_bounds__(kWarps * 32, 1) kv4_attention_kernel(const __grid_constant__ AttnArgs a) {
+__device__ __forceinline__ void store_vector(const AttnArgs& a, int head, int first_row, int cols, int tile, int v,
+                                             const float4& o, const float2& total) {
+    constexpr int MT = HD / 16, COLS = 8 * NT;
+    const int lane = v % 32, i = v / 32 % MT, nt = v / (MT * 32);
+    const int rank = head / a.pools.kv_heads, kvh = head - rank * a.pools.kv_heads;
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+        const int ci = nt * 8 + 2 * (lane & 3) + e;
+        if (ci >= cols) continue;
+        const float sum = e ? total.y : total.x, inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+        const int cc = tile * COLS + ci;
+        const int r = cc / a.group, h = cc - r * a.group;
+        *reinterpret_cast<uint32_t*>(a.out[rank] + (first_row + r) * a.ldo + (kvh * a.group + h) * HD + (lane >> 2) * (HD / 8) +
+                                     2 * i) = pack_bf16x2((e ? o.y : o.x) * inv, (e ? o.w : o.z) * inv);
+    }
+}
+
+template <int HD, int NT>
+__global__ void __launch_bounds__(Cfg<HD, NT>::WARPS * 32, 1) kv4_attention_kernel(const __grid_constant__ AttnArgs a) {
     using B = KvBlock<HD>;
     using C = Cfg<HD, NT>;
-    constexpr int MT = C::MT, COLS = C::COLS;
+    constexpr int MT = C::MT, COLS = C::COLS, WARPS = C::WARPS, THREADS = WARPS * 32;
     extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ __align__(8) uint64_t bars[kWarps * kStages];
-    __shared__ int stage_mask[kWarps * kStages];
-    __shared__ int64_t scan[kWarps];
-    __shared__ int64_t s_items;
-    __shared__ Cursor s_cursor[kWarps];
+    __shared__ __align__(8) uint64_t bars[WARPS * kStages];
+    __shared__ int stage_mask[WARPS * kStages];
+    __shared__ int64_t scan[WARPS], scan_items[WARPS];
+    __shared__ Cursor s_cursor[WARPS];
     __shared__ int s_abort;
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -205,7 +257,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) kv4_attention_kernel(const __g
 
     // ---- the cut: total units, items, then where each of this block's workers begins
     int64_t mine = 0, items = 0;
-    const int per = (a.seqs.nseq + kWarps * 32 - 1) / (kWarps * 32);
+    const int per = (a.seqs.nseq + THREADS - 1) / THREADS;
     for (int s = tid * per; s < min(a.seqs.nseq, (tid + 1) * per); ++s) {
         const Need n = seq_need(a, s, COLS);
         mine += static_cast<int64_t>(n.units) * n.tiles * heads;
@@ -218,28 +270,28 @@ __global__ void __launch_bounds__(kWarps * 32, 1) kv4_attention_kernel(const __g
         if (lane >= m) before += v;
         items += __shfl_xor_sync(0xffffffffu, items, m);
     }
-    if (tid == 0) s_items = 0;
-    if (lane == 31) scan[warp] = before;
+    if (lane == 31) scan[warp] = before, scan_items[warp] = items;
     __syncthreads();
-    if (lane == 0 && items != 0) atomicAdd(reinterpret_cast<unsigned long long*>(&s_items), static_cast<unsigned long long>(items));
-    int64_t total = 0, base = 0;
-    for (int i = 0; i < kWarps; ++i) {
+    int64_t total = 0, base = 0, all_items = 0;
+#pragma unroll
+    for (int i = 0; i < WARPS; ++i) {
         if (i < warp) base += scan[i];
         total += scan[i];
+        all_items += scan_items[i];
     }
     before += base - mine;           // units before this thread's sequences
-    __syncthreads();
     if (total == 0) {
-        if (blockIdx.x == 0 && tid == 0) *reinterpret_cast<Cut*>(a.ws) = Cut{0, 0, 0};
+        if (blockIdx.x == 0 && tid == 0) *reinterpret_cast<Cut*>(a.ws) = Cut{0};
         return;
     }
-    // Warps of a worker: 8 while the average item has at least 32 blocks (4 for each warp, one
-    // stage), fewer below.  At least 4 blocks for each warp where there are few units in all.
-    int ws = kWarps;
-    while (ws > 1 && total < static_cast<int64_t>(4 * ws) * s_items) ws >>= 1;
-    const int groups = kWarps / ws;
-    const int workers = static_cast<int>(
-        max(static_cast<int64_t>(1), min(static_cast<int64_t>(gridDim.x) * groups, (total + 4 * ws - 1) / (4 * ws))));
+    // Warps of a worker: all while the average item has a stage for each, fewer below.  At least a
+    // stage for each warp, too, where there are few units in all: fewer parts to join.
+    int ws = WARPS;
+    while (ws > 1 && total < static_cast<int64_t>(C::BLOCKS * ws) * all_items) ws >>= 1;
+    const int groups = WARPS / ws;
+    const int64_t least = C::BLOCKS * ws;
+    const int workers =
+        static_cast<int>(max(static_cast<int64_t>(1), min(static_cast<int64_t>(gridDim.x) * groups, (total + least - 1) / least)));
     for (int i = 0; i < groups; ++i) {
         const int w = i * gridDim.x + blockIdx.x;
         const int64_t begin = w < workers ? part_begin(total, workers, w) : total;
@@ -258,7 +310,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) kv4_attention_kernel(const __g
                 ++s;
             }
             Cursor c;
-            c.left = end - begin;
+            c.left = static_cast<int>(end - begin);
             c.s = s;
             c.n = seq_need(a, s, COLS);
             const int item = static_cast<int>(u / c.n.units);
@@ -266,68 +318,99 @@ __global__ void __launch_bounds__(kWarps * 32, 1) kv4_attention_kernel(const __g
             c.tile = item / heads;
             c.head = item - c.tile * heads;
             s_cursor[i] = c;
-            Split sp;
-            sp.begin = begin - c.off;
-            sp.units = c.off > 0 ? c.n.units : 0;
-            sp.first_row = c.n.first_row;
-            sp.rows = c.n.rows;
-            sp.tile = c.tile;
-            sp.head = c.head;
-            sp.pad = 0;
+            Split sp = {};
+            if (c.off > 0) {
+                const int64_t first = begin - c.off;
+                sp.units = c.n.units;
+                sp.from = worker_of(total, workers, first);
+                sp.to = worker_of(total, workers, first + c.n.units - 1);
+                sp.from_slot = part_begin(total, workers, sp.from) == first ? 0 : 1;
+                sp.first_row = c.n.first_row;
+                sp.rows = c.n.rows;
+                sp.tile = c.tile;
+                sp.head = c.head;
+            }
             reinterpret_cast<Split*>(a.ws + kSplitAt)[w] = sp;
         }
     }
-    if (blockIdx.x == 0 && tid == 0) {
-        Cut cut;
-        cut.total = total;
-        cut.workers = workers;
-        cut.ws = ws;
-        *reinterpret_cast<Cut*>(a.ws) = cut;
-    }
+    if (blockIdx.x == 0 && tid == 0) *reinterpret_cast<Cut*>(a.ws) = Cut{workers};
     __syncthreads();
 
     const int grp = warp / ws, wi = warp % ws;
     const int worker = grp * gridDim.x + blockIdx.x;
-    float* slots = reinterpret_cast<float*>(a.ws + kSplitAt + static_cast<size_t>(gridDim.x) * kWarps * sizeof(Split));
+    float4* slots = reinterpret_cast<float4*>(a.ws + kSplitAt + static_cast<size_t>(gridDim.x) * kWarps * sizeof(Split));
 
     Cursor cur = s_cursor[grp];      // the item being computed
     if (cur.left <= 0) return;       // the whole worker
     Cursor ahead = cur;              // the item being loaded
     bool first_segment = true;
 
+    // ---- q of an item: a lane holds a quarter of the dimensions of one column of each column tile
+    constexpr int D = HD / 4;
+    uint32_t raw[NT][D / 2];
+    auto fetch_q = [&](const Cursor& c) {
+        const int rank = c.head / a.pools.kv_heads, kvh = c.head - rank * a.pools.kv_heads;
+        const int cols = c.n.rows * a.group - c.tile * COLS;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            const int ci = nt * 8 + g;
+            const bool have = ci < cols;
+            const int cc = c.tile * COLS + ci;
+            const int r = have ? cc / a.group : 0;
+            const int h = cc - r * a.group;
+            const uint4* src = reinterpret_cast<const uint4*>(a.q[rank] + (c.n.first_row + r) * a.ldq +
+                                                              (kvh * a.group + h) * HD + t4 * D);
+#pragma unroll
+            for (int i = 0; i < D / 8; ++i) {
+                const uint4 v = have ? __ldg(src + i) : make_uint4(0, 0, 0, 0);
+                raw[nt][4 * i] = v.x, raw[nt][4 * i + 1] = v.y, raw[nt][4 * i + 2] = v.z, raw[nt][4 * i + 3] = v.w;
+            }
+        }
+    };
+
     // ---- loading
     const uint32_t ring = smem_u32(smem) + warp * kStages * C::STAGE;
     const uint32_t my_bars = smem_u32(&bars[warp * kStages]);
-    int load_u = ahead.off + static_cast<int>(static_cast<int64_t>(ahead.count()) * wi / ws);
-    int load_end = ahead.off + static_cast<int>(static_cast<int64_t>(ahead.count()) * (wi + 1) / ws);
-    int batch_u = -(1 << 30);        // lane l holds the offset of unit batch_u + l
-    int64_t batch_off = -1;
+    // this warp's share of a segment of n units
+    auto share = [&](int n, int w) { return static_cast<int>(static_cast<uint32_t>(n) * static_cast<uint64_t>(w) / ws); };
+    // units of the stage that begins with unit u of a share [u0, u1): it ends with the sinks' blocks and with a batch
+    auto stage_units = [&](int u, int u0, int u1, int front) {
+        return min(min(C::BLOCKS, u1 - u), min(u < front ? front - u : C::BLOCKS, kBatch - ((u - u0) & (kBatch - 1))));
+    };
+    int load_u = 0, load_u0 = 0, load_end = 0;
+    int64_t batch_off = -1;          // lane l holds the address of unit l of the batch
+    uint32_t batch_there = 0;
+    int next_page = -2;              // and the page of unit l of the next batch, -2: none
+    auto block_of = [&](int u) { return u < ahead.n.front ? u : ahead.n.start + u - ahead.n.front; };
+    auto fetch_page = [&](int u) {
+        return u < load_end && u < ahead.n.blocks
+                   ? kv_page_at(a.seqs.table + ahead.s * a.seqs.max_blocks, a.seqs.max_blocks, a.pools.page_shift, block_of(u))
+                   : -2;
+    };
+    auto open_segment = [&]() {
+        load_u = load_u0 = ahead.off + share(ahead.count(), wi);
+        load_end = ahead.off + share(ahead.count(), wi + 1);
+        next_page = fetch_page(load_u + lane);
+    };
     int issued = 0;
     auto load_stage = [&]() {
         while (load_u >= load_end) {
             ahead.next(a, COLS, heads);
             if (ahead.left <= 0) return;
-            load_u = ahead.off + static_cast<int>(static_cast<int64_t>(ahead.count()) * wi / ws);
-            load_end = ahead.off + static_cast<int>(static_cast<int64_t>(ahead.count()) * (wi + 1) / ws);
-            batch_u = -(1 << 30);
+            open_segment();
         }
-        const int cnt = min(kStageBlocks, load_end - load_u);
         const int rank = ahead.head / a.pools.kv_heads;
-        if (load_u + cnt > batch_u + 32) {
-            batch_u = load_u;
-            const int u = load_u + lane;
-            batch_off = -1;
-            if (u < load_end && u < ahead.n.blocks) {
-                const int block = u < ahead.n.front ? u : ahead.n.start + u - ahead.n.front;
-                batch_off = kv_block_offset(a.seqs.table + ahead.s * a.seqs.max_blocks, a.seqs.max_blocks,
-                                            a.pools.pages, a.pools.page_shift, a.pools.kv_heads,
-                                            ahead.head - rank * a.pools.kv_heads, block, B::BYTES);
-                if (batch_off < 0) raise_status(a.seqs.status, TP_ERR_INVALID_ARG);
-            }
+        const int at = (load_u - load_u0) & (kBatch - 1);
+        if (at == 0) {
+            const int u = load_u + lane, page = next_page;
+            batch_off = kv_page_offset(page, a.pools.pages, a.pools.page_shift, a.pools.kv_heads,
+                                       ahead.head - rank * a.pools.kv_heads, block_of(u), B::BYTES);
+            if (batch_off < 0 && page != -2) raise_status(a.seqs.status, TP_ERR_INVALID_ARG);
+            batch_there = __ballot_sync(0xffffffffu, batch_off >= 0);
+            next_page = fetch_page(u + kBatch);
         }
-        const int64_t off = __shfl_sync(0xffffffffu, batch_off, (load_u - batch_u + lane) & 31);
-        const bool go = lane < cnt && off >= 0;
-        const uint32_t mask = __ballot_sync(0xffffffffu, go);
+        const int cnt = stage_units(load_u, load_u0, load_end, ahead.n.front);
+        const uint32_t mask = (batch_there >> at) & ((1u << cnt) - 1u);
         const int st = issued % kStages;
         const uint32_t bar = my_bars + st * 8;
         if (lane == 0) {
@@ -335,10 +418,14 @@ __global__ void __launch_bounds__(kWarps * 32, 1) kv4_attention_kernel(const __g
             mbar_arrive_expect_tx(bar, __popc(mask) * B::BYTES);
         }
         __syncwarp();
-        if (go) bulk_load(ring + st * C::STAGE + lane * B::BYTES, a.pools.pool[rank] + off, B::BYTES, bar);
+        const uint32_t i = static_cast<uint32_t>(lane - at);             // this lane's block of the stage
+        if (i < static_cast<uint32_t>(cnt) && batch_off >= 0)
+            bulk_load(ring + st * C::STAGE + i * B::BYTES, a.pools.pool[rank] + batch_off, B::BYTES, bar);
         ++issued;
         load_u += cnt;
     };
+    open_segment();
+    fetch_q(cur);
     for (int i = 0; i < kStages; ++i) load_stage();
 
     // ---- computing
@@ -347,9 +434,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) kv4_attention_kernel(const __g
     int used = 0;
     while (true) {
         const int seg_off = cur.off, seg_n = cur.count();
-        const int u0 = seg_off + static_cast<int>(static_cast<int64_t>(seg_n) * wi / ws);
-        const int u1 = seg_off + static_cast<int>(static_cast<int64_t>(seg_n) * (wi + 1) / ws);
-        const int rank = cur.head / a.pools.kv_heads, kvh = cur.head - rank * a.pools.kv_heads;
+        const int u0 = seg_off + share(seg_n, wi), u1 = seg_off + share(seg_n, wi + 1);
         const int cols = cur.n.rows * a.group - cur.tile * COLS;         // columns left from this tile on
         const int pos0 = cur.n.len - cur.n.rows;                        // position of the sequence's first row
 
@@ -357,29 +442,14 @@ __global__ void __launch_bounds__(kWarps * 32, 1) kv4_attention_kernel(const __g
         uint32_t qf[NT][HD / 16][2];
         float cmul[NT][2], cadd[NT][2];
         int cpos[NT][2];
-        int row_lo = 0x7fffffff, row_hi = -1;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-            const int ci = nt * 8 + g;
-            const bool have = ci < cols;
-            const int cc = cur.tile * COLS + ci;
-            const int r = have ? cc / a.group : 0;
-            const int h = cc - r * a.group;
-            constexpr int D = HD / 4;                                    // elements of this lane
-            uint32_t raw[D / 2];
-            const uint4* src = reinterpret_cast<const uint4*>(a.q[rank] + (cur.n.first_row + r) * a.ldq +
-                                                              (kvh * a.group + h) * HD + t4 * D);
-#pragma unroll
-            for (int i = 0; i < D / 8; ++i) {
-                const uint4 v = have ? __ldg(src + i) : make_uint4(0, 0, 0, 0);
-                raw[4 * i] = v.x, raw[4 * i + 1] = v.y, raw[4 * i + 2] = v.z, raw[4 * i + 3] = v.w;
-            }
             uint32_t top = 0;
             float sum = 0.0f;
 #pragma unroll
             for (int i = 0; i < D / 2; ++i) {
-                top = max(top, max(raw[i] & 0x7fffu, (raw[i] >> 16) & 0x7fffu));
-                sum += __uint_as_float(raw[i] << 16) + __uint_as_float(raw[i] & 0xffff0000u);
+                top = max(top, max(raw[nt][i] & 0x7fffu, (raw[nt][i] >> 16) & 0x7fffu));
+                sum += __uint_as_float(raw[nt][i] << 16) + __uint_as_float(raw[nt][i] & 0xffff0000u);
             }
 #pragma unroll
             for (int m = 1; m < 4; m <<= 1) {
@@ -395,8 +465,8 @@ __global__ void __launch_bounds__(kWarps * 32, 1) kv4_attention_kernel(const __g
                 float x[8];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    x[2 * i] = __uint_as_float(raw[4 * j + i] << 16);
-                    x[2 * i + 1] = __uint_as_float(raw[4 * j + i] & 0xffff0000u);
+                    x[2 * i] = __uint_as_float(raw[nt][4 * j + i] << 16);
+                    x[2 * i + 1] = __uint_as_float(raw[nt][4 * j + i] & 0xffff0000u);
                 }
                 qf[nt][2 * j][0] = pack_f16x2(x[0] * up, x[4] * up);
                 qf[nt][2 * j][1] = pack_f16x2(x[1] * up16, x[5] * up16);
@@ -414,13 +484,14 @@ __global__ void __launch_bounds__(kWarps * 32, 1) kv4_attention_kernel(const __g
                 cpos[nt][e] = ce < cols ? pos0 + (cur.tile * COLS + ce) / a.group : -1;
             }
         }
-        row_lo = pos0 + (cur.tile * COLS) / a.group;
-        row_hi = pos0 + (cur.tile * COLS + min(cols, COLS) - 1) / a.group;
+        const int row_lo = pos0 + (cur.tile * COLS) / a.group;
+        const int row_hi = pos0 + (cur.tile * COLS + min(cols, COLS) - 1) / a.group;
 
         float acc[NT][MT][4];
         float mx[NT][2], sum[NT][2], corr[NT][2];
         // exponent field of the largest value step, at least 16 so that 2^(kPShift - E) stays finite
         int vexp = 16;
+        bool fresh = true;               // some column has seen nothing
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -431,186 +502,221 @@ __global__ void __launch_bounds__(kWarps * 32, 1) kv4_attention_kernel(const __g
             for (int e = 0; e < 2; ++e) mx[nt][e] = kNegInf, sum[nt][e] = 0.0f, corr[nt][e] = 0.0f;
         }
 
-        for (int u = u0; u < u1; u += kStageBlocks) {
-            const int cnt = min(kStageBlocks, u1 - u);
+        for (int u = u0; u < u1;) {
+            const int cnt = stage_units(u, u0, u1, cur.n.front);
             const int st = used % kStages;
             if (!dead) dead = !mbar_wait_warp(my_bars + st * 8, (used / kStages) & 1, &s_abort, a.seqs.status);
             const uint32_t mask = dead ? 0u : static_cast<uint32_t>(stage_mask[warp * kStages + st]);
             const uint32_t buf = ring + st * C::STAGE;
+            const int j0 = (u < cur.n.front ? u : cur.n.start + u - cur.n.front) * kKvBlock;
+            const int j1 = j0 + C::BLOCKS * kKvBlock - 1;
+            u += cnt;
 
-            // scores of up to 64 tokens
-            float x[kStageBlocks][NT][4];
-            uint32_t vp[kStageBlocks][2];
-            float cmax[NT][2];
-            uint32_t vtop = 0;
+            // One stage; `edge`: some block is missing or some column does not see some token.
+            auto stage = [&](auto edge) {
+                constexpr bool EDGE = decltype(edge)::value;
+                float x[C::BLOCKS][NT][4];
+                uint32_t vp[C::BLOCKS][2];
+                uint32_t vtop = 0;                                       // largest step of the values: not negative
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) cmax[nt][0] = cmax[nt][1] = kNegInf;
-#pragma unroll
-            for (int i = 0; i < kStageBlocks; ++i) {
-                vp[i][0] = vp[i][1] = 0;
-                if (!((mask >> i) & 1)) {
+                for (int i = 0; i < C::BLOCKS; ++i) {
+                    const uint32_t rec = buf + i * B::BYTES;
+                    uint32_t wa[HD / 32], wb[HD / 32];
+                    const uint32_t ka = rec + B::KEYS + tok * B::ROW + t4 * (B::ROW / 4);
+                    if constexpr (HD == 128) {
+                        const uint4 p = lds128(ka), q = lds128(ka + 8 * B::ROW);
+                        wa[0] = p.x, wa[1] = p.y, wa[2] = p.z, wa[3] = p.w;
+                        wb[0] = q.x, wb[1] = q.y, wb[2] = q.z, wb[3] = q.w;
+                    } else {
+                        const uint2 p = lds64(ka), q = lds64(ka + 8 * B::ROW);
+                        wa[0] = p.x, wa[1] = p.y;
+                        wb[0] = q.x, wb[1] = q.y;
+                    }
+                    const uint32_t kp0 = lds32(rec + B::KPAIR + tok * 4), kp1 = lds32(rec + B::KPAIR + (tok + 8) * 4);
+                    vp[i][0] = lds32(rec + B::VPAIR + tok * 4);
+                    vp[i][1] = lds32(rec + B::VPAIR + (tok + 8) * 4);
+                    // two chains of products: the second half of the words has its own accumulators
+                    float y[NT][4];
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) x[i][nt][e] = kNegInf;
-                    continue;
-                }
-                const uint32_t rec = buf + i * B::BYTES;
-                uint32_t wa[HD / 32], wb[HD / 32];
-                const uint32_t ka = rec + B::KEYS + tok * B::ROW + t4 * (B::ROW / 4);
-                if constexpr (HD == 128) {
-                    const uint4 p = lds128(ka), q = lds128(ka + 8 * B::ROW);
-                    wa[0] = p.x, wa[1] = p.y, wa[2] = p.z, wa[3] = p.w;
-                    wb[0] = q.x, wb[1] = q.y, wb[2] = q.z, wb[3] = q.w;
-                } else {
-                    const uint2 p = lds64(ka), q = lds64(ka + 8 * B::ROW);
-                    wa[0] = p.x, wa[1] = p.y;
-                    wb[0] = q.x, wb[1] = q.y;
-                }
+                        for (int e = 0; e < 4; ++e) x[i][nt][e] = y[nt][e] = 0.0f;
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
+                    for (int j = 0; j < HD / 32; ++j) {
+                        const uint32_t ha = wa[j] >> 8, hb = wb[j] >> 8;
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) x[i][nt][e] = 0.0f;
-#pragma unroll
-                for (int j = 0; j < HD / 32; ++j) {
-                    const uint32_t ha = wa[j] >> 8, hb = wb[j] >> 8;
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) {
-                        mma_f16(x[i][nt], wa[j] & 0x000f000fu, wb[j] & 0x000f000fu, wa[j] & 0x00f000f0u,
-                                wb[j] & 0x00f000f0u, qf[nt][2 * j][0], qf[nt][2 * j][1]);
-                        mma_f16(x[i][nt], ha & 0x000f000fu, hb & 0x000f000fu, ha & 0x00f000f0u, hb & 0x00f000f0u,
-                                qf[nt][2 * j + 1][0], qf[nt][2 * j + 1][1]);
+                        for (int nt = 0; nt < NT; ++nt) {
+                            mma_f16(x[i][nt], wa[j] & 0x000f000fu, wb[j] & 0x000f000fu, wa[j] & 0x00f000f0u,
+                                    wb[j] & 0x00f000f0u, qf[nt][2 * j][0], qf[nt][2 * j][1]);
+                            mma_f16(y[nt], ha & 0x000f000fu, hb & 0x000f000fu, ha & 0x00f000f0u, hb & 0x00f000f0u,
+                                    qf[nt][2 * j + 1][0], qf[nt][2 * j + 1][1]);
+                        }
                     }
-                }
-                const uint32_t kp0 = lds32(rec + B::KPAIR + tok * 4), kp1 = lds32(rec + B::KPAIR + (tok + 8) * 4);
-                vp[i][0] = lds32(rec + B::VPAIR + tok * 4);
-                vp[i][1] = lds32(rec + B::VPAIR + (tok + 8) * 4);
-                const int uu = u + i;
-                const int j0 = (uu < cur.n.front ? uu : cur.n.start + uu - cur.n.front) * kKvBlock;
-                const float s0 = __uint_as_float(kp0 << 16), b0 = __uint_as_float(kp0 & 0xffff0000u);
-                const float s1 = __uint_as_float(kp1 << 16), b1 = __uint_as_float(kp1 & 0xffff0000u);
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        x[i][nt][e] = fmaf(x[i][nt][e], cmul[nt][e] * s0, cadd[nt][e] * b0);
-                        x[i][nt][2 + e] = fmaf(x[i][nt][2 + e], cmul[nt][e] * s1, cadd[nt][e] * b1);
-                    }
-                // every column sees the whole block, except at the edges of what is visible
-                const bool whole = j0 + kKvBlock - 1 <= row_lo &&
-                                   (a.window == 0 || j0 > row_hi - a.window || j0 + kKvBlock <= a.sinks);
-                if (!whole) {
-                    const int ja = j0 + tok, jb = ja + 8;
-                    // a pair that no column sees may hold anything
-                    if (ja > row_hi || !(a.window == 0 || ja > row_lo - a.window || ja < a.sinks)) vp[i][0] = 0;
-                    if (jb > row_hi || !(a.window == 0 || jb > row_lo - a.window || jb < a.sinks)) vp[i][1] = 0;
+                    const float s0 = __uint_as_float(kp0 << 16), b0 = __uint_as_float(kp0 & 0xffff0000u);
+                    const float s1 = __uint_as_float(kp1 << 16), b1 = __uint_as_float(kp1 & 0xffff0000u);
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                         for (int e = 0; e < 2; ++e) {
-                            const int p = cpos[nt][e];
-                            if (!(ja <= p && (a.window == 0 || ja > p - a.window || ja < a.sinks))) x[i][nt][e] = kNegInf;
-                            if (!(jb <= p && (a.window == 0 || jb > p - a.window || jb < a.sinks)))
-                                x[i][nt][2 + e] = kNegInf;
+                            x[i][nt][e] = fmaf(x[i][nt][e] + y[nt][e], cmul[nt][e] * s0, cadd[nt][e] * b0);
+                            x[i][nt][2 + e] = fmaf(x[i][nt][2 + e] + y[nt][2 + e], cmul[nt][e] * s1, cadd[nt][e] * b1);
                         }
-                }
-                vtop = max(vtop, max(vp[i][0] & 0xffffu, vp[i][1] & 0xffffu));   // steps are not negative
+                    if constexpr (EDGE) {
+                        const bool there = (mask >> i) & 1u;
+                        const int ja = j0 + i * kKvBlock + tok, jb = ja + 8;
+                        // a pair that no column sees may hold anything
+                        if (!there || ja > row_hi || !(a.window == 0 || ja > row_lo - a.window || ja < a.sinks)) vp[i][0] = 0;
+                        if (!there || jb > row_hi || !(a.window == 0 || jb > row_lo - a.window || jb < a.sinks)) vp[i][1] = 0;
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
+                        for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) cmax[nt][e] = fmaxf(cmax[nt][e], fmaxf(x[i][nt][e], x[i][nt][2 + e]));
-            }
-#pragma unroll
-            for (int m = 4; m < 32; m <<= 1) {
-                vtop = max(vtop, __shfl_xor_sync(0xffffffffu, vtop, m));
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                    for (int e = 0; e < 2; ++e)
-                        cmax[nt][e] = fmaxf(cmax[nt][e], __shfl_xor_sync(0xffffffffu, cmax[nt][e], m));
-            }
-            // new maxima; sums and accumulators follow when any changed
-            const int e_new = max(vexp, min(static_cast<int>(vtop >> 7), 250));
-            const float vdown = __uint_as_float(static_cast<uint32_t>(max(127 - (e_new - vexp), 0)) << 23);
-            vexp = e_new;
-            float alpha[NT][2];
-            bool moved = vdown != 1.0f;
-            float base[NT][2];
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const float m = fmaxf(mx[nt][e], cmax[nt][e]);
-                    base[nt][e] = m == kNegInf ? 0.0f : m;
-                    alpha[nt][e] = ex2(mx[nt][e] - base[nt][e]);
-                    moved |= m != mx[nt][e];
-                    mx[nt][e] = m;
-                }
-            if (__any_sync(0xffffffffu, moved)) {
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        sum[nt][e] *= alpha[nt][e];
-                        corr[nt][e] *= alpha[nt][e];
-                        const float f = alpha[nt][e] * vdown;
-#pragma unroll
-                        for (int i = 0; i < MT; ++i) acc[nt][i][e] *= f, acc[nt][i][2 + e] *= f;
+                            for (int e = 0; e < 2; ++e) {
+                                const int p = there ? cpos[nt][e] : -1;
+                                if (!(ja <= p && (a.window == 0 || ja > p - a.window || ja < a.sinks))) x[i][nt][e] = kNegInf;
+                                if (!(jb <= p && (a.window == 0 || jb > p - a.window || jb < a.sinks)))
+                                    x[i][nt][2 + e] = kNegInf;
+                            }
                     }
-            }
-            const float vscale = __uint_as_float(static_cast<uint32_t>(253 - vexp) << 23) * (1 << kPShift);
-#pragma unroll
-            for (int i = 0; i < kStageBlocks; ++i) {
-                if (!((mask >> i) & 1)) continue;
-                const float s0 = __uint_as_float(vp[i][0] << 16) * vscale, b0 = __uint_as_float(vp[i][0] & 0xffff0000u);
-                const float s1 = __uint_as_float(vp[i][1] << 16) * vscale, b1 = __uint_as_float(vp[i][1] & 0xffff0000u);
-                uint32_t pf[NT][2];
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                    float ps[4];
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const float xa = x[i][nt][e], xb = x[i][nt][2 + e];
-                        const float pa = ex2(xa - base[nt][e]), pb = ex2(xb - base[nt][e]);
-                        sum[nt][e] += pa + pb;
-                        // a token that this column does not see may stand for NaN or infinities
-                        ps[e] = xa == kNegInf ? 0.0f : pa * s0;
-                        ps[2 + e] = xb == kNegInf ? 0.0f : pb * s1;
-                        corr[nt][e] += (xa == kNegInf ? 0.0f : pa * b0) + (xb == kNegInf ? 0.0f : pb * b1);
-                    }
-                    pf[nt][0] = transpose8x8(pack_f16x2(ps[0], ps[1]));
-                    pf[nt][1] = transpose8x8(pack_f16x2(ps[2], ps[3]));
+                    vtop = max(vtop, max(vp[i][0] & 0xffffu, vp[i][1] & 0xffffu));
                 }
-                // values: tokens t4, 4 + (t4 ^ 1) and the same + 8 are this lane's columns of k
-                const uint32_t va = buf + i * B::BYTES + B::VALS + g * (B::ROW / 8);
-                constexpr int W = HD / 64;
-                uint32_t y[4][W];
+
+                // p s' as B fragments, and what the stage adds to the sums
+                uint32_t pf[C::BLOCKS][NT][2];
+                float psum[NT][2], pcorr[NT][2];
+                auto weigh = [&]() {
+                    const float vscale = __uint_as_float(static_cast<uint32_t>(253 - vexp) << 23) * (1 << kPShift);
+                    float m[NT][2];
 #pragma unroll
-                for (int p = 0; p < 4; ++p) {
-                    const int tk = ((p & 1) ? 4 + (t4 ^ 1) : t4) + (p >> 1) * 8;
-                    if constexpr (W == 2) {
-                        const uint2 v = lds64(va + tk * B::ROW);
-                        y[p][0] = v.x, y[p][1] = v.y;
-                    } else {
-                        y[p][0] = lds32(va + tk * B::ROW);
-                    }
-                }
+                    for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                for (int j = 0; j < W; ++j)
+                        for (int e = 0; e < 2; ++e) {
+                            psum[nt][e] = pcorr[nt][e] = 0.0f;
+                            m[nt][e] = mx[nt][e] == kNegInf ? 0.0f : mx[nt][e];
+                        }
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        uint32_t p01 = __byte_perm(y[0][j], y[1][j], h ? 0x7632 : 0x5410);
-                        uint32_t p23 = __byte_perm(y[2][j], y[3][j], h ? 0x7632 : 0x5410);
+                    for (int i = 0; i < C::BLOCKS; ++i) {
+                        const float s0 = __uint_as_float(vp[i][0] << 16) * vscale, b0 = __uint_as_float(vp[i][0] & 0xffff0000u);
+                        const float s1 = __uint_as_float(vp[i][1] << 16) * vscale, b1 = __uint_as_float(vp[i][1] & 0xffff0000u);
 #pragma unroll
-                        for (int b = 0; b < 2; ++b) {
+                        for (int nt = 0; nt < NT; ++nt) {
+                            float ps[4];
 #pragma unroll
-                            for (int nt = 0; nt < NT; ++nt)
-                                mma_f16(acc[nt][j * 4 + h * 2 + b], p01 & 0x000f000fu, p01 & 0x00f000f0u,
-                                        p23 & 0x000f000fu, p23 & 0x00f000f0u, pf[nt][0], pf[nt][1]);
-                            p01 >>= 8, p23 >>= 8;
+                            for (int e = 0; e < 2; ++e) {
+                                const float xa = x[i][nt][e], xb = x[i][nt][2 + e];
+                                const float pa = ex2(xa - m[nt][e]), pb = ex2(xb - m[nt][e]);
+                                psum[nt][e] += pa + pb;
+                                if constexpr (EDGE) {
+                                    // a token that this column does not see may stand for NaN or infinities
+                                    ps[e] = xa == kNegInf ? 0.0f : pa * s0;
+                                    ps[2 + e] = xb == kNegInf ? 0.0f : pb * s1;
+                                    pcorr[nt][e] += (xa == kNegInf ? 0.0f : pa * b0) + (xb == kNegInf ? 0.0f : pb * b1);
+                                } else {
+                                    ps[e] = pa * s0;
+                                    ps[2 + e] = pb * s1;
+                                    pcorr[nt][e] = fmaf(pa, b0, fmaf(pb, b1, pcorr[nt][e]));
+                                }
+                            }
+                            pf[i][nt][0] = pack_f16x2(ps[0], ps[1]);
+                            pf[i][nt][1] = pack_f16x2(ps[2], ps[3]);
                         }
                     }
-            }
+                };
+                bool again = fresh || static_cast<int>(vtop >> 7) > vexp;
+                if (!__any_sync(0xffffffffu, again)) {                   // the old maximum may do
+                    weigh();
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) again |= !(psum[nt][e] <= kMost);
+                }
+                if (__any_sync(0xffffffffu, again)) {
+                    float cmax[NT][2];
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            cmax[nt][e] = kNegInf;
+#pragma unroll
+                            for (int i = 0; i < C::BLOCKS; ++i)
+                                cmax[nt][e] = fmaxf(cmax[nt][e], fmaxf(x[i][nt][e], x[i][nt][2 + e]));
+                        }
+#pragma unroll
+                    for (int m = 4; m < 32; m <<= 1) {
+                        vtop = max(vtop, __shfl_xor_sync(0xffffffffu, vtop, m));
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                            for (int e = 0; e < 2; ++e)
+                                cmax[nt][e] = fmaxf(cmax[nt][e], __shfl_xor_sync(0xffffffffu, cmax[nt][e], m));
+                    }
+                    const int e_new = max(vexp, min(static_cast<int>(vtop >> 7), 250));
+                    const float vdown = __uint_as_float(static_cast<uint32_t>(max(127 - (e_new - vexp), 0)) << 23);
+                    vexp = e_new;
+                    bool unseen = false;
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const float m = fmaxf(mx[nt][e], cmax[nt][e]);
+                            const float alpha = ex2(mx[nt][e] - (m == kNegInf ? 0.0f : m));
+                            mx[nt][e] = m;
+                            unseen |= m == kNegInf && nt * 8 + 2 * t4 + e < cols;
+                            sum[nt][e] *= alpha;
+                            corr[nt][e] *= alpha;
+#pragma unroll
+                            for (int i = 0; i < MT; ++i)
+                                acc[nt][i][e] *= alpha * vdown, acc[nt][i][2 + e] *= alpha * vdown;
+                        }
+                    fresh = __any_sync(0xffffffffu, unseen);
+                    weigh();
+                }
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) sum[nt][e] += psum[nt][e], corr[nt][e] += pcorr[nt][e];
+#pragma unroll
+                for (int i = 0; i < C::BLOCKS; ++i) {
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) pf[i][nt][e] = transpose8x8(pf[i][nt][e]);
+                    // values: tokens t4, 4 + (t4 ^ 1) and the same + 8 are this lane's columns of k
+                    const uint32_t va = buf + i * B::BYTES + B::VALS + g * (B::ROW / 8);
+                    constexpr int W = HD / 64;
+                    uint32_t y[4][W];
+#pragma unroll
+                    for (int p = 0; p < 4; ++p) {
+                        const int tk = ((p & 1) ? 4 + (t4 ^ 1) : t4) + (p >> 1) * 8;
+                        if constexpr (W == 2) {
+                            const uint2 v = lds64(va + tk * B::ROW);
+                            y[p][0] = v.x, y[p][1] = v.y;
+                        } else {
+                            y[p][0] = lds32(va + tk * B::ROW);
+                        }
+                    }
+#pragma unroll
+                    for (int j = 0; j < W; ++j)
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            uint32_t p01 = __byte_perm(y[0][j], y[1][j], h ? 0x7632 : 0x5410);
+                            uint32_t p23 = __byte_perm(y[2][j], y[3][j], h ? 0x7632 : 0x5410);
+#pragma unroll
+                            for (int b = 0; b < 2; ++b) {
+#pragma unroll
+                                for (int nt = 0; nt < NT; ++nt)
+                                    mma_f16(acc[nt][j * 4 + h * 2 + b], p01 & 0x000f000fu, p01 & 0x00f000f0u,
+                                            p23 & 0x000f000fu, p23 & 0x00f000f0u, pf[i][nt][0], pf[i][nt][1]);
+                                p01 >>= 8, p23 >>= 8;
+                            }
+                        }
+                }
+            };
+            const bool whole = mask == (1u << C::BLOCKS) - 1u && j1 <= row_lo &&
+                               (a.window == 0 || j0 > row_hi - a.window || j1 < a.sinks);
+            if (whole)
+                stage(std::false_type{});
+            else
+                stage(std::true_type{});
             __syncwarp();                                                // every lane is done with the stage
             ++used;
             if (!dead) load_stage();
@@ -633,84 +739,45 @@ __global__ void __launch_bounds__(kWarps * 32, 1) kv4_attention_kernel(const __g
                     acc[nt][i][2 + e] = fmaf(acc[nt][i][2 + e], down * 0.0625f, corr[nt][e]);
                 }
             }
-        // merge the worker's warps, halves at a time
-        for (int half = ws / 2; half >= 1; half >>= 1) {
-            float4* area = reinterpret_cast<float4*>(smem + C::RING) + (grp * (ws / 2) + (wi % half)) * (C::MERGE / 16);
-            if (wi >= half && wi < 2 * half) {
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-                    for (int i = 0; i < MT; ++i)
-                        area[(nt * (MT + 1) + i) * 32 + lane] =
-                            make_float4(acc[nt][i][0], acc[nt][i][1], acc[nt][i][2], acc[nt][i][3]);
-                    area[(nt * (MT + 1) + MT) * 32 + lane] = make_float4(mx[nt][0], mx[nt][1], sum[nt][0], sum[nt][1]);
-                }
-            }
-            asm volatile("bar.sync %0, %1;" ::"r"(1 + grp), "r"(ws * 32) : "memory");
-            if (wi < half) {
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                    const float4 o = area[(nt * (MT + 1) + MT) * 32 + lane];
-                    const float om[2] = {o.x, o.y}, os[2] = {o.z, o.w};
-                    float fa[2], fb[2];
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const float m = fmaxf(mx[nt][e], om[e]), b = m == kNegInf ? 0.0f : m;
-                        fa[e] = ex2(mx[nt][e] - b);
-                        fb[e] = ex2(om[e] - b);
-                        mx[nt][e] = m;
-                        sum[nt][e] = sum[nt][e] * fa[e] + os[e] * fb[e];
-                    }
-#pragma unroll
-                    for (int i = 0; i < MT; ++i) {
-                        const float4 v = area[(nt * (MT + 1) + i) * 32 + lane];
-                        acc[nt][i][0] = acc[nt][i][0] * fa[0] + v.x * fb[0];
-                        acc[nt][i][1] = acc[nt][i][1] * fa[1] + v.y * fb[1];
-                        acc[nt][i][2] = acc[nt][i][2] * fa[0] + v.z * fb[0];
-                        acc[nt][i][3] = acc[nt][i][3] * fa[1] + v.w * fb[1];
-                    }
-                }
-            }
-            asm volatile("bar.sync %0, %1;" ::"r"(1 + grp), "r"(ws * 32) : "memory");
-        }
-        if (wi == 0) {
-            const bool complete = seg_off == 0 && seg_n == cur.n.units;
-            constexpr int DL = HD / 8;                                   // dimensions of this lane
-            float* slot = slots + (static_cast<size_t>(worker) * 2 + (first_segment ? 0 : 1)) * slot_floats(COLS, HD);
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const int ci = nt * 8 + 2 * t4 + e;
-                    if (complete) {
-                        if (ci >= cols) continue;
-                        const float inv = sum[nt][e] == 0.0f ? 0.0f : 1.0f / sum[nt][e];
-                        const int cc = cur.tile * COLS + ci;
-                        const int r = cc / a.group, h = cc - r * a.group;
-                        uint16_t* dst = a.out[rank] + (cur.n.first_row + r) * a.ldo + (kvh * a.group + h) * HD + g * DL;
-#pragma unroll
-                        for (int i = 0; i < MT; i += 4)
-                            *reinterpret_cast<uint4*>(dst + 2 * i) =
-                                make_uint4(pack_bf16x2(acc[nt][i][e] * inv, acc[nt][i][2 + e] * inv),
-                                           pack_bf16x2(acc[nt][i + 1][e] * inv, acc[nt][i + 1][2 + e] * inv),
-                                           pack_bf16x2(acc[nt][i + 2][e] * inv, acc[nt][i + 2][2 + e] * inv),
-                                           pack_bf16x2(acc[nt][i + 3][e] * inv, acc[nt][i + 3][2 + e] * inv));
-                    } else {
-                        float4* dst = reinterpret_cast<float4*>(slot + ci * HD + g * DL);
-#pragma unroll
-                        for (int i = 0; i < MT; i += 2)
-                            dst[i / 2] = make_float4(acc[nt][i][e], acc[nt][i][2 + e], acc[nt][i + 1][e],
-                                                     acc[nt][i + 1][2 + e]);
-                        if (g == 0) {
-                            slot[COLS * HD + ci] = mx[nt][e];
-                            slot[COLS * (HD + 1) + ci] = sum[nt][e];
-                        }
-                    }
-                }
-        }
+        const bool complete = seg_off == 0 && seg_n == cur.n.units;
+        const int head = cur.head, first_row = cur.n.first_row, tile = cur.tile;
+        float4* slot = slots + (static_cast<size_t>(worker) * 2 + (first_segment ? 0 : 1)) * C::PART;
         first_segment = false;
         cur.next(a, COLS, heads);
-        if (cur.left <= 0) break;
+        const bool more = cur.left > 0;
+        if (more) fetch_q(cur);
+        // the worker's warps together: every one leaves its part, then they share the sum of the parts
+        float4* parts = reinterpret_cast<float4*>(smem + C::RING) + grp * ws * C::PART;
+        float4* mine_part = ws > 1 || complete ? parts + wi * C::PART : slot;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+            for (int i = 0; i < MT; ++i)
+                mine_part[(nt * MT + i) * 32 + lane] =
+                    make_float4(acc[nt][i][0], acc[nt][i][1], acc[nt][i][2], acc[nt][i][3]);
+            mine_part[(NT * MT + nt) * 32 + lane] = make_float4(mx[nt][0], mx[nt][1], sum[nt][0], sum[nt][1]);
+        }
+        if (ws > 1)
+            asm volatile("bar.sync %0, %1;" ::"r"(1 + grp), "r"(ws * 32) : "memory");
+        else
+            __syncwarp();
+        if (ws > 1 || complete)
+            for (int v = wi * 32 + lane; v < NT * MT * 32; v += ws * 32) {
+                float2 top, all;
+                const float4 o = join_parts<HD, NT>(v, ws, [&](int i) { return parts + i * C::PART; }, top, all);
+                if (complete) {
+                    store_vector<HD, NT>(a, head, first_row, cols, tile, v, o, all);
+                } else {
+                    slot[v] = o;
+                    if (v / 32 % MT == 0)
+                        slot[NT * MT * 32 + v / (MT * 32) * 32 + lane] = make_float4(top.x, top.y, all.x, all.y);
+                }
+            }
+        if (!more) break;
+        if (ws > 1)
+            asm volatile("bar.sync %0, %1;" ::"r"(1 + grp), "r"(ws * 32) : "memory");
+        else
+            __syncwarp();
     }
     if (dead) spin_ns(1000000);      // copies that were issued land before the block's memory is given back
 }
@@ -719,46 +786,22 @@ __global__ void __launch_bounds__(kWarps * 32, 1) kv4_attention_kernel(const __g
 // block per worker; the block of the first worker that begins inside the item does it.
 template <int HD, int NT>
 __global__ void __launch_bounds__(256) kv4_attention_join_kernel(const __grid_constant__ AttnArgs a, int main_grid) {
-    constexpr int COLS = 8 * NT;
+    constexpr int COLS = 8 * NT, MT = HD / 16, PART = slot_vectors(NT, HD);
     pdl_wait();
     pdl_trigger();
-    const Cut cut = *reinterpret_cast<const Cut*>(a.ws);
     const int b = blockIdx.x;
-    if (b >= cut.workers || b == 0) return;
-    const int64_t begin = part_begin(cut.total, cut.workers, b);
-    if (begin >= part_begin(cut.total, cut.workers, b + 1)) return;
-    const Split sp = reinterpret_cast<const Split*>(a.ws + kSplitAt)[b];
-    if (sp.units == 0) return;
-    const int b_lo = worker_of(cut.total, cut.workers, sp.begin);
-    if (worker_of(cut.total, cut.workers, begin - 1) != b_lo) return;
-    const int b_hi = worker_of(cut.total, cut.workers, sp.begin + sp.units - 1);
-    const bool lo_first = part_begin(cut.total, cut.workers, b_lo) == sp.begin;
-    const float* slots = reinterpret_cast<const float*>(a.ws + kSplitAt + static_cast<size_t>(main_grid) * kWarps * sizeof(Split));
-    const int rank = sp.head / a.pools.kv_heads, kvh = sp.head - rank * a.pools.kv_heads;
-    const int cols = min(COLS, sp.rows * a.group - sp.tile * COLS);
-    for (int i = threadIdx.x; i < cols * (HD / 4); i += 256) {
-        const int ci = i / (HD / 4), d = (i - ci * (HD / 4)) * 4;
-        float m = kNegInf, l = 0.0f;
-        float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 4
-        for (int w = b_lo; w <= b_hi; ++w) {
-            const float* slot = slots + (static_cast<size_t>(w) * 2 + (w == b_lo && !lo_first ? 1 : 0)) * slot_floats(COLS, HD);
-            const float wm = slot[COLS * HD + ci], wl = slot[COLS * (HD + 1) + ci];
-            const float4 v = *reinterpret_cast<const float4*>(slot + ci * HD + d);
-            const float nm = fmaxf(m, wm), nb = nm == kNegInf ? 0.0f : nm;
-            const float fa = ex2(m - nb), fb = ex2(wm - nb);
-            m = nm;
-            l = l * fa + wl * fb;
-            o.x = o.x * fa + v.x * fb;
-            o.y = o.y * fa + v.y * fb;
-            o.z = o.z * fa + v.z * fb;
-            o.w = o.w * fa + v.w * fb;
-        }
-        const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-        const int cc = sp.tile * COLS + ci;
-        const int r = cc / a.group, h = cc - r * a.group;
-        *reinterpret_cast<uint2*>(a.out[rank] + (sp.first_row + r) * a.ldo + (kvh * a.group + h) * HD + d) =
-            make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
+    const int workers = reinterpret_cast<const Cut*>(a.ws)->workers;
+    const Split sp = reinterpret_cast<const Split*>(a.ws + kSplitAt)[b];     // anything past the workers
+    if (b >= workers || sp.units == 0 || sp.from != b - 1) return;
+    const float4* slots =
+        reinterpret_cast<const float4*>(a.ws + kSplitAt + static_cast<size_t>(main_grid) * kWarps * sizeof(Split));
+    const int cols = sp.rows * a.group - sp.tile * COLS;
+    for (int v = threadIdx.x; v < NT * MT * 32; v += 256) {
+        float2 top, all;
+        const float4 o = join_parts<HD, NT>(
+            v, sp.to - sp.from + 1,
+            [&](int i) { return slots + (static_cast<size_t>(sp.from + i) * 2 + (i == 0 ? sp.from_slot : 0)) * PART; }, top, all);
+        store_vector<HD, NT>(a, sp.head, sp.first_row, cols, sp.tile, v, o, all);
     }
 }
 
@@ -768,8 +811,8 @@ tp_status launch_few(const AttnArgs& a, int sms, cudaStream_t stream) {
     static std::atomic<uint64_t> smem_set{0};
     auto* kern = kv4_attention_kernel<HD, NT>;
     if (!smem_attribute_once(reinterpret_cast<const void*>(kern), C::SMEM, smem_set)) return TP_ERR_CUDA;
-    if (launch_pdl(kern, dim3(sms), dim3(kWarps * 32), C::SMEM, stream, a) != cudaSuccess) return TP_ERR_CUDA;
-    if (launch_pdl(kv4_attention_join_kernel<HD, NT>, dim3(sms * kWarps), dim3(256), 0, stream, a, sms) != cudaSuccess)
+    if (launch_pdl(kern, dim3(sms), dim3(C::WARPS * 32), C::SMEM, stream, a) != cudaSuccess) return TP_ERR_CUDA;
+    if (launch_pdl(kv4_attention_join_kernel<HD, NT>, dim3(sms * C::WARPS), dim3(256), 0, stream, a, sms) != cudaSuccess)
         return TP_ERR_CUDA;
     return TP_OK;
 }
@@ -778,9 +821,9 @@ tp_status launch_few(const AttnArgs& a, int sms, cudaStream_t stream) {
 
 size_t kv4_attention_workspace(int t, int64_t n, int64_t nseq, int heads, int kv_heads, int head_dim) {
     (void)t, (void)n, (void)nseq, (void)heads, (void)kv_heads;
-    // two slots of 16 columns for each of the 8 workers that an SM can have
+    // two parts for each of the workers that an SM can have: 16 with 8 columns, 8 with 16
     const size_t workers = static_cast<size_t>(std::max(device_sms(), 160)) * kWarps;
-    return kSplitAt + workers * (sizeof(Split) + 2 * slot_floats(16, head_dim) * sizeof(float));
+    return kSplitAt + workers * (sizeof(Split) + 2 * slot_vectors(1, head_dim) * sizeof(float4));
 }
 
 tp_status launch_kv4_attention(const KvAttentionDesc& d, cudaStream_t stream) {
