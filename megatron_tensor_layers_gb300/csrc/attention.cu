@@ -74,7 +74,7 @@ __host__ __device__ constexpr int slot_vectors(int nt, int hd) { return nt * (hd
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                         uint32_t b1) {
-    asm volatile(
+    asm(
         "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
         "{%0, %1, %2, %3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
@@ -83,7 +83,7 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1,
 
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
     uint32_t r;
-    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
     return r;
 }
 
@@ -134,23 +134,27 @@ __device__ __forceinline__ Need seq_need(const AttnArgs& a, int s, int cols_per_
     return n;
 }
 
-__device__ __forceinline__ int64_t seq_weight(const AttnArgs& a, int s, int cols_per_tile, int heads) {
-    const Need n = seq_need(a, s, cols_per_tile);
-    return static_cast<int64_t>(n.units) * n.tiles * heads;
+// a / b for a >= 0, b > 0: 32-bit division where it will do (a 64-bit one takes a hundred instructions).
+__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
+    if (((a | b) >> 32) == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
+    return a / b;
 }
 
-// First unit of part b of `workers` equal parts (the first total % workers parts hold one more);
-// workers <= total.
-__device__ __forceinline__ int64_t part_begin(int64_t total, int workers, int b) {
-    const int64_t q = total / workers, r = total - q * workers;
-    return q * b + min(static_cast<int64_t>(b), r);
-}
-
-// The part that holds unit u.
-__device__ __forceinline__ int worker_of(int64_t total, int workers, int64_t u) {
-    const int64_t q = total / workers, r = total - q * workers;
-    return static_cast<int>(u < r * (q + 1) ? u / (q + 1) : r + (u - r * (q + 1)) / q);
-}
+// The line of `total` units in `workers` <= total equal parts; the first `more` hold one unit more.
+struct Parts {
+    int64_t each;
+    int more;
+    __device__ __forceinline__ Parts(int64_t total, int workers) {
+        each = quotient(total, workers);
+        more = static_cast<int>(total - each * workers);
+    }
+    __device__ __forceinline__ int64_t begin(int b) const { return each * b + min(b, more); }
+    // the part that holds unit u
+    __device__ __forceinline__ int of(int64_t u) const {
+        const int64_t front = (each + 1) * more;
+        return static_cast<int>(u < front ? quotient(u, each + 1) : more + quotient(u - front, each));
+    }
+};
 
 // A position on the line of units, walked item by item.
 struct Cursor {
@@ -258,10 +262,11 @@ __global__ void __launch_bounds__(Cfg<HD, NT>::WARPS * 32, 1) kv4_attention_kern
     // ---- the cut: total units, items, then where each of this block's workers begins
     int64_t mine = 0, items = 0;
     const int per = (a.seqs.nseq + THREADS - 1) / THREADS;
+    Need need = {};                  // of this thread's last sequence: with one each, it is not asked for twice
     for (int s = tid * per; s < min(a.seqs.nseq, (tid + 1) * per); ++s) {
-        const Need n = seq_need(a, s, COLS);
-        mine += static_cast<int64_t>(n.units) * n.tiles * heads;
-        items += static_cast<int64_t>(n.tiles) * heads;
+        need = seq_need(a, s, COLS);
+        mine += static_cast<int64_t>(need.units) * need.tiles * heads;
+        items += static_cast<int64_t>(need.tiles) * heads;
     }
     int64_t before = mine;
 #pragma unroll
@@ -291,42 +296,44 @@ __global__ void __launch_bounds__(Cfg<HD, NT>::WARPS * 32, 1) kv4_attention_kern
     const int groups = WARPS / ws;
     const int64_t least = C::BLOCKS * ws;
     const int workers =
-        static_cast<int>(max(static_cast<int64_t>(1), min(static_cast<int64_t>(gridDim.x) * groups, (total + least - 1) / least)));
+        static_cast<int>(min(static_cast<int64_t>(gridDim.x) * groups, quotient(total + least - 1, least)));
+    const Parts parts(total, workers);
     for (int i = 0; i < groups; ++i) {
         const int w = i * gridDim.x + blockIdx.x;
-        const int64_t begin = w < workers ? part_begin(total, workers, w) : total;
-        const int64_t end = w < workers ? part_begin(total, workers, w + 1) : total;
-        if (begin >= end) {
+        if (w >= workers) {
             if (tid == 0) s_cursor[i].left = 0;
             continue;
         }
+        const int64_t begin = parts.begin(w);
         if (begin >= before && begin < before + mine) {      // one thread's sequences hold the beginning
             int64_t u = begin - before;
             int s = tid * per;
-            while (true) {
-                const int64_t w_s = seq_weight(a, s, COLS, heads);
-                if (u < w_s) break;
-                u -= w_s;
-                ++s;
-            }
+            if (per > 1)
+                while (true) {
+                    need = seq_need(a, s, COLS);
+                    const int64_t w_s = static_cast<int64_t>(need.units) * need.tiles * heads;
+                    if (u < w_s) break;
+                    u -= w_s;
+                    ++s;
+                }
             Cursor c;
-            c.left = static_cast<int>(end - begin);
+            c.left = static_cast<int>(parts.begin(w + 1) - begin);
             c.s = s;
-            c.n = seq_need(a, s, COLS);
-            const int item = static_cast<int>(u / c.n.units);
-            c.off = static_cast<int>(u - static_cast<int64_t>(item) * c.n.units);
+            c.n = need;
+            const int item = static_cast<int>(quotient(u, need.units));
+            c.off = static_cast<int>(u - static_cast<int64_t>(item) * need.units);
             c.tile = item / heads;
             c.head = item - c.tile * heads;
             s_cursor[i] = c;
             Split sp = {};
             if (c.off > 0) {
                 const int64_t first = begin - c.off;
-                sp.units = c.n.units;
-                sp.from = worker_of(total, workers, first);
-                sp.to = worker_of(total, workers, first + c.n.units - 1);
-                sp.from_slot = part_begin(total, workers, sp.from) == first ? 0 : 1;
-                sp.first_row = c.n.first_row;
-                sp.rows = c.n.rows;
+                sp.units = need.units;
+                sp.from = parts.of(first);
+                sp.to = parts.of(first + need.units - 1);
+                sp.from_slot = parts.begin(sp.from) == first ? 0 : 1;
+                sp.first_row = need.first_row;
+                sp.rows = need.rows;
                 sp.tile = c.tile;
                 sp.head = c.head;
             }
@@ -747,8 +754,8 @@ __global__ void __launch_bounds__(Cfg<HD, NT>::WARPS * 32, 1) kv4_attention_kern
         const bool more = cur.left > 0;
         if (more) fetch_q(cur);
         // the worker's warps together: every one leaves its part, then they share the sum of the parts
-        float4* parts = reinterpret_cast<float4*>(smem + C::RING) + grp * ws * C::PART;
-        float4* mine_part = ws > 1 || complete ? parts + wi * C::PART : slot;
+        float4* left = reinterpret_cast<float4*>(smem + C::RING) + grp * ws * C::PART;
+        float4* mine_part = ws > 1 || complete ? left + wi * C::PART : slot;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -764,7 +771,7 @@ __global__ void __launch_bounds__(Cfg<HD, NT>::WARPS * 32, 1) kv4_attention_kern
         if (ws > 1 || complete)
             for (int v = wi * 32 + lane; v < NT * MT * 32; v += ws * 32) {
                 float2 top, all;
-                const float4 o = join_parts<HD, NT>(v, ws, [&](int i) { return parts + i * C::PART; }, top, all);
+                const float4 o = join_parts<HD, NT>(v, ws, [&](int i) { return left + i * C::PART; }, top, all);
                 if (complete) {
                     store_vector<HD, NT>(a, head, first_row, cols, tile, v, o, all);
                 } else {
@@ -782,26 +789,50 @@ __global__ void __launch_bounds__(Cfg<HD, NT>::WARPS * 32, 1) kv4_attention_kern
     if (dead) spin_ns(1000000);      // copies that were issued land before the block's memory is given back
 }
 
-// Adds, in order, the parts of an item that several workers hold.  One thread
-// block per worker; the block of the first worker that begins inside the item does it.
+// Adds, in order, the parts of an item that several workers hold; the block of
+// the first worker that begins inside the item does it.  Half of the threads
+// take half of the parts each, as the loads' latency is what it takes.
+constexpr int kJoinHalves = 2;
 template <int HD, int NT>
-__global__ void __launch_bounds__(256) kv4_attention_join_kernel(const __grid_constant__ AttnArgs a, int main_grid) {
+__global__ void __launch_bounds__(kJoinHalves * 256) kv4_attention_join_kernel(const __grid_constant__ AttnArgs a) {
     constexpr int COLS = 8 * NT, MT = HD / 16, PART = slot_vectors(NT, HD);
+    __shared__ float4 s_o[256], s_st[256];
     pdl_wait();
     pdl_trigger();
-    const int b = blockIdx.x;
+    const int tid = threadIdx.x & 255, half = threadIdx.x >> 8;
     const int workers = reinterpret_cast<const Cut*>(a.ws)->workers;
-    const Split sp = reinterpret_cast<const Split*>(a.ws + kSplitAt)[b];     // anything past the workers
-    if (b >= workers || sp.units == 0 || sp.from != b - 1) return;
     const float4* slots =
-        reinterpret_cast<const float4*>(a.ws + kSplitAt + static_cast<size_t>(main_grid) * kWarps * sizeof(Split));
-    const int cols = sp.rows * a.group - sp.tile * COLS;
-    for (int v = threadIdx.x; v < NT * MT * 32; v += 256) {
-        float2 top, all;
-        const float4 o = join_parts<HD, NT>(
-            v, sp.to - sp.from + 1,
-            [&](int i) { return slots + (static_cast<size_t>(sp.from + i) * 2 + (i == 0 ? sp.from_slot : 0)) * PART; }, top, all);
-        store_vector<HD, NT>(a, sp.head, sp.first_row, cols, sp.tile, v, o, all);
+        reinterpret_cast<const float4*>(a.ws + kSplitAt + static_cast<size_t>(gridDim.x) * kWarps * sizeof(Split));
+    for (int b = blockIdx.x; b < workers; b += gridDim.x) {
+        const Split sp = reinterpret_cast<const Split*>(a.ws + kSplitAt)[b];
+        if (sp.units == 0 || sp.from != b - 1) continue;
+        const int cols = sp.rows * a.group - sp.tile * COLS, count = sp.to - sp.from + 1;
+        const int lo = half * ((count + 1) / 2), n = half ? count - lo : (count + 1) / 2;
+        for (int v0 = 0; v0 < NT * MT * 32; v0 += 256) {
+            const int v = v0 + tid;
+            float2 top = make_float2(kNegInf, kNegInf), all = make_float2(0.0f, 0.0f);
+            float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            if (v < NT * MT * 32)
+                o = join_parts<HD, NT>(
+                    v, n,
+                    [&](int i) {
+                        return slots + (static_cast<size_t>(sp.from + lo + i) * 2 + (lo + i == 0 ? sp.from_slot : 0)) * PART;
+                    },
+                    top, all);
+            if (half) s_o[tid] = o, s_st[tid] = make_float4(top.x, top.y, all.x, all.y);
+            __syncthreads();
+            if (!half && v < NT * MT * 32) {
+                const float4 st = s_st[tid], x = s_o[tid];
+                const float2 m = make_float2(fmaxf(top.x, st.x), fmaxf(top.y, st.y));
+                const float2 c = make_float2(m.x == kNegInf ? 0.0f : m.x, m.y == kNegInf ? 0.0f : m.y);
+                const float2 fa = make_float2(ex2(top.x - c.x), ex2(top.y - c.y)), fb = make_float2(ex2(st.x - c.x), ex2(st.y - c.y));
+                all = make_float2(all.x * fa.x + st.z * fb.x, all.y * fa.y + st.w * fb.y);
+                o = make_float4(o.x * fa.x + x.x * fb.x, o.y * fa.y + x.y * fb.y, o.z * fa.x + x.z * fb.x,
+                                o.w * fa.y + x.w * fb.y);
+                store_vector<HD, NT>(a, sp.head, sp.first_row, cols, sp.tile, v, o, all);
+            }
+            __syncthreads();
+        }
     }
 }
 
@@ -812,7 +843,7 @@ tp_status launch_few(const AttnArgs& a, int sms, cudaStream_t stream) {
     auto* kern = kv4_attention_kernel<HD, NT>;
     if (!smem_attribute_once(reinterpret_cast<const void*>(kern), C::SMEM, smem_set)) return TP_ERR_CUDA;
     if (launch_pdl(kern, dim3(sms), dim3(C::WARPS * 32), C::SMEM, stream, a) != cudaSuccess) return TP_ERR_CUDA;
-    if (launch_pdl(kv4_attention_join_kernel<HD, NT>, dim3(sms * C::WARPS), dim3(256), 0, stream, a, sms) != cudaSuccess)
+    if (launch_pdl(kv4_attention_join_kernel<HD, NT>, dim3(sms), dim3(kJoinHalves * 256), 0, stream, a) != cudaSuccess)
         return TP_ERR_CUDA;
     return TP_OK;
 }
