@@ -27,9 +27,15 @@
 // each worker of WS warps (8, or fewer when items are short, so that a worker
 // then takes whole items); the warps of a worker share each item's part of its
 // range and merge through shared memory.  A worker's part of an item that it
-// does not hold whole goes to the workspace, and a second kernel adds the parts
-// in order.  The cut depends on lengths the host does not know, so every thread
-// block finds its own.
+// does not hold whole goes to the workspace, and the worker that holds the
+// item's end adds the parts in order, after its own range is done: it waits, with
+// a limit, for the flags of the parts before its own, which are raised before
+// their workers wait for anything.  A second kernel for this costs 5 us more.
+// A flag is raised by writing the call's number, which nothing else in the
+// workspace holds, and taken down by whoever waited for it, so that the workspace
+// needs no preparation and a graph that repeats a call finds it as the call did.
+// The cut depends on lengths the host does not know, so every thread block finds
+// its own.
 //
 // Each warp feeds itself: a ring of 2 stages of 4 blocks (2 with 16 columns),
 // filled by bulk copies (a block is one contiguous record) and read as mma.sync
@@ -54,19 +60,12 @@ constexpr float kMost = 128.0f;      // sum of a lane's 2^(x - m) up to which th
 constexpr int kMany = 64;            // columns from which a sequence's rows go to the many-rows kernel
 constexpr float kNegInf = -INFINITY;
 
-// Head of the workspace: what the second kernel needs to know of the cut.
-struct Cut {
-    int workers;                     // parts
-};
-// A worker whose range begins inside an item describes it, and which workers hold the rest.
-struct Split {
-    int units;                       // of the item; 0: the worker begins with an item's first unit
-    int from, to;                    // the workers that hold parts of it
-    int from_slot;                   // which of the first one's two parts is the item's
+// An item whose end a worker holds, but not its beginning.
+struct Join {
+    int active;
+    int from, from_slot;             // the worker that holds the beginning, and which of its two parts that is
     int first_row, rows, tile, head;
 };
-
-constexpr size_t kSplitAt = 256;
 
 // A part of an item: for each (16-row tile of dimensions, column tile) 32 lanes' four accumulators, then
 // 32 lanes' maxima and sums of two columns.
@@ -91,6 +90,26 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
     asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
                  "l"(src), "r"(bytes), "r"(bar)
                  : "memory");
+}
+
+// A flag of 64 bits, raised with a release and awaited, with the limit of every wait here, with an acquire.
+__device__ __forceinline__ void st_release_gpu64(uint64_t* p, uint64_t v) {
+    asm volatile("st.release.gpu.global.b64 [%0], %1;" ::"l"(p), "l"(v) : "memory");
+}
+__device__ __forceinline__ bool flag64_wait(const uint64_t* flag, uint64_t value, volatile int* abort, int* status) {
+    const uint64_t t0 = global_ns();
+    while (true) {
+        uint64_t v;
+        asm volatile("ld.acquire.gpu.global.b64 %0, [%1];" : "=l"(v) : "l"(flag) : "memory");
+        if (v == value) return true;
+        if (*abort) return false;
+        if (global_ns() - t0 > kWaitLimitNs) {
+            *abort = 1;
+            raise_status(status, TP_ERR_TIMEOUT);
+            return false;
+        }
+        __nanosleep(32);
+    }
 }
 
 __device__ __forceinline__ uint4 lds128(uint32_t a) {
@@ -183,6 +202,8 @@ struct Cursor {
     }
 };
 
+__host__ __device__ constexpr size_t flag_bytes(int blocks) { return (static_cast<size_t>(blocks) * kWarps * 2 * 8 + 255) / 256 * 256; }
+
 template <int HD, int NT>
 struct Cfg {
     static constexpr int COLS = 8 * NT;
@@ -246,6 +267,7 @@ __global__ void __launch_bounds__(Cfg<HD, NT>::WARPS * 32, 1) kv4_attention_kern
     __shared__ int stage_mask[WARPS * kStages];
     __shared__ int64_t scan[WARPS], scan_items[WARPS];
     __shared__ Cursor s_cursor[WARPS];
+    __shared__ Join s_join[WARPS];
     __shared__ int s_abort;
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -285,10 +307,7 @@ __global__ void __launch_bounds__(Cfg<HD, NT>::WARPS * 32, 1) kv4_attention_kern
         all_items += scan_items[i];
     }
     before += base - mine;           // units before this thread's sequences
-    if (total == 0) {
-        if (blockIdx.x == 0 && tid == 0) *reinterpret_cast<Cut*>(a.ws) = Cut{0};
-        return;
-    }
+    if (total == 0) return;
     // Warps of a worker: all while the average item has a stage for each, fewer below.  At least a
     // stage for each warp, too, where there are few units in all: fewer parts to join.
     int ws = WARPS;
@@ -325,27 +344,33 @@ __global__ void __launch_bounds__(Cfg<HD, NT>::WARPS * 32, 1) kv4_attention_kern
             c.tile = item / heads;
             c.head = item - c.tile * heads;
             s_cursor[i] = c;
-            Split sp = {};
-            if (c.off > 0) {
+            Join jn = {};
+            if (c.off > 0 && c.off + c.left >= need.units) {
                 const int64_t first = begin - c.off;
-                sp.units = need.units;
-                sp.from = parts.of(first);
-                sp.to = parts.of(first + need.units - 1);
-                sp.from_slot = parts.begin(sp.from) == first ? 0 : 1;
-                sp.first_row = need.first_row;
-                sp.rows = need.rows;
-                sp.tile = c.tile;
-                sp.head = c.head;
+                jn.active = 1;
+                jn.from = parts.of(first);
+                jn.from_slot = parts.begin(jn.from) == first ? 0 : 1;
+                jn.first_row = need.first_row;
+                jn.rows = need.rows;
+                jn.tile = c.tile;
+                jn.head = c.head;
             }
-            reinterpret_cast<Split*>(a.ws + kSplitAt)[w] = sp;
+            s_join[i] = jn;
         }
     }
-    if (blockIdx.x == 0 && tid == 0) *reinterpret_cast<Cut*>(a.ws) = Cut{workers};
     __syncthreads();
 
     const int grp = warp / ws, wi = warp % ws;
     const int worker = grp * gridDim.x + blockIdx.x;
-    float4* slots = reinterpret_cast<float4*>(a.ws + kSplitAt + static_cast<size_t>(gridDim.x) * kWarps * sizeof(Split));
+    // two parts of each worker: the item its range begins in, and the one it ends in
+    uint64_t* flags = reinterpret_cast<uint64_t*>(a.ws);
+    float4* slots = reinterpret_cast<float4*>(a.ws + flag_bytes(gridDim.x));
+    auto together = [&]() {          // the worker's warps
+        if (ws > 1)
+            asm volatile("bar.sync %0, %1;" ::"r"(1 + grp), "r"(ws * 32) : "memory");
+        else
+            __syncwarp();
+    };
 
     Cursor cur = s_cursor[grp];      // the item being computed
     if (cur.left <= 0) return;       // the whole worker
@@ -748,7 +773,9 @@ __global__ void __launch_bounds__(Cfg<HD, NT>::WARPS * 32, 1) kv4_attention_kern
             }
         const bool complete = seg_off == 0 && seg_n == cur.n.units;
         const int head = cur.head, first_row = cur.n.first_row, tile = cur.tile;
-        float4* slot = slots + (static_cast<size_t>(worker) * 2 + (first_segment ? 0 : 1)) * C::PART;
+        const int slot_no = worker * 2 + (first_segment ? 0 : 1);
+        float4* slot = slots + static_cast<size_t>(slot_no) * C::PART;
+        const bool awaited = !complete && seg_off + seg_n < cur.n.units; // by the worker that holds the end
         first_segment = false;
         cur.next(a, COLS, heads);
         const bool more = cur.left > 0;
@@ -764,10 +791,7 @@ __global__ void __launch_bounds__(Cfg<HD, NT>::WARPS * 32, 1) kv4_attention_kern
                     make_float4(acc[nt][i][0], acc[nt][i][1], acc[nt][i][2], acc[nt][i][3]);
             mine_part[(NT * MT + nt) * 32 + lane] = make_float4(mx[nt][0], mx[nt][1], sum[nt][0], sum[nt][1]);
         }
-        if (ws > 1)
-            asm volatile("bar.sync %0, %1;" ::"r"(1 + grp), "r"(ws * 32) : "memory");
-        else
-            __syncwarp();
+        together();
         if (ws > 1 || complete)
             for (int v = wi * 32 + lane; v < NT * MT * 32; v += ws * 32) {
                 float2 top, all;
@@ -780,60 +804,31 @@ __global__ void __launch_bounds__(Cfg<HD, NT>::WARPS * 32, 1) kv4_attention_kern
                         slot[NT * MT * 32 + v / (MT * 32) * 32 + lane] = make_float4(top.x, top.y, all.x, all.y);
                 }
             }
+        if (more || awaited) together();
+        if (awaited && wi == 0 && lane == 0) {
+            __threadfence();
+            st_release_gpu64(flags + slot_no, a.tag);
+        }
         if (!more) break;
-        if (ws > 1)
-            asm volatile("bar.sync %0, %1;" ::"r"(1 + grp), "r"(ws * 32) : "memory");
-        else
-            __syncwarp();
+    }
+    const Join jn = s_join[grp];
+    if (jn.active) {                 // this worker's own part is its first
+        const int count = worker - jn.from + 1;
+        auto slot_of = [&](int i) { return (jn.from + i) * 2 + (i == 0 ? jn.from_slot : 0); };
+        bool have = true;
+        for (int i = wi * 32 + lane; i + 1 < count; i += ws * 32)
+            have = have && flag64_wait(flags + slot_of(i), a.tag, &s_abort, a.seqs.status);
+        together();
+        for (int v = wi * 32 + lane; v < NT * MT * 32; v += ws * 32) {
+            float2 top, all;
+            const float4 o = join_parts<HD, NT>(
+                v, count, [&](int i) { return slots + static_cast<size_t>(slot_of(i)) * C::PART; }, top, all);
+            store_vector<HD, NT>(a, jn.head, jn.first_row, jn.rows * a.group - jn.tile * COLS, jn.tile, v, o, all);
+        }
+        if (have)
+            for (int i = wi * 32 + lane; i + 1 < count; i += ws * 32) flags[slot_of(i)] = 0;
     }
     if (dead) spin_ns(1000000);      // copies that were issued land before the block's memory is given back
-}
-
-// Adds, in order, the parts of an item that several workers hold; the block of
-// the first worker that begins inside the item does it.  Half of the threads
-// take half of the parts each, as the loads' latency is what it takes.
-constexpr int kJoinHalves = 2;
-template <int HD, int NT>
-__global__ void __launch_bounds__(kJoinHalves * 256) kv4_attention_join_kernel(const __grid_constant__ AttnArgs a) {
-    constexpr int COLS = 8 * NT, MT = HD / 16, PART = slot_vectors(NT, HD);
-    __shared__ float4 s_o[256], s_st[256];
-    pdl_wait();
-    pdl_trigger();
-    const int tid = threadIdx.x & 255, half = threadIdx.x >> 8;
-    const int workers = reinterpret_cast<const Cut*>(a.ws)->workers;
-    const float4* slots =
-        reinterpret_cast<const float4*>(a.ws + kSplitAt + static_cast<size_t>(gridDim.x) * kWarps * sizeof(Split));
-    for (int b = blockIdx.x; b < workers; b += gridDim.x) {
-        const Split sp = reinterpret_cast<const Split*>(a.ws + kSplitAt)[b];
-        if (sp.units == 0 || sp.from != b - 1) continue;
-        const int cols = sp.rows * a.group - sp.tile * COLS, count = sp.to - sp.from + 1;
-        const int lo = half * ((count + 1) / 2), n = half ? count - lo : (count + 1) / 2;
-        for (int v0 = 0; v0 < NT * MT * 32; v0 += 256) {
-            const int v = v0 + tid;
-            float2 top = make_float2(kNegInf, kNegInf), all = make_float2(0.0f, 0.0f);
-            float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-            if (v < NT * MT * 32)
-                o = join_parts<HD, NT>(
-                    v, n,
-                    [&](int i) {
-                        return slots + (static_cast<size_t>(sp.from + lo + i) * 2 + (lo + i == 0 ? sp.from_slot : 0)) * PART;
-                    },
-                    top, all);
-            if (half) s_o[tid] = o, s_st[tid] = make_float4(top.x, top.y, all.x, all.y);
-            __syncthreads();
-            if (!half && v < NT * MT * 32) {
-                const float4 st = s_st[tid], x = s_o[tid];
-                const float2 m = make_float2(fmaxf(top.x, st.x), fmaxf(top.y, st.y));
-                const float2 c = make_float2(m.x == kNegInf ? 0.0f : m.x, m.y == kNegInf ? 0.0f : m.y);
-                const float2 fa = make_float2(ex2(top.x - c.x), ex2(top.y - c.y)), fb = make_float2(ex2(st.x - c.x), ex2(st.y - c.y));
-                all = make_float2(all.x * fa.x + st.z * fb.x, all.y * fa.y + st.w * fb.y);
-                o = make_float4(o.x * fa.x + x.x * fb.x, o.y * fa.y + x.y * fb.y, o.z * fa.x + x.z * fb.x,
-                                o.w * fa.y + x.w * fb.y);
-                store_vector<HD, NT>(a, sp.head, sp.first_row, cols, sp.tile, v, o, all);
-            }
-            __syncthreads();
-        }
-    }
 }
 
 template <int HD, int NT>
@@ -843,8 +838,6 @@ tp_status launch_few(const AttnArgs& a, int sms, cudaStream_t stream) {
     auto* kern = kv4_attention_kernel<HD, NT>;
     if (!smem_attribute_once(reinterpret_cast<const void*>(kern), C::SMEM, smem_set)) return TP_ERR_CUDA;
     if (launch_pdl(kern, dim3(sms), dim3(C::WARPS * 32), C::SMEM, stream, a) != cudaSuccess) return TP_ERR_CUDA;
-    if (launch_pdl(kv4_attention_join_kernel<HD, NT>, dim3(sms), dim3(kJoinHalves * 256), 0, stream, a) != cudaSuccess)
-        return TP_ERR_CUDA;
     return TP_OK;
 }
 
@@ -852,9 +845,9 @@ tp_status launch_few(const AttnArgs& a, int sms, cudaStream_t stream) {
 
 size_t kv4_attention_workspace(int t, int64_t n, int64_t nseq, int heads, int kv_heads, int head_dim) {
     (void)t, (void)n, (void)nseq, (void)heads, (void)kv_heads;
-    // two parts for each of the workers that an SM can have: 16 with 8 columns, 8 with 16
-    const size_t workers = static_cast<size_t>(std::max(device_sms(), 160)) * kWarps;
-    return kSplitAt + workers * (sizeof(Split) + 2 * slot_vectors(1, head_dim) * sizeof(float4));
+    // two parts for each of the workers that an SM can have
+    const int sms = std::max(device_sms(), 160);
+    return flag_bytes(sms) + static_cast<size_t>(sms) * kWarps * 2 * slot_vectors(2, head_dim) * sizeof(float4);
 }
 
 tp_status launch_kv4_attention(const KvAttentionDesc& d, cudaStream_t stream) {
@@ -872,6 +865,9 @@ tp_status launch_kv4_attention(const KvAttentionDesc& d, cudaStream_t stream) {
     a.window = d.window;
     a.sinks = d.sinks;
     a.ws = static_cast<uint8_t*>(d.ws);
+    // numbers of calls begin at one that memory does not hold by chance
+    static std::atomic<uint64_t> calls{0x9e3779b97f4a7c15ull ^ static_cast<uint64_t>(reinterpret_cast<uintptr_t>(&calls))};
+    a.tag = calls.fetch_add(1, std::memory_order_relaxed) | 1ull << 63;
     // Sequences with at least kMany columns go to the many-rows kernel (none can without cu_rows).
     a.many = kMany;
     if (d.seqs.cu_rows != nullptr && static_cast<int64_t>(d.seqs.n) * d.group >= kMany) {
@@ -880,7 +876,7 @@ tp_status launch_kv4_attention(const KvAttentionDesc& d, cudaStream_t stream) {
     }
     if (d.seqs.cu_rows == nullptr) a.many = INT32_MAX;
     const int sms = device_sms();
-    if (sms <= 0 || sms > 160) return TP_ERR_CUDA;
+    if (sms <= 0 || sms > 160) return TP_ERR_CUDA;   // the workspace size is asked for without a device too
     // 16 columns per tile when a sequence's rows fill more than 8
     const bool wide = d.group > 8 || (d.seqs.cu_rows != nullptr && d.group * (d.seqs.n / std::max(d.seqs.nseq, 1)) > 8);
     if (d.head_dim == 128) return wide ? launch_few<128, 2>(a, sms, stream) : launch_few<128, 1>(a, sms, stream);

@@ -17,6 +17,7 @@ struct AttnArgs {
     int window, sinks;
     int many;                        // columns (rows * group) from which a sequence goes to the many-rows kernel
     uint8_t* ws;
+    uint64_t tag;                    // number of the call, never 0
 };
 
 __device__ __forceinline__ float ex2(float x) {
