@@ -336,6 +336,8 @@ tp_status tp_beam_select(int t, int64_t items, int beams, int k, const int64_t* 
     TP_CHECK(vocab >= 1, TP_ERR_INVALID_ARG);
     TP_CHECK(vocab <= INT32_MAX, TP_ERR_UNSUPPORTED);
     TP_CHECK(finished == nullptr || (eos >= 0 && eos < vocab), TP_ERR_INVALID_ARG);
+    // candidates of an item are counted in 32 bits
+    TP_CHECK(vocab / 4096 * beams * k <= INT32_MAX / 4, TP_ERR_UNSUPPORTED);
     TP_CHECK(items == 0 || (scores != nullptr && scores_out != nullptr && rows_out != nullptr && tokens_out != nullptr),
              TP_ERR_INVALID_ARG);
     if (items == 0) return TP_OK;

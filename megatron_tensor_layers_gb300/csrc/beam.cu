@@ -3,8 +3,9 @@
 //
 // First kernel, one thread block per (row, slice of a shard), which walks its
 // slice 4096 logits at a time, the next ones already on their way.  Each thread
-// keeps a running maximum and the sum of exponentials under it (fp32; the
-// threads' sums are added in fp64).  A logit and its token make one 64-bit key,
+// keeps a running maximum and the sum of exponentials under it (fp32, an
+// exponential from ex2; what joins sums under different maxima is expf, so that
+// errors do not pile up; the threads' sums are added in fp64).  A logit and its token make one 64-bit key,
 // larger for a larger logit and, among equals, for a lower token, so the k best
 // are unique.  The k-th largest of 64 group maxima (a group is 4 threads) of the
 // first 4096 is a lower bound of the k-th largest of the slice; what is not
@@ -16,7 +17,9 @@
 //
 // Second kernel, one thread block per item: the log-sum-exp of each beam from
 // its slices, then the k best of all beams' candidates by the fp64 sum
-// score - lse + logit, the same way.
+// score - lse + logit, the same way.  It is a chain of latencies; fp64 is slow
+// here (16 cycles an instruction and warp), so a beam takes one logarithm
+// in it and no exponential.
 #include <algorithm>
 
 #include "kv4.cuh"
@@ -31,8 +34,8 @@ constexpr int kRoom = 512;           // candidates that are ranked by counting
 static_assert(kGroups >= TP_MAX_BEAMS, "the bound needs as many groups as there are results");
 
 struct Slice {
-    double sum;
-    float top;
+    double sum;                      // of e^(x - top)
+    float top;                       // -inf: nothing but -inf (and perhaps NaN)
     int pad;
 };
 
@@ -68,19 +71,16 @@ __device__ __forceinline__ double unordered64(uint64_t o) {
     return __longlong_as_double(static_cast<int64_t>(o >> 63 ? o ^ 0x8000000000000000ull : ~o));
 }
 
-// The k-th largest (k >= 1) of the 64 group maxima in `group`, for every thread of a warp; 0 is "none".
+// The k-th largest (k >= 1) of the 64 group maxima in `group`, into *out, by the first 64 threads; 0 is "none".
+// The block synchronises before and after.
 template <typename T>
-__device__ __forceinline__ T kth_of_groups(const T* group, int k, int lane) {
-    const T a = group[lane], b = group[lane + 32];
-    int ra = 0, rb = 0;              // how many are before it (ties by place)
-#pragma unroll 8
-    for (int i = 0; i < 32; ++i) {
-        const T u = __shfl_sync(0xffffffffu, a, i), v = __shfl_sync(0xffffffffu, b, i);
-        ra += (u > a || (u == a && i < lane)) + (v > a);
-        rb += (u >= b) + (v > b || (v == b && i < lane));
-    }
-    const uint32_t ha = __ballot_sync(0xffffffffu, ra == k - 1), hb = __ballot_sync(0xffffffffu, rb == k - 1);
-    return ha ? __shfl_sync(0xffffffffu, a, __ffs(ha) - 1) : __shfl_sync(0xffffffffu, b, __ffs(hb) - 1);
+__device__ __forceinline__ void kth_of_groups(const T* group, int k, int tid, T* out) {
+    if (tid >= kGroups) return;
+    const T mine = group[tid];
+    int before = 0;                  // ties by place
+#pragma unroll 16
+    for (int i = 0; i < kGroups; ++i) before += group[i] > mine || (group[i] == mine && i < tid);
+    if (before == k - 1) *out = mine;
 }
 
 // Group maxima of the threads' values: threads 4g .. 4g + 3 are group g.
@@ -110,6 +110,9 @@ __device__ __forceinline__ uint64_t block_max64(uint64_t v, uint64_t* tmp, int t
 constexpr int kChunk = 16;           // logits of a thread in one go
 constexpr float kLog2e = 1.4426950408889634f;
 
+// What a sum under maximum `from` is worth under `to` >= from: times this (0 for a sum of nothing).
+__device__ __forceinline__ float carried(float from, float to) { return from == -INFINITY ? 0.0f : expf(from - to); }
+
 __device__ __forceinline__ float ex2(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -122,7 +125,7 @@ __global__ void __launch_bounds__(kThreads) beam_slice_kernel(const __grid_const
     constexpr uint32_t NONE = F32 ? 0xff800000u : 0xff80ff80u;           // -inf
     __shared__ float s_top[kWarps];
     __shared__ double s_sum[kWarps];
-    __shared__ uint32_t s_group[kGroups];
+    __shared__ uint32_t s_group[kGroups], s_bound;
     __shared__ uint64_t s_cand[kRoom], s_best[TP_MAX_BEAMS];
     __shared__ uint64_t s_tmp[kWarps];
     __shared__ int s_count;
@@ -207,16 +210,24 @@ __global__ void __launch_bounds__(kThreads) beam_slice_kernel(const __grid_const
         float best = x[0];
 #pragma unroll
         for (int i = 1; i < kChunk; ++i) best = fmaxf(best, x[i]);
-        const float m_new = fmaxf(m, best), b = m_new == -INFINITY ? 0.0f : m_new;
-        s *= ex2((m - b) * kLog2e);
-        m = m_new;
+        if (best > m) {
+            s *= m == -INFINITY ? 1.0f : expf(m - best);                 // a sum of nothing is 0, or NaN
+            m = best;
+        }
+        const float base = m == -INFINITY ? 0.0f : m;
+        float s1 = 0.0f;
 #pragma unroll
-        for (int i = 0; i < kChunk; ++i) s += ex2((x[i] - b) * kLog2e);  // NaN and +inf make it NaN
+        for (int i = 0; i < kChunk; i += 2) {                            // NaN and +inf make it NaN
+            s += ex2((x[i] - base) * kLog2e);
+            s1 += ex2((x[i + 1] - base) * kLog2e);
+        }
+        s += s1;
         if (c == 0) {
             group_max(best > -INFINITY ? ordered(best) : 0u, s_group, tid);
             __syncthreads();
-            const uint32_t o = kth_of_groups(s_group, a.k, lane);
-            bound = o == 0 ? -INFINITY : unordered(o);
+            kth_of_groups(s_group, a.k, tid, &s_bound);
+            __syncthreads();
+            bound = s_bound == 0 ? -INFINITY : unordered(s_bound);
         }
         if (best >= bound) {
 #pragma unroll
@@ -250,7 +261,7 @@ __global__ void __launch_bounds__(kThreads) beam_slice_kernel(const __grid_const
     top = s_top[0];
 #pragma unroll
     for (int i = 1; i < kWarps; ++i) top = fmaxf(top, s_top[i]);
-    double sum = static_cast<double>(s * ex2((m - (top == -INFINITY ? 0.0f : top)) * kLog2e));
+    double sum = s * carried(m, top);            // NaN stays
 #pragma unroll
     for (int i = 16; i >= 1; i >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, i);
     if (lane == 0) s_sum[warp] = sum;
@@ -299,79 +310,97 @@ __device__ __forceinline__ bool before(const Cand& a, const Cand& b) {
 
 __global__ void __launch_bounds__(kThreads) beam_pick_kernel(const __grid_constant__ BeamArgs a) {
     __shared__ double s_add[TP_MAX_BEAMS];       // score - lse; NaN: no continuations
-    __shared__ uint64_t s_group[kGroups];
+    __shared__ uint64_t s_group[kGroups], s_bound;
     __shared__ Cand s_cand[kRoom];
     __shared__ Cand s_best[kWarps];
+    __shared__ float s_top[TP_MAX_BEAMS];
     __shared__ int s_count;
     pdl_wait();
     pdl_trigger();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int item = blockIdx.x;
     const int64_t row0 = static_cast<int64_t>(item) * a.beams;
+    auto done = [&](int b) { return a.finished != nullptr && a.finished[row0 + b] != 0; };
     if (tid == 0) s_count = 0;
+    // this thread's candidates, the first few of which it keeps: a key of a beam's slice each; a finished
+    // beam has its first alone
+    const int per_beam = a.slices * a.k, n = a.beams * per_beam;
+    constexpr int KEEP = 8;
+    uint64_t key[KEEP];
+#pragma unroll
+    for (int j = 0; j < KEEP; ++j) {
+        const int i = tid + j * kThreads;
+        key[j] = i < n ? a.keys[row0 * per_beam + i] : 0;
+    }
     for (int b = warp; b < a.beams; b += kWarps) {
-        const float score = a.scores[row0 + b];
-        double add = __longlong_as_double(0x7ff8000000000000ll);
-        if (a.finished != nullptr && a.finished[row0 + b] != 0) {
-            if (score > -INFINITY) add = score;
-        } else {
-            const Slice* st = a.stats + (row0 + b) * a.slices;
-            float top = -INFINITY;
-            for (int i = lane; i < a.slices; i += 32) top = fmaxf(top, st[i].top);
-#pragma unroll
-            for (int m = 16; m >= 1; m >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, m));
-            double sum = 0.0;
-            for (int i = lane; i < a.slices; i += 32) {
-                const Slice s = st[i];
-                if (s.top > -INFINITY)
-                    sum += s.sum * exp(static_cast<double>(s.top) - top);
-                else
-                    sum += s.sum;                // 0, or NaN
-            }
-#pragma unroll
-            for (int m = 16; m >= 1; m >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, m);
-            const double lse = top + log(sum);
-            if (score > -INFINITY && lse > -INFINITY && lse < INFINITY) add = score - lse;
+        if (done(b)) continue;
+        const Slice* st = a.stats + (row0 + b) * a.slices;
+        Slice mine{0.0, -INFINITY, 0};
+        if (lane < a.slices) mine = st[lane];
+        for (int i = lane + 32; i < a.slices; i += 32) {
+            const Slice o = st[i];
+            const float up = fmaxf(mine.top, o.top);
+            mine.sum = mine.sum * carried(mine.top, up) + o.sum * carried(o.top, up);
+            mine.top = up;
         }
-        if (lane == 0) s_add[b] = add;
+        float top = mine.top;
+#pragma unroll
+        for (int m = 16; m >= 1; m >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, m));
+        double sum = mine.sum * carried(mine.top, top);
+#pragma unroll
+        for (int m = 16; m >= 1; m >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, m);
+        if (lane == 0) s_add[b] = sum, s_top[b] = top;
     }
     __syncthreads();
-    const int per_beam = a.slices * a.k;
-    const int64_t n = static_cast<int64_t>(a.beams) * per_beam;
-    // candidate i of the item: a key of a beam's slice; a finished beam has its first alone
-    auto cand = [&](int64_t i) {
+    for (int b = tid; b < a.beams; b += kThreads) {
+        const float score = a.scores[row0 + b];
+        double add = __longlong_as_double(0x7ff8000000000000ll);
+        if (done(b)) {
+            if (score > -INFINITY) add = score;
+        } else if (score > -INFINITY) {
+            const double lse = s_top[b] + log(s_add[b]);
+            if (lse > -INFINITY && lse < INFINITY) add = score - lse;
+        }
+        s_add[b] = add;
+    }
+    __syncthreads();
+    auto cand = [&](int i, uint64_t k64) {
         Cand c{0, 0};
-        const int b = static_cast<int>(i / per_beam), j = static_cast<int>(i - static_cast<int64_t>(b) * per_beam);
+        const uint32_t b = static_cast<uint32_t>(i) / static_cast<uint32_t>(per_beam);
         const double add = s_add[b];
         if (!(add == add)) return c;
-        if (a.finished != nullptr && a.finished[row0 + b] != 0) {
-            if (j != 0) return c;
+        if (done(b)) {
+            if (i != static_cast<int>(b) * per_beam) return c;
             c.score = ordered64(add);
             c.flat = static_cast<uint64_t>(b) * a.vocab + static_cast<uint32_t>(a.eos);
             return c;
         }
-        const uint64_t key = a.keys[(row0 + b) * per_beam + j];
-        if (key == 0) return c;
-        c.score = ordered64(add + static_cast<double>(unordered(static_cast<uint32_t>(key >> 32))));
-        c.flat = static_cast<uint64_t>(b) * a.vocab + (0xffffffffu - static_cast<uint32_t>(key));
+        if (k64 == 0) return c;
+        c.score = ordered64(add + static_cast<double>(unordered(static_cast<uint32_t>(k64 >> 32))));
+        c.flat = static_cast<uint64_t>(b) * a.vocab + (0xffffffffu - static_cast<uint32_t>(k64));
         return c;
     };
+    // f(candidate) for all of this thread's
+    auto each = [&](auto f) {
+#pragma unroll
+        for (int j = 0; j < KEEP; ++j)
+            if (tid + j * kThreads < n) f(cand(tid + j * kThreads, key[j]));
+        for (int i = tid + KEEP * kThreads; i < n; i += kThreads) f(cand(i, a.keys[row0 * per_beam + i]));
+    };
     uint64_t best = 0;
-    for (int64_t i = tid; i < n; i += kThreads) {
-        const uint64_t s = cand(i).score;
-        best = best > s ? best : s;
-    }
+    each([&](const Cand& c) { best = best > c.score ? best : c.score; });
     group_max(best, s_group, tid);
     __syncthreads();
-    const uint64_t kth = kth_of_groups(s_group, a.k, lane), bound = kth > 1 ? kth : 1;
+    kth_of_groups(s_group, a.k, tid, &s_bound);
+    __syncthreads();
+    const uint64_t bound = s_bound > 1 ? s_bound : 1;
     if (best >= bound)
-        for (int64_t i = tid; i < n; i += kThreads) {
-            const Cand c = cand(i);
+        each([&](const Cand& c) {
             if (c.score >= bound) {
                 const int at = atomicAdd(&s_count, 1);
                 if (at < kRoom) s_cand[at] = c;
             }
-        }
+        });
     __syncthreads();
     const int count = s_count;
     const int64_t out = static_cast<int64_t>(item) * a.k;
@@ -394,10 +423,9 @@ __global__ void __launch_bounds__(kThreads) beam_pick_kernel(const __grid_consta
     Cand last{~0ull, 0};
     for (int m = 0; m < a.k; ++m) {
         Cand mine{0, ~0ull};
-        for (int64_t i = tid; i < n; i += kThreads) {
-            const Cand c = cand(i);
+        each([&](const Cand& c) {
             if (c.score != 0 && before(last, c) && before(c, mine)) mine = c;
-        }
+        });
 #pragma unroll
         for (int s = 16; s >= 1; s >>= 1) {
             const Cand o{__shfl_xor_sync(0xffffffffu, mine.score, s), __shfl_xor_sync(0xffffffffu, mine.flat, s)};
