@@ -153,12 +153,6 @@ __device__ __forceinline__ Need seq_need(const AttnArgs& a, int s, int cols_per_
     return n;
 }
 
-// a / b for a >= 0, b > 0: 32-bit division where it will do (a 64-bit one takes a hundred instructions).
-__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
-    if (((a | b) >> 32) == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
-    return a / b;
-}
-
 // The line of `total` units in `workers` <= total equal parts; the first `more` hold one unit more.
 struct Parts {
     int64_t each;

@@ -1,22 +1,27 @@
 // Beam selection over vocab-sharded logits: one pass over the logits, bound by
 // reading them.
 //
-// First kernel, one thread block per (row, slice of a shard), which walks its
-// slice 4096 logits at a time, the next ones already on their way.  Each thread
-// keeps a running maximum and the sum of exponentials under it (fp32, an
-// exponential from ex2; what joins sums under different maxima is expf, so that
-// errors do not pile up; the threads' sums are added in fp64).  A logit and its token make one 64-bit key,
-// larger for a larger logit and, among equals, for a lower token, so the k best
-// are unique.  The k-th largest of 64 group maxima (a group is 4 threads) of the
-// first 4096 is a lower bound of the k-th largest of the slice; what is not
-// below it goes to shared memory, a few logits in a hundred threads' worth, so
-// the pass costs one comparison per thread and 16 logits.  When the room fills
-// up, the k best are found by counting and the bound rises to the last of them.
+// First kernel: the logits of all rows are one line of chunks of 4096, cut into
+// equal parts, one for each thread block that fits; a block's part of a row is a
+// piece.  A ninth warp brings the chunks by bulk copies into a ring of three, so
+// that two are on their way while one is worked on (128 KB for an SM; loads into
+// registers, one chunk ahead in blocks of one row each, took 40 us for 136 MB,
+// and a thread of the eight that also issues the copies holds up all of them).
+// Each thread keeps a running maximum and the sum of exponentials
+// under it (fp32, an exponential from ex2; what joins sums under different
+// maxima is expf, so that errors do not pile up; the threads' sums are added in
+// fp64).  A logit and its token make one 64-bit key, larger for a larger logit
+// and, among equals, for a lower token, so the k best are unique.  The k-th
+// largest of 64 group maxima (a group is 4 threads) of a piece's first chunk is
+// a lower bound of the k-th largest of the piece; what is not below it goes to
+// shared memory, so the pass costs one comparison per thread and 16 logits.  As
+// the piece goes on, the k best so far are found by counting and the bound rises
+// to the last of them: 40 candidates instead of 145 for k = 8 in 17 chunks.
 // Where more than kRoom at once are not below the bound (many equal logits), k
-// rounds of a block-wide maximum over the slice find them instead.
+// rounds of a block-wide maximum over the piece find them instead.
 //
 // Second kernel, one thread block per item: the log-sum-exp of each beam from
-// its slices, then the k best of all beams' candidates by the fp64 sum
+// its pieces, then the k best of all beams' candidates by the fp64 sum
 // score - lse + logit, the same way.  It is a chain of latencies; fp64 is slow
 // here (16 cycles an instruction and warp), so a beam takes one logarithm
 // in it and no exponential.
@@ -33,7 +38,7 @@ constexpr int kGroups = 64;
 constexpr int kRoom = 512;           // candidates that are ranked by counting
 static_assert(kGroups >= TP_MAX_BEAMS, "the bound needs as many groups as there are results");
 
-struct Slice {
+struct Piece {
     double sum;                      // of e^(x - top)
     float top;                       // -inf: nothing but -inf (and perhaps NaN)
     int pad;
@@ -42,8 +47,11 @@ struct Slice {
 struct BeamArgs {
     const void* logits[TP_MAX_SHARDS];
     int64_t cols[TP_MAX_SHARDS], ldl[TP_MAX_SHARDS], start[TP_MAX_SHARDS];
-    int first_slice[TP_MAX_SHARDS + 1];  // slices of a row, by shard
-    int t, items, beams, k, slices, chunks;
+    int first_chunk[TP_MAX_SHARDS + 1];  // chunks of a row, by shard
+    int t, items, beams, k;
+    int chunks;                      // of a row
+    int blocks;                      // parts of the line
+    int most;                        // pieces that a row can have
     int64_t vocab;
     const float* scores;
     const uint8_t* finished;
@@ -51,8 +59,24 @@ struct BeamArgs {
     float* scores_out;
     int32_t* rows_out;
     int32_t* tokens_out;
-    Slice* stats;                    // [rows, slices]
-    uint64_t* keys;                  // [rows, slices, k], best first, 0 where there are fewer
+    Piece* stats;                    // [rows, most]
+    uint64_t* keys;                  // [rows, most, k], best first, 0 where there are fewer
+    int* status;
+};
+
+// The line of rows * chunks chunks in `blocks` equal parts; the first `more` hold one more.
+struct Line {
+    int64_t each, more;
+    __device__ __forceinline__ explicit Line(const BeamArgs& a) {
+        const int64_t total = static_cast<int64_t>(a.items) * a.beams * a.chunks;
+        each = quotient(total, a.blocks);
+        more = total - each * a.blocks;
+    }
+    __device__ __forceinline__ int64_t begin(int b) const { return each * b + min(static_cast<int64_t>(b), more); }
+    __device__ __forceinline__ int of(int64_t i) const {
+        const int64_t front = (each + 1) * more;
+        return static_cast<int>(i < front ? quotient(i, each + 1) : more + quotient(i - front, each));
+    }
 };
 
 // Order-preserving map of a float (not NaN; -0 as +0) to 32 bits.
@@ -78,8 +102,16 @@ __device__ __forceinline__ void kth_of_groups(const T* group, int k, int tid, T*
     if (tid >= kGroups) return;
     const T mine = group[tid];
     int before = 0;                  // ties by place
-#pragma unroll 16
-    for (int i = 0; i < kGroups; ++i) before += group[i] > mine || (group[i] == mine && i < tid);
+    struct alignas(16) Some {        // one 16-byte read
+        T v[16 / sizeof(T)];
+    };
+    constexpr int PER = 16 / sizeof(T);
+#pragma unroll
+    for (int i = 0; i < kGroups; i += PER) {
+        const Some g = *reinterpret_cast<const Some*>(group + i);
+#pragma unroll
+        for (int j = 0; j < PER; ++j) before += g.v[j] > mine || (g.v[j] == mine && i + j < tid);
+    }
     if (before == k - 1) *out = mine;
 }
 
@@ -93,15 +125,18 @@ __device__ __forceinline__ void group_max(T v, T* group, int tid) {
     if ((tid & 3) == 0) group[tid >> 2] = v;
 }
 
+// The barrier of the kThreads threads that compute.
+__device__ __forceinline__ void sync_all() { asm volatile("bar.sync 1, %0;" ::"n"(kThreads) : "memory"); }
+
 __device__ __forceinline__ uint64_t block_max64(uint64_t v, uint64_t* tmp, int tid) {
 #pragma unroll
     for (int m = 16; m >= 1; m >>= 1) {
         const uint64_t o = __shfl_xor_sync(0xffffffffu, v, m);
         v = v > o ? v : o;
     }
-    __syncthreads();
+    sync_all();
     if ((tid & 31) == 0) tmp[tid >> 5] = v;
-    __syncthreads();
+    sync_all();
     v = tmp[0];
     for (int i = 1; i < kWarps; ++i) v = v > tmp[i] ? v : tmp[i];
     return v;
@@ -113,59 +148,100 @@ constexpr float kLog2e = 1.4426950408889634f;
 // What a sum under maximum `from` is worth under `to` >= from: times this (0 for a sum of nothing).
 __device__ __forceinline__ float carried(float from, float to) { return from == -INFINITY ? 0.0f : expf(from - to); }
 
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ uint64_t pack2(float lo, float hi) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ void unpack2(uint64_t v, float& lo, float& hi) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+
 __device__ __forceinline__ float ex2(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
 
+constexpr int kAtOnce = 4;           // blocks of an SM
+constexpr int kRing = 3;
+
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+                 "l"(src), "r"(bytes), "r"(bar)
+                 : "memory");
+}
+
 template <bool F32>
-__global__ void __launch_bounds__(kThreads) beam_slice_kernel(const __grid_constant__ BeamArgs a) {
+__global__ void __launch_bounds__(kThreads + 32, kAtOnce) beam_scan_kernel(const __grid_constant__ BeamArgs a) {
     constexpr int VEC = F32 ? 4 : 8, NV = kChunk / VEC, ES = F32 ? 4 : 2;
     constexpr uint32_t NONE = F32 ? 0xff800000u : 0xff80ff80u;           // -inf
+    constexpr int WORDS = kThreads * NV;
+    extern __shared__ __align__(128) uint4 ring[];                       // [kRing][WORDS]
+    __shared__ __align__(8) uint64_t full[kRing], empty[kRing];
+    __shared__ int3 s_place[kRing];              // token of the first element, first and one past the last whole word
+    __shared__ int s_abort;
     __shared__ float s_top[kWarps];
     __shared__ double s_sum[kWarps];
-    __shared__ uint32_t s_group[kGroups], s_bound;
-    __shared__ uint64_t s_cand[kRoom], s_best[TP_MAX_BEAMS];
+    __shared__ __align__(16) uint32_t s_group[kGroups];
+    __shared__ uint32_t s_bound;
+    __shared__ __align__(16) uint64_t s_cand[kRoom + 2];
+    __shared__ uint64_t s_best[TP_MAX_BEAMS];
     __shared__ uint64_t s_tmp[kWarps];
     __shared__ int s_count;
     pdl_wait();
     pdl_trigger();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int row = blockIdx.x / a.slices, slice = blockIdx.x - row * a.slices;
-    if (a.finished != nullptr && a.finished[row] != 0) return;   // its logits do not matter
-    int r = 0;
-    while (slice >= a.first_slice[r + 1]) ++r;
-    const int64_t cols = a.cols[r];
-    const uint8_t* base = static_cast<const uint8_t*>(a.logits[r]) + row * a.ldl[r] * ES;
-    // 16-byte words counted from the one that holds the row's first element
-    const int off = static_cast<int>((reinterpret_cast<uintptr_t>(base) & 15u) / ES);
-    const int64_t word0 = static_cast<int64_t>(slice - a.first_slice[r]) * a.chunks * (kThreads * NV);
-    const int64_t words = (off + cols + VEC - 1) / VEC - word0;  // of the row from this slice on
-    const int chunks = static_cast<int>(min(static_cast<int64_t>(a.chunks), (words + kThreads * NV - 1) / (kThreads * NV)));
-    // column of the first element of this thread's word j of a chunk
-    auto column = [&](int chunk, int j) { return (word0 + static_cast<int64_t>(chunk * NV + j) * kThreads + tid) * VEC - off; };
-    auto load = [&](int chunk, uint4 (&w)[NV]) {
+    const Line line(a);
+    const int64_t begin = line.begin(blockIdx.x), end = line.begin(blockIdx.x + 1);
+
+    auto done = [&](int row) { return a.finished != nullptr && a.finished[row] != 0; };   // its logits do not matter
+    // Chunk c of a row: where its first word is (whose first elements a row that begins inside a word does not
+    // have), in columns of its shard, and which words lie in the row whole.
+    struct Place {
+        const uint8_t* base;                     // the row
+        int64_t cols, first;
+        int token, lo, hi;
+    };
+    auto place = [&](int row, int c) {
+        int r = 0;
+        while (c >= a.first_chunk[r + 1]) ++r;
+        Place p;
+        p.cols = a.cols[r];
+        p.base = static_cast<const uint8_t*>(a.logits[r]) + row * a.ldl[r] * ES;
+        const int off = static_cast<int>((reinterpret_cast<uintptr_t>(p.base) & 15u) / ES);
+        p.first = static_cast<int64_t>(c - a.first_chunk[r]) * (kThreads * kChunk) - off;
+        p.token = static_cast<int>(a.start[r] + p.first);
+        p.lo = p.first < 0 ? 1 : 0;
+        p.hi = static_cast<int>(max(static_cast<int64_t>(p.lo), min(static_cast<int64_t>(WORDS), (p.cols - p.first) / VEC)));
+        return p;
+    };
+    // a word that the row's edge cuts, or one outside, element by element
+    auto edge_word = [&](const Place& p, int word) {
+        const int64_t col = p.first + word * VEC;
+        uint32_t v[4] = {NONE, NONE, NONE, NONE};
 #pragma unroll
-        for (int j = 0; j < NV; ++j) {
-            const int64_t c = column(chunk, j);
-            if (c >= 0 && c + VEC <= cols) {
-                w[j] = __ldg(reinterpret_cast<const uint4*>(base + c * ES));
-            } else {                             // a word that the row's edge cuts, or one outside
-                uint32_t v[4] = {NONE, NONE, NONE, NONE};
-#pragma unroll
-                for (int e = 0; e < VEC; ++e)
-                    if (c + e >= 0 && c + e < cols) {
-                        if constexpr (F32) {
-                            v[e] = reinterpret_cast<const uint32_t*>(base)[c + e];
-                        } else {
-                            const uint32_t h = reinterpret_cast<const uint16_t*>(base)[c + e];
-                            v[e / 2] = e & 1 ? (v[e / 2] & 0xffffu) | h << 16 : (v[e / 2] & 0xffff0000u) | h;
-                        }
-                    }
-                w[j] = make_uint4(v[0], v[1], v[2], v[3]);
+        for (int e = 0; e < VEC; ++e)
+            if (col + e >= 0 && col + e < p.cols) {
+                if constexpr (F32) {
+                    v[e] = reinterpret_cast<const uint32_t*>(p.base)[col + e];
+                } else {
+                    const uint32_t h = reinterpret_cast<const uint16_t*>(p.base)[col + e];
+                    v[e / 2] = e & 1 ? (v[e / 2] & 0xffffu) | h << 16 : (v[e / 2] & 0xffff0000u) | h;
+                }
             }
-        }
+        return make_uint4(v[0], v[1], v[2], v[3]);
     };
     auto values = [&](const uint4 (&w)[NV], float (&x)[kChunk]) {
 #pragma unroll
@@ -182,233 +258,340 @@ __global__ void __launch_bounds__(kThreads) beam_slice_kernel(const __grid_const
             }
         }
     };
-    auto key = [&](int chunk, int i, float x) {
+    auto key = [&](int token, int i, float x) {
         return (static_cast<uint64_t>(ordered(x)) << 32) |
-               (0xffffffffu - static_cast<uint32_t>(a.start[r] + column(chunk, i / VEC) + i % VEC));
+               (0xffffffffu - static_cast<uint32_t>(token + i / VEC * kThreads * VEC + i % VEC));
     };
-    // the k best of the candidates, in order, into s_best (0 where there are fewer)
+    // the k best of the candidates, in order, into s_best (0 where there are fewer); up to 128 of them are counted
+    // against by two threads each
     auto rank = [&](int count) {
-        for (int i = tid; i < count; i += kThreads) {
-            const uint64_t mine = s_cand[i];
+        if (tid < 2) s_cand[count + tid] = 0;    // read in pairs
+        sync_all();
+        const int both = count <= kThreads / 2 ? 1 : 0, pairs = (count + 1) / 2;
+        for (int i = tid >> both; i < ((count + 31) & ~31); i += kThreads >> both) {
+            const uint64_t mine = i < count ? s_cand[i] : ~0ull;
+            const int lo = both && (tid & 1) ? pairs / 2 : 0, hi = both && !(tid & 1) ? pairs / 2 : pairs;
             int before = 0;
-            for (int j = 0; j < count; ++j) before += s_cand[j] > mine;
-            if (before < a.k) s_best[before] = mine;
+#pragma unroll 8
+            for (int j = lo; j < hi; ++j) {
+                const ulonglong2 v = *reinterpret_cast<const ulonglong2*>(s_cand + 2 * j);
+                before += (v.x > mine) + (v.y > mine);
+            }
+            if (both) before += __shfl_xor_sync(0xffffffffu, before, 1);
+            if (i < count && before < a.k) s_best[before] = mine;
         }
         for (int i = count + tid; i < a.k; i += kThreads) s_best[i] = 0;
-        __syncthreads();
+        sync_all();
     };
-    if (tid == 0) s_count = 0;
-    uint4 next[NV];
-    load(0, next);
-    float m = -INFINITY, s = 0.0f;
-    float bound = -INFINITY;
-    bool over = false;
-    for (int c = 0; c < chunks; ++c) {
-        float x[kChunk];
-        values(next, x);
-        if (c + 1 < chunks) load(c + 1, next);
-        float best = x[0];
-#pragma unroll
-        for (int i = 1; i < kChunk; ++i) best = fmaxf(best, x[i]);
-        if (best > m) {
-            s *= m == -INFINITY ? 1.0f : expf(m - best);                 // a sum of nothing is 0, or NaN
-            m = best;
-        }
-        const float base = m == -INFINITY ? 0.0f : m;
-        float s1 = 0.0f;
-#pragma unroll
-        for (int i = 0; i < kChunk; i += 2) {                            // NaN and +inf make it NaN
-            s += ex2((x[i] - base) * kLog2e);
-            s1 += ex2((x[i + 1] - base) * kLog2e);
-        }
-        s += s1;
-        if (c == 0) {
-            group_max(best > -INFINITY ? ordered(best) : 0u, s_group, tid);
-            __syncthreads();
-            kth_of_groups(s_group, a.k, tid, &s_bound);
-            __syncthreads();
-            bound = s_bound == 0 ? -INFINITY : unordered(s_bound);
-        }
-        if (best >= bound) {
-#pragma unroll
-            for (int i = 0; i < kChunk; ++i)
-                if (x[i] >= bound && x[i] > -INFINITY) {
-                    const int at = atomicAdd(&s_count, 1);
-                    if (at < kRoom) s_cand[at] = key(c, i, x[i]);
-                }
-        }
-        __syncthreads();
-        const int count = s_count;
-        __syncthreads();                         // nobody adds before everybody has read
-        over = count > kRoom;
-        if (over) {                              // the sum goes on, the candidates are found below
-            bound = INFINITY;
-            if (tid == 0) s_count = kRoom + 1;
-        } else if (count > kRoom / 2 && c + 1 < chunks) {
-            rank(count);
-            if (tid < a.k) s_cand[tid] = s_best[tid];
-            bound = unordered(static_cast<uint32_t>(s_best[a.k - 1] >> 32));
-            if (tid == 0) s_count = a.k;
-            __syncthreads();
-        }
-    }
-    // the slice's maximum and sum
-    float top = m;
-#pragma unroll
-    for (int i = 16; i >= 1; i >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, i));
-    if (lane == 0) s_top[warp] = top;
-    __syncthreads();
-    top = s_top[0];
-#pragma unroll
-    for (int i = 1; i < kWarps; ++i) top = fmaxf(top, s_top[i]);
-    double sum = s * carried(m, top);            // NaN stays
-#pragma unroll
-    for (int i = 16; i >= 1; i >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, i);
-    if (lane == 0) s_sum[warp] = sum;
-    const int64_t out = static_cast<int64_t>(row) * a.slices + slice;
-    uint64_t* keys = a.keys + out * a.k;
-    if (!over) {
-        rank(s_count);
-        if (tid < a.k) keys[tid] = s_best[tid];
-    } else {
-        uint64_t last = ~0ull;
-        for (int n = 0; n < a.k; ++n) {
-            uint64_t mine = 0;
-            for (int c = 0; c < chunks; ++c) {
-                uint4 w[NV];
-                float x[kChunk];
-                load(c, w);
-                values(w, x);
-#pragma unroll
-                for (int i = 0; i < kChunk; ++i)
-                    if (x[i] > -INFINITY) {
-                        const uint64_t v = key(c, i, x[i]);
-                        if (v < last && v > mine) mine = v;
-                    }
-            }
-            last = block_max64(mine, s_tmp, tid);
-            if (tid == 0) keys[n] = last;
-        }
-    }
+
+    int row = static_cast<int>(quotient(begin, a.chunks)), c = static_cast<int>(begin - static_cast<int64_t>(row) * a.chunks);
     if (tid == 0) {
-        Slice st;
-        st.top = top;
-        st.pad = 0;
-        st.sum = 0.0;
-        for (int i = 0; i < kWarps; ++i) st.sum += s_sum[i];
-        a.stats[out] = st;
+        s_abort = 0;
+        s_count = 0;
+        for (int i = 0; i < kRing; ++i) {
+            mbar_init(smem_u32(&full[i]), 1);
+            mbar_init(smem_u32(&empty[i]), kWarps);
+        }
+    }
+    fence_barrier_init();
+    __syncthreads();
+    if (warp == kWarps) {                        // brings the chunks
+        if (lane != 0) return;
+        int slot = 0, phase = 1;
+        for (int64_t i = begin; i < end; ++row, c = 0) {
+            const int n = static_cast<int>(min(static_cast<int64_t>(a.chunks - c), end - i));
+            i += n;
+            if (done(row)) continue;
+            for (const int last = c + n; c < last; ++c) {
+                const Place p = place(row, c);
+                if (!mbar_wait(smem_u32(&empty[slot]), phase, &s_abort, a.status)) {
+                    spin_ns(1000000);            // copies that were issued land
+                    return;
+                }
+                const uint32_t bar = smem_u32(&full[slot]), bytes = static_cast<uint32_t>(p.hi - p.lo) * 16;
+                s_place[slot] = make_int3(p.token, p.lo, p.hi);
+                mbar_arrive_expect_tx(bar, bytes);
+                if (bytes)
+                    bulk_load(smem_u32(ring + slot * WORDS + p.lo), p.base + (p.first + p.lo * VEC) * ES, bytes, bar);
+                if (++slot == kRing) slot = 0, phase ^= 1;
+            }
+        }
+        return;
+    }
+    int slot = 0, phase = 0;
+    bool dead = false;                           // after a lost copy the barriers are kept, the results are not right
+    for (int64_t i = begin; i < end;) {
+        const int c0 = c, c1 = static_cast<int>(min(static_cast<int64_t>(a.chunks), c0 + (end - i)));    // the piece
+        const bool skip = done(row);
+        float m = -INFINITY, s = 0.0f, bound = -INFINITY;
+        bool weak = true;
+        for (; c < c1; ++c, ++i) {
+            if (skip) continue;
+            if (!dead) dead = !mbar_wait_warp(smem_u32(&full[slot]), phase, &s_abort, a.status);
+            const int3 p = s_place[slot];
+            const int token = p.x + tid * VEC;
+            uint4 w[NV];
+            float x[kChunk];
+#pragma unroll
+            for (int j = 0; j < NV; ++j) w[j] = ring[slot * WORDS + j * kThreads + tid];
+            const bool partial = p.y != 0 || p.z != WORDS;
+            if (partial) {
+                const Place q = place(row, c);
+#pragma unroll
+                for (int j = 0; j < NV; ++j) {
+                    const int word = j * kThreads + tid;
+                    if (word < p.y || word >= p.z) ring[slot * WORDS + word] = w[j] = edge_word(q, word);
+                }
+            }
+            values(w, x);
+            float best = x[0];
+#pragma unroll
+            for (int e = 1; e < kChunk; ++e) best = fmaxf(best, x[e]);
+            if (best > m) {
+                s *= m == -INFINITY ? 1.0f : expf(m - best);             // a sum of nothing is 0, or NaN
+                m = best;
+            }
+            // 2^(x log2(e) - h), h = base log2(e) rounded: one fma a term; what the rounding of h makes of
+            // all of them is taken back from their sum
+            const float base = m == -INFINITY ? 0.0f : m;
+            if (fabsf(base) < 1e37f) {
+                const float h = base * kLog2e;
+                const uint64_t l2 = pack2(kLog2e, kLog2e), h2 = pack2(-h, -h);
+                uint64_t u0 = 0, u1 = 0;
+#pragma unroll
+                for (int e = 0; e < kChunk; e += 4) {                    // NaN makes it NaN
+                    float p0, p1, q0, q1;
+                    unpack2(fma2(pack2(x[e], x[e + 1]), l2, h2), p0, p1);
+                    unpack2(fma2(pack2(x[e + 2], x[e + 3]), l2, h2), q0, q1);
+                    u0 = add2(u0, pack2(ex2(p0), ex2(p1)));
+                    u1 = add2(u1, pack2(ex2(q0), ex2(q1)));
+                }
+                float p0, p1;
+                unpack2(add2(u0, u1), p0, p1);
+                s = fmaf(p0 + p1, ex2(-fmaf(base, kLog2e, -h)), s);
+            } else {                                                     // past fp32 times log2(e), or +inf: NaN
+#pragma unroll
+                for (int e = 0; e < kChunk; ++e) s += ex2((x[e] - base) * kLog2e);
+            }
+            if (weak) {                          // until a whole chunk has given the bound
+                group_max(best > -INFINITY ? ordered(best) : 0u, s_group, tid);
+                sync_all();
+                kth_of_groups(s_group, a.k, tid, &s_bound);
+                sync_all();
+                if (s_bound != 0) bound = fmaxf(bound, unordered(s_bound));
+                weak = partial || s_bound == 0;
+                sync_all();
+            }
+            if (best >= bound) {
+                uint32_t set = 0;
+#pragma unroll
+                for (int e = 0; e < kChunk; ++e) set |= x[e] >= bound && x[e] > -INFINITY ? 1u << e : 0u;
+                while (set) {                    // rarely more than one: its logit once more from the ring
+                    const int e = __ffs(set) - 1;
+                    set &= set - 1;
+                    const uint8_t* at_word = reinterpret_cast<const uint8_t*>(ring + slot * WORDS + e / VEC * kThreads + tid) + e % VEC * ES;
+                    const float logit = F32 ? *reinterpret_cast<const float*>(at_word) : bf16_to_f32(*reinterpret_cast<const uint16_t*>(at_word));
+                    const int at = atomicAdd(&s_count, 1);
+                    if (at < kRoom) s_cand[at] = key(token, e, logit);
+                }
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&empty[slot]));
+            if (++slot == kRing) slot = 0, phase ^= 1;
+            // after the piece's chunks 2, 4, 8 .. (and 1, where one chunk's candidates could fill half of the
+            // room): the bound rises to the k-th best so far, so that each chunk lets about k / (its number) pass
+            const int nth = c - c0;
+            if ((nth & (nth + 1)) != 0 || (nth == 0 && a.k <= 16) || c + 1 == c1) continue;
+            sync_all();
+            const int count = s_count;
+            if (count <= kRoom && count >= a.k) {
+                rank(count);
+                if (tid < a.k) s_cand[tid] = s_best[tid];
+                bound = unordered(static_cast<uint32_t>(s_best[a.k - 1] >> 32));
+                if (tid == 0) s_count = a.k;
+            }
+            sync_all();
+        }
+        if (!skip) {
+            // the piece's maximum and sum
+            float top = m;
+#pragma unroll
+            for (int e = 16; e >= 1; e >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, e));
+            if (lane == 0) s_top[warp] = top;
+            sync_all();
+            top = s_top[0];
+#pragma unroll
+            for (int e = 1; e < kWarps; ++e) top = fmaxf(top, s_top[e]);
+            double sum = s * carried(m, top);    // NaN stays
+#pragma unroll
+            for (int e = 16; e >= 1; e >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, e);
+            if (lane == 0) s_sum[warp] = sum;
+            const int64_t out = static_cast<int64_t>(row) * a.most + (blockIdx.x - line.of(static_cast<int64_t>(row) * a.chunks));
+            uint64_t* keys = a.keys + out * a.k;
+            if (s_count <= kRoom) {
+                rank(s_count);
+                if (tid < a.k) keys[tid] = s_best[tid];
+            } else {
+                uint64_t last = ~0ull;
+                for (int n = 0; n < a.k; ++n) {
+                    uint64_t mine = 0;
+                    for (int cc = c0; cc < c1; ++cc) {
+                        const Place p = place(row, cc);
+                        const int token = p.token + tid * VEC;
+                        uint4 w[NV];
+                        float x[kChunk];
+#pragma unroll
+                        for (int j = 0; j < NV; ++j) {
+                            const int word = j * kThreads + tid;
+                            w[j] = word >= p.lo && word < p.hi
+                                       ? __ldg(reinterpret_cast<const uint4*>(p.base + (p.first + word * VEC) * ES))
+                                       : edge_word(p, word);
+                        }
+                        values(w, x);
+#pragma unroll
+                        for (int e = 0; e < kChunk; ++e)
+                            if (x[e] > -INFINITY) {
+                                const uint64_t v = key(token, e, x[e]);
+                                if (v < last && v > mine) mine = v;
+                            }
+                    }
+                    last = block_max64(mine, s_tmp, tid);
+                    if (tid == 0) keys[n] = last;
+                }
+            }
+            sync_all();
+            if (tid == 0) {
+                Piece st;
+                st.top = top;
+                st.pad = 0;
+                st.sum = 0.0;
+                for (int e = 0; e < kWarps; ++e) st.sum += s_sum[e];
+                a.stats[out] = st;
+                s_count = 0;
+            }
+            sync_all();
+        }
+        if (c == a.chunks) c = 0, ++row;
     }
 }
 
-// A continuation: its score (ordered64 of it, 0: none) and its place beam * vocab + token.
+// A continuation: its score (ordered64 of it, 0: none) and its place, beam in the upper half, token in the lower.
 struct Cand {
-    uint64_t score, flat;
+    uint64_t score, place;
 };
 __device__ __forceinline__ bool before(const Cand& a, const Cand& b) {
-    return a.score > b.score || (a.score == b.score && a.flat < b.flat);
+    return a.score > b.score || (a.score == b.score && a.place < b.place);
+}
+
+// log of x >= 2^-1000 to about 1e-14: exponent and the series 2 (z + z^3/3 + ...) of log f, z = (f - 1) / (f + 1),
+// for f in [3/4, 3/2).  A third of the library's fp64 instructions, which are what the second kernel waits for.
+__device__ __forceinline__ double log_of_sum(double x) {
+    const long long bits = __double_as_longlong(x);
+    int e = static_cast<int>(bits >> 52) - 1023;
+    double f = __longlong_as_double((bits & 0xfffffffffffffll) | 0x3ff0000000000000ll);
+    if (f >= 1.5) f *= 0.5, ++e;
+    const double d = f + 1.0;
+    double r = static_cast<double>(1.0f / static_cast<float>(d));
+    r = fma(r, fma(-d, r, 1.0), r);              // the reciprocal, by Newton's step
+    const double z = (f - 1.0) * r, w = z * z;
+    double p = 1.0 / 17;
+    p = fma(p, w, 1.0 / 15);
+    p = fma(p, w, 1.0 / 13);
+    p = fma(p, w, 1.0 / 11);
+    p = fma(p, w, 1.0 / 9);
+    p = fma(p, w, 1.0 / 7);
+    p = fma(p, w, 1.0 / 5);
+    p = fma(p, w, 1.0 / 3);
+    p = fma(p, w, 1.0);
+    return fma(static_cast<double>(e), 0.693147180559945309417, 2.0 * z * p);
 }
 
 __global__ void __launch_bounds__(kThreads) beam_pick_kernel(const __grid_constant__ BeamArgs a) {
     __shared__ double s_add[TP_MAX_BEAMS];       // score - lse; NaN: no continuations
-    __shared__ uint64_t s_group[kGroups], s_bound;
+    __shared__ __align__(16) uint64_t s_group[kGroups];
+    __shared__ uint64_t s_bound;
     __shared__ Cand s_cand[kRoom];
     __shared__ Cand s_best[kWarps];
-    __shared__ float s_top[TP_MAX_BEAMS];
     __shared__ int s_count;
     pdl_wait();
     pdl_trigger();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int item = blockIdx.x;
     const int64_t row0 = static_cast<int64_t>(item) * a.beams;
-    auto done = [&](int b) { return a.finished != nullptr && a.finished[row0 + b] != 0; };
     if (tid == 0) s_count = 0;
-    // this thread's candidates, the first few of which it keeps: a key of a beam's slice each; a finished
-    // beam has its first alone
-    const int per_beam = a.slices * a.k, n = a.beams * per_beam;
-    constexpr int KEEP = 8;
-    uint64_t key[KEEP];
+    // A warp takes every kWarps-th beam: f(continuation) for this lane's keys of each; a finished beam has
+    // one.  With `first` it finds score - lse before.
+    const Line line(a);
+    auto each = [&](bool first, auto f) {
+        for (int b = warp; b < a.beams; b += kWarps) {
+            const bool done = a.finished != nullptr && a.finished[row0 + b] != 0;
+            const int64_t begin = (row0 + b) * a.chunks;
+            const int pieces = line.of(begin + a.chunks - 1) - line.of(begin) + 1, per_beam = pieces * a.k;
+            const uint64_t* keys = a.keys + (row0 + b) * a.most * a.k;
+            uint64_t key = !done && lane < per_beam ? keys[lane] : 0;
+            if (first) {
+                const float score = a.scores[row0 + b];
+                double add = __longlong_as_double(0x7ff8000000000000ll);
+                if (done) {
+                    if (score > -INFINITY) add = score;
+                } else {
+                    const Piece* st = a.stats + (row0 + b) * a.most;
+                    Piece mine{0.0, -INFINITY, 0};
+                    if (lane < pieces) mine = st[lane];
+                    for (int i = lane + 32; i < pieces; i += 32) {
+                        const Piece o = st[i];
+                        const float up = fmaxf(mine.top, o.top);
+                        mine.sum = mine.sum * carried(mine.top, up) + o.sum * carried(o.top, up);
+                        mine.top = up;
+                    }
+                    float top = mine.top;
 #pragma unroll
-    for (int j = 0; j < KEEP; ++j) {
-        const int i = tid + j * kThreads;
-        key[j] = i < n ? a.keys[row0 * per_beam + i] : 0;
-    }
-    for (int b = warp; b < a.beams; b += kWarps) {
-        if (done(b)) continue;
-        const Slice* st = a.stats + (row0 + b) * a.slices;
-        Slice mine{0.0, -INFINITY, 0};
-        if (lane < a.slices) mine = st[lane];
-        for (int i = lane + 32; i < a.slices; i += 32) {
-            const Slice o = st[i];
-            const float up = fmaxf(mine.top, o.top);
-            mine.sum = mine.sum * carried(mine.top, up) + o.sum * carried(o.top, up);
-            mine.top = up;
+                    for (int m = 16; m >= 1; m >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, m));
+                    double sum = mine.sum * carried(mine.top, top);
+#pragma unroll
+                    for (int m = 16; m >= 1; m >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, m);
+                    // a finite maximum's sum is at least 1, unless NaN is in it
+                    if (score > -INFINITY && top > -INFINITY && top < INFINITY && sum >= 0.5)
+                        add = score - (top + log_of_sum(sum));
+                }
+                if (lane == 0) s_add[b] = add;
+                __syncwarp();
+            }
+            const double add = s_add[b];
+            if (!(add == add)) continue;
+            const uint64_t place = static_cast<uint64_t>(b) << 32;
+            if (done) {
+                if (lane == 0) f(Cand{ordered64(add), place | static_cast<uint32_t>(a.eos)});
+                continue;
+            }
+            for (int i = lane; i < per_beam; i += 32) {
+                if (key != 0)
+                    f(Cand{ordered64(add + static_cast<double>(unordered(static_cast<uint32_t>(key >> 32)))),
+                           place | (0xffffffffu - static_cast<uint32_t>(key))});
+                if (i + 32 < per_beam) key = keys[i + 32];
+            }
         }
-        float top = mine.top;
-#pragma unroll
-        for (int m = 16; m >= 1; m >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, m));
-        double sum = mine.sum * carried(mine.top, top);
-#pragma unroll
-        for (int m = 16; m >= 1; m >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, m);
-        if (lane == 0) s_add[b] = sum, s_top[b] = top;
-    }
-    __syncthreads();
-    for (int b = tid; b < a.beams; b += kThreads) {
-        const float score = a.scores[row0 + b];
-        double add = __longlong_as_double(0x7ff8000000000000ll);
-        if (done(b)) {
-            if (score > -INFINITY) add = score;
-        } else if (score > -INFINITY) {
-            const double lse = s_top[b] + log(s_add[b]);
-            if (lse > -INFINITY && lse < INFINITY) add = score - lse;
-        }
-        s_add[b] = add;
-    }
-    __syncthreads();
-    auto cand = [&](int i, uint64_t k64) {
-        Cand c{0, 0};
-        const uint32_t b = static_cast<uint32_t>(i) / static_cast<uint32_t>(per_beam);
-        const double add = s_add[b];
-        if (!(add == add)) return c;
-        if (done(b)) {
-            if (i != static_cast<int>(b) * per_beam) return c;
-            c.score = ordered64(add);
-            c.flat = static_cast<uint64_t>(b) * a.vocab + static_cast<uint32_t>(a.eos);
-            return c;
-        }
-        if (k64 == 0) return c;
-        c.score = ordered64(add + static_cast<double>(unordered(static_cast<uint32_t>(k64 >> 32))));
-        c.flat = static_cast<uint64_t>(b) * a.vocab + (0xffffffffu - static_cast<uint32_t>(k64));
-        return c;
-    };
-    // f(candidate) for all of this thread's
-    auto each = [&](auto f) {
-#pragma unroll
-        for (int j = 0; j < KEEP; ++j)
-            if (tid + j * kThreads < n) f(cand(tid + j * kThreads, key[j]));
-        for (int i = tid + KEEP * kThreads; i < n; i += kThreads) f(cand(i, a.keys[row0 * per_beam + i]));
     };
     uint64_t best = 0;
-    each([&](const Cand& c) { best = best > c.score ? best : c.score; });
+    each(true, [&](const Cand& c) { best = best > c.score ? best : c.score; });
     group_max(best, s_group, tid);
     __syncthreads();
     kth_of_groups(s_group, a.k, tid, &s_bound);
     __syncthreads();
     const uint64_t bound = s_bound > 1 ? s_bound : 1;
-    if (best >= bound)
-        each([&](const Cand& c) {
-            if (c.score >= bound) {
-                const int at = atomicAdd(&s_count, 1);
-                if (at < kRoom) s_cand[at] = c;
-            }
-        });
+    each(false, [&](const Cand& c) {
+        if (c.score >= bound) {
+            const int at = atomicAdd(&s_count, 1);
+            if (at < kRoom) s_cand[at] = c;
+        }
+    });
     __syncthreads();
     const int count = s_count;
     const int64_t out = static_cast<int64_t>(item) * a.k;
     auto put = [&](int at, const Cand& c) {
-        const int b = c.score ? static_cast<int>(c.flat / a.vocab) : 0;
         a.scores_out[out + at] = c.score ? static_cast<float>(unordered64(c.score)) : -INFINITY;
-        a.rows_out[out + at] = c.score ? static_cast<int32_t>(row0 + b) : -1;
-        a.tokens_out[out + at] = c.score ? static_cast<int32_t>(c.flat - static_cast<uint64_t>(b) * a.vocab) : -1;
+        a.rows_out[out + at] = c.score ? static_cast<int32_t>(row0 + (c.place >> 32)) : -1;
+        a.tokens_out[out + at] = c.score ? static_cast<int32_t>(c.place) : -1;
     };
     if (count <= kRoom) {
         for (int i = tid; i < count; i += kThreads) {
@@ -423,12 +606,12 @@ __global__ void __launch_bounds__(kThreads) beam_pick_kernel(const __grid_consta
     Cand last{~0ull, 0};
     for (int m = 0; m < a.k; ++m) {
         Cand mine{0, ~0ull};
-        each([&](const Cand& c) {
-            if (c.score != 0 && before(last, c) && before(c, mine)) mine = c;
+        each(false, [&](const Cand& c) {
+            if (before(last, c) && before(c, mine)) mine = c;
         });
 #pragma unroll
         for (int s = 16; s >= 1; s >>= 1) {
-            const Cand o{__shfl_xor_sync(0xffffffffu, mine.score, s), __shfl_xor_sync(0xffffffffu, mine.flat, s)};
+            const Cand o{__shfl_xor_sync(0xffffffffu, mine.score, s), __shfl_xor_sync(0xffffffffu, mine.place, s)};
             if (before(o, mine)) mine = o;
         }
         __syncthreads();
@@ -444,27 +627,18 @@ __global__ void __launch_bounds__(kThreads) beam_pick_kernel(const __grid_consta
 
 constexpr int kChunkLogits = kThreads * kChunk;
 
-// Chunks of a slice: as many as leave six blocks for each SM (the registers allow five to run at once),
-// at most 16.
-int pick_chunks(int64_t rows, int64_t vocab, int sms) {
-    const int64_t all = rows * ((vocab + kChunkLogits - 1) / kChunkLogits);
-    return static_cast<int>(std::min<int64_t>(16, std::max<int64_t>(1, all / (6 * sms))));
-}
-
-// Slices of a shard: its 16-byte words, one more for a row that begins inside a word.
-int64_t slices_of(int64_t cols, int vec, int chunks) {
-    if (cols == 0) return 0;
-    const int64_t words = (cols + 2 * vec - 2) / vec, per = static_cast<int64_t>(kChunkLogits / vec) * chunks;
-    return (words + per - 1) / per;
+// Chunks of a shard of a row: one more than its columns need where a row can begin inside a 16-byte word.
+int chunks_of(int64_t cols, int vec) {
+    return cols == 0 ? 0 : static_cast<int>((cols + vec - 1 + kChunkLogits - 1) / kChunkLogits);
 }
 
 }  // namespace
 
 size_t beam_workspace(int64_t items, int beams, int k, int64_t vocab) {
-    // the most slices any cut of the vocabulary gives
-    const int64_t slices = (vocab + kChunkLogits - 1) / kChunkLogits + 2 * TP_MAX_SHARDS;
+    // a row has at most as many pieces as chunks, and never more chunks than this
+    const int64_t most = (vocab + kChunkLogits - 1) / kChunkLogits + 2 * TP_MAX_SHARDS;
     const int64_t rows = items * beams;
-    return static_cast<size_t>(rows) * slices * (sizeof(Slice) + static_cast<size_t>(k) * 8);
+    return static_cast<size_t>(rows) * most * (sizeof(Piece) + static_cast<size_t>(k) * 8);
 }
 
 tp_status launch_beam_select(const BeamDesc& d, cudaStream_t stream) {
@@ -480,18 +654,20 @@ tp_status launch_beam_select(const BeamDesc& d, cudaStream_t stream) {
     }
     const int sms = device_sms();
     if (sms <= 0) return TP_ERR_CUDA;
-    a.chunks = pick_chunks(rows, vocab, sms);
-    int64_t slices = 0;
     for (int r = 0; r < TP_MAX_SHARDS; ++r) {
-        a.first_slice[r] = static_cast<int>(slices);
-        if (r < d.t) slices += slices_of(d.cols[r], d.f32 ? 4 : 8, a.chunks);
+        a.first_chunk[r] = a.chunks;
+        if (r < d.t) a.chunks += chunks_of(d.cols[r], d.f32 ? 4 : 8);
     }
-    a.first_slice[TP_MAX_SHARDS] = static_cast<int>(slices);
+    a.first_chunk[TP_MAX_SHARDS] = a.chunks;
+    const int64_t total = rows * a.chunks;
+    a.blocks = static_cast<int>(std::min<int64_t>(total, static_cast<int64_t>(sms) * kAtOnce));
+    // a part holds at least `each` chunks, so a row lies in at most this many
+    const int64_t each = total / a.blocks;
+    a.most = static_cast<int>(std::min<int64_t>(a.chunks, (a.chunks - 1) / each + 2));
     a.t = d.t;
     a.items = d.items;
     a.beams = d.beams;
     a.k = d.k;
-    a.slices = static_cast<int>(slices);
     a.vocab = vocab;
     a.scores = d.scores;
     a.finished = d.finished;
@@ -499,14 +675,20 @@ tp_status launch_beam_select(const BeamDesc& d, cudaStream_t stream) {
     a.scores_out = d.scores_out;
     a.rows_out = d.rows_out;
     a.tokens_out = d.tokens_out;
-    a.stats = static_cast<Slice*>(d.ws);
-    a.keys = reinterpret_cast<uint64_t*>(a.stats + rows * slices);
-    if (slices * rows > INT32_MAX) return TP_ERR_UNSUPPORTED;
-    const dim3 grid(static_cast<unsigned>(slices * rows)), block(kThreads);
-    const cudaError_t e = d.f32 ? launch_pdl(beam_slice_kernel<true>, grid, block, 0, stream, a)
-                                : launch_pdl(beam_slice_kernel<false>, grid, block, 0, stream, a);
+    a.stats = static_cast<Piece*>(d.ws);
+    a.keys = reinterpret_cast<uint64_t*>(a.stats + rows * a.most);
+    const dim3 grid(a.blocks), block(kThreads + 32);
+    a.status = device_status_word();
+    constexpr int kSmem = kRing * kThreads * kChunk * 4;         // of fp32; bf16 takes half
+    static std::atomic<uint64_t> smem_f32{0}, smem_bf16{0};
+    if (!smem_attribute_once(d.f32 ? reinterpret_cast<const void*>(beam_scan_kernel<true>)
+                                   : reinterpret_cast<const void*>(beam_scan_kernel<false>),
+                             kSmem, d.f32 ? smem_f32 : smem_bf16))
+        return TP_ERR_CUDA;
+    const cudaError_t e = d.f32 ? launch_pdl(beam_scan_kernel<true>, grid, block, kSmem, stream, a)
+                                : launch_pdl(beam_scan_kernel<false>, grid, block, kSmem / 2, stream, a);
     if (e != cudaSuccess) return TP_ERR_CUDA;
-    return launch_pdl(beam_pick_kernel, dim3(d.items), block, 0, stream, a) == cudaSuccess ? TP_OK : TP_ERR_CUDA;
+    return launch_pdl(beam_pick_kernel, dim3(d.items), dim3(kThreads), 0, stream, a) == cudaSuccess ? TP_OK : TP_ERR_CUDA;
 }
 
 }  // namespace tpk
