@@ -47,31 +47,4 @@ __device__ __forceinline__ SeqRows seq_rows(const KvSeqs& q, int s) {
     return {a, b - a};
 }
 
-// The sequence that row `row` belongs to, found by the whole warp (32-way
-// search over cu_rows), and the row's position in it; false when no sequence
-// holds the row.
-__device__ __forceinline__ bool row_place(const KvSeqs& q, int row, int lane, int& seq, int& pos) {
-    if (q.cu_rows == nullptr) {
-        seq = row;
-        pos = q.lens[row] - 1;
-        return true;
-    }
-    int lo = 0, len = q.nseq;
-    while (len > 1) {
-        const int step = (len + 31) >> 5;
-        const int at = lane * step;
-        const bool le = at < len && q.cu_rows[lo + at] <= row;
-        const int k = __popc(__ballot_sync(0xffffffffu, le)) - 1;
-        if (k < 0) break;
-        lo += k * step;
-        len = min(step, len - k * step);
-    }
-    const int a = q.cu_rows[lo], b = q.cu_rows[lo + 1];
-    seq = lo;
-    // 64 bits: a length of any value minus any row count stays in range
-    const int64_t p = static_cast<int64_t>(q.lens[lo]) - (static_cast<int64_t>(b) - row);
-    pos = p < 0 ? -1 : static_cast<int>(p);
-    return a >= 0 && a <= row && row < b && b <= q.n;
-}
-
 }  // namespace tpk

@@ -1,10 +1,15 @@
 // Writing to and reading from the paged 4-bit KV cache.
 //
-// Both kernels are elementwise over rows of head_dim elements and bound by the
-// memory traffic of large calls (append: 2 bytes in and about 0.53 out per
-// element) and by the chain of dependent loads (row -> sequence -> page) of
-// small ones.  HD / 8 lanes hold one row, eight elements each: a 16-byte load,
-// a 4-byte store of eight codes.
+// Both kernels are elementwise over rows of head_dim elements: bound by memory
+// traffic for large calls (append: 2 bytes in and about 0.53 out per element), by
+// the chain of dependent loads (row -> sequence -> page) for small ones.  HD / 8
+// lanes hold one sub-row (a kv head's key or value of a row), eight elements
+// each: a 16-byte load, a 4-byte store of eight codes.
+//
+// A warp takes kRows rows of one group of sub-rows (those that its 32 lanes
+// hold).  Lane r looks up the place of row r, so that one chain of loads serves
+// all of them, and the rows' data are on their way before it.  Few rows take one
+// a warp, so that they spread over the GPU.
 #include "kv4.cuh"
 
 namespace tpk {
@@ -12,173 +17,237 @@ namespace {
 
 constexpr int kThreads = 256;
 
-// min, max and "all finite" of a row held by LANES neighbouring lanes.
+__device__ __forceinline__ uint32_t min2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("min.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+__device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+
+// Smallest and largest of a row of bf16 held by LANES neighbouring lanes, eight elements each; NaN when one is.
 template <int LANES>
-__device__ __forceinline__ void row_range(const float (&x)[8], float& lo, float& hi, bool& finite) {
-    lo = hi = x[0];
-    bool bad = false;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        lo = fminf(lo, x[i]);
-        hi = fmaxf(hi, x[i]);
-        bad |= !(fabsf(x[i]) <= 3.402823466e38f);
-    }
-    uint32_t b = bad;
+__device__ __forceinline__ void row_range(const uint4& w, float& lo, float& hi) {
+    uint32_t a = min2(min2(w.x, w.y), min2(w.z, w.w)), b = max2(max2(w.x, w.y), max2(w.z, w.w));
 #pragma unroll
     for (int m = 1; m < LANES; m <<= 1) {
-        lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, m));
-        hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, m));
-        b |= __shfl_xor_sync(0xffffffffu, b, m);
+        a = min2(a, __shfl_xor_sync(0xffffffffu, a, m));
+        b = max2(b, __shfl_xor_sync(0xffffffffu, b, m));
     }
-    finite = b == 0;
+    a = min2(a, a >> 16);                        // the lower half; the upper is not looked at
+    b = max2(b, b >> 16);
+    lo = __uint_as_float(a << 16);
+    hi = __uint_as_float(b << 16);
 }
 
-// One warp per (row, rank, group of sub-rows); a sub-row is one kv head's key or value.
+// The place in its rank's pool of row `row` (offset of its block for kv head 0, and its slot), by one lane:
+// block -1 when it is at a negative position, -2 when it has no place.
+struct RowAt {
+    int64_t block;
+    int slot;
+};
 template <int HD>
-__global__ void __launch_bounds__(kThreads) kv4_append_kernel(KvAppendDesc d) {
+__device__ __forceinline__ RowAt row_at(const KvSeqs& q, const KvPools& p, int row) {
+    int seq = row, pos;
+    if (q.cu_rows == nullptr) {
+        pos = q.lens[row] - 1;
+    } else {
+        int lo = 0, hi = q.nseq;                 // the last sequence that begins at or before the row
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (q.cu_rows[mid] <= row)
+                lo = mid;
+            else
+                hi = mid;
+        }
+        const int a = q.cu_rows[lo], b = q.cu_rows[lo + 1];
+        if (a < 0 || a > row || row >= b || b > q.n) return {-2, 0};
+        // 64 bits: a length of any value minus any row count stays in range
+        const int64_t at = static_cast<int64_t>(q.lens[lo]) - (static_cast<int64_t>(b) - row);
+        seq = lo;
+        pos = at < 0 ? -1 : static_cast<int>(at);
+    }
+    if (pos < 0) return {-1, 0};
+    const int64_t off = kv_block_offset(q.table + seq * q.max_blocks, q.max_blocks, p.pages, p.page_shift, p.kv_heads, 0,
+                                        pos / kKvBlock, KvBlock<HD>::BYTES);
+    return {off < 0 ? -2 : off, pos % kKvBlock};
+}
+
+// What a warp works on: rows row0 .. of rank r, and for each lane its sub-row.
+template <int HD, int ROWS>
+struct Task {
+    static constexpr int LANES = HD / 8, SUB = 32 / LANES;
+    int row0, rows, r, sub, part, head;
+    bool val, active, any;
+    __device__ __forceinline__ Task(const KvSeqs& q, const KvPools& p) {
+        const int lane = threadIdx.x & 31;
+        const int subs = 2 * p.kv_heads, groups = (subs + SUB - 1) / SUB;
+        const int per = p.t * groups;
+        const int64_t warp = static_cast<int64_t>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5);
+        const int64_t set = quotient(warp, per);
+        const int rest = static_cast<int>(warp - set * per);
+        any = set * ROWS < q.n;
+        row0 = static_cast<int>(set) * ROWS;
+        rows = min(ROWS, q.n - row0);
+        r = rest / groups;
+        sub = (rest - r * groups) * SUB + lane / LANES;
+        part = lane % LANES;
+        active = sub < subs;
+        head = active ? sub >> 1 : 0;
+        val = sub & 1;
+    }
+};
+
+template <int HD, int ROWS>
+__global__ void __launch_bounds__(kThreads) kv4_append_kernel(const __grid_constant__ KvAppendDesc d) {
     using B = KvBlock<HD>;
-    constexpr int LANES = HD / 8, SUB = 32 / LANES;
     pdl_wait();
     pdl_trigger();
+    const Task<HD, ROWS> w(d.seqs, d.pools);
+    if (!w.any) return;
     const int lane = threadIdx.x & 31;
-    const int subs = 2 * d.pools.kv_heads, groups = (subs + SUB - 1) / SUB;
-    const int64_t warp = static_cast<int64_t>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5);
-    const int64_t per_row = static_cast<int64_t>(d.pools.t) * groups;
-    if (warp >= d.seqs.n * per_row) return;
-    const int row = static_cast<int>(warp / per_row);
-    const int rest = static_cast<int>(warp - row * per_row);
-    const int r = rest / groups, sub = (rest - r * groups) * SUB + lane / LANES;
-    const int part = lane % LANES;
-    const bool active = sub < subs;
-    const int head = active ? sub >> 1 : 0;
-    const bool val = sub & 1;
-
-    uint4 raw = make_uint4(0, 0, 0, 0);
-    if (active) {
-        const uint16_t* src = static_cast<const uint16_t*>(val ? d.v[r] : d.k[r]) +
-                              row * (val ? d.ldv : d.ldk) + head * HD + part * 8;
-        raw = __ldg(reinterpret_cast<const uint4*>(src));
-    }
-    int seq, pos;
-    const bool found = row_place(d.seqs, row, lane, seq, pos);
-    if (!found) raise_status(d.seqs.status, TP_ERR_INVALID_ARG);
-    if (!found || pos < 0) return;
-    const int64_t off = kv_block_offset(d.seqs.table + seq * d.seqs.max_blocks, d.seqs.max_blocks, d.pools.pages,
-                                        d.pools.page_shift, d.pools.kv_heads, head, pos / kKvBlock, B::BYTES);
-    if (off < 0) {
-        raise_status(d.seqs.status, TP_ERR_INVALID_ARG);
-        return;                                   // page and position are the same for the whole warp
-    }
-    float x[8];
-    const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+    const int64_t ld = w.val ? d.ldv : d.ldk;
+    const uint16_t* src = static_cast<const uint16_t*>(w.val ? d.v[w.r] : d.k[w.r]) + w.row0 * ld + w.head * HD + w.part * 8;
+    uint4 raw[ROWS];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        x[2 * i] = __uint_as_float(w[i] << 16);
-        x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-    }
-    float lo, hi;
-    bool finite;
-    row_range<LANES>(x, lo, hi, finite);
-    // fp32 throughout; the base is a bf16 already (an element of the row), the step is rounded to bf16
-    // once and the codes are taken with the rounded step, so that they are the nearest to it.
-    lo = __fadd_rn(lo, 0.0f);                     // -0 becomes +0
-    const float range = __fadd_rn(__fsub_rn(hi, lo), 0.0f);   // a step is never -0: attention compares its bits
-    finite = finite && range <= 3.402823466e38f;
-    const uint16_t step16 = finite ? f32_to_bf16(__fmul_rn(range, 1.0f / 15.0f)) : 0;
-    const float step = bf16_to_f32(step16);
-    uint32_t code = 0;
-    if (step > 0.0f) {
+    for (int i = 0; i < ROWS; ++i)
+        raw[i] = w.active && i < w.rows ? __ldg(reinterpret_cast<const uint4*>(src + i * ld)) : make_uint4(0, 0, 0, 0);
+    RowAt at{-1, 0};
+    if (lane < w.rows) at = row_at<HD>(d.seqs, d.pools, w.row0 + lane);
+    if (at.block == -2) raise_status(d.seqs.status, TP_ERR_INVALID_ARG);
+    uint8_t* pool = d.pools.pool[w.r] + (static_cast<int64_t>(w.head) << d.pools.page_shift) * B::BYTES;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const float u = rintf(__fdiv_rn(__fsub_rn(x[i], lo), step));
-            code |= static_cast<uint32_t>(fminf(fmaxf(u, 0.0f), 15.0f)) << (4 * i);
+    for (int i = 0; i < ROWS; ++i) {
+        const int64_t block = __shfl_sync(0xffffffffu, at.block, i);
+        const int slot = __shfl_sync(0xffffffffu, at.slot, i);
+        if (block < 0) continue;                  // the same for the whole warp
+        float lo, hi;
+        row_range<Task<HD, ROWS>::LANES>(raw[i], lo, hi);
+        // fp32 throughout; the base is a bf16 already (an element of the row), the step is rounded to bf16
+        // once and the codes are taken with the rounded step, so that they are the nearest to it.
+        lo = __fadd_rn(lo, 0.0f);                 // -0 becomes +0
+        const float range = __fadd_rn(__fsub_rn(hi, lo), 0.0f);   // a step is never -0: attention compares its bits
+        const bool finite = range <= 3.402823466e38f;             // false for NaN: one in the row, or inf - inf
+        const uint16_t step16 = finite ? f32_to_bf16(__fmul_rn(range, 1.0f / 15.0f)) : 0;
+        const float step = bf16_to_f32(step16);
+        uint32_t code = 0;
+        if (step > 0.0f) {
+            const uint32_t word[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+            float x[8];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                x[2 * j] = __fsub_rn(__uint_as_float(word[j] << 16), lo);
+                x[2 * j + 1] = __fsub_rn(__uint_as_float(word[j] & 0xffff0000u), lo);
+            }
+            // A quotient by the reciprocal is off by 2^-21 at most: only within 2^-10 of a border between two
+            // codes, or with a step whose rounding (below the normal numbers) or reciprocal is not that good, does
+            // the definition's division decide.  Adding 1.5 2^23 leaves the nearest whole number, ties to even, in
+            // the low bits; its own bits come off the packed word at the end.
+            const float inv = __frcp_rn(step);
+            bool near = !(step > 1e-30f);
+            uint32_t fast = 0;
+#pragma unroll
+            for (int j = 7; j >= 0; --j) {
+                const float t = fmaf(x[j], inv, 12582912.0f);
+                near |= fabsf(fmaf(x[j], inv, -__fsub_rn(t, 12582912.0f))) > 0.499f;
+                fast = fast * 16 + __float_as_uint(t);
+            }
+            code = fast - (0x4b400000u + 0xb4000000u + 0x40000000u);
+            if (near) {
+                code = 0;
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    code |= static_cast<uint32_t>(fminf(fmaxf(rintf(__fdiv_rn(x[j], step)), 0.0f), 15.0f)) << (4 * j);
+            }
+        }
+        if (!w.active) continue;
+        uint8_t* rec = pool + block;
+        *reinterpret_cast<uint32_t*>(rec + (w.val ? B::VALS : B::KEYS) + slot * B::ROW + w.part * 4) = code;
+        if (w.part == 0) {
+            const uint32_t base16 = finite ? __float_as_uint(lo) >> 16 : 0x7fc0u;
+            *reinterpret_cast<uint32_t*>(rec + (w.val ? B::VPAIR : B::KPAIR) + slot * 4) = step16 | (base16 << 16);
         }
     }
-    if (!active) return;
-    const int slot = pos % kKvBlock;
-    uint8_t* block = d.pools.pool[r] + off;
-    *reinterpret_cast<uint32_t*>(block + (val ? B::VALS : B::KEYS) + slot * B::ROW + part * 4) = code;
-    if (part == 0) {
-        const uint32_t base16 = finite ? __float_as_uint(lo) >> 16 : 0x7fc0u;
-        *reinterpret_cast<uint32_t*>(block + (val ? B::VPAIR : B::KPAIR) + slot * 4) = step16 | (base16 << 16);
-    }
 }
 
-template <int HD>
-__global__ void __launch_bounds__(kThreads) kv4_load_kernel(KvLoadDesc d) {
+template <int HD, int ROWS>
+__global__ void __launch_bounds__(kThreads) kv4_load_kernel(const __grid_constant__ KvLoadDesc d) {
     using B = KvBlock<HD>;
-    constexpr int LANES = HD / 8, SUB = 32 / LANES;
     pdl_wait();
     pdl_trigger();
+    const Task<HD, ROWS> w(d.seqs, d.pools);
+    if (!w.any) return;
     const int lane = threadIdx.x & 31;
-    const int subs = 2 * d.pools.kv_heads, groups = (subs + SUB - 1) / SUB;
-    const int64_t warp = static_cast<int64_t>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5);
-    const int64_t per_row = static_cast<int64_t>(d.pools.t) * groups;
-    if (warp >= d.seqs.n * per_row) return;
-    const int row = static_cast<int>(warp / per_row);
-    const int rest = static_cast<int>(warp - row * per_row);
-    const int r = rest / groups, sub = (rest - r * groups) * SUB + lane / LANES;
-    const int part = lane % LANES;
-    const int head = sub >> 1;
-    const bool val = sub & 1;
-
-    int seq, pos;
-    const bool found = row_place(d.seqs, row, lane, seq, pos);
-    if (!found) raise_status(d.seqs.status, TP_ERR_INVALID_ARG);
-    if (sub >= subs || !(val ? d.with_v : d.with_k)) return;
-    int64_t off = -1;
-    if (found && pos >= 0) {
-        off = kv_block_offset(d.seqs.table + seq * d.seqs.max_blocks, d.seqs.max_blocks, d.pools.pages,
-                              d.pools.page_shift, d.pools.kv_heads, head, pos / kKvBlock, B::BYTES);
-        if (off < 0) raise_status(d.seqs.status, TP_ERR_INVALID_ARG);
-    }
-    float y[8] = {};
-    if (off >= 0) {
-        const int slot = pos % kKvBlock;
-        const uint8_t* block = d.pools.pool[r] + off;
-        const uint32_t code =
-            *reinterpret_cast<const uint32_t*>(block + (val ? B::VALS : B::KEYS) + slot * B::ROW + part * 4);
-        const uint32_t pair = *reinterpret_cast<const uint32_t*>(block + (val ? B::VPAIR : B::KPAIR) + slot * 4);
-        const float step = __uint_as_float(pair << 16), base = __uint_as_float(pair & 0xffff0000u);
+    RowAt at{-1, 0};
+    if (lane < w.rows) at = row_at<HD>(d.seqs, d.pools, w.row0 + lane);
+    if (at.block == -2) raise_status(d.seqs.status, TP_ERR_INVALID_ARG);
+    const bool wanted = w.active && (w.val ? d.with_v : d.with_k);
+    const uint8_t* pool = d.pools.pool[w.r] + (static_cast<int64_t>(w.head) << d.pools.page_shift) * B::BYTES;
+    uint32_t code[ROWS], pair[ROWS];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) y[i] = fmaf(step, static_cast<float>((code >> (4 * i)) & 15u), base);
+    for (int i = 0; i < ROWS; ++i) {
+        const int64_t block = __shfl_sync(0xffffffffu, at.block, i);
+        const int slot = __shfl_sync(0xffffffffu, at.slot, i);
+        code[i] = pair[i] = 0;
+        if (block >= 0 && wanted) {
+            const uint8_t* rec = pool + block;
+            code[i] = *reinterpret_cast<const uint32_t*>(rec + (w.val ? B::VALS : B::KEYS) + slot * B::ROW + w.part * 4);
+            pair[i] = *reinterpret_cast<const uint32_t*>(rec + (w.val ? B::VPAIR : B::KPAIR) + slot * 4);
+        }
     }
-    const int64_t at = row * (val ? d.ldv : d.ldk) + head * HD + part * 8;
-    void* out = val ? d.v[r] : d.k[r];
-    if (d.out_f32) {
-        float4* p = reinterpret_cast<float4*>(static_cast<float*>(out) + at);
-        p[0] = make_float4(y[0], y[1], y[2], y[3]);
-        p[1] = make_float4(y[4], y[5], y[6], y[7]);
-    } else {
-        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(out) + at) =
-            make_uint4(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]), pack_bf16x2(y[4], y[5]), pack_bf16x2(y[6], y[7]));
+    if (!wanted) return;
+    const int64_t ld = w.val ? d.ldv : d.ldk;
+    const int64_t out0 = w.row0 * ld + w.head * HD + w.part * 8;
+    void* out = w.val ? d.v[w.r] : d.k[w.r];
+#pragma unroll
+    for (int i = 0; i < ROWS; ++i) {
+        if (i >= w.rows) break;
+        const float step = __uint_as_float(pair[i] << 16), base = __uint_as_float(pair[i] & 0xffff0000u);
+        float y[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j)          // 2^23 + u in the low bits: no conversion, of which there are few a cycle
+            y[j] = fmaf(step, __uint_as_float(((code[i] >> (4 * j)) & 15u) | 0x4b000000u) - 8388608.0f, base);
+        if (d.out_f32) {
+            float4* p = reinterpret_cast<float4*>(static_cast<float*>(out) + out0 + i * ld);
+            p[0] = make_float4(y[0], y[1], y[2], y[3]);
+            p[1] = make_float4(y[4], y[5], y[6], y[7]);
+        } else {
+            *reinterpret_cast<uint4*>(static_cast<uint16_t*>(out) + out0 + i * ld) =
+                make_uint4(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]), pack_bf16x2(y[4], y[5]), pack_bf16x2(y[6], y[7]));
+        }
     }
 }
 
-int64_t warps_of(int64_t n, const KvPools& p, int head_dim) {
-    const int sub = 32 / (head_dim / 8);
-    return n * p.t * ((2 * p.kv_heads + sub - 1) / sub);
-}
+constexpr int kRows = 4;
 
-template <typename Desc, typename K128, typename K64>
-tp_status launch_rows(const Desc& d, K128 k128, K64 k64, cudaStream_t stream) {
-    const int64_t warps = warps_of(d.seqs.n, d.pools, d.head_dim);
+// Four rows a warp where that leaves 32 warps for an SM, else one.
+template <typename Desc, typename Many, typename One>
+tp_status launch_rows(const Desc& d, Many many, One one, cudaStream_t stream) {
+    const int sub = 32 / (d.head_dim / 8);
+    const int64_t per = static_cast<int64_t>(d.pools.t) * ((2 * d.pools.kv_heads + sub - 1) / sub);
+    const int sms = device_sms();
+    if (sms <= 0) return TP_ERR_CUDA;
+    const bool few = (d.seqs.n + kRows - 1) / kRows * per < static_cast<int64_t>(sms) * 32;
+    const int64_t warps = (few ? d.seqs.n : (d.seqs.n + kRows - 1) / kRows) * per;
     const int64_t blocks = (warps + kThreads / 32 - 1) / (kThreads / 32);
     if (blocks > INT32_MAX) return TP_ERR_UNSUPPORTED;
     const dim3 grid(static_cast<unsigned>(blocks));
-    const cudaError_t e = d.head_dim == 128 ? launch_pdl(k128, grid, dim3(kThreads), 0, stream, d)
-                                            : launch_pdl(k64, grid, dim3(kThreads), 0, stream, d);
-    return e == cudaSuccess ? TP_OK : TP_ERR_CUDA;
+    return launch_pdl(few ? one : many, grid, dim3(kThreads), 0, stream, d) == cudaSuccess ? TP_OK : TP_ERR_CUDA;
 }
 
 }  // namespace
 
 tp_status launch_kv4_append(const KvAppendDesc& d, cudaStream_t stream) {
-    return launch_rows(d, kv4_append_kernel<128>, kv4_append_kernel<64>, stream);
+    return d.head_dim == 128 ? launch_rows(d, kv4_append_kernel<128, kRows>, kv4_append_kernel<128, 1>, stream)
+                             : launch_rows(d, kv4_append_kernel<64, kRows>, kv4_append_kernel<64, 1>, stream);
 }
 
 tp_status launch_kv4_load(const KvLoadDesc& d, cudaStream_t stream) {
-    return launch_rows(d, kv4_load_kernel<128>, kv4_load_kernel<64>, stream);
+    return d.head_dim == 128 ? launch_rows(d, kv4_load_kernel<128, kRows>, kv4_load_kernel<128, 1>, stream)
+                             : launch_rows(d, kv4_load_kernel<64, kRows>, kv4_load_kernel<64, 1>, stream);
 }
 
 }  // namespace tpk
