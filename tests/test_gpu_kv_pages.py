@@ -223,3 +223,22 @@ def test_pages_and_beams_in_a_graph():
     g.replay()
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(plain, got))
+
+
+def test_compact_large_tables():
+    """More pages than one block takes."""
+    rng = np.random.default_rng(12)
+    rows, cols, ps, pages = 700, 40, 16, 60000
+    table, lens = tables(rng, rows, cols, ps, pages, 0.3)
+    want = K.compact(table, lens, ps, pages)
+    got = tp.tp_kv_compact(dev(table), dev(lens), None, page_size=ps, pages=pages)
+    assert np.array_equal(got[0].cpu().numpy(), want[0]) and np.array_equal(got[1].cpu().numpy(), want[1])
+    assert got[2].tolist() == want[2]
+
+
+@pytest.mark.parametrize("rows,cols,pages", [(2048, 31, 12288), (1, 65535, 12288), (2048, 32, 12289), (2049, 1, 100)])
+def test_fork_at_the_limits_of_one_block(rows, cols, pages):
+    rng = np.random.default_rng(13)
+    table = rng.integers(0, pages, (rows, cols)).astype(np.int32)
+    lens = rng.integers(0, min(cols, max(1, pages // rows)) * 16 + 1, rows).astype(np.int32)
+    check_fork(table, lens, rng.integers(0, rows, rows), 1, 16, pages)
