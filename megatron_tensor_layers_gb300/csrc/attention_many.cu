@@ -2,18 +2,22 @@
 // prompts): matrix products on the 5th-generation tensor cores, bound by them
 // and by the exponentials.
 //
-// A thread block takes 256 columns (a column is one row's query head) of one kv
-// head as two tiles of 128, and walks the cached tokens 128 at a time:
+// A pair of thread blocks (a cluster, tcgen05 cta_group::2) takes 512 columns (a
+// column is one row's query head) of one kv head as two tiles of 256, half of
+// each tile in each block, and walks the cached tokens 128 at a time:
 //   S = Q K^T          tcgen05, Q and K from shared memory, S in TMEM;
 //   P = 2^(c S - m)    one thread per column, fp32, P as fp16 over S in TMEM;
 //   O += P V           tcgen05, P from TMEM, V^T from shared memory, O in TMEM.
-// Warps 0-3 and 4-7 are the softmax of one tile each and take turns with the
-// tensor core, warps 8-11 turn codes into operands (two cache blocks of 16
-// tokens each), warp 12 issues the products.
+// In each block warps 0-3 and 4-7 are the softmax of one tile each and take turns
+// with the tensor core, warps 8-11 turn codes into operands; warp 12 of the even
+// block issues the products of both.  Of a step each block unpacks and holds half
+// the keys and half of the values' dimensions, which is all that a pair's
+// products need: against single blocks of 256 columns that halves the unpacking
+// and the traffic of K and V^T through shared memory, which bounded them.
 //
 // Codes to operands.  A code is an fp16 subnormal u 2^-24 (or 16 u 2^-24) after
 // one mask, and one HFMA2 makes the fp16 value (s u + b) 2^-F of two elements:
-// 9 instructions for 8 keys, shared by all 256 columns.  F is the exponent of
+// 9 instructions for 8 keys, shared by all 512 columns.  F is the exponent of
 // the largest step or base of 32 tokens, so that nothing overflows; a value is
 // rounded once, by at most 2^-11 of itself or 2^-25 of their scale 2^F.  The
 // scale of K enters the exponent's factor c, the scale of V the exponent itself
@@ -29,10 +33,9 @@
 // and has no maximum in it (128 fewer operations on the pipe that the unpacking
 // needs too).
 //
-// What bounds it now is shared memory: per step Q and K are read for both
-// tiles' S, V for both O, and the operands written, 256 KB at 128 bytes a cycle.
-// Codes therefore go from global memory to registers (a ring of records in
-// shared memory, filled by bulk copies, measured 5 % slower).
+// Codes go from global memory to registers, one step ahead; a ring of records in
+// shared memory, filled by bulk copies, measured 5 % slower (its reads and writes
+// compete with the operands').
 //
 // A value row that stands for NaN is put in as 0 and its token noted; a column
 // that sees such a token gets a NaN sum, the others are not touched by it.
@@ -53,18 +56,20 @@ constexpr int kLaunchRegs = 128, kSoftmaxRegs = 192, kUnpackRegs = 88, kIssueReg
 static_assert(256 * kSoftmaxRegs + 32 * kUnpackWarps * kUnpackRegs + 128 * kIssueRegs <= kThreads * kLaunchRegs,
               "a warpgroup would wait for registers that never come");
 constexpr int kTile = 128;           // tokens of a step, columns of a tile
-constexpr int kCols = 2 * kTile;     // columns of a thread block
+constexpr int kCols = 4 * kTile;     // columns of a pair of thread blocks
 constexpr int kInfo = 4;
 constexpr float kNegInf = -INFINITY;
 constexpr float kMost = 4096.0f;     // sum of a step's 2^(x - m) up to which the old maximum will do (P is 8 times as much at most)
 
 template <int HD>
 struct Cfg {
-    static constexpr int QB = kTile * HD * 2;            // one tile of Q
-    static constexpr int KB = kTile * HD * 2;            // K, and V^T
-    static constexpr int ATOM = kTile * 128;             // 64 elements of 128 rows
-    static constexpr int VATOM = HD * 128;               // 64 tokens of HD rows
-    static constexpr int Q = 0, K = 2 * QB, V = K + 2 * KB, SMEM = V + 2 * KB + 1024;
+    static constexpr int QB = kTile * HD * 2;            // one tile of Q: 128 columns
+    static constexpr int KB = kTile / 2 * HD * 2;        // this block's half of K: 64 tokens
+    static constexpr int VB = HD / 2 * kTile * 2;        // and of V^T: half of the dimensions
+    static constexpr int QATOM = kTile * 128;            // 64 elements of 128 rows
+    static constexpr int KATOM = kTile / 2 * 128;        // 64 elements of 64 tokens
+    static constexpr int VATOM = HD / 2 * 128;           // 64 tokens of HD / 2 rows
+    static constexpr int Q = 0, K = 2 * QB, V = K + 2 * KB, SMEM = V + 2 * VB + 1024;
     static constexpr int S_COL = 0, O_COL = 256;         // TMEM columns: S of the tiles, then O of the tiles
 };
 
@@ -84,13 +89,13 @@ __host__ __device__ constexpr uint32_t idesc_f16(int m, int n) {
     return (1u << 4) | (static_cast<uint32_t>(n >> 3) << 17) | (static_cast<uint32_t>(m >> 4) << 24);
 }
 
-// D[tmem] (+)= A[tmem] * B[smem]^T, issued by one thread.
-__device__ __forceinline__ void tc_mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
-                                          uint32_t accumulate) {
+// D[tmem of both] (+)= A[tmem of both] * B[smem of both]^T, issued by the even block.
+__device__ __forceinline__ void tc_mma_ts_pair(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
+                                               uint32_t accumulate) {
     asm volatile(
         "{\n\t.reg .pred p;\n\t"
         "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
         "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
         : "memory");
 }
@@ -155,17 +160,23 @@ __device__ __forceinline__ void fewer_registers() {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 
+// q_full, p_full and the peer's two are awaited by the even block, which issues the products; the others are each
+// block's own (a commit arrives at both blocks').  An arrival with release at the other block's barrier waits for
+// all that its thread has in flight, a microsecond for a thread that loads; so the unpacking warps arrive at
+// their own block's barriers, the odd block's idle warp passes that on, and the softmax, whose P is in TMEM by then
+// (tcgen05.wait::st and a tcgen05 fence), arrives without release.
 struct Bars {
-    uint64_t q_full, k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_full[2], o_full;
+    uint64_t q_full, p_full[2], k_peer[2], v_peer[2];
+    uint64_t k_full[2], v_full[2], k_empty[2], v_empty[2], s_full[2], o_full, info[kInfo];
 };
 
-// What the thread block works on.
+// What the pair works on.
 struct Item {
     int seq, first_row, rows, len, tile, head;
 };
 
 template <int HD>
-__global__ void __launch_bounds__(kThreads, 1) kv4_attention_many_kernel(const __grid_constant__ AttnArgs a) {
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) kv4_attention_many_kernel(const __grid_constant__ AttnArgs a) {
     using B = KvBlock<HD>;
     using C = Cfg<HD>;
     extern __shared__ uint8_t smem_raw[];
@@ -183,12 +194,13 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_many_kernel(const _
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t sm = (smem_u32(smem_raw) + 1023u) & ~1023u;
     const int heads = a.pools.t * a.pools.kv_heads;
+    const int half = static_cast<int>(cluster_ctarank());
     pdl_wait();
     pdl_trigger();
 
-    // ---- which sequence and tile: block / heads counts tiles of 256 columns over the sequences
+    // ---- which sequence and tile: pair / heads counts tiles of 512 columns over the sequences
     {
-        const int64_t want = blockIdx.x / heads;
+        const int64_t want = (blockIdx.x >> 1) / heads;
         const int per = (a.seqs.nseq + kThreads - 1) / kThreads;
         auto tiles_of = [&](int s) -> int64_t {
             const int64_t cols = static_cast<int64_t>(seq_rows(a.seqs, s).count) * a.group;
@@ -225,7 +237,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_many_kernel(const _
             it.len = max(a.seqs.lens[s], 0);
             // the last tiles see the most tokens: they start first
             it.tile = static_cast<int>(tiles_of(s) - 1 - u);
-            it.head = static_cast<int>(blockIdx.x % heads);
+            it.head = static_cast<int>((blockIdx.x >> 1) % heads);
             s_item = it;
             s_found = 1;
         }
@@ -240,24 +252,28 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_many_kernel(const _
     const int64_t first_pos = pos0 + col0 / a.group, last_pos = pos0 + (col0 + cols - 1) / a.group;
     const Spans span = visible_spans(a, first_pos, last_pos, kTile);
     const int steps = span.count;
+    const int tiles = cols > 2 * kTile ? 2 : 1;          // of 256 columns, half of them in each block
 
-    if (warp == 0) tmem_alloc<512>(smem_u32(&s_tmem));
+    if (warp == 0) tmem_alloc_pair<512>(smem_u32(&s_tmem));
     if (tid == 0) {
         s_abort = 0;
-        mbar_init(smem_u32(&bars.q_full), kCols);
+        mbar_init(smem_u32(&bars.q_full), 2 * 8);
         for (int i = 0; i < 2; ++i) {
             mbar_init(smem_u32(&bars.k_full[i]), kUnpackWarps);
-            mbar_init(smem_u32(&bars.k_empty[i]), 1);
             mbar_init(smem_u32(&bars.v_full[i]), kUnpackWarps);
+            mbar_init(smem_u32(&bars.k_peer[i]), 1);
+            mbar_init(smem_u32(&bars.v_peer[i]), 1);
+            mbar_init(smem_u32(&bars.p_full[i]), 2 * 4);
+            mbar_init(smem_u32(&bars.k_empty[i]), 1);
             mbar_init(smem_u32(&bars.v_empty[i]), 1);
             mbar_init(smem_u32(&bars.s_full[i]), 1);
-            mbar_init(smem_u32(&bars.p_full[i]), 4);
         }
         mbar_init(smem_u32(&bars.o_full), 1);
+        for (int i = 0; i < kInfo; ++i) mbar_init(smem_u32(&bars.info[i]), kUnpackWarps);
     }
     fence_barrier_init();
     tc_fence_before();
-    __syncthreads();
+    cluster_sync();
     tc_fence_after();
     const uint32_t tmem = s_tmem;
     bool ok = true;
@@ -266,7 +282,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_many_kernel(const _
         more_registers<kSoftmaxRegs>();
         // ------------------------------------------------ softmax: one thread per column
         const int t = warp >> 2;                         // tile
-        const int ci = tid;                              // column of the block
+        const int ci = t * 2 * kTile + half * kTile + (tid & 127);       // column of the pair
         const bool have = ci < cols;
         const int cc = col0 + ci;
         const int r = have ? cc / a.group : 0;
@@ -290,7 +306,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_many_kernel(const _
             if (a.scale_log2 < 0.0f) up = -up;
             if (a.scale_log2 == 0.0f) up = 0.0f;
             cmul = a.scale_log2 == 0.0f ? 1.0f : fabsf(a.scale_log2) * pow2_field(min(127 - k, 254));
-            const uint32_t row = sm + C::Q + t * C::QB + (ci & 127) * 128;
+            const uint32_t row = sm + C::Q + t * C::QB + (tid & 127) * 128;
 #pragma unroll
             for (int i = 0; i < HD / 8; ++i) {           // a word of eight codes: its order of elements
                 float x[8];
@@ -299,24 +315,26 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_many_kernel(const _
                     x[2 * e] = __uint_as_float(raw[4 * i + e] << 16) * up;
                     x[2 * e + 1] = __uint_as_float(raw[4 * i + e] & 0xffff0000u) * up;
                 }
-                st_shared_v4(row + (i >> 3) * C::ATOM + (((i & 7) ^ (ci & 7)) << 4), pack_f16x2(x[0], x[4]),
+                st_shared_v4(row + (i >> 3) * C::QATOM + (((i & 7) ^ (tid & 7)) << 4), pack_f16x2(x[0], x[4]),
                              pack_f16x2(x[1], x[5]), pack_f16x2(x[2], x[6]), pack_f16x2(x[3], x[7]));
             }
         }
         fence_proxy_async_cta();
-        mbar_arrive(smem_u32(&bars.q_full));
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&bars.q_full), 0));
 
         const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
         const uint32_t s_addr = tmem + lane_base + C::S_COL + t * kTile;
         const uint32_t o_addr = tmem + lane_base + C::O_COL + t * HD;
-        // positions of the tile's columns, for whole-tile decisions
-        const int tile_lo = pos0 + (col0 + t * kTile) / a.group;
-        const int tile_hi = pos0 + (col0 + max(min(cols, (t + 1) * kTile), t * kTile + 1) - 1) / a.group;
+        // positions of this block's columns of the tile, for whole-step decisions
+        const int tile0 = t * 2 * kTile + half * kTile;
+        const int tile_lo = pos0 + (col0 + tile0) / a.group;
+        const int tile_hi = pos0 + (col0 + max(min(cols, tile0 + kTile), tile0 + 1) - 1) / a.group;
         float m = kNegInf, l = 0.0f;
         int vref = 0;
-        for (int j = 0; j < steps && ok; ++j) {
+        for (int j = 0; j < steps && t < tiles && ok; ++j) {
             const int tok0 = (j < span.front ? j : span.start + j - span.front) * kTile;
-            ok = mbar_wait_warp(smem_u32(&bars.k_full[j & 1]), (j >> 1) & 1, &s_abort, a.seqs.status) &&
+            ok = mbar_wait_warp(smem_u32(&bars.info[j % kInfo]), (j / kInfo) & 1, &s_abort, a.seqs.status) &&
                  mbar_wait_warp(smem_u32(&bars.s_full[t]), j & 1, &s_abort, a.seqs.status);
             if (!ok) break;
             tc_fence_after();
@@ -430,16 +448,16 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_many_kernel(const _
             tmem_st_wait();
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(&bars.p_full[t]));
+            if (lane == 0) mbar_arrive_cluster_relaxed(mapa_shared(smem_u32(&bars.p_full[t]), 0));
         }
         // ---- the result
         float scale = 0.0f;
-        if (ok && steps > 0) {
+        if (ok && steps > 0 && t < tiles) {
             ok = mbar_wait_warp(smem_u32(&bars.o_full), 0, &s_abort, a.seqs.status);
             tc_fence_after();
             scale = l == 0.0f ? 0.0f : pow2_field(min(max(vref, 1), 254)) / l;
         }
-        if (ok) {
+        if (ok && t < tiles) {
             uint16_t* dst = a.out[rank] + (it.first_row + r) * a.ldo + (kvh * a.group + h) * HD;
 #pragma unroll 1
             for (int i = 0; i < HD; i += 32) {
@@ -466,89 +484,91 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_many_kernel(const _
     } else if (warp < 8 + kUnpackWarps) {
         if constexpr (kUnpackRegs > kLaunchRegs) more_registers<kUnpackRegs>(); else fewer_registers<kUnpackRegs>();
         // ------------------------------------------------ codes to operands
-        const int id = tid - 256, w = warp - 8;
+        // A warp takes a block of keys (16 tokens of this half of the step) and, for this half of the
+        // dimensions, 32 tokens' values; what the softmax must know, of the latter tokens.  F of the keys is
+        // that of 32 tokens, so the warp looks at the pairs of its block's neighbour too.
+        const int w = warp - 8, kq = 2 * half + (w >> 1);
         const int32_t* row = a.seqs.table + it.seq * a.seqs.max_blocks;
         const uint8_t* pool = a.pools.pool[rank];
-        constexpr int PARTS = HD / 32, KU = PARTS;       // 16-byte parts (32 elements) of a key; units of a thread
-        constexpr int VW = HD / 64;                      // words of a value row that a thread takes of eight tokens
-        // A warp takes 32 tokens, so nothing but their shared-memory words passes between its lanes.
-        const int tg = 4 * w + (lane & 3), dw = lane >> 2;
+        constexpr int PARTS = HD / 32, KU = PARTS / 2;   // 16-byte parts (32 elements) of a key; units of a lane
+        // values: a lane takes one word (8 dimensions) of eight tokens; with HD 64 two lanes share a word, half each
+        constexpr int HALVES = HD == 128 ? 2 : 1;
+        const int tg = 4 * w + (lane & 3), word = (lane >> 2) & (HD / 16 - 1);
+        const int half0 = HD == 128 ? word & 1 : lane >> 4, flip0 = HD == 128 ? 0 : word & 1;
         auto first_block = [&](int j) { return (j < span.front ? j : span.start + j - span.front) * (kTile / kKvBlock); };
-        // lanes 0 and 1: the page of the warp's two blocks of step j; -2 past the last visible token, where
-        // nothing is read
+        // lanes 0, 1: the values' two blocks; lanes 2, 3: those of the keys' 32 tokens
+        const int my_block = 2 * (lane & 2 ? kq : w) + (lane & 1);
+        // the page of the lane's block of step j; -2 past the last visible token, where nothing is read
         auto fetch_page = [&](int j) -> int {
-            const int64_t b = first_block(j) + 2 * w + (lane & 1);
+            const int64_t b = first_block(j) + my_block;
             return j < steps && b * kKvBlock <= last_pos ? kv_page_at(row, a.seqs.max_blocks, a.pools.page_shift, b) : -2;
         };
         auto offset_of = [&](int j, int page) -> int64_t {
             const int64_t off = kv_page_offset(page, a.pools.pages, a.pools.page_shift, a.pools.kv_heads, kvh,
-                                               first_block(j) + 2 * w + (lane & 1), B::BYTES);
+                                               first_block(j) + my_block, B::BYTES);
             if (off < 0 && page != -2) raise_status(a.seqs.status, TP_ERR_INVALID_ARG);
             return off;
         };
-        auto fetch_pairs = [&](int j, int64_t off, uint32_t& kp, uint32_t& vp) {
-            const int64_t b = __shfl_sync(0xffffffffu, off, lane >> 4);
-            kp = vp = 0;
-            if (b >= 0 && static_cast<int64_t>(first_block(j)) * kKvBlock + id <= last_pos) {
-                kp = __ldg(reinterpret_cast<const uint32_t*>(pool + b + B::KPAIR) + (lane & 15));
-                vp = __ldg(reinterpret_cast<const uint32_t*>(pool + b + B::VPAIR) + (lane & 15));
+        // pairs of token `lane` of the 32: keys and values where the values are, keys where the keys are
+        struct Pairs {
+            uint32_t k, v, own;
+        };
+        auto fetch_pairs = [&](int j, int64_t off) {
+            Pairs p{0, 0, 0};
+            const int64_t b = __shfl_sync(0xffffffffu, off, lane >> 4), o = __shfl_sync(0xffffffffu, off, 2 + (lane >> 4));
+            const int64_t first = static_cast<int64_t>(first_block(j)) * kKvBlock + lane;
+            if (b >= 0 && first + 32 * w <= last_pos) {
+                p.k = __ldg(reinterpret_cast<const uint32_t*>(pool + b + B::KPAIR) + (lane & 15));
+                p.v = __ldg(reinterpret_cast<const uint32_t*>(pool + b + B::VPAIR) + (lane & 15));
             }
+            if (o >= 0 && first + 32 * kq <= last_pos) p.own = __ldg(reinterpret_cast<const uint32_t*>(pool + o + B::KPAIR) + (lane & 15));
+            return p;
         };
         uint4 kc[KU];
         auto fetch_keys = [&](int64_t off) {
+            const int64_t b = __shfl_sync(0xffffffffu, off, 2 + (w & 1));
 #pragma unroll
-            for (int i = 0; i < KU; ++i) {
-                const int u = i * 32 + lane, token = u / PARTS, part = u % PARTS;      // token of the warp's 32
-                const int64_t b = __shfl_sync(0xffffffffu, off, token >> 4);
-                kc[i] = b >= 0 ? __ldg(reinterpret_cast<const uint4*>(pool + b + B::KEYS + (token & 15) * B::ROW) + part)
+            for (int i = 0; i < KU; ++i)
+                kc[i] = b >= 0 ? __ldg(reinterpret_cast<const uint4*>(pool + b + B::KEYS) + i * 32 + lane)
                                : make_uint4(0, 0, 0, 0);
-            }
         };
-        uint32_t vc[8][VW];
+        uint32_t vc[8];
         auto fetch_values = [&](int64_t off) {
             const int64_t b = __shfl_sync(0xffffffffu, off, (lane >> 1) & 1);
+            const uint8_t* p = pool + b + B::VALS + (lane & 1) * 8 * B::ROW + half * (B::ROW / 2) + word * 4;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const uint8_t* p = pool + b + B::VALS + ((tg & 1) * 8 + i) * B::ROW + dw * 4 * VW;
-                if constexpr (VW == 2) {
-                    const uint2 v = b >= 0 ? __ldg(reinterpret_cast<const uint2*>(p)) : make_uint2(0, 0);
-                    vc[i][0] = v.x, vc[i][1] = v.y;
-                } else {
-                    vc[i][0] = b >= 0 ? __ldg(reinterpret_cast<const uint32_t*>(p)) : 0u;
-                }
-            }
+            for (int i = 0; i < 8; ++i) vc[i] = b >= 0 ? __ldg(reinterpret_cast<const uint32_t*>(p + i * B::ROW)) : 0u;
         };
         // Registers of a step are refilled as soon as they are used: the loads of step j + 1 run under the
         // conversions of step j, and the page numbers are one more step ahead.
         int page_next = fetch_page(1);
         int64_t off = offset_of(0, fetch_page(0));
-        uint32_t kp, vp;
-        fetch_pairs(0, off, kp, vp);
+        Pairs pair = fetch_pairs(0, off);
         fetch_keys(off);
         fetch_values(off);
         for (int j = 0; j < steps; ++j) {
             const int st = j & 1;
             const uint32_t there = __ballot_sync(0xffffffffu, off >= 0) & 3u;
-            const bool vnan = ((vp >> 16) & 0x7f80u) == 0x7f80u || (vp & 0x7f80u) == 0x7f80u;
-            if (vnan) vp = 0;
-            // F of the quarter: s 2^(127 - F) below 2^-8, |b| 2^(127 - F) below 2^15
+            const bool vnan = ((pair.v >> 16) & 0x7f80u) == 0x7f80u || (pair.v & 0x7f80u) == 0x7f80u;
+            if (vnan) pair.v = 0;
+            // F of 32 tokens: s 2^(127 - F) below 2^-8, |b| 2^(127 - F) below 2^15
             auto field = [](uint32_t p) {
                 const int es = static_cast<int>((p >> 7) & 0xffu), eb = static_cast<int>((p >> 23) & 0xffu);
                 return max(es + 9, (eb == 255 ? 0 : eb) - 14);
             };
-            const int kF = min(max(__reduce_max_sync(0xffffffffu, field(kp)), 24), 253);
-            const int vF = min(max(__reduce_max_sync(0xffffffffu, field(vp)), 24), 253);
+            const int kF = min(max(__reduce_max_sync(0xffffffffu, field(pair.k)), 24), 253);
+            const int vF = min(max(__reduce_max_sync(0xffffffffu, field(pair.v)), 24), 253);
+            const int oF = min(max(__reduce_max_sync(0xffffffffu, field(pair.own)), 24), 253);
             const uint32_t nan_set = __ballot_sync(0xffffffffu, vnan);
             __syncwarp();                                // the lanes are done with the words of step j - 1
             {
                 // the step times 2^24: codes are u 2^-24
-                const float ks = __uint_as_float(kp << 16) * pow2_field(278 - kF);
-                const float kb = __uint_as_float(kp & 0xffff0000u) * pow2_field(254 - kF);
-                const float vs = __uint_as_float(vp << 16) * pow2_field(278 - vF);
-                const float vb = __uint_as_float(vp & 0xffff0000u) * pow2_field(254 - vF);
-                s_key[id] = pack_f16x2(ks, kb);
-                s_vstep[id] = static_cast<uint16_t>(pack_f16x2(vs, 0.0f));
-                s_vbase[id] = static_cast<uint16_t>(pack_f16x2(vb, 0.0f));
+                s_key[w * 32 + lane] = pack_f16x2(__uint_as_float(pair.own << 16) * pow2_field(278 - oF),
+                                                  __uint_as_float(pair.own & 0xffff0000u) * pow2_field(254 - oF));
+                const uint32_t sb = pack_f16x2(__uint_as_float(pair.v << 16) * pow2_field(278 - vF),
+                                               __uint_as_float(pair.v & 0xffff0000u) * pow2_field(254 - vF));
+                s_vstep[w * 32 + lane] = static_cast<uint16_t>(sb);
+                s_vbase[w * 32 + lane] = static_cast<uint16_t>(sb >> 16);
                 if (lane == 0) {
                     StepInfo& info = s_info[j % kInfo];
                     reinterpret_cast<float*>(&info.kmul)[w] = pow2_field(kF);
@@ -556,26 +576,27 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_many_kernel(const _
                     reinterpret_cast<uint32_t*>(&info.nan)[w] = nan_set;
                     // past the last visible token nothing is there: hidden by position, no matter
                     reinterpret_cast<uint32_t*>(&info.gone)[w] = ~there & 3u;
+                    mbar_arrive(smem_u32(&bars.info[j % kInfo]));
                 }
             }
             __syncwarp();
             off = offset_of(j + 1, page_next);
-            fetch_pairs(j + 1, off, kp, vp);
+            pair = fetch_pairs(j + 1, off);
             page_next = fetch_page(j + 2);
             if (j >= 2) ok = mbar_wait_warp(smem_u32(&bars.k_empty[st]), ((j >> 1) + 1) & 1, &s_abort, a.seqs.status);
             if (!ok) break;
             constexpr uint32_t M0 = 0x000f000fu, M4 = 0x00f000f0u, SIXTEENTH = 0x2c002c00u;   // (1/16, 1/16)
 #pragma unroll
             for (int i = 0; i < KU; ++i) {
-                const int u = i * 32 + lane, token = 32 * w + u / PARTS, part = u % PARTS;
-                const uint32_t sb = s_key[token];
+                const int u = i * 32 + lane, token = kKvBlock * w + u / PARTS, part = u % PARTS;       // of this half
+                const uint32_t sb = s_key[w * 32 + (w & 1) * kKvBlock + u / PARTS];
                 const uint32_t s1 = __byte_perm(sb, sb, 0x1010), b1 = __byte_perm(sb, sb, 0x3232);
                 const uint32_t s16 = hfma2(s1, SIXTEENTH, 0u);
                 // the two halves of the lanes store in another order, so that eight lanes meet eight bank groups
                 const bool flip = part & 2;
                 const uint32_t wd[4] = {flip ? kc[i].z : kc[i].x, flip ? kc[i].w : kc[i].y, flip ? kc[i].x : kc[i].z,
                                         flip ? kc[i].y : kc[i].w};
-                const uint32_t base = sm + C::K + st * C::KB + (part >> 1) * C::ATOM + token * 128;
+                const uint32_t base = sm + C::K + st * C::KB + (part >> 1) * C::KATOM + token * 128;
 #pragma unroll
                 for (int x = 0; x < 4; ++x) {
                     const int chunk = (part & 1) * 4 + (flip ? x ^ 2 : x);
@@ -598,30 +619,30 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_many_kernel(const _
                 uint32_t s16[4];
 #pragma unroll
                 for (int p = 0; p < 4; ++p) s16[p] = hfma2(s1[p], SIXTEENTH, 0u);
-                const uint32_t at = sm + C::V + st * C::KB + (tg >> 3) * C::VATOM;
+                const uint32_t at = sm + C::V + st * C::VB + (tg >> 3) * C::VATOM;
 #pragma unroll
-                for (int x = 0; x < VW; ++x)
+                for (int i = 0; i < HALVES; ++i) {
+                    // dimensions 0-3 or 4-7 of the word, of these 0-1 or 2-3: in another order from lane to
+                    // lane, so that eight lanes meet eight bank groups
+                    const int hw = half0 ^ i;
+                    const uint32_t sel = hw ? 0x7632u : 0x5410u;
+                    uint32_t pr[4];
 #pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        // dimensions 0-3 or 4-7 of the word; odd lanes of dw the other half first (bank groups)
-                        const int hw = i ^ (dw & 1);
-                        const uint32_t sel = hw ? 0x7632u : 0x5410u;
-                        uint32_t pr[4];
+                    for (int p = 0; p < 4; ++p) pr[p] = __byte_perm(vc[2 * p], vc[2 * p + 1], sel);
 #pragma unroll
-                        for (int p = 0; p < 4; ++p) pr[p] = __byte_perm(vc[2 * p][x], vc[2 * p + 1][x], sel);
+                    for (int bi = 0; bi < 2; ++bi) {
+                        const int b = flip0 ^ bi, d = word * 8 + hw * 4 + b * 2;    // and d + 1, of this half
+                        uint32_t q[4];
 #pragma unroll
-                        for (int b = 0; b < 2; ++b) {
-                            const int d = dw * 8 * VW + x * 8 + hw * 4 + b * 2;     // and d + 1
-                            st_shared_v4(at + d * 128 + (((tg & 7) ^ (d & 7)) << 4), hfma2(pr[0] & M0, s1[0], b1[0]),
-                                         hfma2(pr[1] & M0, s1[1], b1[1]), hfma2(pr[2] & M0, s1[2], b1[2]),
-                                         hfma2(pr[3] & M0, s1[3], b1[3]));
-                            st_shared_v4(at + (d + 1) * 128 + (((tg & 7) ^ ((d + 1) & 7)) << 4),
-                                         hfma2(pr[0] & M4, s16[0], b1[0]), hfma2(pr[1] & M4, s16[1], b1[1]),
-                                         hfma2(pr[2] & M4, s16[2], b1[2]), hfma2(pr[3] & M4, s16[3], b1[3]));
-#pragma unroll
-                            for (int p = 0; p < 4; ++p) pr[p] >>= 8;
-                        }
+                        for (int p = 0; p < 4; ++p) q[p] = pr[p] >> (8 * b);
+                        st_shared_v4(at + d * 128 + (((tg & 7) ^ (d & 7)) << 4), hfma2(q[0] & M0, s1[0], b1[0]),
+                                     hfma2(q[1] & M0, s1[1], b1[1]), hfma2(q[2] & M0, s1[2], b1[2]),
+                                     hfma2(q[3] & M0, s1[3], b1[3]));
+                        st_shared_v4(at + (d + 1) * 128 + (((tg & 7) ^ ((d + 1) & 7)) << 4), hfma2(q[0] & M4, s16[0], b1[0]),
+                                     hfma2(q[1] & M4, s16[1], b1[1]), hfma2(q[2] & M4, s16[2], b1[2]),
+                                     hfma2(q[3] & M4, s16[3], b1[3]));
                     }
+                }
             }
             fence_proxy_async_cta();
             __syncwarp();
@@ -630,11 +651,11 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_many_kernel(const _
         }
     } else {
         fewer_registers<kIssueRegs>();
-        if (warp == 8 + kUnpackWarps && steps > 0) {
-            // ------------------------------------------------ the products
-            constexpr uint32_t QK = idesc_f16(128, 128), PV = idesc_f16(128, HD);
+        if (warp == 8 + kUnpackWarps && half == 0 && steps > 0) {
+            // ------------------------------------------------ the products of both blocks
+            constexpr uint32_t QK = idesc_f16(256, 128), PV = idesc_f16(256, HD);
             auto wait = [&](uint64_t& b, int parity) {
-                ok = ok && mbar_wait_warp(smem_u32(&b), parity, &s_abort, a.seqs.status);
+                ok = ok && mbar_wait_cluster_warp(smem_u32(&b), parity, &s_abort, a.seqs.status);
                 tc_fence_after();
                 return ok;
             };
@@ -643,52 +664,60 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_many_kernel(const _
                 const uint64_t kd = sw128_kmajor_desc(sm + C::K + (j & 1) * C::KB);
                 if (elect_one()) {
 #pragma unroll
-                    for (int k = 0; k < HD / 16; ++k) {
-                        const uint64_t o = static_cast<uint64_t>(((k >> 2) * C::ATOM + (k & 3) * 32) >> 4);
-                        tc_mma(tmem + C::S_COL + t * kTile, qd + o, kd + o, QK, k > 0);
-                    }
-                    tc_commit(smem_u32(&bars.s_full[t]));
-                    if (t == 1) tc_commit(smem_u32(&bars.k_empty[j & 1]));
+                    for (int k = 0; k < HD / 16; ++k)
+                        tc_mma_pair(tmem + C::S_COL + t * kTile, qd + (((k >> 2) * C::QATOM + (k & 3) * 32) >> 4),
+                                    kd + (((k >> 2) * C::KATOM + (k & 3) * 32) >> 4), QK, k > 0);
+                    tc_commit_pair(smem_u32(&bars.s_full[t]), 3);
+                    if (t + 1 == tiles) tc_commit_pair(smem_u32(&bars.k_empty[j & 1]), 3);
                 }
                 __syncwarp();
             };
             auto values = [&](int t, int j) {
-                const uint64_t vd = sw128_kmajor_desc(sm + C::V + (j & 1) * C::KB);
+                const uint64_t vd = sw128_kmajor_desc(sm + C::V + (j & 1) * C::VB);
                 if (elect_one()) {
 #pragma unroll
-                    for (int k = 0; k < kTile / 16; ++k) {
-                        const uint64_t o = static_cast<uint64_t>(((k >> 2) * C::VATOM + (k & 3) * 32) >> 4);
-                        tc_mma_ts(tmem + C::O_COL + t * HD, tmem + C::S_COL + t * kTile + k * 8, vd + o, PV, j > 0 || k > 0);
+                    for (int k = 0; k < kTile / 16; ++k)
+                        tc_mma_ts_pair(tmem + C::O_COL + t * HD, tmem + C::S_COL + t * kTile + k * 8,
+                                       vd + (((k >> 2) * C::VATOM + (k & 3) * 32) >> 4), PV, j > 0 || k > 0);
+                    if (t + 1 == tiles) {
+                        tc_commit_pair(smem_u32(&bars.v_empty[j & 1]), 3);
+                        if (j + 1 == steps) tc_commit_pair(smem_u32(&bars.o_full), 3);
                     }
-                    if (t == 1) tc_commit(smem_u32(&bars.v_empty[j & 1]));
-                    if (t == 1 && j + 1 == steps) tc_commit(smem_u32(&bars.o_full));
                 }
                 __syncwarp();
             };
-            if (wait(bars.q_full, 0) && wait(bars.k_full[0], 0)) {
-                scores(0, 0);
-                scores(1, 0);
-            }
+            auto wait_keys = [&](int j) { return wait(bars.k_full[j & 1], (j >> 1) & 1) && wait(bars.k_peer[j & 1], (j >> 1) & 1); };
+            if (wait(bars.q_full, 0) && wait_keys(0))
+                for (int t = 0; t < tiles; ++t) scores(t, 0);
             for (int j = 0; j < steps && ok; ++j) {
                 const bool more = j + 1 < steps;
-                if (!wait(bars.v_full[j & 1], (j >> 1) & 1) || !wait(bars.p_full[0], j & 1)) break;
-                values(0, j);
-                if (more) {
-                    if (!wait(bars.k_full[(j + 1) & 1], ((j + 1) >> 1) & 1)) break;
-                    scores(0, j + 1);
+                if (!wait(bars.v_full[j & 1], (j >> 1) & 1) || !wait(bars.v_peer[j & 1], (j >> 1) & 1)) break;
+                for (int t = 0; t < tiles; ++t) {
+                    if (!wait(bars.p_full[t], j & 1)) break;
+                    values(t, j);
+                    if (!more) continue;
+                    if (t == 0 && !wait_keys(j + 1)) break;
+                    scores(t, j + 1);
                 }
-                if (!wait(bars.p_full[1], j & 1)) break;
-                values(1, j);
-                if (more) scores(1, j + 1);
+            }
+        }
+        if (warp == 8 + kUnpackWarps && half == 1) {
+            // ------------------------------------------------ tells the even block what this one has unpacked
+            for (int j = 0; j < steps && ok; ++j) {
+                const int st = j & 1, parity = (j >> 1) & 1;
+                ok = mbar_wait_warp(smem_u32(&bars.k_full[st]), parity, &s_abort, a.seqs.status);
+                if (ok && lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&bars.k_peer[st]), 0));
+                ok = ok && mbar_wait_warp(smem_u32(&bars.v_full[st]), parity, &s_abort, a.seqs.status);
+                if (ok && lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&bars.v_peer[st]), 0));
             }
         }
         __syncwarp();
     }
     if (s_abort) spin_ns(1000000);   // products that were issued end before their memory is given back
     tc_fence_before();
-    __syncthreads();
+    cluster_sync();
     tc_fence_after();
-    if (warp == 0) tmem_dealloc<512>(tmem);
+    if (warp == 0) tmem_dealloc_pair<512>(tmem);
 }
 
 template <int HD>
@@ -699,7 +728,7 @@ tp_status launch(const AttnArgs& a, cudaStream_t stream) {
     // as many tiles as n rows in at most nseq sequences can make
     const int64_t cols = static_cast<int64_t>(a.seqs.n) * a.group;
     const int64_t tiles = cols / kCols + std::min<int64_t>(a.seqs.nseq, cols / a.many);
-    const int64_t blocks = tiles * a.pools.t * a.pools.kv_heads;
+    const int64_t blocks = 2 * tiles * a.pools.t * a.pools.kv_heads;
     if (blocks > INT32_MAX) return TP_ERR_UNSUPPORTED;
     const cudaError_t e = launch_pdl(kern, dim3(static_cast<unsigned>(blocks)), dim3(kThreads), Cfg<HD>::SMEM, stream, a);
     return e == cudaSuccess ? TP_OK : TP_ERR_CUDA;
