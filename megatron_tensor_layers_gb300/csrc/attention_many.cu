@@ -654,10 +654,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) kv4_att
         if (warp == 8 + kUnpackWarps && half == 0 && steps > 0) {
             // ------------------------------------------------ the products of both blocks
             constexpr uint32_t QK = idesc_f16(256, 128), PV = idesc_f16(256, HD);
+            // what the other block's threads wrote is behind the peer's barriers alone
             auto wait = [&](uint64_t& b, int parity) {
-                ok = ok && mbar_wait_cluster_warp(smem_u32(&b), parity, &s_abort, a.seqs.status);
+                ok = ok && mbar_wait_warp(smem_u32(&b), parity, &s_abort, a.seqs.status);
                 tc_fence_after();
                 return ok;
+            };
+            auto wait_both = [&](uint64_t& mine, uint64_t& peer, int parity) {
+                ok = ok && mbar_wait_cluster_warp(smem_u32(&peer), parity, &s_abort, a.seqs.status);
+                return wait(mine, parity);
             };
             auto scores = [&](int t, int j) {            // and what waits for them
                 const uint64_t qd = sw128_kmajor_desc(sm + C::Q + t * C::QB);
@@ -686,17 +691,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) kv4_att
                 }
                 __syncwarp();
             };
-            auto wait_keys = [&](int j) { return wait(bars.k_full[j & 1], (j >> 1) & 1) && wait(bars.k_peer[j & 1], (j >> 1) & 1); };
-            if (wait(bars.q_full, 0) && wait_keys(0))
+            auto wait_keys = [&](int j) { return wait_both(bars.k_full[j & 1], bars.k_peer[j & 1], (j >> 1) & 1); };
+            ok = mbar_wait_cluster_warp(smem_u32(&bars.q_full), 0, &s_abort, a.seqs.status);
+            if (ok && wait_keys(0))
                 for (int t = 0; t < tiles; ++t) scores(t, 0);
             for (int j = 0; j < steps && ok; ++j) {
                 const bool more = j + 1 < steps;
-                if (!wait(bars.v_full[j & 1], (j >> 1) & 1) || !wait(bars.v_peer[j & 1], (j >> 1) & 1)) break;
+                if (!wait_both(bars.v_full[j & 1], bars.v_peer[j & 1], (j >> 1) & 1) || (more && !wait_keys(j + 1))) break;
                 for (int t = 0; t < tiles; ++t) {
                     if (!wait(bars.p_full[t], j & 1)) break;
                     values(t, j);
                     if (!more) continue;
-                    if (t == 0 && !wait_keys(j + 1)) break;
                     scores(t, j + 1);
                 }
             }
