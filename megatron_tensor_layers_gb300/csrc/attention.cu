@@ -30,7 +30,8 @@
 // does not hold whole goes to the workspace, and the worker that holds the
 // item's end adds the parts in order, after its own range is done: it waits, with
 // a limit, for the flags of the parts before its own, which are raised before
-// their workers wait for anything.  A second kernel for this costs 5 us more.
+// their workers wait for anything.  A second kernel for this took 16.2 us where
+// this takes 14.7 (one row, 4097 tokens, 8 heads).
 // A flag is raised by writing the call's number, which nothing else in the
 // workspace holds, and taken down by whoever waited for it, so that the workspace
 // needs no preparation and a graph that repeats a call finds it as the call did.
@@ -57,7 +58,7 @@ constexpr int kBatch = 32;           // blocks whose addresses a warp holds, one
 constexpr int kStages = 2;
 constexpr int kPShift = 8;           // p s' is held times 2^(kPShift - E)
 constexpr float kMost = 128.0f;      // sum of a lane's 2^(x - m) up to which the old maximum will do
-constexpr int kMany = 64;            // columns from which a sequence's rows go to the many-rows kernel
+constexpr int kMany = 64;            // columns for each pair of blocks from which the many-rows kernel pays (many_from)
 constexpr float kNegInf = -INFINITY;
 
 // An item whose end a worker holds, but not its beginning.
@@ -136,14 +137,14 @@ struct Need {
     int units, tiles;                // units >= 1 per item (an item that sees nothing writes zeros)
 };
 
-__device__ __forceinline__ Need seq_need(const AttnArgs& a, int s, int cols_per_tile) {
+__device__ __forceinline__ Need seq_need(const AttnArgs& a, int s, int cols_per_tile, int many) {
     Need n;
     const SeqRows r = seq_rows(a.seqs, s);
     n.first_row = r.first;
     n.rows = r.count;
     n.len = max(a.seqs.lens[s], 0);
     const int64_t cols = static_cast<int64_t>(r.count) * a.group;
-    n.tiles = cols >= a.many ? 0 : static_cast<int>((cols + cols_per_tile - 1) / cols_per_tile);
+    n.tiles = cols >= many ? 0 : static_cast<int>((cols + cols_per_tile - 1) / cols_per_tile);
     Spans v{0, 0, 0};
     if (n.tiles > 0) v = visible_spans(a, static_cast<int64_t>(n.len) - r.count, static_cast<int64_t>(n.len) - 1, kKvBlock);
     n.front = v.front;
@@ -175,7 +176,7 @@ struct Cursor {
     int s, tile, head, off;          // current item and the unit in it
     Need n;
     __device__ __forceinline__ int count() const { return min(n.units - off, left); }
-    __device__ __forceinline__ void next(const AttnArgs& a, int cols_per_tile, int heads) {
+    __device__ __forceinline__ void next(const AttnArgs& a, int cols_per_tile, int many, int heads) {
         const int c = count();
         left -= c;
         off += c;
@@ -191,7 +192,7 @@ struct Cursor {
                 left = 0;
                 return;
             }
-            n = seq_need(a, s, cols_per_tile);
+            n = seq_need(a, s, cols_per_tile, many);
         } while (n.tiles == 0);
     }
 };
@@ -275,12 +276,14 @@ __global__ void __launch_bounds__(Cfg<HD, NT>::WARPS * 32, 1) kv4_attention_kern
     pdl_wait();
     pdl_trigger();
 
+    const int many = many_from<THREADS>(a);
+
     // ---- the cut: total units, items, then where each of this block's workers begins
     int64_t mine = 0, items = 0;
     const int per = (a.seqs.nseq + THREADS - 1) / THREADS;
     Need need = {};                  // of this thread's last sequence: with one each, it is not asked for twice
     for (int s = tid * per; s < min(a.seqs.nseq, (tid + 1) * per); ++s) {
-        need = seq_need(a, s, COLS);
+        need = seq_need(a, s, COLS, many);
         mine += static_cast<int64_t>(need.units) * need.tiles * heads;
         items += static_cast<int64_t>(need.tiles) * heads;
     }
@@ -323,7 +326,7 @@ __global__ void __launch_bounds__(Cfg<HD, NT>::WARPS * 32, 1) kv4_attention_kern
             int s = tid * per;
             if (per > 1)
                 while (true) {
-                    need = seq_need(a, s, COLS);
+                    need = seq_need(a, s, COLS, many);
                     const int64_t w_s = static_cast<int64_t>(need.units) * need.tiles * heads;
                     if (u < w_s) break;
                     u -= w_s;
@@ -421,7 +424,7 @@ __global__ void __launch_bounds__(Cfg<HD, NT>::WARPS * 32, 1) kv4_attention_kern
     int issued = 0;
     auto load_stage = [&]() {
         while (load_u >= load_end) {
-            ahead.next(a, COLS, heads);
+            ahead.next(a, COLS, many, heads);
             if (ahead.left <= 0) return;
             open_segment();
         }
@@ -771,7 +774,7 @@ __global__ void __launch_bounds__(Cfg<HD, NT>::WARPS * 32, 1) kv4_attention_kern
         float4* slot = slots + static_cast<size_t>(slot_no) * C::PART;
         const bool awaited = !complete && seg_off + seg_n < cur.n.units; // by the worker that holds the end
         first_segment = false;
-        cur.next(a, COLS, heads);
+        cur.next(a, COLS, many, heads);
         const bool more = cur.left > 0;
         if (more) fetch_q(cur);
         // the worker's warps together: every one leaves its part, then they share the sum of the parts
@@ -862,15 +865,18 @@ tp_status launch_kv4_attention(const KvAttentionDesc& d, cudaStream_t stream) {
     // numbers of calls begin at one that memory does not hold by chance
     static std::atomic<uint64_t> calls{0x9e3779b97f4a7c15ull ^ static_cast<uint64_t>(reinterpret_cast<uintptr_t>(&calls))};
     a.tag = calls.fetch_add(1, std::memory_order_relaxed) | 1ull << 63;
-    // Sequences with at least kMany columns go to the many-rows kernel (none can without cu_rows).
-    a.many = kMany;
-    if (d.seqs.cu_rows != nullptr && static_cast<int64_t>(d.seqs.n) * d.group >= kMany) {
+    const int sms = device_sms();
+    if (sms <= 0 || sms > 160) return TP_ERR_CUDA;   // the workspace size is asked for without a device too
+    // The kernels settle by the sequences' lengths which of them takes which; there is nothing to
+    // settle while all rows together are too few (and without cu_rows each sequence has one).
+    a.pairs = std::max(sms / 2, 1);
+    a.many = INT32_MAX;
+    const int64_t columns = static_cast<int64_t>(d.seqs.n) * d.group * d.pools.t * d.pools.kv_heads;
+    if (d.seqs.cu_rows != nullptr && columns >= static_cast<int64_t>(kMany) * a.pairs) {
+        a.many = kMany;
         const tp_status s = launch_attention_many(a, d.head_dim, stream);
         if (s != TP_OK) return s;
     }
-    if (d.seqs.cu_rows == nullptr) a.many = INT32_MAX;
-    const int sms = device_sms();
-    if (sms <= 0 || sms > 160) return TP_ERR_CUDA;   // the workspace size is asked for without a device too
     // 16 columns per tile when a sequence's rows fill more than 8
     const bool wide = d.group > 8 || (d.seqs.cu_rows != nullptr && d.group * (d.seqs.n / std::max(d.seqs.nseq, 1)) > 8);
     if (d.head_dim == 128) return wide ? launch_few<128, 2>(a, sms, stream) : launch_few<128, 1>(a, sms, stream);

@@ -15,7 +15,8 @@ struct AttnArgs {
     int group;                       // query heads per kv head
     float scale_log2;                // scale * log2(e)
     int window, sinks;
-    int many;                        // columns (rows * group) from which a sequence goes to the many-rows kernel
+    int many;                        // columns (rows * group) from which a sequence may go to the many-rows kernel
+    int pairs;                       // pairs of thread blocks that the device runs at once
     uint8_t* ws;
     uint64_t tag;                    // number of the call, never 0
 };
@@ -55,6 +56,43 @@ __device__ __forceinline__ Spans visible_spans(const AttnArgs& a, int64_t first,
     v.start = max(lo / span, v.front);
     v.count = v.front + max(0, stop - v.start);
     return v;
+}
+
+constexpr int kManyCols = 512;       // columns of a pair of thread blocks of the many-rows kernel
+
+// Which kernel takes a sequence.  The few-rows kernel's time grows with the
+// columns, the many-rows kernel's with the waves of pairs of blocks, however few
+// columns they hold: over 4096 cached tokens of head dimension 128 a full device
+// of the first takes 72 us for 4096 columns and 134 us for 8192, the second 75 us
+// and 77 us (64: 51 us and 93 us against 63 us and 65 us; over 512 tokens, 128:
+// 34 us and 57 us against 30 us and 31 us).  So the second is worth its launch
+// from 64 columns for each pair of each wave, counted over the sequences that
+// have 64 by themselves (a shorter one would leave a pair to fewer).  Returns the
+// columns from which a sequence is the many-rows kernel's; both kernels ask.
+template <int THREADS>
+__device__ __forceinline__ int many_from(const AttnArgs& a) {
+    if (a.many == INT32_MAX) return INT32_MAX;
+    __shared__ int64_t s_cols[THREADS / 32], s_tiles[THREADS / 32];
+    const int heads = a.pools.t * a.pools.kv_heads;
+    int64_t cols = 0, tiles = 0;
+    for (int s = threadIdx.x; s < a.seqs.nseq; s += THREADS) {
+        const int64_t c = static_cast<int64_t>(seq_rows(a.seqs, s).count) * a.group;
+        if (c < a.many) continue;
+        cols += c;
+        tiles += (c + kManyCols - 1) / kManyCols;
+    }
+#pragma unroll
+    for (int m = 16; m > 0; m >>= 1) {
+        cols += __shfl_xor_sync(0xffffffffu, cols, m);
+        tiles += __shfl_xor_sync(0xffffffffu, tiles, m);
+    }
+    if (threadIdx.x % 32 == 0) s_cols[threadIdx.x / 32] = cols, s_tiles[threadIdx.x / 32] = tiles;
+    __syncthreads();
+    cols = tiles = 0;
+#pragma unroll
+    for (int i = 0; i < THREADS / 32; ++i) cols += s_cols[i], tiles += s_tiles[i];
+    const int64_t waves = quotient(tiles * heads + a.pairs - 1, a.pairs);
+    return cols * heads >= waves * a.pairs * a.many ? a.many : INT32_MAX;
 }
 
 tp_status launch_attention_many(const AttnArgs& a, int head_dim, cudaStream_t stream);

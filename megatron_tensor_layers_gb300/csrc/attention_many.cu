@@ -56,7 +56,8 @@ constexpr int kLaunchRegs = 128, kSoftmaxRegs = 192, kUnpackRegs = 88, kIssueReg
 static_assert(256 * kSoftmaxRegs + 32 * kUnpackWarps * kUnpackRegs + 128 * kIssueRegs <= kThreads * kLaunchRegs,
               "a warpgroup would wait for registers that never come");
 constexpr int kTile = 128;           // tokens of a step, columns of a tile
-constexpr int kCols = 4 * kTile;     // columns of a pair of thread blocks
+constexpr int kCols = kManyCols;
+static_assert(kCols == 4 * kTile, "two tiles of 256 columns, half of each in each block");
 constexpr int kInfo = 4;
 constexpr float kNegInf = -INFINITY;
 constexpr float kMost = 4096.0f;     // sum of a step's 2^(x - m) up to which the old maximum will do (P is 8 times as much at most)
@@ -200,11 +201,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) kv4_att
 
     // ---- which sequence and tile: pair / heads counts tiles of 512 columns over the sequences
     {
+        const int many = many_from<kThreads>(a);
         const int64_t want = (blockIdx.x >> 1) / heads;
         const int per = (a.seqs.nseq + kThreads - 1) / kThreads;
         auto tiles_of = [&](int s) -> int64_t {
             const int64_t cols = static_cast<int64_t>(seq_rows(a.seqs, s).count) * a.group;
-            return cols < a.many ? 0 : (cols + kCols - 1) / kCols;
+            return cols < many ? 0 : (cols + kCols - 1) / kCols;
         };
         if (tid == 0) s_found = 0;
         const int lo = min(a.seqs.nseq, tid * per), hi = min(a.seqs.nseq, (tid + 1) * per);
