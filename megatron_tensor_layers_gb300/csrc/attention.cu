@@ -24,9 +24,8 @@
 //
 // Split.  The unit of work is a cache block (16 tokens).  All blocks of all
 // (sequence, row tile, head) items form one line, cut into equal parts, one for
-// each worker of WS warps (8, or fewer when items are short, so that a worker
-// then takes whole items); the warps of a worker share each item's part of its
-// range and merge through shared memory.  A worker's part of an item that it
+// each worker of 8, 2 or 1 warps (see `ws`); the warps of a worker share each
+// item's part of its range and merge through shared memory.  A worker's part of an item that it
 // does not hold whole goes to the workspace, and the worker that holds the
 // item's end adds the parts in order, after its own range is done: it waits, with
 // a limit, for the flags of the parts before its own, which are raised before
@@ -211,44 +210,63 @@ struct Cfg {
     static constexpr int SMEM = RING + WARPS * PART * 16;
 };
 
-// The sum, in order, of `count` parts at part(i), for vector v of the result (see slot_vectors):
-// four accumulators already divided by the sum.
-template <int HD, int NT, typename Part>
-__device__ __forceinline__ float4 join_parts(int v, int count, Part part, float2& top, float2& total) {
-    constexpr int MT = HD / 16;
-    const int nt = v / (MT * 32), stats = nt * 32 + v % 32;
-    top = make_float2(kNegInf, kNegInf);
-    total = make_float2(0.0f, 0.0f);
-    float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 8
-    for (int i = 0; i < count; ++i) {
-        const float4 st = part(i)[NT * MT * 32 + stats], x = part(i)[v];
-        const float2 m = make_float2(fmaxf(top.x, st.x), fmaxf(top.y, st.y));
-        const float2 b = make_float2(m.x == kNegInf ? 0.0f : m.x, m.y == kNegInf ? 0.0f : m.y);
-        const float2 fa = make_float2(ex2(top.x - b.x), ex2(top.y - b.y)), fb = make_float2(ex2(st.x - b.x), ex2(st.y - b.y));
-        top = m;
-        total = make_float2(total.x * fa.x + st.z * fb.x, total.y * fa.y + st.w * fb.y);
-        o = make_float4(o.x * fa.x + x.x * fb.x, o.y * fa.y + x.y * fb.y, o.z * fa.x + x.z * fb.x, o.w * fa.y + x.w * fb.y);
-    }
-    return o;
+// Where a lane's dimensions of column cc of a sequence go, nullptr past the last column.
+template <int HD>
+__device__ __forceinline__ uint16_t* out_of(const AttnArgs& a, int head, int first_row, int rows, int cc, int lane) {
+    const int r = rows == 1 ? 0 : cc / a.group, h = cc - r * a.group;
+    if (r >= rows || h >= a.group) return nullptr;
+    const int rank = head / a.pools.kv_heads, kvh = head - rank * a.pools.kv_heads;
+    return a.out[rank] + (first_row + r) * a.ldo + (kvh * a.group + h) * HD + (lane >> 2) * (HD / 8);
 }
 
-// Vector v of an item's result to the output: two dimensions of two columns.
-template <int HD, int NT>
-__device__ __forceinline__ void store_vector(const AttnArgs& a, int head, int first_row, int cols, int tile, int v,
-                                             const float4& o, const float2& total) {
-    constexpr int MT = HD / 16, COLS = 8 * NT;
-    const int lane = v % 32, i = v / 32 % MT, nt = v / (MT * 32);
-    const int rank = head / a.pools.kv_heads, kvh = head - rank * a.pools.kv_heads;
+// Vectors v .. v + NV - 1 of an item's result (see slot_vectors; of one column tile) to the output.
+template <int HD, int NV>
+__device__ __forceinline__ void store_vectors(const AttnArgs& a, int head, int first_row, int rows, int first_col, int lane,
+                                              int v, const float4 (&o)[NV], const float2& total) {
+    constexpr int MT = HD / 16;
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
-        const int ci = nt * 8 + 2 * (lane & 3) + e;
-        if (ci >= cols) continue;
+        uint16_t* p = out_of<HD>(a, head, first_row, rows, first_col + v / MT * 8 + 2 * (lane & 3) + e, lane);
+        if (p == nullptr) continue;
         const float sum = e ? total.y : total.x, inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-        const int cc = tile * COLS + ci;
-        const int r = cc / a.group, h = cc - r * a.group;
-        *reinterpret_cast<uint32_t*>(a.out[rank] + (first_row + r) * a.ldo + (kvh * a.group + h) * HD + (lane >> 2) * (HD / 8) +
-                                     2 * i) = pack_bf16x2((e ? o.y : o.x) * inv, (e ? o.w : o.z) * inv);
+        uint32_t w[NV];
+#pragma unroll
+        for (int i = 0; i < NV; ++i) w[i] = pack_bf16x2((e ? o[i].y : o[i].x) * inv, (e ? o[i].w : o[i].z) * inv);
+        if constexpr (NV == 4)
+            *reinterpret_cast<uint4*>(p + 2 * (v % MT)) = make_uint4(w[0], w[1], w[2], w[3]);
+        else
+            *reinterpret_cast<uint32_t*>(p + 2 * (v % MT)) = w[0];
+    }
+}
+
+// The sum, in order, of `count` parts at part(p): warp wi of ws gives NV vectors of the result at a
+// time (see slot_vectors) to put(first vector, vectors, maxima, sums).
+template <int HD, int NT, int NV, typename Part, typename Put>
+__device__ __forceinline__ void join_parts(int wi, int ws, int lane, int count, Part part, Put put) {
+    constexpr int MT = HD / 16;
+    for (int v = wi * NV; v < NT * MT; v += ws * NV) {
+        const int nt = v / MT;
+        float2 top = make_float2(kNegInf, kNegInf), total = make_float2(0.0f, 0.0f);
+        float4 o[NV];
+#pragma unroll
+        for (int i = 0; i < NV; ++i) o[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 8 / NV
+        for (int p = 0; p < count; ++p) {
+            const float4* from = part(p) + lane;
+            const float4 st = from[(NT * MT + nt) * 32];
+            const float2 m = make_float2(fmaxf(top.x, st.x), fmaxf(top.y, st.y));
+            const float2 b = make_float2(m.x == kNegInf ? 0.0f : m.x, m.y == kNegInf ? 0.0f : m.y);
+            const float2 fa = make_float2(ex2(top.x - b.x), ex2(top.y - b.y)), fb = make_float2(ex2(st.x - b.x), ex2(st.y - b.y));
+            top = m;
+            total = make_float2(total.x * fa.x + st.z * fb.x, total.y * fa.y + st.w * fb.y);
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                const float4 x = from[(v + i) * 32];
+                o[i] = make_float4(o[i].x * fa.x + x.x * fb.x, o[i].y * fa.y + x.y * fb.y, o[i].z * fa.x + x.z * fb.x,
+                                   o[i].w * fa.y + x.w * fb.y);
+            }
+        }
+        put(v, o, top, total);
     }
 }
 
@@ -305,10 +323,14 @@ __global__ void __launch_bounds__(Cfg<HD, NT>::WARPS * 32, 1) kv4_attention_kern
     }
     before += base - mine;           // units before this thread's sequences
     if (total == 0) return;
-    // Warps of a worker: all while the average item has a stage for each, fewer below.  At least a
-    // stage for each warp, too, where there are few units in all: fewer parts to join.
-    int ws = WARPS;
-    while (ws > 1 && total < static_cast<int64_t>(C::BLOCKS * ws) * all_items) ws >>= 1;
+    // Warps of a worker.  Eight share an item's latency, but meet at its end and pay for each item's
+    // beginning eight times; alone a warp does neither, but a long item is then the sum of many parts.
+    // Of 4096 tokens, head dimension 128, with 8, 2 and 1 warps: 8 items 16.4, 20.3, 62 us; 128: 29, 29,
+    // 38 us; 256: 50, 44, 51 us; 1024: 148, 122, 122 us; 2048: 282, 228, 224 us (4 are between 8 and 2, or
+    // behind both).  Each warp is to have a stage, too: 64 items of 256 tokens take 21, 15, 20 us.
+    const int64_t sms = gridDim.x;
+    const int ws = all_items <= sms && total >= static_cast<int64_t>(C::BLOCKS * WARPS) * all_items ? WARPS
+                   : all_items <= sms * WARPS && total >= static_cast<int64_t>(C::BLOCKS * 2) * all_items ? 2 : 1;
     const int groups = WARPS / ws;
     const int64_t least = C::BLOCKS * ws;
     const int workers =
@@ -374,6 +396,8 @@ __global__ void __launch_bounds__(Cfg<HD, NT>::WARPS * 32, 1) kv4_attention_kern
     Cursor ahead = cur;              // the item being loaded
     bool first_segment = true;
 
+    auto row_of = [&](int rows, int col) { return rows == 1 ? 0 : col / a.group; };
+
     // ---- q of an item: a lane holds a quarter of the dimensions of one column of each column tile
     constexpr int D = HD / 4;
     uint32_t raw[NT][D / 2];
@@ -385,7 +409,7 @@ __global__ void __launch_bounds__(Cfg<HD, NT>::WARPS * 32, 1) kv4_attention_kern
             const int ci = nt * 8 + g;
             const bool have = ci < cols;
             const int cc = c.tile * COLS + ci;
-            const int r = have ? cc / a.group : 0;
+            const int r = have ? row_of(c.n.rows, cc) : 0;
             const int h = cc - r * a.group;
             const uint4* src = reinterpret_cast<const uint4*>(a.q[rank] + (c.n.first_row + r) * a.ldq +
                                                               (kvh * a.group + h) * HD + t4 * D);
@@ -477,14 +501,15 @@ __global__ void __launch_bounds__(Cfg<HD, NT>::WARPS * 32, 1) kv4_attention_kern
             float sum = 0.0f;
 #pragma unroll
             for (int i = 0; i < D / 2; ++i) {
-                top = max(top, max(raw[nt][i] & 0x7fffu, (raw[nt][i] >> 16) & 0x7fffu));
+                top = __vmaxu2(top, raw[nt][i] & 0x7fff7fffu);
                 sum += __uint_as_float(raw[nt][i] << 16) + __uint_as_float(raw[nt][i] & 0xffff0000u);
             }
 #pragma unroll
             for (int m = 1; m < 4; m <<= 1) {
-                top = max(top, __shfl_xor_sync(0xffffffffu, top, m));
+                top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, m));
                 sum += __shfl_xor_sync(0xffffffffu, sum, m);
             }
+            top = max(top & 0xffffu, top >> 16);
             // 2^k with the row's largest element in [2^10, 2^11); k within the fp32 exponents
             const int k = min(10 - (static_cast<int>(top >> 7) - 127), 126);
             const float up = __uint_as_float(static_cast<uint32_t>(k + 127) << 23);
@@ -510,11 +535,11 @@ __global__ void __launch_bounds__(Cfg<HD, NT>::WARPS * 32, 1) kv4_attention_kern
                 cmul[nt][e] = __shfl_sync(0xffffffffu, mul, from);
                 cadd[nt][e] = __shfl_sync(0xffffffffu, add, from);
                 const int ce = nt * 8 + 2 * t4 + e;
-                cpos[nt][e] = ce < cols ? pos0 + (cur.tile * COLS + ce) / a.group : -1;
+                cpos[nt][e] = ce < cols ? pos0 + row_of(cur.n.rows, cur.tile * COLS + ce) : -1;
             }
         }
-        const int row_lo = pos0 + (cur.tile * COLS) / a.group;
-        const int row_hi = pos0 + (cur.tile * COLS + min(cols, COLS) - 1) / a.group;
+        const int row_lo = pos0 + row_of(cur.n.rows, cur.tile * COLS);
+        const int row_hi = pos0 + row_of(cur.n.rows, cur.tile * COLS + min(cols, COLS) - 1);
 
         float acc[NT][MT][4];
         float mx[NT][2], sum[NT][2], corr[NT][2];
@@ -769,7 +794,7 @@ __global__ void __launch_bounds__(Cfg<HD, NT>::WARPS * 32, 1) kv4_attention_kern
                 }
             }
         const bool complete = seg_off == 0 && seg_n == cur.n.units;
-        const int head = cur.head, first_row = cur.n.first_row, tile = cur.tile;
+        const int head = cur.head, first_row = cur.n.first_row, rows = cur.n.rows, tile = cur.tile;
         const int slot_no = worker * 2 + (first_segment ? 0 : 1);
         float4* slot = slots + static_cast<size_t>(slot_no) * C::PART;
         const bool awaited = !complete && seg_off + seg_n < cur.n.units; // by the worker that holds the end
@@ -777,9 +802,26 @@ __global__ void __launch_bounds__(Cfg<HD, NT>::WARPS * 32, 1) kv4_attention_kern
         cur.next(a, COLS, many, heads);
         const bool more = cur.left > 0;
         if (more) fetch_q(cur);
+        auto store = [&](int v, const auto& o, const float2& total) {    // vectors of a complete item
+            store_vectors<HD>(a, head, first_row, rows, tile * COLS, lane, v, o, total);
+        };
+        if (ws == 1 && complete) {
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int i = 0; i < MT; i += 4) {
+                    const float4 o[4] = {make_float4(acc[nt][i][0], acc[nt][i][1], acc[nt][i][2], acc[nt][i][3]),
+                                         make_float4(acc[nt][i + 1][0], acc[nt][i + 1][1], acc[nt][i + 1][2], acc[nt][i + 1][3]),
+                                         make_float4(acc[nt][i + 2][0], acc[nt][i + 2][1], acc[nt][i + 2][2], acc[nt][i + 2][3]),
+                                         make_float4(acc[nt][i + 3][0], acc[nt][i + 3][1], acc[nt][i + 3][2], acc[nt][i + 3][3])};
+                    store(nt * MT + i, o, make_float2(sum[nt][0], sum[nt][1]));
+                }
+            if (!more) break;
+            continue;
+        }
         // the worker's warps together: every one leaves its part, then they share the sum of the parts
         float4* left = reinterpret_cast<float4*>(smem + C::RING) + grp * ws * C::PART;
-        float4* mine_part = ws > 1 || complete ? left + wi * C::PART : slot;
+        float4* mine_part = ws > 1 ? left + wi * C::PART : slot;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -789,18 +831,22 @@ __global__ void __launch_bounds__(Cfg<HD, NT>::WARPS * 32, 1) kv4_attention_kern
             mine_part[(NT * MT + nt) * 32 + lane] = make_float4(mx[nt][0], mx[nt][1], sum[nt][0], sum[nt][1]);
         }
         together();
-        if (ws > 1 || complete)
-            for (int v = wi * 32 + lane; v < NT * MT * 32; v += ws * 32) {
-                float2 top, all;
-                const float4 o = join_parts<HD, NT>(v, ws, [&](int i) { return left + i * C::PART; }, top, all);
+        if (ws > 1) {
+            auto part = [&](int i) { return left + i * C::PART; };
+            auto put = [&](int v, const auto& o, const float2& top, const float2& total) {
                 if (complete) {
-                    store_vector<HD, NT>(a, head, first_row, cols, tile, v, o, all);
-                } else {
-                    slot[v] = o;
-                    if (v / 32 % MT == 0)
-                        slot[NT * MT * 32 + v / (MT * 32) * 32 + lane] = make_float4(top.x, top.y, all.x, all.y);
+                    store(v, o, total);
+                    return;
                 }
-            }
+#pragma unroll
+                for (int i = 0; i < static_cast<int>(sizeof(o) / sizeof(o[0])); ++i) slot[(v + i) * 32 + lane] = o[i];
+                if (v % MT == 0) slot[(NT * MT + v / MT) * 32 + lane] = make_float4(top.x, top.y, total.x, total.y);
+            };
+            if (ws > 2)
+                join_parts<HD, NT, 1>(wi, ws, lane, ws, part, put);
+            else
+                join_parts<HD, NT, 4>(wi, ws, lane, ws, part, put);
+        }
         if (more || awaited) together();
         if (awaited && wi == 0 && lane == 0) {
             __threadfence();
@@ -816,12 +862,14 @@ __global__ void __launch_bounds__(Cfg<HD, NT>::WARPS * 32, 1) kv4_attention_kern
         for (int i = wi * 32 + lane; i + 1 < count; i += ws * 32)
             have = have && flag64_wait(flags + slot_of(i), a.tag, &s_abort, a.seqs.status);
         together();
-        for (int v = wi * 32 + lane; v < NT * MT * 32; v += ws * 32) {
-            float2 top, all;
-            const float4 o = join_parts<HD, NT>(
-                v, count, [&](int i) { return slots + static_cast<size_t>(slot_of(i)) * C::PART; }, top, all);
-            store_vector<HD, NT>(a, jn.head, jn.first_row, jn.rows * a.group - jn.tile * COLS, jn.tile, v, o, all);
-        }
+        auto part = [&](int i) { return slots + static_cast<size_t>(slot_of(i)) * C::PART; };
+        auto put = [&](int v, const auto& o, const float2&, const float2& total) {
+            store_vectors<HD>(a, jn.head, jn.first_row, jn.rows, jn.tile * COLS, lane, v, o, total);
+        };
+        if (ws > 2)
+            join_parts<HD, NT, 1>(wi, ws, lane, count, part, put);
+        else
+            join_parts<HD, NT, 4>(wi, ws, lane, count, part, put);
         if (have)
             for (int i = wi * 32 + lane; i + 1 < count; i += ws * 32) flags[slot_of(i)] = 0;
     }
@@ -877,8 +925,11 @@ tp_status launch_kv4_attention(const KvAttentionDesc& d, cudaStream_t stream) {
         const tp_status s = launch_attention_many(a, d.head_dim, stream);
         if (s != TP_OK) return s;
     }
-    // 16 columns per tile when a sequence's rows fill more than 8
-    const bool wide = d.group > 8 || (d.seqs.cu_rows != nullptr && d.group * (d.seqs.n / std::max(d.seqs.nseq, 1)) > 8);
+    // 16 columns per tile where a sequence's rows fill more than 8 and there are enough tiles for every warp even so.
+    // 4096 tokens, 16 columns for each of eight heads, tiles of 16 and of 8: 64 sequences 122 and 131 us, 16 43 and 41,
+    // 4 28 and 22; of 64 dimensions, which leave more registers: 89 and 105, 31 and 34, 20 and 19 us.
+    const bool filled = d.group > 8 || (d.seqs.cu_rows != nullptr && d.group * (d.seqs.n / std::max(d.seqs.nseq, 1)) > 8);
+    const bool wide = filled && columns >= static_cast<int64_t>(sms) * (d.head_dim == 128 ? 48 : 12);
     if (d.head_dim == 128) return wide ? launch_few<128, 2>(a, sms, stream) : launch_few<128, 1>(a, sms, stream);
     return wide ? launch_few<64, 2>(a, sms, stream) : launch_few<64, 1>(a, sms, stream);
 }

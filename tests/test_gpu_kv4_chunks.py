@@ -181,3 +181,13 @@ def test_chunk_repeats_in_a_graph_and_on_a_stream():
         g.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) and torch.equal(a, e) for a, b, e in zip(plain, captured, again))
+
+
+@pytest.mark.parametrize("hd,window,sinks", [(64, 0, 0), (128, 0, 0), (128, 40, 3)])
+def test_many_sequences_of_few_rows(hd, window, sinks):
+    """Enough columns for tiles of 16 of them, none of the sequences long enough for the many-rows kernel."""
+    rng = np.random.default_rng(49)
+    rows = rng.integers(2, 9, 20).tolist()
+    lens = (np.array(rows) + rng.integers(0, 150, 20)).tolist()
+    c = Cache(4, 8, hd, 32, lens, 50)
+    run(c, rows, 32, 51, window=window, sinks=sinks)
