@@ -1,15 +1,20 @@
 // Writing to and reading from the paged 4-bit KV cache.
 //
-// Both kernels are elementwise over rows of head_dim elements: bound by memory
-// traffic for large calls (append: 2 bytes in and about 0.53 out per element), by
-// the chain of dependent loads (row -> sequence -> page) for small ones.  HD / 8
+// Both kernels are elementwise over rows of head_dim elements.  Large calls are
+// bound by memory traffic (append: 2 bytes in and about 0.53 out per element) and
+// by the instructions of an element: 8192 rows of 8 heads of 128, keys and values,
+// append 23 us with inputs that are not in L2 and 18 with such that are (three
+// quarters of the issue slots), load 11 us.  Small ones are bound by the chain of dependent loads (row ->
+// sequence -> page): append and load of 64 rows 5.9 us.  HD / 8
 // lanes hold one sub-row (a kv head's key or value of a row), eight elements
 // each: a 16-byte load, a 4-byte store of eight codes.
 //
 // A warp takes kRows rows of one group of sub-rows (those that its 32 lanes
 // hold).  Lane r looks up the place of row r, so that one chain of loads serves
-// all of them, and the rows' data are on their way before it.  Few rows take one
-// a warp, so that they spread over the GPU.
+// all of them, and the rows' data are on their way before it.  Few rows to
+// append take one a warp, so that they spread over the GPU.  Half as many lanes
+// a sub-row, with sixteen elements each, take fewer instructions but leave fewer
+// loads in flight: 43 us where append and load of 8192 rows take 36.
 #include "kv4.cuh"
 
 namespace tpk {
@@ -41,6 +46,12 @@ __device__ __forceinline__ void row_range(const uint4& w, float& lo, float& hi) 
     b = max2(b, b >> 16);
     lo = __uint_as_float(a << 16);
     hi = __uint_as_float(b << 16);
+}
+
+__device__ __forceinline__ void store8(float* p, const float (&y)[8]) {
+    asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "f"(y[0]), "f"(y[1]), "f"(y[2]),
+                 "f"(y[3]), "f"(y[4]), "f"(y[5]), "f"(y[6]), "f"(y[7])
+                 : "memory");
 }
 
 // The place in its rank's pool of row `row` (offset of its block for kv head 0, and its slot), by one lane:
@@ -142,17 +153,18 @@ __global__ void __launch_bounds__(kThreads) kv4_append_kernel(const __grid_const
                 x[2 * j] = __fsub_rn(__uint_as_float(word[j] << 16), lo);
                 x[2 * j + 1] = __fsub_rn(__uint_as_float(word[j] & 0xffff0000u), lo);
             }
-            // A quotient by the reciprocal is off by 2^-21 at most: only within 2^-10 of a border between two
-            // codes, or with a step whose rounding (below the normal numbers) or reciprocal is not that good, does
-            // the definition's division decide.  Adding 1.5 2^23 leaves the nearest whole number, ties to even, in
-            // the low bits; its own bits come off the packed word at the end.
+            // A quotient of at most 15.1 by the reciprocal is off by 15.1 2^-24 < 2^-20, and so is the definition's
+            // rounded one: only within 2^-18 of a border between two codes (of 1 warp in 500), or with a step whose
+            // rounding (below the normal numbers) or reciprocal is not that good, does the definition's division
+            // decide.  Adding 1.5 2^23 leaves the nearest whole number, ties to even, in the low bits; its own bits
+            // come off the packed word at the end.
             const float inv = __frcp_rn(step);
             bool near = !(step > 1e-30f);
             uint32_t fast = 0;
 #pragma unroll
             for (int j = 7; j >= 0; --j) {
                 const float t = fmaf(x[j], inv, 12582912.0f);
-                near |= fabsf(fmaf(x[j], inv, -__fsub_rn(t, 12582912.0f))) > 0.499f;
+                near |= fabsf(fmaf(x[j], inv, -__fsub_rn(t, 12582912.0f))) > 0.5f - 0x1p-18f;
                 fast = fast * 16 + __float_as_uint(t);
             }
             code = fast - (0x4b400000u + 0xb4000000u + 0x40000000u);
@@ -211,9 +223,13 @@ __global__ void __launch_bounds__(kThreads) kv4_load_kernel(const __grid_constan
         for (int j = 0; j < 8; ++j)          // 2^23 + u in the low bits: no conversion, of which there are few a cycle
             y[j] = fmaf(step, __uint_as_float(((code[i] >> (4 * j)) & 15u) | 0x4b000000u) - 8388608.0f, base);
         if (d.out_f32) {
-            float4* p = reinterpret_cast<float4*>(static_cast<float*>(out) + out0 + i * ld);
-            p[0] = make_float4(y[0], y[1], y[2], y[3]);
-            p[1] = make_float4(y[4], y[5], y[6], y[7]);
+            float* p = static_cast<float*>(out) + out0 + i * ld;
+            if (reinterpret_cast<uintptr_t>(p) % 32 == 0) {      // whole sectors
+                store8(p, y);
+            } else {
+                reinterpret_cast<float4*>(p)[0] = make_float4(y[0], y[1], y[2], y[3]);
+                reinterpret_cast<float4*>(p)[1] = make_float4(y[4], y[5], y[6], y[7]);
+            }
         } else {
             *reinterpret_cast<uint4*>(static_cast<uint16_t*>(out) + out0 + i * ld) =
                 make_uint4(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]), pack_bf16x2(y[4], y[5]), pack_bf16x2(y[6], y[7]));
@@ -223,31 +239,47 @@ __global__ void __launch_bounds__(kThreads) kv4_load_kernel(const __grid_constan
 
 constexpr int kRows = 4;
 
-// Four rows a warp where that leaves 32 warps for an SM, else one.
-template <typename Desc, typename Many, typename One>
-tp_status launch_rows(const Desc& d, Many many, One one, cudaStream_t stream) {
-    const int sub = 32 / (d.head_dim / 8);
-    const int64_t per = static_cast<int64_t>(d.pools.t) * ((2 * d.pools.kv_heads + sub - 1) / sub);
+// `rows` rows a warp.
+template <typename Desc, typename Kern>
+tp_status launch_rows(const Desc& d, Kern kern, int rows, int64_t per, cudaStream_t stream) {
+    const int64_t warps = (d.seqs.n + rows - 1) / rows * per;
+    const int64_t blocks = (warps + kThreads / 32 - 1) / (kThreads / 32);
+    if (blocks > INT32_MAX) return TP_ERR_UNSUPPORTED;
+    return launch_pdl(kern, dim3(static_cast<unsigned>(blocks)), dim3(kThreads), 0, stream, d) == cudaSuccess ? TP_OK : TP_ERR_CUDA;
+}
+
+// Warps that a group of rows takes: one for each 32 / (hd / 8) sub-rows of a rank.
+int64_t warps_of_rows(int t, int kv_heads, int head_dim) {
+    const int sub = 32 / (head_dim / 8);
+    return static_cast<int64_t>(t) * ((2 * kv_heads + sub - 1) / sub);
+}
+
+// Four rows a warp where that leaves 32 warps for an SM, else one: with four and with one, 4 ranks of 2 heads of
+// 128, 8192 rows take 18.0 and 25.4 us (108 warps), 2048 8.2 and 8.1 (27 warps), 256 4.9 and 3.7.
+template <int HD>
+tp_status append(const KvAppendDesc& d, cudaStream_t stream) {
+    const int64_t per = warps_of_rows(d.pools.t, d.pools.kv_heads, HD);
     const int sms = device_sms();
     if (sms <= 0) return TP_ERR_CUDA;
     const bool few = (d.seqs.n + kRows - 1) / kRows * per < static_cast<int64_t>(sms) * 32;
-    const int64_t warps = (few ? d.seqs.n : (d.seqs.n + kRows - 1) / kRows) * per;
-    const int64_t blocks = (warps + kThreads / 32 - 1) / (kThreads / 32);
-    if (blocks > INT32_MAX) return TP_ERR_UNSUPPORTED;
-    const dim3 grid(static_cast<unsigned>(blocks));
-    return launch_pdl(few ? one : many, grid, dim3(kThreads), 0, stream, d) == cudaSuccess ? TP_OK : TP_ERR_CUDA;
+    return few ? launch_rows(d, kv4_append_kernel<HD, 1>, 1, per, stream)
+               : launch_rows(d, kv4_append_kernel<HD, kRows>, kRows, per, stream);
+}
+
+// Always four: 8192 rows take 10.8 us (20.5 with one a warp), 1024 3.9 (4.5), 256 and fewer the same 3.4.
+template <int HD>
+tp_status load(const KvLoadDesc& d, cudaStream_t stream) {
+    return launch_rows(d, kv4_load_kernel<HD, kRows>, kRows, warps_of_rows(d.pools.t, d.pools.kv_heads, HD), stream);
 }
 
 }  // namespace
 
 tp_status launch_kv4_append(const KvAppendDesc& d, cudaStream_t stream) {
-    return d.head_dim == 128 ? launch_rows(d, kv4_append_kernel<128, kRows>, kv4_append_kernel<128, 1>, stream)
-                             : launch_rows(d, kv4_append_kernel<64, kRows>, kv4_append_kernel<64, 1>, stream);
+    return d.head_dim == 128 ? append<128>(d, stream) : append<64>(d, stream);
 }
 
 tp_status launch_kv4_load(const KvLoadDesc& d, cudaStream_t stream) {
-    return d.head_dim == 128 ? launch_rows(d, kv4_load_kernel<128, kRows>, kv4_load_kernel<128, 1>, stream)
-                             : launch_rows(d, kv4_load_kernel<64, kRows>, kv4_load_kernel<64, 1>, stream);
+    return d.head_dim == 128 ? load<128>(d, stream) : load<64>(d, stream);
 }
 
 }  // namespace tpk

@@ -3,11 +3,10 @@
 //
 // The bookkeeping is a few passes over the tables and over one word per page,
 // with a whole-table dependency between them (which pages are free is known
-// when every row has said what it keeps): a chain of latencies.  Tables of up to
-// 65535 entries and 12288 pages are done by one thread block that keeps the
+// when every row has said what it keeps): a chain of latencies.  Small
+// tables over at most 12288 pages are done by one thread block that keeps the
 // pages' counters and the rows' plans in shared memory, so that only the reading
-// of lengths and tables goes through global memory (256 rows of 39 entries over
-// 2821 pages: 12 us; 17 us the other way).  Larger ones take one cluster of 8
+// of lengths and tables goes through global memory.  Larger ones take one cluster of 8
 // thread blocks with the counters in global memory: cluster barriers separate
 // the passes, and 4096 threads hide the latency of the scattered updates.
 // Prefix sums (rows -> first dealt page, pages -> rank among the free) run over
@@ -345,7 +344,10 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads) kv_
 // ------------------------------------------------------------------ one thread block, counters in shared memory
 
 constexpr int kOne = 1024;           // threads
-constexpr int kFewPages = 12288, kFewRows = 2048, kFewEntries = 65535;
+// What the counters fit and what one block is faster with.  It takes 6.2 us for a fork of 64 rows of 39 entries over
+// 2996 pages (the cluster 11.5), 10.0 for 256 rows over 10484 (15.4), 17.3 for 512 of 60 over 12288 (19.0), and
+// 26.6 for 1024 (26.4); a compaction 6.3 (10.4), 12.2 (15.3), 20.5 (17.0), and 16.7 for 512 of 40 (16.9).
+constexpr int kFewPages = 12288, kFewRows = 2048, kFewFork = 32768, kFewCompact = 16384;
 constexpr int kFewSmem = kFewPages * 12 + kFewRows * 24;
 
 // Exclusive prefix sums over the block's threads, in thread order, and the totals.
@@ -586,8 +588,8 @@ __global__ void __launch_bounds__(kOne) kv_compact_few_kernel(const __grid_const
     for (int p = tid; p < d.pages; p += kOne) d.refs[p] = refs[p];
 }
 
-bool is_few(const KvPagesDesc& d) {
-    return d.pages <= kFewPages && d.rows_out <= kFewRows && d.rows_out * d.max_blocks <= kFewEntries;
+bool is_few(const KvPagesDesc& d, int64_t entries) {
+    return d.pages <= kFewPages && d.rows_out <= kFewRows && d.rows_out * d.max_blocks <= entries;
 }
 
 // Page copies: one thread block per (copy, rank, layer) at a time, 16-byte words, eight in flight per thread.
@@ -622,8 +624,8 @@ __global__ void __launch_bounds__(kCopyThreads) kv_copy_pages_kernel(KvPagesDesc
 }
 
 template <typename Few, typename Many>
-tp_status launch_pages(const KvPagesDesc& d, Few few, Many many, std::atomic<uint64_t>& smem_set, cudaStream_t stream) {
-    if (is_few(d)) {
+tp_status launch_pages(const KvPagesDesc& d, int64_t entries, Few few, Many many, std::atomic<uint64_t>& smem_set, cudaStream_t stream) {
+    if (is_few(d, entries)) {
         if (!smem_attribute_once(reinterpret_cast<const void*>(few), kFewSmem, smem_set)) return TP_ERR_CUDA;
         const size_t smem = (static_cast<size_t>(d.pages) * 3 + static_cast<size_t>(d.rows_out) * 6) * 4;
         if (launch_pdl(few, dim3(1), dim3(kOne), smem, stream, d) != cudaSuccess) return TP_ERR_CUDA;
@@ -647,11 +649,11 @@ size_t kv_pages_workspace(int64_t rows, int64_t pages) {
 
 tp_status launch_kv_fork(const KvPagesDesc& d, cudaStream_t stream) {
     static std::atomic<uint64_t> smem_set{0};
-    return launch_pages(d, kv_fork_few_kernel, kv_fork_kernel, smem_set, stream);
+    return launch_pages(d, kFewFork, kv_fork_few_kernel, kv_fork_kernel, smem_set, stream);
 }
 tp_status launch_kv_compact(const KvPagesDesc& d, cudaStream_t stream) {
     static std::atomic<uint64_t> smem_set{0};
-    return launch_pages(d, kv_compact_few_kernel, kv_compact_kernel, smem_set, stream);
+    return launch_pages(d, kFewCompact, kv_compact_few_kernel, kv_compact_kernel, smem_set, stream);
 }
 
 }  // namespace tpk

@@ -242,3 +242,22 @@ def test_fork_at_the_limits_of_one_block(rows, cols, pages):
     table = rng.integers(0, pages, (rows, cols)).astype(np.int32)
     lens = rng.integers(0, min(cols, max(1, pages // rows)) * 16 + 1, rows).astype(np.int32)
     check_fork(table, lens, rng.integers(0, rows, rows), 1, 16, pages)
+
+
+@pytest.mark.parametrize("rows,cols", [(2048, 16), (1, 32768), (2047, 17), (32, 1025)])
+def test_fork_at_the_most_entries_of_one_block(rows, cols):
+    rng = np.random.default_rng(14)
+    pages = 12288
+    table = rng.integers(0, pages, (rows, cols)).astype(np.int32)
+    lens = rng.integers(0, min(cols, max(1, pages // rows)) * 16 + 1, rows).astype(np.int32)
+    check_fork(table, lens, rng.integers(0, rows, rows), 1, 16, pages)
+
+
+@pytest.mark.parametrize("rows,cols,pages", [(2048, 8, 12288), (1, 16384, 12288), (16, 1025, 12288), (2048, 8, 12289)])
+def test_compact_at_the_limits_of_one_block(rows, cols, pages):
+    rng = np.random.default_rng(15)
+    table, lens = tables(rng, rows, cols, 16, pages, 0.3)
+    want = K.compact(table, lens, 16, pages)
+    got = tp.tp_kv_compact(dev(table), dev(lens), None, page_size=16, pages=pages)
+    assert np.array_equal(got[0].cpu().numpy(), want[0]) and np.array_equal(got[1].cpu().numpy(), want[1])
+    assert got[2].tolist() == want[2]
