@@ -13,7 +13,11 @@ one-kernel path, over 15 weight copies so that each call starts cold), qkv
 (the 70B attention QKV column GEMM at t=8, one token, two weight copies),
 decode64 (70B MLP decode, t=4, 64 tokens, fused: the split-K down GEMM with five
 stages and its staging in the ring), fused200 (70B MLP, t=4, 200 tokens, fused:
-every tile of the down GEMM split along K over two CTA pairs).
+every tile of the down GEMM split along K over two CTA pairs), cache (append and
+load of 8192 rows, t=8, fp32 out), attend (decode attention, t=4, 64 sequences of
+6144 cached tokens), chunk (attention of two chunks of 1024 rows over 3072 tokens,
+t=4), pages (a fork of 256 rows and a compaction of 96 MB), beam (32 requests of 8
+beams, vocabulary 128000 in 4 shards).
 """
 
 import sys
@@ -25,6 +29,17 @@ from . import synth
 from .build import build
 
 H, F = 8192, 28672
+
+
+def paged_cache(t, kv_heads, lens, dev):
+    """t pools of random codes with steps and bases of 0.1, shuffled pages of 64 tokens, and lens on the device."""
+    blocks = [-(-n // 64) for n in lens]
+    pools = [torch.randint(0, 256, (sum(blocks), kv_heads, 4, 16 * 136), dtype=torch.uint8, device=dev) for _ in range(t)]
+    for p in pools: p[..., 16 * 128:].view(torch.bfloat16)[:] = 0.1
+    order = torch.randperm(sum(blocks)).to(torch.int32).split(blocks)
+    table = torch.full((len(lens), max(blocks)), -1, dtype=torch.int32)
+    for row, pages in zip(table, order): row[:len(pages)] = pages
+    return pools, table.to(dev), torch.tensor(lens, dtype=torch.int32, device=dev)
 
 
 def run(mode: str, dev: str = "cuda") -> None:
@@ -90,6 +105,34 @@ def run(mode: str, dev: str = "cuda") -> None:
         wds = [synth.normal_bf16((H, fs), 0.02, 20 + r, device=dev) for r in range(t)]
         scratch = torch.empty((1280, H), dtype=torch.float32, device=dev)      # contiguous: lent as scratch
         for _ in range(2): tp.tp_linear_row(hs, wds, mode="fused", y_dtype=torch.float32, partials=[scratch] * t)
+    elif mode == "cache":                     # append and load, 8192 rows of 8 heads of 128
+        t, n = 8, 8192
+        pools, table, lens = paged_cache(t, 1, [n], dev)
+        k = [synth.normal_bf16((n, 128), 1.0, 40 + r, device=dev) for r in range(t)]
+        cu = torch.tensor([0, n], dtype=torch.int32, device=dev)
+        for _ in range(2):
+            tp.tp_kv4_append(k, k, pools, table, lens, cu_rows=cu)
+            tp.tp_kv4_load(pools, table, lens, n, cu_rows=cu, dtype=torch.float32)
+    elif mode in ("attend", "chunk"):         # 8 query heads for each of 8 kv heads of 128
+        t, rows, seqs, length = (4, 1, 64, 6144) if mode == "attend" else (4, 1024, 2, 3072)
+        pools, table, lens = paged_cache(t, 2, [length] * seqs, dev)
+        q = [synth.normal_bf16((rows * seqs, 16 * 128), 1.0, 50 + r, device=dev) for r in range(t)]
+        cu = torch.arange(seqs + 1, dtype=torch.int32, device=dev) * rows
+        for _ in range(2): tp.tp_kv4_attention(q, pools, table, lens, cu_rows=None if rows == 1 else cu)
+    elif mode == "pages":                     # 256 rows of 8 beams that share pages; 4 ranks of 4 layers
+        t, rows, pages = 4, 256, 4000
+        pools = [torch.zeros((4, pages, 2, 4, 16 * 136), dtype=torch.uint8, device=dev) for _ in range(t)]
+        own = torch.randperm(pages, device=dev)[:rows * 12].to(torch.int32).reshape(rows, 12)
+        table = torch.cat([own, torch.full((rows, 4), -1, dtype=torch.int32, device=dev)], 1)
+        lens = torch.full((rows,), 12 * 64 - 20, dtype=torch.int32, device=dev)
+        parents = torch.arange(rows, dtype=torch.int32, device=dev) // 2 * 2
+        for _ in range(2):
+            tp.tp_kv_fork(table, lens, parents, pools)
+            tp.tp_kv_compact(table, lens, pools)
+    elif mode == "beam":                      # 256 rows of 128000 logits in 4 shards
+        logits = [synth.normal_bf16((256, 32000), 2.0, 60 + r, device=dev) for r in range(4)]
+        scores = torch.zeros((32, 8), dtype=torch.float32, device=dev)
+        for _ in range(2): tp.tp_beam_select(logits, scores, 8)
     else:
         raise ValueError(f"unknown case {mode}")
     torch.cuda.synchronize()
