@@ -294,7 +294,28 @@ __global__ void __launch_bounds__(Cfg<HD, NT>::WARPS * 32, 1) kv4_attention_kern
     pdl_wait();
     pdl_trigger();
 
-    const int many = many_from<THREADS>(a);
+    // ---- which sequences are this kernel's: those with fewer than `many` columns
+    int many = INT32_MAX;
+    if (a.many != INT32_MAX) {
+        int64_t cols = 0, tiles = 0;
+        for (int s = tid; s < a.seqs.nseq; s += THREADS) {
+            const int64_t c = static_cast<int64_t>(seq_rows(a.seqs, s).count) * a.group;
+            const int n = many_tiles(a, c);
+            if (n > 0) cols += c, tiles += n;
+        }
+#pragma unroll
+        for (int m = 16; m > 0; m >>= 1) {
+            cols += __shfl_xor_sync(0xffffffffu, cols, m);
+            tiles += __shfl_xor_sync(0xffffffffu, tiles, m);
+        }
+        if (lane == 0) scan[warp] = cols, scan_items[warp] = tiles;
+        __syncthreads();
+        cols = tiles = 0;
+#pragma unroll
+        for (int i = 0; i < WARPS; ++i) cols += scan[i], tiles += scan_items[i];
+        if (many_pays(a, cols, tiles)) many = a.many;
+        __syncthreads();
+    }
 
     // ---- the cut: total units, items, then where each of this block's workers begins
     int64_t mine = 0, items = 0;

@@ -67,32 +67,16 @@ constexpr int kManyCols = 512;       // columns of a pair of thread blocks of th
 // and 77 us (64: 51 us and 93 us against 63 us and 65 us; over 512 tokens, 128:
 // 34 us and 57 us against 30 us and 31 us).  So the second is worth its launch
 // from 64 columns for each pair of each wave, counted over the sequences that
-// have 64 by themselves (a shorter one would leave a pair to fewer).  Returns the
-// columns from which a sequence is the many-rows kernel's; both kernels ask.
-template <int THREADS>
-__device__ __forceinline__ int many_from(const AttnArgs& a) {
-    if (a.many == INT32_MAX) return INT32_MAX;
-    __shared__ int64_t s_cols[THREADS / 32], s_tiles[THREADS / 32];
+// have 64 by themselves (a shorter one would leave a pair to fewer).  `cols`
+// columns of such sequences for each of the heads make `tiles` tiles; both kernels
+// come to the same answer.
+__device__ __forceinline__ int many_tiles(const AttnArgs& a, int64_t cols) {
+    return cols < a.many ? 0 : static_cast<int>((cols + kManyCols - 1) / kManyCols);
+}
+__device__ __forceinline__ bool many_pays(const AttnArgs& a, int64_t cols, int64_t tiles) {
     const int heads = a.pools.t * a.pools.kv_heads;
-    int64_t cols = 0, tiles = 0;
-    for (int s = threadIdx.x; s < a.seqs.nseq; s += THREADS) {
-        const int64_t c = static_cast<int64_t>(seq_rows(a.seqs, s).count) * a.group;
-        if (c < a.many) continue;
-        cols += c;
-        tiles += (c + kManyCols - 1) / kManyCols;
-    }
-#pragma unroll
-    for (int m = 16; m > 0; m >>= 1) {
-        cols += __shfl_xor_sync(0xffffffffu, cols, m);
-        tiles += __shfl_xor_sync(0xffffffffu, tiles, m);
-    }
-    if (threadIdx.x % 32 == 0) s_cols[threadIdx.x / 32] = cols, s_tiles[threadIdx.x / 32] = tiles;
-    __syncthreads();
-    cols = tiles = 0;
-#pragma unroll
-    for (int i = 0; i < THREADS / 32; ++i) cols += s_cols[i], tiles += s_tiles[i];
     const int64_t waves = quotient(tiles * heads + a.pairs - 1, a.pairs);
-    return cols * heads >= waves * a.pairs * a.many ? a.many : INT32_MAX;
+    return tiles > 0 && cols * heads >= waves * a.pairs * a.many;
 }
 
 tp_status launch_attention_many(const AttnArgs& a, int head_dim, cudaStream_t stream);

@@ -186,7 +186,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) kv4_att
     __shared__ int s_abort;
     __shared__ int s_found;
     __shared__ Item s_item;
-    __shared__ int64_t s_scan[kThreads / 32];
+    __shared__ int64_t s_scan[kThreads / 32], s_cols[kThreads / 32];
     __shared__ StepInfo s_info[kInfo];
     // each unpacking warp's own: fp16 pairs (step, base) of its keys, steps and bases of its values
     __shared__ __align__(16) uint32_t s_key[kTile];
@@ -201,32 +201,40 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) kv4_att
 
     // ---- which sequence and tile: pair / heads counts tiles of 512 columns over the sequences
     {
-        const int many = many_from<kThreads>(a);
         const int64_t want = (blockIdx.x >> 1) / heads;
         const int per = (a.seqs.nseq + kThreads - 1) / kThreads;
-        auto tiles_of = [&](int s) -> int64_t {
-            const int64_t cols = static_cast<int64_t>(seq_rows(a.seqs, s).count) * a.group;
-            return cols < many ? 0 : (cols + kCols - 1) / kCols;
-        };
+        auto cols_of = [&](int s) { return static_cast<int64_t>(seq_rows(a.seqs, s).count) * a.group; };
         if (tid == 0) s_found = 0;
         const int lo = min(a.seqs.nseq, tid * per), hi = min(a.seqs.nseq, (tid + 1) * per);
-        int64_t mine = 0;
-        for (int s = lo; s < hi; ++s) mine += tiles_of(s);
+        int64_t mine = 0, mine_cols = 0;
+        for (int s = lo; s < hi; ++s) {
+            const int64_t c = cols_of(s);
+            const int n = many_tiles(a, c);
+            mine += n;
+            if (n > 0) mine_cols += c;
+        }
         int64_t upto = mine;
 #pragma unroll
         for (int m = 1; m < 32; m <<= 1) {
             const int64_t v = __shfl_up_sync(0xffffffffu, upto, m);
             if (lane >= m) upto += v;
+            mine_cols += __shfl_xor_sync(0xffffffffu, mine_cols, m);
         }
-        if (lane == 31) s_scan[warp] = upto;
+        if (lane == 31) s_scan[warp] = upto, s_cols[warp] = mine_cols;
         __syncthreads();
-        int64_t before = upto - mine;
-        for (int i = 0; i < warp; ++i) before += s_scan[i];
+        int64_t before = upto - mine, all = 0, all_cols = 0;
+#pragma unroll
+        for (int i = 0; i < kThreads / 32; ++i) {
+            if (i < warp) before += s_scan[i];
+            all += s_scan[i];
+            all_cols += s_cols[i];
+        }
+        if (!many_pays(a, all_cols, all)) return;
         if (want >= before && want < before + mine) {
             int64_t u = want - before;
             int s = lo;
             while (true) {
-                const int64_t n = tiles_of(s);
+                const int n = many_tiles(a, cols_of(s));
                 if (u < n) break;
                 u -= n;
                 ++s;
@@ -238,7 +246,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) kv4_att
             it.rows = r.count;
             it.len = max(a.seqs.lens[s], 0);
             // the last tiles see the most tokens: they start first
-            it.tile = static_cast<int>(tiles_of(s) - 1 - u);
+            it.tile = many_tiles(a, cols_of(s)) - 1 - static_cast<int>(u);
             it.head = static_cast<int>((blockIdx.x >> 1) % heads);
             s_item = it;
             s_found = 1;
