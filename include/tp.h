@@ -495,8 +495,12 @@ size_t tp_kv4_attention_workspace_size(int t, int64_t n, int64_t nseq, int heads
  * heads must be a multiple of kv_heads with at most 128 query heads per kv
  * head (TP_ERR_NOT_DIVISIBLE, TP_ERR_UNSUPPORTED).  Statistics and sums are
  * fp32; q enters the products exactly (as fp16 after a power-of-two
- * scaling), the probabilities rounded to fp16.  The order of the sums is
- * fixed by the sizes and lengths.
+ * scaling), the probabilities rounded to fp16.  Where rows * heads come to
+ * 72 and more for each pair of the device's SMs, in sequences with at least
+ * 72 rows * heads / kv_heads, keys and values are rounded to fp16 too, each
+ * by 2^-11 of itself or 2^-25 of the power of two next to the largest step
+ * or base of its 32 tokens; elsewhere they enter as the cache has them.
+ * The order of the sums is fixed by the sizes and lengths.
  */
 tp_status tp_kv4_attention(int t, int64_t n, int64_t nseq, int heads, int kv_heads, int head_dim,
                            const void* const* q, int64_t ldq, const void* const* pool, int64_t pages, int page_size,

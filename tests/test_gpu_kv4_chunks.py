@@ -85,9 +85,10 @@ def run(c, rows, heads, seed, **kw):
     return q, got
 
 
-# Heads and rows give 64 columns for each of 76 pairs of thread blocks and more.
+# Heads and rows give 72 columns for each of 76 pairs of thread blocks and more.
 @pytest.mark.parametrize("window,sinks", [(0, 0), (50, 5), (1, 0), (200, 130)])
-@pytest.mark.parametrize("t,kv,group,hd,ps", [(2, 4, 4, 128, 64), (1, 8, 5, 64, 16), (4, 8, 1, 128, 32), (1, 3, 16, 64, 128)])
+@pytest.mark.parametrize("t,kv,group,hd,ps", [(2, 4, 4, 128, 64), (1, 8, 5, 64, 16), (4, 8, 1, 128, 32), (4, 8, 2, 128, 32),
+                                              (1, 3, 16, 64, 128)])
 def test_ragged_chunks(t, kv, group, hd, ps, window, sinks):
     rows = [3, 0, 1, 70, 9, 160]
     lens = [3, 20, 77, 200, 9, 333]
@@ -95,9 +96,9 @@ def test_ragged_chunks(t, kv, group, hd, ps, window, sinks):
     run(c, rows, kv * group, 32, window=window, sinks=sinks)
 
 
-@pytest.mark.parametrize("rows", [[73], [75], [76], [77], [64, 11, 1], [40, 37]])
+@pytest.mark.parametrize("rows", [[73], [75], [76], [77], [64, 11, 1], [40, 37], [85], [86], [43, 43], [42, 43]])
 def test_around_the_border_of_the_kernels(rows):
-    """64 columns a row and eight heads: 76 rows are as many columns as the many-rows kernel asks for."""
+    """64 columns a row over all heads: 76 pairs of thread blocks ask for 72 columns each, so for 86 rows."""
     c = Cache(1, 8, 128, 64, [m + 150 for m in rows], 33)
     run(c, rows, 64, 34)
 
