@@ -12,6 +12,8 @@ Bound of an attention output (per element, `attention_bound`):
   score changes the output by at most 2 d max|v|: d = (head_dim + 16) 2^-23 A;
 * the store: half a bf16 step of the result (2^-8 relative covers a value that
   crosses a binade).
+Chunks that fill the device round keys and values to fp16 as well; their bound is
+in test_gpu_kv4_chunks.py, and those here stay within this one too.
 """
 
 import numpy as np
