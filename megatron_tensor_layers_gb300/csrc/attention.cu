@@ -26,8 +26,8 @@
 // (so that p s' could leave fp16), a larger step turns up, or a column has seen
 // nothing yet, are the maxima taken across the warp and everything rescaled.
 //
-// Split.  The unit of work is a cache block (16 tokens).  All blocks of all
-// (sequence, row tile, head) items form one line, cut into equal parts, one for
+// Split.  The unit of work is a stage of 4 cache blocks (64 tokens; 2 with 16
+// columns).  All units of all (sequence, row tile, head) items form one line, cut into equal parts, one for
 // each worker of 8, 2 or 1 warps (see `ws`); the warps of a worker share each
 // item's part of its range and merge through shared memory.  A worker's part of an item that it
 // does not hold whole goes to the workspace, and the worker that holds the
@@ -136,11 +136,17 @@ __device__ __forceinline__ uint32_t lds32(uint32_t a) {
 // [0, front) for the sinks, then [start, start + units - front).
 struct Need {
     int first_row, rows, len;
-    int front, start, blocks;        // blocks: how many of the units are cache blocks
+    int front, start, blocks;
     int units, tiles;                // units >= 1 per item (an item that sees nothing writes zeros)
+    // the blocks of unit u, `most` at most: how many, and the first of them in the order of what is seen
+    __device__ __forceinline__ int unit(int u, int most, int& first) const {
+        const int sunk = (front + most - 1) / most;
+        first = u < sunk ? u * most : front + (u - sunk) * most;
+        return max(0, min(most, (u < sunk ? front : blocks) - first));
+    }
 };
 
-__device__ __forceinline__ Need seq_need(const AttnArgs& a, int s, int cols_per_tile, int many) {
+__device__ __forceinline__ Need seq_need(const AttnArgs& a, int s, int cols_per_tile, int most, int many) {
     Need n;
     const SeqRows r = seq_rows(a.seqs, s);
     n.first_row = r.first;
@@ -153,7 +159,7 @@ __device__ __forceinline__ Need seq_need(const AttnArgs& a, int s, int cols_per_
     n.front = v.front;
     n.start = v.start;
     n.blocks = v.count;
-    n.units = max(n.blocks, 1);
+    n.units = max((n.front + most - 1) / most + (n.blocks - n.front + most - 1) / most, 1);
     return n;
 }
 
@@ -179,7 +185,7 @@ struct Cursor {
     int s, tile, head, off;          // current item and the unit in it
     Need n;
     __device__ __forceinline__ int count() const { return min(n.units - off, left); }
-    __device__ __forceinline__ void next(const AttnArgs& a, int cols_per_tile, int many, int heads) {
+    __device__ __forceinline__ void next(const AttnArgs& a, int cols_per_tile, int most, int many, int heads) {
         const int c = count();
         left -= c;
         off += c;
@@ -195,7 +201,7 @@ struct Cursor {
                 left = 0;
                 return;
             }
-            n = seq_need(a, s, cols_per_tile, many);
+            n = seq_need(a, s, cols_per_tile, most, many);
         } while (n.tiles == 0);
     }
 };
@@ -326,7 +332,7 @@ __global__ void __launch_bounds__(Cfg<HD, NT>::WARPS * 32, 1) kv4_attention_kern
     const int per = (a.seqs.nseq + THREADS - 1) / THREADS;
     Need need = {};                  // of this thread's last sequence: with one each, it is not asked for twice
     for (int s = tid * per; s < min(a.seqs.nseq, (tid + 1) * per); ++s) {
-        need = seq_need(a, s, COLS, many);
+        need = seq_need(a, s, COLS, C::BLOCKS, many);
         mine += static_cast<int64_t>(need.units) * need.tiles * heads;
         items += static_cast<int64_t>(need.tiles) * heads;
     }
@@ -354,12 +360,9 @@ __global__ void __launch_bounds__(Cfg<HD, NT>::WARPS * 32, 1) kv4_attention_kern
     // 38 us; 256: 50, 44, 51 us; 1024: 148, 122, 122 us; 2048: 282, 228, 224 us (4 are between 8 and 2, or
     // behind both).  Each warp is to have a stage, too: 64 items of 256 tokens take 21, 15, 20 us.
     const int64_t sms = gridDim.x;
-    const int ws = all_items <= sms && total >= static_cast<int64_t>(C::BLOCKS * WARPS) * all_items ? WARPS
-                   : all_items <= sms * WARPS && total >= static_cast<int64_t>(C::BLOCKS * 2) * all_items ? 2 : 1;
+    const int ws = all_items <= sms && total >= WARPS * all_items ? WARPS : all_items <= sms * WARPS && total >= 2 * all_items ? 2 : 1;
     const int groups = WARPS / ws;
-    const int64_t least = C::BLOCKS * ws;
-    const int workers =
-        static_cast<int>(min(static_cast<int64_t>(gridDim.x) * groups, quotient(total + least - 1, least)));
+    const int workers = static_cast<int>(min(sms * groups, quotient(total + ws - 1, ws)));
     const Parts parts(total, workers);
     for (int i = 0; i < groups; ++i) {
         const int w = i * gridDim.x + blockIdx.x;
@@ -373,7 +376,7 @@ __global__ void __launch_bounds__(Cfg<HD, NT>::WARPS * 32, 1) kv4_attention_kern
             int s = tid * per;
             if (per > 1)
                 while (true) {
-                    need = seq_need(a, s, COLS, many);
+                    need = seq_need(a, s, COLS, C::BLOCKS, many);
                     const int64_t w_s = static_cast<int64_t>(need.units) * need.tiles * heads;
                     if (u < w_s) break;
                     u -= w_s;
@@ -451,44 +454,47 @@ __global__ void __launch_bounds__(Cfg<HD, NT>::WARPS * 32, 1) kv4_attention_kern
     const uint32_t my_bars = smem_u32(&bars[warp * kStages]);
     // this warp's share of a segment of n units
     auto share = [&](int n, int w) { return static_cast<int>(static_cast<uint32_t>(n) * static_cast<uint64_t>(w) / ws); };
-    // units of the stage that begins with unit u of a share [u0, u1): it ends with the sinks' blocks and with a batch
-    auto stage_units = [&](int u, int u0, int u1, int front) {
-        return min(min(C::BLOCKS, u1 - u), min(u < front ? front - u : C::BLOCKS, kBatch - ((u - u0) & (kBatch - 1))));
-    };
     int load_u = 0, load_u0 = 0, load_end = 0;
-    int64_t batch_off = -1;          // lane l holds the address of unit l of the batch
+    int64_t batch_off = -1;          // lane l holds the address of block l of the batch
     uint32_t batch_there = 0;
-    int next_page = -2;              // and the page of unit l of the next batch, -2: none
-    auto block_of = [&](int u) { return u < ahead.n.front ? u : ahead.n.start + u - ahead.n.front; };
+    int next_page = -2;              // and the page of block l of the next batch, -2: none
+    constexpr int kUnits = kBatch / C::BLOCKS;
+    auto block_at = [](const Need& n, int i) { return i < n.front ? i : n.start + i - n.front; };
+    // the block of this lane in the batch that begins with unit u, -1: none
+    auto lane_block = [&](int u) {
+        u += lane / C::BLOCKS;
+        int first;
+        if (u >= load_end || lane % C::BLOCKS >= ahead.n.unit(u, C::BLOCKS, first)) return -1;
+        return block_at(ahead.n, first + lane % C::BLOCKS);
+    };
     auto fetch_page = [&](int u) {
-        return u < load_end && u < ahead.n.blocks
-                   ? kv_page_at(a.seqs.table + ahead.s * a.seqs.max_blocks, a.seqs.max_blocks, a.pools.page_shift, block_of(u))
-                   : -2;
+        const int block = lane_block(u);
+        return block < 0 ? -2
+                         : kv_page_at(a.seqs.table + ahead.s * a.seqs.max_blocks, a.seqs.max_blocks, a.pools.page_shift, block);
     };
     auto open_segment = [&]() {
         load_u = load_u0 = ahead.off + share(ahead.count(), wi);
         load_end = ahead.off + share(ahead.count(), wi + 1);
-        next_page = fetch_page(load_u + lane);
+        next_page = fetch_page(load_u);
     };
     int issued = 0;
     auto load_stage = [&]() {
         while (load_u >= load_end) {
-            ahead.next(a, COLS, many, heads);
+            ahead.next(a, COLS, C::BLOCKS, many, heads);
             if (ahead.left <= 0) return;
             open_segment();
         }
         const int rank = ahead.head / a.pools.kv_heads;
-        const int at = (load_u - load_u0) & (kBatch - 1);
+        const int at = (load_u - load_u0) & (kUnits - 1);
         if (at == 0) {
-            const int u = load_u + lane, page = next_page;
+            const int page = next_page;
             batch_off = kv_page_offset(page, a.pools.pages, a.pools.page_shift, a.pools.kv_heads,
-                                       ahead.head - rank * a.pools.kv_heads, block_of(u), B::BYTES);
+                                       ahead.head - rank * a.pools.kv_heads, lane_block(load_u), B::BYTES);
             if (batch_off < 0 && page != -2) raise_status(a.seqs.status, TP_ERR_INVALID_ARG);
             batch_there = __ballot_sync(0xffffffffu, batch_off >= 0);
-            next_page = fetch_page(u + kBatch);
+            next_page = fetch_page(load_u + kUnits);
         }
-        const int cnt = stage_units(load_u, load_u0, load_end, ahead.n.front);
-        const uint32_t mask = (batch_there >> at) & ((1u << cnt) - 1u);
+        const uint32_t mask = (batch_there >> (at * C::BLOCKS)) & ((1u << C::BLOCKS) - 1u);
         const int st = issued % kStages;
         const uint32_t bar = my_bars + st * 8;
         if (lane == 0) {
@@ -496,11 +502,11 @@ __global__ void __launch_bounds__(Cfg<HD, NT>::WARPS * 32, 1) kv4_attention_kern
             mbar_arrive_expect_tx(bar, __popc(mask) * B::BYTES);
         }
         __syncwarp();
-        const uint32_t i = static_cast<uint32_t>(lane - at);             // this lane's block of the stage
-        if (i < static_cast<uint32_t>(cnt) && batch_off >= 0)
+        const uint32_t i = static_cast<uint32_t>(lane - at * C::BLOCKS); // this lane's block of the stage
+        if (i < static_cast<uint32_t>(C::BLOCKS) && batch_off >= 0)
             bulk_load(ring + st * C::STAGE + i * B::BYTES, a.pools.pool[rank] + batch_off, B::BYTES, bar);
         ++issued;
-        load_u += cnt;
+        ++load_u;
     };
     open_segment();
     fetch_q(cur);
@@ -581,15 +587,15 @@ __global__ void __launch_bounds__(Cfg<HD, NT>::WARPS * 32, 1) kv4_attention_kern
             for (int e = 0; e < 2; ++e) mx[nt][e] = kNegInf, sum[nt][e] = 0.0f, corr[nt][e] = 0.0f;
         }
 
-        for (int u = u0; u < u1;) {
-            const int cnt = stage_units(u, u0, u1, cur.n.front);
+        for (int u = u0; u < u1; ++u) {
             const int st = used % kStages;
             if (!dead) dead = !mbar_wait_warp(my_bars + st * 8, (used / kStages) & 1, &s_abort, a.seqs.status);
             const uint32_t mask = dead ? 0u : static_cast<uint32_t>(stage_mask[warp * kStages + st]);
             const uint32_t buf = ring + st * C::STAGE;
-            const int j0 = (u < cur.n.front ? u : cur.n.start + u - cur.n.front) * kKvBlock;
+            int first;
+            cur.n.unit(u, C::BLOCKS, first);
+            const int j0 = block_at(cur.n, first) * kKvBlock;
             const int j1 = j0 + C::BLOCKS * kKvBlock - 1;
-            u += cnt;
 
             // One stage; `edge`: some block is missing or some column does not see some token.
             auto stage = [&](auto edge) {
@@ -824,7 +830,7 @@ __global__ void __launch_bounds__(Cfg<HD, NT>::WARPS * 32, 1) kv4_attention_kern
         float4* slot = slots + static_cast<size_t>(slot_no) * C::PART;
         const bool awaited = !complete && seg_off + seg_n < cur.n.units; // by the worker that holds the end
         first_segment = false;
-        cur.next(a, COLS, many, heads);
+        cur.next(a, COLS, C::BLOCKS, many, heads);
         const bool more = cur.left > 0;
         if (more) fetch_q(cur);
         auto store = [&](int v, const auto& o, const float2& total) {    // vectors of a complete item
