@@ -356,11 +356,12 @@ __global__ void __launch_bounds__(Cfg<HD, NT>::WARPS * 32, 1) kv4_attention_kern
     if (total == 0) return;
     // Warps of a worker.  Eight share an item's latency, but meet at its end and pay for each item's
     // beginning eight times; alone a warp does neither, but a long item is then the sum of many parts.
-    // Of 4096 tokens, head dimension 128, with 8, 2 and 1 warps: 8 items 16.4, 20.3, 62 us; 128: 29, 29,
-    // 38 us; 256: 50, 44, 51 us; 1024: 148, 122, 122 us; 2048: 282, 228, 224 us (4 are between 8 and 2, or
-    // behind both).  Each warp is to have a stage, too: 64 items of 256 tokens take 21, 15, 20 us.
+    // Of 4097 tokens, head dimension 128, with 8, 2 and 1 warps: 8 items 16, 20, 43 us; 64: 22, 21, 38 us;
+    // 256: 49, 42, 48 us; 1024: 148, 119, 118 us; 2048: 282, 224, 219 us (4 are between 8 and 2, or behind
+    // both).  Each warp is to have a unit, too: 128 items of 128 tokens take 27, 15, 17 us.
     const int64_t sms = gridDim.x;
-    const int ws = all_items <= sms && total >= WARPS * all_items ? WARPS : all_items <= sms * WARPS && total >= 2 * all_items ? 2 : 1;
+    const int ws = all_items * 4 <= sms && total >= WARPS * all_items ? WARPS
+                   : all_items <= sms * WARPS && total >= 2 * all_items ? 2 : 1;
     const int groups = WARPS / ws;
     const int workers = static_cast<int>(min(sms * groups, quotient(total + ws - 1, ws)));
     const Parts parts(total, workers);
@@ -597,15 +598,16 @@ __global__ void __launch_bounds__(Cfg<HD, NT>::WARPS * 32, 1) kv4_attention_kern
             const int j0 = block_at(cur.n, first) * kKvBlock;
             const int j1 = j0 + C::BLOCKS * kKvBlock - 1;
 
-            // One stage; `edge`: some block is missing or some column does not see some token.
-            auto stage = [&](auto edge) {
+            // `blocks` of the stage's blocks, from block `from` on; `edge`: some column does not see some token.
+            auto stage = [&](auto edge, auto blocks, int from) {
                 constexpr bool EDGE = decltype(edge)::value;
-                float x[C::BLOCKS][NT][4];
-                uint32_t vp[C::BLOCKS][2];
+                constexpr int BLOCKS = decltype(blocks)::value;
+                float x[BLOCKS][NT][4];
+                uint32_t vp[BLOCKS][2];
                 uint32_t vtop = 0;                                       // largest step of the values: not negative
 #pragma unroll
-                for (int i = 0; i < C::BLOCKS; ++i) {
-                    const uint32_t rec = buf + i * B::BYTES;
+                for (int i = 0; i < BLOCKS; ++i) {
+                    const uint32_t rec = buf + (from + i) * B::BYTES;
                     uint32_t wa[HD / 32], wb[HD / 32];
                     const uint32_t ka = rec + B::KEYS + tok * B::ROW + t4 * (B::ROW / 4);
                     if constexpr (HD == 128) {
@@ -647,16 +649,15 @@ __global__ void __launch_bounds__(Cfg<HD, NT>::WARPS * 32, 1) kv4_attention_kern
                             x[i][nt][2 + e] = fmaf(x[i][nt][2 + e] + y[nt][2 + e], cmul[nt][e] * s1, cadd[nt][e] * b1);
                         }
                     if constexpr (EDGE) {
-                        const bool there = (mask >> i) & 1u;
-                        const int ja = j0 + i * kKvBlock + tok, jb = ja + 8;
+                        const int ja = j0 + (from + i) * kKvBlock + tok, jb = ja + 8;
                         // a pair that no column sees may hold anything
-                        if (!there || ja > row_hi || !(a.window == 0 || ja > row_lo - a.window || ja < a.sinks)) vp[i][0] = 0;
-                        if (!there || jb > row_hi || !(a.window == 0 || jb > row_lo - a.window || jb < a.sinks)) vp[i][1] = 0;
+                        if (ja > row_hi || !(a.window == 0 || ja > row_lo - a.window || ja < a.sinks)) vp[i][0] = 0;
+                        if (jb > row_hi || !(a.window == 0 || jb > row_lo - a.window || jb < a.sinks)) vp[i][1] = 0;
 #pragma unroll
                         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                             for (int e = 0; e < 2; ++e) {
-                                const int p = there ? cpos[nt][e] : -1;
+                                const int p = cpos[nt][e];
                                 if (!(ja <= p && (a.window == 0 || ja > p - a.window || ja < a.sinks))) x[i][nt][e] = kNegInf;
                                 if (!(jb <= p && (a.window == 0 || jb > p - a.window || jb < a.sinks)))
                                     x[i][nt][2 + e] = kNegInf;
@@ -666,7 +667,7 @@ __global__ void __launch_bounds__(Cfg<HD, NT>::WARPS * 32, 1) kv4_attention_kern
                 }
 
                 // p s' as B fragments, and what the stage adds to the sums
-                uint32_t pf[C::BLOCKS][NT][2];
+                uint32_t pf[BLOCKS][NT][2];
                 float psum[NT][2], pcorr[NT][2];
                 auto weigh = [&]() {
                     const float vscale = __uint_as_float(static_cast<uint32_t>(253 - vexp) << 23) * (1 << kPShift);
@@ -679,7 +680,7 @@ __global__ void __launch_bounds__(Cfg<HD, NT>::WARPS * 32, 1) kv4_attention_kern
                             m[nt][e] = mx[nt][e] == kNegInf ? 0.0f : mx[nt][e];
                         }
 #pragma unroll
-                    for (int i = 0; i < C::BLOCKS; ++i) {
+                    for (int i = 0; i < BLOCKS; ++i) {
                         const float s0 = __uint_as_float(vp[i][0] << 16) * vscale, b0 = __uint_as_float(vp[i][0] & 0xffff0000u);
                         const float s1 = __uint_as_float(vp[i][1] << 16) * vscale, b1 = __uint_as_float(vp[i][1] & 0xffff0000u);
 #pragma unroll
@@ -722,7 +723,7 @@ __global__ void __launch_bounds__(Cfg<HD, NT>::WARPS * 32, 1) kv4_attention_kern
                         for (int e = 0; e < 2; ++e) {
                             cmax[nt][e] = kNegInf;
 #pragma unroll
-                            for (int i = 0; i < C::BLOCKS; ++i)
+                            for (int i = 0; i < BLOCKS; ++i)
                                 cmax[nt][e] = fmaxf(cmax[nt][e], fmaxf(x[i][nt][e], x[i][nt][2 + e]));
                         }
 #pragma unroll
@@ -760,13 +761,13 @@ __global__ void __launch_bounds__(Cfg<HD, NT>::WARPS * 32, 1) kv4_attention_kern
 #pragma unroll
                     for (int e = 0; e < 2; ++e) sum[nt][e] += psum[nt][e], corr[nt][e] += pcorr[nt][e];
 #pragma unroll
-                for (int i = 0; i < C::BLOCKS; ++i) {
+                for (int i = 0; i < BLOCKS; ++i) {
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                         for (int e = 0; e < 2; ++e) pf[i][nt][e] = transpose8x8(pf[i][nt][e]);
                     // values: tokens t4, 4 + (t4 ^ 1) and the same + 8 are this lane's columns of k
-                    const uint32_t va = buf + i * B::BYTES + B::VALS + g * (B::ROW / 8);
+                    const uint32_t va = buf + (from + i) * B::BYTES + B::VALS + g * (B::ROW / 8);
                     constexpr int W = HD / 64;
                     uint32_t y[4][W];
 #pragma unroll
@@ -799,9 +800,12 @@ __global__ void __launch_bounds__(Cfg<HD, NT>::WARPS * 32, 1) kv4_attention_kern
             const bool whole = mask == (1u << C::BLOCKS) - 1u && j1 <= row_lo &&
                                (a.window == 0 || j0 > row_hi - a.window || j1 < a.sinks);
             if (whole)
-                stage(std::false_type{});
+                stage(std::false_type{}, std::integral_constant<int, C::BLOCKS>{}, 0);
             else
-                stage(std::true_type{});
+                // an item's ends: block by block, in a quarter of the instructions, which are rarely in the cache
+#pragma unroll 1
+                for (uint32_t left = mask; left != 0; left &= left - 1)
+                    stage(std::true_type{}, std::integral_constant<int, 1>{}, __ffs(left) - 1);
             __syncwarp();                                                // every lane is done with the stage
             ++used;
             if (!dead) load_stage();
