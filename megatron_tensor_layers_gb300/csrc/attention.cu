@@ -2,8 +2,8 @@
 // speculation): one pass over the cached codes.  Large calls are bound by the
 // instructions that turn codes into operands (236 for a block of 16 tokens and 8
 // columns, at 0.46 an SM quarter and cycle, with two warps there): 64 sequences of
-// 4100 to 8192 tokens for 8 kv heads of 128 take 90 us, 4.7 TB/s.  Small ones by
-// latencies: one sequence of 4097 tokens takes 15 us.
+// 4100 to 8192 tokens for 8 kv heads of 128 take 87 us, 4.8 TB/s.  Small ones by
+// latencies: one sequence of 4097 tokens takes 13.4 us.
 //
 // Mathematics.  With key j = s_j u_j + b_j (u_j the codes),
 //     x_j = c (s_j (q . u_j) + b_j sum(q)),      c = scale log2(e),
@@ -47,7 +47,10 @@
 // the tokens and the head dimension as their 16 rows and only 8 columns, so 8
 // query heads of a group fill them.  tcgen05 would want 128 rows of them.  With
 // two warps on a scheduler it is the independent work within a warp that hides
-// latencies: the blocks of a full, fully visible stage run as one straight line.
+// latencies: the blocks of a full, fully visible stage run as one straight line
+// (87 us; two at a time 91, one at a time 94).  Three warps there, of 168
+// registers, take 100 us and more.  An item's ends, whose instructions are rarely
+// in the cache, go block by block.
 #include <algorithm>
 #include <type_traits>
 
@@ -961,8 +964,8 @@ tp_status launch_kv4_attention(const KvAttentionDesc& d, cudaStream_t stream) {
         if (s != TP_OK) return s;
     }
     // 16 columns per tile where a sequence's rows fill more than 8 and there are enough tiles for every warp even so.
-    // 4096 tokens, 16 columns for each of eight heads, tiles of 16 and of 8: 64 sequences 122 and 131 us, 16 43 and 41,
-    // 4 28 and 22; of 64 dimensions, which leave more registers: 89 and 105, 31 and 34, 20 and 19 us.
+    // 4096 tokens, 16 columns for each of eight heads, tiles of 16 and of 8: 64 sequences 120 and 126 us, 16 42 and 39,
+    // 4 27 and 21; of 64 dimensions, which leave more registers: 87 and 100, 30 and 32, 20 and 19 us.
     const bool filled = d.group > 8 || (d.seqs.cu_rows != nullptr && d.group * (d.seqs.n / std::max(d.seqs.nseq, 1)) > 8);
     const bool wide = filled && columns >= static_cast<int64_t>(sms) * (d.head_dim == 128 ? 48 : 12);
     if (d.head_dim == 128) return wide ? launch_few<128, 2>(a, sms, stream) : launch_few<128, 1>(a, sms, stream);

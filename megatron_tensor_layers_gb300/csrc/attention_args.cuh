@@ -63,9 +63,9 @@ constexpr int kManyCols = 512;       // columns of a pair of thread blocks of th
 // Which kernel takes a sequence.  The few-rows kernel's time grows with the
 // columns, the many-rows kernel's with the waves of pairs of blocks, however few
 // columns they hold: over 4096 cached tokens of head dimension 128 the first takes
-// 65 us for 4096 columns, 95 for 6144 and 114 for 8192, the second 77 to 79 us
-// (dimension 64: 47, 63 and 81 us against 64 to 66; over 512 tokens, 128: 30, 31
-// and 46 us against 32 to 34).  So the second is worth its launch from 72 columns
+// 64 us for 4096 columns, 84 for 5504 and 111 for 8192, the second 77 to 78 us
+// (dimension 64: 46, 59 and 80 us against 64 to 66; over 512 tokens, 128: 23, 26
+// and 39 us against 32 to 33).  So the second is worth its launch from 72 columns
 // for each pair of each wave, counted over the sequences that
 // have 72 by themselves (a shorter one would leave a pair to fewer).  `cols`
 // columns of such sequences for each of the heads make `tiles` tiles; both kernels
