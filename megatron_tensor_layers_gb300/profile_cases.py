@@ -15,7 +15,7 @@ decode64 (70B MLP decode, t=4, 64 tokens, fused: the split-K down GEMM with five
 stages and its staging in the ring), fused200 (70B MLP, t=4, 200 tokens, fused:
 every tile of the down GEMM split along K over two CTA pairs), cache (append and
 load of 8192 rows, t=8, fp32 out), attend (decode attention, t=4, 64 sequences of
-6144 cached tokens), chunk (attention of two chunks of 1024 rows over 3072 tokens,
+6144 cached tokens), chunk (attention of two chunks of 1024 rows over 3000 tokens,
 t=4), pages (a fork of 256 rows and a compaction of 96 MB), beam (32 requests of 8
 beams, vocabulary 128000 in 4 shards).
 """
@@ -114,7 +114,7 @@ def run(mode: str, dev: str = "cuda") -> None:
             tp.tp_kv4_append(k, k, pools, table, lens, cu_rows=cu)
             tp.tp_kv4_load(pools, table, lens, n, cu_rows=cu, dtype=torch.float32)
     elif mode in ("attend", "chunk"):         # 8 query heads for each of 8 kv heads of 128
-        t, rows, seqs, length = (4, 1, 64, 6144) if mode == "attend" else (4, 1024, 2, 3072)
+        t, rows, seqs, length = (4, 1, 64, 6144) if mode == "attend" else (4, 1024, 2, 3000)
         pools, table, lens = paged_cache(t, 2, [length] * seqs, dev)
         q = [synth.normal_bf16((rows * seqs, 16 * 128), 1.0, 50 + r, device=dev) for r in range(t)]
         cu = torch.arange(seqs + 1, dtype=torch.int32, device=dev) * rows
