@@ -1,6 +1,6 @@
 // Attention over the paged 4-bit cache for many rows per sequence (chunks of
 // prompts): matrix products on the 5th-generation tensor cores.  8192 new rows in
-// four chunks over 2100 to 6001 tokens, 64 query heads of 128, take 894 us, 972
+// four chunks over 2100 to 6001 tokens, 64 query heads of 128, take 886 us, 980
 // TFLOP/s.  Bound by the chain of a tile (S, then its exponentials, then the
 // second product, then the next S): a step of both tiles takes about 4000 cycles,
 // its products 2200 of them.
@@ -209,6 +209,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) kv4_att
         auto cols_of = [&](int s) { return static_cast<int64_t>(seq_rows(a.seqs, s).count) * a.group; };
         if (tid == 0) s_found = 0;
         const int lo = min(a.seqs.nseq, tid * per), hi = min(a.seqs.nseq, (tid + 1) * per);
+        const int first_len = lo < hi ? a.seqs.lens[lo] : 0;     // on its way with the offsets
         int64_t mine = 0, mine_cols = 0;
         for (int s = lo; s < hi; ++s) {
             const int64_t c = cols_of(s);
@@ -247,7 +248,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) kv4_att
             it.seq = s;
             it.first_row = r.first;
             it.rows = r.count;
-            it.len = max(a.seqs.lens[s], 0);
+            it.len = max(s == lo ? first_len : a.seqs.lens[s], 0);
             // the last tiles see the most tokens: they start first
             it.tile = many_tiles(a, cols_of(s)) - 1 - static_cast<int>(u);
             it.head = static_cast<int>((blockIdx.x >> 1) % heads);
