@@ -182,6 +182,15 @@ def _dt(dtype) -> int:
 # ctypes objects once, each time it is called.
 
 
+def _scratch(shape, dtype, device) -> torch.Tensor:
+    """Memory that an entry point allocates and does not return: a recorded
+    call keeps it, as its launches have the address."""
+    x = torch.empty(shape, dtype=dtype, device=device)
+    if getattr(_tls, "rec", None) is not None:
+        _tls.kept.append(x)
+    return x
+
+
 def _launch(name: str, *args) -> None:
     rec = getattr(_tls, "rec", None)
     fn = getattr(load(), name)
@@ -209,7 +218,8 @@ class PreparedCall:
 
     Calling it makes the same calls again, on the stream that was current (or
     given) when it was prepared, and returns what the entry point returned then
-    (the same output tensors).  It keeps the tensors it was prepared with alive;
+    (the same output tensors).  It keeps the tensors it was prepared with alive, and
+    what the entry point allocated for itself (a workspace that was not given);
     their contents may change between calls (that is the use: new inputs written
     into the same buffers), but their storage must not be replaced or resized.
     Ownership, layout and error behaviour are those of the entry point: a C call
@@ -240,15 +250,15 @@ def prepare(entry, *args, **kwargs) -> PreparedCall:
     launches it.  Outputs the entry point would allocate are allocated now."""
     if getattr(_tls, "rec", None) is not None:
         raise RuntimeError("prepare() does not nest")
-    rec = []
-    _tls.rec = rec
+    rec, kept = [], []
+    _tls.rec, _tls.kept = rec, kept
     try:
         result = entry(*args, **kwargs)
     finally:
-        _tls.rec = None
+        _tls.rec = _tls.kept = None
     if not rec:
         raise ValueError(f"{getattr(entry, '__name__', entry)!s} made no launch to prepare")
-    return PreparedCall(rec, (args, kwargs), result)
+    return PreparedCall(rec, (args, kwargs, kept), result)
 
 
 # ----------------------------------------------------------------- argument checks
@@ -417,7 +427,7 @@ def tp_linear_row(x: Sequence[torch.Tensor], w: Sequence[torch.Tensor], *, bias:
         _dense("bias", bias, (out,), BF16)
     dev = x[0].device
     if mode != "fused" and partials is None:
-        partials = [torch.empty((n, out), dtype=partial_dtype, device=dev) for _ in range(t)]
+        partials = [_scratch((n, out), partial_dtype, dev) for _ in range(t)]
     if reduce_results and y is None:
         y = torch.empty((n, out), dtype=y_dtype, device=dev)
     if partials is not None:
@@ -496,7 +506,7 @@ def tp_mlp_forward(x: torch.Tensor, w_gate_up: Sequence[torch.Tensor], w_down: S
     t, n, h, f = _mlp_args(x, w_gate_up, w_down, bias_down, act, mode)
     if workspace is None:
         need = tp_mlp_workspace_size(t, n, h, f, mode, partial_dtype)
-        workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=x.device)
+        workspace = _scratch(max(need, 256), torch.uint8, x.device)
     if y is None:
         y = torch.empty((n, h), dtype=y_dtype, device=x.device)
     _dense("workspace", workspace)
@@ -862,7 +872,7 @@ def tp_kv4_attention(q: Sequence[torch.Tensor], pools: Sequence[torch.Tensor], t
     ldo = _matrices("out", out, (n, width), BF16)
     if workspace is None:
         need = tp_kv4_attention_workspace_size(t, n, nseq, heads, kv, hd)
-        workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=q[0].device)
+        workspace = _scratch(max(need, 256), torch.uint8, q[0].device)
     _dense("workspace", workspace)
     _on_gpu(q, pools, table, lens, cu_rows, workspace, out)
     _launch("tp_kv4_attention", t, n, nseq, heads, kv, hd, _ptrs(q), ldq, _ptrs(pools), pages, ps, _ptr(table),
@@ -894,7 +904,7 @@ def _page_args(table, lens, pools, page_size, pages, held, rows_out, table_out, 
     if info is None:
         info = torch.empty(4, dtype=torch.int32, device=dev)
     if workspace is None:
-        workspace = torch.empty(max(load().tp_kv_pages_workspace_size(rows_out, pages), 256), dtype=torch.uint8, device=dev)
+        workspace = _scratch(max(load().tp_kv_pages_workspace_size(rows_out, pages), 256), torch.uint8, dev)
     _dense("table_out", table_out, (rows_out, mb), I32S)
     _dense("refs", refs, (pages,), I32S)
     _dense("info", info, (4,), I32S)
@@ -1015,7 +1025,7 @@ def tp_beam_select(logits: Sequence[Optional[torch.Tensor]], scores: torch.Tenso
     _dense("tokens_out", tokens_out, (items, k), I32S)
     if workspace is None:
         need = tp_beam_workspace_size(items, beams, k, max(vocab, 1))
-        workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=dev)
+        workspace = _scratch(max(need, 256), torch.uint8, dev)
     _dense("workspace", workspace)
     _on_gpu(logits, scores, finished, scores_out, rows_out, tokens_out, workspace)
     _launch("tp_beam_select", t, items, beams, k, cols, _ptrs(logits), ldl, _dt(ref.dtype), _ptr(scores), _ptr(finished),

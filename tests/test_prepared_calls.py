@@ -99,3 +99,41 @@ def test_prepare_keeps_its_tensors(host_tensors):
     name, raw, args = plan._calls[0]
     assert args[4].value == x.data_ptr() and args[13].value == ws.data_ptr()
     assert isinstance(args[6], ctypes.Array) and args[6][1] == wgu[1].data_ptr()
+
+
+def _pointers(plan):
+    return {a.value for _, _, args in plan._calls for a in args if isinstance(a, ctypes.c_void_p) and a.value} | \
+        {p for _, _, args in plan._calls for a in args if isinstance(a, ctypes.Array) and a._type_ is ctypes.c_void_p
+         for p in a if p}
+
+
+def _tensors(x):
+    if isinstance(x, torch.Tensor):
+        yield x
+    elif isinstance(x, dict):
+        yield from _tensors(list(x.values()))
+    elif isinstance(x, (list, tuple)):
+        for y in x:
+            yield from _tensors(y)
+
+
+@pytest.mark.parametrize("what", ["mlp", "linear_row", "attention", "fork", "compact", "beam"])
+def test_prepare_keeps_what_the_entry_point_allocated(host_tensors, what):
+    """Every address of the recorded launches lies in a tensor that the prepared call keeps: the workspace and the
+    partials that the caller did not give, too."""
+    i32 = lambda *s: torch.zeros(s, dtype=torch.int32)  # noqa: E731
+    z = lambda *s: torch.zeros(s, dtype=torch.bfloat16)  # noqa: E731
+    pool = [_lib.tp_kv4_pool(5, 32, 2, 128, device="cpu")]
+    deep = [_lib.tp_kv4_pool(5, 32, 2, 128, layers=2, device="cpu")]
+    entry, args, kw = {
+        "mlp": lambda: (_lib.tp_mlp_forward, _mlp(), {}),
+        "linear_row": lambda: (_lib.tp_linear_row, ([z(8, 128)] * 2, [z(64, 128)] * 2), {}),
+        "attention": lambda: (_lib.tp_kv4_attention, ([z(3, 512)], pool, i32(3, 4), i32(3)), {}),
+        "fork": lambda: (_lib.tp_kv_fork, (i32(3, 4), i32(3), i32(6), deep), {}),
+        "compact": lambda: (_lib.tp_kv_compact, (i32(3, 4), i32(3), deep), {}),
+        "beam": lambda: (_lib.tp_beam_select, ([z(6, 10)], torch.zeros((2, 3)), 3), {}),
+    }[what]()
+    plan = _lib.prepare(entry, *args, stream=0, **kw)
+    held = [(x.data_ptr(), x.data_ptr() + x.numel() * x.element_size()) for x in _tensors((plan._keep, plan.result))]
+    for p in _pointers(plan):
+        assert any(a <= p < b for a, b in held), what
