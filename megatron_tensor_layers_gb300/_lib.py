@@ -182,10 +182,19 @@ def _dt(dtype) -> int:
 # ctypes objects once, each time it is called.
 
 
-def _scratch(shape, dtype, device) -> torch.Tensor:
-    """Memory that an entry point allocates and does not return: a recorded
-    call keeps it, as its launches have the address."""
-    x = torch.empty(shape, dtype=dtype, device=device)
+def _scratch(shape, dtype, device, stream) -> torch.Tensor:
+    """Memory that an entry point allocates and does not return.  It comes from
+    the allocator's pool of the stream that the call runs on (its argument
+    `stream`): once freed, at the entry point's return, only work that comes
+    after the call on that stream can get it.  A recorded call keeps it, as its
+    launches have the address."""
+    if stream is None or device.type != "cuda":
+        x = torch.empty(shape, dtype=dtype, device=device)
+    else:
+        if not isinstance(stream, torch.cuda.Stream):
+            stream = torch.cuda.ExternalStream(_stream(stream), device=device)
+        with torch.cuda.stream(stream):
+            x = torch.empty(shape, dtype=dtype, device=device)
     if getattr(_tls, "rec", None) is not None:
         _tls.kept.append(x)
     return x
@@ -427,7 +436,7 @@ def tp_linear_row(x: Sequence[torch.Tensor], w: Sequence[torch.Tensor], *, bias:
         _dense("bias", bias, (out,), BF16)
     dev = x[0].device
     if mode != "fused" and partials is None:
-        partials = [_scratch((n, out), partial_dtype, dev) for _ in range(t)]
+        partials = [_scratch((n, out), partial_dtype, dev, stream) for _ in range(t)]
     if reduce_results and y is None:
         y = torch.empty((n, out), dtype=y_dtype, device=dev)
     if partials is not None:
@@ -506,7 +515,7 @@ def tp_mlp_forward(x: torch.Tensor, w_gate_up: Sequence[torch.Tensor], w_down: S
     t, n, h, f = _mlp_args(x, w_gate_up, w_down, bias_down, act, mode)
     if workspace is None:
         need = tp_mlp_workspace_size(t, n, h, f, mode, partial_dtype)
-        workspace = _scratch(max(need, 256), torch.uint8, x.device)
+        workspace = _scratch(max(need, 256), torch.uint8, x.device, stream)
     if y is None:
         y = torch.empty((n, h), dtype=y_dtype, device=x.device)
     _dense("workspace", workspace)
@@ -872,7 +881,7 @@ def tp_kv4_attention(q: Sequence[torch.Tensor], pools: Sequence[torch.Tensor], t
     ldo = _matrices("out", out, (n, width), BF16)
     if workspace is None:
         need = tp_kv4_attention_workspace_size(t, n, nseq, heads, kv, hd)
-        workspace = _scratch(max(need, 256), torch.uint8, q[0].device)
+        workspace = _scratch(max(need, 256), torch.uint8, q[0].device, stream)
     _dense("workspace", workspace)
     _on_gpu(q, pools, table, lens, cu_rows, workspace, out)
     _launch("tp_kv4_attention", t, n, nseq, heads, kv, hd, _ptrs(q), ldq, _ptrs(pools), pages, ps, _ptr(table),
@@ -881,7 +890,7 @@ def tp_kv4_attention(q: Sequence[torch.Tensor], pools: Sequence[torch.Tensor], t
     return out
 
 
-def _page_args(table, lens, pools, page_size, pages, held, rows_out, table_out, refs, info, workspace):
+def _page_args(table, lens, pools, page_size, pages, held, rows_out, table_out, refs, info, workspace, stream):
     """What tp_kv_fork and tp_kv_compact share: checks, defaults, and (t, layers, page_bytes, page_size, pages)."""
     t, layers, page_bytes = 1, 1, 16
     if pools is not None:
@@ -904,7 +913,7 @@ def _page_args(table, lens, pools, page_size, pages, held, rows_out, table_out, 
     if info is None:
         info = torch.empty(4, dtype=torch.int32, device=dev)
     if workspace is None:
-        workspace = _scratch(max(load().tp_kv_pages_workspace_size(rows_out, pages), 256), torch.uint8, dev)
+        workspace = _scratch(max(load().tp_kv_pages_workspace_size(rows_out, pages), 256), torch.uint8, dev, stream)
     _dense("table_out", table_out, (rows_out, mb), I32S)
     _dense("refs", refs, (pages,), I32S)
     _dense("info", info, (4,), I32S)
@@ -935,7 +944,7 @@ def tp_kv_fork(table: torch.Tensor, lens: torch.Tensor, parents: torch.Tensor, p
         raise ValueError("parents must be a 1-D int32 tensor")
     m = parents.shape[0]
     t, layers, page_bytes, page_size, pages, table_out, refs, info, workspace = _page_args(
-        table, lens, pools, page_size, pages, held, m, table_out, refs, info, workspace)
+        table, lens, pools, page_size, pages, held, m, table_out, refs, info, workspace, stream)
     if lens_out is None:
         lens_out = torch.empty(m, dtype=torch.int32, device=table.device)
     _dense("lens_out", lens_out, (m,), I32S)
@@ -961,7 +970,7 @@ def tp_kv_compact(table: torch.Tensor, lens: torch.Tensor, pools: Optional[Seque
     pages moved."""
     rows = table.shape[0] if isinstance(table, torch.Tensor) and table.dim() == 2 else 0
     t, layers, page_bytes, page_size, pages, table_out, refs, info, workspace = _page_args(
-        table, lens, pools, page_size, pages, held, rows, table_out, refs, info, workspace)
+        table, lens, pools, page_size, pages, held, rows, table_out, refs, info, workspace, stream)
     _on_gpu(table, lens, held, pools, table_out, refs, info, workspace)
     _launch("tp_kv_compact", t, rows, table.shape[1], page_size, pages, _ptr(table), _ptr(lens), _ptr(held), _ptrs(pools),
             layers, page_bytes, _ptr(table_out), _ptr(refs), _ptr(info), _ptr(workspace),
@@ -1025,7 +1034,7 @@ def tp_beam_select(logits: Sequence[Optional[torch.Tensor]], scores: torch.Tenso
     _dense("tokens_out", tokens_out, (items, k), I32S)
     if workspace is None:
         need = tp_beam_workspace_size(items, beams, k, max(vocab, 1))
-        workspace = _scratch(max(need, 256), torch.uint8, dev)
+        workspace = _scratch(max(need, 256), torch.uint8, dev, stream)
     _dense("workspace", workspace)
     _on_gpu(logits, scores, finished, scores_out, rows_out, tokens_out, workspace)
     _launch("tp_beam_select", t, items, beams, k, cols, _ptrs(logits), ldl, _dt(ref.dtype), _ptr(scores), _ptr(finished),

@@ -117,23 +117,73 @@ def _tensors(x):
             yield from _tensors(y)
 
 
-@pytest.mark.parametrize("what", ["mlp", "linear_row", "attention", "fork", "compact", "beam"])
-def test_prepare_keeps_what_the_entry_point_allocated(host_tensors, what):
-    """Every address of the recorded launches lies in a tensor that the prepared call keeps: the workspace and the
-    partials that the caller did not give, too."""
+WITH_SCRATCH = ["mlp", "linear_row", "attention", "fork", "compact", "beam"]
+
+
+def _with_scratch(what):
+    """(entry point, arguments) of a call that allocates memory it does not return."""
     i32 = lambda *s: torch.zeros(s, dtype=torch.int32)  # noqa: E731
     z = lambda *s: torch.zeros(s, dtype=torch.bfloat16)  # noqa: E731
     pool = [_lib.tp_kv4_pool(5, 32, 2, 128, device="cpu")]
     deep = [_lib.tp_kv4_pool(5, 32, 2, 128, layers=2, device="cpu")]
-    entry, args, kw = {
-        "mlp": lambda: (_lib.tp_mlp_forward, _mlp(), {}),
-        "linear_row": lambda: (_lib.tp_linear_row, ([z(8, 128)] * 2, [z(64, 128)] * 2), {}),
-        "attention": lambda: (_lib.tp_kv4_attention, ([z(3, 512)], pool, i32(3, 4), i32(3)), {}),
-        "fork": lambda: (_lib.tp_kv_fork, (i32(3, 4), i32(3), i32(6), deep), {}),
-        "compact": lambda: (_lib.tp_kv_compact, (i32(3, 4), i32(3), deep), {}),
-        "beam": lambda: (_lib.tp_beam_select, ([z(6, 10)], torch.zeros((2, 3)), 3), {}),
+    return {
+        "mlp": lambda: (_lib.tp_mlp_forward, _mlp()),
+        "linear_row": lambda: (_lib.tp_linear_row, ([z(8, 128)] * 2, [z(64, 128)] * 2)),
+        "attention": lambda: (_lib.tp_kv4_attention, ([z(3, 512)], pool, i32(3, 4), i32(3))),
+        "fork": lambda: (_lib.tp_kv_fork, (i32(3, 4), i32(3), i32(6), deep)),
+        "compact": lambda: (_lib.tp_kv_compact, (i32(3, 4), i32(3), deep)),
+        "beam": lambda: (_lib.tp_beam_select, ([z(6, 10)], torch.zeros((2, 3)), 3)),
     }[what]()
-    plan = _lib.prepare(entry, *args, stream=0, **kw)
+
+
+@pytest.mark.parametrize("what", WITH_SCRATCH)
+def test_prepare_keeps_what_the_entry_point_allocated(host_tensors, what):
+    """Every address of the recorded launches lies in a tensor that the prepared call keeps: the workspace and the
+    partials that the caller did not give, too."""
+    entry, args = _with_scratch(what)
+    plan = _lib.prepare(entry, *args, stream=0)
     held = [(x.data_ptr(), x.data_ptr() + x.numel() * x.element_size()) for x in _tensors((plan._keep, plan.result))]
     for p in _pointers(plan):
         assert any(a <= p < b for a, b in held), what
+
+
+@pytest.mark.parametrize("what", WITH_SCRATCH)
+def test_scratch_belongs_to_the_stream_of_the_call(host_tensors, monkeypatch, what):
+    """What an entry point allocates for itself is taken for the stream it runs on, not for the current one: it is
+    free again when the entry point returns, and the current stream's next work could get it while the call runs."""
+    seen = []
+    real = _lib._scratch
+    monkeypatch.setattr(_lib, "_scratch", lambda shape, dtype, device, stream: (
+        seen.append(stream), real(shape, dtype, device, stream))[1])
+    entry, args = _with_scratch(what)
+    _lib.prepare(entry, *args, stream=4096)
+    assert seen and set(seen) == {4096}
+
+
+def test_scratch_is_allocated_under_its_stream(monkeypatch):
+    active, made = [], []
+
+    class Stream:                            # stands in for a torch stream and for one made of a raw handle
+        def __init__(self, handle, device=None):
+            self.handle = handle
+
+    class Under:
+        def __init__(self, s):
+            self.s = s
+
+        def __enter__(self):
+            active.append(self.s.handle)
+
+        def __exit__(self, *e):
+            active.pop()
+
+    monkeypatch.setattr(torch.cuda, "Stream", Stream)
+    monkeypatch.setattr(torch.cuda, "ExternalStream", Stream)
+    monkeypatch.setattr(torch.cuda, "stream", Under)
+    monkeypatch.setattr(torch, "empty", lambda *a, **kw: made.append(list(active)))
+    dev = torch.device("cuda", 0)
+    for stream in (77, Stream(77)):
+        _lib._scratch((4,), torch.uint8, dev, stream)
+        assert made.pop() == [77] and not active
+    _lib._scratch((4,), torch.uint8, dev, None)
+    assert made.pop() == []
