@@ -346,6 +346,7 @@ __global__ void __launch_bounds__(kThreads + 32, kAtOnce) beam_scan_kernel(const
                     const int word = j * kThreads + tid;
                     if (word < p.y || word >= p.z) ring[slot * WORDS + word] = w[j] = edge_word(q, word);
                 }
+                fence_proxy_async_cta();         // before the slot's next bulk copy may write there
             }
             values(w, x);
             float best = x[0];
