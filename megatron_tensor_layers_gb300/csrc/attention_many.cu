@@ -353,7 +353,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) kv4_att
             if (!ok) break;
             tc_fence_after();
             const StepInfo& info = s_info[j % kInfo];
-            // the quarters' constants: x = c S, P = 2^(x + d - m), d = F - Fref of the values
+            // the quarters' constants: x = c S, P = 2^(x + d - m), d = F - Fref of the values, and their sum is that of
+            // P 2^-d.  Below -40 every P (2^(x - m) is at most 2^12) is 0 in fp16.  So d stops at -60, where 2^-d is finite
+            // and the sum loses nothing above 2^-66 of the maximum's term, whatever the values' sizes.
             const float4 km = info.kmul;
             const int4 ve = info.vexp;
             const uint4 nn = info.nan, gg = info.gone;
@@ -383,7 +385,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) kv4_att
                 float sum = 0.0f;
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    const float dv = static_cast<float>((e == 0 ? ve.x : e == 1 ? ve.y : e == 2 ? ve.z : ve.w) - vref);
+                    const float dv = static_cast<float>(max((e == 0 ? ve.x : e == 1 ? ve.y : e == 2 ? ve.z : ve.w) - vref, -60));
                     const uint64_t cc2 = pack2(c[e], c[e]), off2 = pack2(dv - base, dv - base);
                     uint64_t sum2 = 0;
 #pragma unroll
