@@ -361,12 +361,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) kv4_att
             const uint4 nn = info.nan, gg = info.gone;
             const float c[4] = {fmaxf(cmul * km.x, 1e-37f), fmaxf(cmul * km.y, 1e-37f), fmaxf(cmul * km.z, 1e-37f),
                                 fmaxf(cmul * km.w, 1e-37f)};
-            const int vtop = max(max(ve.x, ve.y), max(ve.z, ve.w));
             const uint32_t gone = gg.x | gg.y << 2 | gg.z << 4 | gg.w << 6;
             const bool any_nan = (nn.x | nn.y | nn.z | nn.w) != 0;
             const bool whole = gone == 0 && tok0 + kTile - 1 <= tile_lo &&
                                (a.window == 0 || tok0 > tile_hi - a.window || tok0 + kTile <= a.sinks);
             const int lim = max(pos - tok0, -1), low = a.window == 0 ? -(1 << 30) : lim - a.window, sk = a.sinks - tok0;
+            // F of the values that this column sees (0: of none), so that those it does not see cost it no bits
+            int vtop = max(max(ve.x, ve.y), max(ve.z, ve.w));
+            if (!whole) {
+                auto seen = [&](int e) { return 32 * e <= lim && (min(32 * e + 31, lim) > low || 32 * e < sk); };
+                vtop = max(max(seen(0) ? ve.x : 0, seen(1) ? ve.y : 0), max(seen(2) ? ve.z : 0, seen(3) ? ve.w : 0));
+            }
             uint32_t s[4][32];
             auto load = [&]() {                          // S, hidden tokens -inf
 #pragma unroll
@@ -403,7 +408,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) kv4_att
                 return sum;
             };
             if (j == 0) vref = vtop;
-            const bool vgrow = vtop > vref + 3;
+            const bool vgrow = vtop > vref + 3;              // from 0, with O still 0, to the first that is seen
             bool again = have && (vgrow || m == kNegInf);
             float sum = 0.0f;
             if (!__any_sync(0xffffffffu, again)) {       // the old maximum may do

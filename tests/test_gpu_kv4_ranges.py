@@ -49,3 +49,45 @@ def test_chunks_over_tokens_of_zero_value(factor):
     got = tp.tp_kv4_attention(q, c.pools, c.dtable, c.dlens, cu_rows=cu_of([90]), scale=scale)
     assert tp.tp_device_status() == 0
     check(c, q, got, [90], 64, scale=scale)
+
+
+def check_some(c, q, got, m, heads, rows, window):
+    """The bound of `check` for rows `rows` of one sequence's last m, with the largest value that each row sees in the
+    place of the sequence's largest."""
+    group, n = heads // c.kv, c.lens[0]
+    for h in range(heads):
+        kk, ks, kb = c.tokens(c.kq, 0, 0, h // group)
+        vv, vs, vb = c.tokens(c.vq, 0, 0, h // group)
+        x, y = (t[0].double().cpu().numpy().reshape(m, heads, c.hd)[rows, h] for t in (q, got))
+        pos, j = (n - m + np.asarray(rows))[:, None], np.arange(n)[None, :]
+        see = (j <= pos) & ((j > pos - window) if window else True)
+        score = np.where(see, c.hd ** -0.5 * (x @ kk.T), -np.inf)
+        p = np.exp(score - score.max(1, keepdims=True))
+        p /= p.sum(1, keepdims=True)
+        want = p @ vv
+        vmost = np.where(see, 15 * vs + np.abs(vb), 0).max(1, keepdims=True)
+        kmost, absq = (15 * ks + np.abs(kb)).max(), np.abs(x).sum(1, keepdims=True)
+        D = c.hd ** -0.5 * (2.0 ** -11 * (np.abs(x) @ np.abs(kk).T).max(1, keepdims=True) +
+                            (2.0 ** -24 + (c.hd + 16) * 2.0 ** -23) * kmost * absq)
+        spread = np.stack([a @ np.abs(vv - w) for a, w in zip(p, want)])
+        tol = (2 * 2.0 ** -11 + (n + 16) * 2.0 ** -23) * vmost + np.expm1(2 * D) * spread + 2.0 ** -8 * np.abs(want)
+        err = np.abs(y - want)
+        assert (err <= tol).all(), (h, float((err / tol).max()))
+
+
+@pytest.mark.parametrize("factor", [1e4, 1e9, 1e20])
+@pytest.mark.parametrize("window", [0, 20])
+def test_a_large_value_that_is_not_seen_costs_nothing(window, factor):
+    """One token's values are `factor` times as large as the others'.  Rows that see none of its group of 32 tokens
+    (before it, or with the window past the group) are as good as without it, beside rows that see it."""
+    c = Cache(1, 8, 128, 64, [512], 64)
+    page, off = c.table[0, 448 // 64], 448 % 64
+    for i in (1, 2):
+        c.vq[i][0, page, :, off // 16, off % 16] = K.bf16(c.vq[i][0, page, :, off // 16, off % 16] * np.float32(factor))
+    c.fill()
+    rng = np.random.default_rng(65)
+    q = [torch.from_numpy(rng.standard_normal((100, 64 * 128)).astype(np.float32)).to(torch.bfloat16).to(DEV)]
+    got = tp.tp_kv4_attention(q, c.pools, c.dtable, c.dlens, cu_rows=cu_of([100]), window=window)
+    assert tp.tp_device_status() == 0
+    rows = [i for i in range(100) if 412 + i < 448 or (window and 412 + i - window >= 479)]
+    check_some(c, q, got, 100, 64, rows, window)
