@@ -79,7 +79,7 @@ struct Cfg {
 
 // What the softmax has to know of a step, by unpacking warp (32 tokens each).
 struct __align__(16) StepInfo {
-    float4 kmul;                     // 2^(F - 127) of the keys
+    float4 kmul;                     // 2^(F - 135) of the keys: F can pass what fp32 holds
     int4 vexp;                       // F of the values
     uint4 nan;                       // tokens whose value row stands for NaN
     uint4 gone;                      // blocks that are not there, two bits each
@@ -87,6 +87,11 @@ struct __align__(16) StepInfo {
 static_assert(kUnpackWarps == 4, "StepInfo has a word for each");
 
 __device__ __forceinline__ float pow2_field(int field) { return __uint_as_float(static_cast<uint32_t>(field) << 23); }
+
+// x 2^e, also where 2^e is no fp32.
+__device__ __forceinline__ float times_pow2(float x, int e) {
+    return x * pow2_field(127 + (e >> 1)) * pow2_field(127 + e - (e >> 1));
+}
 
 // fp16 A and B, f32 accumulator, K-major.
 __host__ __device__ constexpr uint32_t idesc_f16(int m, int n) {
@@ -319,7 +324,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) kv4_att
             float up = pow2_field(k + 127);
             if (a.scale_log2 < 0.0f) up = -up;
             if (a.scale_log2 == 0.0f) up = 0.0f;
-            cmul = a.scale_log2 == 0.0f ? 1.0f : fabsf(a.scale_log2) * pow2_field(min(127 - k, 254));
+            cmul = a.scale_log2 == 0.0f ? 1.0f : fabsf(a.scale_log2) * pow2_field(135 - k);     // k from -118 to 126
             const uint32_t row = sm + C::Q + t * C::QB + (tid & 127) * 128;
 #pragma unroll
             for (int i = 0; i < HD / 8; ++i) {           // a word of eight codes: its order of elements
@@ -476,7 +481,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) kv4_att
         if (ok && steps > 0 && t < tiles) {
             ok = mbar_wait_warp(smem_u32(&bars.o_full), 0, &s_abort, a.seqs.status);
             tc_fence_after();
-            scale = l == 0.0f ? 0.0f : pow2_field(min(max(vref, 1), 254)) / l;
+            scale = l == 0.0f ? 0.0f : pow2_field(max(vref - 8, 1)) / l;     // times 2^8, as 2^vref can pass fp32
         }
         if (ok && t < tiles) {
             uint16_t* dst = a.out[rank] + (it.first_row + r) * a.ldo + (kvh * a.group + h) * HD;
@@ -496,7 +501,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) kv4_att
                         uint32_t w[4];
 #pragma unroll
                         for (int x = 0; x < 4; ++x)
-                            w[x] = pack_bf16x2(__uint_as_float(o[e + 2 * x]) * scale, __uint_as_float(o[e + 2 * x + 1]) * scale);
+                            w[x] = pack_bf16x2(__uint_as_float(o[e + 2 * x]) * 256.0f * scale,
+                                               __uint_as_float(o[e + 2 * x + 1]) * 256.0f * scale);
                         *reinterpret_cast<uint4*>(dst + i + e) = make_uint4(w[0], w[1], w[2], w[3]);
                     }
                 }
@@ -572,27 +578,27 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) kv4_att
             const uint32_t there = __ballot_sync(0xffffffffu, off >= 0) & 3u;
             const bool vnan = ((pair.v >> 16) & 0x7f80u) == 0x7f80u || (pair.v & 0x7f80u) == 0x7f80u;
             if (vnan) pair.v = 0;
-            // F of 32 tokens: s 2^(127 - F) below 2^-8, |b| 2^(127 - F) below 2^15
+            // F of 32 tokens, 9 to 263: s 2^(127 - F) below 2^-8, |b| 2^(127 - F) below 2^15
             auto field = [](uint32_t p) {
                 const int es = static_cast<int>((p >> 7) & 0xffu), eb = static_cast<int>((p >> 23) & 0xffu);
-                return max(es + 9, (eb == 255 ? 0 : eb) - 14);
+                return max((es == 255 ? 0 : es) + 9, (eb == 255 ? 0 : eb) - 14);
             };
-            const int kF = min(max(__reduce_max_sync(0xffffffffu, field(pair.k)), 24), 253);
-            const int vF = min(max(__reduce_max_sync(0xffffffffu, field(pair.v)), 24), 253);
-            const int oF = min(max(__reduce_max_sync(0xffffffffu, field(pair.own)), 24), 253);
+            const int kF = __reduce_max_sync(0xffffffffu, field(pair.k));
+            const int vF = __reduce_max_sync(0xffffffffu, field(pair.v));
+            const int oF = __reduce_max_sync(0xffffffffu, field(pair.own));
             const uint32_t nan_set = __ballot_sync(0xffffffffu, vnan);
             __syncwarp();                                // the lanes are done with the words of step j - 1
             {
                 // the step times 2^24: codes are u 2^-24
-                s_key[w * 32 + lane] = pack_f16x2(__uint_as_float(pair.own << 16) * pow2_field(278 - oF),
-                                                  __uint_as_float(pair.own & 0xffff0000u) * pow2_field(254 - oF));
-                const uint32_t sb = pack_f16x2(__uint_as_float(pair.v << 16) * pow2_field(278 - vF),
-                                               __uint_as_float(pair.v & 0xffff0000u) * pow2_field(254 - vF));
+                s_key[w * 32 + lane] = pack_f16x2(times_pow2(__uint_as_float(pair.own << 16), 151 - oF),
+                                                  times_pow2(__uint_as_float(pair.own & 0xffff0000u), 127 - oF));
+                const uint32_t sb = pack_f16x2(times_pow2(__uint_as_float(pair.v << 16), 151 - vF),
+                                               times_pow2(__uint_as_float(pair.v & 0xffff0000u), 127 - vF));
                 s_vstep[w * 32 + lane] = static_cast<uint16_t>(sb);
                 s_vbase[w * 32 + lane] = static_cast<uint16_t>(sb >> 16);
                 if (lane == 0) {
                     StepInfo& info = s_info[j % kInfo];
-                    reinterpret_cast<float*>(&info.kmul)[w] = pow2_field(kF);
+                    reinterpret_cast<float*>(&info.kmul)[w] = pow2_field(kF - 8);
                     reinterpret_cast<int*>(&info.vexp)[w] = vF;
                     reinterpret_cast<uint32_t*>(&info.nan)[w] = nan_set;
                     // past the last visible token nothing is there: hidden by position, no matter

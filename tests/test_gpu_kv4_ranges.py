@@ -10,7 +10,7 @@ import torch
 
 from oracle import kv_oracle as K
 from test_gpu_kv4 import Cache, DEV, cu_of
-from test_gpu_kv4_chunks import check, run
+from test_gpu_kv4_chunks import check, rows_of, run
 
 tp = pytest.importorskip("megatron_tensor_layers_gb300")
 pytestmark = pytest.mark.gpu
@@ -91,3 +91,24 @@ def test_a_large_value_that_is_not_seen_costs_nothing(window, factor):
     assert tp.tp_device_status() == 0
     rows = [i for i in range(100) if 412 + i < 448 or (window and 412 + i - window >= 479)]
     check_some(c, q, got, 100, 64, rows, window)
+
+
+@pytest.mark.parametrize("hd", [128, 64])
+@pytest.mark.parametrize("factor", [1e37, 1e-36])
+def test_chunks_of_the_largest_and_smallest_values(hd, factor):
+    c = scaled(Cache(1, 8, hd, 64, [300, 129, 70], 66), factor)
+    run(c, [60, 40, 70], 64, 67)
+
+
+@pytest.mark.parametrize("hd", [128, 64])
+@pytest.mark.parametrize("factor", [1e37, 1e20, 1e-30])
+def test_chunks_of_the_largest_and_smallest_keys(hd, factor):
+    """q is as much smaller as the keys are larger."""
+    c = Cache(1, 8, hd, 64, [300, 129, 70], 68)
+    for i in (1, 2):
+        c.kq[i] = K.bf16(c.kq[i] * np.float32(factor))
+    c.fill()
+    q = [(x.float() / factor).to(torch.bfloat16) for x in rows_of(c, [60, 40, 70], 64, 69)]
+    got = tp.tp_kv4_attention(q, c.pools, c.dtable, c.dlens, cu_rows=cu_of([60, 40, 70]))
+    assert tp.tp_device_status() == 0
+    check(c, q, got, [60, 40, 70], 64)
