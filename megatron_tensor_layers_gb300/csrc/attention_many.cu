@@ -525,10 +525,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) kv4_att
         auto first_block = [&](int j) { return (j < span.front ? j : span.start + j - span.front) * (kTile / kKvBlock); };
         // lanes 0, 1: the values' two blocks; lanes 2, 3: those of the keys' 32 tokens
         const int my_block = 2 * (lane & 2 ? kq : w) + (lane & 1);
-        // the page of the lane's block of step j; -2 past the last visible token, where nothing is read
+        // the page of the lane's block of step j; -2 where no row of the tile sees a token of it and nothing is read:
+        // its page may be gone (behind the window, between the sinks and the window, past the last row)
         auto fetch_page = [&](int j) -> int {
-            const int64_t b = first_block(j) + my_block;
-            return j < steps && b * kKvBlock <= last_pos ? kv_page_at(row, a.seqs.max_blocks, a.pools.page_shift, b) : -2;
+            const int64_t b = first_block(j) + my_block, token = b * kKvBlock;
+            const bool seen = token <= last_pos &&
+                              (a.window == 0 || token + kKvBlock - 1 > first_pos - a.window || token < a.sinks);
+            return j < steps && seen ? kv_page_at(row, a.seqs.max_blocks, a.pools.page_shift, b) : -2;
         };
         auto offset_of = [&](int j, int page) -> int64_t {
             const int64_t off = kv_page_offset(page, a.pools.pages, a.pools.page_shift, a.pools.kv_heads, kvh,
