@@ -63,6 +63,7 @@ constexpr int kWarps = 8;
 constexpr int kBatch = 32;           // blocks whose addresses a warp holds, one in each lane
 constexpr int kStages = 2;
 constexpr int kPShift = 8;           // p s' is held times 2^(kPShift - E)
+constexpr int kUnder = 14;           // what p v adds up to is held times 2^-kUnder, so that it passes fp32 only with the values
 constexpr float kMost = 128.0f;      // sum of a lane's 2^(x - m) up to which the old maximum will do
 constexpr int kMany = 72;            // columns for each pair of blocks from which the many-rows kernel pays (many_pays)
 constexpr float kNegInf = -INFINITY;
@@ -241,7 +242,7 @@ __device__ __forceinline__ void store_vectors(const AttnArgs& a, int head, int f
     for (int e = 0; e < 2; ++e) {
         uint16_t* p = out_of<HD>(a, head, first_row, rows, first_col + v / MT * 8 + 2 * (lane & 3) + e, lane);
         if (p == nullptr) continue;
-        const float sum = e ? total.y : total.x, inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+        const float sum = e ? total.y : total.x, inv = sum == 0.0f ? 0.0f : static_cast<float>(1 << kUnder) / sum;
         uint32_t w[NV];
 #pragma unroll
         for (int i = 0; i < NV; ++i) w[i] = pack_bf16x2((e ? o[i].y : o[i].x) * inv, (e ? o[i].w : o[i].z) * inv);
@@ -578,7 +579,8 @@ __global__ void __launch_bounds__(Cfg<HD, NT>::WARPS * 32, 1) kv4_attention_kern
 
         float acc[NT][MT][4];
         float mx[NT][2], sum[NT][2], corr[NT][2];
-        // exponent field of the largest value step, at least 16 so that 2^(kPShift - E) stays finite
+        // exponent field of the largest value step, at least 16 so that 2^(kPShift - E) stays finite; a range that
+        // fp32 holds has a step of at most 2^124.1, field 251
         int vexp = 16;
         bool fresh = true;               // some column has seen nothing
 #pragma unroll
@@ -673,6 +675,7 @@ __global__ void __launch_bounds__(Cfg<HD, NT>::WARPS * 32, 1) kv4_attention_kern
                 uint32_t pf[BLOCKS][NT][2];
                 float psum[NT][2], pcorr[NT][2];
                 auto weigh = [&]() {
+                    constexpr float under = 1.0f / (1 << kUnder);
                     const float vscale = __uint_as_float(static_cast<uint32_t>(253 - vexp) << 23) * (1 << kPShift);
                     float m[NT][2];
 #pragma unroll
@@ -684,8 +687,8 @@ __global__ void __launch_bounds__(Cfg<HD, NT>::WARPS * 32, 1) kv4_attention_kern
                         }
 #pragma unroll
                     for (int i = 0; i < BLOCKS; ++i) {
-                        const float s0 = __uint_as_float(vp[i][0] << 16) * vscale, b0 = __uint_as_float(vp[i][0] & 0xffff0000u);
-                        const float s1 = __uint_as_float(vp[i][1] << 16) * vscale, b1 = __uint_as_float(vp[i][1] & 0xffff0000u);
+                        const float s0 = __uint_as_float(vp[i][0] << 16) * vscale, b0 = __uint_as_float(vp[i][0] & 0xffff0000u) * under;
+                        const float s1 = __uint_as_float(vp[i][1] << 16) * vscale, b1 = __uint_as_float(vp[i][1] & 0xffff0000u) * under;
 #pragma unroll
                         for (int nt = 0; nt < NT; ++nt) {
                             float ps[4];
@@ -738,7 +741,7 @@ __global__ void __launch_bounds__(Cfg<HD, NT>::WARPS * 32, 1) kv4_attention_kern
                             for (int e = 0; e < 2; ++e)
                                 cmax[nt][e] = fmaxf(cmax[nt][e], __shfl_xor_sync(0xffffffffu, cmax[nt][e], m));
                     }
-                    const int e_new = max(vexp, min(static_cast<int>(vtop >> 7), 250));
+                    const int e_new = max(vexp, min(static_cast<int>(vtop >> 7), 251));
                     const float vdown = __uint_as_float(static_cast<uint32_t>(max(127 - (e_new - vexp), 0)) << 23);
                     vexp = e_new;
                     bool unseen = false;
@@ -815,7 +818,8 @@ __global__ void __launch_bounds__(Cfg<HD, NT>::WARPS * 32, 1) kv4_attention_kern
         }
 
         // ---- the warp's result: O, maximum and sum of each column, every lane with its own dimensions
-        const float down = __uint_as_float(static_cast<uint32_t>(min(24 - kPShift + vexp + 1, 254)) << 23);
+        static_assert(24 - kPShift + 251 + 1 - kUnder <= 254 && 24 - kPShift + 16 + 1 - kUnder >= 1, "a normal power of two");
+        const float down = __uint_as_float(static_cast<uint32_t>(24 - kPShift + vexp + 1 - kUnder) << 23);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll

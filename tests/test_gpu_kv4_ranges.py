@@ -9,7 +9,7 @@ import pytest
 import torch
 
 from oracle import kv_oracle as K
-from test_gpu_kv4 import Cache, DEV, cu_of
+from test_gpu_kv4 import Cache, DEV, check_attention, cu_of
 from test_gpu_kv4_chunks import check, rows_of, run
 
 tp = pytest.importorskip("megatron_tensor_layers_gb300")
@@ -112,3 +112,12 @@ def test_chunks_of_the_largest_and_smallest_keys(hd, factor):
     got = tp.tp_kv4_attention(q, c.pools, c.dtable, c.dlens, cu_rows=cu_of([60, 40, 70]))
     assert tp.tp_device_status() == 0
     check(c, q, got, [60, 40, 70], 64)
+
+
+@pytest.mark.parametrize("hd,group", [(128, 8), (64, 3), (128, 16)])
+@pytest.mark.parametrize("factor", [1e34, 1e35, 1e36, 1e37, 1e-33])
+def test_rows_of_the_largest_and_smallest_values(hd, group, factor):
+    """Single rows and a few: sequences that a warp holds, and one that is cut into parts."""
+    c = scaled(Cache(1, 2, hd, 64, [300, 129, 70, 1, 2500], 73), factor)
+    check_attention(c, [1] * 5, 2 * group, 74, cu=False)
+    check_attention(c, [3, 2, 4, 1, 2], 2 * group, 75)
