@@ -563,7 +563,8 @@ __global__ void __launch_bounds__(Cfg<HD, NT>::WARPS * 32, 1) kv4_attention_kern
                 qf[nt][2 * j + 1][0] = pack_f16x2(x[2] * up, x[6] * up);
                 qf[nt][2 * j + 1][1] = pack_f16x2(x[3] * up16, x[7] * up16);
             }
-            const float mul = a.scale_log2 * __uint_as_float(static_cast<uint32_t>(min(24 - k, 127) + 127) << 23);
+            // 2^(24 - k) can pass fp32 where the factor does not; k from -118 to 126
+            const float mul = a.scale_log2 * 0x1p24f * __uint_as_float(static_cast<uint32_t>(127 - k) << 23);
             const float add = a.scale_log2 * sum;
 #pragma unroll
             for (int e = 0; e < 2; ++e) {

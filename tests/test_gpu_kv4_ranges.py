@@ -121,3 +121,17 @@ def test_rows_of_the_largest_and_smallest_values(hd, group, factor):
     c = scaled(Cache(1, 2, hd, 64, [300, 129, 70, 1, 2500], 73), factor)
     check_attention(c, [1] * 5, 2 * group, 74, cu=False)
     check_attention(c, [3, 2, 4, 1, 2], 2 * group, 75)
+
+
+@pytest.mark.parametrize("hd", [128, 64])
+@pytest.mark.parametrize("factor", [1e37, 1e20, 1e-30, 3e-35])
+def test_rows_of_the_largest_and_smallest_keys(hd, factor):
+    """q is as much smaller as the keys are larger."""
+    lens = [300, 129, 70, 1, 2500]
+    c = Cache(1, 2, hd, 64, lens, 76)
+    for i in (1, 2):
+        c.kq[i] = K.bf16(c.kq[i] * np.float32(factor))
+    c.fill()
+    for rows, seed in (([1] * 5, 77), ([3, 2, 4, 1, 2], 78)):
+        q = [(x.float() / factor).to(torch.bfloat16) for x in rows_of(c, rows, 16, seed)]
+        check_attention(c, rows, 16, seed, q=q)
