@@ -664,6 +664,16 @@ int64_t tp_debug_kv4_block(const int32_t* row, int64_t max_blocks, int64_t pages
                            int head_dim, int head, int64_t position);
 
 /*
+ * Test hook for the flags by which attention's thread blocks hand over parts of
+ * a row's context (host logic only, the code the kernels run): what a flag
+ * that holds `word` holds after its part was left by call number `tag` (top
+ * bit set), order 0; after that and a join that gave up, in this order (1), in
+ * the other (2), and with the steps of one after the first step of the other
+ * (3: the join's inside, 4: the part's).
+ */
+uint64_t tp_debug_part_flag(uint64_t word, uint64_t tag, int order);
+
+/*
  * Test hook for the host-side kernel choice (no CUDA call): the GEMM kernel
  * the library would launch, with the automatic settings, for M rows, an
  * output of N columns per group (per shard), K per segment, `groups`

@@ -162,6 +162,35 @@ tp_status tp_kv4_load(int t, int64_t n, int64_t nseq, int kv_heads, int head_dim
     return tpk::launch_kv4_load(d, cs(stream));
 }
 
+uint64_t tp_debug_part_flag(uint64_t word, uint64_t tag, int order) {
+    tag |= uint64_t{1} << 63;
+    auto plain = [&](uint64_t v) {
+        const uint64_t old = word;
+        word = v;
+        return old;
+    };
+    // the other worker's steps all come after the first of these
+    bool first = true;
+    auto then_give_up = [&](uint64_t v) {
+        const uint64_t old = plain(v);
+        if (first) tpk::give_up_part_flag(tag, plain);
+        first = false;
+        return old;
+    };
+    auto then_raise = [&](uint64_t v) {
+        const uint64_t old = plain(v);
+        if (first) tpk::raise_part_flag(tag, plain);
+        first = false;
+        return old;
+    };
+    if (order == 0 || order == 1) tpk::raise_part_flag(tag, plain);
+    if (order == 1 || order == 2) tpk::give_up_part_flag(tag, plain);
+    if (order == 2) tpk::raise_part_flag(tag, plain);
+    if (order == 3) tpk::raise_part_flag(tag, then_give_up);
+    if (order == 4) tpk::give_up_part_flag(tag, then_raise);
+    return word;
+}
+
 static tp_status check_heads(int heads, int kv_heads) {
     TP_CHECK(heads >= 1 && kv_heads >= 1, TP_ERR_INVALID_ARG);
     TP_CHECK(heads % kv_heads == 0, TP_ERR_NOT_DIVISIBLE);

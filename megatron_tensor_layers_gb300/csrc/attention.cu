@@ -37,7 +37,8 @@
 // this takes 14.7 (one row, 4097 tokens, 8 heads).
 // A flag is raised by writing the call's number, which nothing else in the
 // workspace holds, and taken down by whoever waited for it, so that the workspace
-// needs no preparation and a graph that repeats a call finds it as the call did.
+// needs no preparation and a graph that repeats a call finds it as the call did.  Where the wait ran out, whichever of
+// the two comes second takes it down.
 // The cut depends on lengths the host does not know, so every thread block finds
 // its own.
 //
@@ -101,8 +102,10 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
 }
 
 // A flag of 64 bits, raised with a release and awaited, with the limit of every wait here, with an acquire.
-__device__ __forceinline__ void st_release_gpu64(uint64_t* p, uint64_t v) {
-    asm volatile("st.release.gpu.global.b64 [%0], %1;" ::"l"(p), "l"(v) : "memory");
+__device__ __forceinline__ uint64_t exchange_gpu64(uint64_t* p, uint64_t v) {
+    uint64_t old;
+    asm volatile("atom.release.gpu.global.exch.b64 %0, [%1], %2;" : "=l"(old) : "l"(p), "l"(v) : "memory");
+    return old;
 }
 __device__ __forceinline__ bool flag64_wait(const uint64_t* flag, uint64_t value, volatile int* abort, int* status) {
     const uint64_t t0 = global_ns();
@@ -892,8 +895,7 @@ __global__ void __launch_bounds__(Cfg<HD, NT>::WARPS * 32, 1) kv4_attention_kern
         }
         if (more || awaited) together();
         if (awaited && wi == 0 && lane == 0) {
-            __threadfence();
-            st_release_gpu64(flags + slot_no, a.tag);
+            raise_part_flag(a.tag, [&](uint64_t v) { return exchange_gpu64(flags + slot_no, v); });
         }
         if (!more) break;
     }
@@ -913,8 +915,13 @@ __global__ void __launch_bounds__(Cfg<HD, NT>::WARPS * 32, 1) kv4_attention_kern
             join_parts<HD, NT, 1>(wi, ws, lane, count, part, put);
         else
             join_parts<HD, NT, 4>(wi, ws, lane, count, part, put);
-        if (have)
-            for (int i = wi * 32 + lane; i + 1 < count; i += ws * 32) flags[slot_of(i)] = 0;
+        for (int i = wi * 32 + lane; i + 1 < count; i += ws * 32) {
+            uint64_t* flag = flags + slot_of(i);
+            if (have)
+                *flag = 0;
+            else
+                give_up_part_flag(a.tag, [&](uint64_t v) { return exchange_gpu64(flag, v); });
+        }
     }
     if (dead) spin_ns(1000000);      // copies that were issued land before the block's memory is given back
 }

@@ -272,6 +272,20 @@ struct KvAttentionDesc {
     int window = 0, sinks = 0;           // window 0: none
     void* ws = nullptr;
 };
+
+// The flag of a part of an item: a word that its worker raises to the call's number `tag` (whose top bit is set) and
+// that the worker that joins the parts takes down.  A join whose wait ran out gives the flag up, and of the two the
+// one that comes second takes it down: none outlives its call, whose number a graph uses again.  exchange(v) puts v
+// into the word and returns what it held, in one step.
+TPK_BOTH constexpr uint64_t given_up_flag(uint64_t tag) { return tag & ~(uint64_t{1} << 63); }
+template <typename Exchange>
+TPK_BOTH inline void raise_part_flag(uint64_t tag, Exchange exchange) {
+    if (exchange(tag) == given_up_flag(tag)) exchange(0);
+}
+template <typename Exchange>
+TPK_BOTH inline void give_up_part_flag(uint64_t tag, Exchange exchange) {
+    if (exchange(given_up_flag(tag)) == tag) exchange(0);
+}
 size_t kv4_attention_workspace(int t, int64_t n, int64_t nseq, int heads, int kv_heads, int head_dim);
 tp_status launch_kv4_attention(const KvAttentionDesc& d, cudaStream_t stream);
 
