@@ -674,6 +674,14 @@ int64_t tp_debug_kv4_block(const int32_t* row, int64_t max_blocks, int64_t pages
 uint64_t tp_debug_part_flag(uint64_t word, uint64_t tag, int order);
 
 /*
+ * Test hook (host logic only, the code the kernels run): the first of the
+ * `workers` parts of few-row attention's line of work that thread block
+ * `block` of `blocks` takes, with up to `groups` for each; -1 for sizes out of
+ * range.  A part waits for lower parts alone.
+ */
+int tp_debug_first_worker(int block, int blocks, int groups, int workers);
+
+/*
  * Test hook for the host-side kernel choice (no CUDA call): the GEMM kernel
  * the library would launch, with the automatic settings, for M rows, an
  * output of N columns per group (per shard), K per segment, `groups`

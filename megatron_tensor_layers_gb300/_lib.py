@@ -37,7 +37,7 @@ EXPORTED = [
     "tp_reduce_scatter_rmsnorm", "tp_set_gemm_split", "tp_debug_gemm_plan", "tp_mlp_host_blocks",
     "tp_kv4_page_bytes", "tp_kv4_append", "tp_kv4_load", "tp_kv4_attention_workspace_size", "tp_kv4_attention",
     "tp_kv_pages_workspace_size", "tp_kv_fork", "tp_kv_compact", "tp_beam_workspace_size", "tp_beam_select",
-    "tp_debug_kv4_block", "tp_debug_part_flag",
+    "tp_debug_kv4_block", "tp_debug_part_flag", "tp_debug_first_worker",
 ]
 STATIC_SCRATCH_BYTES = 16 * 1024 * 1024
 
@@ -87,6 +87,7 @@ def load() -> ctypes.CDLL:
         "tp_mlp_forward_static": (I32, [I32, I64, I64, I64, P, I64, P, P, I64, P, I32, I32, I32, P, I32, P]),
         "tp_mlp_host_blocks": (I32, [I64, I32, P, I32]),
         "tp_debug_kv4_block": (I64, [P, I64, I64, I32, I32, I32, I32, I64]),
+        "tp_debug_first_worker": (I32, [I32, I32, I32, I32]),
         "tp_debug_part_flag": (ctypes.c_uint64, [ctypes.c_uint64, ctypes.c_uint64, I32]),
         "tp_kv4_page_bytes": (ctypes.c_size_t, [I32, I32, I32]),
         "tp_kv4_append": (I32, [I32, I64, I64, I32, I32, P, I64, P, I64, P, I64, I32, P, I64, P, P, P]),

@@ -162,6 +162,13 @@ tp_status tp_kv4_load(int t, int64_t n, int64_t nseq, int kv_heads, int head_dim
     return tpk::launch_kv4_load(d, cs(stream));
 }
 
+int tp_debug_first_worker(int block, int blocks, int groups, int workers) {
+    if (blocks < 1 || blocks > 4096 || block < 0 || block > blocks || groups < 1 || groups > 8 || workers < 0 ||
+        workers > blocks * groups)
+        return -1;
+    return tpk::first_worker_of(block, blocks, groups, workers);
+}
+
 uint64_t tp_debug_part_flag(uint64_t word, uint64_t tag, int order) {
     tag |= uint64_t{1} << 63;
     auto plain = [&](uint64_t v) {

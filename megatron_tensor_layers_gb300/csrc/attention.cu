@@ -372,9 +372,11 @@ __global__ void __launch_bounds__(Cfg<HD, NT>::WARPS * 32, 1) kv4_attention_kern
     const int groups = WARPS / ws;
     const int workers = static_cast<int>(min(sms * groups, quotient(total + ws - 1, ws)));
     const Parts parts(total, workers);
+    const int worker0 = first_worker_of(blockIdx.x, gridDim.x, groups, workers);
+    const int worker1 = first_worker_of(blockIdx.x + 1, gridDim.x, groups, workers);
     for (int i = 0; i < groups; ++i) {
-        const int w = i * gridDim.x + blockIdx.x;
-        if (w >= workers) {
+        const int w = worker0 + i;
+        if (w >= worker1) {
             if (tid == 0) s_cursor[i].left = 0;
             continue;
         }
@@ -416,7 +418,7 @@ __global__ void __launch_bounds__(Cfg<HD, NT>::WARPS * 32, 1) kv4_attention_kern
     __syncthreads();
 
     const int grp = warp / ws, wi = warp % ws;
-    const int worker = grp * gridDim.x + blockIdx.x;
+    const int worker = worker0 + grp;
     // two parts of each worker: the item its range begins in, and the one it ends in
     uint64_t* flags = reinterpret_cast<uint64_t*>(a.ws);
     float4* slots = reinterpret_cast<float4*>(a.ws + flag_bytes(gridDim.x));

@@ -286,6 +286,15 @@ template <typename Exchange>
 TPK_BOTH inline void give_up_part_flag(uint64_t tag, Exchange exchange) {
     if (exchange(given_up_flag(tag)) == tag) exchange(0);
 }
+
+// The first of `workers` <= blocks * groups workers that thread block `block` of few-row attention holds, at most
+// `groups` of them, neighbours in order: block b has those up to block b + 1's first.  A worker waits for lower ones
+// alone, so for its own and lower blocks': while only the first blocks of a grid run, they wait for nothing that does
+// not.
+TPK_BOTH inline int first_worker_of(unsigned block, unsigned blocks, int groups, int workers) {
+    if (groups == 1) return static_cast<int>(block) < workers ? static_cast<int>(block) : workers;
+    return static_cast<int>(static_cast<unsigned>(workers) * block / blocks);
+}
 size_t kv4_attention_workspace(int t, int64_t n, int64_t nseq, int heads, int kv_heads, int head_dim);
 tp_status launch_kv4_attention(const KvAttentionDesc& d, cudaStream_t stream);
 
