@@ -436,6 +436,8 @@ tp_status tp_shard_gather(int t, int64_t rows, const int64_t* cols, tp_dtype dty
  * table.  A page number outside [0, pages), or a position outside the
  * table, met while a call runs is never read or written: its tokens count
  * as not there, and tp_device_status() then returns TP_ERR_INVALID_ARG.
+ * So it does after offsets that are not as above; rows that then belong to
+ * no sequence are not stored, are loaded as 0, and get no attention output.
  * ---------------------------------------------------------------------
  */
 

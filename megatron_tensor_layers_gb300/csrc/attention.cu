@@ -311,6 +311,10 @@ __global__ void __launch_bounds__(Cfg<HD, NT>::WARPS * 32, 1) kv4_attention_kern
     pdl_wait();
     pdl_trigger();
 
+    if (blockIdx.x == 0 && tid == 0 && a.seqs.cu_rows != nullptr &&
+        (a.seqs.cu_rows[0] != 0 || a.seqs.cu_rows[a.seqs.nseq] != a.seqs.n))
+        raise_status(a.seqs.status, TP_ERR_INVALID_ARG);     // rows that no sequence holds
+
     // ---- which sequences are this kernel's: those with fewer than `many` columns
     int many = INT32_MAX;
     if (a.many != INT32_MAX) {
