@@ -64,7 +64,7 @@ template <int HD>
 __device__ __forceinline__ RowAt row_at(const KvSeqs& q, const KvPools& p, int row) {
     int seq = row, pos;
     if (q.cu_rows == nullptr) {
-        pos = q.lens[row] - 1;
+        pos = max(q.lens[row], 0) - 1;
     } else {
         int lo = 0, hi = q.nseq;                 // the last sequence that begins at or before the row
         while (hi - lo > 1) {

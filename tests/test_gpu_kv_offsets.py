@@ -34,3 +34,14 @@ def test_bad_offsets_are_reported(cu, stored):
     assert changed <= 136 * stored and (changed > 0) == (stored > 0)
     k2, _ = tp.tp_kv4_load(c.pools, c.dtable, c.dlens, 2, cu_rows=cu)
     assert tp.tp_device_status() == 1 and int(k2[0].any(1).sum()) == stored
+
+
+def test_the_least_length():
+    """Lengths below 0 are lengths of 0, down to the least int32: the row is at a negative position and is not stored."""
+    c, _, k = cache()
+    before = c.pools[0].clone()
+    c.dlens.copy_(torch.tensor([-2 ** 31, -1], dtype=torch.int32))
+    tp.tp_kv4_append(k, k, c.pools, c.dtable, c.dlens)
+    assert tp.tp_device_status() == 0 and torch.equal(before, c.pools[0])
+    k2, v2 = tp.tp_kv4_load(c.pools, c.dtable, c.dlens, 2)
+    assert tp.tp_device_status() == 0 and not k2[0].any() and not v2[0].any()
