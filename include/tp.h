@@ -588,9 +588,13 @@ size_t tp_beam_workspace_size(int64_t items, int beams, int k, int64_t vocab);
  * Logits of -inf are no continuations, nor are those of a row whose
  * log-sum-exp is not finite or whose score is -inf or NaN.  Where fewer than
  * k remain the rest are score -inf, row -1, token -1.  k <= TP_MAX_BEAMS,
- * beams <= TP_MAX_BEAMS; vocab = sum(cols) < 2^31.  Scores are ordered as
- * fp64 sums (the log-sum-exp is accumulated in fp64 across threads), so that
- * rounding does not reorder neighbours, and stored as fp32.
+ * beams <= TP_MAX_BEAMS; vocab = sum(cols) < 2^31.  Within a beam the order is
+ * that of the logits.  Beams are compared by fp64 sums of score, logit and
+ * log-sum-exp, whose exponentials are fp32: it is good to about 2^-22, so that
+ * candidates of two beams closer than that can change places.  It depends on
+ * the row's logits, shard widths and dtype alone: equal rows with equal scores
+ * tie, and an item's result does not depend on the others.  Scores are stored
+ * as fp32.
  */
 tp_status tp_beam_select(int t, int64_t items, int beams, int k, const int64_t* cols, const void* const* logits,
                          const int64_t* ldl, tp_dtype dtype, const float* scores, const uint8_t* finished, int32_t eos,

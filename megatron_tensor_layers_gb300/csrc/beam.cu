@@ -1,7 +1,7 @@
 // Beam selection over vocab-sharded logits: one pass over the logits.  256 rows of
-// 151936 fp32 logits take 47 us (38 and 9 for the kernels below; 2.9 TB/s), bound by
+// 151936 fp32 logits take 50 us (39 and 11 for the kernels below; 2.7 TB/s), bound by
 // the instructions of the scan (60 % of the issue slots) and the barriers at a
-// piece's end; four rows of bf16 take 14 us, nearly all of it latency.
+// piece's end; four rows of bf16 take 13 us, nearly all of it latency.
 //
 // First kernel: the logits of all rows are one line of chunks of 4096, cut into
 // equal parts, one for each thread block that fits; a block's part of a row is a
@@ -9,10 +9,12 @@
 // that two are on their way while one is worked on (128 KB for an SM; loads into
 // registers, one chunk ahead in blocks of one row each, took 40 us for 136 MB,
 // and a thread of the eight that also issues the copies holds up all of them).
-// Each thread keeps a running maximum and the sum of exponentials
-// under it (fp32, an exponential from ex2; what joins sums under different
-// maxima is expf, so that errors do not pile up; the threads' sums are added in
-// fp64).  A logit and its token make one 64-bit key, larger for a larger logit
+// Each warp leaves the maximum of its 512 logits of a chunk and the sum of
+// exponentials under it (fp32, an exponential from ex2).  Chunks count from a
+// shard's first column, not from an aligned address, and what is joined over chunks
+// is joined by the second kernel, so that a row's sum is the same wherever the row
+// lies and its pieces begin: equal beams tie.  (Running sums over a piece took
+// 48 us and gave such beams different last bits.)  A logit and its token make one 64-bit key, larger for a larger logit
 // and, among equals, for a lower token, so the k best are unique.  The k-th
 // largest of 64 group maxima (a group is 4 threads) of a piece's first chunk is
 // a lower bound of the k-th largest of the piece; what is not below it goes to
@@ -26,7 +28,7 @@
 // rounds of a block-wide maximum over the piece find them instead.
 //
 // Second kernel, one thread block per item: the log-sum-exp of each beam from
-// its pieces, then the k best of all beams' candidates by the fp64 sum
+// its warps' sums (expf joins them, in fp64 from pairs on), then the k best of all beams' candidates by the fp64 sum
 // score - lse + logit, the same way.  It is a chain of latencies; fp64 is slow
 // here (16 cycles an instruction and warp), so a beam takes one logarithm
 // in it and no exponential.
@@ -43,10 +45,10 @@ constexpr int kGroups = 64;
 constexpr int kRoom = 512;           // candidates that are ranked by counting
 static_assert(kGroups >= TP_MAX_BEAMS, "the bound needs as many groups as there are results");
 
-struct Piece {
-    double sum;                      // of e^(x - top)
-    float top;                       // -inf: nothing but -inf (and perhaps NaN)
-    int pad;
+// A warp's logits of a chunk.
+struct __align__(8) Part {
+    float top;                       // the largest, -inf: nothing but -inf (and perhaps NaN)
+    float sum;                       // of e^(x - top)
 };
 
 struct BeamArgs {
@@ -64,7 +66,7 @@ struct BeamArgs {
     float* scores_out;
     int32_t* rows_out;
     int32_t* tokens_out;
-    Piece* stats;                    // [rows, most]
+    Part* stats;                     // [rows, chunks, kWarps]
     uint64_t* keys;                  // [rows, most, k], best first, 0 where there are fewer
     int* status;
 };
@@ -179,7 +181,15 @@ __device__ __forceinline__ float ex2(float x) {
     return y;
 }
 
+// The largest of the warp's values, NaN aside (-inf where there is nothing else).
+__device__ __forceinline__ float warp_max(float x) {
+    float y;
+    asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(x));
+    return y;
+}
+
 constexpr int kAtOnce = 4;           // blocks of an SM
+constexpr int kAhead = 12;           // parts of a row that a lane of the second kernel asks for at once
 constexpr int kRing = 3;
 
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
@@ -192,13 +202,12 @@ template <bool F32>
 __global__ void __launch_bounds__(kThreads + 32, kAtOnce) beam_scan_kernel(const __grid_constant__ BeamArgs a) {
     constexpr int VEC = F32 ? 4 : 8, NV = kChunk / VEC, ES = F32 ? 4 : 2;
     constexpr uint32_t NONE = F32 ? 0xff800000u : 0xff80ff80u;           // -inf
-    constexpr int WORDS = kThreads * NV;
-    extern __shared__ __align__(128) uint4 ring[];                       // [kRing][WORDS]
+    constexpr int WORDS = kThreads * NV, SLOT = WORDS + 1;               // of 16 bytes
+    extern __shared__ __align__(128) uint4 ring[];                       // [kRing][SLOT]
     __shared__ __align__(8) uint64_t full[kRing], empty[kRing];
-    __shared__ int3 s_place[kRing];              // token of the first element, first and one past the last whole word
+    __shared__ int4 s_place[kRing];              // of Place: token, lo, hi, off
     __shared__ int s_abort;
-    __shared__ float s_top[kWarps];
-    __shared__ double s_sum[kWarps];
+    __shared__ uint32_t s_none[1];               // what a place without a logit reads
     __shared__ __align__(16) uint32_t s_group[kGroups];
     __shared__ uint32_t s_bound;
     __shared__ __align__(16) uint64_t s_cand[kRoom + 2];
@@ -212,12 +221,14 @@ __global__ void __launch_bounds__(kThreads + 32, kAtOnce) beam_scan_kernel(const
     const int64_t begin = line.begin(blockIdx.x), end = line.begin(blockIdx.x + 1);
 
     auto done = [&](int row) { return a.finished != nullptr && a.finished[row] != 0; };   // its logits do not matter
-    // Chunk c of a row: where its first word is (whose first elements a row that begins inside a word does not
-    // have), in columns of its shard, and which words lie in the row whole.
+    // Chunk c of a row, elements first .. of its shard.  A thread's words are VEC of them each, counted from the shard's
+    // first, so that a row's sums do not depend on where it lies; in memory they begin `off` elements into a 16-byte
+    // word, and the ring holds the chunk's memory words (one more where off is not 0), of which lo .. hi - 1 lie in
+    // the row whole.
     struct Place {
         const uint8_t* base;                     // the row
         int64_t cols, first;
-        int token, lo, hi;
+        int token, lo, hi, off;
     };
     auto place = [&](int row, int c) {
         int r = 0;
@@ -225,12 +236,30 @@ __global__ void __launch_bounds__(kThreads + 32, kAtOnce) beam_scan_kernel(const
         Place p;
         p.cols = a.cols[r];
         p.base = static_cast<const uint8_t*>(a.logits[r]) + row * a.ldl[r] * ES;
-        const int off = static_cast<int>((reinterpret_cast<uintptr_t>(p.base) & 15u) / ES);
-        p.first = static_cast<int64_t>(c - a.first_chunk[r]) * (kThreads * kChunk) - off;
+        p.off = static_cast<int>((reinterpret_cast<uintptr_t>(p.base) & 15u) / ES);
+        p.first = static_cast<int64_t>(c - a.first_chunk[r]) * (kThreads * kChunk);
         p.token = static_cast<int>(a.start[r] + p.first);
-        p.lo = p.first < 0 ? 1 : 0;
-        p.hi = static_cast<int>(max(static_cast<int64_t>(p.lo), min(static_cast<int64_t>(WORDS), (p.cols - p.first) / VEC)));
+        const int most = p.off ? SLOT : WORDS;
+        p.lo = p.first == 0 && p.off ? 1 : 0;
+        p.hi = static_cast<int>(max(static_cast<int64_t>(p.lo), min(static_cast<int64_t>(most), (p.cols - p.first + p.off) / VEC)));
         return p;
+    };
+    // whether a thread's word lies in memory words that are in the row whole
+    auto inside = [](int word, int lo, int hi, int off) { return word >= lo && word + (off ? 1 : 0) < hi; };
+    // a thread's word out of the memory words from `from` on
+    auto word_of = [](const uint4* from, int word, int off) {
+        const uint4 x = from[word], y = from[word + 1];
+        uint32_t v[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+        const int skip = off * ES / 4;           // whole 32-bit words, then, of bf16, half of one
+#pragma unroll
+        for (int i = 0; i < 6; ++i) v[i] = skip & 2 ? v[i + 2] : v[i];
+#pragma unroll
+        for (int i = 0; i < 5; ++i) v[i] = skip & 1 ? v[i + 1] : v[i];
+        if constexpr (!F32) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[i] = __funnelshift_r(v[i], v[i + 1], (off & 1) * 16);
+        }
+        return make_uint4(v[0], v[1], v[2], v[3]);
     };
     // a word that the row's edge cuts, or one outside, element by element
     auto edge_word = [&](const Place& p, int word) {
@@ -238,7 +267,7 @@ __global__ void __launch_bounds__(kThreads + 32, kAtOnce) beam_scan_kernel(const
         uint32_t v[4] = {NONE, NONE, NONE, NONE};
 #pragma unroll
         for (int e = 0; e < VEC; ++e)
-            if (col + e >= 0 && col + e < p.cols) {
+            if (col + e < p.cols) {
                 if constexpr (F32) {
                     v[e] = reinterpret_cast<const uint32_t*>(p.base)[col + e];
                 } else {
@@ -293,6 +322,7 @@ __global__ void __launch_bounds__(kThreads + 32, kAtOnce) beam_scan_kernel(const
     if (tid == 0) {
         s_abort = 0;
         s_count = 0;
+        s_none[0] = NONE;
         for (int i = 0; i < kRing; ++i) {
             mbar_init(smem_u32(&full[i]), 1);
             mbar_init(smem_u32(&empty[i]), kWarps);
@@ -314,10 +344,10 @@ __global__ void __launch_bounds__(kThreads + 32, kAtOnce) beam_scan_kernel(const
                     return;
                 }
                 const uint32_t bar = smem_u32(&full[slot]), bytes = static_cast<uint32_t>(p.hi - p.lo) * 16;
-                s_place[slot] = make_int3(p.token, p.lo, p.hi);
+                s_place[slot] = make_int4(p.token, p.lo, p.hi, p.off);
                 mbar_arrive_expect_tx(bar, bytes);
                 if (bytes)
-                    bulk_load(smem_u32(ring + slot * WORDS + p.lo), p.base + (p.first + p.lo * VEC) * ES, bytes, bar);
+                    bulk_load(smem_u32(ring + slot * SLOT + p.lo), p.base + (p.first - p.off + p.lo * VEC) * ES, bytes, bar);
                 if (++slot == kRing) slot = 0, phase ^= 1;
             }
         }
@@ -328,37 +358,40 @@ __global__ void __launch_bounds__(kThreads + 32, kAtOnce) beam_scan_kernel(const
     for (int64_t i = begin; i < end;) {
         const int c0 = c, c1 = static_cast<int>(min(static_cast<int64_t>(a.chunks), c0 + (end - i)));    // the piece
         const bool skip = done(row);
-        float m = -INFINITY, s = 0.0f, bound = -INFINITY;
+        float bound = -INFINITY;
         bool weak = true;
+        Part* stats = a.stats + (static_cast<int64_t>(row) * a.chunks + c) * kWarps + warp;
         for (; c < c1; ++c, ++i) {
             if (skip) continue;
             if (!dead) dead = !mbar_wait_warp(smem_u32(&full[slot]), phase, &s_abort, a.status);
-            const int3 p = s_place[slot];
+            const int4 p = s_place[slot];
+            const uint4* chunk = ring + slot * SLOT;
             uint4 w[NV];
             float x[kChunk];
+            if (p.w == 0) {
 #pragma unroll
-            for (int j = 0; j < NV; ++j) w[j] = ring[slot * WORDS + j * kThreads + tid];
-            const bool partial = p.y != 0 || p.z != WORDS;
+                for (int j = 0; j < NV; ++j) w[j] = chunk[j * kThreads + tid];
+            } else {
+#pragma unroll
+                for (int j = 0; j < NV; ++j) w[j] = word_of(chunk, j * kThreads + tid, p.w);
+            }
+            const bool partial = p.y != 0 || p.z != WORDS + (p.w ? 1 : 0);
             if (partial) {
                 const Place q = place(row, c);
 #pragma unroll
                 for (int j = 0; j < NV; ++j) {
                     const int word = j * kThreads + tid;
-                    if (word < p.y || word >= p.z) ring[slot * WORDS + word] = w[j] = edge_word(q, word);
+                    if (!inside(word, p.y, p.z, p.w)) w[j] = edge_word(q, word);
                 }
-                fence_proxy_async_cta();         // before the slot's next bulk copy may write there
             }
             values(w, x);
-            float best = x[0];
+            float best = -INFINITY;
 #pragma unroll
-            for (int e = 1; e < kChunk; ++e) best = fmaxf(best, x[e]);
-            if (best > m) {
-                s *= m == -INFINITY ? 1.0f : expf(m - best);             // a sum of nothing is 0, or NaN
-                m = best;
-            }
-            // 2^(x log2(e) - h), h = base log2(e) rounded: one fma a term; what the rounding of h makes of
-            // all of them is taken back from their sum
-            const float base = m == -INFINITY ? 0.0f : m;
+            for (int e = 0; e < kChunk; ++e) best = fmaxf(best, x[e]);
+            // The warp's sum under its maximum: 2^(x log2(e) - h), h = base log2(e) rounded, is one fma a term; what
+            // the rounding of h makes of all of them is taken back from their sum.
+            const float top = warp_max(best), base = top == -INFINITY ? 0.0f : top;
+            float sum = 0.0f, back = 1.0f;
             if (fabsf(base) < 1e37f) {
                 const float h = base * kLog2e;
                 const uint64_t l2 = pack2(kLog2e, kLog2e), h2 = pack2(-h, -h);
@@ -373,11 +406,16 @@ __global__ void __launch_bounds__(kThreads + 32, kAtOnce) beam_scan_kernel(const
                 }
                 float p0, p1;
                 unpack2(add2(u0, u1), p0, p1);
-                s = fmaf(p0 + p1, ex2(-fmaf(base, kLog2e, -h)), s);
+                sum = p0 + p1;
+                back = ex2(-fmaf(base, kLog2e, -h));
             } else {                                                     // past fp32 times log2(e), or +inf: NaN
 #pragma unroll
-                for (int e = 0; e < kChunk; ++e) s += ex2((x[e] - base) * kLog2e);
+                for (int e = 0; e < kChunk; ++e) sum += ex2((x[e] - base) * kLog2e);
             }
+#pragma unroll
+            for (int e = 16; e >= 1; e >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, e);
+            if (lane == 0) *stats = Part{top, sum * back};
+            stats += kWarps;
             if (weak) {                          // until a whole chunk has given the bound
                 group_max(best > -INFINITY ? ordered(best) : 0u, s_group, tid);
                 sync_all();
@@ -397,7 +435,13 @@ __global__ void __launch_bounds__(kThreads + 32, kAtOnce) beam_scan_kernel(const
                     const int l1 = lanes != 0 ? __ffs(lanes) - 1 : -1;
                     lanes &= lanes - 1;
                     const int l = lane < kChunk ? l0 : l1, e = lane % kChunk, from = warp * 32 + max(l, 0);
-                    const uint8_t* at_word = reinterpret_cast<const uint8_t*>(ring + slot * WORDS + e / VEC * kThreads + from) + e % VEC * ES;
+                    const int word = e / VEC * kThreads + from;
+                    const uint8_t* at_word = reinterpret_cast<const uint8_t*>(chunk + word) + (p.w + e % VEC) * ES;
+                    if (partial && !inside(word, p.y, p.z, p.w)) {       // from the row itself, where it reaches there
+                        const Place q = place(row, c);
+                        const int64_t col = q.first + word * VEC + e % VEC;
+                        at_word = col < q.cols ? q.base + col * ES : reinterpret_cast<const uint8_t*>(s_none);
+                    }
                     const float logit = F32 ? *reinterpret_cast<const float*>(at_word) : bf16_to_f32(*reinterpret_cast<const uint16_t*>(at_word));
                     const bool take = l >= 0 && logit >= bound && logit > -INFINITY;
                     const uint32_t set = __ballot_sync(0xffffffffu, take);
@@ -425,19 +469,7 @@ __global__ void __launch_bounds__(kThreads + 32, kAtOnce) beam_scan_kernel(const
             sync_all();
         }
         if (!skip) {
-            // the piece's maximum and sum
-            float top = m;
-#pragma unroll
-            for (int e = 16; e >= 1; e >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, e));
-            if (lane == 0) s_top[warp] = top;
-            sync_all();
-            top = s_top[0];
-#pragma unroll
-            for (int e = 1; e < kWarps; ++e) top = fmaxf(top, s_top[e]);
-            double sum = s * carried(m, top);    // NaN stays
-#pragma unroll
-            for (int e = 16; e >= 1; e >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, e);
-            if (lane == 0) s_sum[warp] = sum;
+            sync_all();                          // the candidates are in
             const int64_t out = static_cast<int64_t>(row) * a.most + (blockIdx.x - line.of(static_cast<int64_t>(row) * a.chunks));
             uint64_t* keys = a.keys + out * a.k;
             if (s_count <= kRoom) {
@@ -455,9 +487,10 @@ __global__ void __launch_bounds__(kThreads + 32, kAtOnce) beam_scan_kernel(const
 #pragma unroll
                         for (int j = 0; j < NV; ++j) {
                             const int word = j * kThreads + tid;
-                            w[j] = word >= p.lo && word < p.hi
-                                       ? __ldg(reinterpret_cast<const uint4*>(p.base + (p.first + word * VEC) * ES))
-                                       : edge_word(p, word);
+                            const uint4* from = reinterpret_cast<const uint4*>(p.base + (p.first - p.off) * ES);
+                            w[j] = !inside(word, p.lo, p.hi, p.off) ? edge_word(p, word)
+                                   : p.off == 0                     ? from[word]
+                                                                    : word_of(from, word, p.off);
                         }
                         values(w, x);
 #pragma unroll
@@ -471,16 +504,7 @@ __global__ void __launch_bounds__(kThreads + 32, kAtOnce) beam_scan_kernel(const
                     if (tid == 0) keys[n] = last;
                 }
             }
-            sync_all();
-            if (tid == 0) {
-                Piece st;
-                st.top = top;
-                st.pad = 0;
-                st.sum = 0.0;
-                for (int e = 0; e < kWarps; ++e) st.sum += s_sum[e];
-                a.stats[out] = st;
-                s_count = 0;
-            }
+            if (tid == 0) s_count = 0;
             sync_all();
         }
         if (c == a.chunks) c = 0, ++row;
@@ -495,7 +519,7 @@ __device__ __forceinline__ bool before(const Cand& a, const Cand& b) {
     return a.score > b.score || (a.score == b.score && a.place < b.place);
 }
 
-// log of x >= 2^-1000 to about 1e-14: exponent and the series 2 (z + z^3/3 + ...) of log f, z = (f - 1) / (f + 1),
+// log of x >= 2^-1000 to about 1e-14 (x itself is good to about 2^-22): exponent and the series 2 (z + z^3/3 + ...) of log f, z = (f - 1) / (f + 1),
 // for f in [3/4, 3/2).  A third of the library's fp64 instructions, which are what the second kernel waits for.
 __device__ __forceinline__ double log_of_sum(double x) {
     const long long bits = __double_as_longlong(x);
@@ -547,19 +571,29 @@ __global__ void __launch_bounds__(kThreads) beam_pick_kernel(const __grid_consta
                 if (done) {
                     if (score > -INFINITY) add = score;
                 } else {
-                    const Piece* st = a.stats + (row0 + b) * a.most;
-                    Piece mine{0.0, -INFINITY, 0};
-                    if (lane < pieces) mine = st[lane];
-                    for (int i = lane + 32; i < pieces; i += 32) {
-                        const Piece o = st[i];
-                        const float up = fmaxf(mine.top, o.top);
-                        mine.sum = mine.sum * carried(mine.top, up) + o.sum * carried(o.top, up);
-                        mine.top = up;
-                    }
-                    float top = mine.top;
+                    // the sums of all chunks and warps, joined in an order that a row's sizes give
+                    const Part* st = a.stats + (row0 + b) * a.chunks * kWarps;
+                    const int parts = a.chunks * kWarps;
+                    float top = -INFINITY;
+                    double sum = 0.0;
+                    for (int i0 = 0; i0 < parts; i0 += 32 * kAhead) {
+                        Part part[kAhead];
+                        float up = top;
 #pragma unroll
-                    for (int m = 16; m >= 1; m >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, m));
-                    double sum = mine.sum * carried(mine.top, top);
+                        for (int i = 0; i < kAhead; ++i) {
+                            const int at = i0 + 32 * i + lane;
+                            part[i] = at < parts ? st[at] : Part{-INFINITY, 0.0f};
+                            up = fmaxf(up, part[i].top);
+                        }
+                        up = warp_max(up);
+                        if (i0 != 0) sum *= carried(top, up);
+                        top = up;
+#pragma unroll
+                        for (int i = 0; i < kAhead; i += 2)
+                            if (i0 + 32 * i < parts)
+                                sum += static_cast<double>(part[i].sum * carried(part[i].top, top) +
+                                                           part[i + 1].sum * carried(part[i + 1].top, top));
+                    }
 #pragma unroll
                     for (int m = 16; m >= 1; m >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, m);
                     // a finite maximum's sum is at least 1, unless NaN is in it
@@ -639,18 +673,13 @@ __global__ void __launch_bounds__(kThreads) beam_pick_kernel(const __grid_consta
 
 constexpr int kChunkLogits = kThreads * kChunk;
 
-// Chunks of a shard of a row: one more than its columns need where a row can begin inside a 16-byte word.
-int chunks_of(int64_t cols, int vec) {
-    return cols == 0 ? 0 : static_cast<int>((cols + vec - 1 + kChunkLogits - 1) / kChunkLogits);
-}
-
 }  // namespace
 
 size_t beam_workspace(int64_t items, int beams, int k, int64_t vocab) {
     // a row has at most as many pieces as chunks, and never more chunks than this
-    const int64_t most = (vocab + kChunkLogits - 1) / kChunkLogits + 2 * TP_MAX_SHARDS;
+    const int64_t most = (vocab + kChunkLogits - 1) / kChunkLogits + TP_MAX_SHARDS;
     const int64_t rows = items * beams;
-    return static_cast<size_t>(rows) * most * (sizeof(Piece) + static_cast<size_t>(k) * 8);
+    return static_cast<size_t>(rows) * most * (kWarps * sizeof(Part) + static_cast<size_t>(k) * 8);
 }
 
 tp_status launch_beam_select(const BeamDesc& d, cudaStream_t stream) {
@@ -668,7 +697,7 @@ tp_status launch_beam_select(const BeamDesc& d, cudaStream_t stream) {
     if (sms <= 0) return TP_ERR_CUDA;
     for (int r = 0; r < TP_MAX_SHARDS; ++r) {
         a.first_chunk[r] = a.chunks;
-        if (r < d.t) a.chunks += chunks_of(d.cols[r], d.f32 ? 4 : 8);
+        if (r < d.t) a.chunks += static_cast<int>((d.cols[r] + kChunkLogits - 1) / kChunkLogits);
     }
     a.first_chunk[TP_MAX_SHARDS] = a.chunks;
     const int64_t total = rows * a.chunks;
@@ -687,18 +716,18 @@ tp_status launch_beam_select(const BeamDesc& d, cudaStream_t stream) {
     a.scores_out = d.scores_out;
     a.rows_out = d.rows_out;
     a.tokens_out = d.tokens_out;
-    a.stats = static_cast<Piece*>(d.ws);
-    a.keys = reinterpret_cast<uint64_t*>(a.stats + rows * a.most);
+    a.stats = static_cast<Part*>(d.ws);
+    a.keys = reinterpret_cast<uint64_t*>(a.stats + rows * a.chunks * kWarps);
     const dim3 grid(a.blocks), block(kThreads + 32);
     a.status = device_status_word();
-    constexpr int kSmem = kRing * kThreads * kChunk * 4;         // of fp32; bf16 takes half
+    constexpr int kSmem = kRing * (kThreads * kChunk * 4 + 16), kSmem16 = kRing * (kThreads * kChunk * 2 + 16);
     static std::atomic<uint64_t> smem_f32{0}, smem_bf16{0};
     if (!smem_attribute_once(d.f32 ? reinterpret_cast<const void*>(beam_scan_kernel<true>)
                                    : reinterpret_cast<const void*>(beam_scan_kernel<false>),
                              kSmem, d.f32 ? smem_f32 : smem_bf16))
         return TP_ERR_CUDA;
     const cudaError_t e = d.f32 ? launch_pdl(beam_scan_kernel<true>, grid, block, kSmem, stream, a)
-                                : launch_pdl(beam_scan_kernel<false>, grid, block, kSmem / 2, stream, a);
+                                : launch_pdl(beam_scan_kernel<false>, grid, block, kSmem16, stream, a);
     if (e != cudaSuccess) return TP_ERR_CUDA;
     return launch_pdl(beam_pick_kernel, dim3(d.items), dim3(kThreads), 0, stream, a) == cudaSuccess ? TP_OK : TP_ERR_CUDA;
 }
