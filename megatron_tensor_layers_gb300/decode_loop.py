@@ -118,9 +118,13 @@ def forward(model: Model, cache: Cache, ids: torch.Tensor, cu_rows: Optional[tor
 @torch.no_grad()
 def generate(model: Model, prompts: Sequence[torch.Tensor], beams: int, steps: int, *, pages: int = 0,
              compact_every: int = 0):
-    """Beam search from ragged prompts (1-D int32 CUDA tensors): (tokens [items, beams, steps], scores
-    [items, beams]), best first."""
+    """Beam search from ragged prompts (1-D int32 CUDA tensors, a token each at least): (tokens [items, beams,
+    steps], scores [items, beams]), best first."""
     c = model.cfg
+    if not prompts or any(p.dim() != 1 or p.numel() < 1 or p.dtype != torch.int32 for p in prompts):
+        raise ValueError("prompts must hold 1-D int32 tensors of a token each at least")
+    if steps < 1 or beams < 1:
+        raise ValueError("steps and beams must be 1 or more")
     dev, items = prompts[0].device, len(prompts)
     lengths = [int(p.numel()) for p in prompts]
     blocks = -(-(max(lengths) + steps + 1) // c.page_size)
