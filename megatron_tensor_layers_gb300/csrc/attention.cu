@@ -589,9 +589,9 @@ __global__ void __launch_bounds__(Cfg<HD, NT>::WARPS * 32, 1) kv4_attention_kern
 
         float acc[NT][MT][4];
         float mx[NT][2], sum[NT][2], corr[NT][2];
-        // exponent field of the largest value step, at least 16 so that 2^(kPShift - E) stays finite; a range that
-        // fp32 holds has a step of at most 2^124.1, field 251
-        int vexp = 16;
+        // exponent field of the largest value step that a column has seen, at least 16 so that 2^(kPShift - E) stays
+        // finite; a range that fp32 holds has a step of at most 2^124.1, field 251
+        int vexp[NT][2];
         bool fresh = true;               // some column has seen nothing
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
@@ -600,7 +600,7 @@ __global__ void __launch_bounds__(Cfg<HD, NT>::WARPS * 32, 1) kv4_attention_kern
 #pragma unroll
                 for (int e = 0; e < 4; ++e) acc[nt][i][e] = 0.0f;
 #pragma unroll
-            for (int e = 0; e < 2; ++e) mx[nt][e] = kNegInf, sum[nt][e] = 0.0f, corr[nt][e] = 0.0f;
+            for (int e = 0; e < 2; ++e) mx[nt][e] = kNegInf, sum[nt][e] = 0.0f, corr[nt][e] = 0.0f, vexp[nt][e] = 16;
         }
 
         for (int u = u0; u < u1; ++u) {
@@ -619,7 +619,7 @@ __global__ void __launch_bounds__(Cfg<HD, NT>::WARPS * 32, 1) kv4_attention_kern
                 constexpr int BLOCKS = decltype(blocks)::value;
                 float x[BLOCKS][NT][4];
                 uint32_t vp[BLOCKS][2];
-                uint32_t vtop = 0;                                       // largest step of the values: not negative
+                uint32_t vtop[NT][2] = {};                               // largest step that the columns see: not negative
 #pragma unroll
                 for (int i = 0; i < BLOCKS; ++i) {
                     const uint32_t rec = buf + (from + i) * B::BYTES;
@@ -673,12 +673,22 @@ __global__ void __launch_bounds__(Cfg<HD, NT>::WARPS * 32, 1) kv4_attention_kern
 #pragma unroll
                             for (int e = 0; e < 2; ++e) {
                                 const int p = cpos[nt][e];
-                                if (!(ja <= p && (a.window == 0 || ja > p - a.window || ja < a.sinks))) x[i][nt][e] = kNegInf;
-                                if (!(jb <= p && (a.window == 0 || jb > p - a.window || jb < a.sinks)))
-                                    x[i][nt][2 + e] = kNegInf;
+                                const bool sa = ja <= p && (a.window == 0 || ja > p - a.window || ja < a.sinks);
+                                const bool sb = jb <= p && (a.window == 0 || jb > p - a.window || jb < a.sinks);
+                                if (!sa) x[i][nt][e] = kNegInf;
+                                if (!sb) x[i][nt][2 + e] = kNegInf;
+                                vtop[nt][e] = max(sa ? vp[i][0] & 0xffffu : 0u, sb ? vp[i][1] & 0xffffu : 0u);
                             }
+                    } else {
+                        vtop[0][0] = max(vtop[0][0], max(vp[i][0] & 0xffffu, vp[i][1] & 0xffffu));
                     }
-                    vtop = max(vtop, max(vp[i][0] & 0xffffu, vp[i][1] & 0xffffu));
+                }
+                static_assert(!EDGE || BLOCKS == 1, "vtop is that of one block");
+                if constexpr (!EDGE) {
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) vtop[nt][e] = vtop[0][0];
                 }
 
                 // p s' as B fragments, and what the stage adds to the sums
@@ -686,19 +696,19 @@ __global__ void __launch_bounds__(Cfg<HD, NT>::WARPS * 32, 1) kv4_attention_kern
                 float psum[NT][2], pcorr[NT][2];
                 auto weigh = [&]() {
                     constexpr float under = 1.0f / (1 << kUnder);
-                    const float vscale = __uint_as_float(static_cast<uint32_t>(253 - vexp) << 23) * (1 << kPShift);
-                    float m[NT][2];
+                    float m[NT][2], vscale[NT][2];
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                         for (int e = 0; e < 2; ++e) {
                             psum[nt][e] = pcorr[nt][e] = 0.0f;
                             m[nt][e] = mx[nt][e] == kNegInf ? 0.0f : mx[nt][e];
+                            vscale[nt][e] = __uint_as_float(static_cast<uint32_t>(253 - vexp[nt][e]) << 23) * (1 << kPShift);
                         }
 #pragma unroll
                     for (int i = 0; i < BLOCKS; ++i) {
-                        const float s0 = __uint_as_float(vp[i][0] << 16) * vscale, b0 = __uint_as_float(vp[i][0] & 0xffff0000u) * under;
-                        const float s1 = __uint_as_float(vp[i][1] << 16) * vscale, b1 = __uint_as_float(vp[i][1] & 0xffff0000u) * under;
+                        const float s0 = __uint_as_float(vp[i][0] << 16), b0 = __uint_as_float(vp[i][0] & 0xffff0000u) * under;
+                        const float s1 = __uint_as_float(vp[i][1] << 16), b1 = __uint_as_float(vp[i][1] & 0xffff0000u) * under;
 #pragma unroll
                         for (int nt = 0; nt < NT; ++nt) {
                             float ps[4];
@@ -709,12 +719,12 @@ __global__ void __launch_bounds__(Cfg<HD, NT>::WARPS * 32, 1) kv4_attention_kern
                                 psum[nt][e] += pa + pb;
                                 if constexpr (EDGE) {
                                     // a token that this column does not see may stand for NaN or infinities
-                                    ps[e] = xa == kNegInf ? 0.0f : pa * s0;
-                                    ps[2 + e] = xb == kNegInf ? 0.0f : pb * s1;
+                                    ps[e] = xa == kNegInf ? 0.0f : pa * (s0 * vscale[nt][e]);
+                                    ps[2 + e] = xb == kNegInf ? 0.0f : pb * (s1 * vscale[nt][e]);
                                     pcorr[nt][e] += (xa == kNegInf ? 0.0f : pa * b0) + (xb == kNegInf ? 0.0f : pb * b1);
                                 } else {
-                                    ps[e] = pa * s0;
-                                    ps[2 + e] = pb * s1;
+                                    ps[e] = pa * (s0 * vscale[nt][e]);
+                                    ps[2 + e] = pb * (s1 * vscale[nt][e]);
                                     pcorr[nt][e] = fmaf(pa, b0, fmaf(pb, b1, pcorr[nt][e]));
                                 }
                             }
@@ -723,7 +733,11 @@ __global__ void __launch_bounds__(Cfg<HD, NT>::WARPS * 32, 1) kv4_attention_kern
                         }
                     }
                 };
-                bool again = fresh || static_cast<int>(vtop >> 7) > vexp;
+                bool again = fresh;
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) again |= static_cast<int>(vtop[nt][e] >> 7) > vexp[nt][e];
                 if (!__any_sync(0xffffffffu, again)) {                   // the old maximum may do
                     weigh();
 #pragma unroll
@@ -744,21 +758,22 @@ __global__ void __launch_bounds__(Cfg<HD, NT>::WARPS * 32, 1) kv4_attention_kern
                         }
 #pragma unroll
                     for (int m = 4; m < 32; m <<= 1) {
-                        vtop = max(vtop, __shfl_xor_sync(0xffffffffu, vtop, m));
 #pragma unroll
                         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                            for (int e = 0; e < 2; ++e)
+                            for (int e = 0; e < 2; ++e) {
+                                vtop[nt][e] = max(vtop[nt][e], __shfl_xor_sync(0xffffffffu, vtop[nt][e], m));
                                 cmax[nt][e] = fmaxf(cmax[nt][e], __shfl_xor_sync(0xffffffffu, cmax[nt][e], m));
+                            }
                     }
-                    const int e_new = max(vexp, min(static_cast<int>(vtop >> 7), 251));
-                    const float vdown = __uint_as_float(static_cast<uint32_t>(max(127 - (e_new - vexp), 0)) << 23);
-                    vexp = e_new;
                     bool unseen = false;
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                         for (int e = 0; e < 2; ++e) {
+                            const int e_new = max(vexp[nt][e], min(static_cast<int>(vtop[nt][e] >> 7), 251));
+                            const float vdown = __uint_as_float(static_cast<uint32_t>(max(127 - (e_new - vexp[nt][e]), 0)) << 23);
+                            vexp[nt][e] = e_new;
                             const float m = fmaxf(mx[nt][e], cmax[nt][e]);
                             const float alpha = ex2(mx[nt][e] - (m == kNegInf ? 0.0f : m));
                             mx[nt][e] = m;
@@ -829,11 +844,11 @@ __global__ void __launch_bounds__(Cfg<HD, NT>::WARPS * 32, 1) kv4_attention_kern
 
         // ---- the warp's result: O, maximum and sum of each column, every lane with its own dimensions
         static_assert(24 - kPShift + 251 + 1 - kUnder <= 254 && 24 - kPShift + 16 + 1 - kUnder >= 1, "a normal power of two");
-        const float down = __uint_as_float(static_cast<uint32_t>(24 - kPShift + vexp + 1 - kUnder) << 23);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
+                const float down = __uint_as_float(static_cast<uint32_t>(24 - kPShift + vexp[nt][e] + 1 - kUnder) << 23);
 #pragma unroll
                 for (int m = 4; m < 32; m <<= 1) {
                     sum[nt][e] += __shfl_xor_sync(0xffffffffu, sum[nt][e], m);

@@ -135,3 +135,23 @@ def test_rows_of_the_largest_and_smallest_keys(hd, factor):
     for rows, seed in (([1] * 5, 77), ([3, 2, 4, 1, 2], 78)):
         q = [(x.float() / factor).to(torch.bfloat16) for x in rows_of(c, rows, 16, seed)]
         check_attention(c, rows, 16, seed, q=q)
+
+
+@pytest.mark.parametrize("factor", [1e4, 1e9, 1e20])
+@pytest.mark.parametrize("window", [0, 20])
+def test_a_large_value_that_a_row_does_not_see_costs_it_nothing(window, factor):
+    """The same for a few rows, which share their tokens' loads: the token among the last of a block, seen by the later
+    rows alone, and with the window by the earlier ones alone."""
+    c = Cache(1, 8, 128, 64, [512], 79)
+    big = 507 if window == 0 else 488
+    page, off = c.table[0, big // 64], big % 64
+    for i in (1, 2):
+        c.vq[i][0, page, :, off // 16, off % 16] = K.bf16(c.vq[i][0, page, :, off // 16, off % 16] * np.float32(factor))
+    c.fill()
+    rng = np.random.default_rng(80)
+    q = [torch.from_numpy(rng.standard_normal((8, 16 * 128)).astype(np.float32)).to(torch.bfloat16).to(DEV)]
+    got = tp.tp_kv4_attention(q, c.pools, c.dtable, c.dlens, cu_rows=cu_of([8]), window=window)
+    assert tp.tp_device_status() == 0
+    rows = [i for i in range(8) if 504 + i < big or (window and 504 + i - window >= big)]
+    assert rows == ([0, 1, 2] if window == 0 else [4, 5, 6, 7])
+    check_some(c, q, got, 8, 16, rows, window)
