@@ -460,8 +460,8 @@ tp_status tp_kv4_append(int t, int64_t n, int64_t nseq, int kv_heads, int head_d
                         const int32_t* cu_rows, tp_stream stream);
 
 /*
- * The values that the n rows' cached keys and values stand for, as bf16
- * (rounded once) or fp32 (fp32 step * u + base): the inverse of
+ * The values that the n rows' cached keys and values stand for, as fp32
+ * (step * u + base, rounded once) or as that rounded to bf16: the inverse of
  * tp_kv4_append.  k[r], v[r] are [n, kv_heads * head_dim] of dtype with row
  * strides ldk, ldv; either list may be NULL.  Rows that are not in the
  * cache read as 0.
@@ -496,13 +496,22 @@ size_t tp_kv4_attention_workspace_size(int t, int64_t n, int64_t nseq, int heads
  *           overwritten.
  * heads must be a multiple of kv_heads with at most 128 query heads per kv
  * head (TP_ERR_NOT_DIVISIBLE, TP_ERR_UNSUPPORTED).  Statistics and sums are
- * fp32; q enters the products exactly (as fp16 after a power-of-two
- * scaling), the probabilities rounded to fp16.  Where rows * heads come to
- * 72 and more for each pair of the device's SMs, in sequences with at least
- * 72 rows * heads / kv_heads, keys and values are rounded to fp16 too, each
- * by 2^-11 of itself or 2^-25 of the power of two next to the largest step
- * or base of its 32 tokens; elsewhere they enter as the cache has them.
- * The order of the sums is fixed by the sizes and lengths.
+ * fp32.  Fewer bits are:
+ *   - q, as fp16 under a power of two of its row: exact down to 2^-23 of the
+ *     row's largest element, and off by at most 2^-31 of that below;
+ *   - the probabilities, as fp16 times the values' scale: a token's p v (p
+ *     under the running maximum) is off by at most 2^-11 of itself or 2^-28 of
+ *     the largest step that the row sees; in chunks, 2^-20 of it or 2^-24 of
+ *     the largest base;
+ *   - in chunks, keys and values, as fp16: each off by at most 2^-11 of itself
+ *     or 2^-15 of the largest step or 2^-38 of the largest base of its 32
+ *     tokens, those included that the row does not see.  Elsewhere they enter
+ *     as the cache has them.
+ * Chunks are sequences of at least 72 rows * heads / kv_heads where all of
+ * them together come to 72 rows * heads and more for each pair of the device's
+ * SMs.  The order of the sums is fixed by the sizes and lengths.  Finite keys
+ * and values of any size give finite results as long as the scores, scale *
+ * sum(q) and (times 2^-14, outside chunks) the sum of p v stay in fp32.
  */
 tp_status tp_kv4_attention(int t, int64_t n, int64_t nseq, int heads, int kv_heads, int head_dim,
                            const void* const* q, int64_t ldq, const void* const* pool, int64_t pages, int page_size,

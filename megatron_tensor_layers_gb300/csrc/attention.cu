@@ -1,9 +1,10 @@
 // Attention over the paged 4-bit cache for few rows per sequence (decode,
 // speculation): one pass over the cached codes.  Large calls are bound by the
-// instructions that turn codes into operands (236 for a block of 16 tokens and 8
-// columns, at 0.46 an SM quarter and cycle, with two warps there): 64 sequences of
-// 4100 to 8192 tokens for 8 kv heads of 128 take 87 us, 4.8 TB/s.  Small ones by
-// latencies: one sequence of 4097 tokens takes 13.4 us.
+// instructions that turn codes into operands (243 for a block of 16 tokens and 8
+// columns, at 0.46 an SM quarter and cycle) and by what two warps there wait for
+// of each other's results: 64 sequences of 4100 to 8192 tokens for 8 kv heads of 128
+// take 89 us, 4.7 TB/s, with neither memory (58 %) nor the issue slots full.  Small
+// ones by latencies: one sequence of 4097 tokens takes 13.8 us.
 //
 // Mathematics.  With key j = s_j u_j + b_j (u_j the codes),
 //     x_j = c (s_j (q . u_j) + b_j sum(q)),      c = scale log2(e),
@@ -17,9 +18,11 @@
 // pair scaled by 16, and w >> 8 gives the other two: five instructions for
 // eight codes.  The 16 is taken back in q (keys) and in the output's scale
 // (values), both exact.  q is scaled by a power of two per row so that its
-// largest element is in [2^10, 2^11): a bf16 q is exact in fp16 down to 2^-24 of
-// that.  p s' is scaled by 2^(13 - E), E the exponent of the largest step seen,
-// and rounded to fp16 (2^-11 relative): the one rounding of the products.
+// largest element is in [2^10, 2^11): a bf16 q is exact in fp16 down to 2^-23 of
+// that.  p s' is scaled by 2^(7 - E), E the exponent of the largest step that the
+// column has seen, and rounded to fp16 (by 2^-11 of itself, or 2^-32 of 2^E): the
+// one rounding of the products.  (One E for all columns took 87.6 us instead of
+// 88.9, and a large value cost the rows that do not see it their bits.)
 //
 // What is subtracted, m, is a column's maximum as of the last time it was
 // needed: a stage first takes p under the old m, and only when a sum exceeds 2^7
@@ -49,7 +52,7 @@
 // query heads of a group fill them.  tcgen05 would want 128 rows of them.  With
 // two warps on a scheduler it is the independent work within a warp that hides
 // latencies: the blocks of a full, fully visible stage run as one straight line
-// (87 us; two at a time 91, one at a time 94).  Three warps there, of 168
+// (two at a time takes 5 % longer, one at a time 8 %).  Three warps there, of 168
 // registers, take 100 us and more.  An item's ends, whose instructions are rarely
 // in the cache, go block by block.
 #include <algorithm>
@@ -63,7 +66,7 @@ namespace {
 constexpr int kWarps = 8;
 constexpr int kBatch = 32;           // blocks whose addresses a warp holds, one in each lane
 constexpr int kStages = 2;
-constexpr int kPShift = 8;           // p s' is held times 2^(kPShift - E)
+constexpr int kPShift = 8;           // p s' is held times 2^(kPShift - 1 - E)
 constexpr int kUnder = 14;           // what p v adds up to is held times 2^-kUnder, so that it passes fp32 only with the values
 constexpr float kMost = 128.0f;      // sum of a lane's 2^(x - m) up to which the old maximum will do
 constexpr int kMany = 72;            // columns for each pair of blocks from which the many-rows kernel pays (many_pays)

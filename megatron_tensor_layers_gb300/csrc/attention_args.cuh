@@ -65,9 +65,11 @@ constexpr int kManyCols = 512;       // columns of a pair of thread blocks of th
 // columns they hold: over 4096 cached tokens of head dimension 128 the first takes
 // 64 us for 4096 columns, 84 for 5504 and 111 for 8192, the second 77 to 78 us
 // (dimension 64: 46, 59 and 80 us against 64 to 66; over 512 tokens, 128: 23, 26
-// and 39 us against 32 to 33).  So the second is worth its launch from 72 columns
-// for each pair of each wave, counted over the sequences that
-// have 72 by themselves (a shorter one would leave a pair to fewer).  `cols`
+// and 39 us against 32 to 33).  From 72 columns for each pair of each wave (5472 here),
+// counted over the sequences that have 72 by themselves (a shorter one would leave
+// a pair to fewer), the second is taken.  That is where they cross over 4096 tokens
+// of dimension 128; with dimension 64 or short contexts, whose crossing is at 6000
+// to 7000 columns, the second is up to a quarter slower between the two.  `cols`
 // columns of such sequences for each of the heads make `tiles` tiles; both kernels
 // come to the same answer.
 __device__ __forceinline__ int many_tiles(const AttnArgs& a, int64_t cols) {

@@ -1,6 +1,6 @@
 // Attention over the paged 4-bit cache for many rows per sequence (chunks of
 // prompts): matrix products on the 5th-generation tensor cores.  8192 new rows in
-// four chunks over 2100 to 6001 tokens, 64 query heads of 128, take 886 us, 980
+// four chunks over 2100 to 6001 tokens, 64 query heads of 128, take 888 us, 980
 // TFLOP/s.  Bound by the chain of a tile (S, then its exponentials, then the
 // second product, then the next S): a step of both tiles takes about 4000 cycles,
 // its products 2200 of them.
@@ -20,12 +20,13 @@
 //
 // Codes to operands.  A code is an fp16 subnormal u 2^-24 (or 16 u 2^-24) after
 // one mask, and one HFMA2 makes the fp16 value (s u + b) 2^-F of two elements:
-// 9 instructions for 8 keys, shared by all 512 columns.  F is the exponent of
-// the largest step or base of 32 tokens, so that nothing overflows; a value is
-// rounded once, by at most 2^-11 of itself or 2^-25 of their scale 2^F.  The
-// scale of K enters the exponent's factor c, the scale of V the exponent itself
-// (P 2^(F - Fref)), both per 32 tokens.  Keys keep their packed order
-// (q is permuted to it), values are transposed while they are unpacked: eight
+// 9 instructions for 8 keys, shared by all 512 columns.  2^F is 2^9 times the
+// largest step or 2^-14 times the largest base of 32 tokens (the larger; powers of
+// two), so that nothing overflows; a value is rounded once, by at most 2^-11 of
+// itself or 2^-25 of 2^F.  The scale of K enters the exponent's factor c, the scale
+// of V the exponent itself (P 2^(F - Fref), Fref that of the largest values a column
+// has seen), both per 32 tokens; the sum of the probabilities is free of it.  Keys
+// keep their packed order (q is permuted to it), values are transposed while they are unpacked: eight
 // tokens' words give eight dimensions' 16-byte chunks of V^T.
 //
 // What is subtracted, m, is a column's maximum as of the last time it was

@@ -16,7 +16,7 @@ stages and its staging in the ring), fused200 (70B MLP, t=4, 200 tokens, fused:
 every tile of the down GEMM split along K over two CTA pairs), cache (append and
 load of 8192 rows, t=8, fp32 out), attend (decode attention, t=4, 64 sequences of
 6144 cached tokens), chunk (attention of two chunks of 1024 rows over 3000 tokens,
-t=4), pages (a fork of 256 rows and a compaction of 96 MB), beam (32 requests of 8
+t=4), pages (a fork of 256 rows and a compaction that moves 198 MB), beam (32 requests of 8
 beams, vocabulary 128000 in 4 shards).
 """
 
