@@ -326,6 +326,7 @@ __global__ void __launch_bounds__(kThreads + 32, kAtOnce) beam_scan_kernel(const
         for (int i = 0; i < kRing; ++i) {
             mbar_init(smem_u32(&full[i]), 1);
             mbar_init(smem_u32(&empty[i]), kWarps);
+            s_place[i] = make_int4(0, 0, 0, 0);  // what is read of a slot whose copy is lost stays in the ring
         }
     }
     fence_barrier_init();
@@ -519,8 +520,8 @@ __device__ __forceinline__ bool before(const Cand& a, const Cand& b) {
     return a.score > b.score || (a.score == b.score && a.place < b.place);
 }
 
-// log of x >= 2^-1000 to about 1e-14 (x itself is good to about 2^-22): exponent and the series 2 (z + z^3/3 + ...) of log f, z = (f - 1) / (f + 1),
-// for f in [3/4, 3/2).  A third of the library's fp64 instructions, which are what the second kernel waits for.
+// log of x >= 2^-1000 to about 1e-14 (x itself is good to about 2^-22): exponent and the series
+// 2 (z + z^3/3 + ...) of log f, z = (f - 1) / (f + 1), for f in [3/4, 3/2).  A third of the library's fp64 instructions, which are what the second kernel waits for.
 __device__ __forceinline__ double log_of_sum(double x) {
     const long long bits = __double_as_longlong(x);
     int e = static_cast<int>(bits >> 52) - 1023;
