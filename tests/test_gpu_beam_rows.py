@@ -53,3 +53,21 @@ def test_equal_beams_tie(items, vocab, extra, dtype):
             alone = tp.tp_beam_select([y[i * beams:(i + 1) * beams] for y in shards], scores[i:i + 1], k)
             assert torch.equal(alone[0][0], s[i]) and alone[2][0].tolist() == want_tokens[i]
     assert tp.tp_device_status() == 0
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_vocabulary_of_many_chunks(dtype):
+    """More chunks than the second kernel asks for at once, with the largest logits first, last, or in the middle, and
+    chunks of nothing but -inf."""
+    vocab, beams = 450001, 4
+    g = torch.Generator(device=DEV).manual_seed(6)
+    x = torch.randn((1, beams, vocab), device=DEV, generator=g)
+    ramp = torch.linspace(0, 30, vocab, device=DEV)
+    x[0, 0] += ramp
+    x[0, 1] += ramp.flip(0)
+    x[0, 2, :200000] = -float("inf")
+    x[0, 2, 250000:] = -float("inf")
+    x = x.to(dtype)
+    scores = -torch.rand((1, beams), device=DEV, generator=g)
+    check_beams(x, scores, 10, shards=[x[0]])
+    check_beams(x, scores, 3, 3)
