@@ -352,6 +352,7 @@ __global__ void __launch_bounds__(kThreads + 32, kAtOnce) beam_scan_kernel(const
                 if (++slot == kRing) slot = 0, phase ^= 1;
             }
         }
+        if (*static_cast<volatile int*>(&s_abort)) spin_ns(1000000);     // nobody waits for the last copies then
         return;
     }
     int slot = 0, phase = 0;
