@@ -69,7 +69,8 @@ typedef enum {
     TP_ERR_WORKSPACE = 7      /* workspace missing or too small */
 } tp_status;
 
-typedef enum { TP_BF16 = 0, TP_F32 = 1 } tp_dtype;
+/* TP_FP8 (e4m3 codes with fp32 scales) is taken by the tp_fp8_* calls only, where they name it. */
+typedef enum { TP_BF16 = 0, TP_F32 = 1, TP_FP8 = 2 } tp_dtype;
 
 /* How the t partial sums are reduced ("all-reduce sum").
  * DIRECT: one-shot sum in rank order, float32 carry (page "vLLM source
@@ -404,6 +405,110 @@ tp_status tp_reduce_scatter_rmsnorm(int t, int64_t n, int64_t h, tp_dtype dtype,
  */
 tp_status tp_shard_gather(int t, int64_t rows, const int64_t* cols, tp_dtype dtype,
                           const void* const* shards, void* out, tp_stream stream);
+
+/*
+ * ---------------------------------------------------------------------
+ * Layers in 8-bit floating point: rows and weights held as e4m3 codes (one
+ * byte: 4 exponent, 3 mantissa bits, largest value 448, no infinities) with
+ * fp32 scales.  The pages this library follows name quantised serving
+ * without a form; the definitions below are this library's own.
+ *
+ * Rows.  A row of k columns (k a multiple of 16) has G = ceil(k / 128)
+ * groups of 128 columns, the last one possibly shorter.  Codes are
+ * [n, k] (row stride a multiple of 16 bytes), scales [G, n] fp32 (row
+ * stride lds >= n: the scales of one group of all rows are contiguous).
+ * Weights.  A weight [out, k] has a scale for each block of 128 rows by 128
+ * columns, [ceil(out / 128), G] fp32, contiguous.  A gated weight (gate rows,
+ * then as many up rows) is cut into blocks half by half: its scales are
+ * [2 ceil((out / 2) / 128), G], gate's blocks first.
+ * A code c with scale s stands for c * s.
+ *
+ * Bringing values x to 8 bits: s = max(amax, 2^-100) / 448 with amax the
+ * largest |x| of the group or block, c = e4m3(x / s) to nearest, ties to
+ * even; each operation rounded to fp32.  A group with a NaN or an infinity
+ * has a NaN or infinite scale and stands for NaN in every element.
+ *
+ * Products.  y_ij = sum over the K groups g of (s_x[g, i] * s_w[j / 128, g])
+ * * sum_k c_x c_w, the inner sum on the tensor core, the outer one in fp32 in
+ * the groups' order (rank by rank for a fused reduce; with few tokens, and
+ * with few output tiles, in up to eight runs of consecutive groups that are
+ * added in order).  A product of two scales outside fp32's range is an
+ * infinity or loses bits as in fp32 arithmetic.
+ * ---------------------------------------------------------------------
+ */
+
+/*
+ * Rows to 8 bits: x[r] [n, k] of dtype (bf16 or f32, row stride ldx) to
+ * codes[r] [n, k] (row stride ldc) and scales[r] [G, n] (row stride lds),
+ * for t matrices of one shape in one launch.
+ */
+tp_status tp_fp8_quantize(int t, int64_t n, int64_t k, tp_dtype dtype, const void* const* x, int64_t ldx,
+                          void* const* codes, int64_t ldc, float* const* scales, int64_t lds,
+                          tp_stream stream);
+
+/*
+ * Weights to 8 bits: w[r] [out, k] of dtype (row stride ldw) to codes[r]
+ * (row stride ldc) and scales[r] as above; gated 1 cuts each half of the rows
+ * into blocks by itself (out even, else TP_ERR_NOT_DIVISIBLE).
+ */
+tp_status tp_fp8_quantize_weight(int t, int64_t out, int64_t k, tp_dtype dtype, const void* const* w, int64_t ldw,
+                                 int gated, void* const* codes, int64_t ldc, float* const* scales,
+                                 tp_stream stream);
+
+/*
+ * tp_reduce_scatter_rmsnorm with the normed rows in 8 bits: the fp32 values
+ * of the norm (not rounded to bf16 between) go to codes [n, h] (row stride
+ * ldc) and scales [G, n] (row stride lds).  The other arguments, orders and
+ * limits (h <= 32768) are that call's; h % 16 == 0 and eps finite.
+ */
+tp_status tp_fp8_rmsnorm(int t, int64_t n, int64_t h, tp_dtype dtype, const void* const* partials,
+                         const void* residual, const void* weight, float eps, tp_reduce_mode mode,
+                         void* residual_out, void* codes, int64_t ldc, float* scales, int64_t lds,
+                         tp_stream stream);
+
+/*
+ * tp_linear_col on 8-bit rows and weights.  x [n, in] codes with scales xs
+ * (row stride ldxs); w[r] [out_full/t, in] codes (gated: [2*out_full/t, in])
+ * with scales ws[r].  y_kind TP_BF16 or TP_F32 as tp_linear_col's; TP_FP8
+ * (gated, not gathered) brings act(gate) * up to 8 bits before it leaves the
+ * chip: y[r] [n, out_full/t] codes (row stride ldy bytes), ys[r]
+ * [ceil(out_full/t / 128), n] scales (row stride ldys).
+ * Requires in % 16 == 0, and out_full/t % 16 == 0 for TP_FP8.
+ */
+tp_status tp_fp8_linear_col(int t, int64_t n, int64_t in, int64_t out_full, const void* x, int64_t ldx,
+                            const float* xs, int64_t ldxs, const void* const* w, int64_t ldw,
+                            const float* const* ws, const void* const* bias, tp_act act, int gather_output,
+                            void* const* y, int64_t ldy, int y_kind, float* const* ys, int64_t ldys,
+                            tp_stream stream);
+
+/*
+ * tp_linear_row on 8-bit rows and weights: x[r] [n, in_full/t] codes with
+ * scales xs[r] (row stride ldxs), w[r] [out, in_full/t] codes with scales
+ * ws[r].  The other arguments are tp_linear_row's; a FUSED call uses no
+ * partials.  Requires (in_full/t) % 16 == 0.
+ */
+tp_status tp_fp8_linear_row(int t, int64_t n, int64_t in_full, int64_t out, const void* const* x, int64_t ldx,
+                            const float* const* xs, int64_t ldxs, const void* const* w, int64_t ldw,
+                            const float* const* ws, const void* bias, int reduce_results, tp_reduce_mode mode,
+                            tp_dtype partial_dtype, void* const* partials, int64_t ldp, void* y, int64_t ldy,
+                            tp_dtype y_dtype, tp_stream stream);
+
+/*
+ * The MLP block on 8-bit rows and weights: tp_fp8_linear_col with its hidden
+ * rows in 8 bits, then tp_fp8_linear_row.  w_gate_up[r] [2f/t, h] codes
+ * (contiguous) with gated scales s_gate_up[r]; w_down[r] [h, f/t] codes (row
+ * stride ld_down) with scales s_down[r]; y [n, h] contiguous.  workspace:
+ * tp_fp8_mlp_workspace_size() bytes (hidden codes [n, f] and scales, and t
+ * partials unless FUSED; 0 for invalid arguments), 256-byte aligned,
+ * overwritten.  Requires f % t == 0, (f/t) % 16 == 0 and h % 16 == 0.
+ */
+size_t tp_fp8_mlp_workspace_size(int t, int64_t n, int64_t h, int64_t f, tp_reduce_mode mode, tp_dtype partial_dtype);
+tp_status tp_fp8_mlp_forward(int t, int64_t n, int64_t h, int64_t f, const void* x, int64_t ldx, const float* xs,
+                             int64_t ldxs, const void* const* w_gate_up, const float* const* s_gate_up,
+                             const void* const* w_down, int64_t ld_down, const float* const* s_down,
+                             const void* bias_down, tp_act act, tp_reduce_mode mode, tp_dtype partial_dtype,
+                             void* workspace, size_t workspace_bytes, void* y, tp_dtype y_dtype,
+                             tp_stream stream);
 
 /*
  * ---------------------------------------------------------------------

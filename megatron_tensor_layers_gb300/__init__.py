@@ -19,6 +19,13 @@ from ._lib import (  # noqa: F401
     tp_collective_count,
     tp_debug_expire_wait,
     tp_device_status,
+    tp_fp8_linear_col,
+    tp_fp8_linear_row,
+    tp_fp8_mlp_forward,
+    tp_fp8_mlp_workspace_size,
+    tp_fp8_quantize,
+    tp_fp8_quantize_weight,
+    tp_fp8_rmsnorm,
     tp_kv4_append,
     tp_kv4_attention,
     tp_kv4_attention_workspace_size,

@@ -38,6 +38,8 @@ EXPORTED = [
     "tp_kv4_page_bytes", "tp_kv4_append", "tp_kv4_load", "tp_kv4_attention_workspace_size", "tp_kv4_attention",
     "tp_kv_pages_workspace_size", "tp_kv_fork", "tp_kv_compact", "tp_beam_workspace_size", "tp_beam_select",
     "tp_debug_kv4_block", "tp_debug_part_flag", "tp_debug_first_worker",
+    "tp_fp8_quantize", "tp_fp8_quantize_weight", "tp_fp8_rmsnorm", "tp_fp8_linear_col", "tp_fp8_linear_row",
+    "tp_fp8_mlp_workspace_size", "tp_fp8_mlp_forward",
 ]
 STATIC_SCRATCH_BYTES = 16 * 1024 * 1024
 
@@ -100,6 +102,14 @@ def load() -> ctypes.CDLL:
                              ctypes.c_size_t, P]),
         "tp_kv_compact": (I32, [I32, I64, I64, I32, I64, P, P, P, P, I64, I64, P, P, P, P, ctypes.c_size_t, P]),
         "tp_beam_workspace_size": (ctypes.c_size_t, [I64, I32, I32, I64]),
+        "tp_fp8_quantize": (I32, [I32, I64, I64, I32, P, I64, P, I64, P, I64, P]),
+        "tp_fp8_quantize_weight": (I32, [I32, I64, I64, I32, P, I64, I32, P, I64, P, P]),
+        "tp_fp8_rmsnorm": (I32, [I32, I64, I64, I32, P, P, P, ctypes.c_float, I32, P, P, I64, P, I64, P]),
+        "tp_fp8_linear_col": (I32, [I32, I64, I64, I64, P, I64, P, I64, P, I64, P, P, I32, I32, P, I64, I32, P, I64, P]),
+        "tp_fp8_linear_row": (I32, [I32, I64, I64, I64, P, I64, P, I64, P, I64, P, P, I32, I32, I32, P, I64, P, I64, I32, P]),
+        "tp_fp8_mlp_workspace_size": (ctypes.c_size_t, [I32, I64, I64, I64, I32, I32]),
+        "tp_fp8_mlp_forward": (I32, [I32, I64, I64, I64, P, I64, P, I64, P, P, P, I64, P, P, I32, I32, I32, P,
+                                     ctypes.c_size_t, P, I32, P]),
         "tp_beam_select": (I32, [I32, I64, I32, I32, P, P, P, I32, P, P, ctypes.c_int32, P, P, P, P, ctypes.c_size_t, P]),
     }
     for name, (res, args) in sig.items():
@@ -757,6 +767,274 @@ def tp_reduce_scatter_rmsnorm(partials: Sequence[torch.Tensor], weight: torch.Te
             _ptr(weight), eps, MODES[mode], _ptr(residual_out), _ptr(out),
             _stream(stream))
     return residual_out, out
+
+
+# ----------------------------------------------------------------- layers in 8-bit floating point
+
+FP8 = torch.float8_e4m3fn
+FP8_GROUP = 128
+TP_FP8 = 2
+F32S = (torch.float32,)
+FP8S = (FP8,)
+
+
+def _groups(k: int) -> int:
+    return -(-k // FP8_GROUP)
+
+
+def _codes_buffer(shape, device) -> torch.Tensor:
+    return torch.empty(shape, dtype=FP8, device=device)
+
+
+def _row_scales(name, ss, k: int, n: int) -> int:
+    """Every ss[r] holds the scales [groups, n] of rows of k columns, with one row stride (returned; of a single
+    group, whose stride says nothing, n)."""
+    g, ld = _groups(k), None
+    for r, s in enumerate(ss):
+        _tensor((name, r), s, (g, n), F32S)
+        s0, s1 = s.stride() if g > 1 else (n, s.stride(1))
+        if (s1 != 1 and n > 1) or s0 < n:
+            raise ValueError(f"{_nm((name, r))} must be a row-major matrix with unit column stride")
+        if ld is not None and s0 != ld:
+            raise ValueError(f"every {name}[r] must have the same row stride")
+        ld = s0
+    return max(ld, n)
+
+
+def tp_fp8_quantize(x: Sequence[torch.Tensor], *, codes: Optional[Sequence[torch.Tensor]] = None,
+                    scales: Optional[Sequence[torch.Tensor]] = None, stream=None):
+    """Rows x[r] [n, k] (bf16 or fp32) to 8 bits, t matrices of one shape in one
+    launch.  Returns (codes, scales): lists of [n, k] float8_e4m3fn and
+    [ceil(k/128), n] fp32."""
+    t = _shard_count("x", x)
+    n, k = _matrix("x[0]", x[0], dtypes=BF16_F32).shape
+    ldx = _matrices("x", x, (n, k), (x[0].dtype,))
+    dev = x[0].device
+    if codes is None:
+        codes = [_codes_buffer((n, k), dev) for _ in range(t)]
+    if scales is None:
+        scales = [torch.empty((_groups(k), n), dtype=torch.float32, device=dev) for _ in range(t)]
+    if len(codes) != t or len(scales) != t:
+        raise ValueError("codes and scales must hold one tensor per matrix of x")
+    ldc = _matrices("codes", codes, (n, k), FP8S)
+    lds = _row_scales("scales", scales, k, n)
+    _on_gpu(x, codes, scales)
+    _launch("tp_fp8_quantize", t, n, k, _dt(x[0].dtype), _ptrs(x), ldx, _ptrs(codes), ldc, _ptrs(scales), lds,
+            _stream(stream))
+    return codes, scales
+
+
+def _weight_blocks(out: int, gated: bool) -> int:
+    return 2 * _groups(out // 2) if gated else _groups(out)
+
+
+def tp_fp8_quantize_weight(w: Sequence[torch.Tensor], *, gated: bool = False,
+                           codes: Optional[Sequence[torch.Tensor]] = None,
+                           scales: Optional[Sequence[torch.Tensor]] = None, stream=None):
+    """Weights w[r] [out, k] (bf16 or fp32) to 8 bits with a scale for each
+    block of 128 x 128.  gated=True: w[r] is a merged [gate; up] block, each
+    half cut into blocks by itself.  Returns (codes, scales): lists of [out, k]
+    float8_e4m3fn and [blocks, ceil(k/128)] fp32."""
+    t = _shard_count("w", w)
+    out, k = _matrix("w[0]", w[0], dtypes=BF16_F32).shape
+    ldw = _matrices("w", w, (out, k), (w[0].dtype,))
+    if gated and out % 2:
+        raise ValueError("a gated weight block holds gate rows then as many up rows: its row count must be even")
+    dev = w[0].device
+    if codes is None:
+        codes = [_codes_buffer((out, k), dev) for _ in range(t)]
+    blocks = (_weight_blocks(out, gated), _groups(k))
+    if scales is None:
+        scales = [torch.empty(blocks, dtype=torch.float32, device=dev) for _ in range(t)]
+    if len(codes) != t or len(scales) != t:
+        raise ValueError("codes and scales must hold one tensor per weight")
+    ldc = _matrices("codes", codes, (out, k), FP8S)
+    _denses("scales", scales, blocks, F32S)
+    _on_gpu(w, codes, scales)
+    _launch("tp_fp8_quantize_weight", t, out, k, _dt(w[0].dtype), _ptrs(w), ldw, int(gated), _ptrs(codes), ldc,
+            _ptrs(scales), _stream(stream))
+    return codes, scales
+
+
+def tp_fp8_rmsnorm(partials: Sequence[torch.Tensor], weight: torch.Tensor, *, residual: Optional[torch.Tensor] = None,
+                   eps: float = 1e-6, mode: str = "direct", residual_out: Optional[torch.Tensor] = None,
+                   codes: Optional[torch.Tensor] = None, scales: Optional[torch.Tensor] = None, stream=None):
+    """tp_reduce_scatter_rmsnorm with the normed rows in 8 bits: returns
+    (residual_out, codes, scales), the new residual stream [n, h] bf16, the
+    rows' codes [n, h] and their scales [ceil(h/128), n]."""
+    t = _shard_count("partials", partials)
+    p0 = _dense("partials[0]", partials[0], dtypes=BF16_F32)
+    if p0.dim() != 2:
+        raise ValueError("partials must be [n, h]")
+    n, h = p0.shape
+    _denses("partials", partials, (n, h), (p0.dtype,))
+    if mode not in ("direct", "ring"):
+        raise ValueError("mode must be 'direct' or 'ring'")
+    _dense("weight", weight, (h,), BF16)
+    if residual is not None:
+        _dense("residual", residual, (n, h), BF16)
+    dev = p0.device
+    if residual_out is None:
+        residual_out = torch.empty((n, h), dtype=torch.bfloat16, device=dev)
+    if codes is None:
+        codes = _codes_buffer((n, h), dev)
+    if scales is None:
+        scales = torch.empty((_groups(h), n), dtype=torch.float32, device=dev)
+    _dense("residual_out", residual_out, (n, h), BF16)
+    ldc = _matrices("codes", [codes], (n, h), FP8S)
+    lds = _row_scales("scales", [scales], h, n)
+    _on_gpu(partials, weight, residual, residual_out, codes, scales)
+    _launch("tp_fp8_rmsnorm", t, n, h, _dt(p0.dtype), _ptrs(partials), _ptr(residual), _ptr(weight), eps, MODES[mode],
+            _ptr(residual_out), _ptr(codes), ldc, _ptr(scales), lds, _stream(stream))
+    return residual_out, codes, scales
+
+
+def tp_fp8_linear_col(x: torch.Tensor, x_scales: torch.Tensor, w: Sequence[torch.Tensor],
+                      w_scales: Sequence[torch.Tensor], *, act: str = "none",
+                      bias: Optional[Sequence[torch.Tensor]] = None, gather_output: bool = False, y=None,
+                      y_scales: Optional[Sequence[torch.Tensor]] = None, y_dtype=torch.bfloat16, stream=None):
+    """tp_linear_col on 8-bit rows and weights.  x [n, in] codes with x_scales
+    [ceil(in/128), n]; w[r] codes with w_scales[r] (tp_fp8_quantize_weight, gated
+    with a gated act).  Returns the per-shard outputs (bf16 or fp32), or the
+    gathered tensor; with a gated act and y_dtype=torch.float8_e4m3fn the pair
+    (codes, scales) of lists: the hidden rows in 8 bits."""
+    t = _shard_count("w", w)
+    n, k = _matrix("x", x, dtypes=FP8S).shape
+    ldxs = _row_scales("x_scales", [x_scales], k, n)
+    if act not in ACTS:
+        raise ValueError(f"act must be one of {list(ACTS)}")
+    rows = w[0].shape[0] if w[0].dim() == 2 else -1
+    ldw = _matrices("w", w, (rows, k), FP8S)
+    gated = act != "none"
+    if gated and rows % 2:
+        raise ValueError("a gated weight block holds gate rows then as many up rows: its row count must be even")
+    if len(w_scales) != t:
+        raise ValueError("w_scales must hold one tensor per shard")
+    _denses("w_scales", w_scales, (_weight_blocks(rows, gated), _groups(k)), F32S)
+    os_ = rows // (2 if gated else 1)
+    out_full = os_ * t
+    if bias is not None:
+        if len(bias) != t:
+            raise ValueError("bias must hold one vector per shard")
+        _denses("bias", bias, (os_,), BF16)
+    if y is None:
+        if gather_output:
+            y = torch.empty((n, out_full), dtype=y_dtype, device=x.device)
+        else:
+            y = [torch.empty((n, os_), dtype=y_dtype, device=x.device) for _ in range(t)]
+    ys = [y] if gather_output else list(y)
+    if len(ys) != (1 if gather_output else t):
+        raise ValueError("y must be one tensor with gather_output, else one per shard")
+    ldy = _matrices("y", ys, (n, out_full if gather_output else os_), (ys[0].dtype,))
+    codes = ys[0].dtype is FP8
+    if codes and (not gated or gather_output):
+        raise ValueError("8-bit outputs are a gated act's, per shard")
+    if not codes and ys[0].dtype not in BF16_F32:
+        raise TypeError(f"y has dtype {ys[0].dtype}, expected bf16, fp32 or float8_e4m3fn")
+    if not codes and y_scales is not None:
+        raise ValueError("y_scales belong to 8-bit outputs")
+    ldys = 0
+    if codes:
+        if y_scales is None:
+            y_scales = [torch.empty((_groups(os_), n), dtype=torch.float32, device=x.device) for _ in range(t)]
+        if len(y_scales) != t:
+            raise ValueError("y_scales must hold one tensor per shard")
+        ldys = _row_scales("y_scales", y_scales, os_, n)
+    _on_gpu(x, x_scales, w, w_scales, bias, ys, y_scales)
+    _launch("tp_fp8_linear_col", t, n, k, out_full, _ptr(x), _ld(x), _ptr(x_scales), ldxs, _ptrs(w), ldw,
+            _ptrs(w_scales), _ptrs(bias), ACTS[act], int(gather_output), _ptrs(ys), ldy,
+            TP_FP8 if codes else _dt(ys[0].dtype), _ptrs(y_scales), ldys, _stream(stream))
+    return (y, y_scales) if codes else y
+
+
+def tp_fp8_linear_row(x: Sequence[torch.Tensor], x_scales: Sequence[torch.Tensor], w: Sequence[torch.Tensor],
+                      w_scales: Sequence[torch.Tensor], *, bias: Optional[torch.Tensor] = None,
+                      reduce_results: bool = True, mode: str = "direct", partial_dtype=torch.bfloat16,
+                      partials: Optional[List[torch.Tensor]] = None, y: Optional[torch.Tensor] = None,
+                      y_dtype=torch.bfloat16, stream=None):
+    """tp_linear_row on 8-bit rows and weights: x[r] [n, in/t] codes with
+    x_scales[r] [ceil(in/t/128), n], w[r] [out, in/t] codes with w_scales[r].
+    Returns y (the all-reduced sum) when reduce_results, else the partials."""
+    t = _shard_count("w", w)
+    if len(x) != t or len(x_scales) != t or len(w_scales) != t:
+        raise ValueError("x, x_scales, w and w_scales must hold the same number of shards")
+    n, ks = _matrix("x[0]", x[0], dtypes=FP8S).shape
+    out = _matrix("w[0]", w[0], dtypes=FP8S).shape[0]
+    ldx = _matrices("x", x, (n, ks), FP8S)
+    ldxs = _row_scales("x_scales", x_scales, ks, n)
+    ldw = _matrices("w", w, (out, ks), FP8S)
+    _denses("w_scales", w_scales, (_groups(out), _groups(ks)), F32S)
+    if mode not in MODES:
+        raise ValueError(f"mode must be one of {list(MODES)}")
+    if bias is not None:
+        _dense("bias", bias, (out,), BF16)
+    dev = x[0].device
+    if mode != "fused" and partials is None:
+        partials = [_scratch((n, out), partial_dtype, dev, stream) for _ in range(t)]
+    if reduce_results and y is None:
+        y = torch.empty((n, out), dtype=y_dtype, device=dev)
+    if partials is not None:
+        if len(partials) != t:
+            raise ValueError("partials must hold one buffer per shard")
+        _matrix(("partials", 0), partials[0], (n, out), BF16_F32)
+        _matrices("partials", partials, (n, out), (partials[0].dtype,))
+    if y is not None:
+        _matrix("y", y, (n, out), BF16_F32)
+    _on_gpu(x, x_scales, w, w_scales, bias, partials, y)
+    ldp = _ld(partials[0]) if partials is not None else out
+    pdt = partials[0].dtype if partials is not None else partial_dtype
+    _launch("tp_fp8_linear_row", t, n, ks * t, out, _ptrs(x), ldx, _ptrs(x_scales), ldxs, _ptrs(w), ldw,
+            _ptrs(w_scales), _ptr(bias), int(reduce_results), MODES[mode], _dt(pdt), _ptrs(partials), ldp,
+            _ptr(y), _ld(y) if y is not None else out, _dt(y.dtype) if y is not None else 0, _stream(stream))
+    return y if reduce_results else partials
+
+
+def tp_fp8_mlp_workspace_size(t: int, n: int, h: int, f: int, mode: str = "direct", partial_dtype=torch.bfloat16) -> int:
+    return load().tp_fp8_mlp_workspace_size(t, n, h, f, MODES[mode], _dt(partial_dtype))
+
+
+def tp_fp8_mlp_forward(x: torch.Tensor, x_scales: torch.Tensor, w_gate_up: Sequence[torch.Tensor],
+                       gate_up_scales: Sequence[torch.Tensor], w_down: Sequence[torch.Tensor],
+                       down_scales: Sequence[torch.Tensor], *, bias_down: Optional[torch.Tensor] = None,
+                       act: str = "silu", mode: str = "direct", partial_dtype=torch.bfloat16,
+                       workspace: Optional[torch.Tensor] = None, y: Optional[torch.Tensor] = None,
+                       y_dtype=torch.bfloat16, stream=None):
+    """tp_mlp_forward on 8-bit rows and weights, with the hidden rows in 8 bits
+    too.  x [n, h] codes with x_scales [ceil(h/128), n]; w_gate_up[r] [2f/t, h]
+    (quantised gated), w_down[r] [h, f/t] codes with their scales."""
+    t = _shard_count("w_gate_up", w_gate_up)
+    if len(gate_up_scales) != t or len(w_down) != t or len(down_scales) != t:
+        raise ValueError("weights and scales must hold the same number of shards")
+    if act not in ACTS or act == "none":
+        raise ValueError("act must be 'silu' or 'gelu_tanh' (the MLP is gated)")
+    if mode not in MODES:
+        raise ValueError(f"mode must be one of {list(MODES)}")
+    n, h = _matrix("x", x, dtypes=FP8S).shape
+    ldxs = _row_scales("x_scales", [x_scales], h, n)
+    rows = w_gate_up[0].shape[0] if w_gate_up[0].dim() == 2 else -1
+    if rows % 2:
+        raise ValueError("w_gate_up[r] holds gate rows then as many up rows: its row count must be even")
+    fs = rows // 2
+    f = fs * t
+    _denses("w_gate_up", w_gate_up, (2 * fs, h), FP8S)
+    _denses("gate_up_scales", gate_up_scales, (2 * _groups(fs), _groups(h)), F32S)
+    ldd = _matrices("w_down", w_down, (h, fs), FP8S)
+    _denses("down_scales", down_scales, (_groups(h), _groups(fs)), F32S)
+    if bias_down is not None:
+        _dense("bias_down", bias_down, (h,), BF16)
+    if workspace is None:
+        need = tp_fp8_mlp_workspace_size(t, n, h, f, mode, partial_dtype)
+        workspace = _scratch(max(need, 256), torch.uint8, x.device, stream)
+    if y is None:
+        y = torch.empty((n, h), dtype=y_dtype, device=x.device)
+    _dense("workspace", workspace)
+    _dense("y", y, (n, h), BF16_F32)
+    _on_gpu(x, x_scales, w_gate_up, gate_up_scales, w_down, down_scales, bias_down, workspace, y)
+    _launch("tp_fp8_mlp_forward", t, n, h, f, _ptr(x), _ld(x), _ptr(x_scales), ldxs, _ptrs(w_gate_up),
+            _ptrs(gate_up_scales), _ptrs(w_down), ldd, _ptrs(down_scales), _ptr(bias_down), ACTS[act], MODES[mode],
+            _dt(partial_dtype), _ptr(workspace), workspace.numel() * workspace.element_size(), _ptr(y), _dt(y.dtype),
+            _stream(stream))
+    return y
 
 
 # ----------------------------------------------------------------- decode loop: paged 4-bit cache, pages, beams

@@ -63,6 +63,7 @@ inline cudaStream_t cs(tp_stream s) { return reinterpret_cast<cudaStream_t>(s); 
 }  // namespace
 
 int* tpk::device_status_word() { return status_ptr(); }
+void tpk::count_collective() { g_collectives++; }
 
 // tp_mlp_forward's workspace: H [n, f] bf16, then (unless the reduce is
 // fused) t partials [n, h]; that much is required.  A fused reduce of more

@@ -42,6 +42,32 @@ __device__ __forceinline__ float act_fn(float g, int act) {
     return __fdividef(g, 1.0f + __expf(-g));
 }
 
+// ---------------------------------------------------------------- stores
+
+// Store four consecutive values of one output row, columns [col0, col0 + nvalid).
+__device__ __forceinline__ void store_quad(void* base, int64_t ldo, int out_f32, int64_t row, int col0, int nvalid,
+                                           const float (&v)[4]) {
+    if (out_f32) {
+        float* p = static_cast<float*>(base) + row * ldo + col0;
+        if (nvalid == 4 && (reinterpret_cast<uintptr_t>(p) & 15) == 0) {
+            *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (e < nvalid) p[e] = v[e];
+        }
+    } else {
+        uint16_t* p = static_cast<uint16_t*>(base) + row * ldo + col0;
+        if (nvalid == 4 && (reinterpret_cast<uintptr_t>(p) & 7) == 0) {
+            *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
+        } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (e < nvalid) p[e] = f32_to_bf16(v[e]);
+        }
+    }
+}
+
 // ---------------------------------------------------------------- timers
 
 __device__ __forceinline__ uint64_t global_ns() {

@@ -1,0 +1,503 @@
+// Products of 8-bit rows and 8-bit weights on the 5th-generation tensor core:
+//
+//     y_ij = sum_g  s_x[g, i] * s_w[j / 128, g] * sum_{k in group g} x_ik w_jk
+//
+// with e4m3 codes x [n, K] and w [out, K], one fp32 scale for each row's group
+// of 128 columns and each 128 x 128 block of the weight.  The codes' products
+// are exact and the tensor core adds those of one group (one K block of 128)
+// into a TMEM accumulator of its own; the epilogue warps read each block's
+// accumulator, multiply it by the two scales' product and add it to fp32
+// sums in their registers, so scales may be any fp32 numbers.
+//
+// Launches are programmatic (PDL): weights are loaded before the previous
+// kernel's end only when that kernel belongs to the same call and writes none.
+// Every wait is bounded (1 s) and reports TP_ERR_TIMEOUT.
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <atomic>
+#include <cstdint>
+#include <cstring>
+
+#include "fp8.cuh"
+#include "kernels.h"
+
+namespace tpk {
+
+struct Fp8GemmArgs {
+    CUtensorMap mapX[TP_MAX_SHARDS];
+    CUtensorMap mapW[TP_MAX_SHARDS];
+    const float* xs[TP_MAX_SHARDS];
+    const float* ws[TP_MAX_SHARDS];
+    void* out[TP_MAX_SHARDS];
+    float* os[TP_MAX_SHARDS];
+    const uint16_t* bias[TP_MAX_SHARDS];
+    int64_t ldxs, ldo, ldos;
+    int M, N;             // tokens, output columns per group
+    int k_blocks;         // K blocks of a segment (= the row pitch of a weight's scales)
+    int segs, groups, x_per_group;
+    int up_block;         // first block row of up in a gated weight's scales
+    int m_tiles, n_tiles, total_tiles;
+    int x_box_rows;       // rows of a token tile that a copy brings
+    int act, out_kind;
+    int split;            // CTAs of a cluster that share a tile's K blocks
+    int weights_first;
+    int* status;
+};
+
+// Instruction descriptor of tcgen05.mma kind::f8f6f4 with e4m3 A and B (format
+// 0), f32 accumulator, both operands K-major.
+__host__ __device__ constexpr uint32_t mma_idesc_e4m3(int m, int n) {
+    return (1u << 4) | (static_cast<uint32_t>(n >> 3) << 17) | (static_cast<uint32_t>(m >> 4) << 24);
+}
+
+__device__ __forceinline__ void tc_mma_f8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                          uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+// Each thread of the warp reads 16 consecutive 32-bit columns of its own TMEM lane.
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, float (&r)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+        : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]), "=f"(r[7]), "=f"(r[8]),
+          "=f"(r[9]), "=f"(r[10]), "=f"(r[11]), "=f"(r[12]), "=f"(r[13]), "=f"(r[14]), "=f"(r[15])
+        : "r"(taddr)
+        : "memory");
+}
+
+// ------------------------------------------------------- weights as the rows of the MMA
+//
+// Few tokens: the MMA's M = 128 rows are 128 output columns (a block row of
+// the weight's scales) and its N columns are NT tokens, so that a K block's
+// accumulator holds NT values a lane instead of 128 mostly unused rows.
+// A cluster of `split` CTAs shares an output tile: CTA r runs K blocks
+// [r KB / split, (r + 1) KB / split) and stages its sums in its shared memory,
+// and the cluster's epilogue warps take one token each, add the CTAs' sums in
+// rank order (over distributed shared memory) and store it; the 128 columns
+// of a token's tile are one warp's, which for a gated tile is also the group
+// of the 8-bit hidden row.
+//
+// Roles: warp 0 brings tiles (TMA), warp 1 multiplies, warps 2.. add up: of a
+// gated tile four warps the gate's columns and four up's, of a plain one each
+// warp all NT columns, or half of 128.
+template <int NT, bool GLU>
+struct FewCfg {
+    static constexpr int W_BYTES = (GLU ? 2 : 1) * 128 * 128;
+    static constexpr int X_BYTES = NT * 128;
+    static constexpr int STAGE_BYTES = W_BYTES + X_BYTES;
+    static constexpr bool ONE = NT > 64;                       // CTAs per SM: one, else two
+    static constexpr int BUDGET = (ONE ? 216 : 108) * 1024;
+    static constexpr int STAGES = BUDGET / STAGE_BYTES;
+    static constexpr int STAGING_BYTES = (GLU ? 2 : 1) * NT * 128 * 4;
+    static constexpr int EPI_WARPS = (GLU || NT > 64) ? 8 : 4;
+    static constexpr int NC = (!GLU && NT > 64) ? NT / 2 : NT; // columns of a warp
+    static constexpr int ACC_COLS = NT * (GLU ? 2 : 1);        // TMEM columns of one K block
+    static constexpr int BUFS = (ONE ? 512 : 256) / ACC_COLS > 4 ? 4 : (ONE ? 512 : 256) / ACC_COLS;
+    static constexpr int TMEM_COLS = ACC_COLS * BUFS;
+    static constexpr int THREADS = 64 + 32 * EPI_WARPS;
+    static constexpr int NBARS = 2 * STAGES + 2 * BUFS;
+    static constexpr int SCALE_BYTES = EPI_WARPS * 2 * NC * 4; // a warp's token scales, twice
+    static constexpr int SMEM_BYTES = 1024 + STAGES * STAGE_BYTES + SCALE_BYTES + NBARS * 8 + 16;
+    static_assert(STAGES >= 2 && BUFS >= 2, "both pipelines need two slots");
+    static_assert(STAGES * STAGE_BYTES >= STAGING_BYTES, "the sums are staged in the ring");
+    static_assert(STAGE_BYTES % 1024 == 0 && W_BYTES % 1024 == 0, "swizzled tiles are 1024-byte aligned");
+    static_assert((TMEM_COLS & (TMEM_COLS - 1)) == 0 && TMEM_COLS >= 32 && TMEM_COLS <= 512, "TMEM columns");
+    static_assert(NT % 16 == 0 && NC % 16 == 0, "MMA N, and chunks of 16 columns");
+    static_assert(SMEM_BYTES <= (ONE ? 227 : 113) * 1024, "shared memory");
+};
+
+template <int NT, bool GLU>
+__global__ void __launch_bounds__(FewCfg<NT, GLU>::THREADS, FewCfg<NT, GLU>::ONE ? 1 : 2)
+    fp8_few_kernel(const __grid_constant__ Fp8GemmArgs args) {
+    using Cfg = FewCfg<NT, GLU>;
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw_addr = smem_u32(smem_raw);
+    const uint32_t base = (raw_addr + 1023u) & ~1023u;
+    uint8_t* base_ptr = smem_raw + (base - raw_addr);
+    float* scales_ptr = reinterpret_cast<float*>(base_ptr + Cfg::STAGES * Cfg::STAGE_BYTES);
+    constexpr int kBarOff = Cfg::STAGES * Cfg::STAGE_BYTES + Cfg::SCALE_BYTES;
+    const uint32_t bar_base = base + kBarOff;
+    auto full_bar = [&](int s) { return bar_base + 8u * s; };
+    auto empty_bar = [&](int s) { return bar_base + 8u * (Cfg::STAGES + s); };
+    auto tfull_bar = [&](int b) { return bar_base + 8u * (2 * Cfg::STAGES + b); };
+    auto tempty_bar = [&](int b) { return bar_base + 8u * (2 * Cfg::STAGES + Cfg::BUFS + b); };
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(base_ptr + kBarOff + 8 * Cfg::NBARS);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(base_ptr + kBarOff + 8 * Cfg::NBARS + 4);
+
+    const int warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31;
+    const int split = args.split;
+    const int crank = split > 1 ? static_cast<int>(cluster_ctarank()) : 0;
+    // tile: token tiles fastest, so that a weight's block is read by neighbours in time
+    const int tile = static_cast<int>(blockIdx.x) / split;
+    const int m = tile % args.m_tiles;
+    const int n = (tile / args.m_tiles) % args.n_tiles;
+    const int g = tile / (args.m_tiles * args.n_tiles);
+    const int kb_all = args.k_blocks * args.segs;
+    const int kb_lo = static_cast<int>(static_cast<int64_t>(crank) * kb_all / split);
+    const int kb_hi = static_cast<int>(static_cast<int64_t>(crank + 1) * kb_all / split);
+    const int token0 = m * NT;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < Cfg::STAGES; ++s) {
+            mbar_init(full_bar(s), 1);
+            mbar_init(empty_bar(s), 1);
+        }
+        for (int b = 0; b < Cfg::BUFS; ++b) {
+            mbar_init(tfull_bar(b), 1);
+            mbar_init(tempty_bar(b), Cfg::EPI_WARPS);
+        }
+        *abort_flag = 0;
+        fence_barrier_init();
+    }
+    if (warp == 1) tmem_alloc<Cfg::TMEM_COLS>(smem_u32(tmem_slot));
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem_base = *tmem_slot;
+    if (threadIdx.x == 0) pdl_trigger();
+    bool aborted = false;
+
+    if (warp == 0) {
+        if (lane == 0) {
+            // ------------------------------------------------ TMA producer
+            const uint32_t bytes = Cfg::W_BYTES + static_cast<uint32_t>(args.x_box_rows) * 128u;
+            int seg = kb_lo / args.k_blocks, kb = kb_lo - seg * args.k_blocks;
+            auto load_w = [&](int s, int seg, int kb) {
+                const int wi = args.segs > 1 ? seg : g;
+                const uint32_t sw = base + s * Cfg::STAGE_BYTES;
+                tma_load_2d(sw, &args.mapW[wi], full_bar(s), kb * 128, n * 128);
+                if (GLU) tma_load_2d(sw + 128 * 128, &args.mapW[wi], full_bar(s), kb * 128, args.N + n * 128);
+            };
+            auto load_x = [&](int s, int seg, int kb) {
+                const int xi = args.segs > 1 ? seg : (args.x_per_group ? g : 0);
+                tma_load_2d(base + s * Cfg::STAGE_BYTES + Cfg::W_BYTES, &args.mapX[xi], full_bar(s), kb * 128, token0);
+            };
+            int pre = 0;
+            if (args.weights_first) {          // the first ring of weights before the previous kernel's end
+                int sg = seg, k = kb;
+                pre = min(Cfg::STAGES, kb_hi - kb_lo);
+                for (int s = 0; s < pre; ++s) {
+                    mbar_arrive_expect_tx(full_bar(s), bytes);
+                    load_w(s, sg, k);
+                    if (++k == args.k_blocks) {
+                        k = 0;
+                        ++sg;
+                    }
+                }
+            }
+            pdl_wait();
+            int s = 0;
+            uint32_t phase = 0;
+            for (int i = 0; i < kb_hi - kb_lo; ++i) {
+                if (i >= pre) {
+                    if (!mbar_wait(empty_bar(s), phase ^ 1u, abort_flag, args.status)) {
+                        aborted = true;
+                        break;
+                    }
+                    mbar_arrive_expect_tx(full_bar(s), bytes);
+                    load_w(s, seg, kb);
+                }
+                load_x(s, seg, kb);
+                if (++kb == args.k_blocks) {
+                    kb = 0;
+                    ++seg;
+                }
+                if (++s == Cfg::STAGES) {
+                    s = 0;
+                    phase ^= 1u;
+                }
+            }
+        }
+    } else if (warp == 1) {
+        if (lane == 0) {
+            // ------------------------------------------------ MMA issuer
+            constexpr uint32_t idesc = mma_idesc_e4m3(128, NT);
+            int s = 0, b = 0;
+            uint32_t phase = 0, bphase = 0;
+            for (int i = kb_lo; i < kb_hi; ++i) {
+                if (!mbar_wait(tempty_bar(b), bphase ^ 1u, abort_flag, args.status) ||
+                    !mbar_wait(full_bar(s), phase, abort_flag, args.status)) {
+                    aborted = true;
+                    break;
+                }
+                tc_fence_after();
+                const uint32_t d = tmem_base + static_cast<uint32_t>(b * Cfg::ACC_COLS);
+                const uint32_t sw = base + s * Cfg::STAGE_BYTES;
+                const uint64_t wdesc = sw128_kmajor_desc(sw);
+                const uint64_t xdesc = sw128_kmajor_desc(sw + Cfg::W_BYTES);
+#pragma unroll
+                for (int k = 0; k < 4; ++k)      // 32 codes along K: 32 bytes inside the swizzle row
+                    tc_mma_f8(d, wdesc + 2u * k, xdesc + 2u * k, idesc, k != 0 ? 1u : 0u);
+                if (GLU) {
+                    const uint64_t udesc = sw128_kmajor_desc(sw + 128 * 128);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        tc_mma_f8(d + NT, udesc + 2u * k, xdesc + 2u * k, idesc, k != 0 ? 1u : 0u);
+                }
+                tc_commit(empty_bar(s));
+                tc_commit(tfull_bar(b));
+                if (++s == Cfg::STAGES) {
+                    s = 0;
+                    phase ^= 1u;
+                }
+                if (++b == Cfg::BUFS) {
+                    b = 0;
+                    bphase ^= 1u;
+                }
+            }
+        }
+    } else {
+        // ---------------------------------------------------- scaled sums
+        const int e = warp - 2;
+        const int q = warp & 3;                  // TMEM lane quarter this warp may access
+        const int part = e >> 2;                 // gated: 0 gate, 1 up; plain: which half of the columns
+        const int col0 = GLU ? 0 : part * Cfg::NC;
+        float* sc = scales_ptr + e * 2 * Cfg::NC;
+        constexpr int PRE = (Cfg::NC + 31) / 32;
+        float acc[Cfg::NC];
+#pragma unroll
+        for (int j = 0; j < Cfg::NC; ++j) acc[j] = 0.0f;
+        pdl_wait();                              // the rows' scales may be the previous kernel's output
+        const int wb = n + (GLU && part ? args.up_block : 0);
+        float pre[PRE], wpre = 0.0f;
+        int seg = kb_lo / args.k_blocks, kb = kb_lo - seg * args.k_blocks;
+        auto fetch = [&]() {
+            const float* xs = args.xs[args.segs > 1 ? seg : (args.x_per_group ? g : 0)] + static_cast<int64_t>(kb) * args.ldxs;
+            wpre = args.ws[args.segs > 1 ? seg : g][static_cast<int64_t>(wb) * args.k_blocks + kb];
+#pragma unroll
+            for (int i = 0; i < PRE; ++i) {
+                const int tok = token0 + col0 + i * 32 + lane;
+                pre[i] = (i * 32 + lane < Cfg::NC && tok < args.M) ? xs[tok] : 0.0f;
+            }
+            if (++kb == args.k_blocks) {
+                kb = 0;
+                ++seg;
+            }
+        };
+        if (kb_lo < kb_hi) fetch();
+        int b = 0;
+        uint32_t bphase = 0;
+        const uint32_t lane_base = tmem_base + (static_cast<uint32_t>(q * 32) << 16);
+        for (int i = kb_lo; i < kb_hi; ++i) {
+            float* s = sc + (i & 1) * Cfg::NC;
+#pragma unroll
+            for (int p = 0; p < PRE; ++p)
+                if (p * 32 + lane < Cfg::NC) s[p * 32 + lane] = pre[p] * wpre;
+            if (i + 1 < kb_hi) fetch();
+            __syncwarp();
+            if (!mbar_wait_warp(tfull_bar(b), bphase, abort_flag, args.status)) {
+                aborted = true;
+                break;
+            }
+            tc_fence_after();
+            const uint32_t taddr = lane_base + static_cast<uint32_t>(b * Cfg::ACC_COLS + (GLU ? part * NT : col0));
+#pragma unroll
+            for (int c = 0; c < Cfg::NC / 16; ++c) {
+                float d[16];
+                tmem_ld16(taddr + c * 16, d);
+                tmem_ld_wait();
+                if (c == Cfg::NC / 16 - 1) {     // all of this block is read: its columns are free again
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(tempty_bar(b));
+                }
+#pragma unroll
+                for (int j = 0; j < 16; j += 4) {
+                    const float4 f = *reinterpret_cast<const float4*>(s + c * 16 + j);
+                    acc[c * 16 + j] = fmaf(d[j], f.x, acc[c * 16 + j]);
+                    acc[c * 16 + j + 1] = fmaf(d[j + 1], f.y, acc[c * 16 + j + 1]);
+                    acc[c * 16 + j + 2] = fmaf(d[j + 2], f.z, acc[c * 16 + j + 2]);
+                    acc[c * 16 + j + 3] = fmaf(d[j + 3], f.w, acc[c * 16 + j + 3]);
+                }
+            }
+            if (++b == Cfg::BUFS) {
+                b = 0;
+                bphase ^= 1u;
+            }
+        }
+        // Stage the sums [gate/up][token][128 columns] in the ring: the last block's products
+        // have been waited for, so nothing reads or writes it any more.
+        if (!aborted) {
+            float* st = reinterpret_cast<float*>(base_ptr) + ((GLU ? part * NT : 0) + col0) * 128 + q * 32 + lane;
+#pragma unroll
+            for (int j = 0; j < Cfg::NC; ++j) st[j * 128] = acc[j];
+        }
+    }
+
+    if (aborted) spin_ns(50000);        // let issued copies and products land
+    __syncwarp();
+    tc_fence_before();
+    if (split > 1)
+        cluster_sync();
+    else
+        __syncthreads();
+    if (warp >= 2 && *abort_flag == 0) {
+        const int e = warp - 2;
+        const int tokens = min(NT, args.M - token0);
+        const int col = n * 128 + lane * 4;
+        const int nvalid = args.N - col;                     // this lane's columns inside the group
+        auto sum = [&](int part, int j) {
+            const uint32_t off = base + static_cast<uint32_t>(((part * NT + j) * 128 + lane * 4) * 4);
+            if (split == 1) {
+                float4 v;
+                asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(off) : "memory");
+                return v;
+            }
+            float4 x[8];
+#pragma unroll
+            for (int p = 0; p < 8; ++p)
+                if (p < split) x[p] = ld_shared_cluster_f4(mapa_shared(off, static_cast<uint32_t>(p)));
+            float4 v = x[0];
+#pragma unroll
+            for (int p = 1; p < 8; ++p) {
+                if (p < split) {
+                    v.x += x[p].x;
+                    v.y += x[p].y;
+                    v.z += x[p].z;
+                    v.w += x[p].w;
+                }
+            }
+            return v;
+        };
+        float bias[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        if (!GLU && args.bias[g] != nullptr) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (i < nvalid) bias[i] = bf16_to_f32(args.bias[g][col + i]);
+        }
+        for (int j = crank * Cfg::EPI_WARPS + e; j < tokens; j += split * Cfg::EPI_WARPS) {
+            const float4 a = sum(0, j);
+            float v[4] = {a.x, a.y, a.z, a.w};
+            const int64_t row = token0 + j;
+            if (GLU) {
+                const float4 u = sum(1, j);
+                v[0] = act_fn(v[0], args.act) * u.x;
+                v[1] = act_fn(v[1], args.act) * u.y;
+                v[2] = act_fn(v[2], args.act) * u.z;
+                v[3] = act_fn(v[3], args.act) * u.w;
+                if (args.out_kind == FP8_OUT_CODES) {
+                    float top = 0.0f;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) top = i < nvalid ? max_nan(top, fabsf(v[i])) : top;
+#pragma unroll
+                    for (int o = 16; o > 0; o >>= 1) top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, o));
+                    const float s = fp8_scale(top);
+                    if (nvalid > 0)
+                        *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(args.out[g]) + row * args.ldo + col) =
+                            fp8_codes4(v[0], v[1], v[2], v[3], s);
+                    if (lane == 0) args.os[g][static_cast<int64_t>(n) * args.ldos + row] = s;
+                    continue;
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) v[i] += bias[i];
+            }
+            if (nvalid > 0)
+                store_quad(args.out[g], args.ldo, args.out_kind == FP8_OUT_F32, row, col, min(4, nvalid), v);
+        }
+    }
+    __syncwarp();
+    if (split > 1) cluster_sync_relaxed();      // a peer may still read this CTA's sums
+    else __syncthreads();
+    if (*abort_flag) spin_ns(50000);
+    if (warp == 1) {
+        __syncwarp();
+        tc_fence_after();
+        tmem_dealloc<Cfg::TMEM_COLS>(tmem_base);
+    }
+}
+
+// ------------------------------------------------------------------ host
+
+template <int NT, bool GLU>
+static tp_status launch_few(Fp8GemmArgs& a, const Fp8GemmDesc& d, cudaStream_t stream) {
+    using Cfg = FewCfg<NT, GLU>;
+    a.m_tiles = static_cast<int>((d.M + NT - 1) / NT);
+    a.n_tiles = static_cast<int>((d.N + 127) / 128);
+    const int64_t tiles = static_cast<int64_t>(d.groups) * a.m_tiles * a.n_tiles;
+    const int sms = device_sms();
+    if (sms <= 0) return TP_ERR_CUDA;
+    // CTAs that share a tile: as many as still find an SM of their own
+    const int kb_all = a.k_blocks * d.segs;
+    int split = 1;
+    while (split < 8 && tiles * split * 2 <= sms * (Cfg::ONE ? 1 : 2) && kb_all / (split * 2) >= 2) split *= 2;
+    if (tiles * split > INT32_MAX) return TP_ERR_UNSUPPORTED;
+    a.total_tiles = static_cast<int>(tiles);
+    a.split = split;
+    a.x_box_rows = static_cast<int>(std::min<int64_t>(NT, (d.M + 7) / 8 * 8));
+    const int nX = d.segs > 1 ? d.segs : (d.x_per_group ? d.groups : 1);
+    const int nW = d.segs > 1 ? d.segs : d.groups;
+    for (int i = 0; i < nX; ++i)
+        if (!make_byte_operand_map(&a.mapX[i], d.x[i], d.M, d.K, d.ldx, a.x_box_rows)) return TP_ERR_CUDA;
+    for (int i = 0; i < nW; ++i)
+        if (!make_byte_operand_map(&a.mapW[i], d.w[i], GLU ? 2 * d.N : d.N, d.K, d.ldw, 128)) return TP_ERR_CUDA;
+    auto kern = fp8_few_kernel<NT, GLU>;
+    static std::atomic<uint64_t> smem_set{0};
+    if (!smem_attribute_once(reinterpret_cast<const void*>(kern), Cfg::SMEM_BYTES, smem_set)) return TP_ERR_CUDA;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(tiles * split), 1, 1);
+    cfg.blockDim = dim3(Cfg::THREADS, 1, 1);
+    cfg.dynamicSmemBytes = Cfg::SMEM_BYTES;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = static_cast<unsigned>(split);
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = split > 1 ? 2 : 1;
+    if (cudaLaunchKernelEx(&cfg, kern, a) != cudaSuccess) return TP_ERR_CUDA;
+    return cudaGetLastError() == cudaSuccess ? TP_OK : TP_ERR_CUDA;
+}
+
+tp_status launch_fp8_gemm(const Fp8GemmDesc& d, cudaStream_t stream) {
+    if (d.M == 0 || d.N == 0) return TP_OK;
+    Fp8GemmArgs a;
+    std::memset(&a, 0, sizeof(a));
+    for (int i = 0; i < TP_MAX_SHARDS; ++i) {
+        a.xs[i] = d.xs[i];
+        a.ws[i] = d.ws[i];
+        a.out[i] = d.out[i];
+        a.os[i] = d.os[i];
+        a.bias[i] = static_cast<const uint16_t*>(d.bias[i]);
+    }
+    a.ldxs = d.ldxs;
+    a.ldo = d.ldo;
+    a.ldos = d.ldos;
+    a.M = static_cast<int>(d.M);
+    a.N = static_cast<int>(d.N);
+    a.k_blocks = static_cast<int>(fp8_groups(d.K));
+    a.segs = d.segs;
+    a.groups = d.groups;
+    a.x_per_group = d.x_per_group;
+    a.up_block = static_cast<int>(fp8_groups(d.N));
+    a.act = d.act;
+    a.out_kind = d.out_kind;
+    a.status = d.status;
+    a.weights_first = d.weights_first;
+    if (static_cast<int64_t>(d.groups) * ((d.M + 127) / 128) * ((d.N + 127) / 128) > INT32_MAX / 8) return TP_ERR_UNSUPPORTED;
+    if (d.glu) {
+        if (d.M <= 16) return launch_few<16, true>(a, d, stream);
+        if (d.M <= 32) return launch_few<32, true>(a, d, stream);
+        if (d.M <= 64) return launch_few<64, true>(a, d, stream);
+        return launch_few<128, true>(a, d, stream);
+    }
+    if (d.M <= 16) return launch_few<16, false>(a, d, stream);
+    if (d.M <= 32) return launch_few<32, false>(a, d, stream);
+    if (d.M <= 64) return launch_few<64, false>(a, d, stream);
+    return launch_few<128, false>(a, d, stream);
+}
+
+}  // namespace tpk

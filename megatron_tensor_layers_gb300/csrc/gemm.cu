@@ -1067,30 +1067,6 @@ __device__ __forceinline__ float4 gather_f4(uint32_t staging, int f4col, int row
     return v;
 }
 
-// Store four consecutive values of one output row, columns [col0, col0 + nvalid).
-__device__ __forceinline__ void store_quad(void* base, int64_t ldo, int out_f32, int64_t row, int col0, int nvalid,
-                                           const float (&v)[4]) {
-    if (out_f32) {
-        float* p = static_cast<float*>(base) + row * ldo + col0;
-        if (nvalid == 4 && (reinterpret_cast<uintptr_t>(p) & 15) == 0) {
-            *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
-        } else {
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-                if (e < nvalid) p[e] = v[e];
-        }
-    } else {
-        uint16_t* p = static_cast<uint16_t*>(base) + row * ldo + col0;
-        if (nvalid == 4 && (reinterpret_cast<uintptr_t>(p) & 7) == 0) {
-            *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
-        } else {
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-                if (e < nvalid) p[e] = f32_to_bf16(v[e]);
-        }
-    }
-}
-
 template <int BN, int STAGES, int EPI, int KSUB, int ROWS>
 __global__ void __launch_bounds__(kThreads, 1) tp_gemm_splitk_kernel(const __grid_constant__ GemmArgs args) {
     using Cfg = SplitCfg<BN, STAGES, EPI, ROWS>;
@@ -1435,8 +1411,9 @@ struct MapKey {
     uint64_t strides[3];
     uint32_t box[4];
     uint32_t rank;
+    uint32_t type;                            // CUtensorMapDataType
     bool operator==(const MapKey& o) const {
-        if (ptr != o.ptr || rank != o.rank) return false;
+        if (ptr != o.ptr || rank != o.rank || type != o.type) return false;
         for (int i = 0; i < 4; ++i)
             if (dims[i] != o.dims[i] || box[i] != o.box[i]) return false;
         for (int i = 0; i < 3; ++i)
@@ -1457,19 +1434,22 @@ static MapEntry& map_slot(const MapKey& k) {
     for (uint64_t v : {k.dims[0], k.dims[1], k.dims[2], k.dims[3], k.strides[0], k.strides[1], k.strides[2],
                        static_cast<uint64_t>(k.box[0]) | static_cast<uint64_t>(k.box[1]) << 16 |
                            static_cast<uint64_t>(k.box[2]) << 32 | static_cast<uint64_t>(k.box[3]) << 48,
-                       static_cast<uint64_t>(k.rank)})
+                       static_cast<uint64_t>(k.rank) | static_cast<uint64_t>(k.type) << 32})
         h = (h ^ v) * 0x100000001B3ull;
     return cache[(h >> 32) % kMapCacheSlots];
 }
 
-// Encode (or copy from the cache) one bf16 tensor map of rank 2 to 4 with
-// 128-byte swizzle and the given box (innermost first).
+// Encode (or copy from the cache) one tensor map of rank 2 to 4 with 128-byte
+// swizzle and the given box (innermost first); bf16 elements unless told
+// otherwise.
 static bool encode_map_box(CUtensorMap* m, const void* ptr, uint32_t rank, const cuuint64_t* dims,
-                           const cuuint64_t* strides, const cuuint32_t* box) {
+                           const cuuint64_t* strides, const cuuint32_t* box,
+                           CUtensorMapDataType type = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16) {
     if (rank < 2 || rank > 4) return false;
     MapKey k = {};
     k.ptr = ptr;
     k.rank = rank;
+    k.type = static_cast<uint32_t>(type);
     for (uint32_t i = 0; i < rank; ++i) {
         k.dims[i] = dims[i];
         k.box[i] = box[i];
@@ -1484,7 +1464,7 @@ static bool encode_map_box(CUtensorMap* m, const void* ptr, uint32_t rank, const
     if (enc == nullptr) return false;
     cuuint32_t bx[4] = {box[0], box[1], rank > 2 ? box[2] : 1u, rank > 3 ? box[3] : 1u};
     cuuint32_t estr[4] = {1, 1, 1, 1};
-    CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<void*>(ptr), dims, strides, bx, estr,
+    CUresult r = enc(m, type, rank, const_cast<void*>(ptr), dims, strides, bx, estr,
                      CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     if (r != CUDA_SUCCESS) return false;
@@ -1570,6 +1550,13 @@ bool make_operand_map(CUtensorMap* m, const void* ptr, int64_t rows, int64_t col
 bool make_gated_operand_map(CUtensorMap* m, const void* ptr, int64_t half_rows, int64_t cols, int64_t ld,
                             int box_rows) {
     return make_map_glu(m, ptr, half_rows, cols, ld, box_rows);
+}
+
+bool make_byte_operand_map(CUtensorMap* m, const void* ptr, int64_t rows, int64_t cols, int64_t ld, int box_rows) {
+    const cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
+    const cuuint64_t strides[1] = {static_cast<cuuint64_t>(ld)};
+    const cuuint32_t box[2] = {128, static_cast<cuuint32_t>(box_rows)};
+    return encode_map_box(m, ptr, 2, dims, strides, box, CU_TENSOR_MAP_DATA_TYPE_UINT8);
 }
 
 bool make_kblock_map(CUtensorMap* m, const void* ptr, int64_t rows, int64_t k, int64_t ld, int box_rows,

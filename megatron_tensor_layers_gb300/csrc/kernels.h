@@ -72,6 +72,8 @@ tp_status launch_gemm(const GemmDesc& d, cudaStream_t stream);
 bool make_operand_map(CUtensorMap* m, const void* ptr, int64_t rows, int64_t cols, int64_t ld, int box_rows);
 bool make_gated_operand_map(CUtensorMap* m, const void* ptr, int64_t half_rows, int64_t cols, int64_t ld,
                             int box_rows);
+// The same for 8-bit operands: boxes 128 elements (along K) by box_rows rows.
+bool make_byte_operand_map(CUtensorMap* m, const void* ptr, int64_t rows, int64_t cols, int64_t ld, int box_rows);
 // K-block views, for loading several K blocks with one copy: [rows, k] (row
 // stride ld, k a multiple of 64) seen as {64, rows, k/64} with the K-block
 // stride (128 bytes) below the row stride, so that one box {64, box_rows,
@@ -342,8 +344,78 @@ struct BeamDesc {
 size_t beam_workspace(int64_t items, int beams, int k, int64_t vocab);
 tp_status launch_beam_select(const BeamDesc& d, cudaStream_t stream);
 
+// ---------------------------------------------------------------- 8-bit floating point
+// Codes are e4m3; a row's scales lie [groups][rows] (row stride ld), a group is
+// kFp8Group columns; a weight's scales lie [blocks of kFp8Group rows][groups].
+constexpr int kFp8Group = 128;
+inline int64_t fp8_groups(int64_t k) { return (k + kFp8Group - 1) / kFp8Group; }
+
+// Rows (or, with weight, blocks) of t matrices [n, k] brought to 8 bits.
+struct Fp8QuantDesc {
+    int t = 0;
+    int64_t n = 0, k = 0;
+    int in_f32 = 0;
+    int weight = 0;
+    int64_t half = 0;                    // weight: rows of the first part that is cut into blocks by itself (0: none)
+    const void* x[TP_MAX_SHARDS] = {};
+    int64_t ldx = 0;
+    void* codes[TP_MAX_SHARDS] = {};
+    int64_t ldc = 0;
+    float* scales[TP_MAX_SHARDS] = {};
+    int64_t lds = 0;
+};
+tp_status launch_fp8_quant(const Fp8QuantDesc& d, cudaStream_t stream);
+
+// SeqParDesc's sum, residual and norm with the normed row in 8 bits.
+struct Fp8NormDesc {
+    int t = 0;
+    int64_t n = 0, h = 0;
+    int in_bf16 = 0;
+    const void* p[TP_MAX_SHARDS] = {};
+    const void* residual = nullptr;
+    const void* weight = nullptr;
+    float eps = 0.0f;
+    int ring = 0;
+    void* residual_out = nullptr;
+    void* codes = nullptr;
+    int64_t ldc = 0;
+    float* scales = nullptr;
+    int64_t lds = 0;
+};
+tp_status launch_fp8_norm(const Fp8NormDesc& d, cudaStream_t stream);
+
+// D_g = sum_s X_{g,s} W_{g,s}^T of 8-bit operands (GemmDesc's groups and
+// segments), each K block of 128 scaled by its row's and its weight block's
+// scale.
+enum { FP8_OUT_BF16 = 0, FP8_OUT_F32 = 1, FP8_OUT_CODES = 2 };
+struct Fp8GemmDesc {
+    int64_t M = 0, N = 0, K = 0;         // tokens, output columns per group, K of a segment
+    int groups = 1, segs = 1;
+    int x_per_group = 0;
+    const void* x[TP_MAX_SHARDS] = {};
+    int64_t ldx = 0;
+    const float* xs[TP_MAX_SHARDS] = {};
+    int64_t ldxs = 0;
+    const void* w[TP_MAX_SHARDS] = {};
+    int64_t ldw = 0;
+    const float* ws[TP_MAX_SHARDS] = {}; // [blocks][fp8_groups(K)]
+    int glu = 0;                         // w = [gate rows; up rows], N rows each
+    int act = TP_ACT_NONE;
+    int out_kind = FP8_OUT_BF16;
+    void* out[TP_MAX_SHARDS] = {};
+    int64_t ldo = 0;                     // elements
+    float* os[TP_MAX_SHARDS] = {};       // FP8_OUT_CODES: scales [fp8_groups(N)][ldos]
+    int64_t ldos = 0;
+    const void* bias[TP_MAX_SHARDS] = {};
+    int* status = nullptr;
+    int weights_first = 0;               // 1: the previous kernel is of the same call and writes no weight
+};
+tp_status launch_fp8_gemm(const Fp8GemmDesc& d, cudaStream_t stream);
+
 // Device address of the library's status word on the current device (null on failure).
 int* device_status_word();
+// Counts one simulated collective (tp_collective_count).
+void count_collective();
 // Streaming multiprocessors of the current device, looked up once per device (0 on failure).
 int device_sms();
 
