@@ -41,7 +41,8 @@ struct Fp8GemmArgs {
     int m_tiles, n_tiles, total_tiles;
     int x_box_rows;       // rows of a token tile that a copy brings
     int act, out_kind;
-    int split;            // CTAs of a cluster that share a tile's K blocks
+    int split;            // CTAs (many rows: CTA pairs) of a cluster that share a tile's K blocks
+    int band;             // many rows: row tiles of a raster band
     int weights_first;
     int* status;
 };
@@ -71,6 +72,32 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, float (&r)[16]) {
           "=f"(r[9]), "=f"(r[10]), "=f"(r[11]), "=f"(r[12]), "=f"(r[13]), "=f"(r[14]), "=f"(r[15])
         : "r"(taddr)
         : "memory");
+}
+
+// Four neighbouring columns (lane * 4 of the warp's 128) of one row of a gated
+// tile: act(gate) * up, stored, or brought to 8 bits with the row's group in
+// the warp.
+__device__ __forceinline__ void finish_gated(const Fp8GemmArgs& args, int g, int n, int64_t row, int lane,
+                                             const float (&gate)[4], const float (&up)[4]) {
+    const int col = n * 128 + lane * 4;
+    const int nvalid = args.N - col;                     // this lane's columns inside the group
+    float v[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = act_fn(gate[i], args.act) * up[i];
+    if (args.out_kind == FP8_OUT_CODES) {
+        float top = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) top = i < nvalid ? max_nan(top, fabsf(v[i])) : top;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, o));
+        const float s = fp8_scale(top);
+        if (nvalid > 0)                                  // N is a multiple of 16: all four or none
+            *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(args.out[g]) + row * args.ldo + col) =
+                fp8_codes4(v[0], v[1], v[2], v[3], s);
+        if (lane == 0) args.os[g][static_cast<int64_t>(n) * args.ldos + row] = s;
+    } else if (nvalid > 0) {
+        store_quad(args.out[g], args.ldo, args.out_kind == FP8_OUT_F32, row, col, min(4, nvalid), v);
+    }
 }
 
 // ------------------------------------------------------- weights as the rows of the MMA
@@ -381,23 +408,9 @@ __global__ void __launch_bounds__(FewCfg<NT, GLU>::THREADS, FewCfg<NT, GLU>::ONE
             const int64_t row = token0 + j;
             if (GLU) {
                 const float4 u = sum(1, j);
-                v[0] = act_fn(v[0], args.act) * u.x;
-                v[1] = act_fn(v[1], args.act) * u.y;
-                v[2] = act_fn(v[2], args.act) * u.z;
-                v[3] = act_fn(v[3], args.act) * u.w;
-                if (args.out_kind == FP8_OUT_CODES) {
-                    float top = 0.0f;
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) top = i < nvalid ? max_nan(top, fabsf(v[i])) : top;
-#pragma unroll
-                    for (int o = 16; o > 0; o >>= 1) top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, o));
-                    const float s = fp8_scale(top);
-                    if (nvalid > 0)
-                        *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(args.out[g]) + row * args.ldo + col) =
-                            fp8_codes4(v[0], v[1], v[2], v[3], s);
-                    if (lane == 0) args.os[g][static_cast<int64_t>(n) * args.ldos + row] = s;
-                    continue;
-                }
+                const float up[4] = {u.x, u.y, u.z, u.w};
+                finish_gated(args, g, n, row, lane, v, up);
+                continue;
             } else {
 #pragma unroll
                 for (int i = 0; i < 4; ++i) v[i] += bias[i];
@@ -414,6 +427,475 @@ __global__ void __launch_bounds__(FewCfg<NT, GLU>::THREADS, FewCfg<NT, GLU>::ONE
         __syncwarp();
         tc_fence_after();
         tmem_dealloc<Cfg::TMEM_COLS>(tmem_base);
+    }
+}
+
+// ------------------------------------------------------- many tokens: CTA pairs
+//
+// 256 x 256 tiles of a cluster of two CTAs on neighbouring SMs (cta_group::2),
+// tokens as the MMA's rows: CTA r of a pair brings rows [128 r, 128 r + 128) of
+// the tile's tokens and the r-th 128 rows of its weights (gated: CTA 0 gate's, CTA
+// 1 the same rows of up), and the even CTA issues one M = 256, N = 256 MMA for
+// both.  Every K block of 128 goes to one of two TMEM accumulators; eight
+// epilogue warps a CTA read it (a thread one token's 128 columns), scale it
+// and add it to 128 fp32 sums a thread, while the MMA fills the other one: the
+// read and the multiply-adds of a block (256 + 256 cycles a quarter of the
+// SM) fit the 512 cycles of its MMAs.  With tokens as rows a thread needs
+// one token's scale a block and one product with each weight block's;
+// weights as rows would need one for every column.
+//
+// split > 1: a cluster of `split` pairs shares a tile's K blocks in runs; the
+// pairs' sums meet in shared memory (the ring, idle by then) and CTA p of
+// each row half finishes its share of the rows, summing in the pairs' order.
+constexpr int kManyStages = 6;
+constexpr int kManyThreads = 320;
+
+struct ManyCfg {
+    static constexpr int STAGE_BYTES = 2 * 128 * 128;
+    static constexpr int STG_PITCH = 80;                     // 64 bytes of a row and a pad: no bank conflicts
+    static constexpr int STG_BYTES = 8 * 32 * STG_PITCH;
+    static constexpr int AMAX_BYTES = 2 * 2 * 128 * 4;       // two halves' largest values, two tiles in turn
+    static constexpr int NBARS = 2 * kManyStages + 4 + 4;
+    static constexpr int SUM_PITCH = 260;                    // floats of a staged row of sums
+    static constexpr int SMEM_BYTES = 1024 + kManyStages * STAGE_BYTES + STG_BYTES + AMAX_BYTES + NBARS * 8 + 16;
+    static_assert(SMEM_BYTES <= 227 * 1024, "shared memory per CTA");
+    static_assert(128 * SUM_PITCH * 4 <= kManyStages * STAGE_BYTES, "a CTA's sums fit the ring");
+};
+
+__device__ __forceinline__ void tc_mma_f8_pair(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                               uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+// Two fp32 multiply-adds in one instruction.
+__device__ __forceinline__ void fma2(float& a0, float& a1, float d0, float d1, float s) {
+    asm("{\n\t.reg .b64 a, d, s;\n\t"
+        "mov.b64 a, {%0, %1};\n\t"
+        "mov.b64 d, {%2, %3};\n\t"
+        "mov.b64 s, {%4, %4};\n\t"
+        "fma.rn.f32x2 a, d, s, a;\n\t"
+        "mov.b64 {%0, %1}, a;\n\t}"
+        : "+f"(a0), "+f"(a1)
+        : "f"(d0), "f"(d1), "f"(s));
+}
+
+// Tile index -> (group, row tile, column tile): bands of row tiles, the row
+// tile fastest inside a band; with shared rows a band covers every group's columns.
+__device__ __forceinline__ void many_coords(const Fp8GemmArgs& a, int tile, int& g, int& m, int& n) {
+    const int cols = a.x_per_group ? a.n_tiles : a.groups * a.n_tiles;
+    const int per_span = a.m_tiles * cols;
+    const int outer = tile / per_span;
+    const int l = tile - outer * per_span;
+    const int band = l / (a.band * cols);
+    const int first = band * a.band;
+    const int gm = min(a.m_tiles - first, a.band);
+    const int r = l - band * a.band * cols;
+    m = first + r % gm;
+    const int col = r / gm;
+    g = a.x_per_group ? outer : col / a.n_tiles;
+    n = a.x_per_group ? col : col - g * a.n_tiles;
+}
+
+// A warp writes its rows' 64-byte pieces of an output (rows row0 .. row0 + live - 1, byte offset off of a row): each
+// lane's piece is staged at lane * STG_PITCH.  Whole pieces of aligned rows go out as 16-byte stores of 8 rows at a
+// time, others element by element.
+template <int ES>
+__device__ __forceinline__ void many_store(const uint8_t* st, uint8_t* out, int64_t row0, int live, int64_t pitch,
+                                           int64_t off, int valid_bytes, int lane) {
+    __syncwarp();
+    if (valid_bytes >= 64 && ((reinterpret_cast<uintptr_t>(out) + off) & 15) == 0 && (pitch & 15) == 0) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int r = i * 8 + (lane >> 2);
+            if (r < live)
+                *reinterpret_cast<uint4*>(out + (row0 + r) * pitch + off + (lane & 3) * 16) =
+                    *reinterpret_cast<const uint4*>(st + r * ManyCfg::STG_PITCH + (lane & 3) * 16);
+        }
+    } else {
+        constexpr int PER = 64 / ES;
+        for (int i = lane; i < live * PER; i += 32) {
+            const int r = i / PER, b = (i % PER) * ES;
+            if (b < valid_bytes) {
+                uint8_t* dst = out + (row0 + r) * pitch + off + b;
+                const uint8_t* src = st + r * ManyCfg::STG_PITCH + b;
+                if constexpr (ES == 4)
+                    *reinterpret_cast<uint32_t*>(dst) = *reinterpret_cast<const uint32_t*>(src);
+                else if constexpr (ES == 2)
+                    *reinterpret_cast<uint16_t*>(dst) = *reinterpret_cast<const uint16_t*>(src);
+                else
+                    *dst = *src;
+            }
+        }
+    }
+    __syncwarp();
+}
+
+template <bool GLU>
+__global__ void __launch_bounds__(kManyThreads, 1) fp8_many_kernel(const __grid_constant__ Fp8GemmArgs args) {
+    using Cfg = ManyCfg;
+    constexpr int STAGES = kManyStages;
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw_addr = smem_u32(smem_raw);
+    const uint32_t base = (raw_addr + 1023u) & ~1023u;
+    uint8_t* base_ptr = smem_raw + (base - raw_addr);
+    constexpr int kStgOff = STAGES * Cfg::STAGE_BYTES;
+    constexpr int kAmaxOff = kStgOff + Cfg::STG_BYTES;
+    constexpr int kBarOff = kAmaxOff + Cfg::AMAX_BYTES;
+    const uint32_t bar_base = base + kBarOff;
+    auto full_bar = [&](int s) { return bar_base + 8u * s; };
+    auto empty_bar = [&](int s) { return bar_base + 8u * (STAGES + s); };
+    auto tfull_bar = [&](int b) { return bar_base + 8u * (2 * STAGES + b); };
+    auto tempty_bar = [&](int b) { return bar_base + 8u * (2 * STAGES + 2 + b); };
+    auto half_bar = [&](int q) { return bar_base + 8u * (2 * STAGES + 4 + q); };   // the two warps of a lane quarter
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(base_ptr + kBarOff + 8 * Cfg::NBARS);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(base_ptr + kBarOff + 8 * Cfg::NBARS + 4);
+
+    const int warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31;
+    const int split = args.split;
+    const uint32_t crank = cluster_ctarank();
+    const uint32_t rank = crank & 1;                     // 0: issues the pair's MMAs
+    const uint32_t leader = crank & ~1u;
+    const int part = static_cast<int>(crank >> 1);
+    const uint16_t pair_mask = static_cast<uint16_t>(0x3u << leader);
+    const int cluster = static_cast<int>(blockIdx.x) / (2 * split);
+    const int nclusters = static_cast<int>(gridDim.x) / (2 * split);
+    const int kb_all = args.k_blocks * args.segs;
+    const int kb_lo = static_cast<int>(static_cast<int64_t>(part) * kb_all / split);
+    const int kb_hi = static_cast<int>(static_cast<int64_t>(part + 1) * kb_all / split);
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < STAGES; ++s) {
+            mbar_init(full_bar(s), 1);
+            mbar_init(empty_bar(s), 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(tfull_bar(b), 1);
+            mbar_init(tempty_bar(b), 16);                // eight epilogue warps of each CTA
+        }
+        for (int q = 0; q < 4; ++q) mbar_init(half_bar(q), 2);
+        *abort_flag = 0;
+        fence_barrier_init();
+    }
+    if (warp == 1) tmem_alloc_pair<512>(smem_u32(tmem_slot));
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();                                      // the peer's barriers exist before any remote use
+    tc_fence_after();
+    const uint32_t tmem_base = *tmem_slot;
+    if (threadIdx.x == 0) pdl_trigger();
+    bool aborted = false;
+
+    if (warp == 0) {
+        if (lane == 0) {
+            // ------------------------------------------------ TMA producer (both CTAs)
+            pdl_wait();
+            int s = 0;
+            uint32_t phase = 0;
+            for (int tile = cluster; tile < args.total_tiles && !aborted; tile += nclusters) {
+                int g, m, n;
+                many_coords(args, tile, g, m, n);
+                const int x_row = m * 256 + static_cast<int>(rank) * 128;
+                const int w_row = GLU ? (rank == 0 ? n * 128 : args.N + n * 128) : n * 256 + static_cast<int>(rank) * 128;
+                int seg = kb_lo / args.k_blocks, kb = kb_lo - seg * args.k_blocks;
+                for (int i = kb_lo; i < kb_hi; ++i) {
+                    if (!mbar_wait(empty_bar(s), phase ^ 1u, abort_flag, args.status)) {
+                        aborted = true;
+                        break;
+                    }
+                    if (rank == 0) mbar_arrive_expect_tx(full_bar(s), 2u * Cfg::STAGE_BYTES);
+                    const uint32_t full = mapa_shared(full_bar(s), leader);
+                    const int xi = args.segs > 1 ? seg : (args.x_per_group ? g : 0);
+                    const uint32_t sx = base + s * Cfg::STAGE_BYTES;
+                    tma_load_2d_pair(sx, &args.mapX[xi], full, kb * 128, x_row);
+                    tma_load_2d_pair(sx + 128 * 128, &args.mapW[args.segs > 1 ? seg : g], full, kb * 128, w_row);
+                    if (++kb == args.k_blocks) {
+                        kb = 0;
+                        ++seg;
+                    }
+                    if (++s == STAGES) {
+                        s = 0;
+                        phase ^= 1u;
+                    }
+                }
+            }
+        }
+    } else if (warp == 1) {
+        if (lane == 0 && rank == 0) {
+            // ------------------------------------------------ MMA issuer (even CTA)
+            constexpr uint32_t idesc = mma_idesc_e4m3(256, 256);
+            int s = 0, b = 0;
+            uint32_t phase = 0, bphase = 0;
+            for (int tile = cluster; tile < args.total_tiles && !aborted; tile += nclusters) {
+                for (int i = kb_lo; i < kb_hi; ++i) {
+                    if (!mbar_wait(full_bar(s), phase, abort_flag, args.status) ||
+                        !mbar_wait(tempty_bar(b), bphase ^ 1u, abort_flag, args.status)) {
+                        aborted = true;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint32_t sx = base + s * Cfg::STAGE_BYTES;
+                    const uint64_t xdesc = sw128_kmajor_desc(sx);
+                    const uint64_t wdesc = sw128_kmajor_desc(sx + 128 * 128);
+                    const uint32_t d = tmem_base + static_cast<uint32_t>(b * 256);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        tc_mma_f8_pair(d, xdesc + 2u * k, wdesc + 2u * k, idesc, k != 0 ? 1u : 0u);
+                    tc_commit_pair(empty_bar(s), pair_mask);
+                    tc_commit_pair(tfull_bar(b), pair_mask);
+                    if (++s == STAGES) {
+                        s = 0;
+                        phase ^= 1u;
+                    }
+                    b ^= 1;
+                    if (b == 0) bphase ^= 1u;
+                }
+            }
+        }
+    } else {
+        // ---------------------------------------------------- scaled sums and output (both CTAs)
+        const int q = warp & 3;
+        const int half = (warp - 2) >> 2;                 // plain: columns [128 half, +128); gated: [64 half, +64) of gate and of up
+        const int row_in_tile = static_cast<int>(rank) * 128 + q * 32 + lane;
+        uint8_t* st = base_ptr + kStgOff + (warp - 2) * 32 * Cfg::STG_PITCH;
+        uint8_t* st_lane = st + lane * Cfg::STG_PITCH;
+        float* amax = reinterpret_cast<float*>(base_ptr + kAmaxOff) + q * 32 + lane;
+        const uint32_t lane_base = tmem_base + (static_cast<uint32_t>(q * 32) << 16);
+        const uint32_t col_a = GLU ? half * 64 : half * 128;            // TMEM columns of sums 0..63
+        const uint32_t col_b = GLU ? 128 + half * 64 : half * 128 + 64; // and of 64..127
+        pdl_wait();                                       // the rows' scales may be the previous kernel's output
+        int b = 0, turn = 0;
+        uint32_t bphase = 0, hphase = 0;
+        for (int tile = cluster; tile < args.total_tiles && !aborted; tile += nclusters) {
+            int g, m, n;
+            many_coords(args, tile, g, m, n);
+            const int64_t row = static_cast<int64_t>(m) * 256 + row_in_tile;
+            const bool row_ok = row < args.M;
+            const int wb_a = GLU ? n : n * 2 + half, wb_b = GLU ? args.up_block + n : wb_a;
+            // a column tile's second weight block may not exist: then its scales are not read
+            const bool wb_ok = GLU || wb_a * 128 < args.N;
+            float acc[128];
+#pragma unroll
+            for (int j = 0; j < 128; ++j) acc[j] = 0.0f;
+            int seg = kb_lo / args.k_blocks, kb = kb_lo - seg * args.k_blocks, left = kb_hi - kb_lo;
+            float px[2], pa[2], pb[2];                    // scales of the next two K blocks
+            auto fetch = [&](int i) {
+                px[i] = pa[i] = pb[i] = 0.0f;
+                if (left > 0) {
+                    const float* xs = args.xs[args.segs > 1 ? seg : (args.x_per_group ? g : 0)];
+                    const float* ws = args.ws[args.segs > 1 ? seg : g];
+                    if (row_ok) px[i] = xs[static_cast<int64_t>(kb) * args.ldxs + row];
+                    if (wb_ok) pa[i] = ws[static_cast<int64_t>(wb_a) * args.k_blocks + kb];
+                    if (GLU) pb[i] = ws[static_cast<int64_t>(wb_b) * args.k_blocks + kb];
+                    --left;
+                    if (++kb == args.k_blocks) {
+                        kb = 0;
+                        ++seg;
+                    }
+                }
+            };
+            fetch(0);
+            fetch(1);
+            for (int i = kb_lo; i < kb_hi; ++i) {
+                const float sa = px[0] * pa[0], sb = GLU ? px[0] * pb[0] : sa;
+                px[0] = px[1];
+                pa[0] = pa[1];
+                pb[0] = pb[1];
+                fetch(1);
+                if (!mbar_wait_warp(tfull_bar(b), bphase, abort_flag, args.status)) {
+                    aborted = true;
+                    break;
+                }
+                tc_fence_after();
+                const uint32_t taddr = lane_base + static_cast<uint32_t>(b * 256);
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    float d[32];
+                    tmem_ld16(taddr + (c < 2 ? col_a : col_b) + (c & 1) * 32, *reinterpret_cast<float(*)[16]>(&d[0]));
+                    tmem_ld16(taddr + (c < 2 ? col_a : col_b) + (c & 1) * 32 + 16, *reinterpret_cast<float(*)[16]>(&d[16]));
+                    tmem_ld_wait();
+                    if (c == 3) {                         // the accumulator is read: the MMA may have it again
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive_cluster_relaxed(mapa_shared(tempty_bar(b), leader));
+                    }
+                    const float s = c < 2 ? sa : sb;
+#pragma unroll
+                    for (int j = 0; j < 32; j += 2) fma2(acc[c * 32 + j], acc[c * 32 + j + 1], d[j], d[j + 1], s);
+                }
+                b ^= 1;
+                if (b == 0) bphase ^= 1u;
+            }
+            if (aborted) break;
+            const int64_t row0 = static_cast<int64_t>(m) * 256 + static_cast<int64_t>(rank) * 128 + q * 32;
+            const int live = static_cast<int>(min(static_cast<int64_t>(32), args.M - row0));   // rows of this warp
+            if (split > 1) {
+                // this CTA's sums to the ring, a row of 256 at SUM_PITCH; joined below
+                float* sums = reinterpret_cast<float*>(base_ptr) + (q * 32 + lane) * Cfg::SUM_PITCH;
+#pragma unroll
+                for (int j = 0; j < 128; j += 4)
+                    *reinterpret_cast<float4*>(sums + (j < 64 ? col_a + j : col_b + j - 64)) =
+                        make_float4(acc[j], acc[j + 1], acc[j + 2], acc[j + 3]);
+            } else if (GLU) {
+                uint8_t* out = static_cast<uint8_t*>(args.out[g]);
+                const int col0 = n * 128 + half * 64;
+                const int valid = args.N - col0;          // columns of this half inside the group
+#pragma unroll
+                for (int j = 0; j < 64; ++j) acc[j] = act_fn(row_ok ? acc[j] : 0.0f, args.act) * acc[64 + j];
+                if (args.out_kind == FP8_OUT_CODES) {
+                    float top = 0.0f;
+#pragma unroll
+                    for (int j = 0; j < 64; ++j) top = j < valid ? max_nan(top, fabsf(acc[j])) : top;
+                    float* mine = amax + turn * 256;
+                    mine[half * 128] = top;
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(half_bar(q));
+                    if (!mbar_wait_warp(half_bar(q), hphase, abort_flag, args.status)) {
+                        aborted = true;
+                        break;
+                    }
+                    hphase ^= 1u;
+                    const float s = fp8_scale(max_nan(mine[0], mine[128]));
+                    turn ^= 1;
+                    if (half == 0 && row_ok) args.os[g][static_cast<int64_t>(n) * args.ldos + row] = s;
+                    if (live > 0 && valid > 0) {
+#pragma unroll
+                        for (int j = 0; j < 64; j += 16)
+                            *reinterpret_cast<uint4*>(st_lane + j) =
+                                make_uint4(fp8_codes4(acc[j], acc[j + 1], acc[j + 2], acc[j + 3], s),
+                                           fp8_codes4(acc[j + 4], acc[j + 5], acc[j + 6], acc[j + 7], s),
+                                           fp8_codes4(acc[j + 8], acc[j + 9], acc[j + 10], acc[j + 11], s),
+                                           fp8_codes4(acc[j + 12], acc[j + 13], acc[j + 14], acc[j + 15], s));
+                        many_store<1>(st, out, row0, live, args.ldo, col0, valid, lane);
+                    }
+                } else if (live > 0 && valid > 0) {
+                    if (args.out_kind == FP8_OUT_F32) {
+#pragma unroll
+                        for (int c = 0; c < 64; c += 16) {
+#pragma unroll
+                            for (int j = 0; j < 16; j += 4)
+                                *reinterpret_cast<float4*>(st_lane + j * 4) =
+                                    make_float4(acc[c + j], acc[c + j + 1], acc[c + j + 2], acc[c + j + 3]);
+                            many_store<4>(st, out, row0, live, args.ldo * 4, (col0 + c) * 4LL, (valid - c) * 4, lane);
+                        }
+                    } else {
+#pragma unroll
+                        for (int c = 0; c < 64; c += 32) {
+#pragma unroll
+                            for (int j = 0; j < 32; j += 8)
+                                *reinterpret_cast<uint4*>(st_lane + j * 2) =
+                                    make_uint4(pack_bf16x2(acc[c + j], acc[c + j + 1]), pack_bf16x2(acc[c + j + 2], acc[c + j + 3]),
+                                               pack_bf16x2(acc[c + j + 4], acc[c + j + 5]), pack_bf16x2(acc[c + j + 6], acc[c + j + 7]));
+                            many_store<2>(st, out, row0, live, args.ldo * 2, (col0 + c) * 2LL, (valid - c) * 2, lane);
+                        }
+                    }
+                }
+            } else {
+                uint8_t* out = static_cast<uint8_t*>(args.out[g]);
+                const int col0 = n * 256 + half * 128;
+                const int valid = args.N - col0;
+                if (live > 0 && valid > 0) {
+                    const uint16_t* bias = args.bias[g];
+                    if (bias != nullptr) {
+#pragma unroll
+                        for (int j = 0; j < 128; ++j)
+                            if (j < valid) acc[j] += bf16_to_f32(bias[col0 + j]);
+                    }
+                    if (args.out_kind == FP8_OUT_F32) {
+#pragma unroll
+                        for (int c = 0; c < 128; c += 16) {
+#pragma unroll
+                            for (int j = 0; j < 16; j += 4)
+                                *reinterpret_cast<float4*>(st_lane + j * 4) =
+                                    make_float4(acc[c + j], acc[c + j + 1], acc[c + j + 2], acc[c + j + 3]);
+                            many_store<4>(st, out, row0, live, args.ldo * 4, (col0 + c) * 4LL, (valid - c) * 4, lane);
+                        }
+                    } else {
+#pragma unroll
+                        for (int c = 0; c < 128; c += 32) {
+#pragma unroll
+                            for (int j = 0; j < 32; j += 8)
+                                *reinterpret_cast<uint4*>(st_lane + j * 2) =
+                                    make_uint4(pack_bf16x2(acc[c + j], acc[c + j + 1]), pack_bf16x2(acc[c + j + 2], acc[c + j + 3]),
+                                               pack_bf16x2(acc[c + j + 4], acc[c + j + 5]), pack_bf16x2(acc[c + j + 6], acc[c + j + 7]));
+                            many_store<2>(st, out, row0, live, args.ldo * 2, (col0 + c) * 2LL, (valid - c) * 2, lane);
+                        }
+                    }
+                }
+            }
+        }
+    }
+
+    if (aborted) spin_ns(50000);
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    if (*abort_flag) spin_ns(50000);
+    cluster_sync();                                      // no MMA or remote arrive still targets the peer; sums are staged
+    if (split > 1) {
+        // Rows [part * 128 / split, ...) of this CTA's 128: a warp a row, a lane columns [4 lane, +4) of both halves.
+        if (warp >= 2 && *abort_flag == 0) {
+            int g, m, n;
+            many_coords(args, cluster, g, m, n);         // one tile a cluster
+            const int per = 128 / split;
+            for (int r = part * per + warp - 2; r < (part + 1) * per; r += 8) {
+                const int64_t row = static_cast<int64_t>(m) * 256 + static_cast<int64_t>(rank) * 128 + r;
+                if (row >= args.M) break;
+                float v[2][4];
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const uint32_t off = base + static_cast<uint32_t>((r * Cfg::SUM_PITCH + h * 128 + lane * 4) * 4);
+                    float4 x[4];
+#pragma unroll
+                    for (int p = 0; p < 4; ++p)
+                        if (p < split) x[p] = ld_shared_cluster_f4(mapa_shared(off, static_cast<uint32_t>(2 * p) + rank));
+                    float4 a = x[0];
+#pragma unroll
+                    for (int p = 1; p < 4; ++p) {
+                        if (p < split) {
+                            a.x += x[p].x;
+                            a.y += x[p].y;
+                            a.z += x[p].z;
+                            a.w += x[p].w;
+                        }
+                    }
+                    v[h][0] = a.x;
+                    v[h][1] = a.y;
+                    v[h][2] = a.z;
+                    v[h][3] = a.w;
+                }
+                if (GLU) {
+                    finish_gated(args, g, n, row, lane, v[0], v[1]);
+                } else {
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const int col = n * 256 + h * 128 + lane * 4;
+                        const int nvalid = args.N - col;
+                        if (nvalid > 0) {
+                            if (args.bias[g] != nullptr) {
+#pragma unroll
+                                for (int i = 0; i < 4; ++i)
+                                    if (i < nvalid) v[h][i] += bf16_to_f32(args.bias[g][col + i]);
+                            }
+                            store_quad(args.out[g], args.ldo, args.out_kind == FP8_OUT_F32, row, col, min(4, nvalid), v[h]);
+                        }
+                    }
+                }
+            }
+        }
+        __syncwarp();
+        cluster_sync_relaxed();                          // a peer may still read this CTA's sums
+    }
+    if (warp == 1) {
+        __syncwarp();
+        tc_fence_after();
+        tmem_dealloc_pair<512>(tmem_base);
     }
 }
 
@@ -462,6 +944,87 @@ static tp_status launch_few(Fp8GemmArgs& a, const Fp8GemmDesc& d, cudaStream_t s
     return cudaGetLastError() == cudaSuccess ? TP_OK : TP_ERR_CUDA;
 }
 
+// CTA pairs: 256 x 256 tiles.  The K blocks of a tile are split over 1, 2 or 4 pairs, whichever takes the least:
+// waves of tiles times a part's K blocks and what a tile costs beside them.
+constexpr int kManyTileCost = 8;        // K blocks' worth: filling the pipeline and the output of a tile
+constexpr int kManyJoinCost = 6;        // and of joining the parts
+
+template <bool GLU>
+static tp_status launch_many(Fp8GemmArgs& a, const Fp8GemmDesc& d, cudaStream_t stream) {
+    using Cfg = ManyCfg;
+    const int out_cols = GLU ? 128 : 256;
+    a.m_tiles = static_cast<int>((d.M + 255) / 256);
+    a.n_tiles = static_cast<int>((d.N + out_cols - 1) / out_cols);
+    const int64_t tiles = static_cast<int64_t>(d.groups) * a.m_tiles * a.n_tiles;
+    a.total_tiles = static_cast<int>(tiles);
+    a.x_box_rows = 128;
+    // a band's rows stay in L2 while its columns of weights stream past: about 48 MB of them
+    a.band = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(a.m_tiles, (int64_t(48) << 20) / (256 * d.K * d.segs))));
+    const int nX = d.segs > 1 ? d.segs : (d.x_per_group ? d.groups : 1);
+    const int nW = d.segs > 1 ? d.segs : d.groups;
+    for (int i = 0; i < nX; ++i)
+        if (!make_byte_operand_map(&a.mapX[i], d.x[i], d.M, d.K, d.ldx, 128)) return TP_ERR_CUDA;
+    for (int i = 0; i < nW; ++i)
+        if (!make_byte_operand_map(&a.mapW[i], d.w[i], GLU ? 2 * d.N : d.N, d.K, d.ldw, 128)) return TP_ERR_CUDA;
+    auto kern = fp8_many_kernel<GLU>;
+    static std::atomic<uint64_t> smem_set{0};
+    if (!smem_attribute_once(reinterpret_cast<const void*>(kern), Cfg::SMEM_BYTES, smem_set)) return TP_ERR_CUDA;
+    const int sms = device_sms();
+    if (sms < 2) return TP_ERR_CUDA;
+    cudaLaunchConfig_t cfg = {};
+    cfg.blockDim = dim3(kManyThreads, 1, 1);
+    cfg.dynamicSmemBytes = Cfg::SMEM_BYTES;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    // clusters of 2, 4 and 8 CTAs that can be resident at once (per device)
+    static std::atomic<int> resident[64][3];             // relaxed: racing first calls store the same value
+    int dev = 0;
+    cudaGetDevice(&dev);
+    const bool cached = dev >= 0 && dev < 64;
+    const int kb_all = a.k_blocks * d.segs;
+    int best_split = 1, best_clusters = 0;
+    int64_t best = -1;
+    for (int i = 0; i < 3; ++i) {
+        const int split = 1 << i;
+        if (split > 1 && kb_all / split < 4) break;
+        int mc = cached ? resident[dev][i].load(std::memory_order_relaxed) : 0;
+        if (mc <= 0) {
+            attr[0].val.clusterDim.x = static_cast<unsigned>(2 * split);
+            cfg.numAttrs = 1;
+            cfg.gridDim = dim3(static_cast<unsigned>(sms / (2 * split) * 2 * split), 1, 1);
+            int v = 0;
+            if (cudaOccupancyMaxActiveClusters(&v, kern, &cfg) != cudaSuccess || v <= 0) {
+                if (split == 1) return TP_ERR_CUDA;
+                break;
+            }
+            mc = std::min(v, sms / (2 * split));
+            if (cached) resident[dev][i].store(mc, std::memory_order_relaxed);
+        }
+        const int64_t waves = (tiles + mc - 1) / mc;
+        const int64_t cost = waves * ((kb_all + split - 1) / split + kManyTileCost + (split > 1 ? kManyJoinCost : 0));
+        if (best < 0 || cost < best) {
+            best = cost;
+            best_split = split;
+            best_clusters = mc;
+        }
+    }
+    if (tiles * best_split > INT32_MAX / 2) return TP_ERR_UNSUPPORTED;
+    a.split = best_split;
+    // one pair a tile: a persistent grid; parts: a cluster a tile
+    const int64_t clusters = best_split == 1 ? std::min<int64_t>(tiles, best_clusters) : tiles;
+    attr[0].val.clusterDim.x = static_cast<unsigned>(2 * best_split);
+    cfg.gridDim = dim3(static_cast<unsigned>(clusters * 2 * best_split), 1, 1);
+    cfg.numAttrs = 2;
+    if (cudaLaunchKernelEx(&cfg, kern, a) != cudaSuccess) return TP_ERR_CUDA;
+    return cudaGetLastError() == cudaSuccess ? TP_OK : TP_ERR_CUDA;
+}
+
 tp_status launch_fp8_gemm(const Fp8GemmDesc& d, cudaStream_t stream) {
     if (d.M == 0 || d.N == 0) return TP_OK;
     Fp8GemmArgs a;
@@ -488,6 +1051,7 @@ tp_status launch_fp8_gemm(const Fp8GemmDesc& d, cudaStream_t stream) {
     a.status = d.status;
     a.weights_first = d.weights_first;
     if (static_cast<int64_t>(d.groups) * ((d.M + 127) / 128) * ((d.N + 127) / 128) > INT32_MAX / 8) return TP_ERR_UNSUPPORTED;
+    if (d.M > 128) return d.glu ? launch_many<true>(a, d, stream) : launch_many<false>(a, d, stream);
     if (d.glu) {
         if (d.M <= 16) return launch_few<16, true>(a, d, stream);
         if (d.M <= 32) return launch_few<32, true>(a, d, stream);

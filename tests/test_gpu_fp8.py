@@ -183,6 +183,22 @@ def test_col(n, t, k, out, dtype):
         check(y[r], *P.product([x64], [P.weight64(*ws[r])], bias[r]))
 
 
+@pytest.mark.parametrize("n", [1, 20, 100, 130, 256, 300])
+@pytest.mark.parametrize("t,k,out", [(1, 4096, 128), (4, 2064, 520), (8, 1040, 1024)])
+def test_long_sums_in_parts(n, t, k, out):
+    """Few output tiles and long sums: the K blocks are cut over a cluster."""
+    xs = [quantised(n, k, n + r) for r in range(t)]
+    ws = [weights(out, k, 200 + r) for r in range(t)]
+    y = tp.tp_fp8_linear_row([x.to(DEV) for x, _ in xs], [s.to(DEV) for _, s in xs], [w.to(DEV) for w, _ in ws],
+                             [s.to(DEV) for _, s in ws], mode="fused", y_dtype=torch.float32)
+    check(y, *P.product([P.rows64(*x) for x in xs], [P.weight64(*w) for w in ws]))
+    x, s = xs[0]
+    gw, gs = weights(2 * 272, k, 300, True)
+    c, cs = tp.tp_fp8_linear_col(x.to(DEV), s.to(DEV), [gw.to(DEV)], [gs.to(DEV)], act="silu", y_dtype=FP8)
+    v, e = P.gated(P.rows64(x, s), *P.halves64(gw, gs), "silu")
+    assert ((P.rows64(c[0], cs[0]) - v).abs() <= P.held(v, e, cs[0])).all()
+
+
 @pytest.mark.parametrize("n", NS)
 @pytest.mark.parametrize("t,k,out", [(1, 48, 200), (4, 272, 1000), (8, 128, 64)])
 def test_row_modes(n, t, k, out):
