@@ -63,8 +63,10 @@ __device__ __forceinline__ void tc_mma_f8(uint32_t d_tmem, uint64_t a_desc, uint
         : "memory");
 }
 
-// Each thread of the warp reads 16 consecutive 32-bit columns of its own TMEM lane.
-__device__ __forceinline__ void tmem_ld16(uint32_t taddr, float (&r)[16]) {
+// Each thread of the warp reads 16 or 32 consecutive 32-bit columns of its own
+// TMEM lane.  The values are there after tmem_wait on the same array, which
+// the compiler sees as writing them, so that no use moves before it.
+__device__ __forceinline__ void tmem_ld(uint32_t taddr, float (&r)[16]) {
     asm volatile(
         "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
         "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
@@ -72,6 +74,36 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, float (&r)[16]) {
           "=f"(r[9]), "=f"(r[10]), "=f"(r[11]), "=f"(r[12]), "=f"(r[13]), "=f"(r[14]), "=f"(r[15])
         : "r"(taddr)
         : "memory");
+}
+__device__ __forceinline__ void tmem_wait(float (&r)[16]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+f"(r[0]), "+f"(r[1]), "+f"(r[2]), "+f"(r[3]), "+f"(r[4]), "+f"(r[5]), "+f"(r[6]), "+f"(r[7]),
+                   "+f"(r[8]), "+f"(r[9]), "+f"(r[10]), "+f"(r[11]), "+f"(r[12]), "+f"(r[13]), "+f"(r[14]), "+f"(r[15])
+                 :
+                 : "memory");
+}
+__device__ __forceinline__ void tmem_ld(uint32_t taddr, float (&r)[32]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+        : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]), "=f"(r[7]), "=f"(r[8]),
+          "=f"(r[9]), "=f"(r[10]), "=f"(r[11]), "=f"(r[12]), "=f"(r[13]), "=f"(r[14]), "=f"(r[15]), "=f"(r[16]),
+          "=f"(r[17]), "=f"(r[18]), "=f"(r[19]), "=f"(r[20]), "=f"(r[21]), "=f"(r[22]), "=f"(r[23]), "=f"(r[24]),
+          "=f"(r[25]), "=f"(r[26]), "=f"(r[27]), "=f"(r[28]), "=f"(r[29]), "=f"(r[30]), "=f"(r[31])
+        : "r"(taddr)
+        : "memory");
+}
+__device__ __forceinline__ void tmem_wait(float (&r)[32]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+f"(r[0]), "+f"(r[1]), "+f"(r[2]), "+f"(r[3]), "+f"(r[4]), "+f"(r[5]), "+f"(r[6]), "+f"(r[7]),
+                   "+f"(r[8]), "+f"(r[9]), "+f"(r[10]), "+f"(r[11]), "+f"(r[12]), "+f"(r[13]), "+f"(r[14]),
+                   "+f"(r[15]), "+f"(r[16]), "+f"(r[17]), "+f"(r[18]), "+f"(r[19]), "+f"(r[20]), "+f"(r[21]),
+                   "+f"(r[22]), "+f"(r[23]), "+f"(r[24]), "+f"(r[25]), "+f"(r[26]), "+f"(r[27]), "+f"(r[28]),
+                   "+f"(r[29])
+                 :
+                 : "memory");
+    asm volatile("" : "+f"(r[30]), "+f"(r[31]));
 }
 
 // Four neighbouring columns (lane * 4 of the warp's 128) of one row of a gated
@@ -331,8 +363,8 @@ __global__ void __launch_bounds__(FewCfg<NT, GLU>::THREADS, FewCfg<NT, GLU>::ONE
 #pragma unroll
             for (int c = 0; c < Cfg::NC / 16; ++c) {
                 float d[16];
-                tmem_ld16(taddr + c * 16, d);
-                tmem_ld_wait();
+                tmem_ld(taddr + c * 16, d);
+                tmem_wait(d);
                 if (c == Cfg::NC / 16 - 1) {     // all of this block is read: its columns are free again
                     tc_fence_before();
                     __syncwarp();
@@ -448,7 +480,11 @@ __global__ void __launch_bounds__(FewCfg<NT, GLU>::THREADS, FewCfg<NT, GLU>::ONE
 // pairs' sums meet in shared memory (the ring, idle by then) and CTA p of
 // each row half finishes its share of the rows, summing in the pairs' order.
 constexpr int kManyStages = 6;
-constexpr int kManyThreads = 320;
+constexpr int kManyThreads = 384;         // a warpgroup of producers, two of sums
+constexpr int kManyFirst = 4;             // first warp of those
+// Registers: 168 a thread at launch; the producers' warpgroup gives up 128 of them, each of the others takes 64.
+constexpr int kManyProducerRegs = 40, kManySumRegs = 232;
+static_assert(kManyProducerRegs + 2 * kManySumRegs <= 3 * 168, "a split takes no more than the launch has");
 
 struct ManyCfg {
     static constexpr int STAGE_BYTES = 2 * 128 * 128;
@@ -590,10 +626,21 @@ __global__ void __launch_bounds__(kManyThreads, 1) fp8_many_kernel(const __grid_
     tc_fence_after();
     const uint32_t tmem_base = *tmem_slot;
     if (threadIdx.x == 0) pdl_trigger();
-    bool aborted = false;
 
-    if (warp == 0) {
-        if (lane == 0) {
+    // The end of either role: nothing of this CTA is in flight and every sum is staged when it returns.
+    auto meet = [&](bool gave_up) {
+        if (gave_up) spin_ns(50000);                     // let issued copies and products land
+        __syncwarp();
+        tc_fence_before();
+        __syncthreads();
+        if (*abort_flag) spin_ns(50000);
+        cluster_sync();                                  // no MMA or remote arrive still targets the peer
+    };
+
+    if (warp < kManyFirst) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kManyProducerRegs));
+        bool aborted = false;
+        if (warp == 0 && lane == 0) {
             // ------------------------------------------------ TMA producer (both CTAs)
             pdl_wait();
             int s = 0;
@@ -626,8 +673,7 @@ __global__ void __launch_bounds__(kManyThreads, 1) fp8_many_kernel(const __grid_
                 }
             }
         }
-    } else if (warp == 1) {
-        if (lane == 0 && rank == 0) {
+        if (warp == 1 && lane == 0 && rank == 0) {
             // ------------------------------------------------ MMA issuer (even CTA)
             constexpr uint32_t idesc = mma_idesc_e4m3(256, 256);
             int s = 0, b = 0;
@@ -658,12 +704,21 @@ __global__ void __launch_bounds__(kManyThreads, 1) fp8_many_kernel(const __grid_
                 }
             }
         }
+        meet(aborted);
+        if (split > 1) cluster_sync_relaxed();           // a peer may still read this CTA's sums
+        if (warp == 1) {
+            __syncwarp();
+            tc_fence_after();
+            tmem_dealloc_pair<512>(tmem_base);
+        }
     } else {
         // ---------------------------------------------------- scaled sums and output (both CTAs)
+        bool aborted = false;
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kManySumRegs));
         const int q = warp & 3;
-        const int half = (warp - 2) >> 2;                 // plain: columns [128 half, +128); gated: [64 half, +64) of gate and of up
+        const int half = (warp - kManyFirst) >> 2;                 // plain: columns [128 half, +128); gated: [64 half, +64) of gate and of up
         const int row_in_tile = static_cast<int>(rank) * 128 + q * 32 + lane;
-        uint8_t* st = base_ptr + kStgOff + (warp - 2) * 32 * Cfg::STG_PITCH;
+        uint8_t* st = base_ptr + kStgOff + (warp - kManyFirst) * 32 * Cfg::STG_PITCH;
         uint8_t* st_lane = st + lane * Cfg::STG_PITCH;
         float* amax = reinterpret_cast<float*>(base_ptr + kAmaxOff) + q * 32 + lane;
         const uint32_t lane_base = tmem_base + (static_cast<uint32_t>(q * 32) << 16);
@@ -683,20 +738,31 @@ __global__ void __launch_bounds__(kManyThreads, 1) fp8_many_kernel(const __grid_
             float acc[128];
 #pragma unroll
             for (int j = 0; j < 128; ++j) acc[j] = 0.0f;
+            // the scales, fetched two K blocks ahead
             int seg = kb_lo / args.k_blocks, kb = kb_lo - seg * args.k_blocks, left = kb_hi - kb_lo;
-            float px[2], pa[2], pb[2];                    // scales of the next two K blocks
+            const float *xs, *wa, *wb;
+            auto segment = [&]() {
+                xs = args.xs[args.segs > 1 ? seg : (args.x_per_group ? g : 0)] + static_cast<int64_t>(kb) * args.ldxs +
+                     (row_ok ? row : 0);
+                const float* ws = args.ws[args.segs > 1 ? seg : g];
+                wa = ws + static_cast<int64_t>(wb_ok ? wb_a : 0) * args.k_blocks + kb;
+                wb = ws + static_cast<int64_t>(GLU ? wb_b : 0) * args.k_blocks + kb;
+            };
+            segment();
+            float px[2] = {0.0f, 0.0f}, pa[2] = {0.0f, 0.0f}, pb[2] = {0.0f, 0.0f};
             auto fetch = [&](int i) {
-                px[i] = pa[i] = pb[i] = 0.0f;
                 if (left > 0) {
-                    const float* xs = args.xs[args.segs > 1 ? seg : (args.x_per_group ? g : 0)];
-                    const float* ws = args.ws[args.segs > 1 ? seg : g];
-                    if (row_ok) px[i] = xs[static_cast<int64_t>(kb) * args.ldxs + row];
-                    if (wb_ok) pa[i] = ws[static_cast<int64_t>(wb_a) * args.k_blocks + kb];
-                    if (GLU) pb[i] = ws[static_cast<int64_t>(wb_b) * args.k_blocks + kb];
+                    px[i] = *xs;
+                    pa[i] = *wa;
+                    if (GLU) pb[i] = *wb;
+                    xs += args.ldxs;
+                    ++wa;
+                    ++wb;
                     --left;
-                    if (++kb == args.k_blocks) {
+                    if (++kb == args.k_blocks && left > 0) {
                         kb = 0;
                         ++seg;
+                        segment();
                     }
                 }
             };
@@ -714,21 +780,26 @@ __global__ void __launch_bounds__(kManyThreads, 1) fp8_many_kernel(const __grid_
                 }
                 tc_fence_after();
                 const uint32_t taddr = lane_base + static_cast<uint32_t>(b * 256);
-#pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    float d[32];
-                    tmem_ld16(taddr + (c < 2 ? col_a : col_b) + (c & 1) * 32, *reinterpret_cast<float(*)[16]>(&d[0]));
-                    tmem_ld16(taddr + (c < 2 ? col_a : col_b) + (c & 1) * 32 + 16, *reinterpret_cast<float(*)[16]>(&d[16]));
-                    tmem_ld_wait();
-                    if (c == 3) {                         // the accumulator is read: the MMA may have it again
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive_cluster_relaxed(mapa_shared(tempty_bar(b), leader));
-                    }
-                    const float s = c < 2 ? sa : sb;
+                float d0[32], d1[32];                     // one is read while the other is added
+                auto add = [&](int c, float (&d)[32], float s) {
 #pragma unroll
                     for (int j = 0; j < 32; j += 2) fma2(acc[c * 32 + j], acc[c * 32 + j + 1], d[j], d[j + 1], s);
-                }
+                };
+                tmem_ld(taddr + col_a, d0);
+                tmem_wait(d0);
+                tmem_ld(taddr + col_a + 32, d1);
+                add(0, d0, sa);
+                tmem_wait(d1);
+                tmem_ld(taddr + col_b, d0);
+                add(1, d1, sa);
+                tmem_wait(d0);
+                tmem_ld(taddr + col_b + 32, d1);
+                add(2, d0, sb);
+                tmem_wait(d1);
+                tc_fence_before();                        // the accumulator is read: the MMA may have it again
+                __syncwarp();
+                if (lane == 0) mbar_arrive_cluster_relaxed(mapa_shared(tempty_bar(b), leader));
+                add(3, d1, sb);
                 b ^= 1;
                 if (b == 0) bphase ^= 1u;
             }
@@ -830,72 +901,61 @@ __global__ void __launch_bounds__(kManyThreads, 1) fp8_many_kernel(const __grid_
                 }
             }
         }
-    }
-
-    if (aborted) spin_ns(50000);
-    __syncwarp();
-    tc_fence_before();
-    __syncthreads();
-    if (*abort_flag) spin_ns(50000);
-    cluster_sync();                                      // no MMA or remote arrive still targets the peer; sums are staged
-    if (split > 1) {
-        // Rows [part * 128 / split, ...) of this CTA's 128: a warp a row, a lane columns [4 lane, +4) of both halves.
-        if (warp >= 2 && *abort_flag == 0) {
-            int g, m, n;
-            many_coords(args, cluster, g, m, n);         // one tile a cluster
-            const int per = 128 / split;
-            for (int r = part * per + warp - 2; r < (part + 1) * per; r += 8) {
-                const int64_t row = static_cast<int64_t>(m) * 256 + static_cast<int64_t>(rank) * 128 + r;
-                if (row >= args.M) break;
-                float v[2][4];
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const uint32_t off = base + static_cast<uint32_t>((r * Cfg::SUM_PITCH + h * 128 + lane * 4) * 4);
-                    float4 x[4];
-#pragma unroll
-                    for (int p = 0; p < 4; ++p)
-                        if (p < split) x[p] = ld_shared_cluster_f4(mapa_shared(off, static_cast<uint32_t>(2 * p) + rank));
-                    float4 a = x[0];
-#pragma unroll
-                    for (int p = 1; p < 4; ++p) {
-                        if (p < split) {
-                            a.x += x[p].x;
-                            a.y += x[p].y;
-                            a.z += x[p].z;
-                            a.w += x[p].w;
-                        }
-                    }
-                    v[h][0] = a.x;
-                    v[h][1] = a.y;
-                    v[h][2] = a.z;
-                    v[h][3] = a.w;
-                }
-                if (GLU) {
-                    finish_gated(args, g, n, row, lane, v[0], v[1]);
-                } else {
-#pragma unroll
+        meet(aborted);
+        if (split > 1) {
+            // Rows [part * 128 / split, ...) of this CTA's 128: a warp a row, a lane columns [4 lane, +4) of both halves.
+            if (*abort_flag == 0) {
+                int g, m, n;
+                many_coords(args, cluster, g, m, n);         // one tile a cluster
+                const int per = 128 / split;
+                for (int r = part * per + warp - kManyFirst; r < (part + 1) * per; r += 8) {
+                    const int64_t row = static_cast<int64_t>(m) * 256 + static_cast<int64_t>(rank) * 128 + r;
+                    if (row >= args.M) break;
+                    float v[2][4];
+    #pragma unroll
                     for (int h = 0; h < 2; ++h) {
-                        const int col = n * 256 + h * 128 + lane * 4;
-                        const int nvalid = args.N - col;
-                        if (nvalid > 0) {
-                            if (args.bias[g] != nullptr) {
-#pragma unroll
-                                for (int i = 0; i < 4; ++i)
-                                    if (i < nvalid) v[h][i] += bf16_to_f32(args.bias[g][col + i]);
+                        const uint32_t off = base + static_cast<uint32_t>((r * Cfg::SUM_PITCH + h * 128 + lane * 4) * 4);
+                        float4 x[4];
+    #pragma unroll
+                        for (int p = 0; p < 4; ++p)
+                            if (p < split) x[p] = ld_shared_cluster_f4(mapa_shared(off, static_cast<uint32_t>(2 * p) + rank));
+                        float4 a = x[0];
+    #pragma unroll
+                        for (int p = 1; p < 4; ++p) {
+                            if (p < split) {
+                                a.x += x[p].x;
+                                a.y += x[p].y;
+                                a.z += x[p].z;
+                                a.w += x[p].w;
                             }
-                            store_quad(args.out[g], args.ldo, args.out_kind == FP8_OUT_F32, row, col, min(4, nvalid), v[h]);
+                        }
+                        v[h][0] = a.x;
+                        v[h][1] = a.y;
+                        v[h][2] = a.z;
+                        v[h][3] = a.w;
+                    }
+                    if (GLU) {
+                        finish_gated(args, g, n, row, lane, v[0], v[1]);
+                    } else {
+    #pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            const int col = n * 256 + h * 128 + lane * 4;
+                            const int nvalid = args.N - col;
+                            if (nvalid > 0) {
+                                if (args.bias[g] != nullptr) {
+    #pragma unroll
+                                    for (int i = 0; i < 4; ++i)
+                                        if (i < nvalid) v[h][i] += bf16_to_f32(args.bias[g][col + i]);
+                                }
+                                store_quad(args.out[g], args.ldo, args.out_kind == FP8_OUT_F32, row, col, min(4, nvalid), v[h]);
+                            }
                         }
                     }
                 }
             }
+            __syncwarp();
+            cluster_sync_relaxed();                      // a peer may still read this CTA's sums
         }
-        __syncwarp();
-        cluster_sync_relaxed();                          // a peer may still read this CTA's sums
-    }
-    if (warp == 1) {
-        __syncwarp();
-        tc_fence_after();
-        tmem_dealloc_pair<512>(tmem_base);
     }
 }
 
