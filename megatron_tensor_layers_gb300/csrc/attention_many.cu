@@ -129,18 +129,6 @@ __device__ __forceinline__ uint32_t hfma2(uint32_t a, uint32_t b, uint32_t c) {
     return d;
 }
 
-// One lane of the (converged) warp.  The compiler knows elect.sync's predicate for one lane's and keeps
-// descriptors in uniform registers under it.
-__device__ __forceinline__ bool elect_one() {
-    uint32_t e;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "elect.sync _|p, 0xffffffff;\n\t"
-        "selp.b32 %0, 1, 0, p;\n\t}"
-        : "=r"(e));
-    return e != 0;
-}
-
 // Two fp32 operations in one instruction.
 __device__ __forceinline__ uint64_t pack2(float lo, float hi) {
     uint64_t r;

@@ -88,6 +88,20 @@ __device__ __forceinline__ void spin_ns(uint64_t ns) {
 // as lost (1 s; a full-size GEMM tile takes tens of microseconds).
 constexpr uint64_t kWaitLimitNs = 1000000000ull;
 
+// ---------------------------------------------------------------- one lane
+
+// One lane of the (converged) warp.  The compiler knows elect.sync's predicate for one lane's and keeps
+// descriptors in uniform registers under it.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t e;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xffffffff;\n\t"
+        "selp.b32 %0, 1, 0, p;\n\t}"
+        : "=r"(e));
+    return e != 0;
+}
+
 // ---------------------------------------------------------------- smem
 
 __device__ __forceinline__ uint32_t smem_u32(const void* p) {

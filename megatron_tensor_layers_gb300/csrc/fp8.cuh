@@ -30,10 +30,54 @@ __device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
     return static_cast<uint32_t>(lo) | (static_cast<uint32_t>(hi) << 16);
 }
 
-// Codes of x / scale: the quotient rounded to fp32, then to e4m3.
-__device__ __forceinline__ uint32_t fp8_codes4(float a, float b, float c, float d, float scale) {
-    return e4m3x4(__fdiv_rn(a, scale), __fdiv_rn(b, scale), __fdiv_rn(c, scale), __fdiv_rn(d, scale));
+// Quotients x / scale rounded to nearest as a division's: with r = 1 / s
+// rounded to nearest, q0 = x r is within 1.5 units of the last place, one
+// correction q1 = q0 + (x - q0 s) r (the remainder is exact in an fma) brings it
+// within one, and by Markstein's theorem a second then rounds correctly.  Five
+// multiply-adds instead of a division's reciprocal and steps each.  Scales
+// below 2^-60 and their values are taken times 2^64, so that no remainder is
+// subnormal.  An infinite scale's quotients are 0 (NaN of an infinity): there the
+// remainders are taken with 0 in place of the scale.
+struct Fp8Quotient {
+    float f, s, r;
+    __device__ __forceinline__ explicit Fp8Quotient(float scale) {
+        f = scale < 8.6736173798840355e-19f ? 1.8446744073709552e19f : 1.0f;   // 2^-60, 2^64
+        s = scale * f;
+        r = __frcp_rn(s);
+        s = s == __int_as_float(0x7f800000) ? 0.0f : s;
+    }
+    __device__ __forceinline__ float operator()(float x) const {
+        x *= f;
+        const float q0 = x * r;
+        const float q1 = fmaf(-fmaf(q0, s, -x), r, q0);  // the remainder negated: a quotient of -0 stays one
+        return fmaf(-fmaf(q1, s, -x), r, q1);
+    }
+};
+
+// Codes of four values.
+__device__ __forceinline__ uint32_t fp8_codes4(float a, float b, float c, float d, const Fp8Quotient& q) {
+    return e4m3x4(q(a), q(b), q(c), q(d));
 }
+
+// act(g) of a gated block as g / (1 + exp(-z)): SiLU has z = g, and GeLU-tanh's
+// 0.5 g (1 + tanh(u)) is z = 2 u with u = sqrt(2/pi) (g + 0.044715 g^3).  With
+// coefficients in place of a branch, exp as 2^(g (a + b g^2)), and the hardware's
+// 2^x and reciprocal (2^-22 and 1 ulp).
+struct GateAct {
+    float a, b;
+    __device__ __forceinline__ explicit GateAct(int act) {
+        constexpr float log2e = 1.4426950408889634f, k = 2.0f * 0.7978845608028654f;
+        a = act == TP_ACT_GELU_TANH_MUL ? -k * log2e : -log2e;
+        b = act == TP_ACT_GELU_TANH_MUL ? -k * 0.044715f * log2e : 0.0f;
+    }
+    __device__ __forceinline__ float operator()(float g) const {
+        const float g2 = fminf(g * g, 3.0e38f);          // finite: b may be 0
+        float e, r;
+        asm("ex2.approx.f32 %0, %1;" : "=f"(e) : "f"(g * fmaf(b, g2, a)));
+        asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(1.0f + e));
+        return g * r;
+    }
+};
 
 // Largest |x| of eight values.
 __device__ __forceinline__ float amax8(const float (&x)[8]) {
@@ -80,7 +124,8 @@ __device__ __forceinline__ float max16(float m) {
 }
 
 __device__ __forceinline__ uint2 fp8_codes8(const float (&x)[8], float scale) {
-    return make_uint2(fp8_codes4(x[0], x[1], x[2], x[3], scale), fp8_codes4(x[4], x[5], x[6], x[7], scale));
+    const Fp8Quotient q(scale);
+    return make_uint2(fp8_codes4(x[0], x[1], x[2], x[3], q), fp8_codes4(x[4], x[5], x[6], x[7], q));
 }
 
 }  // namespace tpk

@@ -94,16 +94,20 @@ __device__ __forceinline__ void tmem_ld(uint32_t taddr, float (&r)[32]) {
         : "r"(taddr)
         : "memory");
 }
-__device__ __forceinline__ void tmem_wait(float (&r)[32]) {
-    asm volatile("tcgen05.wait::ld.sync.aligned;"
-                 : "+f"(r[0]), "+f"(r[1]), "+f"(r[2]), "+f"(r[3]), "+f"(r[4]), "+f"(r[5]), "+f"(r[6]), "+f"(r[7]),
-                   "+f"(r[8]), "+f"(r[9]), "+f"(r[10]), "+f"(r[11]), "+f"(r[12]), "+f"(r[13]), "+f"(r[14]),
-                   "+f"(r[15]), "+f"(r[16]), "+f"(r[17]), "+f"(r[18]), "+f"(r[19]), "+f"(r[20]), "+f"(r[21]),
-                   "+f"(r[22]), "+f"(r[23]), "+f"(r[24]), "+f"(r[25]), "+f"(r[26]), "+f"(r[27]), "+f"(r[28]),
-                   "+f"(r[29])
-                 :
-                 : "memory");
-    asm volatile("" : "+f"(r[30]), "+f"(r[31]));
+// An asm statement takes 30 operands: the arrays are named in four.
+__device__ __forceinline__ void tmem_wait(float (&x)[32], float (&y)[32]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+    for (int i = 0; i < 32; i += 16) {
+        asm volatile(""
+                     : "+f"(x[i]), "+f"(x[i + 1]), "+f"(x[i + 2]), "+f"(x[i + 3]), "+f"(x[i + 4]), "+f"(x[i + 5]),
+                       "+f"(x[i + 6]), "+f"(x[i + 7]), "+f"(x[i + 8]), "+f"(x[i + 9]), "+f"(x[i + 10]),
+                       "+f"(x[i + 11]), "+f"(x[i + 12]), "+f"(x[i + 13]), "+f"(x[i + 14]), "+f"(x[i + 15]));
+        asm volatile(""
+                     : "+f"(y[i]), "+f"(y[i + 1]), "+f"(y[i + 2]), "+f"(y[i + 3]), "+f"(y[i + 4]), "+f"(y[i + 5]),
+                       "+f"(y[i + 6]), "+f"(y[i + 7]), "+f"(y[i + 8]), "+f"(y[i + 9]), "+f"(y[i + 10]),
+                       "+f"(y[i + 11]), "+f"(y[i + 12]), "+f"(y[i + 13]), "+f"(y[i + 14]), "+f"(y[i + 15]));
+    }
 }
 
 // Four neighbouring columns (lane * 4 of the warp's 128) of one row of a gated
@@ -113,9 +117,10 @@ __device__ __forceinline__ void finish_gated(const Fp8GemmArgs& args, int g, int
                                              const float (&gate)[4], const float (&up)[4]) {
     const int col = n * 128 + lane * 4;
     const int nvalid = args.N - col;                     // this lane's columns inside the group
+    const GateAct act(args.act);
     float v[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = act_fn(gate[i], args.act) * up[i];
+    for (int i = 0; i < 4; ++i) v[i] = act(gate[i]) * up[i];
     if (args.out_kind == FP8_OUT_CODES) {
         float top = 0.0f;
 #pragma unroll
@@ -125,7 +130,7 @@ __device__ __forceinline__ void finish_gated(const Fp8GemmArgs& args, int g, int
         const float s = fp8_scale(top);
         if (nvalid > 0)                                  // N is a multiple of 16: all four or none
             *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(args.out[g]) + row * args.ldo + col) =
-                fp8_codes4(v[0], v[1], v[2], v[3], s);
+                fp8_codes4(v[0], v[1], v[2], v[3], Fp8Quotient(s));
         if (lane == 0) args.os[g][static_cast<int64_t>(n) * args.ldos + row] = s;
     } else if (nvalid > 0) {
         store_quad(args.out[g], args.ldo, args.out_kind == FP8_OUT_F32, row, col, min(4, nvalid), v);
@@ -467,19 +472,36 @@ __global__ void __launch_bounds__(FewCfg<NT, GLU>::THREADS, FewCfg<NT, GLU>::ONE
 // 256 x 256 tiles of a cluster of two CTAs on neighbouring SMs (cta_group::2),
 // tokens as the MMA's rows: CTA r of a pair brings rows [128 r, 128 r + 128) of
 // the tile's tokens and the r-th 128 rows of its weights (gated: CTA 0 gate's, CTA
-// 1 the same rows of up), and the even CTA issues one M = 256, N = 256 MMA for
-// both.  Every K block of 128 goes to one of two TMEM accumulators; eight
-// epilogue warps a CTA read it (a thread one token's 128 columns), scale it
-// and add it to 128 fp32 sums a thread, while the MMA fills the other one: the
-// read and the multiply-adds of a block (256 + 256 cycles a quarter of the
-// SM) fit the 512 cycles of its MMAs.  With tokens as rows a thread needs
-// one token's scale a block and one product with each weight block's;
-// weights as rows would need one for every column.
+// 1 the same rows of up).  With tokens as rows a thread needs one token's scale a
+// block and one product with each weight block's; weights as rows would
+// need one for every column.
+//
+// A K block's products (M = 256, N = 256) go to one of two TMEM accumulators,
+// which eight warps a CTA read (a thread one token's 128 columns), scale and
+// add to 128 fp32 sums a thread, while the MMAs fill the other.  From an
+// accumulator's MMAs to the next ones that may overwrite it pass its MMAs (513
+// cycles), their commit (300), the reading (250) and the release across the
+// pair (250), so a K block takes about 650 cycles.  What keeps each of these
+// short was measured:
+//  - one warp issues the MMAs, elected lanes in converged loops under a
+//    warp-uniform branch (four MMAs, a wait and a commit: 380 cycles; one lane of a
+//    diverged warp 690; two issuers' MMAs drain the tensor core between
+//    them).  A wait and a commit cost it 50 to 100 cycles each, so one barrier a
+//    stage says both that the tiles are there and that the accumulator is free,
+//    and one that the products are done: the accumulator may be read and the
+//    tiles overwritten.  Halves of N = 128 in twice the accumulators would need
+//    eight MMAs a block, 900 cycles of issue.
+//  - the scales come through shared memory, far ahead (loaded by the warps that
+//    use them, their latency bounded the kernel).
+//  - the last columns are read before the first half's multiply-adds are
+//    all done: the registers hold 64 of the 128.
 //
 // split > 1: a cluster of `split` pairs shares a tile's K blocks in runs; the
 // pairs' sums meet in shared memory (the ring, idle by then) and CTA p of
 // each row half finishes its share of the rows, summing in the pairs' order.
 constexpr int kManyStages = 6;
+constexpr int kScaleAhead = 6;            // K blocks ahead that scales are asked for
+constexpr int kScaleSlots = kScaleAhead + kManyStages + 2;
 constexpr int kManyThreads = 384;         // a warpgroup of producers, two of sums
 constexpr int kManyFirst = 4;             // first warp of those
 // Registers: 168 a thread at launch; the producers' warpgroup gives up 128 of them, each of the others takes 64.
@@ -491,9 +513,11 @@ struct ManyCfg {
     static constexpr int STG_PITCH = 80;                     // 64 bytes of a row and a pad: no bank conflicts
     static constexpr int STG_BYTES = 8 * 32 * STG_PITCH;
     static constexpr int AMAX_BYTES = 2 * 2 * 128 * 4;       // two halves' largest values, two tiles in turn
-    static constexpr int NBARS = 2 * kManyStages + 4 + 4;
+    static constexpr int NBARS = 2 * kManyStages + 4;
+    static constexpr int RAW_FLOATS = 128 + 4;               // a block's scales: 128 rows', the two weight blocks'
+    static constexpr int RAW_BYTES = kScaleSlots * RAW_FLOATS * 4;
     static constexpr int SUM_PITCH = 260;                    // floats of a staged row of sums
-    static constexpr int SMEM_BYTES = 1024 + kManyStages * STAGE_BYTES + STG_BYTES + AMAX_BYTES + NBARS * 8 + 16;
+    static constexpr int SMEM_BYTES = 1024 + kManyStages * STAGE_BYTES + STG_BYTES + AMAX_BYTES + RAW_BYTES + NBARS * 8 + 16;
     static_assert(SMEM_BYTES <= 227 * 1024, "shared memory per CTA");
     static_assert(128 * SUM_PITCH * 4 <= kManyStages * STAGE_BYTES, "a CTA's sums fit the ring");
 };
@@ -508,16 +532,31 @@ __device__ __forceinline__ void tc_mma_f8_pair(uint32_t d_tmem, uint64_t a_desc,
         : "memory");
 }
 
-// Two fp32 multiply-adds in one instruction.
-__device__ __forceinline__ void fma2(float& a0, float& a1, float d0, float d1, float s) {
-    asm("{\n\t.reg .b64 a, d, s;\n\t"
-        "mov.b64 a, {%0, %1};\n\t"
-        "mov.b64 d, {%2, %3};\n\t"
-        "mov.b64 s, {%4, %4};\n\t"
-        "fma.rn.f32x2 a, d, s, a;\n\t"
-        "mov.b64 {%0, %1}, a;\n\t}"
-        : "+f"(a0), "+f"(a1)
-        : "f"(d0), "f"(d1), "f"(s));
+// Pairs of fp32 values in one register pair, and two multiply-adds in one
+// instruction.  The sums stay packed over the whole loop and a block's factor is packed
+// once: packed in each multiply-add anew, 128 of them took a warp 220 cycles
+// instead of 153.
+using f32x2 = unsigned long long;
+__device__ __forceinline__ f32x2 pack2(float a, float b) {
+    f32x2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ void unpack2(f32x2 v, float& a, float& b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v)); }
+__device__ __forceinline__ f32x2 fma2(f32x2 d, f32x2 s, f32x2 a) {
+    f32x2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(d), "l"(s), "l"(a));
+    return r;
+}
+
+// Asynchronous copies of one float to shared memory, in groups.
+__device__ __forceinline__ void cp_async4(uint32_t dst, const float* src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
 // Tile index -> (group, row tile, column tile): bands of row tiles, the row
@@ -581,17 +620,18 @@ __global__ void __launch_bounds__(kManyThreads, 1) fp8_many_kernel(const __grid_
     uint8_t* base_ptr = smem_raw + (base - raw_addr);
     constexpr int kStgOff = STAGES * Cfg::STAGE_BYTES;
     constexpr int kAmaxOff = kStgOff + Cfg::STG_BYTES;
-    constexpr int kBarOff = kAmaxOff + Cfg::AMAX_BYTES;
+    constexpr int kRawOff = kAmaxOff + Cfg::AMAX_BYTES;
+    constexpr int kBarOff = kRawOff + Cfg::RAW_BYTES;
     const uint32_t bar_base = base + kBarOff;
-    auto full_bar = [&](int s) { return bar_base + 8u * s; };
-    auto empty_bar = [&](int s) { return bar_base + 8u * (STAGES + s); };
-    auto tfull_bar = [&](int b) { return bar_base + 8u * (2 * STAGES + b); };
-    auto tempty_bar = [&](int b) { return bar_base + 8u * (2 * STAGES + 2 + b); };
-    auto half_bar = [&](int q) { return bar_base + 8u * (2 * STAGES + 4 + q); };   // the two warps of a lane quarter
+    // a stage's products may start: its tiles are there and the accumulator is free
+    // ... and are done: the scales are there too, the accumulator may be read and the tiles overwritten
+    auto start_bar = [&](int s) { return bar_base + 8u * s; };
+    auto done_bar = [&](int s) { return bar_base + 8u * (STAGES + s); };
+    auto half_bar = [&](int q) { return bar_base + 8u * (2 * STAGES + q); };   // the two warps of a lane quarter
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(base_ptr + kBarOff + 8 * Cfg::NBARS);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(base_ptr + kBarOff + 8 * Cfg::NBARS + 4);
 
-    const int warp = threadIdx.x >> 5;
+    const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0);   // uniform to the compiler
     const int lane = threadIdx.x & 31;
     const int split = args.split;
     const uint32_t crank = cluster_ctarank();
@@ -607,12 +647,8 @@ __global__ void __launch_bounds__(kManyThreads, 1) fp8_many_kernel(const __grid_
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < STAGES; ++s) {
-            mbar_init(full_bar(s), 1);
-            mbar_init(empty_bar(s), 1);
-        }
-        for (int b = 0; b < 2; ++b) {
-            mbar_init(tfull_bar(b), 1);
-            mbar_init(tempty_bar(b), 16);                // eight epilogue warps of each CTA
+            mbar_init(start_bar(s), 1 + 16);             // the tiles, the eight warps of sums in either CTA
+            mbar_init(done_bar(s), 2);                   // the products, the scales
         }
         for (int q = 0; q < 4; ++q) mbar_init(half_bar(q), 2);
         *abort_flag = 0;
@@ -624,7 +660,7 @@ __global__ void __launch_bounds__(kManyThreads, 1) fp8_many_kernel(const __grid_
     __syncthreads();
     cluster_sync();                                      // the peer's barriers exist before any remote use
     tc_fence_after();
-    const uint32_t tmem_base = *tmem_slot;
+    const uint32_t tmem_base = __shfl_sync(0xffffffffu, *tmem_slot, 0);
     if (threadIdx.x == 0) pdl_trigger();
 
     // The end of either role: nothing of this CTA is in flight and every sum is staged when it returns.
@@ -640,7 +676,7 @@ __global__ void __launch_bounds__(kManyThreads, 1) fp8_many_kernel(const __grid_
     if (warp < kManyFirst) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kManyProducerRegs));
         bool aborted = false;
-        if (warp == 0 && lane == 0) {
+        if (warp == 0) {
             // ------------------------------------------------ TMA producer (both CTAs)
             pdl_wait();
             int s = 0;
@@ -652,16 +688,20 @@ __global__ void __launch_bounds__(kManyThreads, 1) fp8_many_kernel(const __grid_
                 const int w_row = GLU ? (rank == 0 ? n * 128 : args.N + n * 128) : n * 256 + static_cast<int>(rank) * 128;
                 int seg = kb_lo / args.k_blocks, kb = kb_lo - seg * args.k_blocks;
                 for (int i = kb_lo; i < kb_hi; ++i) {
-                    if (!mbar_wait(empty_bar(s), phase ^ 1u, abort_flag, args.status)) {
+                    if (!mbar_wait_warp(done_bar(s), phase ^ 1u, abort_flag, args.status)) {
                         aborted = true;
                         break;
                     }
-                    if (rank == 0) mbar_arrive_expect_tx(full_bar(s), 2u * Cfg::STAGE_BYTES);
-                    const uint32_t full = mapa_shared(full_bar(s), leader);
                     const int xi = args.segs > 1 ? seg : (args.x_per_group ? g : 0);
+                    const int wi = args.segs > 1 ? seg : g;
+                    const uint32_t full = mapa_shared(start_bar(s), leader);
                     const uint32_t sx = base + s * Cfg::STAGE_BYTES;
-                    tma_load_2d_pair(sx, &args.mapX[xi], full, kb * 128, x_row);
-                    tma_load_2d_pair(sx + 128 * 128, &args.mapW[args.segs > 1 ? seg : g], full, kb * 128, w_row);
+                    if (elect_one()) {
+                        if (rank == 0) mbar_arrive_expect_tx(start_bar(s), 2u * Cfg::STAGE_BYTES);
+                        tma_load_2d_pair(sx, &args.mapX[xi], full, kb * 128, x_row);
+                        tma_load_2d_pair(sx + 128 * 128, &args.mapW[wi], full, kb * 128, w_row);
+                    }
+                    __syncwarp();
                     if (++kb == args.k_blocks) {
                         kb = 0;
                         ++seg;
@@ -673,34 +713,95 @@ __global__ void __launch_bounds__(kManyThreads, 1) fp8_many_kernel(const __grid_
                 }
             }
         }
-        if (warp == 1 && lane == 0 && rank == 0) {
-            // ------------------------------------------------ MMA issuer (even CTA)
-            constexpr uint32_t idesc = mma_idesc_e4m3(256, 256);
-            int s = 0, b = 0;
-            uint32_t phase = 0, bphase = 0;
+        if (warp == 3) {
+            // ------------------------------------------------ scales (both CTAs)
+            // Those of this CTA's 128 rows and the two weight blocks, by asynchronous copies kScaleAhead blocks ahead
+            // (loaded two blocks ahead by the warps that use them, their latency bounded the kernel).  Block j's
+            // arrival waits for block j - 6's products, the barriers' phase before; by then the sums have read block
+            // j - 8's scales, since block j - 6's products waited for that, and its slot may be asked for again.
+            pdl_wait();
+            float* raw = reinterpret_cast<float*>(base_ptr + kRawOff);
+            int s = 0, ask_slot = 0;
+            uint32_t phase = 0;
             for (int tile = cluster; tile < args.total_tiles && !aborted; tile += nclusters) {
-                for (int i = kb_lo; i < kb_hi; ++i) {
-                    if (!mbar_wait(full_bar(s), phase, abort_flag, args.status) ||
-                        !mbar_wait(tempty_bar(b), bphase ^ 1u, abort_flag, args.status)) {
+                int g, m, n;
+                many_coords(args, tile, g, m, n);
+                const int64_t row0 = static_cast<int64_t>(m) * 256 + static_cast<int64_t>(rank) * 128 + lane;
+                // the weight blocks of the tile's two halves; where the second does not exist its sums are never stored
+                const int wb = lane == 0 ? (GLU ? n : n * 2)
+                               : GLU     ? args.up_block + n
+                                         : ((n * 2 + 1) * 128 < args.N ? n * 2 + 1 : n * 2);
+                const int blocks = kb_hi - kb_lo;
+                int seg = kb_lo / args.k_blocks, kb = kb_lo - seg * args.k_blocks;     // of the next block asked for
+                const float *xs = nullptr, *ws = nullptr;
+                auto segment = [&]() {
+                    xs = args.xs[args.segs > 1 ? seg : (args.x_per_group ? g : 0)] + static_cast<int64_t>(kb) * args.ldxs + row0;
+                    ws = args.ws[args.segs > 1 ? seg : g] + static_cast<int64_t>(wb) * args.k_blocks + kb;
+                };
+                segment();
+                auto ask = [&](int i) {
+                    if (i < blocks) {
+                        const uint32_t at = smem_u32(raw + ask_slot * Cfg::RAW_FLOATS) + lane * 4;
+#pragma unroll
+                        for (int r = 0; r < 4; ++r)
+                            if (row0 + r * 32 < args.M) cp_async4(at + r * 128, xs + r * 32);
+                        if (lane < 2) cp_async4(at + 512, ws);
+                        xs += args.ldxs;
+                        ++ws;
+                        if (++kb == args.k_blocks && i + 1 < blocks) {
+                            kb = 0;
+                            ++seg;
+                            segment();
+                        }
+                        ask_slot = ask_slot == kScaleSlots - 1 ? 0 : ask_slot + 1;
+                    }
+                    cp_async_commit();
+                };
+                // the first ones of a tile are asked for as its blocks come up, each after its wait
+                int asked = 0;
+                for (int i = 0; i < blocks; ++i) {
+                    if (!mbar_wait_warp(done_bar(s), phase ^ 1u, abort_flag, args.status)) {
                         aborted = true;
                         break;
                     }
-                    tc_fence_after();
+                    for (; asked <= i + kScaleAhead; ++asked) ask(asked);
+                    cp_async_wait<kScaleAhead>();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(done_bar(s));
+                    if (++s == STAGES) {
+                        s = 0;
+                        phase ^= 1u;
+                    }
+                }
+            }
+            cp_async_wait<0>();
+        }
+        if (warp == 1 && rank == 0) {
+            // ------------------------------------------------ MMA issuer (even CTA)
+            constexpr uint32_t idesc = mma_idesc_e4m3(256, 256);
+            int s = 0, b = 0;
+            uint32_t phase = 0;
+            const int tiles = cluster < args.total_tiles ? (args.total_tiles - 1 - cluster) / nclusters + 1 : 0;
+            for (int64_t i = static_cast<int64_t>(tiles) * (kb_hi - kb_lo); i > 0; --i) {   // K blocks of all of the cluster's tiles
+                if (!mbar_wait_warp(start_bar(s), phase, abort_flag, args.status)) {
+                    aborted = true;
+                    break;
+                }
+                tc_fence_after();
+                if (elect_one()) {
                     const uint32_t sx = base + s * Cfg::STAGE_BYTES;
                     const uint64_t xdesc = sw128_kmajor_desc(sx);
                     const uint64_t wdesc = sw128_kmajor_desc(sx + 128 * 128);
                     const uint32_t d = tmem_base + static_cast<uint32_t>(b * 256);
 #pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        tc_mma_f8_pair(d, xdesc + 2u * k, wdesc + 2u * k, idesc, k != 0 ? 1u : 0u);
-                    tc_commit_pair(empty_bar(s), pair_mask);
-                    tc_commit_pair(tfull_bar(b), pair_mask);
-                    if (++s == STAGES) {
-                        s = 0;
-                        phase ^= 1u;
-                    }
-                    b ^= 1;
-                    if (b == 0) bphase ^= 1u;
+                    for (int k = 0; k < 4; ++k) tc_mma_f8_pair(d, xdesc + 2u * k, wdesc + 2u * k, idesc, k != 0 ? 1u : 0u);
+                    tc_commit_pair(done_bar(s), pair_mask);
+                }
+                __syncwarp();
+                b ^= 1;
+                if (++s == STAGES) {
+                    s = 0;
+                    phase ^= 1u;
                 }
             }
         }
@@ -722,103 +823,82 @@ __global__ void __launch_bounds__(kManyThreads, 1) fp8_many_kernel(const __grid_
         uint8_t* st_lane = st + lane * Cfg::STG_PITCH;
         float* amax = reinterpret_cast<float*>(base_ptr + kAmaxOff) + q * 32 + lane;
         const uint32_t lane_base = tmem_base + (static_cast<uint32_t>(q * 32) << 16);
-        const uint32_t col_a = GLU ? half * 64 : half * 128;            // TMEM columns of sums 0..63
-        const uint32_t col_b = GLU ? 128 + half * 64 : half * 128 + 64; // and of 64..127
-        pdl_wait();                                       // the rows' scales may be the previous kernel's output
-        int b = 0, turn = 0;
-        uint32_t bphase = 0, hphase = 0;
+        const int col_a = half * 64, col_b = 128 + half * 64;            // the tile's columns of sums 0..63 and 64..127
+        pdl_wait();                                       // the previous kernel may read what this one writes
+        const float* raw = reinterpret_cast<const float*>(base_ptr + kRawOff);
+        // the accumulators are free to begin with: the first two blocks' starts
+        auto release = [&](int s) {
+            if (elect_one()) mbar_arrive_cluster_relaxed(mapa_shared(start_bar(s), leader));
+        };
+        release(0);
+        release(1);
+        int s = 0, b = 0, turn = 0, slot = 0;
+        uint32_t phase = 0, hphase = 0;
         for (int tile = cluster; tile < args.total_tiles && !aborted; tile += nclusters) {
             int g, m, n;
             many_coords(args, tile, g, m, n);
             const int64_t row = static_cast<int64_t>(m) * 256 + row_in_tile;
             const bool row_ok = row < args.M;
-            const int wb_a = GLU ? n : n * 2 + half, wb_b = GLU ? args.up_block + n : wb_a;
-            // a column tile's second weight block may not exist: then its scales are not read
-            const bool wb_ok = GLU || wb_a * 128 < args.N;
-            float acc[128];
+            f32x2 sums[64];
 #pragma unroll
-            for (int j = 0; j < 128; ++j) acc[j] = 0.0f;
-            // the scales, fetched two K blocks ahead
-            int seg = kb_lo / args.k_blocks, kb = kb_lo - seg * args.k_blocks, left = kb_hi - kb_lo;
-            const float *xs, *wa, *wb;
-            auto segment = [&]() {
-                xs = args.xs[args.segs > 1 ? seg : (args.x_per_group ? g : 0)] + static_cast<int64_t>(kb) * args.ldxs +
-                     (row_ok ? row : 0);
-                const float* ws = args.ws[args.segs > 1 ? seg : g];
-                wa = ws + static_cast<int64_t>(wb_ok ? wb_a : 0) * args.k_blocks + kb;
-                wb = ws + static_cast<int64_t>(GLU ? wb_b : 0) * args.k_blocks + kb;
-            };
-            segment();
-            float px[2] = {0.0f, 0.0f}, pa[2] = {0.0f, 0.0f}, pb[2] = {0.0f, 0.0f};
-            auto fetch = [&](int i) {
-                if (left > 0) {
-                    px[i] = *xs;
-                    pa[i] = *wa;
-                    if (GLU) pb[i] = *wb;
-                    xs += args.ldxs;
-                    ++wa;
-                    ++wb;
-                    --left;
-                    if (++kb == args.k_blocks && left > 0) {
-                        kb = 0;
-                        ++seg;
-                        segment();
-                    }
-                }
-            };
-            fetch(0);
-            fetch(1);
+            for (int j = 0; j < 64; ++j) sums[j] = 0;
             for (int i = kb_lo; i < kb_hi; ++i) {
-                const float sa = px[0] * pa[0], sb = GLU ? px[0] * pb[0] : sa;
-                px[0] = px[1];
-                pa[0] = pa[1];
-                pb[0] = pb[1];
-                fetch(1);
-                if (!mbar_wait_warp(tfull_bar(b), bphase, abort_flag, args.status)) {
+                if (!mbar_wait_warp(done_bar(s), phase, abort_flag, args.status)) {
                     aborted = true;
                     break;
                 }
                 tc_fence_after();
-                const uint32_t taddr = lane_base + static_cast<uint32_t>(b * 256);
-                float d0[32], d1[32];                     // one is read while the other is added
-                auto add = [&](int c, float (&d)[32], float s) {
+                const uint32_t taddr = lane_base + static_cast<uint32_t>(b * 256 + half * 64);
+                float d0[32], d1[32];
+                tmem_ld(taddr, d0);
+                tmem_ld(taddr + 32, d1);
+                const float* scales = raw + slot * Cfg::RAW_FLOATS;
+                const float sx = scales[q * 32 + lane];
+                const float2 sw = *reinterpret_cast<const float2*>(scales + 128);
+                const float fa = sx * sw.x, fb = sx * sw.y;
+                const f32x2 sa = pack2(fa, fa), sb = pack2(fb, fb);
+                auto add = [&](int c, float (&d)[32], f32x2 s) {
 #pragma unroll
-                    for (int j = 0; j < 32; j += 2) fma2(acc[c * 32 + j], acc[c * 32 + j + 1], d[j], d[j + 1], s);
+                    for (int j = 0; j < 16; ++j) sums[c * 16 + j] = fma2(pack2(d[2 * j], d[2 * j + 1]), s, sums[c * 16 + j]);
                 };
-                tmem_ld(taddr + col_a, d0);
-                tmem_wait(d0);
-                tmem_ld(taddr + col_a + 32, d1);
+                tmem_wait(d0, d1);
                 add(0, d0, sa);
-                tmem_wait(d1);
-                tmem_ld(taddr + col_b, d0);
+                tmem_ld(taddr + 128, d0);
                 add(1, d1, sa);
-                tmem_wait(d0);
-                tmem_ld(taddr + col_b + 32, d1);
-                add(2, d0, sb);
-                tmem_wait(d1);
-                tc_fence_before();                        // the accumulator is read: the MMA may have it again
+                tmem_ld(taddr + 160, d1);
+                tmem_wait(d0, d1);
+                tc_fence_before();                        // the accumulator is read: block i + 2's products may have it
                 __syncwarp();
-                if (lane == 0) mbar_arrive_cluster_relaxed(mapa_shared(tempty_bar(b), leader));
+                release(s + 2 < STAGES ? s + 2 : s + 2 - STAGES);
+                add(2, d0, sb);
                 add(3, d1, sb);
                 b ^= 1;
-                if (b == 0) bphase ^= 1u;
+                slot = slot == kScaleSlots - 1 ? 0 : slot + 1;
+                if (++s == STAGES) {
+                    s = 0;
+                    phase ^= 1u;
+                }
             }
             if (aborted) break;
+            float acc[128];
+#pragma unroll
+            for (int j = 0; j < 64; ++j) unpack2(sums[j], acc[2 * j], acc[2 * j + 1]);
             const int64_t row0 = static_cast<int64_t>(m) * 256 + static_cast<int64_t>(rank) * 128 + q * 32;
             const int live = static_cast<int>(min(static_cast<int64_t>(32), args.M - row0));   // rows of this warp
             if (split > 1) {
                 // this CTA's sums to the ring, a row of 256 at SUM_PITCH; joined below
-                float* sums = reinterpret_cast<float*>(base_ptr) + (q * 32 + lane) * Cfg::SUM_PITCH;
+                float* to = reinterpret_cast<float*>(base_ptr) + (q * 32 + lane) * Cfg::SUM_PITCH;
 #pragma unroll
                 for (int j = 0; j < 128; j += 4)
-                    *reinterpret_cast<float4*>(sums + (j < 64 ? col_a + j : col_b + j - 64)) =
+                    *reinterpret_cast<float4*>(to + (j < 64 ? col_a + j : col_b + j - 64)) =
                         make_float4(acc[j], acc[j + 1], acc[j + 2], acc[j + 3]);
             } else if (GLU) {
+                const GateAct act(args.act);
                 uint8_t* out = static_cast<uint8_t*>(args.out[g]);
                 const int col0 = n * 128 + half * 64;
                 const int valid = args.N - col0;          // columns of this half inside the group
 #pragma unroll
-                for (int j = 0; j < 64; ++j) acc[j] = act_fn(row_ok ? acc[j] : 0.0f, args.act) * acc[64 + j];
+                for (int j = 0; j < 64; ++j) acc[j] = act(acc[j]) * acc[64 + j];
                 if (args.out_kind == FP8_OUT_CODES) {
                     float top = 0.0f;
 #pragma unroll
@@ -836,13 +916,14 @@ __global__ void __launch_bounds__(kManyThreads, 1) fp8_many_kernel(const __grid_
                     turn ^= 1;
                     if (half == 0 && row_ok) args.os[g][static_cast<int64_t>(n) * args.ldos + row] = s;
                     if (live > 0 && valid > 0) {
+                        const Fp8Quotient quot(s);
 #pragma unroll
                         for (int j = 0; j < 64; j += 16)
                             *reinterpret_cast<uint4*>(st_lane + j) =
-                                make_uint4(fp8_codes4(acc[j], acc[j + 1], acc[j + 2], acc[j + 3], s),
-                                           fp8_codes4(acc[j + 4], acc[j + 5], acc[j + 6], acc[j + 7], s),
-                                           fp8_codes4(acc[j + 8], acc[j + 9], acc[j + 10], acc[j + 11], s),
-                                           fp8_codes4(acc[j + 12], acc[j + 13], acc[j + 14], acc[j + 15], s));
+                                make_uint4(fp8_codes4(acc[j], acc[j + 1], acc[j + 2], acc[j + 3], quot),
+                                           fp8_codes4(acc[j + 4], acc[j + 5], acc[j + 6], acc[j + 7], quot),
+                                           fp8_codes4(acc[j + 8], acc[j + 9], acc[j + 10], acc[j + 11], quot),
+                                           fp8_codes4(acc[j + 12], acc[j + 13], acc[j + 14], acc[j + 15], quot));
                         many_store<1>(st, out, row0, live, args.ldo, col0, valid, lane);
                     }
                 } else if (live > 0 && valid > 0) {
@@ -869,32 +950,34 @@ __global__ void __launch_bounds__(kManyThreads, 1) fp8_many_kernel(const __grid_
                 }
             } else {
                 uint8_t* out = static_cast<uint8_t*>(args.out[g]);
-                const int col0 = n * 256 + half * 128;
-                const int valid = args.N - col0;
-                if (live > 0 && valid > 0) {
-                    const uint16_t* bias = args.bias[g];
+                const uint16_t* bias = args.bias[g];
+#pragma unroll
+                for (int p = 0; p < 2; ++p) {
+                    const int col0 = n * 256 + p * 128 + half * 64;
+                    const int valid = args.N - col0;
+                    if (live <= 0 || valid <= 0) break;
                     if (bias != nullptr) {
 #pragma unroll
-                        for (int j = 0; j < 128; ++j)
-                            if (j < valid) acc[j] += bf16_to_f32(bias[col0 + j]);
+                        for (int j = 0; j < 64; ++j)
+                            if (j < valid) acc[p * 64 + j] += bf16_to_f32(bias[col0 + j]);
                     }
                     if (args.out_kind == FP8_OUT_F32) {
 #pragma unroll
-                        for (int c = 0; c < 128; c += 16) {
+                        for (int c = 0; c < 64; c += 16) {
 #pragma unroll
-                            for (int j = 0; j < 16; j += 4)
-                                *reinterpret_cast<float4*>(st_lane + j * 4) =
-                                    make_float4(acc[c + j], acc[c + j + 1], acc[c + j + 2], acc[c + j + 3]);
+                            for (int j = p * 64 + c; j < p * 64 + c + 16; j += 4)
+                                *reinterpret_cast<float4*>(st_lane + (j - p * 64 - c) * 4) =
+                                    make_float4(acc[j], acc[j + 1], acc[j + 2], acc[j + 3]);
                             many_store<4>(st, out, row0, live, args.ldo * 4, (col0 + c) * 4LL, (valid - c) * 4, lane);
                         }
                     } else {
 #pragma unroll
-                        for (int c = 0; c < 128; c += 32) {
+                        for (int c = 0; c < 64; c += 32) {
 #pragma unroll
-                            for (int j = 0; j < 32; j += 8)
-                                *reinterpret_cast<uint4*>(st_lane + j * 2) =
-                                    make_uint4(pack_bf16x2(acc[c + j], acc[c + j + 1]), pack_bf16x2(acc[c + j + 2], acc[c + j + 3]),
-                                               pack_bf16x2(acc[c + j + 4], acc[c + j + 5]), pack_bf16x2(acc[c + j + 6], acc[c + j + 7]));
+                            for (int j = p * 64 + c; j < p * 64 + c + 32; j += 8)
+                                *reinterpret_cast<uint4*>(st_lane + (j - p * 64 - c) * 2) =
+                                    make_uint4(pack_bf16x2(acc[j], acc[j + 1]), pack_bf16x2(acc[j + 2], acc[j + 3]),
+                                               pack_bf16x2(acc[j + 4], acc[j + 5]), pack_bf16x2(acc[j + 6], acc[j + 7]));
                             many_store<2>(st, out, row0, live, args.ldo * 2, (col0 + c) * 2LL, (valid - c) * 2, lane);
                         }
                     }
