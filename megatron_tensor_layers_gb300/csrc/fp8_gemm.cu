@@ -110,6 +110,38 @@ __device__ __forceinline__ void tmem_wait(float (&x)[32], float (&y)[32]) {
     }
 }
 
+// Pairs of fp32 values in one register pair, and two multiply-adds in one
+// instruction.  The sums stay packed over the whole loop and a block's factor is packed
+// once: packed in each multiply-add anew, 128 of them took a warp 220 cycles
+// instead of 153.
+using f32x2 = unsigned long long;
+__device__ __forceinline__ f32x2 pack2(float a, float b) {
+    f32x2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ void unpack2(f32x2 v, float& a, float& b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v)); }
+__device__ __forceinline__ f32x2 fma2(f32x2 d, f32x2 s, f32x2 a) {
+    f32x2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(d), "l"(s), "l"(a));
+    return r;
+}
+__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
+    f32x2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+
+// Asynchronous copies of one float to shared memory, in groups.
+__device__ __forceinline__ void cp_async4(uint32_t dst, const float* src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
 // Four neighbouring columns (lane * 4 of the warp's 128) of one row of a gated
 // tile: act(gate) * up, stored, or brought to 8 bits with the row's group in
 // the warp.
@@ -149,28 +181,33 @@ __device__ __forceinline__ void finish_gated(const Fp8GemmArgs& args, int g, int
 // of a token's tile are one warp's, which for a gated tile is also the group
 // of the 8-bit hidden row.
 //
-// Roles: warp 0 brings tiles (TMA), warp 1 multiplies, warps 2.. add up: of a
-// gated tile four warps the gate's columns and four up's, of a plain one each
-// warp all NT columns, or half of 128.
+// Roles: warp 0 brings tiles (TMA), warp 1 multiplies, warp 2 brings scales,
+// warps 3.. add up: of a gated tile four warps the gate's columns and four up's,
+// of a plain one each warp all NT columns, or half of 128.
 template <int NT, bool GLU>
 struct FewCfg {
     static constexpr int W_BYTES = (GLU ? 2 : 1) * 128 * 128;
     static constexpr int X_BYTES = NT * 128;
     static constexpr int STAGE_BYTES = W_BYTES + X_BYTES;
-    static constexpr bool ONE = NT > 64;                       // CTAs per SM: one, else two
-    static constexpr int BUDGET = (ONE ? 216 : 108) * 1024;
+    static constexpr bool ONE = NT > (GLU ? 32 : 64);          // CTAs per SM: one, else two
+    static constexpr int BUDGET = (ONE ? 216 : 110) * 1024;    // of the ring
     static constexpr int STAGES = BUDGET / STAGE_BYTES;
     static constexpr int STAGING_BYTES = (GLU ? 2 : 1) * NT * 128 * 4;
     static constexpr int EPI_WARPS = (GLU || NT > 64) ? 8 : 4;
     static constexpr int NC = (!GLU && NT > 64) ? NT / 2 : NT; // columns of a warp
     static constexpr int ACC_COLS = NT * (GLU ? 2 : 1);        // TMEM columns of one K block
-    static constexpr int BUFS = (ONE ? 512 : 256) / ACC_COLS > 4 ? 4 : (ONE ? 512 : 256) / ACC_COLS;
+    static constexpr int TMEM_BUFS = (ONE ? 512 : 256) / ACC_COLS;
+    // accumulators in turn; no more than stages, so that a block's start has one phase ahead of it at most
+    static constexpr int BUFS = TMEM_BUFS >= 4 && STAGES >= 4 ? 4 : 2;
     static constexpr int TMEM_COLS = ACC_COLS * BUFS;
-    static constexpr int THREADS = 64 + 32 * EPI_WARPS;
-    static constexpr int NBARS = 2 * STAGES + 2 * BUFS;
-    static constexpr int SCALE_BYTES = EPI_WARPS * 2 * NC * 4; // a warp's token scales, twice
+    static constexpr int THREADS = 96 + 32 * EPI_WARPS;
+    static constexpr int NBARS = 2 * STAGES;
+    static constexpr int AHEAD = 4;                            // K blocks ahead that scales are asked for
+    static constexpr int SLOTS = AHEAD + STAGES + BUFS;
+    static constexpr int SLOT_FLOATS = NT + 4;                 // a block's scales: the tokens', the weight blocks'
+    static constexpr int SCALE_BYTES = SLOTS * SLOT_FLOATS * 4;
     static constexpr int SMEM_BYTES = 1024 + STAGES * STAGE_BYTES + SCALE_BYTES + NBARS * 8 + 16;
-    static_assert(STAGES >= 2 && BUFS >= 2, "both pipelines need two slots");
+    static_assert(STAGES >= BUFS && TMEM_BUFS >= 2, "both pipelines need two slots");
     static_assert(STAGES * STAGE_BYTES >= STAGING_BYTES, "the sums are staged in the ring");
     static_assert(STAGE_BYTES % 1024 == 0 && W_BYTES % 1024 == 0, "swizzled tiles are 1024-byte aligned");
     static_assert((TMEM_COLS & (TMEM_COLS - 1)) == 0 && TMEM_COLS >= 32 && TMEM_COLS <= 512, "TMEM columns");
@@ -189,14 +226,13 @@ __global__ void __launch_bounds__(FewCfg<NT, GLU>::THREADS, FewCfg<NT, GLU>::ONE
     float* scales_ptr = reinterpret_cast<float*>(base_ptr + Cfg::STAGES * Cfg::STAGE_BYTES);
     constexpr int kBarOff = Cfg::STAGES * Cfg::STAGE_BYTES + Cfg::SCALE_BYTES;
     const uint32_t bar_base = base + kBarOff;
-    auto full_bar = [&](int s) { return bar_base + 8u * s; };
-    auto empty_bar = [&](int s) { return bar_base + 8u * (Cfg::STAGES + s); };
-    auto tfull_bar = [&](int b) { return bar_base + 8u * (2 * Cfg::STAGES + b); };
-    auto tempty_bar = [&](int b) { return bar_base + 8u * (2 * Cfg::STAGES + Cfg::BUFS + b); };
+    // a stage's products may start: its tiles are there and the accumulator is free; they are done
+    auto start_bar = [&](int s) { return bar_base + 8u * s; };
+    auto done_bar = [&](int s) { return bar_base + 8u * (Cfg::STAGES + s); };
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(base_ptr + kBarOff + 8 * Cfg::NBARS);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(base_ptr + kBarOff + 8 * Cfg::NBARS + 4);
 
-    const int warp = threadIdx.x >> 5;
+    const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0);   // uniform to the compiler
     const int lane = threadIdx.x & 31;
     const int split = args.split;
     const int crank = split > 1 ? static_cast<int>(cluster_ctarank()) : 0;
@@ -212,12 +248,8 @@ __global__ void __launch_bounds__(FewCfg<NT, GLU>::THREADS, FewCfg<NT, GLU>::ONE
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < Cfg::STAGES; ++s) {
-            mbar_init(full_bar(s), 1);
-            mbar_init(empty_bar(s), 1);
-        }
-        for (int b = 0; b < Cfg::BUFS; ++b) {
-            mbar_init(tfull_bar(b), 1);
-            mbar_init(tempty_bar(b), Cfg::EPI_WARPS);
+            mbar_init(start_bar(s), 1 + Cfg::EPI_WARPS);
+            mbar_init(done_bar(s), 2);                   // the products, the scales
         }
         *abort_flag = 0;
         fence_barrier_init();
@@ -227,74 +259,72 @@ __global__ void __launch_bounds__(FewCfg<NT, GLU>::THREADS, FewCfg<NT, GLU>::ONE
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem_base = *tmem_slot;
+    const uint32_t tmem_base = __shfl_sync(0xffffffffu, *tmem_slot, 0);
     if (threadIdx.x == 0) pdl_trigger();
     bool aborted = false;
 
     if (warp == 0) {
-        if (lane == 0) {
-            // ------------------------------------------------ TMA producer
-            const uint32_t bytes = Cfg::W_BYTES + static_cast<uint32_t>(args.x_box_rows) * 128u;
-            int seg = kb_lo / args.k_blocks, kb = kb_lo - seg * args.k_blocks;
-            auto load_w = [&](int s, int seg, int kb) {
-                const int wi = args.segs > 1 ? seg : g;
-                const uint32_t sw = base + s * Cfg::STAGE_BYTES;
-                tma_load_2d(sw, &args.mapW[wi], full_bar(s), kb * 128, n * 128);
-                if (GLU) tma_load_2d(sw + 128 * 128, &args.mapW[wi], full_bar(s), kb * 128, args.N + n * 128);
-            };
-            auto load_x = [&](int s, int seg, int kb) {
-                const int xi = args.segs > 1 ? seg : (args.x_per_group ? g : 0);
-                tma_load_2d(base + s * Cfg::STAGE_BYTES + Cfg::W_BYTES, &args.mapX[xi], full_bar(s), kb * 128, token0);
-            };
-            int pre = 0;
-            if (args.weights_first) {          // the first ring of weights before the previous kernel's end
-                int sg = seg, k = kb;
-                pre = min(Cfg::STAGES, kb_hi - kb_lo);
-                for (int s = 0; s < pre; ++s) {
-                    mbar_arrive_expect_tx(full_bar(s), bytes);
-                    load_w(s, sg, k);
-                    if (++k == args.k_blocks) {
-                        k = 0;
-                        ++sg;
-                    }
-                }
-            }
-            pdl_wait();
-            int s = 0;
-            uint32_t phase = 0;
-            for (int i = 0; i < kb_hi - kb_lo; ++i) {
-                if (i >= pre) {
-                    if (!mbar_wait(empty_bar(s), phase ^ 1u, abort_flag, args.status)) {
-                        aborted = true;
-                        break;
-                    }
-                    mbar_arrive_expect_tx(full_bar(s), bytes);
-                    load_w(s, seg, kb);
-                }
-                load_x(s, seg, kb);
-                if (++kb == args.k_blocks) {
-                    kb = 0;
-                    ++seg;
-                }
-                if (++s == Cfg::STAGES) {
-                    s = 0;
-                    phase ^= 1u;
+        // ---------------------------------------------------- TMA producer
+        const uint32_t bytes = Cfg::W_BYTES + static_cast<uint32_t>(args.x_box_rows) * 128u;
+        int seg = kb_lo / args.k_blocks, kb = kb_lo - seg * args.k_blocks;
+        auto load_w = [&](int s, int seg, int kb) {
+            const int wi = args.segs > 1 ? seg : g;
+            const uint32_t sw = base + s * Cfg::STAGE_BYTES;
+            mbar_arrive_expect_tx(start_bar(s), bytes);
+            tma_load_2d(sw, &args.mapW[wi], start_bar(s), kb * 128, n * 128);
+            if (GLU) tma_load_2d(sw + 128 * 128, &args.mapW[wi], start_bar(s), kb * 128, args.N + n * 128);
+        };
+        auto load_x = [&](int s, int seg, int kb) {
+            const int xi = args.segs > 1 ? seg : (args.x_per_group ? g : 0);
+            tma_load_2d(base + s * Cfg::STAGE_BYTES + Cfg::W_BYTES, &args.mapX[xi], start_bar(s), kb * 128, token0);
+        };
+        int pre = 0;
+        if (args.weights_first) {              // the first ring of weights before the previous kernel's end
+            int sg = seg, k = kb;
+            pre = min(Cfg::STAGES, kb_hi - kb_lo);
+            for (int s = 0; s < pre; ++s) {
+                if (elect_one()) load_w(s, sg, k);
+                __syncwarp();
+                if (++k == args.k_blocks) {
+                    k = 0;
+                    ++sg;
                 }
             }
         }
+        pdl_wait();
+        int s = 0;
+        uint32_t phase = 0;
+        for (int i = 0; i < kb_hi - kb_lo; ++i) {
+            if (i >= pre && !mbar_wait_warp(done_bar(s), phase ^ 1u, abort_flag, args.status)) {
+                aborted = true;
+                break;
+            }
+            if (elect_one()) {
+                if (i >= pre) load_w(s, seg, kb);
+                load_x(s, seg, kb);
+            }
+            __syncwarp();
+            if (++kb == args.k_blocks) {
+                kb = 0;
+                ++seg;
+            }
+            if (++s == Cfg::STAGES) {
+                s = 0;
+                phase ^= 1u;
+            }
+        }
     } else if (warp == 1) {
-        if (lane == 0) {
-            // ------------------------------------------------ MMA issuer
-            constexpr uint32_t idesc = mma_idesc_e4m3(128, NT);
-            int s = 0, b = 0;
-            uint32_t phase = 0, bphase = 0;
-            for (int i = kb_lo; i < kb_hi; ++i) {
-                if (!mbar_wait(tempty_bar(b), bphase ^ 1u, abort_flag, args.status) ||
-                    !mbar_wait(full_bar(s), phase, abort_flag, args.status)) {
-                    aborted = true;
-                    break;
-                }
-                tc_fence_after();
+        // ---------------------------------------------------- MMA issuer (see the many-row kernel's)
+        constexpr uint32_t idesc = mma_idesc_e4m3(128, NT);
+        int s = 0, b = 0;
+        uint32_t phase = 0;
+        for (int i = kb_lo; i < kb_hi; ++i) {
+            if (!mbar_wait_warp(start_bar(s), phase, abort_flag, args.status)) {
+                aborted = true;
+                break;
+            }
+            tc_fence_after();
+            if (elect_one()) {
                 const uint32_t d = tmem_base + static_cast<uint32_t>(b * Cfg::ACC_COLS);
                 const uint32_t sw = base + s * Cfg::STAGE_BYTES;
                 const uint64_t wdesc = sw128_kmajor_desc(sw);
@@ -303,90 +333,124 @@ __global__ void __launch_bounds__(FewCfg<NT, GLU>::THREADS, FewCfg<NT, GLU>::ONE
                 for (int k = 0; k < 4; ++k)      // 32 codes along K: 32 bytes inside the swizzle row
                     tc_mma_f8(d, wdesc + 2u * k, xdesc + 2u * k, idesc, k != 0 ? 1u : 0u);
                 if (GLU) {
-                    const uint64_t udesc = sw128_kmajor_desc(sw + 128 * 128);
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
-                        tc_mma_f8(d + NT, udesc + 2u * k, xdesc + 2u * k, idesc, k != 0 ? 1u : 0u);
+                        tc_mma_f8(d + NT, wdesc + ((128 * 128) >> 4) + 2u * k, xdesc + 2u * k, idesc, k != 0 ? 1u : 0u);
                 }
-                tc_commit(empty_bar(s));
-                tc_commit(tfull_bar(b));
-                if (++s == Cfg::STAGES) {
-                    s = 0;
-                    phase ^= 1u;
+                tc_commit(done_bar(s));
+            }
+            __syncwarp();
+            if (++s == Cfg::STAGES) {
+                s = 0;
+                phase ^= 1u;
+            }
+            b = (b + 1) & (Cfg::BUFS - 1);
+        }
+    } else if (warp == 2) {
+        // ---------------------------------------------------- scales
+        // By asynchronous copies AHEAD blocks ahead (loaded one block ahead by the warps that use them, their latency
+        // bounded the loop).  Block j's arrival waits for block j - STAGES's products, the barrier's phase before; by
+        // then the sums have read block j - STAGES - BUFS's scales, whose slot may be asked for again.
+        pdl_wait();
+        const int blocks = kb_hi - kb_lo;
+        const int tok = token0 + lane;
+        const int wb = n + (lane == 1 ? args.up_block : 0);
+        int seg = kb_lo / args.k_blocks, kb = kb_lo - seg * args.k_blocks, ask_slot = 0, asked = 0;
+        const float *xs = nullptr, *ws = nullptr;
+        auto segment = [&]() {
+            xs = args.xs[args.segs > 1 ? seg : (args.x_per_group ? g : 0)] + static_cast<int64_t>(kb) * args.ldxs + tok;
+            ws = args.ws[args.segs > 1 ? seg : g] + static_cast<int64_t>(wb) * args.k_blocks + kb;
+        };
+        segment();
+        auto ask = [&](int i) {
+            if (i < blocks) {
+                const uint32_t at = smem_u32(scales_ptr + ask_slot * Cfg::SLOT_FLOATS + lane);
+#pragma unroll
+                for (int p = 0; p < NT; p += 32)
+                    if (p + lane < NT && tok + p < args.M) cp_async4(at + p * 4, xs + p);
+                if (lane < (GLU ? 2 : 1)) cp_async4(at + NT * 4, ws);
+                xs += args.ldxs;
+                ++ws;
+                if (++kb == args.k_blocks && i + 1 < blocks) {
+                    kb = 0;
+                    ++seg;
+                    segment();
                 }
-                if (++b == Cfg::BUFS) {
-                    b = 0;
-                    bphase ^= 1u;
-                }
+                ask_slot = ask_slot == Cfg::SLOTS - 1 ? 0 : ask_slot + 1;
+            }
+            cp_async_commit();
+        };
+        int s = 0;
+        uint32_t phase = 0;
+        for (int i = 0; i < blocks; ++i) {
+            if (!mbar_wait_warp(done_bar(s), phase ^ 1u, abort_flag, args.status)) {
+                aborted = true;
+                break;
+            }
+            for (; asked <= i + Cfg::AHEAD; ++asked) ask(asked);
+            cp_async_wait<Cfg::AHEAD>();
+            __syncwarp();
+            if (elect_one()) mbar_arrive(done_bar(s));
+            if (++s == Cfg::STAGES) {
+                s = 0;
+                phase ^= 1u;
             }
         }
+        cp_async_wait<0>();
     } else {
         // ---------------------------------------------------- scaled sums
-        const int e = warp - 2;
+        const int e = warp - 3;
         const int q = warp & 3;                  // TMEM lane quarter this warp may access
         const int part = e >> 2;                 // gated: 0 gate, 1 up; plain: which half of the columns
         const int col0 = GLU ? 0 : part * Cfg::NC;
-        float* sc = scales_ptr + e * 2 * Cfg::NC;
-        constexpr int PRE = (Cfg::NC + 31) / 32;
-        float acc[Cfg::NC];
-#pragma unroll
-        for (int j = 0; j < Cfg::NC; ++j) acc[j] = 0.0f;
-        pdl_wait();                              // the rows' scales may be the previous kernel's output
-        const int wb = n + (GLU && part ? args.up_block : 0);
-        float pre[PRE], wpre = 0.0f;
-        int seg = kb_lo / args.k_blocks, kb = kb_lo - seg * args.k_blocks;
-        auto fetch = [&]() {
-            const float* xs = args.xs[args.segs > 1 ? seg : (args.x_per_group ? g : 0)] + static_cast<int64_t>(kb) * args.ldxs;
-            wpre = args.ws[args.segs > 1 ? seg : g][static_cast<int64_t>(wb) * args.k_blocks + kb];
-#pragma unroll
-            for (int i = 0; i < PRE; ++i) {
-                const int tok = token0 + col0 + i * 32 + lane;
-                pre[i] = (i * 32 + lane < Cfg::NC && tok < args.M) ? xs[tok] : 0.0f;
-            }
-            if (++kb == args.k_blocks) {
-                kb = 0;
-                ++seg;
-            }
+        const int blocks = kb_hi - kb_lo;
+        // block i + BUFS may have block i's accumulator; the first ones' are free to begin with
+        auto release = [&](int s) {
+            if (elect_one()) mbar_arrive(start_bar(s));
         };
-        if (kb_lo < kb_hi) fetch();
-        int b = 0;
-        uint32_t bphase = 0;
-        const uint32_t lane_base = tmem_base + (static_cast<uint32_t>(q * 32) << 16);
-        for (int i = kb_lo; i < kb_hi; ++i) {
-            float* s = sc + (i & 1) * Cfg::NC;
+        for (int i = 0; i < Cfg::BUFS; ++i) release(i);
+        f32x2 acc[Cfg::NC / 2];
 #pragma unroll
-            for (int p = 0; p < PRE; ++p)
-                if (p * 32 + lane < Cfg::NC) s[p * 32 + lane] = pre[p] * wpre;
-            if (i + 1 < kb_hi) fetch();
-            __syncwarp();
-            if (!mbar_wait_warp(tfull_bar(b), bphase, abort_flag, args.status)) {
+        for (int j = 0; j < Cfg::NC / 2; ++j) acc[j] = 0;
+        pdl_wait();                              // the previous kernel may read what this one writes
+        int s = 0, b = 0, slot = 0;
+        uint32_t phase = 0;
+        const uint32_t lane_base = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(GLU ? part * NT : col0);
+        for (int i = 0; i < blocks; ++i) {
+            if (!mbar_wait_warp(done_bar(s), phase, abort_flag, args.status)) {
                 aborted = true;
                 break;
             }
             tc_fence_after();
-            const uint32_t taddr = lane_base + static_cast<uint32_t>(b * Cfg::ACC_COLS + (GLU ? part * NT : col0));
+            const uint32_t taddr = lane_base + static_cast<uint32_t>(b * Cfg::ACC_COLS);
+            const float* f = scales_ptr + slot * Cfg::SLOT_FLOATS;
+            const float w = f[NT + (GLU ? part : 0)];
+            const f32x2 w2 = pack2(w, w);
 #pragma unroll
             for (int c = 0; c < Cfg::NC / 16; ++c) {
                 float d[16];
                 tmem_ld(taddr + c * 16, d);
+                f32x2 x[8];                      // the columns' factors
+#pragma unroll
+                for (int j = 0; j < 16; j += 4) {
+                    const float4 v = *reinterpret_cast<const float4*>(f + col0 + c * 16 + j);
+                    x[j / 2] = mul2(pack2(v.x, v.y), w2);
+                    x[j / 2 + 1] = mul2(pack2(v.z, v.w), w2);
+                }
                 tmem_wait(d);
                 if (c == Cfg::NC / 16 - 1) {     // all of this block is read: its columns are free again
                     tc_fence_before();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(tempty_bar(b));
+                    release(s + Cfg::BUFS < Cfg::STAGES ? s + Cfg::BUFS : s + Cfg::BUFS - Cfg::STAGES);
                 }
 #pragma unroll
-                for (int j = 0; j < 16; j += 4) {
-                    const float4 f = *reinterpret_cast<const float4*>(s + c * 16 + j);
-                    acc[c * 16 + j] = fmaf(d[j], f.x, acc[c * 16 + j]);
-                    acc[c * 16 + j + 1] = fmaf(d[j + 1], f.y, acc[c * 16 + j + 1]);
-                    acc[c * 16 + j + 2] = fmaf(d[j + 2], f.z, acc[c * 16 + j + 2]);
-                    acc[c * 16 + j + 3] = fmaf(d[j + 3], f.w, acc[c * 16 + j + 3]);
-                }
+                for (int j = 0; j < 8; ++j) acc[c * 8 + j] = fma2(pack2(d[2 * j], d[2 * j + 1]), x[j], acc[c * 8 + j]);
             }
-            if (++b == Cfg::BUFS) {
-                b = 0;
-                bphase ^= 1u;
+            slot = slot == Cfg::SLOTS - 1 ? 0 : slot + 1;
+            b = (b + 1) & (Cfg::BUFS - 1);
+            if (++s == Cfg::STAGES) {
+                s = 0;
+                phase ^= 1u;
             }
         }
         // Stage the sums [gate/up][token][128 columns] in the ring: the last block's products
@@ -394,7 +458,12 @@ __global__ void __launch_bounds__(FewCfg<NT, GLU>::THREADS, FewCfg<NT, GLU>::ONE
         if (!aborted) {
             float* st = reinterpret_cast<float*>(base_ptr) + ((GLU ? part * NT : 0) + col0) * 128 + q * 32 + lane;
 #pragma unroll
-            for (int j = 0; j < Cfg::NC; ++j) st[j * 128] = acc[j];
+            for (int j = 0; j < Cfg::NC / 2; ++j) {
+                float lo, hi;
+                unpack2(acc[j], lo, hi);
+                st[2 * j * 128] = lo;
+                st[(2 * j + 1) * 128] = hi;
+            }
         }
     }
 
@@ -405,8 +474,8 @@ __global__ void __launch_bounds__(FewCfg<NT, GLU>::THREADS, FewCfg<NT, GLU>::ONE
         cluster_sync();
     else
         __syncthreads();
-    if (warp >= 2 && *abort_flag == 0) {
-        const int e = warp - 2;
+    if (warp >= 3 && *abort_flag == 0) {
+        const int e = warp - 3;
         const int tokens = min(NT, args.M - token0);
         const int col = n * 128 + lane * 4;
         const int nvalid = args.N - col;                     // this lane's columns inside the group
@@ -530,33 +599,6 @@ __device__ __forceinline__ void tc_mma_f8_pair(uint32_t d_tmem, uint64_t a_desc,
         "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
         "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
         : "memory");
-}
-
-// Pairs of fp32 values in one register pair, and two multiply-adds in one
-// instruction.  The sums stay packed over the whole loop and a block's factor is packed
-// once: packed in each multiply-add anew, 128 of them took a warp 220 cycles
-// instead of 153.
-using f32x2 = unsigned long long;
-__device__ __forceinline__ f32x2 pack2(float a, float b) {
-    f32x2 r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
-    return r;
-}
-__device__ __forceinline__ void unpack2(f32x2 v, float& a, float& b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v)); }
-__device__ __forceinline__ f32x2 fma2(f32x2 d, f32x2 s, f32x2 a) {
-    f32x2 r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(d), "l"(s), "l"(a));
-    return r;
-}
-
-// Asynchronous copies of one float to shared memory, in groups.
-__device__ __forceinline__ void cp_async4(uint32_t dst, const float* src) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
-}
-__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_async_wait() {
-    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
 // Tile index -> (group, row tile, column tile): bands of row tiles, the row
@@ -1044,6 +1086,31 @@ __global__ void __launch_bounds__(kManyThreads, 1) fp8_many_kernel(const __grid_
 
 // ------------------------------------------------------------------ host
 
+// Costs of a wave in hundredths of a microsecond, from both kernels' times: the 128-token few-row kernel takes 0.34 us
+// a K block (gated 0.88) and 3 us beside them, the many-row kernel 0.50 and 3.5, and 3 more where parts are joined.
+// Times that the weight stream bounds are below both; the comparison stands there too (100 tokens, four shards of the
+// down projection: few 44 us, many 64; 300 tokens, QKV of eight shards: few 48, many 72; gate_up of 100: few
+// 112, many 104).
+constexpr int64_t kFewBlock = 34, kFewGatedBlock = 88, kFewWave = 300;
+constexpr int64_t kManyBlock = 50, kManyWave = 350, kManyJoin = 300;
+
+// CTAs that share a few-row tile: as many as all find a place at once, with eight K blocks each at least.  QKV of 8
+// shards (80 tiles, 304 places), 16 tokens: 18.4, 17.9, 15.9, 20.0 us in 1, 2, 3, 4 parts; the down projection of 32
+// tokens (64 tiles of 224 blocks) 65, 41, 40, 38, 46 us in 1 to 5; 8 tiles of 32 blocks 7.5, 5.4, 4.7, 4.1, 4.1,
+// 4.4, 4.2 in 1 to 6 and 8.
+static int few_split(int64_t tiles, int64_t kb_all, int64_t places) {
+    return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({places / tiles, kb_all / 8, 8})));
+}
+
+static int64_t few_tiles(const Fp8GemmDesc& d, int nt) { return d.groups * ((d.M + nt - 1) / nt) * ((d.N + 127) / 128); }
+
+static int64_t few_cost(const Fp8GemmDesc& d, int sms) {
+    const int64_t tiles = few_tiles(d, 128), kb = fp8_groups(d.K) * d.segs;
+    const int split = few_split(tiles, kb, sms);
+    const int64_t waves = (tiles * split + sms - 1) / sms;
+    return waves * ((kb + split - 1) / split * (d.glu ? kFewGatedBlock : kFewBlock) + kFewWave);
+}
+
 template <int NT, bool GLU>
 static tp_status launch_few(Fp8GemmArgs& a, const Fp8GemmDesc& d, cudaStream_t stream) {
     using Cfg = FewCfg<NT, GLU>;
@@ -1052,10 +1119,7 @@ static tp_status launch_few(Fp8GemmArgs& a, const Fp8GemmDesc& d, cudaStream_t s
     const int64_t tiles = static_cast<int64_t>(d.groups) * a.m_tiles * a.n_tiles;
     const int sms = device_sms();
     if (sms <= 0) return TP_ERR_CUDA;
-    // CTAs that share a tile: as many as still find an SM of their own
-    const int kb_all = a.k_blocks * d.segs;
-    int split = 1;
-    while (split < 8 && tiles * split * 2 <= sms * (Cfg::ONE ? 1 : 2) && kb_all / (split * 2) >= 2) split *= 2;
+    const int split = few_split(tiles, static_cast<int64_t>(a.k_blocks) * d.segs, static_cast<int64_t>(sms) * (Cfg::ONE ? 1 : 2));
     if (tiles * split > INT32_MAX) return TP_ERR_UNSUPPORTED;
     a.total_tiles = static_cast<int>(tiles);
     a.split = split;
@@ -1087,13 +1151,57 @@ static tp_status launch_few(Fp8GemmArgs& a, const Fp8GemmDesc& d, cudaStream_t s
     return cudaGetLastError() == cudaSuccess ? TP_OK : TP_ERR_CUDA;
 }
 
-// CTA pairs: 256 x 256 tiles.  The K blocks of a tile are split over 1, 2 or 4 pairs, whichever takes the least:
-// waves of tiles times a part's K blocks and what a tile costs beside them.
-constexpr int kManyTileCost = 8;        // K blocks' worth: filling the pipeline and the output of a tile
-constexpr int kManyJoinCost = 6;        // and of joining the parts
+// CTA pairs: 256 x 256 tiles, whose K blocks are split over 1, 2 or 4 pairs, whichever takes the least.
+struct ManyPlan {
+    int split = 1, clusters = 0;
+    int64_t cost = -1;
+};
 
 template <bool GLU>
-static tp_status launch_many(Fp8GemmArgs& a, const Fp8GemmDesc& d, cudaStream_t stream) {
+static ManyPlan plan_many(const Fp8GemmDesc& d, int sms) {
+    // clusters of 2, 4 and 8 CTAs that can be resident at once (per device)
+    static std::atomic<int> resident[64][3];             // relaxed: racing first calls store the same value
+    auto kern = fp8_many_kernel<GLU>;
+    int dev = 0;
+    cudaGetDevice(&dev);
+    const bool cached = dev >= 0 && dev < 64;
+    const int64_t tiles = d.groups * ((d.M + 255) / 256) * ((d.N + (GLU ? 127 : 255)) / (GLU ? 128 : 256));
+    const int64_t kb = fp8_groups(d.K) * d.segs;
+    ManyPlan best;
+    for (int i = 0; i < 3; ++i) {
+        const int split = 1 << i;
+        if (split > 1 && kb / split < 4) break;
+        int mc = cached ? resident[dev][i].load(std::memory_order_relaxed) : 0;
+        if (mc <= 0) {
+            cudaLaunchAttribute attr[1];
+            attr[0].id = cudaLaunchAttributeClusterDimension;
+            attr[0].val.clusterDim.x = static_cast<unsigned>(2 * split);
+            attr[0].val.clusterDim.y = 1;
+            attr[0].val.clusterDim.z = 1;
+            cudaLaunchConfig_t cfg = {};
+            cfg.gridDim = dim3(static_cast<unsigned>(sms / (2 * split) * 2 * split), 1, 1);
+            cfg.blockDim = dim3(kManyThreads, 1, 1);
+            cfg.dynamicSmemBytes = ManyCfg::SMEM_BYTES;
+            cfg.attrs = attr;
+            cfg.numAttrs = 1;
+            int v = 0;
+            if (cudaOccupancyMaxActiveClusters(&v, kern, &cfg) != cudaSuccess || v <= 0) break;
+            mc = std::min(v, sms / (2 * split));
+            if (cached) resident[dev][i].store(mc, std::memory_order_relaxed);
+        }
+        const int64_t waves = (tiles + mc - 1) / mc;
+        const int64_t cost = waves * ((kb + split - 1) / split * kManyBlock + kManyWave + (split > 1 ? kManyJoin : 0));
+        if (best.cost < 0 || cost < best.cost) {
+            best.cost = cost;
+            best.split = split;
+            best.clusters = mc;
+        }
+    }
+    return best;
+}
+
+template <bool GLU>
+static tp_status launch_many(Fp8GemmArgs& a, const Fp8GemmDesc& d, const ManyPlan& plan, cudaStream_t stream) {
     using Cfg = ManyCfg;
     const int out_cols = GLU ? 128 : 256;
     a.m_tiles = static_cast<int>((d.M + 255) / 256);
@@ -1109,63 +1217,39 @@ static tp_status launch_many(Fp8GemmArgs& a, const Fp8GemmDesc& d, cudaStream_t 
         if (!make_byte_operand_map(&a.mapX[i], d.x[i], d.M, d.K, d.ldx, 128)) return TP_ERR_CUDA;
     for (int i = 0; i < nW; ++i)
         if (!make_byte_operand_map(&a.mapW[i], d.w[i], GLU ? 2 * d.N : d.N, d.K, d.ldw, 128)) return TP_ERR_CUDA;
-    auto kern = fp8_many_kernel<GLU>;
-    static std::atomic<uint64_t> smem_set{0};
-    if (!smem_attribute_once(reinterpret_cast<const void*>(kern), Cfg::SMEM_BYTES, smem_set)) return TP_ERR_CUDA;
-    const int sms = device_sms();
-    if (sms < 2) return TP_ERR_CUDA;
-    cudaLaunchConfig_t cfg = {};
-    cfg.blockDim = dim3(kManyThreads, 1, 1);
-    cfg.dynamicSmemBytes = Cfg::SMEM_BYTES;
-    cfg.stream = stream;
+    if (tiles * plan.split > INT32_MAX / 2) return TP_ERR_UNSUPPORTED;
+    a.split = plan.split;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = static_cast<unsigned>(2 * plan.split);
     attr[0].val.clusterDim.y = 1;
     attr[0].val.clusterDim.z = 1;
     attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[1].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    // clusters of 2, 4 and 8 CTAs that can be resident at once (per device)
-    static std::atomic<int> resident[64][3];             // relaxed: racing first calls store the same value
-    int dev = 0;
-    cudaGetDevice(&dev);
-    const bool cached = dev >= 0 && dev < 64;
-    const int kb_all = a.k_blocks * d.segs;
-    int best_split = 1, best_clusters = 0;
-    int64_t best = -1;
-    for (int i = 0; i < 3; ++i) {
-        const int split = 1 << i;
-        if (split > 1 && kb_all / split < 4) break;
-        int mc = cached ? resident[dev][i].load(std::memory_order_relaxed) : 0;
-        if (mc <= 0) {
-            attr[0].val.clusterDim.x = static_cast<unsigned>(2 * split);
-            cfg.numAttrs = 1;
-            cfg.gridDim = dim3(static_cast<unsigned>(sms / (2 * split) * 2 * split), 1, 1);
-            int v = 0;
-            if (cudaOccupancyMaxActiveClusters(&v, kern, &cfg) != cudaSuccess || v <= 0) {
-                if (split == 1) return TP_ERR_CUDA;
-                break;
-            }
-            mc = std::min(v, sms / (2 * split));
-            if (cached) resident[dev][i].store(mc, std::memory_order_relaxed);
-        }
-        const int64_t waves = (tiles + mc - 1) / mc;
-        const int64_t cost = waves * ((kb_all + split - 1) / split + kManyTileCost + (split > 1 ? kManyJoinCost : 0));
-        if (best < 0 || cost < best) {
-            best = cost;
-            best_split = split;
-            best_clusters = mc;
-        }
-    }
-    if (tiles * best_split > INT32_MAX / 2) return TP_ERR_UNSUPPORTED;
-    a.split = best_split;
+    cudaLaunchConfig_t cfg = {};
     // one pair a tile: a persistent grid; parts: a cluster a tile
-    const int64_t clusters = best_split == 1 ? std::min<int64_t>(tiles, best_clusters) : tiles;
-    attr[0].val.clusterDim.x = static_cast<unsigned>(2 * best_split);
-    cfg.gridDim = dim3(static_cast<unsigned>(clusters * 2 * best_split), 1, 1);
+    const int64_t clusters = plan.split == 1 ? std::min<int64_t>(tiles, plan.clusters) : tiles;
+    cfg.gridDim = dim3(static_cast<unsigned>(clusters * 2 * plan.split), 1, 1);
+    cfg.blockDim = dim3(kManyThreads, 1, 1);
+    cfg.dynamicSmemBytes = Cfg::SMEM_BYTES;
+    cfg.stream = stream;
+    cfg.attrs = attr;
     cfg.numAttrs = 2;
-    if (cudaLaunchKernelEx(&cfg, kern, a) != cudaSuccess) return TP_ERR_CUDA;
+    if (cudaLaunchKernelEx(&cfg, fp8_many_kernel<GLU>, a) != cudaSuccess) return TP_ERR_CUDA;
     return cudaGetLastError() == cudaSuccess ? TP_OK : TP_ERR_CUDA;
+}
+
+// More than 64 tokens: whichever kernel should take less time.
+template <bool GLU>
+static tp_status launch_either(Fp8GemmArgs& a, const Fp8GemmDesc& d, cudaStream_t stream) {
+    const int sms = device_sms();
+    if (sms < 2) return TP_ERR_CUDA;
+    static std::atomic<uint64_t> smem_set{0};
+    if (!smem_attribute_once(reinterpret_cast<const void*>(fp8_many_kernel<GLU>), ManyCfg::SMEM_BYTES, smem_set)) return TP_ERR_CUDA;
+    const ManyPlan plan = plan_many<GLU>(d, sms);
+    if (plan.cost < 0) return TP_ERR_CUDA;
+    if (few_cost(d, sms) < plan.cost) return launch_few<128, GLU>(a, d, stream);
+    return launch_many<GLU>(a, d, plan, stream);
 }
 
 tp_status launch_fp8_gemm(const Fp8GemmDesc& d, cudaStream_t stream) {
@@ -1194,17 +1278,16 @@ tp_status launch_fp8_gemm(const Fp8GemmDesc& d, cudaStream_t stream) {
     a.status = d.status;
     a.weights_first = d.weights_first;
     if (static_cast<int64_t>(d.groups) * ((d.M + 127) / 128) * ((d.N + 127) / 128) > INT32_MAX / 8) return TP_ERR_UNSUPPORTED;
-    if (d.M > 128) return d.glu ? launch_many<true>(a, d, stream) : launch_many<false>(a, d, stream);
     if (d.glu) {
         if (d.M <= 16) return launch_few<16, true>(a, d, stream);
         if (d.M <= 32) return launch_few<32, true>(a, d, stream);
         if (d.M <= 64) return launch_few<64, true>(a, d, stream);
-        return launch_few<128, true>(a, d, stream);
+        return launch_either<true>(a, d, stream);
     }
     if (d.M <= 16) return launch_few<16, false>(a, d, stream);
     if (d.M <= 32) return launch_few<32, false>(a, d, stream);
     if (d.M <= 64) return launch_few<64, false>(a, d, stream);
-    return launch_few<128, false>(a, d, stream);
+    return launch_either<false>(a, d, stream);
 }
 
 }  // namespace tpk
