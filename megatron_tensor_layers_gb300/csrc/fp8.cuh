@@ -80,39 +80,51 @@ struct Fp8Quotient {
         s = pack2(sr, sr);
         nr = pack2(-r, -r);
     }
-    __device__ __forceinline__ void operator()(float a, float b, float& qa, float& qb) const {
-        const f32x2 nx = mul2(pack2(a, b), nf);
+    __device__ __forceinline__ f32x2 operator()(f32x2 x) const {
+        const f32x2 nx = mul2(x, nf);
         const f32x2 q0 = mul2(nx, nr);
         const f32x2 q1 = fma2(fma2(q0, s, nx), nr, q0);
-        unpack2(fma2(fma2(q1, s, nx), nr, q1), qa, qb);
+        return fma2(fma2(q1, s, nx), nr, q1);
     }
 };
 
 // Codes of four values.
 __device__ __forceinline__ uint32_t fp8_codes4(float a, float b, float c, float d, const Fp8Quotient& q) {
     float x, y, z, w;
-    q(a, b, x, y);
-    q(c, d, z, w);
+    unpack2(q(pack2(a, b)), x, y);
+    unpack2(q(pack2(c, d)), z, w);
+    return e4m3x4(x, y, z, w);
+}
+__device__ __forceinline__ uint32_t fp8_codes4(f32x2 ab, f32x2 cd, const Fp8Quotient& q) {
+    float x, y, z, w;
+    unpack2(q(ab), x, y);
+    unpack2(q(cd), z, w);
     return e4m3x4(x, y, z, w);
 }
 
 // act(g) of a gated block as g / (1 + exp(-z)): SiLU has z = g, and GeLU-tanh's
 // 0.5 g (1 + tanh(u)) is z = 2 u with u = sqrt(2/pi) (g + 0.044715 g^3).  With
 // coefficients in place of a branch, exp as 2^(g (a + b g^2)), and the hardware's
-// 2^x and reciprocal (2^-22 and 1 ulp).
+// 2^x and reciprocal (2^-22 and 1 ulp); two values at a time.
 struct GateAct {
-    float a, b;
+    f32x2 a, b;
     __device__ __forceinline__ explicit GateAct(int act) {
         constexpr float log2e = 1.4426950408889634f, k = 2.0f * 0.7978845608028654f;
-        a = act == TP_ACT_GELU_TANH_MUL ? -k * log2e : -log2e;
-        b = act == TP_ACT_GELU_TANH_MUL ? -k * 0.044715f * log2e : 0.0f;
+        const bool gelu = act == TP_ACT_GELU_TANH_MUL;
+        const float fa = gelu ? -k * log2e : -log2e, fb = gelu ? -k * 0.044715f * log2e : 0.0f;
+        a = pack2(fa, fa);
+        b = pack2(fb, fb);
     }
-    __device__ __forceinline__ float operator()(float g) const {
-        const float g2 = fminf(g * g, 3.0e38f);          // finite: b may be 0
-        float e, r;
-        asm("ex2.approx.f32 %0, %1;" : "=f"(e) : "f"(g * fmaf(b, g2, a)));
-        asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(1.0f + e));
-        return g * r;
+    __device__ __forceinline__ f32x2 operator()(f32x2 g) const {
+        float s0, s1, e0, e1;
+        unpack2(mul2(g, g), s0, s1);
+        const f32x2 g2 = pack2(fminf(s0, 3.0e38f), fminf(s1, 3.0e38f));       // finite: b may be 0
+        unpack2(mul2(g, fma2(b, g2, a)), s0, s1);
+        asm("ex2.approx.f32 %0, %1;" : "=f"(e0) : "f"(s0));
+        asm("ex2.approx.f32 %0, %1;" : "=f"(e1) : "f"(s1));
+        asm("rcp.approx.f32 %0, %1;" : "=f"(s0) : "f"(1.0f + e0));
+        asm("rcp.approx.f32 %0, %1;" : "=f"(s1) : "f"(1.0f + e1));
+        return mul2(g, pack2(s0, s1));
     }
 };
 

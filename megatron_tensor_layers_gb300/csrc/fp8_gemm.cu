@@ -129,8 +129,8 @@ __device__ __forceinline__ void finish_gated(const Fp8GemmArgs& args, int g, int
     const int nvalid = args.N - col;                     // this lane's columns inside the group
     const GateAct act(args.act);
     float v[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = act(gate[i]) * up[i];
+    unpack2(mul2(act(pack2(gate[0], gate[1])), pack2(up[0], up[1])), v[0], v[1]);
+    unpack2(mul2(act(pack2(gate[2], gate[3])), pack2(up[2], up[3])), v[2], v[3]);
     if (args.out_kind == FP8_OUT_CODES) {
         float top = 0.0f;
 #pragma unroll
@@ -630,6 +630,42 @@ __device__ __forceinline__ void many_store(const uint8_t* st, uint8_t* out, int6
     __syncwarp();
 }
 
+// A warp's rows of 2 * PAIRS columns from col0 on, as fp32 or bf16.
+template <int PAIRS>
+__device__ __forceinline__ void store_sums(const Fp8GemmArgs& args, uint8_t* st, uint8_t* out, int64_t row0, int live,
+                                           int col0, int valid, int lane, const f32x2 (&v)[PAIRS]) {
+    uint8_t* st_lane = st + lane * ManyCfg::STG_PITCH;
+    if (args.out_kind == FP8_OUT_F32) {
+#pragma unroll
+        for (int c = 0; c < PAIRS; c += 8) {
+#pragma unroll
+            for (int j = 0; j < 8; j += 2) {
+                float4 x;
+                unpack2(v[c + j], x.x, x.y);
+                unpack2(v[c + j + 1], x.z, x.w);
+                *reinterpret_cast<float4*>(st_lane + j * 8) = x;
+            }
+            many_store<4>(st, out, row0, live, args.ldo * 4, (col0 + 2 * c) * 4LL, (valid - 2 * c) * 4, lane);
+        }
+    } else {
+#pragma unroll
+        for (int c = 0; c < PAIRS; c += 16) {
+#pragma unroll
+            for (int j = 0; j < 16; j += 4) {
+                uint32_t x[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    float lo, hi;
+                    unpack2(v[c + j + i], lo, hi);
+                    x[i] = pack_bf16x2(lo, hi);
+                }
+                *reinterpret_cast<uint4*>(st_lane + j * 4) = make_uint4(x[0], x[1], x[2], x[3]);
+            }
+            many_store<2>(st, out, row0, live, args.ldo * 2, (col0 + 2 * c) * 2LL, (valid - 2 * c) * 2, lane);
+        }
+    }
+}
+
 template <bool GLU>
 __global__ void __launch_bounds__(kManyThreads, 1) fp8_many_kernel(const __grid_constant__ Fp8GemmArgs args) {
     using Cfg = ManyCfg;
@@ -900,29 +936,38 @@ __global__ void __launch_bounds__(kManyThreads, 1) fp8_many_kernel(const __grid_
                 }
             }
             if (aborted) break;
-            float acc[128];
-#pragma unroll
-            for (int j = 0; j < 64; ++j) unpack2(sums[j], acc[2 * j], acc[2 * j + 1]);
             const int64_t row0 = static_cast<int64_t>(m) * 256 + static_cast<int64_t>(rank) * 128 + q * 32;
             const int live = static_cast<int>(min(static_cast<int64_t>(32), args.M - row0));   // rows of this warp
             if (split > 1) {
                 // this CTA's sums to the ring, a row of 256 at SUM_PITCH; joined below
                 float* to = reinterpret_cast<float*>(base_ptr) + (q * 32 + lane) * Cfg::SUM_PITCH;
 #pragma unroll
-                for (int j = 0; j < 128; j += 4)
-                    *reinterpret_cast<float4*>(to + (j < 64 ? col_a + j : col_b + j - 64)) =
-                        make_float4(acc[j], acc[j + 1], acc[j + 2], acc[j + 3]);
+                for (int j = 0; j < 128; j += 4) {
+                    float4 v;
+                    unpack2(sums[j / 2], v.x, v.y);
+                    unpack2(sums[j / 2 + 1], v.z, v.w);
+                    *reinterpret_cast<float4*>(to + (j < 64 ? col_a + j : col_b + j - 64)) = v;
+                }
             } else if (GLU) {
                 const GateAct act(args.act);
                 uint8_t* out = static_cast<uint8_t*>(args.out[g]);
                 const int col0 = n * 128 + half * 64;
                 const int valid = args.N - col0;          // columns of this half inside the group
+                f32x2 v[32];
 #pragma unroll
-                for (int j = 0; j < 64; ++j) acc[j] = act(acc[j]) * acc[64 + j];
+                for (int j = 0; j < 32; ++j) v[j] = mul2(act(sums[j]), sums[32 + j]);
                 if (args.out_kind == FP8_OUT_CODES) {
+                    if (valid < 64) {                     // N is a multiple of 16: pairs are in or out
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) v[j] = 2 * j < valid ? v[j] : 0;
+                    }
                     float top = 0.0f;
 #pragma unroll
-                    for (int j = 0; j < 64; ++j) top = j < valid ? max_nan(top, fabsf(acc[j])) : top;
+                    for (int j = 0; j < 32; ++j) {
+                        float lo, hi;
+                        unpack2(v[j], lo, hi);
+                        top = max_nan(top, max_nan(fabsf(lo), fabsf(hi)));
+                    }
                     float* mine = amax + turn * 256;
                     mine[half * 128] = top;
                     __syncwarp();
@@ -938,35 +983,14 @@ __global__ void __launch_bounds__(kManyThreads, 1) fp8_many_kernel(const __grid_
                     if (live > 0 && valid > 0) {
                         const Fp8Quotient quot(s);
 #pragma unroll
-                        for (int j = 0; j < 64; j += 16)
-                            *reinterpret_cast<uint4*>(st_lane + j) =
-                                make_uint4(fp8_codes4(acc[j], acc[j + 1], acc[j + 2], acc[j + 3], quot),
-                                           fp8_codes4(acc[j + 4], acc[j + 5], acc[j + 6], acc[j + 7], quot),
-                                           fp8_codes4(acc[j + 8], acc[j + 9], acc[j + 10], acc[j + 11], quot),
-                                           fp8_codes4(acc[j + 12], acc[j + 13], acc[j + 14], acc[j + 15], quot));
+                        for (int j = 0; j < 32; j += 8)
+                            *reinterpret_cast<uint4*>(st_lane + j * 2) =
+                                make_uint4(fp8_codes4(v[j], v[j + 1], quot), fp8_codes4(v[j + 2], v[j + 3], quot),
+                                           fp8_codes4(v[j + 4], v[j + 5], quot), fp8_codes4(v[j + 6], v[j + 7], quot));
                         many_store<1>(st, out, row0, live, args.ldo, col0, valid, lane);
                     }
                 } else if (live > 0 && valid > 0) {
-                    if (args.out_kind == FP8_OUT_F32) {
-#pragma unroll
-                        for (int c = 0; c < 64; c += 16) {
-#pragma unroll
-                            for (int j = 0; j < 16; j += 4)
-                                *reinterpret_cast<float4*>(st_lane + j * 4) =
-                                    make_float4(acc[c + j], acc[c + j + 1], acc[c + j + 2], acc[c + j + 3]);
-                            many_store<4>(st, out, row0, live, args.ldo * 4, (col0 + c) * 4LL, (valid - c) * 4, lane);
-                        }
-                    } else {
-#pragma unroll
-                        for (int c = 0; c < 64; c += 32) {
-#pragma unroll
-                            for (int j = 0; j < 32; j += 8)
-                                *reinterpret_cast<uint4*>(st_lane + j * 2) =
-                                    make_uint4(pack_bf16x2(acc[c + j], acc[c + j + 1]), pack_bf16x2(acc[c + j + 2], acc[c + j + 3]),
-                                               pack_bf16x2(acc[c + j + 4], acc[c + j + 5]), pack_bf16x2(acc[c + j + 6], acc[c + j + 7]));
-                            many_store<2>(st, out, row0, live, args.ldo * 2, (col0 + c) * 2LL, (valid - c) * 2, lane);
-                        }
-                    }
+                    store_sums<32>(args, st, out, row0, live, col0, valid, lane, v);
                 }
             } else {
                 uint8_t* out = static_cast<uint8_t*>(args.out[g]);
@@ -976,31 +1000,20 @@ __global__ void __launch_bounds__(kManyThreads, 1) fp8_many_kernel(const __grid_
                     const int col0 = n * 256 + p * 128 + half * 64;
                     const int valid = args.N - col0;
                     if (live <= 0 || valid <= 0) break;
+                    f32x2 v[32];
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) v[j] = sums[p * 32 + j];
                     if (bias != nullptr) {
 #pragma unroll
-                        for (int j = 0; j < 64; ++j)
-                            if (j < valid) acc[p * 64 + j] += bf16_to_f32(bias[col0 + j]);
-                    }
-                    if (args.out_kind == FP8_OUT_F32) {
-#pragma unroll
-                        for (int c = 0; c < 64; c += 16) {
-#pragma unroll
-                            for (int j = p * 64 + c; j < p * 64 + c + 16; j += 4)
-                                *reinterpret_cast<float4*>(st_lane + (j - p * 64 - c) * 4) =
-                                    make_float4(acc[j], acc[j + 1], acc[j + 2], acc[j + 3]);
-                            many_store<4>(st, out, row0, live, args.ldo * 4, (col0 + c) * 4LL, (valid - c) * 4, lane);
-                        }
-                    } else {
-#pragma unroll
-                        for (int c = 0; c < 64; c += 32) {
-#pragma unroll
-                            for (int j = p * 64 + c; j < p * 64 + c + 32; j += 8)
-                                *reinterpret_cast<uint4*>(st_lane + (j - p * 64 - c) * 2) =
-                                    make_uint4(pack_bf16x2(acc[j], acc[j + 1]), pack_bf16x2(acc[j + 2], acc[j + 3]),
-                                               pack_bf16x2(acc[j + 4], acc[j + 5]), pack_bf16x2(acc[j + 6], acc[j + 7]));
-                            many_store<2>(st, out, row0, live, args.ldo * 2, (col0 + c) * 2LL, (valid - c) * 2, lane);
+                        for (int j = 0; j < 32; ++j) {
+                            float lo, hi;
+                            unpack2(v[j], lo, hi);
+                            if (2 * j < valid) lo += bf16_to_f32(bias[col0 + 2 * j]);
+                            if (2 * j + 1 < valid) hi += bf16_to_f32(bias[col0 + 2 * j + 1]);
+                            v[j] = pack2(lo, hi);
                         }
                     }
+                    store_sums<32>(args, st, out, row0, live, col0, valid, lane, v);
                 }
             }
         }
