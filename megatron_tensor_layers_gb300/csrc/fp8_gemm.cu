@@ -1077,40 +1077,87 @@ __global__ void __launch_bounds__(kManyThreads, 1) fp8_many_kernel(const __grid_
 
 // ------------------------------------------------------------------ host
 
-// Costs of a wave in hundredths of a microsecond, from both kernels' times: the 128-token few-row kernel takes 0.34 us
-// a K block (gated 0.88) and 3 us beside them, the many-row kernel 0.50 and 3.5, and 3 more where parts are joined.
-// Times that the weight stream bounds are below both; the comparison stands there too (100 tokens, four shards of the
-// down projection: few 44 us, many 64; 300 tokens, QKV of eight shards: few 48, many 72; gate_up of 100: few
-// 112, many 104).
-constexpr int64_t kFewBlock = 34, kFewGatedBlock = 88, kFewWave = 300;
+// Costs in hundredths of a microsecond, fitted to both kernels' times.  A wave of the few-row kernel takes so much a K block (by
+// its tokens, plain and gated; from memory, with nothing else to wait for) and 260 beside them, parts that are joined 30
+// and 15 each; a wave of the many-row kernel 50 a block, 350, and 300 where parts are joined.  Neither is less than the
+// weights take, at 6.4 TB/s with 240 CTAs and a little less with fewer (the down projection of 32 tokens: 5.5 TB/s with
+// 128, 6.2 with 256).
+constexpr int64_t few_block_cost(int nt, bool glu) {
+    return nt <= 16 ? (glu ? 35 : 26) : nt <= 32 ? (glu ? 40 : 28) : nt <= 64 ? (glu ? 50 : 44) : (glu ? 88 : 33);
+}
+constexpr int64_t kFewWave = 260, kFewJoin = 30, kFewPart = 15;
 constexpr int64_t kManyBlock = 50, kManyWave = 350, kManyJoin = 300;
 
-// CTAs that share a few-row tile: as many as all find a place at once, with eight K blocks each at least.  QKV of 8
-// shards (80 tiles, 304 places), 16 tokens: 18.4, 17.9, 15.9, 20.0 us in 1, 2, 3, 4 parts; the down projection of 32
-// tokens (64 tiles of 224 blocks) 65, 41, 40, 38, 46 us in 1 to 5; 8 tiles of 32 blocks 7.5, 5.4, 4.7, 4.1, 4.1,
-// 4.4, 4.2 in 1 to 6 and 8.
-static int few_split(int64_t tiles, int64_t kb_all, int64_t places) {
-    return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({places / tiles, kb_all / 8, 8})));
+static int64_t stream_cost(const Fp8GemmDesc& d, int64_t ctas) {
+    const int64_t bytes = d.groups * d.segs * d.N * (d.glu ? 2 : 1) * d.K;
+    return bytes / 64000 * 24000 / (20400 + 15 * std::min<int64_t>(ctas, 240));
 }
 
-static int64_t few_tiles(const Fp8GemmDesc& d, int nt) { return d.groups * ((d.M + nt - 1) / nt) * ((d.N + 127) / 128); }
+// Clusters of `size` CTAs of a kernel that can be resident at once, looked up once per device (cache: the kernel's).
+static int resident_clusters(const void* kern, int size, int threads, int smem, std::atomic<int>* cache) {
+    int dev = 0;
+    cudaGetDevice(&dev);
+    std::atomic<int>* slot = dev >= 0 && dev < 64 ? cache + dev : nullptr;       // relaxed: racing first calls store the same value
+    if (slot != nullptr && slot->load(std::memory_order_relaxed) != 0) return slot->load(std::memory_order_relaxed);
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = static_cast<unsigned>(size);
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(std::max(1, device_sms()) / size * size * 2), 1, 1);
+    cfg.blockDim = dim3(static_cast<unsigned>(threads), 1, 1);
+    cfg.dynamicSmemBytes = static_cast<size_t>(smem);
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    int v = 0;
+    if (cudaOccupancyMaxActiveClusters(&v, kern, &cfg) != cudaSuccess || v <= 0) v = -1;
+    if (slot != nullptr) slot->store(v, std::memory_order_relaxed);
+    return v;
+}
 
-static int64_t few_cost(const Fp8GemmDesc& d, int sms) {
-    const int64_t tiles = few_tiles(d, 128), kb = fp8_groups(d.K) * d.segs;
-    const int split = few_split(tiles, kb, sms);
-    const int64_t waves = (tiles * split + sms - 1) / sms;
-    return waves * ((kb + split - 1) / split * (d.glu ? kFewGatedBlock : kFewBlock) + kFewWave);
+struct Fp8Plan {
+    int split = 1, clusters = 0;
+    int64_t cost = -1;                   // none possible
+};
+
+// The number of CTAs (1 to 8) that share a tile, with two K blocks each at least, and what that costs.  What the sizes of
+// clusters that fit the GPU at once decide most: QKV of 8 shards (80 tiles), 16 tokens: 18.4, 17.9, 15.9, 20.0 us in 1, 2, 3, 4
+// parts; the down projection of 32 tokens (64 tiles of 224 blocks) 65, 41, 40, 38, 46 us in 1 to 5; 8 tiles of 32 blocks
+// 7.5, 5.4, 4.7, 4.1, 4.1, 4.2 us in 1 to 5 and 8.
+template <int NT, bool GLU>
+static Fp8Plan plan_few(const Fp8GemmDesc& d) {
+    using Cfg = FewCfg<NT, GLU>;
+    static std::atomic<int> resident[8][64];
+    static std::atomic<uint64_t> smem_set{0};
+    Fp8Plan best;
+    const void* kern = reinterpret_cast<const void*>(fp8_few_kernel<NT, GLU>);
+    if (!smem_attribute_once(kern, Cfg::SMEM_BYTES, smem_set)) return best;
+    const int64_t tiles = d.groups * ((d.M + NT - 1) / NT) * ((d.N + 127) / 128), kb = fp8_groups(d.K) * d.segs;
+    for (int split = 1; split <= 8 && (split == 1 || kb / split >= 2); ++split) {
+        // the occupancy query counts one CTA an SM of every kernel here; the times show that two of the smaller ones share it
+        const int mc = resident_clusters(kern, split, Cfg::THREADS, Cfg::SMEM_BYTES, resident[split - 1]) * (Cfg::ONE ? 1 : 2);
+        if (mc <= 0) continue;
+        const int64_t waves = (tiles + mc - 1) / mc;
+        const int64_t stream = stream_cost(d, std::min<int64_t>(tiles, mc) * split);
+        const int64_t cost = std::max(waves * ((kb + split - 1) / split) * few_block_cost(NT, GLU), stream) + waves * kFewWave +
+                             (split > 1 ? kFewJoin + kFewPart * split : 0);
+        if (best.cost < 0 || cost < best.cost) {
+            best.cost = cost;
+            best.split = split;
+        }
+    }
+    return best;
 }
 
 template <int NT, bool GLU>
-static tp_status launch_few(Fp8GemmArgs& a, const Fp8GemmDesc& d, cudaStream_t stream) {
+static tp_status launch_few(Fp8GemmArgs& a, const Fp8GemmDesc& d, const Fp8Plan& plan, cudaStream_t stream) {
     using Cfg = FewCfg<NT, GLU>;
     a.m_tiles = static_cast<int>((d.M + NT - 1) / NT);
     a.n_tiles = static_cast<int>((d.N + 127) / 128);
     const int64_t tiles = static_cast<int64_t>(d.groups) * a.m_tiles * a.n_tiles;
-    const int sms = device_sms();
-    if (sms <= 0) return TP_ERR_CUDA;
-    const int split = few_split(tiles, static_cast<int64_t>(a.k_blocks) * d.segs, static_cast<int64_t>(sms) * (Cfg::ONE ? 1 : 2));
+    if (plan.cost < 0) return TP_ERR_CUDA;
+    const int split = plan.split;
     if (tiles * split > INT32_MAX) return TP_ERR_UNSUPPORTED;
     a.total_tiles = static_cast<int>(tiles);
     a.split = split;
@@ -1122,8 +1169,6 @@ static tp_status launch_few(Fp8GemmArgs& a, const Fp8GemmDesc& d, cudaStream_t s
     for (int i = 0; i < nW; ++i)
         if (!make_byte_operand_map(&a.mapW[i], d.w[i], GLU ? 2 * d.N : d.N, d.K, d.ldw, 128)) return TP_ERR_CUDA;
     auto kern = fp8_few_kernel<NT, GLU>;
-    static std::atomic<uint64_t> smem_set{0};
-    if (!smem_attribute_once(reinterpret_cast<const void*>(kern), Cfg::SMEM_BYTES, smem_set)) return TP_ERR_CUDA;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(tiles * split), 1, 1);
     cfg.blockDim = dim3(Cfg::THREADS, 1, 1);
@@ -1143,45 +1188,23 @@ static tp_status launch_few(Fp8GemmArgs& a, const Fp8GemmDesc& d, cudaStream_t s
 }
 
 // CTA pairs: 256 x 256 tiles, whose K blocks are split over 1, 2 or 4 pairs, whichever takes the least.
-struct ManyPlan {
-    int split = 1, clusters = 0;
-    int64_t cost = -1;
-};
-
 template <bool GLU>
-static ManyPlan plan_many(const Fp8GemmDesc& d, int sms) {
-    // clusters of 2, 4 and 8 CTAs that can be resident at once (per device)
-    static std::atomic<int> resident[64][3];             // relaxed: racing first calls store the same value
-    auto kern = fp8_many_kernel<GLU>;
-    int dev = 0;
-    cudaGetDevice(&dev);
-    const bool cached = dev >= 0 && dev < 64;
+static Fp8Plan plan_many(const Fp8GemmDesc& d) {
+    static std::atomic<int> resident[3][64];
+    static std::atomic<uint64_t> smem_set{0};
+    Fp8Plan best;
+    const void* kern = reinterpret_cast<const void*>(fp8_many_kernel<GLU>);
+    if (!smem_attribute_once(kern, ManyCfg::SMEM_BYTES, smem_set)) return best;
     const int64_t tiles = d.groups * ((d.M + 255) / 256) * ((d.N + (GLU ? 127 : 255)) / (GLU ? 128 : 256));
     const int64_t kb = fp8_groups(d.K) * d.segs;
-    ManyPlan best;
     for (int i = 0; i < 3; ++i) {
         const int split = 1 << i;
         if (split > 1 && kb / split < 4) break;
-        int mc = cached ? resident[dev][i].load(std::memory_order_relaxed) : 0;
-        if (mc <= 0) {
-            cudaLaunchAttribute attr[1];
-            attr[0].id = cudaLaunchAttributeClusterDimension;
-            attr[0].val.clusterDim.x = static_cast<unsigned>(2 * split);
-            attr[0].val.clusterDim.y = 1;
-            attr[0].val.clusterDim.z = 1;
-            cudaLaunchConfig_t cfg = {};
-            cfg.gridDim = dim3(static_cast<unsigned>(sms / (2 * split) * 2 * split), 1, 1);
-            cfg.blockDim = dim3(kManyThreads, 1, 1);
-            cfg.dynamicSmemBytes = ManyCfg::SMEM_BYTES;
-            cfg.attrs = attr;
-            cfg.numAttrs = 1;
-            int v = 0;
-            if (cudaOccupancyMaxActiveClusters(&v, kern, &cfg) != cudaSuccess || v <= 0) break;
-            mc = std::min(v, sms / (2 * split));
-            if (cached) resident[dev][i].store(mc, std::memory_order_relaxed);
-        }
+        const int mc = resident_clusters(kern, 2 * split, kManyThreads, ManyCfg::SMEM_BYTES, resident[i]);
+        if (mc <= 0) continue;
         const int64_t waves = (tiles + mc - 1) / mc;
-        const int64_t cost = waves * ((kb + split - 1) / split * kManyBlock + kManyWave + (split > 1 ? kManyJoin : 0));
+        const int64_t stream = stream_cost(d, std::min<int64_t>(tiles, mc) * split * 2);
+        const int64_t cost = std::max(waves * ((kb + split - 1) / split) * kManyBlock, stream) + waves * (kManyWave + (split > 1 ? kManyJoin : 0));
         if (best.cost < 0 || cost < best.cost) {
             best.cost = cost;
             best.split = split;
@@ -1192,7 +1215,7 @@ static ManyPlan plan_many(const Fp8GemmDesc& d, int sms) {
 }
 
 template <bool GLU>
-static tp_status launch_many(Fp8GemmArgs& a, const Fp8GemmDesc& d, const ManyPlan& plan, cudaStream_t stream) {
+static tp_status launch_many(Fp8GemmArgs& a, const Fp8GemmDesc& d, const Fp8Plan& plan, cudaStream_t stream) {
     using Cfg = ManyCfg;
     const int out_cols = GLU ? 128 : 256;
     a.m_tiles = static_cast<int>((d.M + 255) / 256);
@@ -1230,17 +1253,23 @@ static tp_status launch_many(Fp8GemmArgs& a, const Fp8GemmDesc& d, const ManyPla
     return cudaGetLastError() == cudaSuccess ? TP_OK : TP_ERR_CUDA;
 }
 
-// More than 64 tokens: whichever kernel should take less time.
+template <int NT, bool GLU>
+static tp_status run_few(Fp8GemmArgs& a, const Fp8GemmDesc& d, cudaStream_t stream) {
+    return launch_few<NT, GLU>(a, d, plan_few<NT, GLU>(d), stream);
+}
+
+// Up to 64 tokens one tile of them; more: whichever kernel and tile should take least.  100 tokens of four shards' down projection:
+// 44 us in tiles of 128, 64 on CTA pairs; 300 in QKV of eight shards 48 and 72; gate_up of 100 tokens 112 and 104.
 template <bool GLU>
-static tp_status launch_either(Fp8GemmArgs& a, const Fp8GemmDesc& d, cudaStream_t stream) {
-    const int sms = device_sms();
-    if (sms < 2) return TP_ERR_CUDA;
-    static std::atomic<uint64_t> smem_set{0};
-    if (!smem_attribute_once(reinterpret_cast<const void*>(fp8_many_kernel<GLU>), ManyCfg::SMEM_BYTES, smem_set)) return TP_ERR_CUDA;
-    const ManyPlan plan = plan_many<GLU>(d, sms);
-    if (plan.cost < 0) return TP_ERR_CUDA;
-    if (few_cost(d, sms) < plan.cost) return launch_few<128, GLU>(a, d, stream);
-    return launch_many<GLU>(a, d, plan, stream);
+static tp_status launch_sized(Fp8GemmArgs& a, const Fp8GemmDesc& d, cudaStream_t stream) {
+    if (d.M <= 16) return run_few<16, GLU>(a, d, stream);
+    if (d.M <= 32) return run_few<32, GLU>(a, d, stream);
+    if (d.M <= 64) return run_few<64, GLU>(a, d, stream);
+    const Fp8Plan many = plan_many<GLU>(d), few = plan_few<128, GLU>(d), fewer = plan_few<64, GLU>(d);
+    if (many.cost < 0 || few.cost < 0 || fewer.cost < 0) return TP_ERR_CUDA;
+    if (many.cost <= few.cost && many.cost <= fewer.cost) return launch_many<GLU>(a, d, many, stream);
+    if (few.cost <= fewer.cost) return launch_few<128, GLU>(a, d, few, stream);
+    return launch_few<64, GLU>(a, d, fewer, stream);
 }
 
 tp_status launch_fp8_gemm(const Fp8GemmDesc& d, cudaStream_t stream) {
@@ -1269,16 +1298,7 @@ tp_status launch_fp8_gemm(const Fp8GemmDesc& d, cudaStream_t stream) {
     a.status = d.status;
     a.weights_first = d.weights_first;
     if (static_cast<int64_t>(d.groups) * ((d.M + 127) / 128) * ((d.N + 127) / 128) > INT32_MAX / 8) return TP_ERR_UNSUPPORTED;
-    if (d.glu) {
-        if (d.M <= 16) return launch_few<16, true>(a, d, stream);
-        if (d.M <= 32) return launch_few<32, true>(a, d, stream);
-        if (d.M <= 64) return launch_few<64, true>(a, d, stream);
-        return launch_either<true>(a, d, stream);
-    }
-    if (d.M <= 16) return launch_few<16, false>(a, d, stream);
-    if (d.M <= 32) return launch_few<32, false>(a, d, stream);
-    if (d.M <= 64) return launch_few<64, false>(a, d, stream);
-    return launch_either<false>(a, d, stream);
+    return d.glu ? launch_sized<true>(a, d, stream) : launch_sized<false>(a, d, stream);
 }
 
 }  // namespace tpk
