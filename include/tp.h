@@ -434,6 +434,10 @@ tp_status tp_shard_gather(int t, int64_t rows, const int64_t* cols, tp_dtype dty
  * with few output tiles, in up to eight runs of consecutive groups that are
  * added in order).  A product of two scales outside fp32's range is an
  * infinity or loses bits as in fp32 arithmetic.
+ *
+ * Sizes of the products (n, in, out, h, f) are at most 2^29
+ * (TP_ERR_INVALID_ARG), a weight to be quantised has at most 65535 blocks of
+ * rows (TP_ERR_UNSUPPORTED).
  * ---------------------------------------------------------------------
  */
 

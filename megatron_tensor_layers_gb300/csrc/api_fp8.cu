@@ -22,6 +22,9 @@ inline cudaStream_t cs(tp_stream s) { return reinterpret_cast<cudaStream_t>(s); 
         if (!(cond)) return (code); \
     } while (0)
 
+// Rows and columns of a product: twice as many, and a tile more, still count in 32 bits.
+constexpr int64_t kMaxSize = int64_t(1) << 29;
+
 // Row strides of codes (bytes), multiples of 16 as the TMA tiles need.
 inline bool codes_ld_ok(int64_t ld, int64_t minimum) { return ld >= minimum && ld % 16 == 0; }
 
@@ -32,7 +35,7 @@ struct HiddenLayout {
 
 bool hidden_layout(int t, int64_t n, int64_t h, int64_t f, tp_reduce_mode mode, tp_dtype pdt, HiddenLayout& l) {
     if (t < 1 || t > TP_MAX_SHARDS || n < 0 || h <= 0 || f <= 0 || f % t != 0 || !dtype_ok(pdt)) return false;
-    if (n > INT32_MAX || h > INT32_MAX || f > INT32_MAX) return false;
+    if (n > kMaxSize || h > kMaxSize || f > kMaxSize) return false;
     if (mode != TP_REDUCE_DIRECT && mode != TP_REDUCE_RING && mode != TP_REDUCE_FUSED) return false;
     l.codes = align256(static_cast<size_t>(n) * static_cast<size_t>(f));
     l.scales_each = align256(static_cast<size_t>(tpk::fp8_groups(f / t)) * static_cast<size_t>(n) * 4);
@@ -184,7 +187,7 @@ tp_status tp_fp8_linear_col(int t, int64_t n, int64_t in, int64_t out_full, cons
                             int y_kind, float* const* ys, int64_t ldys, tp_stream stream) {
     TP_CHECK(t >= 1 && t <= TP_MAX_SHARDS, TP_ERR_INVALID_ARG);
     TP_CHECK(n >= 0 && in > 0 && out_full > 0, TP_ERR_INVALID_ARG);
-    TP_CHECK(n <= INT32_MAX && out_full <= INT32_MAX / 2 && in <= INT32_MAX, TP_ERR_INVALID_ARG);
+    TP_CHECK(n <= kMaxSize && out_full <= kMaxSize && in <= kMaxSize, TP_ERR_INVALID_ARG);
     TP_CHECK((x != nullptr && xs != nullptr) || n == 0, TP_ERR_INVALID_ARG);
     TP_CHECK(w != nullptr && ws != nullptr && y != nullptr, TP_ERR_INVALID_ARG);
     TP_CHECK(act == TP_ACT_NONE || act == TP_ACT_SILU_MUL || act == TP_ACT_GELU_TANH_MUL, TP_ERR_INVALID_ARG);
@@ -233,7 +236,7 @@ static tp_status linear_row_impl(int t, int64_t n, int64_t in_full, int64_t out,
                                  tp_dtype y_dtype, int weights_first, tp_stream stream) {
     TP_CHECK(t >= 1 && t <= TP_MAX_SHARDS, TP_ERR_INVALID_ARG);
     TP_CHECK(n >= 0 && in_full > 0 && out > 0, TP_ERR_INVALID_ARG);
-    TP_CHECK(n <= INT32_MAX && out <= INT32_MAX && in_full <= INT32_MAX, TP_ERR_INVALID_ARG);
+    TP_CHECK(n <= kMaxSize && out <= kMaxSize && in_full <= kMaxSize, TP_ERR_INVALID_ARG);
     TP_CHECK(x != nullptr && xs != nullptr && w != nullptr && ws != nullptr, TP_ERR_INVALID_ARG);
     TP_CHECK(reduce_results == 0 || reduce_results == 1, TP_ERR_INVALID_ARG);
     TP_CHECK(mode == TP_REDUCE_DIRECT || mode == TP_REDUCE_RING || mode == TP_REDUCE_FUSED, TP_ERR_INVALID_ARG);
@@ -323,7 +326,7 @@ tp_status tp_fp8_mlp_forward(int t, int64_t n, int64_t h, int64_t f, const void*
                              void* workspace, size_t workspace_bytes, void* y, tp_dtype y_dtype, tp_stream stream) {
     TP_CHECK(t >= 1 && t <= TP_MAX_SHARDS, TP_ERR_INVALID_ARG);
     TP_CHECK(n >= 0 && h > 0 && f > 0, TP_ERR_INVALID_ARG);
-    TP_CHECK(n <= INT32_MAX && h <= INT32_MAX && f <= INT32_MAX / 2, TP_ERR_INVALID_ARG);
+    TP_CHECK(n <= kMaxSize && h <= kMaxSize && f <= kMaxSize, TP_ERR_INVALID_ARG);
     TP_CHECK((x != nullptr && xs != nullptr && y != nullptr) || n == 0, TP_ERR_INVALID_ARG);
     TP_CHECK(w_gate_up != nullptr && s_gate_up != nullptr && w_down != nullptr && s_down != nullptr, TP_ERR_INVALID_ARG);
     TP_CHECK(act == TP_ACT_SILU_MUL || act == TP_ACT_GELU_TANH_MUL, TP_ERR_INVALID_ARG);

@@ -238,7 +238,6 @@ __global__ void __launch_bounds__(FewCfg<NT, GLU>::THREADS, FewCfg<NT, GLU>::ONE
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem_base = __shfl_sync(0xffffffffu, *tmem_slot, 0);
-    if (threadIdx.x == 0) pdl_trigger();
     bool aborted = false;
 
     if (warp == 0) {
@@ -269,7 +268,10 @@ __global__ void __launch_bounds__(FewCfg<NT, GLU>::THREADS, FewCfg<NT, GLU>::ONE
                 }
             }
         }
+        // The next kernel may start from here on, not sooner: it may be one that loads weights before its own wait, and a
+        // kernel before this one may be writing them still.
         pdl_wait();
+        if (lane == 0) pdl_trigger();
         int s = 0;
         uint32_t phase = 0;
         for (int i = 0; i < kb_hi - kb_lo; ++i) {
@@ -293,6 +295,7 @@ __global__ void __launch_bounds__(FewCfg<NT, GLU>::THREADS, FewCfg<NT, GLU>::ONE
         }
     } else if (warp == 1) {
         // ---------------------------------------------------- MMA issuer (see the many-row kernel's)
+        pdl_wait();                              // what the waits below wait for comes after it: their limit starts here
         constexpr uint32_t idesc = mma_idesc_e4m3(128, NT);
         int s = 0, b = 0;
         uint32_t phase = 0;
@@ -448,10 +451,19 @@ __global__ void __launch_bounds__(FewCfg<NT, GLU>::THREADS, FewCfg<NT, GLU>::ONE
     if (aborted) spin_ns(50000);        // let issued copies and products land
     __syncwarp();
     tc_fence_before();
-    if (split > 1)
+    __syncthreads();
+    if (*abort_flag) spin_ns(50000);
+    // TMEM goes back before any peer is waited for: another kernel's CTAs that wait for some on this SM may be
+    // what keeps a peer from having its own.
+    if (warp == 1) {
+        __syncwarp();
+        tc_fence_after();
+        tmem_dealloc<Cfg::TMEM_COLS>(tmem_base);
+    }
+    if (split > 1) {
+        __syncwarp();
         cluster_sync();
-    else
-        __syncthreads();
+    }
     if (warp >= 3 && *abort_flag == 0) {
         const int e = warp - 3;
         const int tokens = min(NT, args.M - token0);
@@ -503,14 +515,9 @@ __global__ void __launch_bounds__(FewCfg<NT, GLU>::THREADS, FewCfg<NT, GLU>::ONE
                 store_quad(args.out[g], args.ldo, args.out_kind == FP8_OUT_F32, row, col, min(4, nvalid), v);
         }
     }
-    __syncwarp();
-    if (split > 1) cluster_sync_relaxed();      // a peer may still read this CTA's sums
-    else __syncthreads();
-    if (*abort_flag) spin_ns(50000);
-    if (warp == 1) {
+    if (split > 1) {
         __syncwarp();
-        tc_fence_after();
-        tmem_dealloc<Cfg::TMEM_COLS>(tmem_base);
+        cluster_sync_relaxed();                  // a peer may still read this CTA's sums
     }
 }
 
@@ -717,7 +724,6 @@ __global__ void __launch_bounds__(kManyThreads, 1) fp8_many_kernel(const __grid_
     cluster_sync();                                      // the peer's barriers exist before any remote use
     tc_fence_after();
     const uint32_t tmem_base = __shfl_sync(0xffffffffu, *tmem_slot, 0);
-    if (threadIdx.x == 0) pdl_trigger();
 
     // The end of either role: nothing of this CTA is in flight and every sum is staged when it returns.
     auto meet = [&](bool gave_up) {
@@ -735,6 +741,7 @@ __global__ void __launch_bounds__(kManyThreads, 1) fp8_many_kernel(const __grid_
         if (warp == 0) {
             // ------------------------------------------------ TMA producer (both CTAs)
             pdl_wait();
+            if (lane == 0) pdl_trigger();                // not sooner: see the few-row kernel's
             int s = 0;
             uint32_t phase = 0;
             for (int tile = cluster; tile < args.total_tiles && !aborted; tile += nclusters) {
@@ -834,6 +841,7 @@ __global__ void __launch_bounds__(kManyThreads, 1) fp8_many_kernel(const __grid_
         }
         if (warp == 1 && rank == 0) {
             // ------------------------------------------------ MMA issuer (even CTA)
+            pdl_wait();                                  // the limit of the waits below starts after it
             constexpr uint32_t idesc = mma_idesc_e4m3(256, 256);
             int s = 0, b = 0;
             uint32_t phase = 0;

@@ -17,7 +17,8 @@ every tile of the down GEMM split along K over two CTA pairs), cache (append and
 load of 8192 rows, t=8, fp32 out), attend (decode attention, t=4, 64 sequences of
 6144 cached tokens), chunk (attention of two chunks of 1024 rows over 3000 tokens,
 t=4), pages (a fork of 256 rows and a compaction that moves 198 MB), beam (32 requests of 8
-beams, vocabulary 128000 in 4 shards).
+beams, vocabulary 128000 in 4 shards), fp8rows (8-bit operators: norm of 2048 rows, rows and a
+weight to 8 bits), fp8few (8-bit MLP of 32 tokens, t=4), fp8many (the same of 1024 tokens).
 """
 
 import sys
@@ -133,6 +134,21 @@ def run(mode: str, dev: str = "cuda") -> None:
         logits = [synth.normal_bf16((256, 32000), 2.0, 60 + r, device=dev) for r in range(4)]
         scores = torch.zeros((32, 8), dtype=torch.float32, device=dev)
         for _ in range(2): tp.tp_beam_select(logits, scores, 8)
+    elif mode == "fp8rows":                   # 2048 rows of 8192 from four shards; a shard of a gate_up weight
+        parts = [torch.randn((2048, H), device=dev).to(torch.bfloat16) for _ in range(4)]
+        w = torch.randn((H,), device=dev).to(torch.bfloat16)
+        big = synth.normal_bf16((14336, H), 0.02, 70, device=dev)
+        for _ in range(2):
+            r, _, _ = tp.tp_fp8_rmsnorm(parts, w, residual=parts[0])
+            tp.tp_fp8_quantize([r, parts[1], parts[2], parts[3]])
+            tp.tp_fp8_quantize_weight([big], gated=True)
+    elif mode in ("fp8few", "fp8many"):       # 70B MLP in 8 bits, t=4, fused reduce
+        t = 4; fs = F // t
+        n = 32 if mode == "fp8few" else 1024
+        (x,), (xs,) = tp.tp_fp8_quantize([synth.normal_bf16((n, H), 1.0, 0, device=dev)])
+        wgu, sgu = tp.tp_fp8_quantize_weight([synth.normal_bf16((2 * fs, H), 0.02, 10 + r, device=dev) for r in range(t)], gated=True)
+        wds, sds = tp.tp_fp8_quantize_weight([synth.normal_bf16((H, fs), 0.02, 20 + r, device=dev) for r in range(t)])
+        for _ in range(2): tp.tp_fp8_mlp_forward(x, xs, wgu, sgu, wds, sds, mode="fused")
     else:
         raise ValueError(f"unknown case {mode}")
     torch.cuda.synchronize()

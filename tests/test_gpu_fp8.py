@@ -366,3 +366,52 @@ def test_streams_graphs_and_prepared_calls(n):
     call = tp.prepare(tp.tp_fp8_mlp_forward, c[0], s[0], aw, as_, bw, bs, mode="direct")
     assert torch.equal(call(), tp.tp_fp8_mlp_forward(c[0], s[0], aw, as_, bw, bs, mode="direct"))
     assert tp.tp_device_status() == 0
+
+
+@pytest.mark.parametrize("n", [1, 24, 200])
+def test_weights_written_just_before(n):
+    """A weight that the call before brings to 8 bits is what the MLP multiplies by, with nothing waited for between."""
+    t, h, f = 2, 2048, 4096
+    fs = f // t
+    x, xs = (v.to(DEV) for v in quantised(n, h, 1))
+    wa = [[(torch.randn((2 * fs, h), generator=gen(i * 10 + r)) * 0.05).to(torch.bfloat16).to(DEV) for r in range(t)] for i in range(2)]
+    wb = [[(torch.randn((h, fs), generator=gen(i * 10 + 5 + r)) * 0.05).to(torch.bfloat16).to(DEV) for r in range(t)] for i in range(2)]
+    want = []
+    for i in range(2):
+        a, b = tp.tp_fp8_quantize_weight(wa[i], gated=True), tp.tp_fp8_quantize_weight(wb[i])
+        torch.cuda.synchronize()
+        want.append(tp.tp_fp8_mlp_forward(x, xs, *a, *b, mode="fused"))
+        torch.cuda.synchronize()
+    ca, sa = tp.tp_fp8_quantize_weight(wa[0], gated=True)
+    cb, sb = tp.tp_fp8_quantize_weight(wb[0])
+    ys = []
+    for i in range(40):                                  # the same buffers, other weights each time
+        tp.tp_fp8_quantize_weight(wa[i % 2], gated=True, codes=ca, scales=sa)
+        tp.tp_fp8_quantize_weight(wb[i % 2], codes=cb, scales=sb)
+        ys.append(tp.tp_fp8_mlp_forward(x, xs, ca, sa, cb, sb, mode="fused"))
+    assert all(torch.equal(y, want[i % 2]) for i, y in enumerate(ys))
+
+
+def test_two_streams_at_once():
+    """Products of different kernels on two streams, each with its own buffers."""
+    k, out = 4096, 1024
+    w, s = (v.to(DEV) for v in weights(out, k, 3))
+    g, gs = (v.to(DEV) for v in weights(2 * 512, k, 4, True))
+    sizes = [1, 20, 60, 100, 300]
+    xs = [tuple(v.to(DEV) for v in quantised(n, k, n)) for n in sizes]
+    want = [(tp.tp_fp8_linear_row([x], [sc], [w], [s], mode="fused", y_dtype=torch.float32),
+             tp.tp_fp8_linear_col(x, sc, [g], [gs], act="silu")[0]) for x, sc in xs]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    got = {0: [], 1: []}
+    for _ in range(10):
+        for i in range(len(sizes)):
+            for j, st in enumerate(streams):
+                x, sc = xs[(i + 2 * j) % len(sizes)]
+                with torch.cuda.stream(st):
+                    got[j].append(((i + 2 * j) % len(sizes), tp.tp_fp8_linear_row([x], [sc], [w], [s], mode="fused", y_dtype=torch.float32),
+                                   tp.tp_fp8_linear_col(x, sc, [g], [gs], act="silu")[0]))
+    torch.cuda.synchronize()
+    for i, y, z in got[0] + got[1]:
+        assert torch.equal(y, want[i][0]) and torch.equal(z, want[i][1])
+    assert tp.tp_device_status() == 0
