@@ -19,15 +19,23 @@ __device__ __forceinline__ float max_nan(float a, float b) {
     return r;
 }
 
-// amax / 448 rounded to nearest: the quotient of a constant, as Fp8Quotient's below (amax is at least 2^-100, so no
-// remainder is subnormal); an infinity's remainder would be NaN and is left out.
+// The larger magnitudes of two pairs of bf16, with signs that mean nothing.
+__device__ __forceinline__ uint32_t max_abs_bf16x2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("max.NaN.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+
+// amax / 448 rounded to nearest: q0 = a r with r = 1 / 448 rounded, and one
+// correction by the exact remainder, which gives the rounded quotient for every
+// 24-bit a (all of them were compared; amax is at least 2^-100, so no remainder is
+// subnormal).  An infinity's remainder would be NaN and is left out.
 __device__ __forceinline__ float fp8_scale(float amax) {
     constexpr float r = 1.0f / kFp8Max;
     const float a = max_nan(amax, kFp8LeastAmax);
     const float q0 = a * r;
     const float q1 = fmaf(fmaf(-q0, kFp8Max, a), r, q0);
-    const float q2 = fmaf(fmaf(-q1, kFp8Max, a), r, q1);
-    return a == __int_as_float(0x7f800000) ? a : q2;
+    return a == __int_as_float(0x7f800000) ? a : q1;
 }
 
 // Codes of four values (the first in the low byte), rounded to nearest even;
@@ -61,54 +69,78 @@ __device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
     return r;
 }
 
-// Quotients x / scale rounded to nearest as a division's: with r = 1 / s
-// rounded to nearest, q0 = x r is within 1.5 units of the last place, one
-// correction q1 = q0 + (x - q0 s) r (the remainder is exact in an fma) brings it
-// within one, and by Markstein's theorem a second then rounds correctly.  Two
-// at a time, six packed operations instead of a reciprocal and steps for each.
-// Scales below 2^-60 and their values are taken times 2^64, so that no
-// remainder is subnormal.  An infinite scale's quotients are 0 (NaN of an
-// infinity): there the remainders are taken with 0 in place of the scale.  Values
-// and remainders are carried negated, so that a quotient of -0 stays one.
+// Quotients x / scale rounded to nearest as a division's, of values given
+// negated: with r = 1 / s rounded to nearest, q0 = x r is within 1.5 units of the
+// last place, one correction q1 = q0 + (x - q0 s) r (the remainder is exact in an
+// fma) brings it within one, and by Markstein's theorem a second then rounds
+// correctly.  Two at a time, five packed operations instead of a reciprocal and
+// steps for each.  An infinite scale's quotients are 0 (NaN of an infinity): there
+// the remainders are taken with 0 in place of the scale.  Carried negated, values
+// and remainders leave a quotient of -0 one.  Where `tiny`, s is below 2^-60, and
+// it and the values are taken times 2^64 first, so that no remainder is subnormal.
 struct Fp8Quotient {
-    f32x2 nf, s, nr;
+    f32x2 s, nr;
+    bool tiny;
     __device__ __forceinline__ explicit Fp8Quotient(float scale) {
-        const float f = scale < 8.6736173798840355e-19f ? 1.8446744073709552e19f : 1.0f;   // 2^-60, 2^64
-        const float sf = scale * f, r = __frcp_rn(sf);
+        tiny = scale < 8.6736173798840355e-19f;             // 2^-60
+        const float sf = tiny ? scale * 1.8446744073709552e19f : scale;
         const float sr = sf == __int_as_float(0x7f800000) ? 0.0f : sf;
-        nf = pack2(-f, -f);
+        const float r = __frcp_rn(sf);
         s = pack2(sr, sr);
         nr = pack2(-r, -r);
     }
-    __device__ __forceinline__ f32x2 operator()(f32x2 x) const {
-        const f32x2 nx = mul2(x, nf);
+    // Asked of the whole warp, for it is rare.
+    __device__ __forceinline__ bool any_tiny() const { return __any_sync(0xffffffffu, tiny); }
+    __device__ __forceinline__ f32x2 scaled(f32x2 nx) const {
+        const float f = tiny ? 1.8446744073709552e19f : 1.0f;   // 2^64
+        return mul2(nx, pack2(f, f));
+    }
+    __device__ __forceinline__ f32x2 operator()(f32x2 nx) const {
         const f32x2 q0 = mul2(nx, nr);
         const f32x2 q1 = fma2(fma2(q0, s, nx), nr, q0);
         return fma2(fma2(q1, s, nx), nr, q1);
     }
 };
 
-// Codes of four values.
-__device__ __forceinline__ uint32_t fp8_codes4(float a, float b, float c, float d, const Fp8Quotient& q) {
-    float x, y, z, w;
-    unpack2(q(pack2(a, b)), x, y);
-    unpack2(q(pack2(c, d)), z, w);
-    return e4m3x4(x, y, z, w);
+// Codes of 4 PAIRS / 2 values given negated, four a word; all lanes of the warp.
+template <int PAIRS>
+__device__ __forceinline__ void fp8_codes(f32x2 (&nx)[PAIRS], float scale, uint32_t (&out)[PAIRS / 2]) {
+    const Fp8Quotient q(scale);
+    if (q.any_tiny()) {
+#pragma unroll
+        for (int i = 0; i < PAIRS; ++i) nx[i] = q.scaled(nx[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < PAIRS; i += 2) {
+        float x, y, z, w;
+        unpack2(q(nx[i]), x, y);
+        unpack2(q(nx[i + 1]), z, w);
+        out[i / 2] = e4m3x4(x, y, z, w);
+    }
 }
-__device__ __forceinline__ uint32_t fp8_codes4(f32x2 ab, f32x2 cd, const Fp8Quotient& q) {
-    float x, y, z, w;
-    unpack2(q(ab), x, y);
-    unpack2(q(cd), z, w);
-    return e4m3x4(x, y, z, w);
+
+// Largest magnitude of pairs.
+template <int PAIRS>
+__device__ __forceinline__ float amax_pairs(const f32x2 (&x)[PAIRS]) {
+    float m = 0.0f;
+#pragma unroll
+    for (int i = 0; i < PAIRS; ++i) {
+        float lo, hi;
+        unpack2(x[i], lo, hi);
+        m = max_nan(m, max_nan(fabsf(lo), fabsf(hi)));
+    }
+    return m;
 }
 
 // act(g) of a gated block as g / (1 + exp(-z)): SiLU has z = g, and GeLU-tanh's
 // 0.5 g (1 + tanh(u)) is z = 2 u with u = sqrt(2/pi) (g + 0.044715 g^3).  With
 // coefficients in place of a branch, exp as 2^(g (a + b g^2)), and the hardware's
-// 2^x and reciprocal (2^-22 and 1 ulp); two values at a time.
+// 2^x and reciprocal (2^-22 and 1 ulp); two values at a time.  `negated` gives
+// -act(g), with the same magnitude, as the codes' quotients take it.
 struct GateAct {
     f32x2 a, b;
-    __device__ __forceinline__ explicit GateAct(int act) {
+    float one;
+    __device__ __forceinline__ GateAct(int act, bool negated) : one(negated ? -1.0f : 1.0f) {
         constexpr float log2e = 1.4426950408889634f, k = 2.0f * 0.7978845608028654f;
         const bool gelu = act == TP_ACT_GELU_TANH_MUL;
         const float fa = gelu ? -k * log2e : -log2e, fb = gelu ? -k * 0.044715f * log2e : 0.0f;
@@ -122,19 +154,11 @@ struct GateAct {
         unpack2(mul2(g, fma2(b, g2, a)), s0, s1);
         asm("ex2.approx.f32 %0, %1;" : "=f"(e0) : "f"(s0));
         asm("ex2.approx.f32 %0, %1;" : "=f"(e1) : "f"(s1));
-        asm("rcp.approx.f32 %0, %1;" : "=f"(s0) : "f"(1.0f + e0));
-        asm("rcp.approx.f32 %0, %1;" : "=f"(s1) : "f"(1.0f + e1));
+        asm("rcp.approx.f32 %0, %1;" : "=f"(s0) : "f"(fmaf(e0, one, one)));
+        asm("rcp.approx.f32 %0, %1;" : "=f"(s1) : "f"(fmaf(e1, one, one)));
         return mul2(g, pack2(s0, s1));
     }
 };
-
-// Largest |x| of eight values.
-__device__ __forceinline__ float amax8(const float (&x)[8]) {
-    float m = fabsf(x[0]);
-#pragma unroll
-    for (int i = 1; i < 8; ++i) m = max_nan(m, fabsf(x[i]));
-    return m;
-}
 
 // Eight consecutive bf16 (one 16-byte load) or fp32 values (two).
 template <bool F32>
@@ -148,6 +172,31 @@ struct Vec8 {
     __device__ __forceinline__ void zero() {
 #pragma unroll
         for (int i = 0; i < (F32 ? 2 : 1); ++i) q[i] = make_uint4(0u, 0u, 0u, 0u);
+    }
+    // the largest magnitude
+    __device__ __forceinline__ float amax() const {
+        if constexpr (F32) {
+            const uint32_t w[8] = {q[0].x, q[0].y, q[0].z, q[0].w, q[1].x, q[1].y, q[1].z, q[1].w};
+            float m = 0.0f;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) m = max_nan(m, fabsf(__uint_as_float(w[i])));
+            return m;
+        } else {
+            const uint32_t m = max_abs_bf16x2(max_abs_bf16x2(q[0].x, q[0].y), max_abs_bf16x2(q[0].z, q[0].w));
+            return max_nan(fabsf(__uint_as_float(m << 16)), fabsf(__uint_as_float(m & 0xFFFF0000u)));
+        }
+    }
+    // the eight values negated, in pairs
+    __device__ __forceinline__ void negated(f32x2 (&x)[4]) const {
+        if constexpr (F32) {
+            const uint32_t w[8] = {q[0].x, q[0].y, q[0].z, q[0].w, q[1].x, q[1].y, q[1].z, q[1].w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) x[i] = pack2(-__uint_as_float(w[2 * i]), -__uint_as_float(w[2 * i + 1]));
+        } else {
+            const uint32_t w[4] = {q[0].x ^ 0x80008000u, q[0].y ^ 0x80008000u, q[0].z ^ 0x80008000u, q[0].w ^ 0x80008000u};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) x[i] = pack2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u));
+        }
     }
     __device__ __forceinline__ void get(float (&x)[8]) const {
         if constexpr (F32) {
@@ -170,11 +219,6 @@ __device__ __forceinline__ float max16(float m) {
 #pragma unroll
     for (int o = 8; o > 0; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
     return m;
-}
-
-__device__ __forceinline__ uint2 fp8_codes8(const float (&x)[8], float scale) {
-    const Fp8Quotient q(scale);
-    return make_uint2(fp8_codes4(x[0], x[1], x[2], x[3], q), fp8_codes4(x[4], x[5], x[6], x[7], q));
 }
 
 }  // namespace tpk

@@ -127,10 +127,11 @@ __device__ __forceinline__ void finish_gated(const Fp8GemmArgs& args, int g, int
                                              const float (&gate)[4], const float (&up)[4]) {
     const int col = n * 128 + lane * 4;
     const int nvalid = args.N - col;                     // this lane's columns inside the group
-    const GateAct act(args.act);
+    const GateAct act(args.act, args.out_kind == FP8_OUT_CODES);
+    f32x2 v2[2] = {mul2(act(pack2(gate[0], gate[1])), pack2(up[0], up[1])), mul2(act(pack2(gate[2], gate[3])), pack2(up[2], up[3]))};
     float v[4];
-    unpack2(mul2(act(pack2(gate[0], gate[1])), pack2(up[0], up[1])), v[0], v[1]);
-    unpack2(mul2(act(pack2(gate[2], gate[3])), pack2(up[2], up[3])), v[2], v[3]);
+    unpack2(v2[0], v[0], v[1]);
+    unpack2(v2[1], v[2], v[3]);
     if (args.out_kind == FP8_OUT_CODES) {
         float top = 0.0f;
 #pragma unroll
@@ -138,9 +139,10 @@ __device__ __forceinline__ void finish_gated(const Fp8GemmArgs& args, int g, int
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, o));
         const float s = fp8_scale(top);
+        uint32_t code[1];
+        fp8_codes(v2, s, code);
         if (nvalid > 0)                                  // N is a multiple of 16: all four or none
-            *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(args.out[g]) + row * args.ldo + col) =
-                fp8_codes4(v[0], v[1], v[2], v[3], Fp8Quotient(s));
+            *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(args.out[g]) + row * args.ldo + col) = code[0];
         if (lane == 0) args.os[g][static_cast<int64_t>(n) * args.ldos + row] = s;
     } else if (nvalid > 0) {
         store_quad(args.out[g], args.ldo, args.out_kind == FP8_OUT_F32, row, col, min(4, nvalid), v);
@@ -957,7 +959,7 @@ __global__ void __launch_bounds__(kManyThreads, 1) fp8_many_kernel(const __grid_
                     *reinterpret_cast<float4*>(to + (j < 64 ? col_a + j : col_b + j - 64)) = v;
                 }
             } else if (GLU) {
-                const GateAct act(args.act);
+                const GateAct act(args.act, args.out_kind == FP8_OUT_CODES);
                 uint8_t* out = static_cast<uint8_t*>(args.out[g]);
                 const int col0 = n * 128 + half * 64;
                 const int valid = args.N - col0;          // columns of this half inside the group
@@ -969,13 +971,7 @@ __global__ void __launch_bounds__(kManyThreads, 1) fp8_many_kernel(const __grid_
 #pragma unroll
                         for (int j = 0; j < 32; ++j) v[j] = 2 * j < valid ? v[j] : 0;
                     }
-                    float top = 0.0f;
-#pragma unroll
-                    for (int j = 0; j < 32; ++j) {
-                        float lo, hi;
-                        unpack2(v[j], lo, hi);
-                        top = max_nan(top, max_nan(fabsf(lo), fabsf(hi)));
-                    }
+                    const float top = amax_pairs(v);
                     float* mine = amax + turn * 256;
                     mine[half * 128] = top;
                     __syncwarp();
@@ -989,12 +985,11 @@ __global__ void __launch_bounds__(kManyThreads, 1) fp8_many_kernel(const __grid_
                     turn ^= 1;
                     if (half == 0 && row_ok) args.os[g][static_cast<int64_t>(n) * args.ldos + row] = s;
                     if (live > 0 && valid > 0) {
-                        const Fp8Quotient quot(s);
+                        uint32_t code[16];
+                        fp8_codes(v, s, code);
 #pragma unroll
-                        for (int j = 0; j < 32; j += 8)
-                            *reinterpret_cast<uint4*>(st_lane + j * 2) =
-                                make_uint4(fp8_codes4(v[j], v[j + 1], quot), fp8_codes4(v[j + 2], v[j + 3], quot),
-                                           fp8_codes4(v[j + 4], v[j + 5], quot), fp8_codes4(v[j + 6], v[j + 7], quot));
+                        for (int j = 0; j < 16; j += 4)
+                            *reinterpret_cast<uint4*>(st_lane + j * 4) = make_uint4(code[j], code[j + 1], code[j + 2], code[j + 3]);
                         many_store<1>(st, out, row0, live, args.ldo, col0, valid, lane);
                     }
                 } else if (live > 0 && valid > 0) {

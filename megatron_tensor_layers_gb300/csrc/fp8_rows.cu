@@ -30,9 +30,9 @@ struct Fp8QuantArgs {
 //
 // A thread has eight columns of ROWS consecutive rows, whose loads it issues
 // before it uses the first; sixteen neighbouring lanes hold a group.  Blocks are
-// as wide as the rows up to 1024 columns.  Four matrices of 8192 x 2048: 38 us, 5.3
-// TB/s; what is left beside the memory is the arithmetic of the quotients (256
-// threads of 8 rows 43.7 us).
+// as wide as the rows up to 1024 columns.  Four matrices of 8192 x 2048: 32.6 us, 6.2
+// TB/s (with the largest magnitude taken from fp32 values 34.2 us, values scaled
+// and negated one by one 38 us).
 constexpr int kRowThreads = 128;
 
 template <bool F32, int ROWS>
@@ -42,38 +42,46 @@ __global__ void __launch_bounds__(kRowThreads) fp8_quant_rows_kernel(const __gri
     const int r = blockIdx.z;
     const int64_t col = (static_cast<int64_t>(blockIdx.y) * blockDim.x + threadIdx.x) * 8;
     const int64_t row0 = static_cast<int64_t>(blockIdx.x) * ROWS;
-    const bool in = col < a.k;
+    const int rows = col < a.k ? static_cast<int>(min(static_cast<int64_t>(ROWS), a.n - row0)) : 0;   // of this thread's columns
+    const char* from = static_cast<const char*>(a.x[r]) + (row0 * a.ldx + col) * (F32 ? 4 : 2);
     Vec8<F32> v[ROWS];
 #pragma unroll
     for (int u = 0; u < ROWS; ++u) {
-        if (in && row0 + u < a.n)
-            v[u].load(a.x[r], (row0 + u) * a.ldx + col);
+        if (u < rows)
+            v[u].load(from, 0);
         else
             v[u].zero();
+        from += a.ldx * (F32 ? 4 : 2);
     }
+    uint8_t* to = a.codes[r] + row0 * a.ldc + col;
+    float* scale = a.scales[r] + (col / kFp8Group) * a.lds + row0;
 #pragma unroll
     for (int u = 0; u < ROWS; ++u) {
-        float x[8];
-        v[u].get(x);
-        const float s = fp8_scale(max16(amax8(x)));
-        if (in && row0 + u < a.n) {
-            *reinterpret_cast<uint2*>(a.codes[r] + (row0 + u) * a.ldc + col) = fp8_codes8(x, s);
-            if ((threadIdx.x & 15) == 0) a.scales[r][(col / kFp8Group) * a.lds + row0 + u] = s;
+        f32x2 x[4];
+        uint32_t code[2];
+        const float s = fp8_scale(max16(v[u].amax()));
+        v[u].negated(x);
+        fp8_codes(x, s, code);
+        if (u < rows) {
+            *reinterpret_cast<uint2*>(to) = make_uint2(code[0], code[1]);
+            if ((threadIdx.x & 15) == 0) scale[u] = s;
         }
+        to += a.ldc;
     }
 }
 
 // ------------------------------------------------------------------ weights
 //
 // One thread block per 128 x 128 block, held in registers between its largest
-// value and its codes.  14336 x 8192: 72 us, 4.9 TB/s (two thread blocks an SM
-// 83 us).
+// value and its codes.  What it takes beside the memory is arithmetic, which other
+// thread blocks' loads cover: 14336 x 8192 with four an SM 55 us, 6.4 TB/s (three
+// 61 us, five 72 us; two or three of 512 threads 76 and 65 us).
 constexpr int kQuantThreads = 256;
 constexpr int kWeightRowsPerPass = kQuantThreads / 16;
 constexpr int kWeightPasses = kFp8Group / kWeightRowsPerPass;
 
 template <bool F32>
-__global__ void __launch_bounds__(kQuantThreads, F32 ? 2 : 3) fp8_quant_weight_kernel(const __grid_constant__ Fp8QuantArgs a) {
+__global__ void __launch_bounds__(kQuantThreads, F32 ? 2 : 4) fp8_quant_weight_kernel(const __grid_constant__ Fp8QuantArgs a) {
     pdl_wait();
     if (threadIdx.x == 0) pdl_trigger();
     __shared__ float warp_max[kQuantThreads / 32];
@@ -85,22 +93,22 @@ __global__ void __launch_bounds__(kQuantThreads, F32 ? 2 : 3) fp8_quant_weight_k
     const int64_t row0 = second ? a.half + (nb - a.blocks_half) * kFp8Group : nb * kFp8Group;
     const int64_t row_end = a.half > 0 && !second ? a.half : a.n;
     const int64_t col = static_cast<int64_t>(blockIdx.x) * kFp8Group + lane16 * 8;
+    const int64_t first = row0 + (threadIdx.x >> 4);     // this thread's rows: every 16th from here
+    const int64_t left = col < a.k ? min(static_cast<int64_t>(kFp8Group), row_end - first) : 0;
+    const int rows = static_cast<int>((left + kWeightRowsPerPass - 1) / kWeightRowsPerPass);
+    const char* from = static_cast<const char*>(a.x[r]) + (first * a.ldx + col) * (F32 ? 4 : 2);
     Vec8<F32> v[kWeightPasses];
 #pragma unroll
     for (int i = 0; i < kWeightPasses; ++i) {
-        const int64_t row = row0 + i * kWeightRowsPerPass + (threadIdx.x >> 4);
-        if (row < row_end && col < a.k)
-            v[i].load(a.x[r], row * a.ldx + col);
+        if (i < rows)
+            v[i].load(from, 0);
         else
             v[i].zero();
+        from += a.ldx * (kWeightRowsPerPass * (F32 ? 4 : 2));
     }
     float m = 0.0f;
 #pragma unroll
-    for (int i = 0; i < kWeightPasses; ++i) {
-        float x[8];
-        v[i].get(x);
-        m = max_nan(m, amax8(x));
-    }
+    for (int i = 0; i < kWeightPasses; ++i) m = max_nan(m, v[i].amax());
     m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, 16));
     m = max16(m);
     if ((threadIdx.x & 31) == 0) warp_max[threadIdx.x >> 5] = m;
@@ -108,12 +116,15 @@ __global__ void __launch_bounds__(kQuantThreads, F32 ? 2 : 3) fp8_quant_weight_k
 #pragma unroll
     for (int w = 0; w < kQuantThreads / 32; ++w) m = max_nan(m, warp_max[w]);
     const float s = fp8_scale(m);
+    uint8_t* to = a.codes[r] + first * a.ldc + col;
 #pragma unroll
     for (int i = 0; i < kWeightPasses; ++i) {
-        const int64_t row = row0 + i * kWeightRowsPerPass + (threadIdx.x >> 4);
-        float x[8];
-        v[i].get(x);
-        if (row < row_end && col < a.k) *reinterpret_cast<uint2*>(a.codes[r] + row * a.ldc + col) = fp8_codes8(x, s);
+        f32x2 x[4];
+        uint32_t code[2];
+        v[i].negated(x);
+        fp8_codes(x, s, code);
+        if (i < rows) *reinterpret_cast<uint2*>(to) = make_uint2(code[0], code[1]);
+        to += a.ldc * kWeightRowsPerPass;
     }
     if (threadIdx.x == 0) a.scales[r][nb * a.lds + blockIdx.x] = s;
 }
@@ -250,7 +261,7 @@ __global__ void __launch_bounds__(THREADS) fp8_norm_kernel(const __grid_constant
     float tot = 0.0f;
 #pragma unroll
     for (int w = 0; w < THREADS / 32; ++w) tot += warp_sums[w];
-    const float rstd = rsqrtf(tot / static_cast<float>(a.h) + a.eps);
+    const float nrstd = -rsqrtf(tot / static_cast<float>(a.h) + a.eps);
 #pragma unroll
     for (int v = 0; v < VPT; ++v) {
         const int64_t col = (static_cast<int64_t>(v) * THREADS + threadIdx.x) * 8;
@@ -266,12 +277,16 @@ __global__ void __launch_bounds__(THREADS) fp8_norm_kernel(const __grid_constant
         else
             q.zero();
         q.get(w);
-        // beyond the row: exact zeros, whatever the row's scale is
+        // the normed values, negated; beyond the row exact zeros, whatever the row's scale is
+        f32x2 y[4];
+        uint32_t code[2];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) w[i] = in ? x[v][i] * rstd * w[i] : 0.0f;
-        const float s = fp8_scale(max16(amax8(w)));
+        for (int i = 0; i < 4; ++i)
+            y[i] = in ? pack2(x[v][2 * i] * nrstd * w[2 * i], x[v][2 * i + 1] * nrstd * w[2 * i + 1]) : 0;
+        const float s = fp8_scale(max16(amax_pairs(y)));
+        fp8_codes(y, s, code);
         if (in) {
-            *reinterpret_cast<uint2*>(a.codes + row * a.ldc + col) = fp8_codes8(w, s);
+            *reinterpret_cast<uint2*>(a.codes + row * a.ldc + col) = make_uint2(code[0], code[1]);
             if ((threadIdx.x & 15) == 0) a.scales[(col / kFp8Group) * a.lds + row] = s;
         }
     }
