@@ -242,7 +242,7 @@ __global__ void __launch_bounds__(THREADS) fp8_norm_kernel(const __grid_constant
             }
         }
     }
-    float ss = 0.0f;
+    float sq[4] = {};
 #pragma unroll
     for (int v = 0; v < VPT; ++v) {
         if (a.residual != nullptr) {
@@ -252,16 +252,21 @@ __global__ void __launch_bounds__(THREADS) fp8_norm_kernel(const __grid_constant
             for (int i = 0; i < 8; ++i) x[v][i] = y[i] + x[v][i];
         }
 #pragma unroll
-        for (int i = 0; i < 8; ++i) ss += x[v][i] * x[v][i];
+        for (int i = 0; i < 8; ++i) sq[i & 3] += x[v][i] * x[v][i];
     }
+    float ss = (sq[0] + sq[1]) + (sq[2] + sq[3]);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
     if ((threadIdx.x & 31) == 0) warp_sums[threadIdx.x >> 5] = ss;
     __syncthreads();
-    float tot = 0.0f;
+    float part[THREADS / 32];                            // in pairs: an addition's rounding is not carried along
 #pragma unroll
-    for (int w = 0; w < THREADS / 32; ++w) tot += warp_sums[w];
-    const float nrstd = -rsqrtf(tot / static_cast<float>(a.h) + a.eps);
+    for (int w = 0; w < THREADS / 32; ++w) part[w] = warp_sums[w];
+#pragma unroll
+    for (int d = THREADS / 64; d > 0; d >>= 1)
+#pragma unroll
+        for (int w = 0; w < d; ++w) part[w] += part[w + d];
+    const float nrstd = -rsqrtf(part[0] / static_cast<float>(a.h) + a.eps);
 #pragma unroll
     for (int v = 0; v < VPT; ++v) {
         const int64_t col = (static_cast<int64_t>(v) * THREADS + threadIdx.x) * 8;
