@@ -19,6 +19,13 @@ __device__ __forceinline__ float max_nan(float a, float b) {
     return r;
 }
 
+// The largest magnitude of three values; NaN if one of them is NaN.
+__device__ __forceinline__ float max_abs(float a, float b, float c) {
+    float r;
+    asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+
 // The larger magnitudes of two pairs of bf16, with signs that mean nothing.
 __device__ __forceinline__ uint32_t max_abs_bf16x2(uint32_t a, uint32_t b) {
     uint32_t r;
@@ -69,15 +76,18 @@ __device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
     return r;
 }
 
-// Quotients x / scale rounded to nearest as a division's, of values given
-// negated: with r = 1 / s rounded to nearest, q0 = x r is within 1.5 units of the
-// last place, one correction q1 = q0 + (x - q0 s) r (the remainder is exact in an
-// fma) brings it within one, and by Markstein's theorem a second then rounds
-// correctly.  Two at a time, five packed operations instead of a reciprocal and
-// steps for each.  An infinite scale's quotients are 0 (NaN of an infinity): there
-// the remainders are taken with 0 in place of the scale.  Carried negated, values
-// and remainders leave a quotient of -0 one.  Where `tiny`, s is below 2^-60, and
-// it and the values are taken times 2^64 first, so that no remainder is subnormal.
+// Quotients x / scale, of values given negated, as close as codes need: with r =
+// 1 / s rounded to nearest, q0 = x r is within 1.5 units of the last place, and one
+// correction q1 = q0 + (x - q0 s) r (the remainder is exact in an fma) leaves
+// less than a unit.  A code goes by the side of the ties between codes (values of
+// up to five significant bits) that the quotient lies on, and q1 lies on, or not
+// on, the side of every tie as the rounded quotient does: compared for all 2^23
+// significands of s, every tie t and the x next to s t.  Two at a time, three packed
+// operations instead of a reciprocal and steps for each.  An infinite scale's
+// quotients are 0 (NaN of an infinity): there the remainders are taken with 0 in
+// place of the scale.  Carried negated, values and remainders leave a quotient of -0
+// one.  Where `tiny`, s is below 2^-60, and it and the values are taken times 2^64
+// first, so that no remainder is subnormal.
 struct Fp8Quotient {
     f32x2 s, nr;
     bool tiny;
@@ -97,8 +107,7 @@ struct Fp8Quotient {
     }
     __device__ __forceinline__ f32x2 operator()(f32x2 nx) const {
         const f32x2 q0 = mul2(nx, nr);
-        const f32x2 q1 = fma2(fma2(q0, s, nx), nr, q0);
-        return fma2(fma2(q1, s, nx), nr, q1);
+        return fma2(fma2(q0, s, nx), nr, q0);
     }
 };
 
@@ -127,7 +136,7 @@ __device__ __forceinline__ float amax_pairs(const f32x2 (&x)[PAIRS]) {
     for (int i = 0; i < PAIRS; ++i) {
         float lo, hi;
         unpack2(x[i], lo, hi);
-        m = max_nan(m, max_nan(fabsf(lo), fabsf(hi)));
+        m = max_abs(m, lo, hi);
     }
     return m;
 }
@@ -179,11 +188,11 @@ struct Vec8 {
             const uint32_t w[8] = {q[0].x, q[0].y, q[0].z, q[0].w, q[1].x, q[1].y, q[1].z, q[1].w};
             float m = 0.0f;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) m = max_nan(m, fabsf(__uint_as_float(w[i])));
+            for (int i = 0; i < 8; i += 2) m = max_abs(m, __uint_as_float(w[i]), __uint_as_float(w[i + 1]));
             return m;
         } else {
             const uint32_t m = max_abs_bf16x2(max_abs_bf16x2(q[0].x, q[0].y), max_abs_bf16x2(q[0].z, q[0].w));
-            return max_nan(fabsf(__uint_as_float(m << 16)), fabsf(__uint_as_float(m & 0xFFFF0000u)));
+            return max_abs(0.0f, __uint_as_float(m << 16), __uint_as_float(m & 0xFFFF0000u));
         }
     }
     // the eight values negated, in pairs
