@@ -302,16 +302,17 @@ __global__ void __launch_bounds__(FewCfg<NT, GLU>::THREADS, FewCfg<NT, GLU>::ONE
         int s = 0, b = 0;
         uint32_t phase = 0;
         for (int i = kb_lo; i < kb_hi; ++i) {
+            const uint32_t d = tmem_base + static_cast<uint32_t>(b * Cfg::ACC_COLS);
+            const uint32_t sw = base + s * Cfg::STAGE_BYTES;
+            uint64_t wdesc = sw128_kmajor_desc(sw);
+            uint64_t xdesc = sw128_kmajor_desc(sw + Cfg::W_BYTES);
+            asm volatile("" : "+l"(xdesc), "+l"(wdesc));     // ready before the wait, not after it
             if (!mbar_wait_warp(start_bar(s), phase, abort_flag, args.status)) {
                 aborted = true;
                 break;
             }
             tc_fence_after();
             if (elect_one()) {
-                const uint32_t d = tmem_base + static_cast<uint32_t>(b * Cfg::ACC_COLS);
-                const uint32_t sw = base + s * Cfg::STAGE_BYTES;
-                const uint64_t wdesc = sw128_kmajor_desc(sw);
-                const uint64_t xdesc = sw128_kmajor_desc(sw + Cfg::W_BYTES);
 #pragma unroll
                 for (int k = 0; k < 4; ++k)      // 32 codes along K: 32 bytes inside the swizzle row
                     tc_mma_f8(d, wdesc + 2u * k, xdesc + 2u * k, idesc, k != 0 ? 1u : 0u);
@@ -409,10 +410,12 @@ __global__ void __launch_bounds__(FewCfg<NT, GLU>::THREADS, FewCfg<NT, GLU>::ONE
             const float* f = scales_ptr + slot * Cfg::SLOT_FLOATS;
             const float w = f[NT + (GLU ? part : 0)];
             const f32x2 w2 = pack2(w, w);
+            constexpr bool kAhead = GLU && NT == 128;
+            float dd[kAhead ? 2 : 1][16];
 #pragma unroll
             for (int c = 0; c < Cfg::NC / 16; ++c) {
-                float d[16];
-                tmem_ld(taddr + c * 16, d);
+                float (&d)[16] = dd[kAhead ? c & 1 : 0];
+                if (!kAhead || c == 0) tmem_ld(taddr + c * 16, d);
                 f32x2 x[8];                      // the columns' factors
 #pragma unroll
                 for (int j = 0; j < 16; j += 4) {
@@ -421,6 +424,7 @@ __global__ void __launch_bounds__(FewCfg<NT, GLU>::THREADS, FewCfg<NT, GLU>::ONE
                     x[j / 2 + 1] = mul2(pack2(v.z, v.w), w2);
                 }
                 tmem_wait(d);
+                if (kAhead && c + 1 < Cfg::NC / 16) tmem_ld(taddr + (c + 1) * 16, dd[(c + 1) & 1]);
                 if (c == Cfg::NC / 16 - 1) {     // all of this block is read: its columns are free again
                     tc_fence_before();
                     __syncwarp();
@@ -849,15 +853,16 @@ __global__ void __launch_bounds__(kManyThreads, 1) fp8_many_kernel(const __grid_
             uint32_t phase = 0;
             const int tiles = cluster < args.total_tiles ? (args.total_tiles - 1 - cluster) / nclusters + 1 : 0;
             for (int64_t i = static_cast<int64_t>(tiles) * (kb_hi - kb_lo); i > 0; --i) {   // K blocks of all of the cluster's tiles
+                const uint32_t sx = base + s * Cfg::STAGE_BYTES;
+                uint64_t xdesc = sw128_kmajor_desc(sx);
+                uint64_t wdesc = sw128_kmajor_desc(sx + 128 * 128);
+                asm volatile("" : "+l"(xdesc), "+l"(wdesc));     // ready before the wait, not after it
                 if (!mbar_wait_warp(start_bar(s), phase, abort_flag, args.status)) {
                     aborted = true;
                     break;
                 }
                 tc_fence_after();
                 if (elect_one()) {
-                    const uint32_t sx = base + s * Cfg::STAGE_BYTES;
-                    const uint64_t xdesc = sw128_kmajor_desc(sx);
-                    const uint64_t wdesc = sw128_kmajor_desc(sx + 128 * 128);
                     const uint32_t d = tmem_base + static_cast<uint32_t>(b * 256);
 #pragma unroll
                     for (int k = 0; k < 4; ++k) tc_mma_f8_pair(d, xdesc + 2u * k, wdesc + 2u * k, idesc, k != 0 ? 1u : 0u);
@@ -893,8 +898,9 @@ __global__ void __launch_bounds__(kManyThreads, 1) fp8_many_kernel(const __grid_
         pdl_wait();                                       // the previous kernel may read what this one writes
         const float* raw = reinterpret_cast<const float*>(base_ptr + kRawOff);
         // the accumulators are free to begin with: the first two blocks' starts
+        const uint32_t start0 = mapa_shared(start_bar(0), leader);
         auto release = [&](int s) {
-            if (elect_one()) mbar_arrive_cluster_relaxed(mapa_shared(start_bar(s), leader));
+            if (elect_one()) mbar_arrive_cluster_relaxed(start0 + 8u * s);
         };
         release(0);
         release(1);
