@@ -1089,16 +1089,18 @@ __global__ void __launch_bounds__(kManyThreads, 1) fp8_many_kernel(const __grid_
 
 // ------------------------------------------------------------------ host
 
-// Costs in hundredths of a microsecond, fitted to both kernels' times.  A wave of the few-row kernel takes so much a K block (by
-// its tokens, plain and gated; from memory, with nothing else to wait for) and 260 beside them, parts that are joined 30
-// and 15 each; a wave of the many-row kernel 50 a block, 350, and 300 where parts are joined.  Neither is less than the
-// weights take, at 6.4 TB/s with 240 CTAs and a little less with fewer (the down projection of 32 tokens: 5.5 TB/s with
-// 128, 6.2 with 256).
-constexpr int64_t few_block_cost(int nt, bool glu) {
-    return nt <= 16 ? (glu ? 35 : 26) : nt <= 32 ? (glu ? 40 : 28) : nt <= 64 ? (glu ? 50 : 44) : (glu ? 88 : 33);
+// Costs in hundredths of a microsecond, fitted to the kernels' times over 70 shapes (the choice costs 1 % over the best of all
+// variants there and over 140 others).  A wave of the few-row kernel takes so much a K block, by its tokens, plain and
+// gated, and more where two CTAs share an SM and its tensor core; 260 beside them (128 tokens 310); and parts that are joined
+// 30 and 15 each (28).  A wave of the many-row kernel takes 34 a block, 380, and 400 where parts are joined.  Neither is less
+// than the weights take, at 6.4 TB/s with 240 CTAs and a little less with fewer (the down projection of 32 tokens: 5.5
+// TB/s with 128, 6.2 with 256).
+constexpr int64_t few_block_cost(int nt, bool glu, bool shared) {
+    return nt <= 16 ? (glu ? 35 : 26) : nt <= 32 ? (glu ? 40 : 28) : nt <= 64 ? (!glu ? 44 : shared ? 70 : 50) : glu ? 85 : shared ? 70 : 32;
 }
-constexpr int64_t kFewWave = 260, kFewJoin = 30, kFewPart = 15;
-constexpr int64_t kManyBlock = 50, kManyWave = 350, kManyJoin = 300;
+constexpr int64_t few_wave_cost(int nt) { return nt > 64 ? 310 : 260; }
+constexpr int64_t few_join_cost(int nt, int split) { return split > 1 ? 30 + (nt > 64 ? 28 : 15) * split : 0; }
+constexpr int64_t kManyBlock = 34, kManyWave = 380, kManyJoin = 400;
 
 static int64_t stream_cost(const Fp8GemmDesc& d, int64_t ctas) {
     const int64_t bytes = d.groups * d.segs * d.N * (d.glu ? 2 : 1) * d.K;
@@ -1150,10 +1152,11 @@ static Fp8Plan plan_few(const Fp8GemmDesc& d) {
         // the occupancy query counts one CTA an SM of every kernel here; the times show that two of the smaller ones share it
         const int mc = resident_clusters(kern, split, Cfg::THREADS, Cfg::SMEM_BYTES, resident[split - 1]) * (Cfg::ONE ? 1 : 2);
         if (mc <= 0) continue;
-        const int64_t waves = (tiles + mc - 1) / mc;
-        const int64_t stream = stream_cost(d, std::min<int64_t>(tiles, mc) * split);
-        const int64_t cost = std::max(waves * ((kb + split - 1) / split) * few_block_cost(NT, GLU), stream) + waves * kFewWave +
-                             (split > 1 ? kFewJoin + kFewPart * split : 0);
+        const int64_t waves = (tiles + mc - 1) / mc, ctas = std::min<int64_t>(tiles, mc) * split;
+        const int64_t stream = stream_cost(d, ctas);
+        const int64_t block = few_block_cost(NT, GLU, ctas > std::max(1, device_sms()));
+        const int64_t cost = std::max(waves * ((kb + split - 1) / split) * block, stream) + waves * few_wave_cost(NT) +
+                             few_join_cost(NT, split);
         if (best.cost < 0 || cost < best.cost) {
             best.cost = cost;
             best.split = split;
@@ -1271,7 +1274,7 @@ static tp_status run_few(Fp8GemmArgs& a, const Fp8GemmDesc& d, cudaStream_t stre
 }
 
 // Up to 64 tokens one tile of them; more: whichever kernel and tile should take least.  100 tokens of four shards' down projection:
-// 44 us in tiles of 128, 64 on CTA pairs; 300 in QKV of eight shards 48 and 72; gate_up of 100 tokens 112 and 104.
+// 44 us in tiles of 128, 48 on CTA pairs; 300 in QKV of eight shards 48 and 50; gate_up of 100 tokens 102 and 86.
 template <bool GLU>
 static tp_status launch_sized(Fp8GemmArgs& a, const Fp8GemmDesc& d, cudaStream_t stream) {
     if (d.M <= 16) return run_few<16, GLU>(a, d, stream);
