@@ -30,9 +30,9 @@ struct Fp8QuantArgs {
 //
 // A thread has eight columns of ROWS consecutive rows, whose loads it issues
 // before it uses the first; sixteen neighbouring lanes hold a group.  Blocks are
-// as wide as the rows up to 1024 columns.  Four matrices of 8192 x 2048: 32.6 us, 6.2
-// TB/s (with the largest magnitude taken from fp32 values 34.2 us, values scaled
-// and negated one by one 38 us).
+// as wide as the rows up to 1024 columns.  Four matrices of 8192 x 2048: 32.1 us, 6.3
+// TB/s (quotients with a second correction 32.6 us, the largest magnitude taken
+// from fp32 values 34.2 us, values scaled and negated one by one 38 us).
 constexpr int kRowThreads = 128;
 
 template <bool F32, int ROWS>
@@ -74,8 +74,9 @@ __global__ void __launch_bounds__(kRowThreads) fp8_quant_rows_kernel(const __gri
 //
 // One thread block per 128 x 128 block, held in registers between its largest
 // value and its codes.  What it takes beside the memory is arithmetic, which other
-// thread blocks' loads cover: 14336 x 8192 with four an SM 55 us, 6.4 TB/s (three
-// 61 us, five 72 us; two or three of 512 threads 76 and 65 us).
+// thread blocks' loads cover: 14336 x 8192 with four an SM 52.7 us, 6.7 TB/s (with
+// quotients of a second correction 55 us, three an SM 61, five 72, two or three of
+// 512 threads 76 and 65).
 constexpr int kQuantThreads = 256;
 constexpr int kWeightRowsPerPass = kQuantThreads / 16;
 constexpr int kWeightPasses = kFp8Group / kWeightRowsPerPass;
@@ -179,7 +180,7 @@ tp_status launch_fp8_quant(const Fp8QuantDesc& d, cudaStream_t stream) {
 // stored, rounded once), the squares are summed over the block, and the
 // normed values go from fp32 to 8 bits without a rounding between.  Eight
 // elements a thread and vector, so that a group is a half warp's.  8192 rows of
-// 8192 from four bf16 shards: 136 us, 6.4 TB/s.
+// 8192 from four bf16 shards: 135 us, 6.5 TB/s.
 struct Fp8NormArgs {
     const void* p[TP_MAX_SHARDS];
     const uint16_t* residual;
