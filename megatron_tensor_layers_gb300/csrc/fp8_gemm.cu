@@ -1092,17 +1092,16 @@ __global__ void __launch_bounds__(kManyThreads, 1) fp8_many_kernel(const __grid_
 // ------------------------------------------------------------------ host
 
 // Costs in hundredths of a microsecond, fitted to the kernels' times over 70 shapes (the choice costs 1 % over the best of all
-// variants there and over 140 others).  A wave of the few-row kernel takes so much a K block, by its tokens, plain and
-// gated, and more where two CTAs share an SM and its tensor core; 260 to 1000 beside them; and parts that are joined 30 and 15
-// each (28).  A wave of the many-row kernel takes 34 a block, 380, and 400 where parts are joined.  Neither is less
-// than the weights take, at 6.4 TB/s with 240 CTAs and a little less with fewer (the down projection of 32 tokens: 5.5
-// TB/s with 128, 6.2 with 256).
-constexpr int64_t few_block_cost(int nt, bool glu, bool shared) {
-    return nt <= 16 ? (glu ? 35 : 26) : nt <= 32 ? (glu ? 40 : 28) : nt <= 64 ? (!glu ? 44 : shared ? 70 : 50) : glu ? 85 : shared ? 70 : 32;
+// variants there and over 250 others).  A wave of the few-row kernel takes so much a K block, by its tokens, plain and
+// gated; 260 to 600 beside them, most of it the ends of tiles, which parts share; and parts that are joined 30 and 15 each
+// (28).  A wave of the many-row kernel takes 34 a block, 380, and 400 where parts are joined.  Neither is less than the weights
+// take, at 6.4 TB/s with 240 CTAs and a little less with fewer (the down projection of 32 tokens: 5.5 TB/s with 128, 6.2
+// with 256).
+constexpr int64_t few_block_cost(int nt, bool glu) {
+    return nt <= 16 ? (glu ? 35 : 26) : nt <= 32 ? (glu ? 40 : 28) : nt <= 64 ? (glu ? 50 : 44) : glu ? 85 : 32;
 }
-// ... beside its K blocks: most of it the ends of tiles, which parts share
 constexpr int64_t few_wave_cost(int nt, bool glu, bool shared, int split) {
-    return 260 + (nt > 64 ? (glu ? 340 : shared ? 590 : 50) : nt > 32 && shared ? (glu ? 740 : 340) : 0) / split;
+    return 260 + (nt > 64 ? (glu ? 340 : 50) : nt > 32 && !glu && shared ? 340 : 0) / split;
 }
 constexpr int64_t few_join_cost(int nt, int split) { return split > 1 ? 30 + (nt > 64 ? 28 : 15) * split : 0; }
 constexpr int64_t kManyBlock = 34, kManyWave = 380, kManyJoin = 400;
@@ -1159,10 +1158,9 @@ static Fp8Plan plan_few(const Fp8GemmDesc& d) {
         if (mc <= 0) continue;
         const int64_t waves = (tiles + mc - 1) / mc, ctas = std::min<int64_t>(tiles, mc) * split;
         const int64_t stream = stream_cost(d, ctas);
-        const bool shared = ctas > std::max(1, device_sms());
-        const int64_t block = few_block_cost(NT, GLU, shared);
-        const int64_t cost = std::max(waves * ((kb + split - 1) / split) * block, stream) + waves * few_wave_cost(NT, GLU, shared, split) +
-                             few_join_cost(NT, split);
+        const bool shared = ctas > std::max(1, device_sms());            // two CTAs on an SM
+        const int64_t cost = std::max(waves * ((kb + split - 1) / split) * few_block_cost(NT, GLU), stream) +
+                             waves * few_wave_cost(NT, GLU, shared, split) + few_join_cost(NT, split);
         if (best.cost < 0 || cost < best.cost) {
             best.cost = cost;
             best.split = split;
