@@ -129,22 +129,20 @@ __device__ __forceinline__ void finish_gated(const Fp8GemmArgs& args, int g, int
     const int nvalid = args.N - col;                     // this lane's columns inside the group
     const GateAct act(args.act, args.out_kind == FP8_OUT_CODES);
     f32x2 v2[2] = {mul2(act(pack2(gate[0], gate[1])), pack2(up[0], up[1])), mul2(act(pack2(gate[2], gate[3])), pack2(up[2], up[3]))};
-    float v[4];
-    unpack2(v2[0], v[0], v[1]);
-    unpack2(v2[1], v[2], v[3]);
     if (args.out_kind == FP8_OUT_CODES) {
-        float top = 0.0f;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) top = i < nvalid ? max_nan(top, fabsf(v[i])) : top;
+        float top = nvalid > 0 ? amax_pairs(v2) : 0.0f;  // N is a multiple of 16: all four or none
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, o));
         const float s = fp8_scale(top);
         uint32_t code[1];
         fp8_codes(v2, s, code);
-        if (nvalid > 0)                                  // N is a multiple of 16: all four or none
+        if (nvalid > 0)
             *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(args.out[g]) + row * args.ldo + col) = code[0];
         if (lane == 0) args.os[g][static_cast<int64_t>(n) * args.ldos + row] = s;
     } else if (nvalid > 0) {
+        float v[4];
+        unpack2(v2[0], v[0], v[1]);
+        unpack2(v2[1], v[2], v[3]);
         store_quad(args.out[g], args.ldo, args.out_kind == FP8_OUT_F32, row, col, min(4, nvalid), v);
     }
 }
