@@ -561,7 +561,7 @@ __global__ void __launch_bounds__(FewCfg<NT, GLU>::THREADS, FewCfg<NT, GLU>::ONE
 // each row half finishes its share of the rows, summing in the pairs' order.
 constexpr int kManyStages = 6;
 constexpr int kScaleAhead = 6;            // K blocks ahead that scales are asked for
-constexpr int kScaleSlots = kScaleAhead + kManyStages + 2;
+constexpr int kScaleSlots = kScaleAhead + kManyStages + 3;   // see the scales' warp
 constexpr int kManyThreads = 384;         // a warpgroup of producers, two of sums
 constexpr int kManyFirst = 4;             // first warp of those
 // Registers: 168 a thread at launch; the producers' warpgroup gives up 128 of them, each of the others takes 64.
@@ -786,8 +786,9 @@ __global__ void __launch_bounds__(kManyThreads, 1) fp8_many_kernel(const __grid_
             // ------------------------------------------------ scales (both CTAs)
             // Those of this CTA's 128 rows and the two weight blocks, by asynchronous copies kScaleAhead blocks ahead
             // (loaded two blocks ahead by the warps that use them, their latency bounded the kernel).  Block j's
-            // arrival waits for block j - 6's products, the barriers' phase before; by then the sums have read block
-            // j - 8's scales, since block j - 6's products waited for that, and its slot may be asked for again.
+            // arrival waits for block j - 6's products, the barriers' phase before, which waited until the sums' warps had
+            // read block j - 8's accumulator.  One scale of a block is read after that, but block j - 9's are all used by
+            // then: its slot may be asked for again.
             pdl_wait();
             float* raw = reinterpret_cast<float*>(base_ptr + kRawOff);
             int s = 0, ask_slot = 0;
