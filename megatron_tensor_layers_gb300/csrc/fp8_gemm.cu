@@ -182,7 +182,8 @@ struct FewCfg {
     static constexpr int NBARS = 2 * STAGES;
     static constexpr int AHEAD = 4;                            // K blocks ahead that scales are asked for
     static constexpr int SLOTS = AHEAD + STAGES + BUFS;
-    static constexpr int SLOT_FLOATS = NT + 4;                 // a block's scales: the tokens', the weight blocks'
+    static constexpr int FACTORS = (GLU ? 2 : 1) * NT;         // of a block: the tokens' scales times gate's, and times up's
+    static constexpr int SLOT_FLOATS = FACTORS + 4;            // ... and the weight blocks' scales
     static constexpr int SCALE_BYTES = SLOTS * SLOT_FLOATS * 4;
     static constexpr int SMEM_BYTES = 1024 + STAGES * STAGE_BYTES + SCALE_BYTES + NBARS * 8 + 16;
     static_assert(STAGES >= BUFS && TMEM_BUFS >= 2, "both pipelines need two slots");
@@ -350,7 +351,7 @@ __global__ void __launch_bounds__(FewCfg<NT, GLU>::THREADS, FewCfg<NT, GLU>::ONE
 #pragma unroll
                 for (int p = 0; p < NT; p += 32)
                     if (p + lane < NT && tok + p < args.M) cp_async4(at + p * 4, xs + p);
-                if (lane < (GLU ? 2 : 1)) cp_async4(at + NT * 4, ws);
+                if (lane < (GLU ? 2 : 1)) cp_async4(at + Cfg::FACTORS * 4, ws);
                 xs += args.ldxs;
                 ++ws;
                 if (++kb == args.k_blocks && i + 1 < blocks) {
@@ -362,7 +363,7 @@ __global__ void __launch_bounds__(FewCfg<NT, GLU>::THREADS, FewCfg<NT, GLU>::ONE
             }
             cp_async_commit();
         };
-        int s = 0;
+        int s = 0, slot = 0;
         uint32_t phase = 0;
         for (int i = 0; i < blocks; ++i) {
             if (!mbar_wait_warp(done_bar(s), phase ^ 1u, abort_flag, args.status)) {
@@ -372,6 +373,19 @@ __global__ void __launch_bounds__(FewCfg<NT, GLU>::THREADS, FewCfg<NT, GLU>::ONE
             for (; asked <= i + Cfg::AHEAD; ++asked) ask(asked);
             cp_async_wait<Cfg::AHEAD>();
             __syncwarp();
+            // the tokens' scales become the columns' factors here, once for all warps that use them
+            float* f = scales_ptr + slot * Cfg::SLOT_FLOATS;
+            const float w = f[Cfg::FACTORS], up = f[Cfg::FACTORS + (GLU ? 1 : 0)];
+#pragma unroll
+            for (int p = 0; p < NT; p += 32) {
+                if (p + lane < NT) {
+                    const float x = f[p + lane];
+                    if (GLU) f[NT + p + lane] = x * up;
+                    f[p + lane] = x * w;
+                }
+            }
+            __syncwarp();
+            slot = slot == Cfg::SLOTS - 1 ? 0 : slot + 1;
             if (elect_one()) mbar_arrive(done_bar(s));
             if (++s == Cfg::STAGES) {
                 s = 0;
@@ -405,9 +419,7 @@ __global__ void __launch_bounds__(FewCfg<NT, GLU>::THREADS, FewCfg<NT, GLU>::ONE
             }
             tc_fence_after();
             const uint32_t taddr = lane_base + static_cast<uint32_t>(b * Cfg::ACC_COLS);
-            const float* f = scales_ptr + slot * Cfg::SLOT_FLOATS;
-            const float w = f[NT + (GLU ? part : 0)];
-            const f32x2 w2 = pack2(w, w);
+            const float* f = scales_ptr + slot * Cfg::SLOT_FLOATS + (GLU ? part * NT : col0);
             constexpr bool kAhead = GLU && NT == 128;
             float dd[kAhead ? 2 : 1][16];
 #pragma unroll
@@ -417,9 +429,9 @@ __global__ void __launch_bounds__(FewCfg<NT, GLU>::THREADS, FewCfg<NT, GLU>::ONE
                 f32x2 x[8];                      // the columns' factors
 #pragma unroll
                 for (int j = 0; j < 16; j += 4) {
-                    const float4 v = *reinterpret_cast<const float4*>(f + col0 + c * 16 + j);
-                    x[j / 2] = mul2(pack2(v.x, v.y), w2);
-                    x[j / 2 + 1] = mul2(pack2(v.z, v.w), w2);
+                    const float4 v = *reinterpret_cast<const float4*>(f + c * 16 + j);
+                    x[j / 2] = pack2(v.x, v.y);
+                    x[j / 2 + 1] = pack2(v.z, v.w);
                 }
                 tmem_wait(d);
                 if (kAhead && c + 1 < Cfg::NC / 16) tmem_ld(taddr + (c + 1) * 16, dd[(c + 1) & 1]);
