@@ -182,7 +182,10 @@ struct FewCfg {
     static constexpr int NBARS = 2 * STAGES;
     static constexpr int AHEAD = 4;                            // K blocks ahead that scales are asked for
     static constexpr int SLOTS = AHEAD + STAGES + BUFS;
-    static constexpr int FACTORS = (GLU ? 2 : 1) * NT;         // of a block: the tokens' scales times gate's, and times up's
+    // whether the scales' warp multiplies the tokens' scales with the weight blocks'; with 128 tokens of gate and up the warps
+    // that use them do, for whose sums leave no registers for factors read ahead (100 tokens 102 us and 135)
+    static constexpr bool FACTORED = !(GLU && NT == 128);
+    static constexpr int FACTORS = (GLU && FACTORED ? 2 : 1) * NT;   // of a block: times gate's, and times up's
     static constexpr int SLOT_FLOATS = FACTORS + 4;            // ... and the weight blocks' scales
     static constexpr int SCALE_BYTES = SLOTS * SLOT_FLOATS * 4;
     static constexpr int SMEM_BYTES = 1024 + STAGES * STAGE_BYTES + SCALE_BYTES + NBARS * 8 + 16;
@@ -373,18 +376,19 @@ __global__ void __launch_bounds__(FewCfg<NT, GLU>::THREADS, FewCfg<NT, GLU>::ONE
             for (; asked <= i + Cfg::AHEAD; ++asked) ask(asked);
             cp_async_wait<Cfg::AHEAD>();
             __syncwarp();
-            // the tokens' scales become the columns' factors here, once for all warps that use them
-            float* f = scales_ptr + slot * Cfg::SLOT_FLOATS;
-            const float w = f[Cfg::FACTORS], up = f[Cfg::FACTORS + (GLU ? 1 : 0)];
+            if (Cfg::FACTORED) {                 // the columns' factors, once for all warps that use them
+                float* f = scales_ptr + slot * Cfg::SLOT_FLOATS;
+                const float w = f[Cfg::FACTORS], up = f[Cfg::FACTORS + (GLU ? 1 : 0)];
 #pragma unroll
-            for (int p = 0; p < NT; p += 32) {
-                if (p + lane < NT) {
-                    const float x = f[p + lane];
-                    if (GLU) f[NT + p + lane] = x * up;
-                    f[p + lane] = x * w;
+                for (int p = 0; p < NT; p += 32) {
+                    if (p + lane < NT) {
+                        const float x = f[p + lane];
+                        if (GLU) f[NT + p + lane] = x * up;
+                        f[p + lane] = x * w;
+                    }
                 }
+                __syncwarp();
             }
-            __syncwarp();
             slot = slot == Cfg::SLOTS - 1 ? 0 : slot + 1;
             if (elect_one()) mbar_arrive(done_bar(s));
             if (++s == Cfg::STAGES) {
@@ -419,8 +423,10 @@ __global__ void __launch_bounds__(FewCfg<NT, GLU>::THREADS, FewCfg<NT, GLU>::ONE
             }
             tc_fence_after();
             const uint32_t taddr = lane_base + static_cast<uint32_t>(b * Cfg::ACC_COLS);
-            const float* f = scales_ptr + slot * Cfg::SLOT_FLOATS + (GLU ? part * NT : col0);
-            constexpr bool kAhead = GLU && NT == 128;
+            const float* f = scales_ptr + slot * Cfg::SLOT_FLOATS + (GLU && Cfg::FACTORED ? part * NT : col0);
+            const float w = Cfg::FACTORED ? 1.0f : f[Cfg::FACTORS + part];
+            const f32x2 w2 = pack2(w, w);
+            constexpr bool kAhead = !Cfg::FACTORED;
             float dd[kAhead ? 2 : 1][16];
 #pragma unroll
             for (int c = 0; c < Cfg::NC / 16; ++c) {
@@ -430,8 +436,8 @@ __global__ void __launch_bounds__(FewCfg<NT, GLU>::THREADS, FewCfg<NT, GLU>::ONE
 #pragma unroll
                 for (int j = 0; j < 16; j += 4) {
                     const float4 v = *reinterpret_cast<const float4*>(f + c * 16 + j);
-                    x[j / 2] = pack2(v.x, v.y);
-                    x[j / 2 + 1] = pack2(v.z, v.w);
+                    x[j / 2] = Cfg::FACTORED ? pack2(v.x, v.y) : mul2(pack2(v.x, v.y), w2);
+                    x[j / 2 + 1] = Cfg::FACTORED ? pack2(v.z, v.w) : mul2(pack2(v.z, v.w), w2);
                 }
                 tmem_wait(d);
                 if (kAhead && c + 1 < Cfg::NC / 16) tmem_ld(taddr + (c + 1) * 16, dd[(c + 1) & 1]);
