@@ -1110,15 +1110,15 @@ __global__ void __launch_bounds__(kManyThreads, 1) fp8_many_kernel(const __grid_
 
 // Costs in hundredths of a microsecond, fitted to the kernels' times over 70 shapes (the choice costs 1 % over the best of all
 // variants there and over 250 others).  A wave of the few-row kernel takes so much a K block, by its tokens, plain and
-// gated; 260 to 600 beside them, most of it the ends of tiles, which parts share; and parts that are joined 30 and 15 each
+// gated; 260 to 660 beside them, most of it the ends of tiles, which parts share; and parts that are joined 30 and 15 each
 // (28).  A wave of the many-row kernel takes 34 a block, 380, and 400 where parts are joined.  Neither is less than the weights
 // take, at 6.4 TB/s with 240 CTAs and a little less with fewer (the down projection of 32 tokens: 5.5 TB/s with 128, 6.2
 // with 256).
 constexpr int64_t few_block_cost(int nt, bool glu) {
-    return nt <= 16 ? (glu ? 35 : 26) : nt <= 32 ? (glu ? 40 : 28) : nt <= 64 ? (glu ? 50 : 44) : glu ? 85 : 32;
+    return nt <= 16 ? (glu ? 35 : 26) : nt <= 32 ? (glu ? 40 : 28) : nt <= 64 ? (glu ? 44 : 39) : glu ? 66 : 31;
 }
 constexpr int64_t few_wave_cost(int nt, bool glu, bool shared, int split) {
-    return 260 + (nt > 64 ? (glu ? 340 : 50) : nt > 32 && !glu && shared ? 340 : 0) / split;
+    return 260 + (nt > 64 ? (glu ? 400 : 70) : nt > 32 ? (glu ? 60 : shared ? 300 : 0) : 0) / split;
 }
 constexpr int64_t few_join_cost(int nt, int split) { return split > 1 ? 30 + (nt > 64 ? 28 : 15) * split : 0; }
 constexpr int64_t kManyBlock = 34, kManyWave = 380, kManyJoin = 400;
@@ -1295,7 +1295,7 @@ static tp_status run_few(Fp8GemmArgs& a, const Fp8GemmDesc& d, cudaStream_t stre
 }
 
 // Up to 64 tokens one tile of them; more: whichever kernel and tile should take least.  100 tokens of four shards' down projection:
-// 44 us in tiles of 128, 48 on CTA pairs; 300 in QKV of eight shards 48 and 50; gate_up of 100 tokens 102 and 86.
+// 44 us in tiles of 128, 48 on CTA pairs; 300 in QKV of eight shards 47 and 50; gate_up of 100 tokens 102 and 86.
 template <bool GLU>
 static tp_status launch_sized(Fp8GemmArgs& a, const Fp8GemmDesc& d, cudaStream_t stream) {
     if (d.M <= 16) return run_few<16, GLU>(a, d, stream);
