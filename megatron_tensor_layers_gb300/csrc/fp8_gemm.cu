@@ -627,6 +627,13 @@ __device__ __forceinline__ void many_coords(const Fp8GemmArgs& a, int tile, int&
     n = a.x_per_group ? col : col - g * a.n_tiles;
 }
 
+// 32 bytes to a 32-byte boundary.
+__device__ __forceinline__ void st_global_32(void* to, const uint32_t* v) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(to), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]),
+                 "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                 : "memory");
+}
+
 // A warp writes its rows' 64-byte pieces of an output (rows row0 .. row0 + live - 1, byte offset off of a row): each
 // lane's piece is staged at lane * STG_PITCH.  Whole pieces of aligned rows go out as 16-byte stores of 8 rows at a
 // time, others element by element.
@@ -1015,10 +1022,18 @@ __global__ void __launch_bounds__(kManyThreads, 1) fp8_many_kernel(const __grid_
                     if (live > 0 && valid > 0) {
                         uint32_t code[16];
                         fp8_codes(v, s, code);
+                        if (valid >= 64 && ((reinterpret_cast<uintptr_t>(out) | args.ldo) & 31) == 0) {
+                            uint8_t* to = out + (row0 + lane) * args.ldo + col0;       // this lane's 64 bytes, a sector each
+                            if (lane < live) {
+                                st_global_32(to, &code[0]);
+                                st_global_32(to + 32, &code[8]);
+                            }
+                        } else {
 #pragma unroll
-                        for (int j = 0; j < 16; j += 4)
-                            *reinterpret_cast<uint4*>(st_lane + j * 4) = make_uint4(code[j], code[j + 1], code[j + 2], code[j + 3]);
-                        many_store<1>(st, out, row0, live, args.ldo, col0, valid, lane);
+                            for (int j = 0; j < 16; j += 4)
+                                *reinterpret_cast<uint4*>(st_lane + j * 4) = make_uint4(code[j], code[j + 1], code[j + 2], code[j + 3]);
+                            many_store<1>(st, out, row0, live, args.ldo, col0, valid, lane);
+                        }
                     }
                 } else if (live > 0 && valid > 0) {
                     store_sums<32>(args, st, out, row0, live, col0, valid, lane, v);
