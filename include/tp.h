@@ -769,6 +769,18 @@ tp_status tp_set_gemm_cta_pair(int mode);
 tp_status tp_set_gemm_split(int mode, int max_clusters);
 
 /*
+ * The kernel of later tp_fp8_* products: tile 16, 32, 64 or 128 = that many
+ * tokens a tile, with weights as the MMA's rows; 256 = CTA pairs; 0 = automatic
+ * (by what each should take).  parts CTAs (pairs: 1, 2 or 4 of them) share
+ * a tile's K blocks; 0 = automatic, else a product with fewer blocks of 128
+ * columns returns TP_ERR_UNSUPPORTED.  max_clusters > 0 caps the pairs that are
+ * launched at once where none share a tile, so that each walks several.  For
+ * tests and tuning.  TP_ERR_INVALID_ARG for other values, and for parts of an
+ * automatic tile.
+ */
+tp_status tp_set_fp8_gemm(int tile, int parts, int max_clusters);
+
+/*
  * Test hook for the failure path: launches one thread block that waits, with
  * the library's bounded wait, on a shared-memory barrier that nothing ever
  * signals.  The wait gives up after `limit_ns` nanoseconds (capped at 1 s)
@@ -817,6 +829,15 @@ int tp_debug_first_worker(int block, int blocks, int groups, int workers);
  */
 tp_status tp_debug_gemm_plan(int64_t m, int64_t n, int64_t k, int groups, int segs, int gated, int sms,
                              int* kind, int* tile_n, int* cluster);
+
+/*
+ * The same for the tp_fp8_* products: tile and parts of tp_set_fp8_gemm that
+ * the library would take, where resident[5][8] clusters of tiles of 16, 32, 64,
+ * 128 and 256 tokens in 1 to 8 parts run at once (0 or less: that variant
+ * cannot run; TP_ERR_UNSUPPORTED when nothing can).
+ */
+tp_status tp_debug_fp8_plan(int64_t m, int64_t n, int64_t k, int groups, int segs, int gated, int sms,
+                            const int* resident, int* tile, int* parts);
 
 #ifdef __cplusplus
 }

@@ -44,6 +44,7 @@ from ._lib import (  # noqa: F401
     tp_mlp_workspace_size,
     tp_reduce_scatter_rmsnorm,
     tp_reset_collective_count,
+    tp_set_fp8_gemm,
     tp_set_gemm_cta_pair,
     tp_set_gemm_split,
     tp_set_gemm_tile_n,

@@ -39,7 +39,7 @@ EXPORTED = [
     "tp_kv_pages_workspace_size", "tp_kv_fork", "tp_kv_compact", "tp_beam_workspace_size", "tp_beam_select",
     "tp_debug_kv4_block", "tp_debug_part_flag", "tp_debug_first_worker",
     "tp_fp8_quantize", "tp_fp8_quantize_weight", "tp_fp8_rmsnorm", "tp_fp8_linear_col", "tp_fp8_linear_row",
-    "tp_fp8_mlp_workspace_size", "tp_fp8_mlp_forward",
+    "tp_fp8_mlp_workspace_size", "tp_fp8_mlp_forward", "tp_set_fp8_gemm", "tp_debug_fp8_plan",
 ]
 STATIC_SCRATCH_BYTES = 16 * 1024 * 1024
 
@@ -110,6 +110,8 @@ def load() -> ctypes.CDLL:
         "tp_fp8_mlp_workspace_size": (ctypes.c_size_t, [I32, I64, I64, I64, I32, I32]),
         "tp_fp8_mlp_forward": (I32, [I32, I64, I64, I64, P, I64, P, I64, P, P, P, I64, P, P, I32, I32, I32, P,
                                      ctypes.c_size_t, P, I32, P]),
+        "tp_set_fp8_gemm": (I32, [I32, I32, I32]),
+        "tp_debug_fp8_plan": (I32, [I64, I64, I64, I32, I32, I32, I32, P, P, P]),
         "tp_beam_select": (I32, [I32, I64, I32, I32, P, P, P, I32, P, P, ctypes.c_int32, P, P, P, P, ctypes.c_size_t, P]),
     }
     for name, (res, args) in sig.items():
@@ -670,6 +672,24 @@ def tp_set_gemm_split(mode: int, max_clusters: int = 0) -> None:
 def tp_set_gemm_tile_n(n: int) -> None:
     """Force the GEMM tile width (64/96/128/256) for later launches; 0 = automatic."""
     _check("tp_set_gemm_tile_n", load().tp_set_gemm_tile_n(n))
+
+
+def tp_set_fp8_gemm(tile: int = 0, parts: int = 0, max_clusters: int = 0) -> None:
+    """Kernel of later tp_fp8_* products: tile 16, 32, 64 or 128 tokens, or 256
+    for CTA pairs (0 automatic), whose K blocks `parts` CTAs or pairs share (0
+    automatic); max_clusters > 0 caps the pairs at once."""
+    _check("tp_set_fp8_gemm", load().tp_set_fp8_gemm(tile, parts, max_clusters))
+
+
+def tp_debug_fp8_plan(m: int, n: int, k: int, resident, *, groups: int = 1, segs: int = 1, gated: bool = False, sms: int = 152):
+    """The (tile, parts) the library would choose for an 8-bit product (host
+    logic only); resident: 5 x 8 clusters at once, of tiles of 16, 32, 64, 128
+    and 256 tokens in 1 to 8 parts."""
+    counts = (I32 * 40)(*[c for row in resident for c in row])
+    tile, parts = I32(), I32()
+    _check("tp_debug_fp8_plan", load().tp_debug_fp8_plan(m, n, k, groups, segs, int(gated), sms, counts, ctypes.byref(tile),
+                                                         ctypes.byref(parts)))
+    return tile.value, parts.value
 
 
 def tp_mlp_forward_static(x: torch.Tensor, w_gate_up: Sequence[torch.Tensor], w_down: Sequence[torch.Tensor], *,

@@ -2,6 +2,7 @@
 // carving and the kernel launches.  See include/tp.h for the contract.
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cmath>
 #include <cstdint>
 
@@ -27,6 +28,15 @@ constexpr int64_t kMaxSize = int64_t(1) << 29;
 
 // Row strides of codes (bytes), multiples of 16 as the TMA tiles need.
 inline bool codes_ld_ok(int64_t ld, int64_t minimum) { return ld >= minimum && ld % 16 == 0; }
+
+std::atomic<int> g_tile{0}, g_parts{0}, g_max_clusters{0};
+
+// The kernel choice in effect for a launch (tp_set_fp8_gemm).
+void apply_choice(tpk::Fp8GemmDesc& d) {
+    d.force_tile = g_tile.load();
+    d.force_parts = g_parts.load();
+    d.max_clusters = g_max_clusters.load();
+}
 
 // A gated block's hidden rows, one rank's: codes at columns [r fs, (r + 1) fs) of [n, f], scales [groups, n].
 struct HiddenLayout {
@@ -178,6 +188,7 @@ static tp_status linear_col_run(int t, int64_t n, int64_t in, int64_t out_full, 
         d.bias[r] = bias != nullptr ? bias[r] : nullptr;
     }
     d.status = tpk::device_status_word();
+    apply_choice(d);
     return tpk::launch_fp8_gemm(d, cs(stream));
 }
 
@@ -283,6 +294,7 @@ static tp_status linear_row_impl(int t, int64_t n, int64_t in_full, int64_t out,
         d.ws[r] = ws[r];
     }
     d.status = tpk::device_status_word();
+    apply_choice(d);
     d.weights_first = weights_first;
     if (fused) {
         d.segs = t;
@@ -362,6 +374,40 @@ tp_status tp_fp8_mlp_forward(int t, int64_t n, int64_t h, int64_t f, const void*
     if (st != TP_OK) return st;
     return linear_row_impl(t, n, f, h, reinterpret_cast<const void* const*>(hidden), f, hscales, n, w_down, ld_down,
                            s_down, bias_down, 1, mode, partial_dtype, parts, h, y, h, y_dtype, 1, stream);
+}
+
+static bool choice_ok(int tile, int parts) {
+    if (tile == 0) return parts == 0;
+    if (tile == 256) return parts == 0 || parts == 1 || parts == 2 || parts == 4;
+    return (tile == 16 || tile == 32 || tile == 64 || tile == 128) && parts >= 0 && parts <= 8;
+}
+
+tp_status tp_set_fp8_gemm(int tile, int parts, int max_clusters) {
+    TP_CHECK(choice_ok(tile, parts) && max_clusters >= 0, TP_ERR_INVALID_ARG);
+    g_tile.store(tile);
+    g_parts.store(parts);
+    g_max_clusters.store(max_clusters);
+    return TP_OK;
+}
+
+tp_status tp_debug_fp8_plan(int64_t m, int64_t n, int64_t k, int groups, int segs, int gated, int sms, const int* resident,
+                            int* tile, int* parts) {
+    TP_CHECK(m > 0 && n > 0 && k > 0 && m <= kMaxSize && n <= kMaxSize && k <= kMaxSize && sms >= 1, TP_ERR_INVALID_ARG);
+    TP_CHECK(groups >= 1 && groups <= TP_MAX_SHARDS && segs >= 1 && segs <= TP_MAX_SHARDS, TP_ERR_INVALID_ARG);
+    TP_CHECK((groups == 1 || segs == 1) && (gated == 0 || gated == 1), TP_ERR_INVALID_ARG);
+    TP_CHECK(resident != nullptr && tile != nullptr && parts != nullptr, TP_ERR_INVALID_ARG);
+    tpk::Fp8GemmDesc d;
+    d.M = m;
+    d.N = n;
+    d.K = k;
+    d.groups = groups;
+    d.segs = segs;
+    d.glu = gated;
+    const tpk::Fp8Plan p = tpk::plan_fp8_gemm(d, sms, resident);
+    TP_CHECK(p.cost >= 0, TP_ERR_UNSUPPORTED);
+    *tile = p.tile;
+    *parts = p.parts;
+    return TP_OK;
 }
 
 }  // extern "C"

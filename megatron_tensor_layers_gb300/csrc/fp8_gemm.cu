@@ -1166,39 +1166,79 @@ static int resident_clusters(const void* kern, int size, int threads, int smem, 
     return v;
 }
 
-struct Fp8Plan {
-    int split = 1, clusters = 0;
-    int64_t cost = -1;                   // none possible
-};
-
-// The number of CTAs (1 to 8) that share a tile, with two K blocks each at least, and what that costs.  What the sizes of
+// The number of CTAs (1 to 8; of CTA pairs 1, 2 or 4) that share a tile, with two K blocks each at least (pairs four), and what that costs;
+// resident(tile, parts) says how many such clusters run at once.  What the sizes of
 // clusters that fit the GPU at once decide most: QKV of 8 shards (80 tiles), 16 tokens: 18.4, 17.9, 15.9, 20.0 us in 1, 2, 3, 4
 // parts; the down projection of 32 tokens (64 tiles of 224 blocks) 65, 41, 40, 38, 46 us in 1 to 5; 8 tiles of 32 blocks
 // 7.5, 5.4, 4.7, 4.1, 4.1, 4.2 us in 1 to 5 and 8.
-template <int NT, bool GLU>
-static Fp8Plan plan_few(const Fp8GemmDesc& d) {
-    using Cfg = FewCfg<NT, GLU>;
-    static std::atomic<int> resident[8][64];
-    static std::atomic<uint64_t> smem_set{0};
+template <typename Resident>
+static Fp8Plan plan_tile(const Fp8GemmDesc& d, int tile, int sms, Resident&& resident) {
     Fp8Plan best;
-    const void* kern = reinterpret_cast<const void*>(fp8_few_kernel<NT, GLU>);
-    if (!smem_attribute_once(kern, Cfg::SMEM_BYTES, smem_set)) return best;
-    const int64_t tiles = d.groups * ((d.M + NT - 1) / NT) * ((d.N + 127) / 128), kb = fp8_groups(d.K) * d.segs;
-    for (int split = 1; split <= 8 && (split == 1 || kb / split >= 2); ++split) {
-        // the occupancy query counts one CTA an SM of every kernel here; the times show that two of the smaller ones share it
-        const int mc = resident_clusters(kern, split, Cfg::THREADS, Cfg::SMEM_BYTES, resident[split - 1]) * (Cfg::ONE ? 1 : 2);
+    const bool pairs = tile == 256, glu = d.glu != 0;
+    const int cols = pairs && !glu ? 256 : 128;
+    const int64_t tiles = d.groups * ((d.M + tile - 1) / tile) * ((d.N + cols - 1) / cols), kb = fp8_groups(d.K) * d.segs;
+    for (int parts = 1; parts <= (pairs ? 4 : 8); ++parts) {
+        if (pairs && parts == 3) continue;
+        if (d.force_parts > 0 ? parts != d.force_parts || kb < parts : parts > 1 && kb / parts < (pairs ? 4 : 2)) continue;
+        const int mc = resident(tile, parts);
         if (mc <= 0) continue;
-        const int64_t waves = (tiles + mc - 1) / mc, ctas = std::min<int64_t>(tiles, mc) * split;
-        const int64_t stream = stream_cost(d, ctas);
-        const bool shared = ctas > std::max(1, device_sms());            // two CTAs on an SM
-        const int64_t cost = std::max(waves * ((kb + split - 1) / split) * few_block_cost(NT, GLU), stream) +
-                             waves * few_wave_cost(NT, GLU, shared, split) + few_join_cost(NT, split);
+        const int64_t waves = (tiles + mc - 1) / mc, ctas = std::min<int64_t>(tiles, mc) * parts * (pairs ? 2 : 1);
+        const int64_t stream = stream_cost(d, ctas), blocks = (kb + parts - 1) / parts;
+        int64_t cost;
+        if (pairs) {
+            cost = std::max(waves * blocks * kManyBlock, stream) + waves * (kManyWave + (parts > 1 ? kManyJoin : 0));
+        } else {
+            const bool shared = ctas > sms;                              // two CTAs on an SM
+            cost = std::max(waves * blocks * few_block_cost(tile, glu), stream) + waves * few_wave_cost(tile, glu, shared, parts) +
+                   few_join_cost(tile, parts);
+        }
         if (best.cost < 0 || cost < best.cost) {
             best.cost = cost;
-            best.split = split;
+            best.tile = tile;
+            best.parts = parts;
+            best.clusters = mc;
         }
     }
     return best;
+}
+
+// Up to 64 tokens one tile of them; more: whichever kernel and tile should take least.  100 tokens of four shards' down projection:
+// 44 us in tiles of 128, 48 on CTA pairs; 300 in QKV of eight shards 47 and 50; gate_up of 100 tokens 102 and 86.
+template <typename Resident>
+static Fp8Plan plan_product(const Fp8GemmDesc& d, int sms, Resident&& resident) {
+    if (d.force_tile > 0) return plan_tile(d, d.force_tile, sms, resident);
+    if (d.M <= 64) return plan_tile(d, d.M <= 16 ? 16 : d.M <= 32 ? 32 : 64, sms, resident);
+    const Fp8Plan many = plan_tile(d, 256, sms, resident), few = plan_tile(d, 128, sms, resident), fewer = plan_tile(d, 64, sms, resident);
+    if (many.cost < 0 || few.cost < 0 || fewer.cost < 0) return Fp8Plan();
+    if (many.cost <= few.cost && many.cost <= fewer.cost) return many;
+    return few.cost <= fewer.cost ? few : fewer;
+}
+
+Fp8Plan plan_fp8_gemm(const Fp8GemmDesc& d, int sms, const int* resident) {
+    return plan_product(d, sms, [&](int tile, int parts) {
+        return resident[(tile == 16 ? 0 : tile == 32 ? 1 : tile == 64 ? 2 : tile == 128 ? 3 : 4) * 8 + parts - 1];
+    });
+}
+
+// Clusters of `parts` CTAs (CTA pairs) that share a tile and can be resident at once; 0 or less: none.
+template <int NT, bool GLU>
+static int resident_few(int parts) {
+    using Cfg = FewCfg<NT, GLU>;
+    static std::atomic<int> resident[8][64];
+    static std::atomic<uint64_t> smem_set{0};
+    const void* kern = reinterpret_cast<const void*>(fp8_few_kernel<NT, GLU>);
+    if (!smem_attribute_once(kern, Cfg::SMEM_BYTES, smem_set)) return 0;
+    // the occupancy query counts one CTA an SM of every kernel here; the times show that two of the smaller ones share it
+    return resident_clusters(kern, parts, Cfg::THREADS, Cfg::SMEM_BYTES, resident[parts - 1]) * (Cfg::ONE ? 1 : 2);
+}
+
+template <bool GLU>
+static int resident_many(int parts) {
+    static std::atomic<int> resident[3][64];
+    static std::atomic<uint64_t> smem_set{0};
+    const void* kern = reinterpret_cast<const void*>(fp8_many_kernel<GLU>);
+    if (!smem_attribute_once(kern, ManyCfg::SMEM_BYTES, smem_set)) return 0;
+    return resident_clusters(kern, 2 * parts, kManyThreads, ManyCfg::SMEM_BYTES, resident[parts >> 1]);
 }
 
 template <int NT, bool GLU>
@@ -1207,8 +1247,7 @@ static tp_status launch_few(Fp8GemmArgs& a, const Fp8GemmDesc& d, const Fp8Plan&
     a.m_tiles = static_cast<int>((d.M + NT - 1) / NT);
     a.n_tiles = static_cast<int>((d.N + 127) / 128);
     const int64_t tiles = static_cast<int64_t>(d.groups) * a.m_tiles * a.n_tiles;
-    if (plan.cost < 0) return TP_ERR_CUDA;
-    const int split = plan.split;
+    const int split = plan.parts;
     if (tiles * split > INT32_MAX) return TP_ERR_UNSUPPORTED;
     a.total_tiles = static_cast<int>(tiles);
     a.split = split;
@@ -1238,33 +1277,7 @@ static tp_status launch_few(Fp8GemmArgs& a, const Fp8GemmDesc& d, const Fp8Plan&
     return cudaGetLastError() == cudaSuccess ? TP_OK : TP_ERR_CUDA;
 }
 
-// CTA pairs: 256 x 256 tiles, whose K blocks are split over 1, 2 or 4 pairs, whichever takes the least.
-template <bool GLU>
-static Fp8Plan plan_many(const Fp8GemmDesc& d) {
-    static std::atomic<int> resident[3][64];
-    static std::atomic<uint64_t> smem_set{0};
-    Fp8Plan best;
-    const void* kern = reinterpret_cast<const void*>(fp8_many_kernel<GLU>);
-    if (!smem_attribute_once(kern, ManyCfg::SMEM_BYTES, smem_set)) return best;
-    const int64_t tiles = d.groups * ((d.M + 255) / 256) * ((d.N + (GLU ? 127 : 255)) / (GLU ? 128 : 256));
-    const int64_t kb = fp8_groups(d.K) * d.segs;
-    for (int i = 0; i < 3; ++i) {
-        const int split = 1 << i;
-        if (split > 1 && kb / split < 4) break;
-        const int mc = resident_clusters(kern, 2 * split, kManyThreads, ManyCfg::SMEM_BYTES, resident[i]);
-        if (mc <= 0) continue;
-        const int64_t waves = (tiles + mc - 1) / mc;
-        const int64_t stream = stream_cost(d, std::min<int64_t>(tiles, mc) * split * 2);
-        const int64_t cost = std::max(waves * ((kb + split - 1) / split) * kManyBlock, stream) + waves * (kManyWave + (split > 1 ? kManyJoin : 0));
-        if (best.cost < 0 || cost < best.cost) {
-            best.cost = cost;
-            best.split = split;
-            best.clusters = mc;
-        }
-    }
-    return best;
-}
-
+// CTA pairs: 256 x 256 tiles, whose K blocks are split over 1, 2 or 4 pairs.
 template <bool GLU>
 static tp_status launch_many(Fp8GemmArgs& a, const Fp8GemmDesc& d, const Fp8Plan& plan, cudaStream_t stream) {
     using Cfg = ManyCfg;
@@ -1282,19 +1295,20 @@ static tp_status launch_many(Fp8GemmArgs& a, const Fp8GemmDesc& d, const Fp8Plan
         if (!make_byte_operand_map(&a.mapX[i], d.x[i], d.M, d.K, d.ldx, 128)) return TP_ERR_CUDA;
     for (int i = 0; i < nW; ++i)
         if (!make_byte_operand_map(&a.mapW[i], d.w[i], GLU ? 2 * d.N : d.N, d.K, d.ldw, 128)) return TP_ERR_CUDA;
-    if (tiles * plan.split > INT32_MAX / 2) return TP_ERR_UNSUPPORTED;
-    a.split = plan.split;
+    if (tiles * plan.parts > INT32_MAX / 2) return TP_ERR_UNSUPPORTED;
+    a.split = plan.parts;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = static_cast<unsigned>(2 * plan.split);
+    attr[0].val.clusterDim.x = static_cast<unsigned>(2 * plan.parts);
     attr[0].val.clusterDim.y = 1;
     attr[0].val.clusterDim.z = 1;
     attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[1].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
     // one pair a tile: a persistent grid; parts: a cluster a tile
-    const int64_t clusters = plan.split == 1 ? std::min<int64_t>(tiles, plan.clusters) : tiles;
-    cfg.gridDim = dim3(static_cast<unsigned>(clusters * 2 * plan.split), 1, 1);
+    const int64_t resident = d.max_clusters > 0 ? std::min(d.max_clusters, plan.clusters) : plan.clusters;
+    const int64_t clusters = plan.parts == 1 ? std::min<int64_t>(tiles, resident) : tiles;
+    cfg.gridDim = dim3(static_cast<unsigned>(clusters * 2 * plan.parts), 1, 1);
     cfg.blockDim = dim3(kManyThreads, 1, 1);
     cfg.dynamicSmemBytes = Cfg::SMEM_BYTES;
     cfg.stream = stream;
@@ -1304,23 +1318,25 @@ static tp_status launch_many(Fp8GemmArgs& a, const Fp8GemmDesc& d, const Fp8Plan
     return cudaGetLastError() == cudaSuccess ? TP_OK : TP_ERR_CUDA;
 }
 
-template <int NT, bool GLU>
-static tp_status run_few(Fp8GemmArgs& a, const Fp8GemmDesc& d, cudaStream_t stream) {
-    return launch_few<NT, GLU>(a, d, plan_few<NT, GLU>(d), stream);
-}
-
-// Up to 64 tokens one tile of them; more: whichever kernel and tile should take least.  100 tokens of four shards' down projection:
-// 44 us in tiles of 128, 48 on CTA pairs; 300 in QKV of eight shards 47 and 50; gate_up of 100 tokens 102 and 86.
 template <bool GLU>
 static tp_status launch_sized(Fp8GemmArgs& a, const Fp8GemmDesc& d, cudaStream_t stream) {
-    if (d.M <= 16) return run_few<16, GLU>(a, d, stream);
-    if (d.M <= 32) return run_few<32, GLU>(a, d, stream);
-    if (d.M <= 64) return run_few<64, GLU>(a, d, stream);
-    const Fp8Plan many = plan_many<GLU>(d), few = plan_few<128, GLU>(d), fewer = plan_few<64, GLU>(d);
-    if (many.cost < 0 || few.cost < 0 || fewer.cost < 0) return TP_ERR_CUDA;
-    if (many.cost <= few.cost && many.cost <= fewer.cost) return launch_many<GLU>(a, d, many, stream);
-    if (few.cost <= fewer.cost) return launch_few<128, GLU>(a, d, few, stream);
-    return launch_few<64, GLU>(a, d, fewer, stream);
+    const Fp8Plan plan = plan_product(d, std::max(1, device_sms()), [](int tile, int parts) {
+        switch (tile) {
+            case 16: return resident_few<16, GLU>(parts);
+            case 32: return resident_few<32, GLU>(parts);
+            case 64: return resident_few<64, GLU>(parts);
+            case 128: return resident_few<128, GLU>(parts);
+            default: return resident_many<GLU>(parts);
+        }
+    });
+    if (plan.cost < 0) return d.force_parts > 0 ? TP_ERR_UNSUPPORTED : TP_ERR_CUDA;
+    switch (plan.tile) {
+        case 16: return launch_few<16, GLU>(a, d, plan, stream);
+        case 32: return launch_few<32, GLU>(a, d, plan, stream);
+        case 64: return launch_few<64, GLU>(a, d, plan, stream);
+        case 128: return launch_few<128, GLU>(a, d, plan, stream);
+        default: return launch_many<GLU>(a, d, plan, stream);
+    }
 }
 
 tp_status launch_fp8_gemm(const Fp8GemmDesc& d, cudaStream_t stream) {

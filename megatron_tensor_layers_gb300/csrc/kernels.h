@@ -409,8 +409,18 @@ struct Fp8GemmDesc {
     const void* bias[TP_MAX_SHARDS] = {};
     int* status = nullptr;
     int weights_first = 0;               // 1: the previous kernel is of the same call and writes no weight
+    int force_tile = 0, force_parts = 0, max_clusters = 0;   // tp_set_fp8_gemm's
 };
 tp_status launch_fp8_gemm(const Fp8GemmDesc& d, cudaStream_t stream);
+
+// What a product runs on: tiles of 16 to 128 tokens with weights as the MMA's rows, or (256) CTA pairs; CTAs or pairs
+// that share a tile's K blocks; clusters of them at once.
+struct Fp8Plan {
+    int tile = 0, parts = 1, clusters = 0;
+    int64_t cost = -1;                   // none possible
+};
+// resident[5][8]: clusters at once of tiles of 16, 32, 64, 128 and 256 tokens, in 1 to 8 parts.
+Fp8Plan plan_fp8_gemm(const Fp8GemmDesc& d, int sms, const int* resident);
 
 // Device address of the library's status word on the current device (null on failure).
 int* device_status_word();
