@@ -222,6 +222,18 @@ inline cudaError_t launch_pdl(Kern kern, dim3 grid, dim3 block, size_t smem, cud
     return cudaLaunchKernelEx(&cfg, kern, args...);
 }
 
+// Host: launch `kern` in plain stream order.  A launch answers with its own
+// error, here as everywhere in the library: the runtime's last error may be an
+// earlier call's.
+template <typename Kern, typename... Args>
+inline cudaError_t launch_plain(Kern kern, dim3 grid, dim3 block, cudaStream_t stream, Args... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = block;
+    cfg.stream = stream;
+    return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+
 // ---------------------------------------------------------------- TMA
 
 // 2-D tiled bulk-tensor load global -> shared, completing on `bar`.

@@ -1273,8 +1273,7 @@ static tp_status launch_few(Fp8GemmArgs& a, const Fp8GemmDesc& d, const Fp8Plan&
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = split > 1 ? 2 : 1;
-    if (cudaLaunchKernelEx(&cfg, kern, a) != cudaSuccess) return TP_ERR_CUDA;
-    return cudaGetLastError() == cudaSuccess ? TP_OK : TP_ERR_CUDA;
+    return cudaLaunchKernelEx(&cfg, kern, a) == cudaSuccess ? TP_OK : TP_ERR_CUDA;
 }
 
 // CTA pairs: 256 x 256 tiles, whose K blocks are split over 1, 2 or 4 pairs.
@@ -1314,8 +1313,7 @@ static tp_status launch_many(Fp8GemmArgs& a, const Fp8GemmDesc& d, const Fp8Plan
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    if (cudaLaunchKernelEx(&cfg, fp8_many_kernel<GLU>, a) != cudaSuccess) return TP_ERR_CUDA;
-    return cudaGetLastError() == cudaSuccess ? TP_OK : TP_ERR_CUDA;
+    return cudaLaunchKernelEx(&cfg, fp8_many_kernel<GLU>, a) == cudaSuccess ? TP_OK : TP_ERR_CUDA;
 }
 
 template <bool GLU>

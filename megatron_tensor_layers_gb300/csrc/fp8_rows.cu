@@ -170,7 +170,7 @@ tp_status launch_fp8_quant(const Fp8QuantDesc& d, cudaStream_t stream) {
             e = d.in_f32 ? launch_pdl(fp8_quant_rows_kernel<true, 1>, grid, block, 0, stream, a)
                          : launch_pdl(fp8_quant_rows_kernel<false, 1>, grid, block, 0, stream, a);
     }
-    return e == cudaSuccess && cudaGetLastError() == cudaSuccess ? TP_OK : TP_ERR_CUDA;
+    return e == cudaSuccess ? TP_OK : TP_ERR_CUDA;
 }
 
 // ------------------------------------------------------------------ norm
@@ -343,7 +343,7 @@ tp_status launch_fp8_norm(const Fp8NormDesc& d, cudaStream_t stream) {
     a.t = d.t;
     a.ring = d.ring;
     const cudaError_t e = d.in_bf16 ? launch_norm_typed<false>(a, stream) : launch_norm_typed<true>(a, stream);
-    return e == cudaSuccess && cudaGetLastError() == cudaSuccess ? TP_OK : TP_ERR_CUDA;
+    return e == cudaSuccess ? TP_OK : TP_ERR_CUDA;
 }
 
 }  // namespace tpk

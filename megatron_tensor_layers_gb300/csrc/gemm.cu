@@ -1647,8 +1647,7 @@ static tp_status launch_cfg(GemmArgs& a, const GemmDesc& d, cudaStream_t stream)
     set_pdl(attr[0]);
     cfg.attrs = attr;
     cfg.numAttrs = d.pdl ? 1 : 0;
-    if (cudaLaunchKernelEx(&cfg, kern, a) != cudaSuccess) return TP_ERR_CUDA;
-    return cudaGetLastError() == cudaSuccess ? TP_OK : TP_ERR_CUDA;
+    return cudaLaunchKernelEx(&cfg, kern, a) == cudaSuccess ? TP_OK : TP_ERR_CUDA;
 }
 
 template <int STAGES, int EPI, int KSUB = 1>
@@ -1724,8 +1723,7 @@ static tp_status launch_pair(GemmArgs& a, const GemmDesc& d, cudaStream_t stream
     }
     cfg.gridDim = dim3(2 * clusters, 1, 1);
     cfg.numAttrs = d.pdl ? 2 : 1;
-    if (cudaLaunchKernelEx(&cfg, kern, a) != cudaSuccess) return TP_ERR_CUDA;
-    return cudaGetLastError() == cudaSuccess ? TP_OK : TP_ERR_CUDA;
+    return cudaLaunchKernelEx(&cfg, kern, a) == cudaSuccess ? TP_OK : TP_ERR_CUDA;
 }
 
 template <int BN, int STAGES, int EPI, int KSUB = 1, int ROWS = 64>
@@ -1785,8 +1783,7 @@ static tp_status launch_split(GemmArgs& a, const GemmDesc& d, int cs, cudaStream
     }
     cfg.gridDim = dim3(cs * std::min(a.total_tiles, cap), 1, 1);
     cfg.numAttrs = d.pdl ? 2 : 1;
-    if (cudaLaunchKernelEx(&cfg, kern, a) != cudaSuccess) return TP_ERR_CUDA;
-    return cudaGetLastError() == cudaSuccess ? TP_OK : TP_ERR_CUDA;
+    return cudaLaunchKernelEx(&cfg, kern, a) == cudaSuccess ? TP_OK : TP_ERR_CUDA;
 }
 
 // Split-K plan for GEMMs of at most 64 rows: the tile width (256 or 128) and

@@ -398,11 +398,10 @@ tp_status launch_small_mlp(const SmallMlpDesc& d, cudaStream_t stream) {
 
     const int count4 = static_cast<int>(d.n * d.h / 4);
     const int blocks = (count4 + kRedCols - 1) / kRedCols;
-    if (launch_pdl(tp_mlp_small_reduce_kernel, dim3(blocks), dim3(kRedGroups * kRedCols), 0, stream,
-                   static_cast<const float*>(d.part), slices, count4, a.h, static_cast<const uint16_t*>(d.bias),
-                   d.y, d.y_f32) != cudaSuccess)
-        return TP_ERR_CUDA;
-    return cudaGetLastError() == cudaSuccess ? TP_OK : TP_ERR_CUDA;
+    const cudaError_t e = launch_pdl(tp_mlp_small_reduce_kernel, dim3(blocks), dim3(kRedGroups * kRedCols), 0, stream,
+                                     static_cast<const float*>(d.part), slices, count4, a.h,
+                                     static_cast<const uint16_t*>(d.bias), d.y, d.y_f32);
+    return e == cudaSuccess ? TP_OK : TP_ERR_CUDA;
 }
 
 }  // namespace tpk

@@ -222,7 +222,7 @@ static int sm_count_cached() {
 }
 
 template <bool IN_BF16, int G>
-static void launch_reduce_cfg(const ReduceArgs& a, int64_t count, int t, bool ring, int pdl, cudaStream_t stream) {
+static cudaError_t launch_reduce_cfg(const ReduceArgs& a, int64_t count, int t, bool ring, int pdl, cudaStream_t stream) {
     constexpr int VEC = IN_BF16 ? 8 : 4;
     const int slices = ring ? t : 1;
     const int64_t per_slice = (ring ? (count + t - 1) / t : count) / VEC + 1;
@@ -240,7 +240,7 @@ static void launch_reduce_cfg(const ReduceArgs& a, int64_t count, int t, bool ri
     at[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = at;
     cfg.numAttrs = pdl ? 1 : 0;
-    cudaLaunchKernelEx(&cfg, shard_reduce_kernel<IN_BF16, G>, a);
+    return cudaLaunchKernelEx(&cfg, shard_reduce_kernel<IN_BF16, G>, a);
 }
 
 tp_status launch_shard_reduce(const ReduceDesc& d, cudaStream_t stream) {
@@ -256,17 +256,18 @@ tp_status launch_shard_reduce(const ReduceDesc& d, cudaStream_t stream) {
     a.out_bf16 = d.out_bf16;
     a.replicate = d.replicate;
     const bool ring = d.ring != 0;
+    cudaError_t e;
     // vectors in flight per thread: about 8 loads of 16 bytes whatever t is
     if (d.in_bf16) {
-        if (d.t <= 2) launch_reduce_cfg<true, 4>(a, d.count, d.t, ring, d.pdl, stream);
-        else if (d.t <= 4) launch_reduce_cfg<true, 2>(a, d.count, d.t, ring, d.pdl, stream);
-        else launch_reduce_cfg<true, 1>(a, d.count, d.t, ring, d.pdl, stream);
+        if (d.t <= 2) e = launch_reduce_cfg<true, 4>(a, d.count, d.t, ring, d.pdl, stream);
+        else if (d.t <= 4) e = launch_reduce_cfg<true, 2>(a, d.count, d.t, ring, d.pdl, stream);
+        else e = launch_reduce_cfg<true, 1>(a, d.count, d.t, ring, d.pdl, stream);
     } else {
-        if (d.t <= 2) launch_reduce_cfg<false, 4>(a, d.count, d.t, ring, d.pdl, stream);
-        else if (d.t <= 4) launch_reduce_cfg<false, 2>(a, d.count, d.t, ring, d.pdl, stream);
-        else launch_reduce_cfg<false, 1>(a, d.count, d.t, ring, d.pdl, stream);
+        if (d.t <= 2) e = launch_reduce_cfg<false, 4>(a, d.count, d.t, ring, d.pdl, stream);
+        else if (d.t <= 4) e = launch_reduce_cfg<false, 2>(a, d.count, d.t, ring, d.pdl, stream);
+        else e = launch_reduce_cfg<false, 1>(a, d.count, d.t, ring, d.pdl, stream);
     }
-    return cudaGetLastError() == cudaSuccess ? TP_OK : TP_ERR_CUDA;
+    return e == cudaSuccess ? TP_OK : TP_ERR_CUDA;
 }
 
 // ------------------------------------------------------------------ gather
@@ -339,7 +340,7 @@ tp_status launch_shard_gather(const GatherDesc& d, cudaStream_t stream) {
     const int64_t nseg = d.rows * d.t;
     const int grid = static_cast<int>(std::min<int64_t>(nseg, static_cast<int64_t>(sms) * 16));
     const cudaError_t e = launch_pdl(shard_gather_kernel, dim3(grid), dim3(256), 0, stream, a);
-    return e == cudaSuccess && cudaGetLastError() == cudaSuccess ? TP_OK : TP_ERR_CUDA;
+    return e == cudaSuccess ? TP_OK : TP_ERR_CUDA;
 }
 
 // ------------------------------------------------------------------ probe
@@ -360,8 +361,7 @@ __global__ void expire_wait_kernel(uint64_t limit_ns, int* status) {
 }
 
 tp_status launch_expire_wait(uint64_t limit_ns, int* status, cudaStream_t stream) {
-    expire_wait_kernel<<<1, 32, 0, stream>>>(limit_ns, status);
-    return cudaGetLastError() == cudaSuccess ? TP_OK : TP_ERR_CUDA;
+    return launch_plain(expire_wait_kernel, dim3(1), dim3(32), stream, limit_ns, status) == cudaSuccess ? TP_OK : TP_ERR_CUDA;
 }
 
 }  // namespace tpk

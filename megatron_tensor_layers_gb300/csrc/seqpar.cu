@@ -195,7 +195,7 @@ static tp_status launch_seqpar_cfg(const SeqParArgs& a, int64_t n, size_t smem, 
     const int64_t resident = static_cast<int64_t>(std::max(sms, 1)) * std::max(per_sm, 1);
     const int grid = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(n, resident)));
     const cudaError_t e = launch_pdl(kern, dim3(grid), dim3(kSeqThreads), smem, stream, a);
-    return e == cudaSuccess && cudaGetLastError() == cudaSuccess ? TP_OK : TP_ERR_CUDA;
+    return e == cudaSuccess ? TP_OK : TP_ERR_CUDA;
 }
 
 tp_status launch_seqpar_rmsnorm(const SeqParDesc& d, cudaStream_t stream) {
