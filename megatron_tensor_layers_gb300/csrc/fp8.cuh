@@ -141,31 +141,71 @@ __device__ __forceinline__ float amax_pairs(const f32x2 (&x)[PAIRS]) {
     return m;
 }
 
-// act(g) of a gated block as g / (1 + exp(-z)): SiLU has z = g, and GeLU-tanh's
-// 0.5 g (1 + tanh(u)) is z = 2 u with u = sqrt(2/pi) (g + 0.044715 g^3).  With
-// coefficients in place of a branch, exp as 2^(g (a + b g^2)), and the hardware's
-// 2^x and reciprocal (2^-22 and 1 ulp); two values at a time.  `negated` gives
-// -act(g), with the same magnitude, as the codes' quotients take it.
+__device__ __forceinline__ f32x2 both(float v) { return pack2(v, v); }
+__device__ __forceinline__ f32x2 neg2(f32x2 v) { return v ^ 0x8000000080000000ull; }
+
+// act(g) of a gated block as g s, s = 1 / (1 + exp(-z)): SiLU has z = g, and
+// GeLU-tanh's 0.5 g (1 + tanh(u)) is z = 2 u with u = sqrt(2/pi) (g + 0.044715
+// g^3).  Two values at a time, with the hardware's 2^x (2 ulp) and reciprocal (1 ulp).  The
+// exponential of t = -z log2(e) alone would carry t's rounding, which grows with |g| (57 units of
+// 2^-24 at g = -60, 148 for GeLU at -9), so what t's rounding left, times ln 2, goes along as m and
+// moves s by its derivative, -s (1 - s) m (3876 rows of 4 x 5440 columns, K of 688: 170 us without,
+// 183 with it; K of 8192: no difference that the clock does not hide).  act(g) times up is then within 10
+// units of 2^-24: four of 2^x, one of the sum, two of the reciprocal, one each of the
+// correction and the two products; where 2^t passes fp32's range act(g) is 0.  `negated`
+// gives -act(g), with the same magnitude, as the codes' quotients take it.
+template <int ACT>
 struct GateAct {
-    f32x2 a, b;
-    float one;
-    __device__ __forceinline__ GateAct(int act, bool negated) : one(negated ? -1.0f : 1.0f) {
-        constexpr float log2e = 1.4426950408889634f, k = 2.0f * 0.7978845608028654f;
-        const bool gelu = act == TP_ACT_GELU_TANH_MUL;
-        const float fa = gelu ? -k * log2e : -log2e, fb = gelu ? -k * 0.044715f * log2e : 0.0f;
-        a = pack2(fa, fa);
-        b = pack2(fb, fb);
+    f32x2 sign;
+    __device__ __forceinline__ explicit GateAct(bool negated) : sign(negated ? 0ull : 0x8000000080000000ull) {}
+    // |g| past this has s of 0 or 1, and t and its rounding stay finite
+    static constexpr float kLimit = ACT == TP_ACT_GELU_TANH_MUL ? 32.0f : 1.0e30f;
+    // v where |v| is within the limit, else the limit with v's sign (of NaN either)
+    static __device__ __forceinline__ float limited(float v) {
+        float d;
+        asm("min.xorsign.abs.f32 %0, %1, %2;" : "=f"(d) : "f"(v), "f"(kLimit));
+        return d;
+    }
+    // -t, and -m
+    static __device__ __forceinline__ f32x2 exponent(f32x2 g, f32x2& m) {
+        constexpr double log2e = 1.4426950408889634074, k = 2.0 * 0.79788456080286535588, c = 0.044715;
+        constexpr float ln2 = 0.69314718055994531f;
+        if constexpr (ACT == TP_ACT_GELU_TANH_MUL) {
+            // -t = h q, h = p g and q = 1 + c g^2, each with what its rounding left; 1 - q is exact below 2^24
+            constexpr float p = static_cast<float>(k * log2e), pl = static_cast<float>(k * log2e - static_cast<double>(p));
+            constexpr float ch = static_cast<float>(c), cl = static_cast<float>(c - static_cast<double>(ch));
+            const f32x2 w = mul2(g, g), wl = fma2(g, g, neg2(w));
+            const f32x2 q = fma2(w, both(ch), both(1.0f));
+            f32x2 ql = fma2(w, both(ch), fma2(q, both(-1.0f), both(1.0f)));
+            ql = fma2(w, both(cl), ql);
+            ql = fma2(wl, both(ch), ql);
+            const f32x2 h = mul2(g, both(p)), hl = fma2(g, both(pl), fma2(g, both(p), neg2(h)));
+            const f32x2 nt = mul2(h, q);
+            f32x2 r = fma2(h, q, neg2(nt));
+            r = fma2(hl, q, r);
+            r = fma2(h, ql, r);
+            m = mul2(r, both(ln2));
+            return nt;
+        } else {
+            constexpr float p = static_cast<float>(log2e), pl = static_cast<float>(log2e - static_cast<double>(p));
+            const f32x2 nt = mul2(g, both(p));
+            const f32x2 r = fma2(g, both(-p), nt);               // t's rounding, but for p's own
+            m = mul2(fma2(g, both(-pl), r), both(-ln2));
+            return nt;
+        }
     }
     __device__ __forceinline__ f32x2 operator()(f32x2 g) const {
-        float s0, s1, e0, e1;
-        unpack2(mul2(g, g), s0, s1);
-        const f32x2 g2 = pack2(fminf(s0, 3.0e38f), fminf(s1, 3.0e38f));       // finite: b may be 0
-        unpack2(mul2(g, fma2(b, g2, a)), s0, s1);
-        asm("ex2.approx.f32 %0, %1;" : "=f"(e0) : "f"(s0));
-        asm("ex2.approx.f32 %0, %1;" : "=f"(e1) : "f"(s1));
-        asm("rcp.approx.f32 %0, %1;" : "=f"(s0) : "f"(fmaf(e0, one, one)));
-        asm("rcp.approx.f32 %0, %1;" : "=f"(s1) : "f"(fmaf(e1, one, one)));
-        return mul2(g, pack2(s0, s1));
+        float x0, x1, e0, e1;
+        unpack2(g, x0, x1);
+        f32x2 m;
+        unpack2(exponent(pack2(limited(x0), limited(x1)), m), x0, x1);
+        asm("ex2.approx.f32 %0, %1;" : "=f"(e0) : "f"(-x0));
+        asm("ex2.approx.f32 %0, %1;" : "=f"(e1) : "f"(-x1));
+        unpack2(fma2(pack2(e0, e1), both(-1.0f), both(-1.0f)), e0, e1);
+        asm("rcp.approx.f32 %0, %1;" : "=f"(x0) : "f"(e0));
+        asm("rcp.approx.f32 %0, %1;" : "=f"(x1) : "f"(e1));
+        const f32x2 ns = pack2(x0, x1);                          // -s; with ns^2 + ns = -s (1 - s)
+        return mul2(g ^ sign, fma2(m, fma2(ns, ns, ns), ns));
     }
 };
 

@@ -40,7 +40,7 @@ struct Fp8GemmArgs {
     int up_block;         // first block row of up in a gated weight's scales
     int m_tiles, n_tiles, total_tiles;
     int x_box_rows;       // rows of a token tile that a copy brings
-    int act, out_kind;
+    int out_kind;
     int split;            // CTAs (many rows: CTA pairs) of a cluster that share a tile's K blocks
     int band;             // many rows: row tiles of a raster band
     int weights_first;
@@ -123,11 +123,12 @@ __device__ __forceinline__ void cp_async_wait() {
 // Four neighbouring columns (lane * 4 of the warp's 128) of one row of a gated
 // tile: act(gate) * up, stored, or brought to 8 bits with the row's group in
 // the warp.
+template <int ACT>
 __device__ __forceinline__ void finish_gated(const Fp8GemmArgs& args, int g, int n, int64_t row, int lane,
                                              const float (&gate)[4], const float (&up)[4]) {
     const int col = n * 128 + lane * 4;
     const int nvalid = args.N - col;                     // this lane's columns inside the group
-    const GateAct act(args.act, args.out_kind == FP8_OUT_CODES);
+    const GateAct<ACT> act(args.out_kind == FP8_OUT_CODES);
     f32x2 v2[2] = {mul2(act(pack2(gate[0], gate[1])), pack2(up[0], up[1])), mul2(act(pack2(gate[2], gate[3])), pack2(up[2], up[3]))};
     if (args.out_kind == FP8_OUT_CODES) {
         float top = nvalid > 0 ? amax_pairs(v2) : 0.0f;  // N is a multiple of 16: all four or none
@@ -197,9 +198,10 @@ struct FewCfg {
     static_assert(SMEM_BYTES <= (ONE ? 227 : 113) * 1024, "shared memory");
 };
 
-template <int NT, bool GLU>
-__global__ void __launch_bounds__(FewCfg<NT, GLU>::THREADS, FewCfg<NT, GLU>::ONE ? 1 : 2)
+template <int NT, int ACT>
+__global__ void __launch_bounds__(FewCfg<NT, ACT != TP_ACT_NONE>::THREADS, FewCfg<NT, ACT != TP_ACT_NONE>::ONE ? 1 : 2)
     fp8_few_kernel(const __grid_constant__ Fp8GemmArgs args) {
+    constexpr bool GLU = ACT != TP_ACT_NONE;
     using Cfg = FewCfg<NT, GLU>;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw_addr = smem_u32(smem_raw);
@@ -527,7 +529,7 @@ __global__ void __launch_bounds__(FewCfg<NT, GLU>::THREADS, FewCfg<NT, GLU>::ONE
             if (GLU) {
                 const float4 u = sum(1, j);
                 const float up[4] = {u.x, u.y, u.z, u.w};
-                finish_gated(args, g, n, row, lane, v, up);
+                finish_gated<ACT>(args, g, n, row, lane, v, up);
                 continue;
             } else {
 #pragma unroll
@@ -704,8 +706,9 @@ __device__ __forceinline__ void store_sums(const Fp8GemmArgs& args, uint8_t* st,
     }
 }
 
-template <bool GLU>
+template <int ACT>
 __global__ void __launch_bounds__(kManyThreads, 1) fp8_many_kernel(const __grid_constant__ Fp8GemmArgs args) {
+    constexpr bool GLU = ACT != TP_ACT_NONE;
     using Cfg = ManyCfg;
     constexpr int STAGES = kManyStages;
     extern __shared__ uint8_t smem_raw[];
@@ -994,7 +997,7 @@ __global__ void __launch_bounds__(kManyThreads, 1) fp8_many_kernel(const __grid_
                     *reinterpret_cast<float4*>(to + (j < 64 ? col_a + j : col_b + j - 64)) = v;
                 }
             } else if (GLU) {
-                const GateAct act(args.act, args.out_kind == FP8_OUT_CODES);
+                const GateAct<ACT> act(args.out_kind == FP8_OUT_CODES);
                 uint8_t* out = static_cast<uint8_t*>(args.out[g]);
                 const int col0 = n * 128 + half * 64;
                 const int valid = args.N - col0;          // columns of this half inside the group
@@ -1097,7 +1100,7 @@ __global__ void __launch_bounds__(kManyThreads, 1) fp8_many_kernel(const __grid_
                         v[h][3] = a.w;
                     }
                     if (GLU) {
-                        finish_gated(args, g, n, row, lane, v[0], v[1]);
+                        finish_gated<ACT>(args, g, n, row, lane, v[0], v[1]);
                     } else {
     #pragma unroll
                         for (int h = 0; h < 2; ++h) {
@@ -1221,29 +1224,29 @@ Fp8Plan plan_fp8_gemm(const Fp8GemmDesc& d, int sms, const int* resident) {
 }
 
 // Clusters of `parts` CTAs (CTA pairs) that share a tile and can be resident at once; 0 or less: none.
-template <int NT, bool GLU>
+template <int NT, int ACT>
 static int resident_few(int parts) {
-    using Cfg = FewCfg<NT, GLU>;
+    using Cfg = FewCfg<NT, ACT != TP_ACT_NONE>;
     static std::atomic<int> resident[8][64];
     static std::atomic<uint64_t> smem_set{0};
-    const void* kern = reinterpret_cast<const void*>(fp8_few_kernel<NT, GLU>);
+    const void* kern = reinterpret_cast<const void*>(fp8_few_kernel<NT, ACT>);
     if (!smem_attribute_once(kern, Cfg::SMEM_BYTES, smem_set)) return 0;
     // the occupancy query counts one CTA an SM of every kernel here; the times show that two of the smaller ones share it
     return resident_clusters(kern, parts, Cfg::THREADS, Cfg::SMEM_BYTES, resident[parts - 1]) * (Cfg::ONE ? 1 : 2);
 }
 
-template <bool GLU>
+template <int ACT>
 static int resident_many(int parts) {
     static std::atomic<int> resident[3][64];
     static std::atomic<uint64_t> smem_set{0};
-    const void* kern = reinterpret_cast<const void*>(fp8_many_kernel<GLU>);
+    const void* kern = reinterpret_cast<const void*>(fp8_many_kernel<ACT>);
     if (!smem_attribute_once(kern, ManyCfg::SMEM_BYTES, smem_set)) return 0;
     return resident_clusters(kern, 2 * parts, kManyThreads, ManyCfg::SMEM_BYTES, resident[parts >> 1]);
 }
 
-template <int NT, bool GLU>
+template <int NT, int ACT>
 static tp_status launch_few(Fp8GemmArgs& a, const Fp8GemmDesc& d, const Fp8Plan& plan, cudaStream_t stream) {
-    using Cfg = FewCfg<NT, GLU>;
+    using Cfg = FewCfg<NT, ACT != TP_ACT_NONE>;
     a.m_tiles = static_cast<int>((d.M + NT - 1) / NT);
     a.n_tiles = static_cast<int>((d.N + 127) / 128);
     const int64_t tiles = static_cast<int64_t>(d.groups) * a.m_tiles * a.n_tiles;
@@ -1257,8 +1260,8 @@ static tp_status launch_few(Fp8GemmArgs& a, const Fp8GemmDesc& d, const Fp8Plan&
     for (int i = 0; i < nX; ++i)
         if (!make_byte_operand_map(&a.mapX[i], d.x[i], d.M, d.K, d.ldx, a.x_box_rows)) return TP_ERR_CUDA;
     for (int i = 0; i < nW; ++i)
-        if (!make_byte_operand_map(&a.mapW[i], d.w[i], GLU ? 2 * d.N : d.N, d.K, d.ldw, 128)) return TP_ERR_CUDA;
-    auto kern = fp8_few_kernel<NT, GLU>;
+        if (!make_byte_operand_map(&a.mapW[i], d.w[i], ACT != TP_ACT_NONE ? 2 * d.N : d.N, d.K, d.ldw, 128)) return TP_ERR_CUDA;
+    auto kern = fp8_few_kernel<NT, ACT>;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(tiles * split), 1, 1);
     cfg.blockDim = dim3(Cfg::THREADS, 1, 1);
@@ -1277,10 +1280,10 @@ static tp_status launch_few(Fp8GemmArgs& a, const Fp8GemmDesc& d, const Fp8Plan&
 }
 
 // CTA pairs: 256 x 256 tiles, whose K blocks are split over 1, 2 or 4 pairs.
-template <bool GLU>
+template <int ACT>
 static tp_status launch_many(Fp8GemmArgs& a, const Fp8GemmDesc& d, const Fp8Plan& plan, cudaStream_t stream) {
     using Cfg = ManyCfg;
-    const int out_cols = GLU ? 128 : 256;
+    const int out_cols = ACT != TP_ACT_NONE ? 128 : 256;
     a.m_tiles = static_cast<int>((d.M + 255) / 256);
     a.n_tiles = static_cast<int>((d.N + out_cols - 1) / out_cols);
     const int64_t tiles = static_cast<int64_t>(d.groups) * a.m_tiles * a.n_tiles;
@@ -1293,7 +1296,7 @@ static tp_status launch_many(Fp8GemmArgs& a, const Fp8GemmDesc& d, const Fp8Plan
     for (int i = 0; i < nX; ++i)
         if (!make_byte_operand_map(&a.mapX[i], d.x[i], d.M, d.K, d.ldx, 128)) return TP_ERR_CUDA;
     for (int i = 0; i < nW; ++i)
-        if (!make_byte_operand_map(&a.mapW[i], d.w[i], GLU ? 2 * d.N : d.N, d.K, d.ldw, 128)) return TP_ERR_CUDA;
+        if (!make_byte_operand_map(&a.mapW[i], d.w[i], ACT != TP_ACT_NONE ? 2 * d.N : d.N, d.K, d.ldw, 128)) return TP_ERR_CUDA;
     if (tiles * plan.parts > INT32_MAX / 2) return TP_ERR_UNSUPPORTED;
     a.split = plan.parts;
     cudaLaunchAttribute attr[2];
@@ -1313,27 +1316,27 @@ static tp_status launch_many(Fp8GemmArgs& a, const Fp8GemmDesc& d, const Fp8Plan
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, fp8_many_kernel<GLU>, a) == cudaSuccess ? TP_OK : TP_ERR_CUDA;
+    return cudaLaunchKernelEx(&cfg, fp8_many_kernel<ACT>, a) == cudaSuccess ? TP_OK : TP_ERR_CUDA;
 }
 
-template <bool GLU>
+template <int ACT>
 static tp_status launch_sized(Fp8GemmArgs& a, const Fp8GemmDesc& d, cudaStream_t stream) {
     const Fp8Plan plan = plan_product(d, std::max(1, device_sms()), [](int tile, int parts) {
         switch (tile) {
-            case 16: return resident_few<16, GLU>(parts);
-            case 32: return resident_few<32, GLU>(parts);
-            case 64: return resident_few<64, GLU>(parts);
-            case 128: return resident_few<128, GLU>(parts);
-            default: return resident_many<GLU>(parts);
+            case 16: return resident_few<16, ACT>(parts);
+            case 32: return resident_few<32, ACT>(parts);
+            case 64: return resident_few<64, ACT>(parts);
+            case 128: return resident_few<128, ACT>(parts);
+            default: return resident_many<ACT>(parts);
         }
     });
     if (plan.cost < 0) return d.force_parts > 0 ? TP_ERR_UNSUPPORTED : TP_ERR_CUDA;
     switch (plan.tile) {
-        case 16: return launch_few<16, GLU>(a, d, plan, stream);
-        case 32: return launch_few<32, GLU>(a, d, plan, stream);
-        case 64: return launch_few<64, GLU>(a, d, plan, stream);
-        case 128: return launch_few<128, GLU>(a, d, plan, stream);
-        default: return launch_many<GLU>(a, d, plan, stream);
+        case 16: return launch_few<16, ACT>(a, d, plan, stream);
+        case 32: return launch_few<32, ACT>(a, d, plan, stream);
+        case 64: return launch_few<64, ACT>(a, d, plan, stream);
+        case 128: return launch_few<128, ACT>(a, d, plan, stream);
+        default: return launch_many<ACT>(a, d, plan, stream);
     }
 }
 
@@ -1358,12 +1361,15 @@ tp_status launch_fp8_gemm(const Fp8GemmDesc& d, cudaStream_t stream) {
     a.groups = d.groups;
     a.x_per_group = d.x_per_group;
     a.up_block = static_cast<int>(fp8_groups(d.N));
-    a.act = d.act;
     a.out_kind = d.out_kind;
     a.status = d.status;
     a.weights_first = d.weights_first;
     if (static_cast<int64_t>(d.groups) * ((d.M + 127) / 128) * ((d.N + 127) / 128) > INT32_MAX / 8) return TP_ERR_UNSUPPORTED;
-    return d.glu ? launch_sized<true>(a, d, stream) : launch_sized<false>(a, d, stream);
+    switch (d.glu ? d.act : TP_ACT_NONE) {
+        case TP_ACT_SILU_MUL: return launch_sized<TP_ACT_SILU_MUL>(a, d, stream);
+        case TP_ACT_GELU_TANH_MUL: return launch_sized<TP_ACT_GELU_TANH_MUL>(a, d, stream);
+        default: return launch_sized<TP_ACT_NONE>(a, d, stream);
+    }
 }
 
 }  // namespace tpk
