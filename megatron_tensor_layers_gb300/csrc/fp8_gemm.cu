@@ -581,7 +581,13 @@ __global__ void __launch_bounds__(FewCfg<NT, ACT != TP_ACT_NONE>::THREADS, FewCf
 // each row half finishes its share of the rows, summing in the pairs' order.
 constexpr int kManyStages = 6;
 constexpr int kScaleAhead = 6;            // K blocks ahead that scales are asked for
-constexpr int kScaleSlots = kScaleAhead + kManyStages + 3;   // see the scales' warp
+constexpr int kScaleTurn = 5;             // stage of a turn of the ring at which the scales' warp waits for the last turn's reads
+constexpr int kScaleSlots = 18;
+// That wait, of a turn that begins with block T, says that the scales of blocks up to T - 2 have been read.  Until the next one, at
+// blocks T + kScaleTurn to T + kScaleTurn + kManyStages - 1, scales of kScaleAhead blocks more are asked for, the last into
+// the slot of block T + kScaleTurn + kManyStages - 1 + kScaleAhead - kScaleSlots.
+static_assert(kScaleTurn + kManyStages - 1 + kScaleAhead - kScaleSlots <= -2 && kScaleTurn < kManyStages,
+              "no slot is asked for before it is read");
 constexpr int kManyThreads = 384;         // a warpgroup of producers, two of sums
 constexpr int kManyFirst = 4;             // first warp of those
 // Registers: 168 a thread at launch; the producers' warpgroup gives up 128 of them, each of the others takes 64.
@@ -593,7 +599,7 @@ struct ManyCfg {
     static constexpr int STG_PITCH = 80;                     // 64 bytes of a row and a pad: no bank conflicts
     static constexpr int STG_BYTES = 8 * 32 * STG_PITCH;
     static constexpr int AMAX_BYTES = 2 * 2 * 128 * 4;       // two halves' largest values, two tiles in turn
-    static constexpr int NBARS = 2 * kManyStages + 4;
+    static constexpr int NBARS = 2 * kManyStages + 5;
     static constexpr int RAW_FLOATS = 128 + 4;               // a block's scales: 128 rows', the two weight blocks'
     static constexpr int RAW_BYTES = kScaleSlots * RAW_FLOATS * 4;
     static constexpr int SUM_PITCH = 260;                    // floats of a staged row of sums
@@ -725,6 +731,7 @@ __global__ void __launch_bounds__(kManyThreads, 1) fp8_many_kernel(const __grid_
     auto start_bar = [&](int s) { return bar_base + 8u * s; };
     auto done_bar = [&](int s) { return bar_base + 8u * (STAGES + s); };
     auto half_bar = [&](int q) { return bar_base + 8u * (2 * STAGES + q); };   // the two warps of a lane quarter
+    const uint32_t turn_bar = bar_base + 8u * (2 * STAGES + 4);   // this CTA's sums have read a turn's scales
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(base_ptr + kBarOff + 8 * Cfg::NBARS);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(base_ptr + kBarOff + 8 * Cfg::NBARS + 4);
 
@@ -748,6 +755,7 @@ __global__ void __launch_bounds__(kManyThreads, 1) fp8_many_kernel(const __grid_
             mbar_init(done_bar(s), 2);                   // the products, the scales
         }
         for (int q = 0; q < 4; ++q) mbar_init(half_bar(q), 2);
+        mbar_init(turn_bar, 8 * STAGES);
         *abort_flag = 0;
         fence_barrier_init();
     }
@@ -813,10 +821,10 @@ __global__ void __launch_bounds__(kManyThreads, 1) fp8_many_kernel(const __grid_
         if (warp == 3) {
             // ------------------------------------------------ scales (both CTAs)
             // Those of this CTA's 128 rows and the two weight blocks, by asynchronous copies kScaleAhead blocks ahead
-            // (loaded two blocks ahead by the warps that use them, their latency bounded the kernel).  Block j's
-            // arrival waits for block j - 6's products, the barriers' phase before, which waited until the sums' warps had
-            // read block j - 8's accumulator.  One scale of a block is read after that, but block j - 9's are all used by
-            // then: its slot may be asked for again.
+            // (loaded two blocks ahead by the warps that use them, their latency bounded the kernel).  That a slot's scales
+            // have been read says a barrier of its own, waited for once a turn of the ring: the accumulators' releases, by which
+            // the products' barriers follow each other, order no reads of shared memory.  It costs 1 % (down projection of
+            // 4096 rows 709 us without, 718 with it); one arrival a turn under a branch in place of one a block, 7 %.
             pdl_wait();
             float* raw = reinterpret_cast<float*>(base_ptr + kRawOff);
             int s = 0, ask_slot = 0;
@@ -859,6 +867,10 @@ __global__ void __launch_bounds__(kManyThreads, 1) fp8_many_kernel(const __grid_
                 int asked = 0;
                 for (int i = 0; i < blocks; ++i) {
                     if (!mbar_wait_warp(done_bar(s), phase ^ 1u, abort_flag, args.status)) {
+                        aborted = true;
+                        break;
+                    }
+                    if (s == kScaleTurn && !mbar_wait_warp(turn_bar, phase ^ 1u, abort_flag, args.status)) {
                         aborted = true;
                         break;
                     }
@@ -928,11 +940,14 @@ __global__ void __launch_bounds__(kManyThreads, 1) fp8_many_kernel(const __grid_
         const float* raw = reinterpret_cast<const float*>(base_ptr + kRawOff);
         // the accumulators are free to begin with: the first two blocks' starts
         const uint32_t start0 = mapa_shared(start_bar(0), leader);
-        auto release = [&](int s) {
-            if (elect_one()) mbar_arrive_cluster_relaxed(start0 + 8u * s);
+        auto release = [&](int s, bool read) {
+            if (elect_one()) {
+                mbar_arrive_cluster_relaxed(start0 + 8u * s);
+                if (read) mbar_arrive(turn_bar);          // the scales of the blocks before
+            }
         };
-        release(0);
-        release(1);
+        release(0, false);
+        release(1, false);
         int s = 0, b = 0, turn = 0, slot = 0;
         uint32_t phase = 0, hphase = 0;
         for (int tile = cluster; tile < args.total_tiles && !aborted; tile += nclusters) {
@@ -969,7 +984,7 @@ __global__ void __launch_bounds__(kManyThreads, 1) fp8_many_kernel(const __grid_
                 tmem_wait(d0, d1);
                 tc_fence_before();                        // the accumulator is read: block i + 2's products may have it
                 __syncwarp();
-                release(s + 2 < STAGES ? s + 2 : s + 2 - STAGES);
+                release(s + 2 < STAGES ? s + 2 : s + 2 - STAGES, true);
                 // read here, and not before: what is left to add is then scheduled behind the release (4096 gated rows of
                 // 14336 x 8192 in four shards 1564 us without)
                 const float fb = sx * *reinterpret_cast<const volatile float*>(scales + 129);
