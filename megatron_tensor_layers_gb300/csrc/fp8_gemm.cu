@@ -1226,10 +1226,12 @@ template <typename Resident>
 static Fp8Plan plan_product(const Fp8GemmDesc& d, int sms, Resident&& resident) {
     if (d.force_tile > 0) return plan_tile(d, d.force_tile, sms, resident);
     if (d.M <= 64) return plan_tile(d, d.M <= 16 ? 16 : d.M <= 32 ? 32 : 64, sms, resident);
-    const Fp8Plan many = plan_tile(d, 256, sms, resident), few = plan_tile(d, 128, sms, resident), fewer = plan_tile(d, 64, sms, resident);
-    if (many.cost < 0 || few.cost < 0 || fewer.cost < 0) return Fp8Plan();
-    if (many.cost <= few.cost && many.cost <= fewer.cost) return many;
-    return few.cost <= fewer.cost ? few : fewer;
+    Fp8Plan best;
+    for (int tile : {256, 128, 64}) {
+        const Fp8Plan p = plan_tile(d, tile, sms, resident);
+        if (p.cost >= 0 && (best.cost < 0 || p.cost < best.cost)) best = p;
+    }
+    return best;
 }
 
 Fp8Plan plan_fp8_gemm(const Fp8GemmDesc& d, int sms, const int* resident) {

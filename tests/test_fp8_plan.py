@@ -40,6 +40,16 @@ def test_plan_refuses(bad):
         tp.tp_debug_fp8_plan(a.pop("m"), a.pop("n"), a.pop("k"), residents(), **a)
 
 
+@pytest.mark.parametrize("gated", [False, True])
+@pytest.mark.parametrize("left", [2, 3, 4])
+def test_one_kernel_that_can_run_is_enough(left, gated):
+    """More than 64 tokens: tiles of 64 or 128 tokens or CTA pairs, of which two cannot run."""
+    r = [row if i == left else [0] * 8 for i, row in enumerate(residents())]
+    for m, n, k in [(65, 128, 128), (500, 1280, 8192), (4096, 7168, 8192)]:
+        tile, parts = tp.tp_debug_fp8_plan(m, n, k, r, gated=gated)
+        assert tile == (64, 128, 256)[left - 2] and parts >= 1
+
+
 def test_no_kernel_that_can_run():
     with pytest.raises(tp.TPError, match=UNSUPPORTED):
         tp.tp_debug_fp8_plan(8, 128, 128, [[0] * 8] * 5)
