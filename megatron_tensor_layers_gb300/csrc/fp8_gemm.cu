@@ -1161,8 +1161,10 @@ static int64_t stream_cost(const Fp8GemmDesc& d, int64_t ctas) {
     return bytes / 64000 * 24000 / (20400 + 15 * std::min<int64_t>(ctas, 240));
 }
 
-// Clusters of `size` CTAs of a kernel that can be resident at once, looked up once per device (cache: the kernel's).
-static int resident_clusters(const void* kern, int size, int threads, int smem, std::atomic<int>* cache) {
+// Clusters of `size` CTAs of a kernel that can be resident at once, looked up once per device (cache: the kernel's).  Its
+// registers, shared memory and TMEM leave room for per_sm CTAs an SM.  The runtime's queries count one for every kernel that allocates TMEM
+// (with 64 KB of shared memory as with 112; without the allocation 3 and 2), but two run at once, as their clocks on the SM show.
+static int resident_clusters(const void* kern, int size, int threads, int smem, int per_sm, std::atomic<int>* cache) {
     int dev = 0;
     cudaGetDevice(&dev);
     std::atomic<int>* slot = dev >= 0 && dev < 64 ? cache + dev : nullptr;       // relaxed: racing first calls store the same value
@@ -1178,8 +1180,12 @@ static int resident_clusters(const void* kern, int size, int threads, int smem, 
     cfg.dynamicSmemBytes = static_cast<size_t>(smem);
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    int v = 0;
-    if (cudaOccupancyMaxActiveClusters(&v, kern, &cfg) != cudaSuccess || v <= 0) v = -1;
+    int v = 0, counted = 0;
+    if (cudaOccupancyMaxActiveClusters(&v, kern, &cfg) != cudaSuccess || v <= 0 ||
+        cudaOccupancyMaxActiveBlocksPerMultiprocessor(&counted, kern, threads, static_cast<size_t>(smem)) != cudaSuccess || counted <= 0)
+        v = -1;
+    else if (counted < per_sm)
+        v = v / counted * per_sm;
     if (slot != nullptr) slot->store(v, std::memory_order_relaxed);
     return v;
 }
@@ -1248,8 +1254,7 @@ static int resident_few(int parts) {
     static std::atomic<uint64_t> smem_set{0};
     const void* kern = reinterpret_cast<const void*>(fp8_few_kernel<NT, ACT>);
     if (!smem_attribute_once(kern, Cfg::SMEM_BYTES, smem_set)) return 0;
-    // the occupancy query counts one CTA an SM of every kernel here; the times show that two of the smaller ones share it
-    return resident_clusters(kern, parts, Cfg::THREADS, Cfg::SMEM_BYTES, resident[parts - 1]) * (Cfg::ONE ? 1 : 2);
+    return resident_clusters(kern, parts, Cfg::THREADS, Cfg::SMEM_BYTES, Cfg::ONE ? 1 : 2, resident[parts - 1]);
 }
 
 template <int ACT>
@@ -1258,7 +1263,7 @@ static int resident_many(int parts) {
     static std::atomic<uint64_t> smem_set{0};
     const void* kern = reinterpret_cast<const void*>(fp8_many_kernel<ACT>);
     if (!smem_attribute_once(kern, ManyCfg::SMEM_BYTES, smem_set)) return 0;
-    return resident_clusters(kern, 2 * parts, kManyThreads, ManyCfg::SMEM_BYTES, resident[parts >> 1]);
+    return resident_clusters(kern, 2 * parts, kManyThreads, ManyCfg::SMEM_BYTES, 1, resident[parts >> 1]);
 }
 
 template <int NT, int ACT>
