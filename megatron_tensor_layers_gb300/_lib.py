@@ -134,6 +134,9 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 _raw_device = getattr(torch._C, "_cuda_getDevice", None)
 
 
+_current_device = _raw_device or torch.cuda.current_device
+
+
 def _stream(stream) -> Optional[int]:
     if stream is None:
         if _raw_stream is not None and _raw_device is not None:
@@ -364,7 +367,8 @@ def _shard_count(name: str, ts) -> int:
 
 
 def _on_gpu(*groups) -> None:
-    """Every tensor (or list of tensors; None entries skipped) is a CUDA tensor of one device."""
+    """Every tensor (or list of tensors; None entries skipped) is a CUDA tensor of one device, the current one: the
+    library launches there, and another device's memory may be out of its kernels' reach."""
     dev = None
     for g in groups:
         if g is None:
@@ -379,6 +383,8 @@ def _on_gpu(*groups) -> None:
                 dev = d
             elif d != dev:
                 raise ValueError(f"tensor arguments span devices cuda:{dev} and cuda:{d}")
+    if dev is not None and dev != _current_device():
+        raise ValueError(f"tensor arguments are on cuda:{dev}, the current device is cuda:{_current_device()}")
 
 
 BF16 = (torch.bfloat16,)
