@@ -407,7 +407,7 @@ def tp_linear_col(x: torch.Tensor, w: Sequence[torch.Tensor], *, act: str = "non
     n, k = _matrix("x", x, dtypes=BF16).shape
     if act not in ACTS:
         raise ValueError(f"act must be one of {list(ACTS)}")
-    rows = w[0].shape[0] if w[0].dim() == 2 else -1
+    rows = _matrix(("w", 0), w[0]).shape[0]
     ldw = _matrices("w", w, (rows, k), BF16)
     gated = act != "none"
     if gated and rows % 2:
@@ -511,7 +511,7 @@ def _mlp_args(x, w_gate_up, w_down, bias_down, act, mode):
     if mode not in MODES:
         raise ValueError(f"mode must be one of {list(MODES)}")
     n, h = _matrix("x", x, dtypes=BF16).shape
-    rows = w_gate_up[0].shape[0] if w_gate_up[0].dim() == 2 else -1
+    rows = _matrix(("w_gate_up", 0), w_gate_up[0]).shape[0]
     if rows % 2:
         raise ValueError("w_gate_up[r] holds gate rows then as many up rows: its row count must be even")
     fs = rows // 2
@@ -929,7 +929,7 @@ def tp_fp8_linear_col(x: torch.Tensor, x_scales: torch.Tensor, w: Sequence[torch
     ldxs = _row_scales("x_scales", [x_scales], k, n)
     if act not in ACTS:
         raise ValueError(f"act must be one of {list(ACTS)}")
-    rows = w[0].shape[0] if w[0].dim() == 2 else -1
+    rows = _matrix(("w", 0), w[0]).shape[0]
     ldw = _matrices("w", w, (rows, k), FP8S)
     gated = act != "none"
     if gated and rows % 2:
@@ -1037,7 +1037,7 @@ def tp_fp8_mlp_forward(x: torch.Tensor, x_scales: torch.Tensor, w_gate_up: Seque
         raise ValueError(f"mode must be one of {list(MODES)}")
     n, h = _matrix("x", x, dtypes=FP8S).shape
     ldxs = _row_scales("x_scales", [x_scales], h, n)
-    rows = w_gate_up[0].shape[0] if w_gate_up[0].dim() == 2 else -1
+    rows = _matrix(("w_gate_up", 0), w_gate_up[0]).shape[0]
     if rows % 2:
         raise ValueError("w_gate_up[r] holds gate rows then as many up rows: its row count must be even")
     fs = rows // 2
