@@ -24,7 +24,8 @@
  *    bounded wait that expired) are reported by tp_device_status().
  *  - Alignment: every device pointer and the row stride in bytes of every
  *    GEMM input (x, w, table) must be a multiple of 16 bytes (TMA tiles and
- *    128-bit loads), else TP_ERR_ALIGNMENT.  GEMM outputs only need a row
+ *    128-bit loads), else TP_ERR_ALIGNMENT; a bias and the scales of 8-bit
+ *    values only need their elements' alignment.  GEMM outputs only need a row
  *    stride at least their width (TP_ERR_INVALID_ARG otherwise); rows whose
  *    16-byte chunks are not aligned are written element by element.
  *    Shard counts must be in 1..TP_MAX_SHARDS, else TP_ERR_INVALID_ARG.  Splits that do not divide evenly return

@@ -49,6 +49,7 @@ int* status_ptr() {
 }
 
 inline bool al16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+inline bool al2(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 1u) == 0; }
 inline int esize(tp_dtype d) { return d == TP_F32 ? 4 : 2; }
 inline bool dtype_ok(int d) { return d == TP_BF16 || d == TP_F32; }
 inline bool ld_ok(int64_t ld, int64_t minimum, int elem) { return ld >= minimum && (ld * elem) % 16 == 0; }
@@ -124,7 +125,10 @@ tp_status tp_linear_col(int t, int64_t n, int64_t in, int64_t out_full, const vo
     for (int r = 0; r < t; ++r) {
         TP_CHECK(w[r] != nullptr, TP_ERR_INVALID_ARG);
         TP_CHECK(al16(w[r]), TP_ERR_ALIGNMENT);
-        if (bias != nullptr) TP_CHECK(bias[r] != nullptr, TP_ERR_INVALID_ARG);
+        if (bias != nullptr) {
+            TP_CHECK(bias[r] != nullptr, TP_ERR_INVALID_ARG);
+            TP_CHECK(al2(bias[r]), TP_ERR_ALIGNMENT);
+        }
         if (!gather_output || r == 0) {
             TP_CHECK(y[r] != nullptr || n == 0, TP_ERR_INVALID_ARG);
             TP_CHECK(al16(y[r]), TP_ERR_ALIGNMENT);
@@ -220,7 +224,7 @@ static tp_status linear_row_impl(int t, int64_t n, int64_t in_full, int64_t out,
     TP_CHECK(in_full % t == 0, TP_ERR_NOT_DIVISIBLE);
     const int64_t ks = in_full / t;
     TP_CHECK(ks % 8 == 0, TP_ERR_ALIGNMENT);
-    TP_CHECK(ld_ok(ldx, ks, 2) && ld_ok(ldw, ks, 2), TP_ERR_ALIGNMENT);
+    TP_CHECK(ld_ok(ldx, ks, 2) && ld_ok(ldw, ks, 2) && al2(bias), TP_ERR_ALIGNMENT);
     const bool fused = mode == TP_REDUCE_FUSED;
     if (!fused) {
         TP_CHECK(partials != nullptr, TP_ERR_INVALID_ARG);
@@ -327,7 +331,7 @@ tp_status tp_mlp_forward(int t, int64_t n, int64_t h, int64_t f, const void* x, 
     TP_CHECK(f % t == 0, TP_ERR_NOT_DIVISIBLE);
     const int64_t fs = f / t;
     TP_CHECK(fs % 8 == 0 && h % 8 == 0, TP_ERR_ALIGNMENT);
-    TP_CHECK(al16(x) && ld_ok(ldx, h, 2) && ld_ok(ld_down, fs, 2) && al16(y), TP_ERR_ALIGNMENT);
+    TP_CHECK(al16(x) && ld_ok(ldx, h, 2) && ld_ok(ld_down, fs, 2) && al16(y) && al2(bias_down), TP_ERR_ALIGNMENT);
     for (int r = 0; r < t; ++r) {
         TP_CHECK(w_gate_up[r] != nullptr && w_down[r] != nullptr, TP_ERR_INVALID_ARG);
         TP_CHECK(al16(w_gate_up[r]) && al16(w_down[r]), TP_ERR_ALIGNMENT);

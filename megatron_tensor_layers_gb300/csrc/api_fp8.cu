@@ -12,6 +12,7 @@
 namespace {
 
 inline bool al16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+inline bool al2(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 1u) == 0; }
 inline bool al4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 inline int esize(tp_dtype d) { return d == TP_F32 ? 4 : 2; }
 inline bool dtype_ok(int d) { return d == TP_BF16 || d == TP_F32; }
@@ -220,7 +221,10 @@ tp_status tp_fp8_linear_col(int t, int64_t n, int64_t in, int64_t out_full, cons
     for (int r = 0; r < t; ++r) {
         TP_CHECK(w[r] != nullptr && ws[r] != nullptr, TP_ERR_INVALID_ARG);
         TP_CHECK(al16(w[r]) && al4(ws[r]), TP_ERR_ALIGNMENT);
-        if (bias != nullptr) TP_CHECK(bias[r] != nullptr, TP_ERR_INVALID_ARG);
+        if (bias != nullptr) {
+            TP_CHECK(bias[r] != nullptr, TP_ERR_INVALID_ARG);
+            TP_CHECK(al2(bias[r]), TP_ERR_ALIGNMENT);
+        }
         if (!gather_output || r == 0) {
             TP_CHECK(y[r] != nullptr || n == 0, TP_ERR_INVALID_ARG);
             TP_CHECK(al16(y[r]), TP_ERR_ALIGNMENT);
@@ -255,7 +259,7 @@ static tp_status linear_row_impl(int t, int64_t n, int64_t in_full, int64_t out,
     TP_CHECK(in_full % t == 0, TP_ERR_NOT_DIVISIBLE);
     const int64_t ks = in_full / t;
     const bool fused = mode == TP_REDUCE_FUSED;
-    TP_CHECK(ks % 16 == 0 && codes_ld_ok(ldx, ks) && codes_ld_ok(ldw, ks), TP_ERR_ALIGNMENT);
+    TP_CHECK(ks % 16 == 0 && codes_ld_ok(ldx, ks) && codes_ld_ok(ldw, ks) && al2(bias), TP_ERR_ALIGNMENT);
     TP_CHECK(ldxs >= n, TP_ERR_INVALID_ARG);
     if (!fused) {
         TP_CHECK(partials != nullptr, TP_ERR_INVALID_ARG);
@@ -347,7 +351,7 @@ tp_status tp_fp8_mlp_forward(int t, int64_t n, int64_t h, int64_t f, const void*
     TP_CHECK(f % t == 0, TP_ERR_NOT_DIVISIBLE);
     const int64_t fs = f / t;
     TP_CHECK(fs % 16 == 0 && h % 16 == 0, TP_ERR_ALIGNMENT);
-    TP_CHECK(al16(x) && al4(xs) && codes_ld_ok(ldx, h) && codes_ld_ok(ld_down, fs) && al16(y), TP_ERR_ALIGNMENT);
+    TP_CHECK(al16(x) && al4(xs) && codes_ld_ok(ldx, h) && codes_ld_ok(ld_down, fs) && al16(y) && al2(bias_down), TP_ERR_ALIGNMENT);
     TP_CHECK(ldxs >= n, TP_ERR_INVALID_ARG);
     for (int r = 0; r < t; ++r) {
         TP_CHECK(w_gate_up[r] != nullptr && s_gate_up[r] != nullptr && w_down[r] != nullptr && s_down[r] != nullptr,
