@@ -6,23 +6,12 @@
 #include <cmath>
 #include <cstdint>
 
+#include "api_checks.h"
 #include "kernels.h"
 #include "tp.h"
 
 namespace {
 
-inline bool al16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-inline bool al2(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 1u) == 0; }
-inline bool al4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
-inline int esize(tp_dtype d) { return d == TP_F32 ? 4 : 2; }
-inline bool dtype_ok(int d) { return d == TP_BF16 || d == TP_F32; }
-inline size_t align256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
-inline cudaStream_t cs(tp_stream s) { return reinterpret_cast<cudaStream_t>(s); }
-
-#define TP_CHECK(cond, code) \
-    do {                     \
-        if (!(cond)) return (code); \
-    } while (0)
 
 // Rows and columns of a product: twice as many, and a tile more, still count in 32 bits.
 constexpr int64_t kMaxSize = int64_t(1) << 29;

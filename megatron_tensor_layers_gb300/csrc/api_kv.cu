@@ -6,24 +6,18 @@
 #include <cmath>
 #include <cstdint>
 
+#include "api_checks.h"
 #include "kernels.h"
 #include "tp.h"
 
 namespace {
 
-inline bool al16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-inline cudaStream_t cs(tp_stream s) { return reinterpret_cast<cudaStream_t>(s); }
 inline bool page_size_ok(int p) { return p == 16 || p == 32 || p == 64 || p == 128; }
 inline bool head_dim_ok(int d) { return d == 64 || d == 128; }
 
 // Sizes that keep row, position and block numbers within 31 bits.
 constexpr int64_t kMaxRows = int64_t(1) << 30;
 constexpr int kMaxKvHeads = 1024;
-
-#define TP_CHECK(cond, code) \
-    do {                     \
-        if (!(cond)) return (code); \
-    } while (0)
 
 // The checks that append, load and attention share; fills seqs and pools.
 tp_status check_cache(int t, int64_t n, int64_t nseq, int kv_heads, int head_dim, void* const* pool, int64_t pages,

@@ -54,28 +54,6 @@ __device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
     return static_cast<uint32_t>(lo) | (static_cast<uint32_t>(hi) << 16);
 }
 
-// Pairs of fp32 values in one register pair, and two multiply-adds in one
-// instruction.  The sums stay packed over the whole loop and a block's factor is packed
-// once: packed in each multiply-add anew, 128 of them took a warp 220 cycles
-// instead of 153.
-using f32x2 = unsigned long long;
-__device__ __forceinline__ f32x2 pack2(float a, float b) {
-    f32x2 r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
-    return r;
-}
-__device__ __forceinline__ void unpack2(f32x2 v, float& a, float& b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v)); }
-__device__ __forceinline__ f32x2 fma2(f32x2 d, f32x2 s, f32x2 a) {
-    f32x2 r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(d), "l"(s), "l"(a));
-    return r;
-}
-__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
-    f32x2 r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-
 // Quotients x / scale, of values given negated, as close as codes need: with r =
 // 1 / s rounded to nearest, q0 = x r is within 1.5 units of the last place, and one
 // correction q1 = q0 + (x - q0 s) r (the remainder is exact in an fma) leaves
@@ -140,9 +118,6 @@ __device__ __forceinline__ float amax_pairs(const f32x2 (&x)[PAIRS]) {
     }
     return m;
 }
-
-__device__ __forceinline__ f32x2 both(float v) { return pack2(v, v); }
-__device__ __forceinline__ f32x2 neg2(f32x2 v) { return v ^ 0x8000000080000000ull; }
 
 // act(g) of a gated block as g s, s = 1 / (1 + exp(-z)): SiLU has z = g, and
 // GeLU-tanh's 0.5 g (1 + tanh(u)) is z = 2 u with u = sqrt(2/pi) (g + 0.044715

@@ -22,7 +22,6 @@ struct Fp8QuantArgs {
     uint8_t* codes[TP_MAX_SHARDS];
     float* scales[TP_MAX_SHARDS];
     int64_t n, k, ldx, ldc, lds, half;
-    int groups;          // groups of a row
     int blocks_half;     // weight: blocks of the first part's rows
 };
 
@@ -144,13 +143,12 @@ tp_status launch_fp8_quant(const Fp8QuantDesc& d, cudaStream_t stream) {
     a.ldc = d.ldc;
     a.lds = d.lds;
     a.half = d.half;
-    a.groups = static_cast<int>(fp8_groups(d.k));
     cudaError_t e;
     if (d.weight) {
         a.blocks_half = static_cast<int>(fp8_groups(d.half));
         const int64_t blocks = d.half > 0 ? a.blocks_half + fp8_groups(d.n - d.half) : fp8_groups(d.n);
         if (blocks > 65535) return TP_ERR_UNSUPPORTED;
-        const dim3 grid(static_cast<unsigned>(a.groups), static_cast<unsigned>(blocks), static_cast<unsigned>(d.t));
+        const dim3 grid(static_cast<unsigned>(fp8_groups(d.k)), static_cast<unsigned>(blocks), static_cast<unsigned>(d.t));
         e = d.in_f32 ? launch_pdl(fp8_quant_weight_kernel<true>, grid, dim3(kQuantThreads), 0, stream, a)
                      : launch_pdl(fp8_quant_weight_kernel<false>, grid, dim3(kQuantThreads), 0, stream, a);
     } else {

@@ -175,3 +175,18 @@ def test_untouched_bytes(choose):
             tp.tp_fp8_linear_col(*a, [pw], [ps], y=[y[1:n + 1, 8:309]])
             y[1:n + 1, 8:309] = 5.0
             assert (y == 5.0).all(), variant
+
+
+@pytest.mark.parametrize("variant", [(16, 2, 0), (64, 1, 0), (256, 1, 0), (256, 2, 0)])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_gathered_columns_of_an_odd_width(choose, variant, dtype):
+    """The second and third shards' columns begin at no 16-byte boundary."""
+    t, n, k, out = 3, 270, 528, 301
+    x, xs = quantised(n, k, 5)
+    ws = [weights(out, k, 30 + r) for r in range(t)]
+    choose(*variant)
+    y = torch.full((n, t * out + 13), 5.0, dtype=dtype, device=DEV)
+    tp.tp_fp8_linear_col(x.to(DEV), xs.to(DEV), *dev(ws), gather_output=True, y=y[:, :t * out])
+    for r in range(t):
+        check(y[:, r * out:(r + 1) * out], *P.product([P.rows64(x, xs)], [P.weight64(*ws[r])]))
+    assert (y[:, t * out:] == 5.0).all()
