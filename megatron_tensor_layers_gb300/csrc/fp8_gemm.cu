@@ -559,9 +559,9 @@ __global__ void __launch_bounds__(FewCfg<NT, ACT != TP_ACT_NONE>::THREADS, FewCf
 // add to 128 fp32 sums a thread, while the MMAs fill the other.  From an
 // accumulator's MMAs to the next ones that may overwrite it pass its MMAs (513
 // cycles), their commit (330), the reading (310) and the release across the
-// pair (265), with a trace's own cost; a K block takes about 600 cycles: 4096 rows
-// of four shards' down projection 490 us with codes of zero (3.9 PFLOP/s), 700 with
-// random ones, whose power lowers the clock; their gated products 1038 and 1376.
+// pair (265), with a trace's own cost; a K block takes about 610 cycles: 4096 rows
+// of four shards' down projection 499 us with codes of zero (3.9 PFLOP/s), 718 with
+// random ones, whose power lowers the clock; their gated products 1055 and 1397.
 // What keeps each of these short was measured:
 //  - one warp issues the MMAs, elected lanes in converged loops under a
 //    warp-uniform branch (four MMAs, a wait and a commit: 380 cycles; one lane of a
